@@ -1,8 +1,9 @@
-"""Builds libgemm_bf16.so in-tree from csrc/ with nvcc for sm_103a.
+"""Builds libgemm_bf16.so and libfp8_ops.so in-tree from csrc/ with nvcc for sm_103a.
 
 The translation units compile in parallel; the CUDA runtime is linked
-statically and every symbol except the C ABI of include/gemm_bf16.h is hidden,
-so the library loads (and exports its ABI) on a machine without a GPU.
+statically and every symbol except the C ABIs of include/gemm_bf16.h and
+include/fp8_ops.h is hidden, so each library loads (and exports its ABI) on a
+machine without a GPU.
 """
 from __future__ import annotations
 
@@ -19,10 +20,12 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemm_bf16.so")
+FP8_LIB = os.path.join(PKG, "libfp8_ops.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gemm_bf16_api.cu", "gemm_ws_c1.cu", "gemm_ws_c2.cu", "gemm_nows.cu", "gemm_bf16_noalloc.cu",
            "gemm_repack.cu", "gemm_thin.cu"]
+FP8_SOURCES = ["fp8_api.cu", "fp8_gemm.cu", "fp8_quantize.cu", "fp8_norm.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
@@ -32,7 +35,7 @@ def nvcc() -> str:
     for cand in (shutil.which("nvcc"), "/usr/local/cuda/bin/nvcc"):
         if cand and os.path.exists(cand):
             return cand
-    raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libgemm_bf16.so")
+    raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the libraries")
 
 
 def source_digest() -> str:
@@ -87,7 +90,7 @@ def build_stamp(cc: str | None = None) -> str:
 
 
 def up_to_date(cc: str | None = None) -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(_stamp_path()):
+    if not (os.path.exists(LIB) and os.path.exists(FP8_LIB) and os.path.exists(_stamp_path())):
         return False
     with open(_stamp_path()) as fh:
         return fh.read().strip() == build_stamp(cc)
@@ -112,14 +115,19 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    with ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
-        objs = list(ex.map(compile_one, SOURCES))
-    tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL", "-o", tmp, *objs]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
-    os.replace(tmp, LIB)
+    def link(lib: str, objs: list) -> None:
+        tmp = lib + f".tmp{os.getpid()}"
+        cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL", "-o", tmp, *objs]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
+        os.replace(tmp, lib)
+
+    sources = SOURCES + FP8_SOURCES
+    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+        objs = list(ex.map(compile_one, sources))
+    link(LIB, objs[:len(SOURCES)])
+    link(FP8_LIB, objs[len(SOURCES):])
     with open(_stamp_path(), "w") as fh:
         fh.write(build_stamp(cc))
     return LIB

@@ -1,0 +1,122 @@
+// The 8-bit block format: e4m3 codes with one power-of-two scale per block of
+// 128, shared by the quantiser and the norm.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+namespace wstma {
+
+constexpr int kFp8Block = 128;
+
+// Biased exponent of the least power of two s with amax / s <= 448.  448 is
+// 1.75 * 2^8, so amax = m * 2^E with m in [1, 2) needs 2^(E-8) where m <= 1.75
+// and 2^(E-7) above: integer arithmetic on the bits, exact for every finite
+// amax.  Subnormal amax (and zero) ends at the least scale, 2^-127.
+__device__ __forceinline__ uint32_t scale_byte(float amax)
+{
+    const uint32_t bits = __float_as_uint(amax);
+    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
+    return (uint32_t)(e > 0 ? e : 0);
+}
+
+// 1 / 2^(byte - 127), a normal number for every byte scale_byte() gives (<= 247).
+__device__ __forceinline__ float scale_inverse(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }
+
+// Two values -> two e4m3 codes, round to nearest even; `lo` lands in the low
+// byte.  Inputs are at most 448 in magnitude, or NaN.
+__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d)
+{
+    return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
+}
+
+__device__ __forceinline__ bool is_inf(float f) { return (__float_as_uint(f) & 0x7FFFFFFFu) == 0x7F800000u; }
+
+__device__ __forceinline__ float inf_to_nan(float f) { return is_inf(f) ? __uint_as_float(0x7FFFFFFFu) : f; }
+
+// |f| of a finite value, 0 for an infinity (fmaxf already passes over NaN).
+__device__ __forceinline__ float finite_abs(float f) { return is_inf(f) ? 0.f : fabsf(f); }
+
+__device__ __forceinline__ void unpack8(const uint4 q, float (&f)[8])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+}
+
+__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
+{
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Elements c .. c+7 of a bf16 row of C elements as floats; those past the end
+// read as zero.  `vec`: the row is 16-byte aligned, so whole groups load at once.
+__device__ __forceinline__ uint4 load8_bf16(const uint16_t *row, int32_t c, int32_t C, bool vec)
+{
+    if (vec && c + 8 <= C)
+        return *reinterpret_cast<const uint4 *>(row + c);
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < C)
+            w[i >> 1] |= (uint32_t)row[c + i] << (16 * (i & 1));
+    return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void load8_float(const float *row, int32_t c, int32_t C, bool vec, float (&f)[8])
+{
+    if (vec && c + 8 <= C) {
+        const float4 a = *reinterpret_cast<const float4 *>(row + c);
+        const float4 b = *reinterpret_cast<const float4 *>(row + c + 4);
+        f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+        f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        f[i] = c + i < C ? row[c + i] : 0.f;
+}
+
+__device__ __forceinline__ void store8_bf16(uint16_t *row, int32_t c, int32_t C, bool vec, uint4 q)
+{
+    if (vec && c + 8 <= C) {
+        *reinterpret_cast<uint4 *>(row + c) = q;
+        return;
+    }
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < C)
+            row[c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+}
+
+// Codes c .. c+7 of a row (rows are 16-byte aligned).
+__device__ __forceinline__ void store8_codes(uint8_t *row, int32_t c, int32_t C, uint2 q)
+{
+    if (c + 8 <= C) {
+        *reinterpret_cast<uint2 *>(row + c) = q;
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        if (c + i < C)
+            row[c + i] = (uint8_t)((i < 4 ? q.x : q.y) >> (8 * (i & 3)));
+}
+
+}  // namespace wstma

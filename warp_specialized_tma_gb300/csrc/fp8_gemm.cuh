@@ -1,0 +1,610 @@
+// The block-scaled 8-bit product: D = A * B^T of two quantised matrices.
+//
+//   D[m][n] = sum over blocks b of 128: 2^(ea[m][b]) 2^(eb[n][b]) sum_{k in b} a[m][k] b[n][k]
+//
+// tcgen05.mma's block-scaled kind multiplies each product of 32 elements of k by
+// the two rows' e8m0 scales before adding it to the fp32 accumulator; four such
+// MMAs make a block of 128, with the same scales.  So the scales cost no pass over
+// the accumulator: they are copied to tensor memory once per four blocks (one
+// 32-bit word per row) and picked by a byte index in the instruction descriptor.
+//
+// One of A and B is on the MMA's row side (128 rows to a CTA, 256 to an SM pair),
+// the other on its column side (`width` <= 224 columns to a tile).  For a few
+// tokens the weights take the row side, and the accumulator holds D transposed.
+//
+// Roles (384 threads, one CTA per SM):
+//   warp 0, lane 0   TMA producer: per (item, k-block) wait "empty", load both tiles
+//   warp 1, lane 0   MMA issuer (leader CTA only in pairs)
+//   warp 2           allocates and frees tensor memory
+//   warp 3           scales: 4 k-blocks' words per row from global to shared memory
+//   warps 4..11      epilogue: tensor memory -> registers -> D
+//
+// Work: tiles [0, sk_tiles) are split along k, their (tile, k-block) units cut
+// into one contiguous range per cluster; the other tiles are walked whole.  The
+// pieces of a split tile meet through global memory as fp32, added in range
+// order by the piece that holds k-block 0, so the result is the same every time.
+// Every wait is bounded by the watchdog (WaitCtl in ptx.cuh).
+#pragma once
+
+#include "fp8_kernels.h"
+#include "fp8_ptx.cuh"
+#include "gemm_common.cuh"
+
+namespace wstma {
+
+struct Fp8Item {
+    int32_t tile, kb0, kb1;
+};
+
+__host__ __device__ __forceinline__ int64_t fp8_range_begin(int64_t units, int32_t clusters, int32_t c)
+{
+    return (int64_t)c * units / clusters;
+}
+
+// A cluster's items in order: its range of the split tiles' units (a range is no
+// longer than a tile, since sk_tiles < clusters, so it touches at most two
+// tiles), then every clusters-th whole tile.  A range's first piece may start
+// inside a tile (it then leaves a partial); a piece that starts at k-block 0 and
+// does not reach the tile's end is the last of its range.  So no cluster waits
+// for a partial before it has left its own.
+struct Fp8Work {
+    int64_t u, u_end;
+    int32_t dp, C, T, KB;
+
+    __host__ __device__ __forceinline__ void init(const Fp8GemmParams &p, int32_t cluster, int32_t clusters)
+    {
+        KB = p.num_k_blocks;
+        C = clusters;
+        T = p.num_tiles;
+        dp = p.sk_tiles + cluster;
+        u = fp8_range_begin(p.sk_units, clusters, cluster);
+        u_end = fp8_range_begin(p.sk_units, clusters, cluster + 1);
+    }
+
+    __host__ __device__ __forceinline__ bool next(Fp8Item &w)
+    {
+        if (u < u_end) {
+            const int64_t t = u / KB;
+            const int64_t k0 = u - t * KB;
+            const int64_t k1 = k0 + (u_end - u) < KB ? k0 + (u_end - u) : KB;
+            w.tile = (int32_t)t;
+            w.kb0 = (int32_t)k0;
+            w.kb1 = (int32_t)k1;
+            u += k1 - k0;
+            return true;
+        }
+        if (dp < T) {
+            w.tile = dp;
+            w.kb0 = 0;
+            w.kb1 = KB;
+            dp += C;
+            return true;
+        }
+        return false;
+    }
+};
+
+// Tile -> (row tile, column tile): bands of raster_group row tiles, walked column
+// by column, odd bands right to left, so that tiles running at the same time
+// share operands in L2.
+__host__ __device__ __forceinline__ TileCoord fp8_tile_coord(int32_t t, const Fp8GemmParams &p)
+{
+    const int32_t span = p.raster_group * p.num_col_tiles;
+    const int32_t band = t / span;
+    const int32_t first = band * p.raster_group;
+    const int32_t rows = p.num_row_tiles - first < p.raster_group ? p.num_row_tiles - first : p.raster_group;
+    const int32_t r = t - band * span;
+    const int32_t col = r / rows;
+    return {first + r % rows, (band & 1) ? p.num_col_tiles - 1 - col : col};
+}
+
+constexpr uint32_t kFp8ScaleCol = 2u * kFp8MaxWidth;  // tensor-memory columns of the scales: two buffers of 32
+constexpr uint32_t kFp8ScaleColB = 16u;               // inside a buffer: row side at 0..3, column side at 16..23
+
+// A 32 x 32 chunk of D, staged in shared memory as rows of D in the TMA swizzle
+// of its row size (64 bytes of bf16, 128 of fp32): byte offset of element (r, c).
+__device__ __forceinline__ uint32_t fp8_chunk_offset(uint32_t r, uint32_t c, bool fp32)
+{
+    if (fp32)
+        return r * 128u + (((c >> 2) ^ (r & 7u)) << 4) + (c & 3u) * 4u;
+    return r * 64u + (((c >> 3) ^ ((r >> 1) & 3u)) << 4) + (c & 7u) * 2u;
+}
+
+// Stores the staged chunk at D[y..y+31][x..x+31] by a TMA store, or, where D's
+// layout or its last columns do not allow one (a TMA store writes whole 16-byte
+// groups), by the warp's masked stores.
+__device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, const CUtensorMap *tmD, int32_t x, int32_t y,
+                                                const Fp8GemmParams &p)
+{
+    const bool fp32 = p.out_fp32 != 0;
+    const int32_t group = fp32 ? 4 : 8;
+    if (p.d_tma && (x + 32 <= p.D_cols || p.D_cols % group == 0)) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(tmD, staging, x, y);
+            bulk_commit_group();
+        }
+        return;
+    }
+    if (lane == 0)
+        bulk_wait_read_all();  // the next chunk counts on at most one store in flight, the last one
+    __syncwarp();
+    const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
+    if (fp32) {
+        float *const D = static_cast<float *>(p.D) + (int64_t)y * p.ldd + x + lane;
+        if (x + lane < p.D_cols)
+            for (int32_t r = 0; r < rows; ++r)
+                D[(int64_t)r * p.ldd] =
+                    __uint_as_float(ld_shared_u32(staging + fp8_chunk_offset((uint32_t)r, (uint32_t)lane, true)));
+        return;
+    }
+    // lanes 0-15 take even rows, 16-31 odd ones, two columns each
+    const int32_t c = (lane & 15) * 2;
+    for (int32_t r = lane >> 4; r < rows; r += 2) {
+        const uint32_t w = ld_shared_u32(staging + fp8_chunk_offset((uint32_t)r, (uint32_t)c, false));
+        uint16_t *const dst = static_cast<uint16_t *>(p.D) + (int64_t)(y + r) * p.ldd + x + c;
+        if (x + c + 1 < p.D_cols && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+            *reinterpret_cast<uint32_t *>(dst) = w;
+        } else {
+            if (x + c < p.D_cols)
+                dst[0] = (uint16_t)w;
+            if (x + c + 1 < p.D_cols)
+                dst[1] = (uint16_t)(w >> 16);
+        }
+    }
+}
+
+// Stages the warp's 32 accumulator rows x 32 columns (thread = row) as a chunk of
+// D, `live` columns of it when D is the accumulator transposed.
+template <bool kTransposed>
+__device__ __forceinline__ void fp8_stage_chunk(const uint32_t (&v)[32], uint32_t staging, uint32_t lane, int32_t live,
+                                                bool fp32)
+{
+    if constexpr (kTransposed) {
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) {
+            if ((int32_t)i >= live)
+                break;
+            const uint32_t at = staging + fp8_chunk_offset(i, lane, fp32);
+            if (fp32)
+                st_shared_u32(at, v[i]);
+            else
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pack_bf16x2(v[i], 0u)) : "memory");
+        }
+    } else if (fp32) {
+#pragma unroll
+        for (uint32_t u = 0; u < 8; ++u)
+            st_shared_v4(staging + fp8_chunk_offset(lane, 4 * u, true), v[4 * u], v[4 * u + 1], v[4 * u + 2],
+                         v[4 * u + 3]);
+    } else {
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            st_shared_v4(staging + fp8_chunk_offset(lane, 8 * u, false), pack_bf16x2(v[8 * u], v[8 * u + 1]),
+                         pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
+                         pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+    }
+}
+
+// This thread's 32 values of chunk number `ci` of its warp in a CTA's partial:
+// float4 groups, each 512 contiguous bytes over the warp.
+__device__ __forceinline__ float4 *fp8_partial(float *partials, int32_t cta, int ew, int ci, int lane)
+{
+    return reinterpret_cast<float4 *>(partials + (size_t)cta * kFp8PartialFloats) + ((ew * 4 + ci) * 8) * 32 + lane;
+}
+
+template <int CG, bool kTransposed>
+__global__ void __launch_bounds__(kFp8Threads, 1)
+    fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC,
+                    const __grid_constant__ CUtensorMap tmD, const Fp8GemmParams p)
+{
+    constexpr bool kCluster = CG == 2;
+    constexpr uint32_t kRBytes = (uint32_t)kFp8RowsPerCta * kFp8BlockK;
+    const int32_t width = p.width;
+    const uint32_t stage_bytes = kRBytes + (uint32_t)(width / CG) * kFp8BlockK;  // a multiple of 1024
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int S = p.stages;  // even: stages are released in pairs
+    const uint32_t stage0 = base;
+    const uint32_t staging0 = base + (uint32_t)S * stage_bytes;
+    const uint32_t scales0 = staging0 + kFp8EpiWarps * kFp8StagingBytes;
+    const uint32_t full_bar = scales0 + kFp8ScaleSlots * kFp8ScaleBytes;
+    const uint32_t empty_bar = full_bar + 8u * S;
+    const uint32_t sfull_bar = empty_bar + 8u * S;
+    const uint32_t sempty_bar = sfull_bar + 8u * kFp8ScaleSlots;
+    const uint32_t accf_bar = sempty_bar + 8u * kFp8ScaleSlots;
+    const uint32_t acce_bar = accf_bar + 16u;
+    const uint32_t done_bar = acce_bar + 16u;
+    const uint32_t tmem_slot = done_bar + 8u;
+    const uint32_t abort_flag = tmem_slot + 4u;
+    const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
+
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar + 8u * s, 1);
+            mbar_init(empty_bar + 8u * s, 1);
+        }
+        for (int s = 0; s < kFp8ScaleSlots; ++s) {
+            mbar_init(sfull_bar + 8u * s, CG);  // the scale warp of each CTA
+            mbar_init(sempty_bar + 8u * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(accf_bar + 8u * a, 1);
+            mbar_init(acce_bar + 8u * a, kFp8EpiWarps * CG);
+        }
+        mbar_init(done_bar, 1);
+        st_shared_u32(abort_flag, 0u);
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x == 32) {
+        prefetch_tensormap(&tmR);
+        prefetch_tensormap(&tmC);
+    }
+    // both CTAs of a pair have initialised their barriers before any cross-CTA
+    // arrive, TMA completion or the paired allocation
+    if constexpr (kCluster)
+        cluster_arrive_wait();
+    else
+        __syncthreads();
+    if (warp == 2) {
+        tmem_alloc<CG>(tmem_slot, 512);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ld_shared_u32(tmem_slot);
+    // Up to here only shared and tensor memory was touched: it overlaps the
+    // previous kernel on the stream.  Every role that reads or writes global
+    // memory waits for that kernel first.
+
+    WaitCtl ctl;
+    ctl.abort_flag = abort_flag;
+    ctl.peer_abort_flag = kCluster ? mapa_shared(abort_flag, rank ^ 1u) : 0u;
+    ctl.err = p.err;
+    ctl.set_limit(p.watchdog_ns);
+
+    const int32_t cluster_id = (int32_t)blockIdx.x / CG;
+    const int32_t num_clusters = (int32_t)gridDim.x / CG;
+    const int32_t KB = p.num_k_blocks;
+    Fp8Work wi;
+    wi.init(p, cluster_id, num_clusters);
+    Fp8Item w;
+
+    if (warp == 0 && lane == 0) {
+        // ---------------- TMA producer ----------------
+        const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
+        int s = 0;
+        uint32_t ph = 0;
+        int32_t it = 0;
+        bool ok = true;
+        grid_dependency_wait();
+        while (ok && wi.next(w)) {
+            const TileCoord tc = fp8_tile_coord(w.tile, p);
+            const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta;
+            const int32_t yc = tc.nb * width + (int32_t)rank * (width / CG);
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                if (ring_group_first(s, 1u) &&
+                    !ctl.wait<kCluster>(empty_bar + 8u * ring_group(s, 1u), ring_empty_parity(ph), kRoleProducer,
+                                        (uint32_t)s)) {
+                    ok = false;
+                    break;
+                }
+                if (it != p.fault_skip_it) {
+                    if (!kCluster || rank == 0)
+                        mbar_arrive_expect_tx(full_bar + 8u * s, stage_bytes * CG);
+                    const uint32_t fb = full_target + 8u * s;
+                    const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
+                    if constexpr (kCluster) {
+                        tma_load_2d_pair(sa, &tmR, kb * kFp8BlockK, yr, fb);
+                        tma_load_2d_pair(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
+                    } else {
+                        tma_load_2d(sa, &tmR, kb * kFp8BlockK, yr, fb);
+                        tma_load_2d(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
+                    }
+                }
+                ++it;
+                ring_advance(s, ph, S);
+            }
+        }
+        grid_launch_dependents();
+        // Teardown: the last S loads may still be in flight if a role gave up.
+        if (!kCluster || rank == 0) {
+            const int32_t n = it < S ? it : S;
+            for (int32_t d = 1; d <= n; ++d) {
+                const int32_t j = it - d;
+                if (j == p.fault_skip_it)
+                    continue;
+                ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
+                                         (uint32_t)ring_stage_of(j, S));
+            }
+        } else if (ctl.aborted()) {
+            // the peer's loads complete on the leader's barriers, which this CTA
+            // cannot poll: a fixed grace period instead
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 50000ull) {
+            }
+        }
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        // ---------------- MMA issuer ----------------
+        const uint64_t rdesc0 = smem_desc_sw128(stage0);
+        const uint64_t cdesc0 = smem_desc_sw128(stage0 + kRBytes);
+        const uint32_t idesc0 = idesc_mxf8(kFp8RowsPerCta * CG, 0) | ((uint32_t)(width >> 3) << 17);
+        const uint32_t step = stage_bytes >> 4;
+        int s = 0;
+        uint32_t ph = 0;
+        int acc = 0;
+        uint32_t acc_ph = 0;
+        uint32_t sseq = 0;  // scale words taken so far, in groups of 4 k-blocks
+        bool ok = true;
+        bool ready = false;
+        while (ok && wi.next(w)) {
+            if (!ctl.wait<kCluster>(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc)) {
+                ok = false;
+                break;
+            }
+            tc_fence_after_sync();
+            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFp8MaxWidth);
+            uint32_t stm = 0;
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                const uint32_t slot = sseq & (kFp8ScaleSlots - 1);
+                if (kb == w.kb0 || (kb & 3) == 0) {
+                    if (!ctl.wait<kCluster>(sfull_bar + 8u * slot, (sseq / kFp8ScaleSlots) & 1u, kRoleScales, slot)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after_sync();
+                    // copies and MMAs of one thread execute in order: the copy
+                    // into a buffer follows the MMAs that last read it
+                    stm = tmem_base + kFp8ScaleCol + 32u * (sseq & 1u);
+                    const uint64_t sd = smem_desc_scales(scales0 + slot * kFp8ScaleBytes);
+                    copy_scales<CG>(stm, sd);
+                    copy_scales<CG>(stm + kFp8ScaleColB, sd + (512u >> 4));
+                    if (width > 128)
+                        copy_scales<CG>(stm + kFp8ScaleColB + 4u, sd + (1024u >> 4));
+                }
+                if (!ready && !ctl.wait<kCluster>(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s)) {
+                    ok = false;
+                    break;
+                }
+                tc_fence_after_sync();
+                const uint64_t off = (uint64_t)((uint32_t)s * step);
+                const uint32_t idesc = idesc0 | scale_id((uint32_t)kb & 3u);
+#pragma unroll
+                for (int kk = 0; kk < kFp8BlockK / 32; ++kk)
+                    mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
+                                 stm + kFp8ScaleColB, (kb != w.kb0 || kk != 0) ? 1u : 0u);
+                if (ring_group_last(s, 1u)) {
+                    if constexpr (kCluster)
+                        mma_commit_pair(empty_bar + 8u * ring_group(s, 1u), (uint16_t)0x3);
+                    else
+                        mma_commit(empty_bar + 8u * ring_group(s, 1u));
+                }
+                if ((kb & 3) == 3 || kb == w.kb1 - 1) {
+                    if constexpr (kCluster)
+                        mma_commit_pair(sempty_bar + 8u * slot, (uint16_t)0x3);
+                    else
+                        mma_commit(sempty_bar + 8u * slot);
+                    ++sseq;
+                }
+                ring_advance(s, ph, S);
+                ready = mbar_try_wait<kCluster>(full_bar + 8u * s, ring_full_parity(ph), 0u);
+            }
+            if (!ok)
+                break;
+            if constexpr (kCluster)
+                mma_commit_pair(accf_bar + 8u * acc, (uint16_t)0x3);
+            else
+                mma_commit(accf_bar + 8u * acc);
+            acc ^= 1;
+            if (acc == 0)
+                acc_ph ^= 1u;
+        }
+        // no MMA may still be writing tensor memory when it is freed
+        if constexpr (kCluster)
+            mma_commit_pair(done_bar, (uint16_t)0x1);
+        else
+            mma_commit(done_bar);
+        ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+    } else if (warp == 3) {
+        // ---------------- scales ----------------
+        // A slot holds 32 rows of four words: the words of rows r, r + 32, r + 64
+        // and r + 96 of the row side at 16 r, those of the column side's rows
+        // behind them in two such blocks.  Rows past the end count as scale 1;
+        // they meet only zeros, in parts of the tile that are not stored.
+        grid_dependency_wait();
+        const uint32_t sfull_target = kCluster ? mapa_shared(sfull_bar, 0u) : sfull_bar;
+        uint32_t sseq = 0;
+        bool ok = true;
+        while (ok && wi.next(w)) {
+            const TileCoord tc = fp8_tile_coord(w.tile, p);
+            const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + lane;
+            const int32_t yc = tc.nb * width + lane;
+            const int32_t kt0 = w.kb0 >> 2, kt1 = (w.kb1 - 1) >> 2;
+            uint32_t cur[12], nxt[12];
+            auto load = [&](int32_t kt, uint32_t(&v)[12]) {
+                const uint32_t *const sr = p.s_rows + (int64_t)kt * p.rows + yr;
+                const uint32_t *const sc = p.s_cols + (int64_t)kt * p.cols + yc;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] = yr + 32 * j < p.rows ? sr[32 * j] : 0x7F7F7F7Fu;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    v[4 + j] = 32 * j < width && yc + 32 * j < p.cols ? sc[32 * j] : 0x7F7F7F7Fu;
+            };
+            load(kt0, cur);
+            for (int32_t kt = kt0; kt <= kt1; ++kt) {
+                if (kt < kt1)
+                    load(kt + 1, nxt);
+                const uint32_t slot = sseq & (kFp8ScaleSlots - 1);
+                if (!warp_wait<kCluster>(ctl, sempty_bar + 8u * slot, ((sseq / kFp8ScaleSlots) & 1u) ^ 1u, kRoleScales,
+                                         0x800u | slot, lane)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t at = scales0 + slot * kFp8ScaleBytes + 16u * (uint32_t)lane;
+                st_shared_v4(at, cur[0], cur[1], cur[2], cur[3]);
+                st_shared_v4(at + 512u, cur[4], cur[5], cur[6], cur[7]);
+                if (width > 128)
+                    st_shared_v4(at + 1024u, cur[8], cur[9], cur[10], cur[11]);
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (kCluster)
+                        mbar_arrive_cluster(sfull_target + 8u * slot);
+                    else
+                        mbar_arrive(sfull_target + 8u * slot);
+                }
+                ++sseq;
+#pragma unroll
+                for (int j = 0; j < 12; ++j)
+                    cur[j] = nxt[j];
+            }
+        }
+    } else if (warp >= 4) {
+        // ---------------- epilogue ----------------
+        grid_dependency_wait();
+        const int ew = warp - 4;
+        const int q = warp & 3;         // tensor-memory lane quadrant
+        const int half = ew >> 2;       // takes chunks half, half + 2, ... of 32 columns
+        const int nchunks = (width + 31) / 32;
+        const uint32_t staging = staging0 + (uint32_t)ew * kFp8StagingBytes;
+        const uint32_t acce_target = kCluster ? mapa_shared(acce_bar, 0u) : acce_bar;
+        const bool fp32 = p.out_fp32 != 0;
+        const int32_t cta = cluster_id * CG + (int32_t)rank;
+        int acc = 0;
+        uint32_t acc_ph = 0;
+        uint32_t item_parity = 0;
+        uint32_t buf = 0;
+        while (wi.next(w)) {
+            // one thread waits for the accumulator and posts the outcome, so that
+            // all warps take the same branch; the word alternates with the item
+            const uint32_t go = go_words + 4u * item_parity;
+            item_parity ^= 1u;
+            if (threadIdx.x == 128)
+                st_volatile_shared_u32(
+                    go, ctl.wait<kCluster>(accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc) ? 1u : 0u);
+            named_barrier_sync(1u, kFp8EpiWarps * 32u);
+            if (ld_volatile_shared_u32(go) == 0u)
+                break;
+            tc_fence_after_sync();
+            const TileCoord tc = fp8_tile_coord(w.tile, p);
+            const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + q * 32;
+            const int32_t yc = tc.nb * width;
+            const bool contributor = w.kb0 > 0;
+            const bool owner = w.kb0 == 0 && w.kb1 < KB;
+            // the clusters whose ranges start inside this tile, owner only
+            int32_t last = cluster_id;
+            bool parts = owner;
+            if (owner) {
+                while (last + 1 < num_clusters &&
+                       fp8_range_begin(p.sk_units, num_clusters, last + 1) < (int64_t)(w.tile + 1) * KB) {
+                    ++last;
+                    // a give-up stores the tile unsummed, and the status says so
+                    parts = parts && warp_wait_flag(
+                                         ctl, p.flags + (last * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u, lane);
+                }
+            }
+            for (int c = half; c < nchunks; c += 2) {
+                uint32_t v[32];
+                tmem_load_32x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kFp8MaxWidth + c * 32), v);
+                tmem_load_wait();
+                reg_fence(v);
+                if (c + 2 >= nchunks) {
+                    // this warp has read its part of the accumulator: hand it back
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        if constexpr (kCluster)
+                            mbar_arrive_cluster_handoff(acce_target + 8u * acc);
+                        else
+                            mbar_arrive(acce_bar + 8u * acc);
+                    }
+                }
+                if (contributor) {
+                    float4 *const mine = fp8_partial(p.partials, cta, ew, c >> 1, lane);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(mine + j * 32, make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                          __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])));
+                    continue;
+                }
+                if (parts) {
+                    for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
+                        const float4 *const part = fp8_partial(p.partials, j2 * CG + (int32_t)rank, ew, c >> 1, lane);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 f = __ldcg(part + j * 32);
+                            v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
+                            v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
+                            v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
+                            v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
+                        }
+                    }
+                }
+                const int32_t cols = yc + c * 32;
+                if (yr >= p.rows || cols >= p.cols)
+                    continue;
+                // the staging buffer is free once its last store has read it (or
+                // every lane has finished the masked path's loads)
+                if (lane == 0) {
+                    if (fp32)
+                        bulk_wait_read_all();
+                    else
+                        bulk_wait_read_one();
+                }
+                __syncwarp();
+                const uint32_t st = staging + (fp32 ? 0u : buf * 2048u);
+                buf ^= 1u;
+                fp8_stage_chunk<kTransposed>(v, st, (uint32_t)lane, p.cols - cols, fp32);
+                if constexpr (kTransposed)
+                    fp8_store_chunk(st, lane, &tmD, yr, cols, p);
+                else
+                    fp8_store_chunk(st, lane, &tmD, cols, yr, p);
+            }
+            if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
+                if (lane == 0) {
+                    if constexpr (kCluster)
+                        mbar_arrive_cluster_handoff(acce_target + 8u * acc);
+                    else
+                        mbar_arrive(acce_bar + 8u * acc);
+                }
+            }
+            if (contributor) {
+                __syncwarp();  // the warp's stores come before lane 0's release
+                if (lane == 0)
+                    st_release_gpu_u32(p.flags + cta * kFp8EpiWarps + ew, 1u);
+            } else if (parts) {
+                // every lane's loads have returned (their sums are stored): the
+                // flags go back to 0 for the next launch
+                __syncwarp();
+                for (int32_t j2 = cluster_id + 1 + lane; j2 <= last; j2 += 32)
+                    p.flags[(j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew] = 0u;
+            }
+            acc ^= 1;
+            if (acc == 0)
+                acc_ph ^= 1u;
+        }
+        // the staging buffers have been read before the CTA exits
+        if (lane == 0)
+            bulk_wait_read_all();
+        __syncwarp();
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before_sync();
+    __syncthreads();
+    if constexpr (kCluster)
+        cluster_arrive_wait();
+    if (warp == 2) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, 512);
+    }
+}
+
+}  // namespace wstma
