@@ -1,4 +1,5 @@
-"""Builds libgemm_bf16.so and libfp8_ops.so in-tree from csrc/ with nvcc for sm_103a.
+"""Builds the libraries in-tree from csrc/: libgemm_bf16.so and libfp8_ops.so with nvcc
+for sm_103a, and the Python binding of the latter, _fp8_bind.so, with the host compiler.
 
 The translation units compile in parallel; the CUDA runtime is linked
 statically and every symbol except the C ABIs of include/gemm_bf16.h and
@@ -21,11 +22,13 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgemm_bf16.so")
 FP8_LIB = os.path.join(PKG, "libfp8_ops.so")
+FP8_BIND = os.path.join(PKG, "_fp8_bind.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["gemm_bf16_api.cu", "gemm_ws_c1.cu", "gemm_ws_c2.cu", "gemm_nows.cu", "gemm_bf16_noalloc.cu",
            "gemm_repack.cu", "gemm_thin.cu"]
 FP8_SOURCES = ["fp8_api.cu", "fp8_gemm.cu", "fp8_quantize.cu", "fp8_norm.cu"]
+FP8_BIND_SOURCE = "fp8_bind.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
@@ -36,6 +39,31 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build the libraries")
+
+
+def cxx() -> str:
+    for cand in (shutil.which("g++"), shutil.which("c++")):
+        if cand:
+            return cand
+    raise RuntimeError("g++ not found: a host compiler is required to build the Python binding")
+
+
+def bind_flags() -> tuple:
+    """(compile flags, link flags) of the Python binding: torch's headers and libraries."""
+    import sysconfig
+
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    include = [os.path.join(root, "include"), os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    comp = ["-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden",
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
+    for path in include:
+        comp += ["-isystem", path]
+    link = ["-shared", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-L", PKG, "-lfp8_ops", "-Wl,-rpath,$ORIGIN"]
+    return comp, link
 
 
 def source_digest() -> str:
@@ -85,12 +113,13 @@ def build_stamp(cc: str | None = None) -> str:
     was linked for, the compiler and the flags.  A library built on another
     machine (an x86_64 build seen on an aarch64 host) never matches."""
     cc = cc or nvcc()
-    return "\n".join([source_digest(), "machine=" + platform.machine(), "nvcc=" + _nvcc_version(cc),
+    import torch
+    return "\n".join([source_digest(), "torch=" + torch.__version__, "machine=" + platform.machine(), "nvcc=" + _nvcc_version(cc),
                       "flags=" + " ".join(ARCH + FLAGS)])
 
 
 def up_to_date(cc: str | None = None) -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(FP8_LIB) and os.path.exists(_stamp_path())):
+    if not (os.path.exists(LIB) and os.path.exists(FP8_LIB) and os.path.exists(FP8_BIND) and os.path.exists(_stamp_path())):
         return False
     with open(_stamp_path()) as fh:
         return fh.read().strip() == build_stamp(cc)
@@ -115,19 +144,30 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(res.stderr)
         return obj
 
-    def link(lib: str, objs: list) -> None:
-        tmp = lib + f".tmp{os.getpid()}"
-        cmd = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL", "-o", tmp, *objs]
+    def compile_bind() -> str:
+        obj = os.path.join(BUILD_DIR, FP8_BIND_SOURCE.replace(".cpp", ".o"))
+        cmd = [cxx(), *bind_flags()[0], "-c", os.path.join(CSRC, FP8_BIND_SOURCE), "-o", obj]
         res = subprocess.run(cmd, capture_output=True, text=True)
+        if res.returncode != 0:
+            raise RuntimeError(f"{cmd[0]} failed on {FP8_BIND_SOURCE}:\n{res.stdout}\n{res.stderr}")
+        return obj
+
+    def link(lib: str, cmd: list) -> None:
+        tmp = lib + f".tmp{os.getpid()}"
+        res = subprocess.run([*cmd, "-o", tmp], capture_output=True, text=True)
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, lib)
 
     sources = SOURCES + FP8_SOURCES
-    with ThreadPoolExecutor(max_workers=len(sources)) as ex:
+    with ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
+        bind_obj = ex.submit(compile_bind)
         objs = list(ex.map(compile_one, sources))
-    link(LIB, objs[:len(SOURCES)])
-    link(FP8_LIB, objs[len(SOURCES):])
+        bind_obj = bind_obj.result()
+    shared = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL"]
+    link(LIB, [*shared, *objs[:len(SOURCES)]])
+    link(FP8_LIB, [*shared, *objs[len(SOURCES):]])
+    link(FP8_BIND, [cxx(), bind_obj, *bind_flags()[1]])
     with open(_stamp_path(), "w") as fh:
         fh.write(build_stamp(cc))
     return LIB
