@@ -17,9 +17,9 @@ constexpr int kFp8Block = 128;
 // amax.  Subnormal amax (and zero) ends at the least scale, 2^-127.
 __device__ __forceinline__ uint32_t scale_byte(float amax)
 {
-    const uint32_t bits = __float_as_uint(amax);
-    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return (uint32_t)(e > 0 ? e : 0);
+    // a mantissa above 0.75 carries into the exponent
+    const int e = (int)((__float_as_uint(amax) + 0x1FFFFFu) >> 23) - 8;
+    return (uint32_t)max(e, 0);
 }
 
 // 1 / 2^(byte - 127), a normal number for every byte scale_byte() gives (<= 247).

@@ -8,6 +8,12 @@
 // half-warps, whose maxima meet in shared memory.  The transposed codes are
 // turned in shared memory, so that both outputs are written in rows of 128
 // contiguous bytes.
+//
+// Memory-bound by its bytes (2 or 4 read, 1 or 2 written per element) only if it
+// spends few instructions an element.  So bf16 input stays packed in pairs: a
+// power of two scales it exactly in bf16, and maxima and products take one
+// instruction for two elements.  Scales are found with integer arithmetic on the
+// maximum's bits.
 #include <cuda_runtime.h>
 
 #include <cstdint>
@@ -22,11 +28,171 @@ namespace {
 
 constexpr int kThreads = 256;
 
-__device__ __forceinline__ float half_warp_max(float v)
+__device__ __forceinline__ uint32_t max_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t abs_bf16x2(uint32_t a)
+{
+    uint32_t r;
+    asm("abs.bf16x2 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
+
+// Both halves of a pair: infinities become NaN.
+__device__ __forceinline__ uint32_t inf_to_nan_bf16x2(uint32_t w)
+{
+    if ((w & 0x7FFFu) == 0x7F80u)
+        w |= 0x7Fu;
+    if ((w & 0x7FFF0000u) == 0x7F800000u)
+        w |= 0x7F0000u;
+    return w;
+}
+
+// A thread's 8 x 8 elements.  kPacked: bf16 pairs along the row.
+template <bool kPacked>
+struct Elements;
+
+template <>
+struct Elements<true> {
+    uint32_t v[8][4];
+
+    // rm[i], cm[c]: packed maxima of row i (two strands) and columns 2c, 2c + 1
+    __device__ __forceinline__ void maxima(uint32_t (&rm)[8], uint32_t (&cm)[4]) const
+    {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            cm[c] = 0u;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            uint32_t a[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                a[c] = abs_bf16x2(v[i][c]);
+                cm[c] = max_bf16x2(cm[c], a[c]);
+            }
+            // the zero keeps a strand of nothing but NaN from being NaN itself
+            rm[i] = max_bf16x2(max_bf16x2(max_bf16x2(a[0], a[1]), max_bf16x2(a[2], a[3])), 0u);
+        }
+    }
+
+    __device__ __forceinline__ void no_infinities()
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                v[i][c] = inf_to_nan_bf16x2(v[i][c]);
+    }
+
+    // codes of row i, scaled by 2^(127 - e)
+    __device__ __forceinline__ uint2 row_codes(int i, uint32_t e) const
+    {
+        const uint32_t s = (254u - e) << 7, up = s | (s << 16);
+        uint32_t w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+            w[c] = mul_bf16x2(v[i][c], up);
+        return make_uint2(pack_e4m3x4(bf16_lo(w[0]), bf16_hi(w[0]), bf16_lo(w[1]), bf16_hi(w[1])),
+                          pack_e4m3x4(bf16_lo(w[2]), bf16_hi(w[2]), bf16_lo(w[3]), bf16_hi(w[3])));
+    }
+
+    // codes of columns 2 c and 2 c + 1 down the rows
+    __device__ __forceinline__ void column_codes(int c, uint32_t e0, uint32_t e1, uint2 &q0, uint2 &q1) const
+    {
+        const uint32_t up = ((254u - e0) << 7) | ((254u - e1) << 23);
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            w[i] = mul_bf16x2(v[i][c], up);
+        q0 = make_uint2(pack_e4m3x4(bf16_lo(w[0]), bf16_lo(w[1]), bf16_lo(w[2]), bf16_lo(w[3])),
+                        pack_e4m3x4(bf16_lo(w[4]), bf16_lo(w[5]), bf16_lo(w[6]), bf16_lo(w[7])));
+        q1 = make_uint2(pack_e4m3x4(bf16_hi(w[0]), bf16_hi(w[1]), bf16_hi(w[2]), bf16_hi(w[3])),
+                        pack_e4m3x4(bf16_hi(w[4]), bf16_hi(w[5]), bf16_hi(w[6]), bf16_hi(w[7])));
+    }
+};
+
+template <>
+struct Elements<false> {
+    float y[8][8];
+
+    // maxima rounded up to bf16 pairs would lose the fp32 value that decides the
+    // scale, so these are fp32 bits: rm[i] of row i, cm[j] of column j
+    __device__ __forceinline__ void maxima(uint32_t (&rm)[8], uint32_t (&cm)[8]) const
+    {
+        float c[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            c[j] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float r = 0.f;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                r = fmaxf(r, fabsf(y[i][j]));
+                c[j] = fmaxf(c[j], fabsf(y[i][j]));
+            }
+            rm[i] = __float_as_uint(r);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            cm[j] = __float_as_uint(c[j]);
+    }
+
+    __device__ __forceinline__ void no_infinities()
+    {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                y[i][j] = inf_to_nan(y[i][j]);
+    }
+
+    __device__ __forceinline__ uint2 row_codes(int i, uint32_t e) const
+    {
+        const float up = scale_inverse(e);
+        return make_uint2(pack_e4m3x4(y[i][0] * up, y[i][1] * up, y[i][2] * up, y[i][3] * up),
+                          pack_e4m3x4(y[i][4] * up, y[i][5] * up, y[i][6] * up, y[i][7] * up));
+    }
+
+    __device__ __forceinline__ void column_codes(int c, uint32_t e0, uint32_t e1, uint2 &q0, uint2 &q1) const
+    {
+        const float u0 = scale_inverse(e0), u1 = scale_inverse(e1);
+        const int a = 2 * c, b = 2 * c + 1;
+        q0 = make_uint2(pack_e4m3x4(y[0][a] * u0, y[1][a] * u0, y[2][a] * u0, y[3][a] * u0),
+                        pack_e4m3x4(y[4][a] * u0, y[5][a] * u0, y[6][a] * u0, y[7][a] * u0));
+        q1 = make_uint2(pack_e4m3x4(y[0][b] * u1, y[1][b] * u1, y[2][b] * u1, y[3][b] * u1),
+                        pack_e4m3x4(y[4][b] * u1, y[5][b] * u1, y[6][b] * u1, y[7][b] * u1));
+    }
+};
+
+// Magnitudes (no NaN) order like their bits, so maxima travel as integers from here on.
+__device__ __forceinline__ uint32_t half_warp_max(uint32_t v)
 {
 #pragma unroll
     for (int d = 8; d > 0; d >>= 1)
-        v = fmaxf(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+        v = max(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t half_warp_max_bf16x2(uint32_t v)
+{
+#pragma unroll
+    for (int d = 8; d > 0; d >>= 1)
+        v = max_bf16x2(v, __shfl_xor_sync(0xFFFFFFFFu, v, d));
     return v;
 }
 
@@ -41,11 +207,24 @@ __device__ __forceinline__ void store_scale(uint8_t *scales, int64_t rows, int64
             word[b] = 127;
 }
 
-template <bool kFp32, bool kRows, bool kCols>
-__global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantizeParams p)
+// a, b, c, d: rows of four bytes -> columns of four bytes.
+__device__ __forceinline__ void transpose_bytes(uint32_t &a, uint32_t &b, uint32_t &c, uint32_t &d)
 {
-    __shared__ float colmax[kCols ? 16 : 1][kFp8Block];
-    __shared__ float tilemax[kThreads / 32];
+    const uint32_t ab0 = __byte_perm(a, b, 0x5140), ab1 = __byte_perm(a, b, 0x7362);
+    const uint32_t cd0 = __byte_perm(c, d, 0x5140), cd1 = __byte_perm(c, d, 0x7362);
+    a = __byte_perm(ab0, cd0, 0x5410);
+    b = __byte_perm(ab0, cd0, 0x7632);
+    c = __byte_perm(ab1, cd1, 0x5410);
+    d = __byte_perm(ab1, cd1, 0x7632);
+}
+
+// kPacked: bf16 input without factors; else fp32 arithmetic on either type.
+template <bool kPacked, bool kRows, bool kCols>
+__global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2) quantize_kernel(const QuantizeParams p)
+{
+    // a warp's column maxima: bf16 of 128 columns (packed) or fp32
+    __shared__ __align__(16) uint32_t colmax[kCols ? kThreads / 32 : 1][kPacked ? 64 : 128];
+    __shared__ uint32_t tilemax[kThreads / 32];
     __shared__ __align__(16) uint8_t turned[kCols ? kFp8Block * kFp8Block : 16];
     grid_dependency_wait();
     grid_launch_dependents();
@@ -54,146 +233,232 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantizeParams
     const int32_t rb = (int32_t)(blockIdx.x / col_tiles), cb = (int32_t)(blockIdx.x % col_tiles);
     const int32_t r0 = rb * kFp8Block + g * 8, c0 = cb * kFp8Block + l * 8;
     const int32_t R = p.R, C = p.C;
+    const bool full = (rb + 1) * (int64_t)kFp8Block <= R && (cb + 1) * (int64_t)kFp8Block <= C;
 
-    float y[8][8];
+    Elements<kPacked> y;
+    if constexpr (kPacked) {
+        const uint16_t *const x = static_cast<const uint16_t *>(p.x) + (int64_t)r0 * p.ldx;
+        if (full && p.x_vec) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int64_t r = r0 + i;
-        if (r < R && c0 < C) {
-            if constexpr (kFp32)
-                load8_float(static_cast<const float *>(p.x) + r * p.ldx, c0, C, p.x_vec, y[i]);
-            else
-                unpack8(load8_bf16(static_cast<const uint16_t *>(p.x) + r * p.ldx, c0, C, p.x_vec), y[i]);
-            if (p.row_factor) {
-                const float f = p.row_factor[r];
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    y[i][j] *= f;
+            for (int i = 0; i < 8; ++i) {
+                const uint4 q = *reinterpret_cast<const uint4 *>(x + i * p.ldx + c0);
+                y.v[i][0] = q.x, y.v[i][1] = q.y, y.v[i][2] = q.z, y.v[i][3] = q.w;
             }
         } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[i][j] = 0.f;
+            for (int i = 0; i < 8; ++i) {
+                uint4 q = make_uint4(0u, 0u, 0u, 0u);
+                if (r0 + i < R && c0 < C)
+                    q = load8_bf16(x + i * p.ldx, c0, C, p.x_vec);
+                y.v[i][0] = q.x, y.v[i][1] = q.y, y.v[i][2] = q.z, y.v[i][3] = q.w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int64_t r = r0 + i;
+            if (r < R && c0 < C) {
+                if (p.x_fp32)
+                    load8_float(static_cast<const float *>(p.x) + r * p.ldx, c0, C, p.x_vec, y.y[i]);
+                else
+                    unpack8(load8_bf16(static_cast<const uint16_t *>(p.x) + r * p.ldx, c0, C, p.x_vec), y.y[i]);
+                if (p.row_factor) {
+                    const float f = p.row_factor[r];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        y.y[i][j] *= f;
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y.y[i][j] = 0.f;
+            }
+        }
+        if (p.column_factor && c0 < C) {
+            float f[8];
+            if (p.column_fp32)
+                load8_float(static_cast<const float *>(p.column_factor), c0, C, false, f);
+            else
+                unpack8(load8_bf16(static_cast<const uint16_t *>(p.column_factor), c0, C, false), f);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y.y[i][j] *= c0 + j < C ? f[j] : 0.f;
         }
     }
-    if (p.column_factor && c0 < C) {
-        float f[8];
-        if (p.column_fp32)
-            load8_float(static_cast<const float *>(p.column_factor), c0, C, false, f);
-        else
-            unpack8(load8_bf16(static_cast<const uint16_t *>(p.column_factor), c0, C, false), f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[i][j] *= c0 + j < C ? f[j] : 0.f;
-    }
 
-    // Infinities are rare: one vote for the CTA decides whether they become NaN
-    // here, so that the maxima below are over finite values.
+    // Maxima pass over NaN.  An infinity shows in them: rare, and then the tile's
+    // infinities become NaN and the maxima are those of its finite values.
+    constexpr int kColWords = kPacked ? 4 : 8;
+    uint32_t rm[8], cm[kColWords];
+    y.maxima(rm, cm);
     bool inf = false;
 #pragma unroll
     for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-            inf = inf || is_inf(y[i][j]);
-    if (inf) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                y[i][j] = inf_to_nan(y[i][j]);
+        inf = inf || (kPacked ? (rm[i] & 0x7F800000u) == 0x7F800000u || (rm[i] & 0x7F80u) == 0x7F80u
+                              : rm[i] == 0x7F800000u);
+    if (kCols || p.tile ? __syncthreads_or(inf) : __any_sync(0xFFFFFFFFu, inf)) {
+        y.no_infinities();
+        y.maxima(rm, cm);
     }
 
-    float rmax[8], cmax[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        cmax[j] = 0.f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        rmax[i] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            rmax[i] = fmaxf(rmax[i], fabsf(y[i][j]));
-            cmax[j] = fmaxf(cmax[j], fabsf(y[i][j]));
-        }
-    }
-
+    uint32_t re[8], ce[8];  // scale bytes of the thread's rows and columns
     if (p.tile) {
-        float m = 0.f;
+        uint32_t m = 0u;
+        if constexpr (kPacked) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            m = fmaxf(m, rmax[i]);
-        m = half_warp_max(m);
-        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, 16));
+            for (int i = 0; i < 8; ++i)
+                m = i ? max_bf16x2(m, rm[i]) : rm[i];
+            m = max(m & 0xFFFFu, m >> 16) << 16;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                m = max(m, rm[i]);
+        }
+        m = __reduce_max_sync(0xFFFFFFFFu, m);
         if ((threadIdx.x & 31) == 0)
             tilemax[threadIdx.x >> 5] = m;
         __syncthreads();
 #pragma unroll
         for (int k = 0; k < kThreads / 32; ++k)
-            m = fmaxf(m, tilemax[k]);
+            m = max(m, tilemax[k]);
+        const uint32_t e = scale_byte(__uint_as_float(m));
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            rmax[i] = cmax[i] = m;
+            re[i] = ce[i] = e;
     } else {
         if constexpr (kRows) {
+            if constexpr (kPacked) {
+                // two rows to a word: half the shuffles
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                rmax[i] = half_warp_max(rmax[i]);
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t m = half_warp_max_bf16x2(
+                        max_bf16x2(__byte_perm(rm[i], rm[i + 1], 0x5410), __byte_perm(rm[i], rm[i + 1], 0x7632)));
+                    re[i] = scale_byte(bf16_lo(m));
+                    re[i + 1] = scale_byte(bf16_hi(m));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    re[i] = scale_byte(__uint_as_float(half_warp_max(rm[i])));
+            }
         }
         if constexpr (kCols) {
+            const int warp = threadIdx.x >> 5;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                colmax[g][l * 8 + j] = cmax[j];
+            for (int c = 0; c < kColWords; ++c) {
+                const uint32_t o = __shfl_xor_sync(0xFFFFFFFFu, cm[c], 16);
+                cm[c] = kPacked ? max_bf16x2(cm[c], o) : max(cm[c], o);
+            }
+            if ((threadIdx.x & 16) == 0) {
+#pragma unroll
+                for (int c = 0; c < kColWords; c += 4)
+                    *reinterpret_cast<uint4 *>(&colmax[warp][l * kColWords + c]) =
+                        make_uint4(cm[c], cm[c + 1], cm[c + 2], cm[c + 3]);
+            }
             __syncthreads();
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
+            for (int k = 0; k < kThreads / 32; ++k)
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                    cmax[j] = fmaxf(cmax[j], colmax[k][l * 8 + j]);
+                for (int c = 0; c < kColWords; c += 4) {
+                    const uint4 o = *reinterpret_cast<const uint4 *>(&colmax[k][l * kColWords + c]);
+                    const uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+                    for (int d = 0; d < 4; ++d)
+                        cm[c + d] = kPacked ? max_bf16x2(cm[c + d], w[d]) : max(cm[c + d], w[d]);
+                }
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                ce[j] = scale_byte(kPacked ? (j & 1 ? bf16_hi(cm[j >> 1]) : bf16_lo(cm[j >> 1]))
+                                           : __uint_as_float(cm[kPacked ? 0 : j]));
         }
     }
 
+    // lane l < 8 of a half-warp stores the scale of its row l; group g < 8 that of column g
+    const int32_t KB = (C + kFp8Block - 1) / kFp8Block, KBt = (R + kFp8Block - 1) / kFp8Block;
     if constexpr (kRows) {
-        const int32_t KB = (C + kFp8Block - 1) / kFp8Block;
+        uint32_t e = re[0];
+#pragma unroll
+        for (int i = 1; i < 8; ++i)
+            e = l == i ? re[i] : e;
+        if (l < 8 && r0 + l < R)
+            store_scale(p.scales, R, r0 + l, cb, KB, e);
+    }
+    if constexpr (kCols) {
+        uint32_t e = ce[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            e = g == j ? ce[j] : e;
+        if (g < 8 && c0 + g < C)
+            store_scale(p.scales_t, C, c0 + g, rb, KBt, e);
+    }
+
+    uint8_t *const turn = turned + ((g ^ l) << 3) + l * 8 * kFp8Block;  // + j * kFp8Block: column j
+    if (kRows && kCols && p.tile) {
+        // one scale: the row codes are the column codes, turned 4 x 4 bytes at a time
+        uint2 q[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t r = r0 + i;
-            if (r >= R)
-                break;
-            const uint32_t e = scale_byte(rmax[i]);
-            const float up = scale_inverse(e);
-            if (c0 < C)
-                store8_codes(p.codes + r * p.ldq, c0, C,
-                             make_uint2(pack_e4m3x4(y[i][0] * up, y[i][1] * up, y[i][2] * up, y[i][3] * up),
-                                        pack_e4m3x4(y[i][4] * up, y[i][5] * up, y[i][6] * up, y[i][7] * up)));
-            if (l == 0)
-                store_scale(p.scales, R, r, cb, KB, e);
+            q[i] = y.row_codes(i, re[0]);
+            if (full)
+                *reinterpret_cast<uint2 *>(p.codes + (int64_t)(r0 + i) * p.ldq + c0) = q[i];
+            else if (r0 + i < R && c0 < C)
+                store8_codes(p.codes + (int64_t)(r0 + i) * p.ldq, c0, C, q[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i += 4) {
+            transpose_bytes(q[i].x, q[i + 1].x, q[i + 2].x, q[i + 3].x);
+            transpose_bytes(q[i].y, q[i + 1].y, q[i + 2].y, q[i + 3].y);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            *reinterpret_cast<uint2 *>(turn + j * kFp8Block) = make_uint2(q[j].x, q[4 + j].x);
+            *reinterpret_cast<uint2 *>(turn + (4 + j) * kFp8Block) = make_uint2(q[j].y, q[4 + j].y);
+        }
+    } else {
+        if constexpr (kRows) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint2 q = y.row_codes(i, re[i]);
+                if (full)
+                    *reinterpret_cast<uint2 *>(p.codes + (int64_t)(r0 + i) * p.ldq + c0) = q;
+                else if (r0 + i < R && c0 < C)
+                    store8_codes(p.codes + (int64_t)(r0 + i) * p.ldq, c0, C, q);
+            }
+        }
+        if constexpr (kCols) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                uint2 q0, q1;
+                y.column_codes(c, ce[2 * c], ce[2 * c + 1], q0, q1);
+                *reinterpret_cast<uint2 *>(turn + 2 * c * kFp8Block) = q0;
+                *reinterpret_cast<uint2 *>(turn + (2 * c + 1) * kFp8Block) = q1;
+            }
         }
     }
     if constexpr (kCols) {
-        // row c of the turned tile: 16 units of 8 bytes, unit u at u ^ (c / 8)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const uint32_t e = scale_byte(cmax[j]);
-            const float up = scale_inverse(e);
-            const uint2 q = make_uint2(pack_e4m3x4(y[0][j] * up, y[1][j] * up, y[2][j] * up, y[3][j] * up),
-                                       pack_e4m3x4(y[4][j] * up, y[5][j] * up, y[6][j] * up, y[7][j] * up));
-            *reinterpret_cast<uint2 *>(turned + (l * 8 + j) * kFp8Block + ((g ^ l) << 3)) = q;
-            if (g == 0 && c0 + j < C)
-                store_scale(p.scales_t, C, c0 + j, rb, (R + kFp8Block - 1) / kFp8Block, e);
-        }
+        // row c of the turned tile: 16 units of 8 bytes, unit u at u ^ (c / 8); the
+        // half-warp g writes its rows 8 g .. 8 g + 7, 8 bytes a lane
         __syncthreads();
-        // half-warp g writes rows 8 g .. 8 g + 7 of the turned tile, 8 bytes a lane
         const int32_t rl = rb * kFp8Block + l * 8;
+        const int64_t cg = (int64_t)cb * kFp8Block + g * 8;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            const int64_t c = (int64_t)cb * kFp8Block + g * 8 + i;
-            if (c < C && rl < R)
-                store8_codes(p.codes_t + c * p.ldqt, rl, R,
-                             *reinterpret_cast<const uint2 *>(turned + (g * 8 + i) * kFp8Block + ((l ^ g) << 3)));
+            const uint2 q = *reinterpret_cast<const uint2 *>(turned + (g * 8 + i) * kFp8Block + ((l ^ g) << 3));
+            if (full)
+                *reinterpret_cast<uint2 *>(p.codes_t + (cg + i) * p.ldqt + rl) = q;
+            else if (cg + i < C && rl < R)
+                store8_codes(p.codes_t + (cg + i) * p.ldqt, rl, R, q);
         }
     }
+}
+
+template <bool kPacked>
+auto quantize_fn(bool rows, bool cols)
+{
+    return rows ? (cols ? &quantize_kernel<kPacked, true, true> : &quantize_kernel<kPacked, true, false>)
+                : &quantize_kernel<kPacked, false, true>;
 }
 
 }  // namespace
@@ -201,13 +466,8 @@ __global__ void __launch_bounds__(kThreads) quantize_kernel(const QuantizeParams
 int launch_quantize(const QuantizeParams &p, cudaStream_t stream)
 {
     const bool rows = p.codes != nullptr, cols = p.codes_t != nullptr;
-    void (*fn)(QuantizeParams) = nullptr;
-    if (p.x_fp32)
-        fn = rows ? (cols ? &quantize_kernel<true, true, true> : &quantize_kernel<true, true, false>)
-                  : &quantize_kernel<true, false, true>;
-    else
-        fn = rows ? (cols ? &quantize_kernel<false, true, true> : &quantize_kernel<false, true, false>)
-                  : &quantize_kernel<false, false, true>;
+    const bool packed = !p.x_fp32 && !p.row_factor && !p.column_factor;
+    auto fn = packed ? quantize_fn<true>(rows, cols) : quantize_fn<false>(rows, cols);
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     const int64_t tiles = (((int64_t)p.C + kFp8Block - 1) / kFp8Block) * (((int64_t)p.R + kFp8Block - 1) / kFp8Block);
