@@ -644,6 +644,7 @@ FP8_API int fp8_quantize(const void *x, int x_type, int64_t ldx, int64_t R, int6
     p.column_factor = column_factor;
     p.column_fp32 = column_type == FP8_FP32 ? 1 : 0;
     p.x_vec = aligned(x, 16) && (ldx * (int64_t)esize) % 16 == 0 ? 1 : 0;
+    p.column_vec = aligned(column_factor, 16) ? 1 : 0;
     p.codes = static_cast<uint8_t *>(codes);
     p.ldq = ldq;
     p.scales = static_cast<uint8_t *>(scales);

@@ -79,6 +79,49 @@ __device__ __forceinline__ uint4 load8_bf16(const uint16_t *row, int32_t c, int3
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// The same from a row that is only 2-byte aligned: the 16 lanes of a half-warp
+// (all of them call this) hold the vectors of 128 consecutive columns, lane l
+// columns c = c0 + 8 l.  Each loads the aligned 16 bytes its vector starts in and
+// takes the rest from its neighbour.  Only 16-byte granules that hold a byte of
+// the row are read.
+__device__ __forceinline__ uint4 load8_bf16_shifted(const uint16_t *row, int32_t c, int32_t C, bool live)
+{
+    const int l = (int)(threadIdx.x & 15u);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const uintptr_t end = reinterpret_cast<uintptr_t>(row + C);
+    const uint32_t mis = (uint32_t)(at & 15u);
+    const uintptr_t granule = at - mis;
+    uint32_t w[8];
+    uint4 q = make_uint4(0u, 0u, 0u, 0u), x = q;
+    if (live && granule < end)
+        q = *reinterpret_cast<const uint4 *>(granule);
+    if (live && l == 15 && mis != 0u && granule + 16 < end)
+        x = *reinterpret_cast<const uint4 *>(granule + 16);
+    w[0] = q.x, w[1] = q.y, w[2] = q.z, w[3] = q.w;
+    const uint32_t extra[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const uint32_t n = __shfl_down_sync(0xFFFFFFFFu, w[k], 1, 16);
+        w[4 + k] = l == 15 ? extra[k] : n;
+    }
+    // shift right by mis bytes: two words, one word, half a word
+#pragma unroll
+    for (int k = 0; k < 6; ++k)
+        w[k] = mis & 8u ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        w[k] = mis & 4u ? w[k + 1] : w[k];
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[k] = __funnelshift_r(w[k], w[k + 1], (mis & 2u) * 8u);
+        // columns past the end
+        if (c + 2 * k + 1 >= C)
+            o[k] = c + 2 * k < C ? o[k] & 0xFFFFu : 0u;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 __device__ __forceinline__ void load8_float(const float *row, int32_t c, int32_t C, bool vec, float (&f)[8])
 {
     if (vec && c + 8 <= C) {

@@ -19,7 +19,8 @@ struct QuantizeParams {
     const float *row_factor;
     const void *column_factor;
     int32_t column_fp32;
-    int32_t x_vec;  // rows of x are 16-byte aligned
+    int32_t x_vec;       // rows of x are 16-byte aligned
+    int32_t column_vec;  // column_factor is
     uint8_t *codes;
     int64_t ldq;
     uint8_t *scales;

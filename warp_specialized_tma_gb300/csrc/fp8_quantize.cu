@@ -62,12 +62,16 @@ __device__ __forceinline__ uint32_t inf_to_nan_bf16x2(uint32_t w)
     return w;
 }
 
-// A thread's 8 x 8 elements.  kPacked: bf16 pairs along the row.
-template <bool kPacked>
+// How a thread holds its 8 x 8 elements: bf16 pairs along the row; the same with
+// factors, applied in fp32 wherever a value is used (holding 64 products instead
+// costs half the occupancy); fp32.
+enum { kPairs = 0, kFactored = 1, kFloats = 2 };
+
+template <int kMode>
 struct Elements;
 
 template <>
-struct Elements<true> {
+struct Elements<kPairs> {
     uint32_t v[8][4];
 
     // rm[i], cm[c]: packed maxima of row i (two strands) and columns 2c, 2c + 1
@@ -125,14 +129,14 @@ struct Elements<true> {
     }
 };
 
-template <>
-struct Elements<false> {
-    float y[8][8];
-
-    // maxima rounded up to bf16 pairs would lose the fp32 value that decides the
+// What the two fp32 forms share, over their at(i, j).
+template <typename Self>
+struct FloatElements {
+    // maxima rounded to bf16 pairs would lose the fp32 value that decides the
     // scale, so these are fp32 bits: rm[i] of row i, cm[j] of column j
     __device__ __forceinline__ void maxima(uint32_t (&rm)[8], uint32_t (&cm)[8]) const
     {
+        const Self &self = static_cast<const Self &>(*this);
         float c[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -142,8 +146,9 @@ struct Elements<false> {
             float r = 0.f;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                r = fmaxf(r, fabsf(y[i][j]));
-                c[j] = fmaxf(c[j], fabsf(y[i][j]));
+                const float a = fabsf(self.at(i, j));
+                r = fmaxf(r, a);
+                c[j] = fmaxf(c[j], a);
             }
             rm[i] = __float_as_uint(r);
         }
@@ -151,6 +156,37 @@ struct Elements<false> {
         for (int j = 0; j < 8; ++j)
             cm[j] = __float_as_uint(c[j]);
     }
+
+    __device__ __forceinline__ uint2 row_codes(int i, uint32_t e) const
+    {
+        const Self &self = static_cast<const Self &>(*this);
+        const float up = scale_inverse(e);
+        return make_uint2(
+            pack_e4m3x4(self.at(i, 0) * up, self.at(i, 1) * up, self.at(i, 2) * up, self.at(i, 3) * up),
+            pack_e4m3x4(self.at(i, 4) * up, self.at(i, 5) * up, self.at(i, 6) * up, self.at(i, 7) * up));
+    }
+
+    __device__ __forceinline__ uint2 one_column(int j, uint32_t e) const
+    {
+        const Self &self = static_cast<const Self &>(*this);
+        const float up = scale_inverse(e);
+        return make_uint2(
+            pack_e4m3x4(self.at(0, j) * up, self.at(1, j) * up, self.at(2, j) * up, self.at(3, j) * up),
+            pack_e4m3x4(self.at(4, j) * up, self.at(5, j) * up, self.at(6, j) * up, self.at(7, j) * up));
+    }
+
+    __device__ __forceinline__ void column_codes(int c, uint32_t e0, uint32_t e1, uint2 &q0, uint2 &q1) const
+    {
+        q0 = one_column(2 * c, e0);
+        q1 = one_column(2 * c + 1, e1);
+    }
+};
+
+template <>
+struct Elements<kFloats> : FloatElements<Elements<kFloats>> {
+    float y[8][8];
+
+    __device__ __forceinline__ float at(int i, int j) const { return y[i][j]; }
 
     __device__ __forceinline__ void no_infinities()
     {
@@ -160,22 +196,27 @@ struct Elements<false> {
             for (int j = 0; j < 8; ++j)
                 y[i][j] = inf_to_nan(y[i][j]);
     }
+};
 
-    __device__ __forceinline__ uint2 row_codes(int i, uint32_t e) const
+template <>
+struct Elements<kFactored> : FloatElements<Elements<kFactored>> {
+    uint32_t v[8][4];
+    float rf[8], cf[8];
+
+    __device__ __forceinline__ float at(int i, int j) const
     {
-        const float up = scale_inverse(e);
-        return make_uint2(pack_e4m3x4(y[i][0] * up, y[i][1] * up, y[i][2] * up, y[i][3] * up),
-                          pack_e4m3x4(y[i][4] * up, y[i][5] * up, y[i][6] * up, y[i][7] * up));
+        return (j & 1 ? bf16_hi(v[i][j >> 1]) : bf16_lo(v[i][j >> 1])) * rf[i] * cf[j];
     }
 
-    __device__ __forceinline__ void column_codes(int c, uint32_t e0, uint32_t e1, uint2 &q0, uint2 &q1) const
+    // an element whose product is infinite becomes NaN, and so does its product
+    __device__ __forceinline__ void no_infinities()
     {
-        const float u0 = scale_inverse(e0), u1 = scale_inverse(e1);
-        const int a = 2 * c, b = 2 * c + 1;
-        q0 = make_uint2(pack_e4m3x4(y[0][a] * u0, y[1][a] * u0, y[2][a] * u0, y[3][a] * u0),
-                        pack_e4m3x4(y[4][a] * u0, y[5][a] * u0, y[6][a] * u0, y[7][a] * u0));
-        q1 = make_uint2(pack_e4m3x4(y[0][b] * u1, y[1][b] * u1, y[2][b] * u1, y[3][b] * u1),
-                        pack_e4m3x4(y[4][b] * u1, y[5][b] * u1, y[6][b] * u1, y[7][b] * u1));
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (is_inf(at(i, j)))
+                    v[i][j >> 1] |= j & 1 ? 0x7FFF0000u : 0x7FFFu;
     }
 };
 
@@ -218,10 +259,23 @@ __device__ __forceinline__ void transpose_bytes(uint32_t &a, uint32_t &b, uint32
     d = __byte_perm(ab1, cd1, 0x7632);
 }
 
-// kPacked: bf16 input without factors; else fp32 arithmetic on either type.
-template <bool kPacked, bool kRows, bool kCols>
-__global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2) quantize_kernel(const QuantizeParams p)
+__device__ __forceinline__ void load_column_factor(const QuantizeParams &p, int32_t c, float (&f)[8])
 {
+    if (!p.column_factor || c >= p.C) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            f[j] = 1.f;
+    } else if (p.column_fp32) {
+        load8_float(static_cast<const float *>(p.column_factor), c, p.C, p.column_vec, f);
+    } else {
+        unpack8(load8_bf16(static_cast<const uint16_t *>(p.column_factor), c, p.C, p.column_vec), f);
+    }
+}
+
+template <int kMode, bool kRows, bool kCols>
+__global__ void __launch_bounds__(kThreads, kMode == kFloats ? 2 : 3) quantize_kernel(const QuantizeParams p)
+{
+    constexpr bool kPacked = kMode == kPairs;  // maxima as bf16 pairs, else as fp32
     // a warp's column maxima: bf16 of 128 columns (packed) or fp32
     __shared__ __align__(16) uint32_t colmax[kCols ? kThreads / 32 : 1][kPacked ? 64 : 128];
     __shared__ uint32_t tilemax[kThreads / 32];
@@ -235,8 +289,8 @@ __global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2) quantize_kernel(con
     const int32_t R = p.R, C = p.C;
     const bool full = (rb + 1) * (int64_t)kFp8Block <= R && (cb + 1) * (int64_t)kFp8Block <= C;
 
-    Elements<kPacked> y;
-    if constexpr (kPacked) {
+    Elements<kMode> y;
+    if constexpr (kMode != kFloats) {
         const uint16_t *const x = static_cast<const uint16_t *>(p.x) + (int64_t)r0 * p.ldx;
         if (full && p.x_vec) {
 #pragma unroll
@@ -247,44 +301,45 @@ __global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2) quantize_kernel(con
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                uint4 q = make_uint4(0u, 0u, 0u, 0u);
-                if (r0 + i < R && c0 < C)
-                    q = load8_bf16(x + i * p.ldx, c0, C, p.x_vec);
+                const uint4 q = load8_bf16_shifted(x + i * p.ldx, c0, C, r0 + i < R);
                 y.v[i][0] = q.x, y.v[i][1] = q.y, y.v[i][2] = q.z, y.v[i][3] = q.w;
             }
+        }
+        if constexpr (kMode == kFactored) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                y.rf[i] = p.row_factor && r0 + i < R ? p.row_factor[r0 + i] : 1.f;
+            load_column_factor(p, c0, y.cf);
         }
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int64_t r = r0 + i;
             if (r < R && c0 < C) {
-                if (p.x_fp32)
-                    load8_float(static_cast<const float *>(p.x) + r * p.ldx, c0, C, p.x_vec, y.y[i]);
-                else
-                    unpack8(load8_bf16(static_cast<const uint16_t *>(p.x) + r * p.ldx, c0, C, p.x_vec), y.y[i]);
-                if (p.row_factor) {
-                    const float f = p.row_factor[r];
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        y.y[i][j] *= f;
-                }
+                load8_float(static_cast<const float *>(p.x) + r * p.ldx, c0, C, p.x_vec, y.y[i]);
             } else {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     y.y[i][j] = 0.f;
             }
         }
-        if (p.column_factor && c0 < C) {
-            float f[8];
-            if (p.column_fp32)
-                load8_float(static_cast<const float *>(p.column_factor), c0, C, false, f);
-            else
-                unpack8(load8_bf16(static_cast<const uint16_t *>(p.column_factor), c0, C, false), f);
+        if (p.row_factor) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float f = r0 + i < R ? p.row_factor[r0 + i] : 1.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    y.y[i][j] *= f;
+            }
+        }
+        if (p.column_factor) {
+            float cf[8];
+            load_column_factor(p, c0, cf);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
-                    y.y[i][j] *= c0 + j < C ? f[j] : 0.f;
+                    y.y[i][j] *= cf[j];
         }
     }
 
@@ -454,11 +509,11 @@ __global__ void __launch_bounds__(kThreads, kPacked ? 3 : 2) quantize_kernel(con
     }
 }
 
-template <bool kPacked>
+template <int kMode>
 auto quantize_fn(bool rows, bool cols)
 {
-    return rows ? (cols ? &quantize_kernel<kPacked, true, true> : &quantize_kernel<kPacked, true, false>)
-                : &quantize_kernel<kPacked, false, true>;
+    return rows ? (cols ? &quantize_kernel<kMode, true, true> : &quantize_kernel<kMode, true, false>)
+                : &quantize_kernel<kMode, false, true>;
 }
 
 }  // namespace
@@ -466,8 +521,9 @@ auto quantize_fn(bool rows, bool cols)
 int launch_quantize(const QuantizeParams &p, cudaStream_t stream)
 {
     const bool rows = p.codes != nullptr, cols = p.codes_t != nullptr;
-    const bool packed = !p.x_fp32 && !p.row_factor && !p.column_factor;
-    auto fn = packed ? quantize_fn<true>(rows, cols) : quantize_fn<false>(rows, cols);
+    auto fn = p.x_fp32 ? quantize_fn<kFloats>(rows, cols)
+                       : (p.row_factor || p.column_factor ? quantize_fn<kFactored>(rows, cols)
+                                                          : quantize_fn<kPairs>(rows, cols));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     const int64_t tiles = (((int64_t)p.C + kFp8Block - 1) / kFp8Block) * (((int64_t)p.R + kFp8Block - 1) / kFp8Block);
