@@ -56,8 +56,9 @@ typedef enum fp8_gemm_option {
                                      a multiple of 16 (32 for SM pairs), at most 224 */
     FP8_GEMM_OPT_SPLIT = 4,       /* 1 = tiles that would leave SMs idle are split along K (default), 0 = never */
     FP8_GEMM_OPT_WATCHDOG_NS = 5, /* limit of any wait inside the kernel (default 2e9) */
-    FP8_GEMM_OPT_FAULT_SKIP_LOAD = 6 /* test hook: each producer leaves out this load (-1 = none), so that
-                                        a bounded wait runs out and the call reports DEVICE_TIMEOUT */
+    FP8_GEMM_OPT_FAULT_SKIP_LOAD = 6, /* test hook: each producer leaves out this load (-1 = none), so that
+                                         a bounded wait runs out and the call reports DEVICE_TIMEOUT */
+    FP8_GEMM_OPT_RASTER_GROUP = 7 /* tiles are walked in bands of this many row tiles; 0 = automatic */
 } fp8_gemm_option;
 
 typedef struct fp8_gemm *fp8_gemm_t;

@@ -20,7 +20,7 @@ namespace {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL;
 constexpr int64_t kMaxPitch = int64_t(1) << 38;
-constexpr int kNumOptions = 7;
+constexpr int kNumOptions = 8;
 constexpr int kPlans = 32;          // plans a handle remembers
 constexpr int kMaxCtas = 1024;      // bounds the workspace of split tiles
 constexpr int64_t kMinSplitBlocks = 4;  // k-blocks per cluster below which tiles are not split further
@@ -53,7 +53,7 @@ struct fp8_gemm {
     uint32_t *d_err = nullptr;
     float *partials = nullptr;  // allocated by the first plan that splits tiles, at its final size
     uint32_t *flags = nullptr;
-    int64_t opt[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1};
+    int64_t opt[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0};
     Plan plans[kPlans];
     Plan *plan = nullptr;
     uint64_t clock = 0;
@@ -408,6 +408,7 @@ FP8_API int fp8_gemm_set_option(fp8_gemm_t h, int key, int64_t value)
     case FP8_GEMM_OPT_SPLIT: ok = value == 0 || value == 1; break;
     case FP8_GEMM_OPT_WATCHDOG_NS: ok = value >= 1000 && value <= 60000000000LL; break;
     case FP8_GEMM_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
+    case FP8_GEMM_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
     default: break;
     }
     if (!ok)
@@ -539,7 +540,7 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     p.num_row_tiles = (int32_t)pl.row_tiles;
     p.num_col_tiles = (int32_t)pl.col_tiles;
     p.num_tiles = (int32_t)pl.tiles;
-    p.raster_group = 8;
+    p.raster_group = h->opt[FP8_GEMM_OPT_RASTER_GROUP] ? (int32_t)h->opt[FP8_GEMM_OPT_RASTER_GROUP] : 8;
     p.width = pl.width;
     p.stages = pl.stages;
     p.sk_tiles = (int32_t)pl.sk_tiles;

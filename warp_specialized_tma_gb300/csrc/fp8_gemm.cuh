@@ -14,9 +14,10 @@
 //
 // Roles (384 threads, one CTA per SM):
 //   warp 0, lane 0   TMA producer: per (item, k-block) wait "empty", load both tiles
-//   warp 1, lane 0   MMA issuer (leader CTA only in pairs)
-//   warp 2           allocates and frees tensor memory
-//   warp 3           scales: 4 k-blocks' words per row from global to shared memory
+//   warp 1           MMA issuer (leader CTA only in pairs), one elected lane
+//   warps 2, 3       scales: 4 k-blocks' words per row from global to shared memory,
+//                    with the ring stage of the first of them; warp 2 also allocates
+//                    and frees tensor memory
 //   warps 4..11      epilogue: tensor memory -> registers -> D
 //
 // Work: tiles [0, sk_tiles) are split along k, their (tile, k-block) units cut
@@ -209,29 +210,23 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const uint32_t stage0 = base;
     const uint32_t staging0 = base + (uint32_t)S * stage_bytes;
     const uint32_t scales0 = staging0 + kFp8EpiWarps * kFp8StagingBytes;
-    const uint32_t full_bar = scales0 + kFp8ScaleSlots * kFp8ScaleBytes;
+    const uint32_t full_bar = scales0 + (uint32_t)S * kFp8ScaleBytes;
     const uint32_t empty_bar = full_bar + 8u * S;
-    const uint32_t sfull_bar = empty_bar + 8u * S;
-    const uint32_t sempty_bar = sfull_bar + 8u * kFp8ScaleSlots;
-    const uint32_t accf_bar = sempty_bar + 8u * kFp8ScaleSlots;
+    const uint32_t accf_bar = empty_bar + 8u * S;
     const uint32_t acce_bar = accf_bar + 16u;
     const uint32_t done_bar = acce_bar + 16u;
     const uint32_t tmem_slot = done_bar + 8u;
     const uint32_t abort_flag = tmem_slot + 4u;
     const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
 
-    const int warp = threadIdx.x >> 5;
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(full_bar + 8u * s, 1);
+            mbar_init(full_bar + 8u * s, 1 + 2 * CG);  // the producer's expect_tx, each CTA's two scale warps
             mbar_init(empty_bar + 8u * s, 1);
-        }
-        for (int s = 0; s < kFp8ScaleSlots; ++s) {
-            mbar_init(sfull_bar + 8u * s, CG);  // the scale warp of each CTA
-            mbar_init(sempty_bar + 8u * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar + 8u * a, 1);
@@ -330,140 +325,176 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             while (globaltimer_ns() - t0 < 50000ull) {
             }
         }
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {
         // ---------------- MMA issuer ----------------
         const uint64_t rdesc0 = smem_desc_sw128(stage0);
         const uint64_t cdesc0 = smem_desc_sw128(stage0 + kRBytes);
+        const uint64_t sdesc0 = smem_desc_scales(scales0);
         const uint32_t idesc0 = idesc_mxf8(kFp8RowsPerCta * CG, 0) | ((uint32_t)(width >> 3) << 17);
         const uint32_t step = stage_bytes >> 4;
+        const uint32_t leader = elect_one();
+        // Waits here are loops inside one statement, and a wait that runs out does
+        // not leave the k loop: it records the fact and the rest of the item runs
+        // with single probes (its result is wrong, and the status says so).
+        const uint32_t probe_ns = ctl.suspend_ns;
+        uint32_t tries = (uint32_t)(ctl.limit_ns / probe_ns) + 1u;
+        uint32_t bad = 0u;
+        auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role, uint32_t where) {
+            if (mbar_wait_tries(bar, parity, probe_ns, tries) == 0u) {
+                if (bad == 0u && leader)
+                    ctl.fail(role, where);
+                bad = 1u;
+                tries = 1u;
+            }
+        };
         int s = 0;
         uint32_t ph = 0;
         int acc = 0;
         uint32_t acc_ph = 0;
-        uint32_t sseq = 0;  // scale words taken so far, in groups of 4 k-blocks
-        bool ok = true;
-        bool ready = false;
-        while (ok && wi.next(w)) {
-            if (!ctl.wait<kCluster>(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc)) {
-                ok = false;
-                break;
-            }
+        uint32_t group = 0;  // groups of 4 k-blocks so far: their parity picks the scales' buffer
+        while (wi.next(w)) {
+            wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
             tc_fence_after_sync();
             const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFp8MaxWidth);
             uint32_t stm = 0;
             for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                const uint32_t slot = sseq & (kFp8ScaleSlots - 1);
+                wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
+                tc_fence_after_sync();
                 if (kb == w.kb0 || (kb & 3) == 0) {
-                    if (!ctl.wait<kCluster>(sfull_bar + 8u * slot, (sseq / kFp8ScaleSlots) & 1u, kRoleScales, slot)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after_sync();
                     // copies and MMAs of one thread execute in order: the copy
                     // into a buffer follows the MMAs that last read it
-                    stm = tmem_base + kFp8ScaleCol + 32u * (sseq & 1u);
-                    const uint64_t sd = smem_desc_scales(scales0 + slot * kFp8ScaleBytes);
-                    copy_scales<CG>(stm, sd);
-                    copy_scales<CG>(stm + kFp8ScaleColB, sd + (512u >> 4));
+                    stm = tmem_base + kFp8ScaleCol + 32u * (group & 1u);
+                    ++group;
+                    const uint64_t sd = sdesc0 + (uint64_t)((uint32_t)s * (kFp8ScaleBytes >> 4));
+                    copy_scales<CG>(stm, sd, leader);
+                    copy_scales<CG>(stm + kFp8ScaleColB, sd + (512u >> 4), leader);
                     if (width > 128)
-                        copy_scales<CG>(stm + kFp8ScaleColB + 4u, sd + (1024u >> 4));
+                        copy_scales<CG>(stm + kFp8ScaleColB + 4u, sd + (1024u >> 4), leader);
                 }
-                if (!ready && !ctl.wait<kCluster>(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s)) {
-                    ok = false;
-                    break;
-                }
-                tc_fence_after_sync();
                 const uint64_t off = (uint64_t)((uint32_t)s * step);
                 const uint32_t idesc = idesc0 | scale_id((uint32_t)kb & 3u);
 #pragma unroll
                 for (int kk = 0; kk < kFp8BlockK / 32; ++kk)
                     mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
-                                 stm + kFp8ScaleColB, (kb != w.kb0 || kk != 0) ? 1u : 0u);
-                if (ring_group_last(s, 1u)) {
-                    if constexpr (kCluster)
-                        mma_commit_pair(empty_bar + 8u * ring_group(s, 1u), (uint16_t)0x3);
-                    else
-                        mma_commit(empty_bar + 8u * ring_group(s, 1u));
-                }
-                if ((kb & 3) == 3 || kb == w.kb1 - 1) {
-                    if constexpr (kCluster)
-                        mma_commit_pair(sempty_bar + 8u * slot, (uint16_t)0x3);
-                    else
-                        mma_commit(sempty_bar + 8u * slot);
-                    ++sseq;
-                }
+                                 stm + kFp8ScaleColB, (kb != w.kb0 || kk != 0) ? 1u : 0u, leader);
+                if (ring_group_last(s, 1u))
+                    mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);
                 ring_advance(s, ph, S);
-                ready = mbar_try_wait<kCluster>(full_bar + 8u * s, ring_full_parity(ph), 0u);
             }
-            if (!ok)
-                break;
-            if constexpr (kCluster)
-                mma_commit_pair(accf_bar + 8u * acc, (uint16_t)0x3);
-            else
-                mma_commit(accf_bar + 8u * acc);
+            mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
             acc ^= 1;
             if (acc == 0)
                 acc_ph ^= 1u;
+            if (__any_sync(0xFFFFFFFFu, bad))
+                break;
         }
         // no MMA may still be writing tensor memory when it is freed
-        if constexpr (kCluster)
-            mma_commit_pair(done_bar, (uint16_t)0x1);
-        else
-            mma_commit(done_bar);
-        ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
-    } else if (warp == 3) {
+        mma_commit_elected<CG>(done_bar, leader);
+        if (leader)
+            ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+        __syncwarp();
+    } else if (warp == 2 || warp == 3) {
         // ---------------- scales ----------------
-        // A slot holds 32 rows of four words: the words of rows r, r + 32, r + 64
-        // and r + 96 of the row side at 16 r, those of the column side's rows
-        // behind them in two such blocks.  Rows past the end count as scale 1;
-        // they meet only zeros, in parts of the tile that are not stored.
+        // The stage of a group's first k-block carries the group's words: 32 rows of
+        // four, the words of rows r, r + 32, r + 64 and r + 96 of the row side at
+        // 16 r, those of the column side's rows behind them in two such blocks.
+        // Rows past the end count as scale 1; they meet only zeros, in parts of the
+        // tile that are not stored.  The two warps bring groups in turn (one alone
+        // is busy 400 of the 450 clocks that a wide tile's k-block lasts), each with
+        // its next group's words in flight while it hands over the last ones.  Both
+        // wait for every release and arrive on every stage's full barrier: so the
+        // MMA issuer waits for scales and operands at once, and neither warp can
+        // run two phases of a barrier ahead or behind, which its parity would not
+        // tell.
+        const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
+        const uint32_t which = (uint32_t)warp & 1u;
+        Fp8Work wl = wi;  // the loads' place in the work
+        Fp8Item il = {0, 0, 0};
+        int32_t left = 0;       // groups of the loads' item still to come
+        uint32_t gl = 0;        // groups the loads have passed
+        uint32_t live = 0u;     // which of the twelve words exist
+        const uint32_t *sr = nullptr, *sc = nullptr;
+        uint32_t v[2][12];
+        auto load = [&](uint32_t(&x)[12]) {
+            for (;;) {
+                if (left == 0) {
+                    if (!wl.next(il))
+                        return;
+                    const TileCoord tc = fp8_tile_coord(il.tile, p);
+                    const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + lane;
+                    const int32_t yc = tc.nb * width + lane;
+                    const int32_t kt = il.kb0 >> 2;
+                    left = ((il.kb1 - 1) >> 2) + 1 - kt;
+                    sr = p.s_rows + (int64_t)kt * p.rows + yr;
+                    sc = p.s_cols + (int64_t)kt * p.cols + yc;
+                    live = 0u;
+#pragma unroll
+                    for (int j = 0; j < 12; ++j)
+                        if (j < 4 ? yr + 32 * j < p.rows : 32 * (j - 4) < width && yc + 32 * (j - 4) < p.cols)
+                            live |= 1u << j;
+                }
+                const bool mine = (gl & 1u) == which;
+                if (mine) {
+#pragma unroll
+                    for (int j = 0; j < 12; ++j)
+                        x[j] = live & (1u << j) ? (j < 4 ? sr[32 * j] : sc[32 * (j - 4)]) : 0x7F7F7F7Fu;
+                }
+                sr += p.rows;
+                sc += p.cols;
+                --left;
+                ++gl;
+                if (mine)
+                    return;
+            }
+        };
         grid_dependency_wait();
-        const uint32_t sfull_target = kCluster ? mapa_shared(sfull_bar, 0u) : sfull_bar;
-        uint32_t sseq = 0;
+        load(v[0]);
+        load(v[1]);
+        int s = 0;
+        uint32_t ph = 0;
+        uint32_t g = 0;
         bool ok = true;
         while (ok && wi.next(w)) {
-            const TileCoord tc = fp8_tile_coord(w.tile, p);
-            const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + lane;
-            const int32_t yc = tc.nb * width + lane;
-            const int32_t kt0 = w.kb0 >> 2, kt1 = (w.kb1 - 1) >> 2;
-            uint32_t cur[12], nxt[12];
-            auto load = [&](int32_t kt, uint32_t(&v)[12]) {
-                const uint32_t *const sr = p.s_rows + (int64_t)kt * p.rows + yr;
-                const uint32_t *const sc = p.s_cols + (int64_t)kt * p.cols + yc;
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] = yr + 32 * j < p.rows ? sr[32 * j] : 0x7F7F7F7Fu;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    v[4 + j] = 32 * j < width && yc + 32 * j < p.cols ? sc[32 * j] : 0x7F7F7F7Fu;
-            };
-            load(kt0, cur);
-            for (int32_t kt = kt0; kt <= kt1; ++kt) {
-                if (kt < kt1)
-                    load(kt + 1, nxt);
-                const uint32_t slot = sseq & (kFp8ScaleSlots - 1);
-                if (!warp_wait<kCluster>(ctl, sempty_bar + 8u * slot, ((sseq / kFp8ScaleSlots) & 1u) ^ 1u, kRoleScales,
-                                         0x800u | slot, lane)) {
-                    ok = false;
-                    break;
+            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                if (ring_group_first(s, 1u)) {
+                    const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                        !warp_wait<false>(ctl, bar, parity, kRoleScales, (uint32_t)s, lane)) {
+                        ok = false;
+                        break;
+                    }
                 }
-                const uint32_t at = scales0 + slot * kFp8ScaleBytes + 16u * (uint32_t)lane;
-                st_shared_v4(at, cur[0], cur[1], cur[2], cur[3]);
-                st_shared_v4(at + 512u, cur[4], cur[5], cur[6], cur[7]);
-                if (width > 128)
-                    st_shared_v4(at + 1024u, cur[8], cur[9], cur[10], cur[11]);
-                fence_proxy_async_shared();
-                __syncwarp();
+                const bool first = kb == w.kb0 || (kb & 3) == 0;
+                const bool last = kb == w.kb1 - 1 || (kb & 3) == 3;
+                const bool mine = (g & 1u) == which;
+                if (mine && first) {
+                    const uint32_t at = scales0 + (uint32_t)s * kFp8ScaleBytes + 16u * (uint32_t)lane;
+                    st_shared_v4(at, v[0][0], v[0][1], v[0][2], v[0][3]);
+                    st_shared_v4(at + 512u, v[0][4], v[0][5], v[0][6], v[0][7]);
+                    if (width > 128)
+                        st_shared_v4(at + 1024u, v[0][8], v[0][9], v[0][10], v[0][11]);
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                }
+                // Each CTA's words stay in its own shared memory, where its own half
+                // of the paired copy reads them: the proxy fence has put them there
+                // before the arrive leaves.  So the arrive on the leader's barrier
+                // releases at CTA scope; at cluster scope it waits for all of this
+                // thread's memory traffic, loads too (measured 600 ns).
                 if (lane == 0) {
                     if constexpr (kCluster)
-                        mbar_arrive_cluster(sfull_target + 8u * slot);
+                        mbar_arrive_cluster_handoff(full_target + 8u * s);
                     else
-                        mbar_arrive(sfull_target + 8u * slot);
+                        mbar_arrive(full_target + 8u * s);
                 }
-                ++sseq;
+                if (mine && last) {
 #pragma unroll
-                for (int j = 0; j < 12; ++j)
-                    cur[j] = nxt[j];
+                    for (int j = 0; j < 12; ++j)
+                        v[0][j] = v[1][j];
+                    load(v[1]);
+                }
+                g += last ? 1u : 0u;
+                ring_advance(s, ph, S);
             }
         }
     } else if (warp >= 4) {

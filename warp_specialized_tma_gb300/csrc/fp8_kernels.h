@@ -79,8 +79,7 @@ constexpr int kFp8BlockK = 128;       // k per ring stage: 128 e4m3, one 128-byt
 constexpr int kFp8MaxWidth = 224;     // column side of a tile: two accumulators and the scales fit tensor memory
 constexpr int kFp8Threads = 384;      // warps 0-3: producer, MMA, tensor memory, scales; 4-11: epilogue
 constexpr int kFp8EpiWarps = 8;
-constexpr int kFp8ScaleSlots = 4;     // ring of scale words, one slot per 4 k-blocks
-constexpr int kFp8ScaleBytes = 512 + 1024;  // a slot: 128 words of the row side, 256 of the column side
+constexpr int kFp8ScaleBytes = 512 + 1024;  // a stage's scales: 128 words of the row side, 256 of the column side
 constexpr int kFp8StagingBytes = 4096;      // per epilogue warp: 32 rows of 32 fp32 (or two of 32 bf16)
 constexpr int kFp8MaxStages = 12;
 constexpr int kFp8PartialFloats = kFp8RowsPerCta * 256;  // one CTA's fp32 partial of a split tile
@@ -116,8 +115,8 @@ inline size_t fp8_stage_bytes(int cta_group, int width)
 
 inline size_t fp8_smem_bytes(int cta_group, int width, int stages)
 {
-    return 1024 /* alignment slack */ + (size_t)stages * fp8_stage_bytes(cta_group, width) +
-           (size_t)kFp8EpiWarps * kFp8StagingBytes + (size_t)kFp8ScaleSlots * kFp8ScaleBytes + 512 /* barriers */;
+    return 1024 /* alignment slack */ + (size_t)stages * (fp8_stage_bytes(cta_group, width) + kFp8ScaleBytes) +
+           (size_t)kFp8EpiWarps * kFp8StagingBytes + 512 /* barriers */;
 }
 
 // (CUtensorMap rows, CUtensorMap cols, CUtensorMap D, Fp8GemmParams)

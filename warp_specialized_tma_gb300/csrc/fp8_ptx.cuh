@@ -9,28 +9,92 @@ namespace wstma {
 // Watchdog role code of the warp that brings the scales (see WaitCtl).
 constexpr uint32_t kRoleScales = 9;
 
+// The MMA issuer runs as a whole, converged warp, and these act for one elected
+// lane by a predicate instead of a branch: so the compiler keeps descriptors and
+// addresses in uniform registers, where the tensor core reads them.  From a
+// branch that one lane takes, every operand of every MMA is first moved there:
+// 70 clocks an MMA and 190 a commit, measured on GB300, which bounded the kernel.
+
+// 1 in one lane of the (converged) warp.
+__device__ __forceinline__ uint32_t elect_one()
+{
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xFFFFFFFF;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r;
+}
+
 // D[tmem] (+)= (A * sA) (B * sB)^T over 32 elements of k: e4m3 operands in
 // shared memory, one e8m0 scale per row for these 32 in tensor memory, fp32 sums.
 template <int CG>
 __device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate)
+                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate, uint32_t leader)
 {
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
                 "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p;\n\t"
+            "{\n\t.reg .pred p, q;\n\t"
             "setp.ne.b32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
+            "setp.ne.b32 q, %7, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
                 "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate)
+            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader)
             : "memory");
+}
+
+// mma_commit (CG = 1) or mma_commit_pair (CG = 2) of the elected lane.
+template <int CG>
+__device__ __forceinline__ void mma_commit_elected(uint32_t bar, uint32_t leader)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %1, 0;\n\t"
+            "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar),
+            "r"(leader)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}" ::"r"(
+                bar),
+            "h"((uint16_t)0x3), "r"(leader)
+            : "memory");
+}
+
+// Waits, up to `tries` probes of `suspend_ns` each, for the phase with this
+// parity; 0 if it did not complete.  A loop inside one statement: the warp
+// stays converged around it.
+__device__ __forceinline__ uint32_t mbar_wait_tries(uint32_t bar, uint32_t parity, uint32_t suspend_ns, uint32_t tries)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %4;\n\t"
+        "WAIT:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra WAIT;\n\t"
+        "DONE:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity), "r"(suspend_ns), "r"(tries)
+        : "memory");
+    return ok;
 }
 
 // Instruction descriptor of kind::mxf8f6f4: A and B e4m3 (bits 7..9 and 10..12
@@ -48,12 +112,22 @@ __host__ __device__ constexpr uint32_t scale_id(uint32_t byte) { return (byte <<
 // the same in all four lane quadrants: row r's word j lands in lane r, column j.
 // In paired mode each CTA of the pair copies from its own shared memory.
 template <int CG>
-__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc)
+__device__ __forceinline__ void copy_scales(uint32_t taddr, uint64_t desc, uint32_t leader)
 {
     if constexpr (CG == 1)
-        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+            "l"(desc), "r"(leader)
+            : "memory");
     else
-        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %2, 0;\n\t"
+            "@q tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n\t}" ::"r"(taddr),
+            "l"(desc), "r"(leader)
+            : "memory");
 }
 
 // Shared-memory descriptor of such a 512-byte block: no swizzle, groups of 8

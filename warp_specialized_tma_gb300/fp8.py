@@ -54,6 +54,7 @@ OPTIONS = {
     "split": 4,
     "watchdog_ns": 5,
     "fault_skip_load": 6,
+    "raster_group": 7,
 }
 
 NORM_MAX_COLUMNS = 32768
