@@ -687,7 +687,8 @@ FP8_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_
     p.R = (int32_t)R;
     p.C = (int32_t)C;
     p.eps = eps;
-    p.vec = aligned(x, 16) && ldx % 8 == 0 && aligned(weight, 16) &&
+    p.w_vec = aligned(weight, 16) ? 1 : 0;
+    p.vec = aligned(x, 16) && ldx % 8 == 0 &&
             (!residual || (aligned(residual, 16) && ldr % 8 == 0 && aligned(h, 16) && ldh % 8 == 0));
     p.h = static_cast<uint16_t *>(h);
     p.ldh = ldh;
@@ -756,8 +757,9 @@ FP8_API int fp8_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, in
     p.dw = dweight;
     p.R = (int32_t)R;
     p.C = (int32_t)C;
-    p.vec = aligned(dy, 16) && lddy % 8 == 0 && aligned(h, 16) && ldh % 8 == 0 && aligned(weight, 16) &&
-            aligned(dx, 16) && lddx % 8 == 0 && (!dresidual || (aligned(dresidual, 16) && lddr % 8 == 0));
+    p.w_vec = aligned(weight, 16) ? 1 : 0;
+    p.vec = aligned(dy, 16) && lddy % 8 == 0 && aligned(h, 16) && ldh % 8 == 0 && aligned(dx, 16) &&
+            lddx % 8 == 0 && (!dresidual || (aligned(dresidual, 16) && lddr % 8 == 0));
     p.partials = static_cast<float *>(workspace);
     return from_cuda((cudaError_t)launch_rmsnorm_backward(p, sms, st));
 }

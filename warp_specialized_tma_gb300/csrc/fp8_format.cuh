@@ -149,6 +149,62 @@ __device__ __forceinline__ void store8_bf16(uint16_t *row, int32_t c, int32_t C,
             row[c + i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
 
+// The same to a row that is only 2-byte aligned, by the 16 lanes of a half-warp
+// (all of them call this): each lane stores the aligned 16 bytes its vector starts
+// in, with its neighbour's last elements before its own; the half-warp's first
+// and last bytes, and the row's end, go element by element.  Nothing outside
+// columns c .. C - 1 of the half-warp is written.
+__device__ __forceinline__ void store8_bf16_shifted(uint16_t *row, int32_t c, int32_t C, bool live, uint4 q)
+{
+    const int l = (int)(threadIdx.x & 15u);
+    const uintptr_t at = reinterpret_cast<uintptr_t>(row + c);
+    const uint32_t mis = (uint32_t)(at & 15u);
+    uint32_t w[8];  // the neighbour's vector, then this one
+    w[4] = q.x, w[5] = q.y, w[6] = q.z, w[7] = q.w;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        w[k] = __shfl_up_sync(0xFFFFFFFFu, w[4 + k], 1, 16);
+    if (!live)
+        return;
+    const int32_t end = c + 8 < C ? 8 : C - c;  // this vector's live elements
+    if ((l > 0 || mis == 0u) && C - c >= 8 - (int32_t)(mis >> 1)) {
+        // bytes 16 - mis .. 31 - mis of the two vectors: shift right by 16 - mis
+        const uint32_t by = 16u - mis;
+        uint32_t s[5];
+#pragma unroll
+        for (int k = 0; k < 5; ++k)  // by / 4 words: 1 to 4
+            s[k] = by >= 16u ? (k < 4 ? w[k + 4] : 0u)
+                             : (by >= 12u ? w[k + 3] : (by >= 8u ? w[k + 2] : (by >= 4u ? w[k + 1] : w[k])));
+        uint32_t o[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            o[k] = __funnelshift_r(s[k], s[k + 1], (by & 2u) * 8u);
+        *reinterpret_cast<uint4 *>(at - mis) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+        // this vector's part of its first granule (and, for later lanes, the
+        // neighbour's part of it)
+        const int32_t own = 8 - (int32_t)(mis >> 1);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (j < own && j < end)
+                row[c + j] = (uint16_t)(w[4 + (j >> 1)] >> (16 * (j & 1)));
+        if (l > 0) {
+#pragma unroll
+            for (int j = 1; j < 8; ++j)
+                if (j >= own)
+                    row[c - 8 + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+        }
+    }
+    // what no later lane stores: the last lane's rest, or that of the row's last vector
+    if (l == 15 || c + 8 >= C) {
+        const int32_t own = 8 - (int32_t)(mis >> 1);
+#pragma unroll
+        for (int j = 1; j < 8; ++j)
+            if (j >= own && j < end)
+                row[c + j] = (uint16_t)(w[4 + (j >> 1)] >> (16 * (j & 1)));
+    }
+}
+
 // Codes c .. c+7 of a row (rows are 16-byte aligned).
 __device__ __forceinline__ void store8_codes(uint8_t *row, int32_t c, int32_t C, uint2 q)
 {

@@ -41,7 +41,8 @@ struct NormParams {
     int32_t w_fp32;
     int32_t R, C;
     float eps;
-    int32_t vec;  // every row and the weight are 16-byte aligned
+    int32_t vec;    // every row is 16-byte aligned
+    int32_t w_vec;  // the weight is
     uint16_t *h;
     int64_t ldh;
     uint8_t *codes;
@@ -66,7 +67,8 @@ struct NormBackwardParams {
     int64_t lddx;
     float *dw;
     int32_t R, C;
-    int32_t vec;
+    int32_t vec;    // as in NormParams
+    int32_t w_vec;
     float *partials;  // rmsnorm_backward_ctas() rows of C floats
 };
 

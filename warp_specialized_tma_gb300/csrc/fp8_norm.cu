@@ -3,6 +3,7 @@
 #include <cuda_runtime.h>
 
 #include <cstdint>
+#include <mutex>
 
 #include "fp8_format.cuh"
 #include "fp8_kernels.h"
@@ -45,9 +46,24 @@ __device__ __forceinline__ void load8_weight(const void *w, int fp32, int32_t c,
         unpack8(load8_bf16(static_cast<const uint16_t *>(w), c, C, vec), f);
 }
 
+// Rows that are not 16-byte aligned (an odd number of columns) go by aligned
+// accesses and shifts, 8 columns a lane all the same.
+__device__ __forceinline__ uint4 load8_row(const uint16_t *row, int32_t c, int32_t C, bool vec)
+{
+    return vec ? load8_bf16(row, c, C, true) : load8_bf16_shifted(row, c, C, true);
+}
+
+__device__ __forceinline__ void store8_row(uint16_t *row, int32_t c, int32_t C, bool vec, uint4 q)
+{
+    if (!vec)
+        store8_bf16_shifted(row, c, C, c < C, q);
+    else if (c < C)
+        store8_bf16(row, c, C, true, q);
+}
+
 // Vector v of a row (8 columns each): thread t of the row's T holds vectors t,
 // t + T, ..., so the 16 lanes of a half-warp always hold one block of 128.
-template <int V, bool kWarpRow, bool kRes>
+template <int V, bool kWarpRow, bool kRes, bool vec>
 __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
 {
     __shared__ float red[32];
@@ -58,7 +74,6 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
     const int64_t row = kWarpRow ? (int64_t)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5) : blockIdx.x;
     if (row >= p.R)
         return;  // whole warps, and only where rows are warps
-    const bool vec = p.vec != 0;
     const int32_t C = p.C;
     const uint16_t *const xr = p.x + row * p.ldx;
     const uint16_t *const rr = kRes ? p.residual + row * p.ldr : nullptr;
@@ -66,12 +81,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
     uint4 hv[V];
 #pragma unroll
     for (int i = 0; i < V; ++i)
-        hv[i] = load8_bf16(xr, (t + i * T) * 8, C, vec);
+        hv[i] = load8_row(xr, (t + i * T) * 8, C, vec);
     if constexpr (kRes) {
         uint4 rv[V];
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            rv[i] = load8_bf16(rr, (t + i * T) * 8, C, vec);
+            rv[i] = load8_row(rr, (t + i * T) * 8, C, vec);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             float a[8], b[8];
@@ -93,8 +108,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
         for (int j = 0; j < 8; ++j)
             sum = fmaf(a[j], a[j], sum);
         if constexpr (kRes)
-            if ((t + i * T) * 8 < C)
-                store8_bf16(p.h + row * p.ldh, (t + i * T) * 8, C, vec, hv[i]);
+            store8_row(p.h + row * p.ldh, (t + i * T) * 8, C, vec, hv[i]);
     }
     sum = row_sum<kWarpRow>(sum, red);
     const float rstd = 1.f / sqrtf(sum / (float)C + p.eps);
@@ -108,7 +122,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
         const int32_t c = (t + i * T) * 8;
         float y[8], w[8];
         unpack8(hv[i], y);
-        load8_weight(p.weight, p.w_fp32, c, C, vec, w);
+        load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w);
         float amax = 0.f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -148,12 +162,42 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
     }
 }
 
+// A row's share of one thread.
+template <int V, bool kDres, bool kVec>
+struct BackwardRow {
+    uint4 dy[V], h[V], dres[kDres ? V : 1];
+    float rstd;
+
+    __device__ __forceinline__ void load(const NormBackwardParams &p, int64_t row, int t, int T)
+    {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            dy[i] = load8_row(p.dy + row * p.lddy, c, p.C, kVec);
+            h[i] = load8_row(p.h + row * p.ldh, c, p.C, kVec);
+            if constexpr (kDres)
+                dres[i] = load8_row(p.dres + row * p.lddr, c, p.C, kVec);
+        }
+        rstd = p.rstd[row];
+    }
+};
+
+constexpr int kBackwardThreads = 512;
+
 // A CTA (or each of its warps) takes rows in a stride of the grid and keeps its
 // threads' share of dweight in registers; the CTAs' sums meet in `partials`,
-// one row of C floats each, which column_sum_kernel adds in a fixed order.
-template <int V, bool kWarpRow>
-__global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwardParams p)
+// one row of C floats each, which column_sum_kernel adds in a fixed order.  Bound
+// by HBM (4 to 8 bytes an element) if loads are always in flight: the next
+// row's are issued before the current row's reduction (V <= 2, where the registers
+// suffice).
+//
+// kThreads bounds the CTA: with V = 1, or up to 320 threads, two CTAs share an SM,
+// so that one's reduction overlaps the other's loads and stores.
+template <int V, bool kWarpRow, bool kDres, bool kVec, int kThreads>
+__global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
+    rmsnorm_backward_kernel(const NormBackwardParams p)
 {
+    constexpr bool kAhead = V <= 2;
     extern __shared__ float dw_smem[];  // warp rows: C floats
     __shared__ float red[32];
     grid_dependency_wait();
@@ -163,59 +207,69 @@ __global__ void __launch_bounds__(1024) rmsnorm_backward_kernel(const NormBackwa
     const int t = kWarpRow ? (int)(threadIdx.x & 31u) : (int)threadIdx.x;
     const int64_t row0 = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
     const int64_t step = kWarpRow ? (int64_t)gridDim.x * warps : gridDim.x;
-    const bool vec = p.vec != 0;
     const int32_t C = p.C;
-    float dw[V][8];
+    const float inv = 1.f / (float)C;
+    float dw[V][8], w[kAhead ? V : 1][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.f;
 
-    for (int64_t row = row0; row < p.R; row += step) {
-        uint4 dv[V], hv[V];
+    BackwardRow<V, kDres, kVec> cur, next;
+    if (row0 < p.R)
+        cur.load(p, row0, t, T);
+    if constexpr (kAhead) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            dv[i] = load8_bf16(p.dy + row * p.lddy, (t + i * T) * 8, C, vec);
-            hv[i] = load8_bf16(p.h + row * p.ldh, (t + i * T) * 8, C, vec);
+        for (int i = 0; i < V; ++i)
+            load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[i]);
+    }
+    for (int64_t row = row0; row < p.R; row += step) {
+        if constexpr (kAhead) {
+            if (row + step < p.R)
+                next.load(p, row + step, t, T);
         }
-        const float rstd = p.rstd[row];
+        const float rstd = cur.rstd;
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float d[8], h[8], w[8];
-            unpack8(dv[i], d);
-            unpack8(hv[i], h);
-            load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, vec, w);
+            float d[8], h[8];
+            unpack8(cur.dy[i], d);
+            unpack8(cur.h[i], h);
+            if constexpr (!kAhead)
+                load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[0]);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
                 const float n = h[j] * rstd;
-                dot = fmaf(d[j] * w[j], n, dot);
+                dot = fmaf(d[j] * w[kAhead ? i : 0][j], n, dot);
                 dw[i][j] = fmaf(d[j], n, dw[i][j]);
             }
         }
-        const float mean = row_sum<kWarpRow>(dot, red) / (float)C;
+        const float mean = row_sum<kWarpRow>(dot, red) * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            if (c >= C)
-                continue;
-            float d[8], h[8], w[8], r[8];
-            unpack8(dv[i], d);
-            unpack8(hv[i], h);
-            load8_weight(p.weight, p.w_fp32, c, C, vec, w);
-            if (p.dres)
-                unpack8(load8_bf16(p.dres + row * p.lddr, c, C, vec), r);
+            float d[8], h[8], r[8];
+            unpack8(cur.dy[i], d);
+            unpack8(cur.h[i], h);
+            if constexpr (!kAhead)
+                load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w[0]);
+            if constexpr (kDres)
+                unpack8(cur.dres[i], r);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                d[j] = rstd * (d[j] * w[j] - h[j] * rstd * mean);
-                if (p.dres)
+                d[j] = rstd * (d[j] * w[kAhead ? i : 0][j] - h[j] * rstd * mean);
+                if constexpr (kDres)
                     d[j] += r[j];
             }
-            store8_bf16(p.dx + row * p.lddx, c, C, vec,
-                        make_uint4(bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]),
-                                   bf16_pair(d[6], d[7])));
+            store8_row(p.dx + row * p.lddx, c, C, kVec,
+                       make_uint4(bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]),
+                                  bf16_pair(d[6], d[7])));
         }
+        if constexpr (kAhead)
+            cur = next;
+        else if (row + step < p.R)
+            cur.load(p, row + step, t, T);
     }
 
     float *const out = p.partials + (int64_t)blockIdx.x * C;
@@ -298,58 +352,99 @@ struct RowSplit {
     int V;
 };
 
-RowSplit split_row(int64_t C, int max_v)
+// V is 1, 2, 4 or 8: the least that keeps a CTA within `most` threads, then up
+// to max_v while the CTA has more than `wanted`.
+RowSplit split_row(int64_t C, int max_v, int most, int wanted)
 {
     const int64_t nv = (C + 7) / 8;
     if (nv <= 32 * max_v && nv <= 128)
         return {true, 128, nv <= 32 ? 1 : (nv <= 64 ? 2 : 4)};
     int V = 1;
-    while (V < 4 && (nv + V - 1) / V > 1024)
+    while ((nv + V - 1) / V > most)
         V *= 2;
-    while (V < max_v && (nv + V - 1) / V > 256)
+    while (V < max_v && (nv + V - 1) / V > wanted)
         V *= 2;
     return {false, (int)(((nv + V - 1) / V + 31) / 32 * 32), V};
 }
 
-template <bool kWarpRow, bool kRes>
-auto norm_fn(int V)
+template <bool kRes, bool kVec>
+auto norm_fn(const RowSplit &s)
 {
-    return V == 1 ? &rmsnorm_kernel<1, kWarpRow, kRes>
-                  : (V == 2 ? &rmsnorm_kernel<2, kWarpRow, kRes> : &rmsnorm_kernel<4, kWarpRow, kRes>);
+    if (s.warp_row)
+        return s.V == 1 ? &rmsnorm_kernel<1, true, kRes, kVec>
+                        : (s.V == 2 ? &rmsnorm_kernel<2, true, kRes, kVec> : &rmsnorm_kernel<4, true, kRes, kVec>);
+    return s.V == 1 ? &rmsnorm_kernel<1, false, kRes, kVec>
+                    : (s.V == 2 ? &rmsnorm_kernel<2, false, kRes, kVec> : &rmsnorm_kernel<4, false, kRes, kVec>);
 }
 
-template <bool kWarpRow>
-auto norm_backward_fn(int V)
+template <bool kDres, bool kVec>
+auto norm_backward_fn(const RowSplit &s)
 {
-    return V == 1 ? &rmsnorm_backward_kernel<1, kWarpRow>
-                  : (V == 2 ? &rmsnorm_backward_kernel<2, kWarpRow> : &rmsnorm_backward_kernel<4, kWarpRow>);
+    constexpr int kT = kBackwardThreads;
+    if (s.warp_row)
+        return s.V == 1 ? &rmsnorm_backward_kernel<1, true, kDres, kVec, 128>
+                        : &rmsnorm_backward_kernel<2, true, kDres, kVec, 128>;
+    switch (s.V) {
+    case 1: return &rmsnorm_backward_kernel<1, false, kDres, kVec, kT>;
+    case 2:
+        return s.threads <= 320 ? &rmsnorm_backward_kernel<2, false, kDres, kVec, 320>
+                                : &rmsnorm_backward_kernel<2, false, kDres, kVec, kT>;
+    case 4: return &rmsnorm_backward_kernel<4, false, kDres, kVec, kT>;
+    default: return &rmsnorm_backward_kernel<8, false, kDres, kVec, kT>;
+    }
 }
+
+// Rows of 8 vectors a thread end at 512 * 8 * 8 columns, the limit of the API.
+static_assert(kBackwardThreads * 8 * 8 >= 32768, "every width up to the limit has a kernel");
 
 }  // namespace
 
 int launch_rmsnorm(const NormParams &p, int num_sms, cudaStream_t stream)
 {
     // few rows: more threads a row, for latency; many: 4 vectors a thread
-    const RowSplit s = split_row(p.C, p.R <= 2 * num_sms ? 1 : 4);
+    const RowSplit s = split_row(p.C, p.R <= 2 * num_sms ? 1 : 4, 1024, 256);
     const int64_t grid = s.warp_row ? ((int64_t)p.R + 3) / 4 : p.R;
-    auto fn = s.warp_row ? (p.residual ? norm_fn<true, true>(s.V) : norm_fn<true, false>(s.V))
-                         : (p.residual ? norm_fn<false, true>(s.V) : norm_fn<false, false>(s.V));
+    auto fn = p.residual ? (p.vec ? norm_fn<true, true>(s) : norm_fn<true, false>(s))
+                         : (p.vec ? norm_fn<false, true>(s) : norm_fn<false, false>(s));
     return launch(fn, grid, s.threads, 0, stream, p);
+}
+
+// CTAs of the gradient kernel that fit on an SM, looked up once per split (the
+// variant with the most registers, so that the workspace's size does not depend
+// on which gradients are given).
+int backward_blocks(const RowSplit &s)
+{
+    static int known[2][4][kBackwardThreads / 32 + 1];
+    static std::mutex lock;
+    const int v = s.V == 1 ? 0 : (s.V == 2 ? 1 : (s.V == 4 ? 2 : 3));
+    std::lock_guard<std::mutex> hold(lock);
+    int &n = known[s.warp_row ? 1 : 0][v][s.threads / 32];
+    if (n == 0) {
+        const size_t smem = s.warp_row ? (size_t)s.V * 256 * sizeof(float) : 0;
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_backward_fn<true, true>(s), s.threads, smem) !=
+                cudaSuccess ||
+            n < 1) {
+            cudaGetLastError();
+            n = 1;
+        }
+    }
+    return n;
 }
 
 int rmsnorm_backward_ctas(int64_t R, int64_t C, int num_sms)
 {
-    const RowSplit s = split_row(C, 2);
+    const RowSplit s = split_row(C, 2, kBackwardThreads, kBackwardThreads);
     const int64_t rows = s.warp_row ? (R + 3) / 4 : R;
-    const int64_t most = (int64_t)num_sms * (s.threads >= 1024 ? 1 : 1024 / s.threads);
+    const int64_t most = (int64_t)num_sms * backward_blocks(s);
     return (int)(rows < most ? rows : most);
 }
 
 int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t stream)
 {
-    const RowSplit s = split_row(p.C, 2);
+    const RowSplit s = split_row(p.C, 2, kBackwardThreads, kBackwardThreads);
     const int grid = rmsnorm_backward_ctas(p.R, p.C, num_sms);
-    auto fn = s.warp_row ? norm_backward_fn<true>(s.V) : norm_backward_fn<false>(s.V);
+    auto fn = p.dres ? (p.vec ? norm_backward_fn<true, true>(s) : norm_backward_fn<true, false>(s))
+                     : (p.vec ? norm_backward_fn<false, true>(s) : norm_backward_fn<false, false>(s));
     const size_t smem = s.warp_row ? (size_t)p.C * sizeof(float) : 0;
     cudaError_t rc = launch(fn, grid, s.threads, smem, stream, p);
     if (rc != cudaSuccess)
