@@ -2,12 +2,12 @@
 // and the norm's gradients.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cstdint>
-#include <mutex>
 
 #include "fp8_format.cuh"
 #include "fp8_kernels.h"
-#include "ptx.cuh"
+#include "fp8_ptx.cuh"
 
 namespace wstma {
 
@@ -183,6 +183,8 @@ struct BackwardRow {
 };
 
 constexpr int kBackwardThreads = 512;
+constexpr int kRingMax = 32;               // slots of the ring of rows
+constexpr int kRingBytes = 208 * 1024;     // of an SM's shared memory, shared by its CTAs
 
 // A CTA (or each of its warps) takes rows in a stride of the grid and keeps its
 // threads' share of dweight in registers; the CTAs' sums meet in `partials`,
@@ -194,7 +196,7 @@ constexpr int kBackwardThreads = 512;
 // kThreads bounds the CTA: with V = 1, or up to 320 threads, two CTAs share an SM,
 // so that one's reduction overlaps the other's loads and stores.
 template <int V, bool kWarpRow, bool kDres, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
+__global__ void __launch_bounds__(kThreads, kWarpRow ? 6 : (V == 1 || kThreads <= 320 ? 2 : 1))
     rmsnorm_backward_kernel(const NormBackwardParams p)
 {
     constexpr bool kAhead = V <= 2;
@@ -303,7 +305,142 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     }
 }
 
-constexpr int kSumRows = 16;
+// The same for rows that start and end at multiples of 16 bytes: rows come through
+// a ring of bulk copies in shared memory, slots of dy, h (and dresidual), so the
+// bytes in flight are the ring's (up to 200 KB an SM) and not what the registers
+// hold: that left HBM idle half of the time (6143 x 4104: 42 us with one row ahead
+// in registers).  Thread 0 refills a slot after the barrier in the next row's
+// reduction, which every thread reaches when it is done with the slot.
+template <int V, bool kDres, int kThreads>
+__global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
+    rmsnorm_backward_ring_kernel(const NormBackwardParams p, const int32_t slots)
+{
+    extern __shared__ __align__(128) uint8_t ring[];
+    __shared__ float red[2][32];
+    __shared__ __align__(8) uint64_t full[kRingMax];
+    constexpr int kRows = kDres ? 3 : 2;
+    const int T = (int)blockDim.x, t = (int)threadIdx.x;
+    const int warp = t >> 5, lane = t & 31, warps = T >> 5;
+    const int32_t C = p.C;
+    const uint32_t row_bytes = (uint32_t)C * 2u;
+    const uint32_t slot_bytes = row_bytes * kRows;
+    const uint32_t base = smem_u32(ring), bars = smem_u32(full);
+    const float inv = 1.f / (float)C;
+    const int64_t step = gridDim.x;
+    if (t == 0) {
+        for (int s = 0; s < slots; ++s)
+            mbar_init(bars + 8u * s, 1);
+        fence_mbarrier_init();
+    }
+    __syncthreads();
+    grid_dependency_wait();
+    grid_launch_dependents();
+
+    auto fill = [&](int s, int64_t row) {
+        const uint32_t at = base + (uint32_t)s * slot_bytes, bar = bars + 8u * s;
+        mbar_arrive_expect_tx(bar, slot_bytes);
+        bulk_load(at, p.dy + row * p.lddy, row_bytes, bar);
+        bulk_load(at + row_bytes, p.h + row * p.ldh, row_bytes, bar);
+        if constexpr (kDres)
+            bulk_load(at + 2u * row_bytes, p.dres + row * p.lddr, row_bytes, bar);
+    };
+    if (t == 0)
+        for (int s = 0; s < slots && blockIdx.x + s * step < p.R; ++s)
+            fill(s, blockIdx.x + s * step);
+
+    float dw[V][8], w[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            dw[i][j] = 0.f;
+    }
+    float rstd = blockIdx.x < p.R ? p.rstd[blockIdx.x] : 0.f;
+    int s = 0;
+    uint32_t ph = 0, buf = 0;
+    bool ok = true;
+    int64_t refill = -1;  // row to load into the slot before this one
+    int before = 0;
+    for (int64_t row = blockIdx.x; row < p.R; row += step) {
+        const float next_rstd = row + step < p.R ? p.rstd[row + step] : 0.f;
+        ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
+        const uint32_t at = base + (uint32_t)s * slot_bytes;
+        uint4 dy[V], h[V];
+        float dot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            dy[i] = h[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < C) {
+                ld_shared_v4(at + (uint32_t)c * 2u, dy[i].x, dy[i].y, dy[i].z, dy[i].w);
+                ld_shared_v4(at + row_bytes + (uint32_t)c * 2u, h[i].x, h[i].y, h[i].z, h[i].w);
+            }
+            float d[8], x[8];
+            unpack8(dy[i], d);
+            unpack8(h[i], x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float n = x[j] * rstd;
+                dot = fmaf(d[j] * w[i][j], n, dot);
+                dw[i][j] = fmaf(d[j], n, dw[i][j]);
+            }
+        }
+        // one barrier a row: the sums alternate between two buffers
+        dot = warp_sum(dot);
+        if (lane == 0)
+            red[buf][warp] = dot;
+        __syncthreads();
+        if (t == 0 && refill >= 0)
+            fill(before, refill);
+        const float mean = warp_sum(lane < warps ? red[buf][lane] : 0.f) * inv;
+        buf ^= 1u;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            if (c >= C)
+                continue;
+            float d[8], x[8], r[8];
+            unpack8(dy[i], d);
+            unpack8(h[i], x);
+            if constexpr (kDres) {
+                uint4 q;
+                ld_shared_v4(at + 2u * row_bytes + (uint32_t)c * 2u, q.x, q.y, q.z, q.w);
+                unpack8(q, r);
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                d[j] = rstd * (d[j] * w[i][j] - x[j] * rstd * mean);
+                if constexpr (kDres)
+                    d[j] += r[j];
+            }
+            *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c) = make_uint4(
+                bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]), bf16_pair(d[6], d[7]));
+        }
+        rstd = next_rstd;
+        before = s;
+        refill = row + slots * step < p.R ? row + slots * step : -1;
+        if (++s == slots) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+    // a wait that ran out (its copies never landed): dweight says so
+    const float poison = ok ? 0.f : __int_as_float(0x7FFFFFFF);
+    float *const out = p.partials + (int64_t)blockIdx.x * C;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t c = (t + i * T) * 8;
+        if (c < C) {
+            *reinterpret_cast<float4 *>(out + c) =
+                make_float4(dw[i][0] + poison, dw[i][1] + poison, dw[i][2] + poison, dw[i][3] + poison);
+            *reinterpret_cast<float4 *>(out + c + 4) =
+                make_float4(dw[i][4] + poison, dw[i][5] + poison, dw[i][6] + poison, dw[i][7] + poison);
+        }
+    }
+}
+
+constexpr int kSumRows = 32;
 
 // dw[c] = sum of n rows of partials, 32 columns and kSumRows strands a CTA.
 __global__ void __launch_bounds__(32 * kSumRows) column_sum_kernel(const float *partials, int32_t n, int32_t C,
@@ -315,9 +452,11 @@ __global__ void __launch_bounds__(32 * kSumRows) column_sum_kernel(const float *
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
     const int32_t c = (int32_t)blockIdx.x * 32 + x;
     float s = 0.f;
-    if (c < C)
+    if (c < C) {
+#pragma unroll 8
         for (int32_t g = y; g < n; g += kSumRows)
             s += partials[(int64_t)g * C + c];
+    }
     red[y][x] = s;
     __syncthreads();
     if (y == 0 && c < C) {
@@ -409,26 +548,12 @@ int launch_rmsnorm(const NormParams &p, int num_sms, cudaStream_t stream)
     return launch(fn, grid, s.threads, 0, stream, p);
 }
 
-// CTAs of the gradient kernel that fit on an SM, looked up once per split (the
-// variant with the most registers, so that the workspace's size does not depend
-// on which gradients are given).
+// CTAs of the gradient kernel on an SM: the bounds of the kernels' registers.
 int backward_blocks(const RowSplit &s)
 {
-    static int known[2][4][kBackwardThreads / 32 + 1];
-    static std::mutex lock;
-    const int v = s.V == 1 ? 0 : (s.V == 2 ? 1 : (s.V == 4 ? 2 : 3));
-    std::lock_guard<std::mutex> hold(lock);
-    int &n = known[s.warp_row ? 1 : 0][v][s.threads / 32];
-    if (n == 0) {
-        const size_t smem = s.warp_row ? (size_t)s.V * 256 * sizeof(float) : 0;
-        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, norm_backward_fn<true, true>(s), s.threads, smem) !=
-                cudaSuccess ||
-            n < 1) {
-            cudaGetLastError();
-            n = 1;
-        }
-    }
-    return n;
+    if (s.warp_row)
+        return 6;
+    return s.V == 1 ? std::min(kBackwardThreads / s.threads * 2, 8) : (s.V == 2 && s.threads <= 320 ? 2 : 1);
 }
 
 int rmsnorm_backward_ctas(int64_t R, int64_t C, int num_sms)
@@ -439,6 +564,15 @@ int rmsnorm_backward_ctas(int64_t R, int64_t C, int num_sms)
     return (int)(rows < most ? rows : most);
 }
 
+template <bool kDres>
+auto norm_backward_ring_fn(const RowSplit &s)
+{
+    constexpr int kT = kBackwardThreads;
+    return s.V == 1 ? &rmsnorm_backward_ring_kernel<1, kDres, kT>
+                    : (s.threads <= 320 ? &rmsnorm_backward_ring_kernel<2, kDres, 320>
+                                        : &rmsnorm_backward_ring_kernel<2, kDres, kT>);
+}
+
 int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t stream)
 {
     const RowSplit s = split_row(p.C, 2, kBackwardThreads, kBackwardThreads);
@@ -446,7 +580,18 @@ int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream
     auto fn = p.dres ? (p.vec ? norm_backward_fn<true, true>(s) : norm_backward_fn<true, false>(s))
                      : (p.vec ? norm_backward_fn<false, true>(s) : norm_backward_fn<false, false>(s));
     const size_t smem = s.warp_row ? (size_t)p.C * sizeof(float) : 0;
-    cudaError_t rc = launch(fn, grid, s.threads, smem, stream, p);
+    // the ring where rows are whole 16-byte groups and two or more slots fit
+    const int64_t slot = (int64_t)p.C * 2 * (p.dres ? 3 : 2);
+    const int64_t slots = std::min<int64_t>(kRingBytes / backward_blocks(s) / slot, kRingMax);
+    cudaError_t rc;
+    if (p.vec && p.C % 8 == 0 && !s.warp_row && s.V <= 2 && slots >= 2) {
+        auto ring = p.dres ? norm_backward_ring_fn<true>(s) : norm_backward_ring_fn<false>(s);
+        rc = cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+        if (rc == cudaSuccess)
+            rc = launch(ring, grid, s.threads, (size_t)(slots * slot), stream, p, (int32_t)slots);
+    } else {
+        rc = launch(fn, grid, s.threads, smem, stream, p);
+    }
     if (rc != cudaSuccess)
         return rc;
     return launch(&column_sum_kernel, ((int64_t)p.C + 31) / 32, 32 * kSumRows, 0, stream,
