@@ -54,7 +54,8 @@ typedef enum fp8_gemm_option {
     FP8_GEMM_OPT_TRANSPOSED = 2,  /* 0 = automatic, 1 = A's rows on the MMA's row side, 2 = B's rows */
     FP8_GEMM_OPT_WIDTH = 3,       /* 0 = automatic, else the tile's width on the MMA's column side:
                                      a multiple of 16 (32 for SM pairs), at most 224 */
-    FP8_GEMM_OPT_SPLIT = 4,       /* 1 = tiles that would leave SMs idle are split along K (default), 0 = never */
+    FP8_GEMM_OPT_SPLIT = 4,       /* tiles that would leave SMs idle are split along K: 1 = among clusters of CTAs or
+                                     through global memory (default), 2 = through global memory only, 0 = never */
     FP8_GEMM_OPT_WATCHDOG_NS = 5, /* limit of any wait inside the kernel (default 2e9) */
     FP8_GEMM_OPT_FAULT_SKIP_LOAD = 6, /* test hook: each producer leaves out this load (-1 = none), so that
                                          a bounded wait runs out and the call reports DEVICE_TIMEOUT */
@@ -74,6 +75,7 @@ typedef struct fp8_gemm_plan_info_s {
     int32_t split_tiles;     /* tiles split along K */
     int32_t smem_bytes;
     int32_t regs_per_thread;
+    int32_t cluster;         /* CTAs of a cluster that share a tile (1: none) */
 } fp8_gemm_plan_info_t;
 
 FP8_API const char *fp8_strerror(int status);

@@ -91,7 +91,7 @@ def test_gemm_exact_integers(shape, out_dtype):
     exact_check(*shape, out_dtype)
 
 
-@pytest.mark.parametrize("split", [0, 1])
+@pytest.mark.parametrize("split", [0, 1, 2])
 @pytest.mark.parametrize("transposed", [1, 2])
 @pytest.mark.parametrize("cta_group,width", [(1, 32), (1, 64), (1, 128), (1, 160), (1, 224), (2, 32), (2, 96), (2, 128),
                                              (2, 192), (2, 224)])
@@ -110,6 +110,18 @@ def test_gemm_exact_few_tokens_both_ways(tokens):
     if tokens <= 16:  # the narrowest tile
         info = exact_check(tokens, 2000, 2048, torch.bfloat16, width=16, cta_group=1, transposed=2)
         assert info["width"] == 16
+
+
+@pytest.mark.parametrize("tiles", [64, 48, 36, 30, 25, 21, 16])
+def test_gemm_exact_tiles_shared_by_clusters(tiles):
+    # 152 // tiles CTAs to a tile, up to 8, as far as the device can place them
+    info = exact_check(20, 128 * tiles - 3, 8192, torch.bfloat16, cta_group=1, transposed=2, width=32)
+    assert 1 <= info["cluster"] <= 8 and info["split_tiles"] == tiles
+    assert info["cluster"] == 1 or info["grid_ctas"] == tiles * info["cluster"]
+    if tiles == 64:
+        assert info["cluster"] == 2
+    info = exact_check(128 * tiles - 1, 20, 8000, torch.float32, cta_group=1, transposed=1, width=32)
+    assert info["split_tiles"] == tiles
 
 
 @pytest.mark.parametrize("N", [127, 120, 124, 126])

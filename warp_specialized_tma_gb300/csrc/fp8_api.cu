@@ -30,7 +30,7 @@ struct Plan {
     uint64_t used = 0;  // for replacing the plan used longest ago
     int64_t M = 0, N = 0, K = 0, lda = 0, ldb = 0, ldd = 0;
     int out_type = 0;
-    int cta_group = 1, width = 32, stages = 2, grid = 0;
+    int cta_group = 1, width = 32, stages = 2, grid = 0, cluster = 1;
     bool transposed = false;
     int64_t tiles = 0, row_tiles = 0, col_tiles = 0, k_blocks = 0, sk_tiles = 0;
     size_t smem = 0;
@@ -192,31 +192,79 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct Tiling {
     bool transposed;
     int cta_group, width;
+    // found by tiling_cost()
+    int64_t clusters = 0;  // SM pairs, or CTAs, of the grid
+    int64_t sk_tiles = 0;
+    int cluster = 1;       // CTAs that share a tile in a cluster
 };
+
+int ring_stages(const fp8_gemm *h, int cta_group, int width)
+{
+    int S = kFp8MaxStages;
+    while (S > 2 && fp8_smem_bytes(cta_group, width, S) > h->max_smem)
+        S -= 2;
+    return S;
+}
+
+cudaError_t configure(const fp8_gemm *h, const void *fn)
+{
+    return cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->max_smem);
+}
+
+// How many clusters of c CTAs of a one-SM kernel are resident at once.
+int resident_clusters(const fp8_gemm *h, const Tiling &t, int c)
+{
+    const void *fn = fp8_gemm_kernel_fn(1, t.transposed);
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    int n = 0;
+    cfg.gridDim = dim3((unsigned)c, 1, 1);
+    cfg.blockDim = dim3(kFp8Threads, 1, 1);
+    cfg.dynamicSmemBytes = fp8_smem_bytes(1, t.width, ring_stages(h, 1, t.width));
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (configure(h, fn) != cudaSuccess || cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
 
 // Estimated time of a tiling, in clocks of an SM: the larger of the MMAs (8192
 // e4m3 multiply-adds a clock and SM) and the loads of a ring stage, times the
 // stages a cluster works through, plus what follows the last MMA.
-double tiling_cost(const fp8_gemm *h, const Plan &pl, const Tiling &t, int64_t *clusters, int64_t *sk_tiles)
+double tiling_cost(const fp8_gemm *h, const Plan &pl, Tiling &t)
 {
     const int64_t rows = t.transposed ? pl.N : pl.M, cols = t.transposed ? pl.M : pl.N;
     const int64_t KB = pl.k_blocks;
     const int64_t tiles = ceil_div(rows, kFp8RowsPerCta * t.cta_group) * ceil_div(cols, t.width);
-    int64_t most = t.cta_group == 2 ? h->max_pairs : h->num_sms;
+    const int64_t split = h->opt[FP8_GEMM_OPT_SPLIT];
+    const int64_t most = t.cta_group == 2 ? h->max_pairs : h->num_sms;
     int64_t sk = 0, C;
+    t.cluster = 1;
     if (tiles >= most) {
         C = most;
-        sk = h->opt[FP8_GEMM_OPT_SPLIT] ? tiles % C : 0;
+        sk = split ? tiles % C : 0;
     } else {
-        C = h->opt[FP8_GEMM_OPT_SPLIT] ? std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks)) : tiles;
+        C = split ? std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks)) : tiles;
         sk = C > tiles ? tiles : 0;
+        // a cluster of CTAs to a tile, where that uses most of those SMs
+        const int64_t c = std::min<int64_t>(C / tiles, 8);
+        if (split == 1 && t.cta_group == 1 && c >= 2 && tiles * c * 10 >= C * 6) {
+            t.cluster = (int)c;
+            C = tiles * c;
+        }
     }
-    *clusters = C;
-    *sk_tiles = sk;
+    t.clusters = C;
+    t.sk_tiles = sk;
     const double mma = std::max(2.0 * t.width, 128.0);
     const double load = (double)fp8_stage_bytes(t.cta_group, t.width) / 56.0;
     const double stages = sk ? (double)((tiles - sk) / C * KB) + (double)sk * KB / C : (double)(ceil_div(tiles, C) * KB);
-    return stages * std::max(mma, load) + 8.0 * t.width + (sk ? 3000.0 : 0.0);
+    return stages * std::max(mma, load) + 8.0 * t.width + (sk ? (t.cluster > 1 ? 2000.0 : 7000.0) : 0.0);
 }
 
 int make_plan(fp8_gemm_t h, Plan &pl)
@@ -225,7 +273,6 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     const int64_t want_w = h->opt[FP8_GEMM_OPT_WIDTH];
     Tiling best = {false, 0, 0};
     double best_cost = 0.0;
-    int64_t clusters = 0, sk = 0;
     for (int cg = 1; cg <= 2; ++cg)
         for (int tr = 0; tr <= 1; ++tr)
             for (int wd = 16; wd <= kFp8MaxWidth; wd += 16) {
@@ -235,12 +282,10 @@ int make_plan(fp8_gemm_t h, Plan &pl)
                 const int64_t cols = tr ? pl.M : pl.N;
                 if (wd % 32 != 0 && (cg == 2 || wd < cols))
                     continue;
-                const Tiling t = {tr != 0, cg, wd};
-                int64_t c, s;
-                const double cost = tiling_cost(h, pl, t, &c, &s);
-                if (best.cta_group == 0 || cost < best_cost) {
-                    best = t, best_cost = cost, clusters = c, sk = s;
-                }
+                Tiling t = {tr != 0, cg, wd};
+                const double cost = tiling_cost(h, pl, t);
+                if (best.cta_group == 0 || cost < best_cost)
+                    best = t, best_cost = cost;
             }
     if (best.cta_group == 0)
         return FP8_ERR_UNSUPPORTED;
@@ -253,20 +298,32 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     pl.tiles = pl.row_tiles * pl.col_tiles;
     if (pl.tiles > kMaxDim)
         return FP8_ERR_UNSUPPORTED;
-    pl.sk_tiles = sk;
-    pl.grid = (int)(clusters * best.cta_group);
-    int S = kFp8MaxStages;
-    while (S > 2 && fp8_smem_bytes(best.cta_group, best.width, S) > h->max_smem)
-        S -= 2;
-    pl.stages = S;
-    pl.smem = fp8_smem_bytes(best.cta_group, best.width, S);
+    // Rank 0 of a cluster waits for the others, so all clusters must be resident:
+    // the largest size that the device can place so often, or the exchange
+    // through global memory where that would leave too many SMs idle.
+    if (best.cluster > 1) {
+        int c = best.cluster;
+        while (c > 1 && resident_clusters(h, best, c) < pl.tiles)
+            --c;
+        if (c != best.cluster) {
+            const int64_t all = std::min<int64_t>(h->num_sms, pl.tiles * pl.k_blocks / kMinSplitBlocks);
+            const bool enough = c > 1 && pl.tiles * c * 10 >= all * 6;
+            best.cluster = enough ? c : 1;
+            best.clusters = enough ? pl.tiles * c : std::max(all, pl.tiles);
+            best.sk_tiles = best.clusters > pl.tiles ? pl.tiles : 0;
+        }
+    }
+    pl.sk_tiles = best.sk_tiles;
+    pl.cluster = best.cluster;
+    pl.grid = (int)(best.clusters * best.cta_group);
+    pl.stages = ring_stages(h, best.cta_group, best.width);
+    pl.smem = fp8_smem_bytes(best.cta_group, best.width, pl.stages);
     pl.fn = fp8_gemm_kernel_fn(best.cta_group, best.transposed);
     cudaFuncAttributes a;
-    if (cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)h->max_smem) != cudaSuccess ||
-        cudaFuncGetAttributes(&a, pl.fn) != cudaSuccess)
+    if (configure(h, pl.fn) != cudaSuccess || cudaFuncGetAttributes(&a, pl.fn) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     pl.regs = a.numRegs;
-    if (sk && !h->partials) {
+    if (pl.sk_tiles && pl.cluster == 1 && !h->partials) {
         const size_t ctas = (size_t)std::max(h->num_sms, 2 * h->max_pairs);
         void *f = nullptr, *g = nullptr;
         int rc = alloc_zeroed(&f, ctas * kFp8PartialFloats * sizeof(float));
@@ -405,7 +462,7 @@ FP8_API int fp8_gemm_set_option(fp8_gemm_t h, int key, int64_t value)
     case FP8_GEMM_OPT_CTA_GROUP: ok = value >= 0 && value <= 2; break;
     case FP8_GEMM_OPT_TRANSPOSED: ok = value >= 0 && value <= 2; break;
     case FP8_GEMM_OPT_WIDTH: ok = value >= 0 && value <= kFp8MaxWidth && value % 16 == 0; break;
-    case FP8_GEMM_OPT_SPLIT: ok = value == 0 || value == 1; break;
+    case FP8_GEMM_OPT_SPLIT: ok = value >= 0 && value <= 2; break;
     case FP8_GEMM_OPT_WATCHDOG_NS: ok = value >= 1000 && value <= 60000000000LL; break;
     case FP8_GEMM_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
     case FP8_GEMM_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
@@ -484,6 +541,7 @@ FP8_API int fp8_gemm_plan_info(fp8_gemm_t h, fp8_gemm_plan_info_t *info)
     info->split_tiles = (int32_t)pl.sk_tiles;
     info->smem_bytes = (int32_t)pl.smem;
     info->regs_per_thread = pl.regs;
+    info->cluster = pl.cluster;
     return FP8_OK;
 }
 
@@ -545,6 +603,7 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     p.stages = pl.stages;
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
+    p.cluster = pl.cluster;
     p.D_rows = (int32_t)pl.M;
     p.D_cols = (int32_t)pl.N;
     p.out_fp32 = pl.out_type == FP8_FP32 ? 1 : 0;
@@ -570,11 +629,12 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)pl.cta_group;
+    const int together = pl.cta_group * pl.cluster;  // one of the two is 1
+    attr[1].val.clusterDim.x = (unsigned)together;
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = pl.cta_group > 1 ? 2 : 1;
+    cfg.numAttrs = together > 1 ? 2 : 1;
     void *args[4] = {&pl.tmR, &pl.tmC, &pl.tmD, &p};
     const int rc = from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
     if (rc == FP8_OK)

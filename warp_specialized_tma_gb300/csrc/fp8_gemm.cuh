@@ -24,6 +24,10 @@
 // into one contiguous range per cluster; the other tiles are walked whole.  The
 // pieces of a split tile meet through global memory as fp32, added in range
 // order by the piece that holds k-block 0, so the result is the same every time.
+// Where the tiles times 2..8 nearly fill the GPU, the CTAs of a thread-block
+// cluster share a tile instead (the same ranges, every C-th of which starts at a
+// tile's start), and the pieces meet through distributed shared memory: the
+// exchange through global memory takes 4 us at the end of a 17 us call.
 // Every wait is bounded by the watchdog (WaitCtl in ptx.cuh).
 #pragma once
 
@@ -218,10 +222,12 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const uint32_t tmem_slot = done_bar + 8u;
     const uint32_t abort_flag = tmem_slot + 4u;
     const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
+    const uint32_t ready_bar = go_words + 8u;   // cluster form, rank 0: one per epilogue warp
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
-    const uint32_t rank = kCluster ? cluster_ctarank() : 0u;
+    const uint32_t rank = kCluster ? cluster_ctarank() : 0u;  // in an SM pair
+    const bool shared_tile = !kCluster && p.cluster > 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -233,6 +239,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             mbar_init(acce_bar + 8u * a, kFp8EpiWarps * CG);
         }
         mbar_init(done_bar, 1);
+        if (shared_tile)
+            for (int e = 0; e < kFp8EpiWarps; ++e)
+                mbar_init(ready_bar + 8u * e, (uint32_t)p.cluster - 1u);  // an arrival from every other rank
         st_shared_u32(abort_flag, 0u);
         fence_mbarrier_init();
     }
@@ -240,12 +249,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         prefetch_tensormap(&tmR);
         prefetch_tensormap(&tmC);
     }
-    // both CTAs of a pair have initialised their barriers before any cross-CTA
+    // all CTAs of a cluster have initialised their barriers before any cross-CTA
     // arrive, TMA completion or the paired allocation
-    if constexpr (kCluster)
+    if (kCluster || shared_tile) {
+        __syncwarp();
         cluster_arrive_wait();
-    else
+    } else {
         __syncthreads();
+    }
     if (warp == 2) {
         tmem_alloc<CG>(tmem_slot, 512);
         tmem_relinquish<CG>();
@@ -532,7 +543,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             // the clusters whose ranges start inside this tile, owner only
             int32_t last = cluster_id;
             bool parts = owner;
-            if (owner) {
+            if (owner && shared_tile) {
+                uint32_t got = 1u;
+                if (lane == 0)
+                    got = ctl.wait<true>(ready_bar + 8u * (uint32_t)ew, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
+                __syncwarp();  // lane 0's acquire comes before the lanes' loads
+                parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
+            } else if (owner) {
                 while (last + 1 < num_clusters &&
                        fp8_range_begin(p.sk_units, num_clusters, last + 1) < (int64_t)(w.tile + 1) * KB) {
                     ++last;
@@ -557,6 +574,15 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                             mbar_arrive(acce_bar + 8u * acc);
                     }
                 }
+                // The cluster form keeps a partial in the CTA's own ring: a
+                // contributor's only item has consumed all of its loads by now.
+                const uint32_t local = stage0 + (uint32_t)(((ew * 4 + (c >> 1)) * 8) * 32 + lane) * 16u;
+                if (contributor && shared_tile) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        st_shared_v4(local + 512u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    continue;
+                }
                 if (contributor) {
                     float4 *const mine = fp8_partial(p.partials, cta, ew, c >> 1, lane);
 #pragma unroll
@@ -565,7 +591,18 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                                                           __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])));
                     continue;
                 }
-                if (parts) {
+                if (parts && shared_tile) {
+                    for (int32_t rk = 1; rk < p.cluster; ++rk) {
+                        const uint32_t remote = mapa_shared(local, (uint32_t)rk);
+                        uint32_t x[32];  // all loads before the adds: their round trips overlap
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            ld_shared_cluster_v4(remote + 512u * j, x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(x[j]));
+                    }
+                } else if (parts) {
                     for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
                         const float4 *const part = fp8_partial(p.partials, j2 * CG + (int32_t)rank, ew, c >> 1, lane);
 #pragma unroll
@@ -608,9 +645,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             }
             if (contributor) {
                 __syncwarp();  // the warp's stores come before lane 0's release
-                if (lane == 0)
+                if (lane == 0 && shared_tile)
+                    mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (uint32_t)ew, 0u));
+                else if (lane == 0)
                     st_release_gpu_u32(p.flags + cta * kFp8EpiWarps + ew, 1u);
-            } else if (parts) {
+            } else if (parts && !shared_tile) {
                 // every lane's loads have returned (their sums are stored): the
                 // flags go back to 0 for the next launch
                 __syncwarp();
@@ -630,8 +669,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     // ---------------- teardown ----------------
     tc_fence_before_sync();
     __syncthreads();
-    if constexpr (kCluster)
-        cluster_arrive_wait();
+    if (kCluster || shared_tile)
+        cluster_arrive_wait();  // the peer is done with this CTA's memory
     if (warp == 2) {
         tc_fence_after_sync();
         tmem_dealloc<CG>(tmem_base, 512);

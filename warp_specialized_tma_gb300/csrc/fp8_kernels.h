@@ -96,6 +96,7 @@ struct Fp8GemmParams {
     int32_t stages;
     int32_t sk_tiles;       // tiles [0, sk_tiles) are split along k among all clusters
     int64_t sk_units;       // sk_tiles * num_k_blocks
+    int32_t cluster;        // > 1 (one SM per tile only): each tile is split among the CTAs of a cluster
     int32_t D_rows, D_cols;
     int32_t out_fp32;
     int32_t d_tma;          // D's layout allows TMA stores

@@ -93,6 +93,7 @@ class PlanInfo(ctypes.Structure):
         ("split_tiles", ctypes.c_int32),
         ("smem_bytes", ctypes.c_int32),
         ("regs_per_thread", ctypes.c_int32),
+        ("cluster", ctypes.c_int32),
     ]
 
     def as_dict(self) -> dict:
