@@ -112,16 +112,26 @@ def test_gemm_exact_few_tokens_both_ways(tokens):
         assert info["width"] == 16
 
 
-@pytest.mark.parametrize("tiles", [64, 48, 36, 30, 25, 21, 16])
+@pytest.mark.parametrize("tiles", [64, 48, 36, 30, 25, 21, 16, 5])
 def test_gemm_exact_tiles_shared_by_clusters(tiles):
     # 152 // tiles CTAs to a tile, up to 8, as far as the device can place them
     info = exact_check(20, 128 * tiles - 3, 8192, torch.bfloat16, cta_group=1, transposed=2, width=32)
-    assert 1 <= info["cluster"] <= 8 and info["split_tiles"] == tiles
-    assert info["cluster"] == 1 or info["grid_ctas"] == tiles * info["cluster"]
-    if tiles == 64:
-        assert info["cluster"] == 2
+    assert 2 <= info["cluster"] <= 8 and info["split_tiles"] == tiles
+    assert info["grid_ctas"] == tiles * info["cluster"]
     info = exact_check(128 * tiles - 1, 20, 8000, torch.float32, cta_group=1, transposed=1, width=32)
-    assert info["split_tiles"] == tiles
+    assert 2 <= info["cluster"] <= 8
+
+
+@pytest.mark.parametrize("over", [1, 3, 70, 140])
+@pytest.mark.parametrize("cta_group,K", [(1, 8192), (2, 8192), (1, 12000)])
+def test_gemm_exact_partial_wave_shared_by_all(cta_group, K, over):
+    # a few tiles more than SMs (or SM pairs): the rest is split through global
+    # memory, down to fewer k-blocks than there are clusters to take them
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    tiles = sms // cta_group + over // cta_group
+    info = exact_check(32, 128 * cta_group * tiles, K, torch.bfloat16, cta_group=cta_group, transposed=2, width=32,
+                       split=2)
+    assert info["tiles"] == tiles and info["split_tiles"] in (0, tiles - sms // cta_group)
 
 
 @pytest.mark.parametrize("N", [127, 120, 124, 126])

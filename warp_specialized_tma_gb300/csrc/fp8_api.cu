@@ -234,9 +234,14 @@ int resident_clusters(const fp8_gemm *h, const Tiling &t, int c)
     return n;
 }
 
-// Estimated time of a tiling, in clocks of an SM: the larger of the MMAs (8192
-// e4m3 multiply-adds a clock and SM) and the loads of a ring stage, times the
-// stages a cluster works through, plus what follows the last MMA.
+// Estimated time of a tiling, in clocks of an SM (1.9 GHz), without what every
+// launch costs: the stages (k-blocks) of the longest chain, each the longest of
+// its MMAs (8192 e4m3 multiply-adds a clock and SM), its loads (56 bytes a clock
+// and SM with all SMs loading) and what the MMA issuer needs (400 clocks); or the
+// operands' time in HBM, if longer; then the epilogue and the exchange between a
+// split tile's pieces.  The exchanges' costs are fitted to measurements: through a
+// cluster 8x700x1500 loses 0.5 us by saving 8 of 12 stages; through global memory
+// 1x8192x8192 spends 4 us, 1000x1000x8000 in four pieces of 224 columns 14 us.  Fills in how the tiles are shared out.
 double tiling_cost(const fp8_gemm *h, const Plan &pl, Tiling &t)
 {
     const int64_t rows = t.transposed ? pl.N : pl.M, cols = t.transposed ? pl.M : pl.N;
@@ -244,27 +249,47 @@ double tiling_cost(const fp8_gemm *h, const Plan &pl, Tiling &t)
     const int64_t tiles = ceil_div(rows, kFp8RowsPerCta * t.cta_group) * ceil_div(cols, t.width);
     const int64_t split = h->opt[FP8_GEMM_OPT_SPLIT];
     const int64_t most = t.cta_group == 2 ? h->max_pairs : h->num_sms;
-    int64_t sk = 0, C;
+    const double stage = std::max({2.0 * t.width, 400.0, (double)fp8_stage_bytes(t.cta_group, t.width) / 56.0});
+    const double hbm = (double)(pl.M + pl.N) * (double)pl.K / 3500.0;
+    const double epilogue = 8.0 * t.width;
+
+    t.clusters = std::min(tiles, most);
+    t.sk_tiles = 0;
     t.cluster = 1;
-    if (tiles >= most) {
-        C = most;
-        sk = split ? tiles % C : 0;
-    } else {
-        C = split ? std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks)) : tiles;
-        sk = C > tiles ? tiles : 0;
-        // a cluster of CTAs to a tile, where that uses most of those SMs
-        const int64_t c = std::min<int64_t>(C / tiles, 8);
-        if (split == 1 && t.cta_group == 1 && c >= 2 && tiles * c * 10 >= C * 6) {
-            t.cluster = (int)c;
-            C = tiles * c;
+    double best = std::max((double)(ceil_div(tiles, t.clusters) * KB) * stage, hbm) + epilogue;
+    if (split == 1 && t.cta_group == 1) {
+        // each tile shared by a cluster of CTAs
+        const int64_t c = std::min<int64_t>({most / tiles, 8, KB});
+        if (c >= 2) {
+            const double cost =
+                std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + 4500.0 + (400.0 + 8.0 * t.width) * (double)(c - 1);
+            if (cost < best) {
+                best = cost;
+                t.clusters = tiles * c;
+                t.sk_tiles = tiles;
+                t.cluster = (int)c;
+            }
         }
     }
-    t.clusters = C;
-    t.sk_tiles = sk;
-    const double mma = std::max(2.0 * t.width, 128.0);
-    const double load = (double)fp8_stage_bytes(t.cta_group, t.width) / 56.0;
-    const double stages = sk ? (double)((tiles - sk) / C * KB) + (double)sk * KB / C : (double)(ceil_div(tiles, C) * KB);
-    return stages * std::max(mma, load) + 8.0 * t.width + (sk ? (t.cluster > 1 ? 2000.0 : 7000.0) : 0.0);
+    if (split) {
+        // the last, partial wave of tiles (or all, if they do not fill one) shared by all clusters
+        const int64_t sk = tiles % most;
+        const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
+        if (sk && C > sk) {
+            // behind whole tiles the exchange is out of sight: the split tiles come first
+            const int64_t whole = (tiles - sk) / C;
+            const double exchange = whole ? 3000.0 : 7500.0 + (700.0 + 12.0 * t.width) * (double)C / (double)sk;
+            const double cost =
+                std::max((double)(whole * KB + ceil_div(sk * KB, C)) * stage, hbm) + epilogue + exchange;
+            if (cost < best) {
+                best = cost;
+                t.clusters = C;
+                t.sk_tiles = sk;
+                t.cluster = 1;
+            }
+        }
+    }
+    return best;
 }
 
 int make_plan(fp8_gemm_t h, Plan &pl)
@@ -299,19 +324,12 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     if (pl.tiles > kMaxDim)
         return FP8_ERR_UNSUPPORTED;
     // Rank 0 of a cluster waits for the others, so all clusters must be resident:
-    // the largest size that the device can place so often, or the exchange
-    // through global memory where that would leave too many SMs idle.
+    // the largest size that the device can place so often.
     if (best.cluster > 1) {
-        int c = best.cluster;
-        while (c > 1 && resident_clusters(h, best, c) < pl.tiles)
-            --c;
-        if (c != best.cluster) {
-            const int64_t all = std::min<int64_t>(h->num_sms, pl.tiles * pl.k_blocks / kMinSplitBlocks);
-            const bool enough = c > 1 && pl.tiles * c * 10 >= all * 6;
-            best.cluster = enough ? c : 1;
-            best.clusters = enough ? pl.tiles * c : std::max(all, pl.tiles);
-            best.sk_tiles = best.clusters > pl.tiles ? pl.tiles : 0;
-        }
+        while (best.cluster > 1 && resident_clusters(h, best, best.cluster) < pl.tiles)
+            --best.cluster;
+        best.clusters = pl.tiles * best.cluster;
+        best.sk_tiles = best.cluster > 1 ? pl.tiles : 0;
     }
     pl.sk_tiles = best.sk_tiles;
     pl.cluster = best.cluster;

@@ -46,6 +46,17 @@ __host__ __device__ __forceinline__ int64_t fp8_range_begin(int64_t units, int32
     return (int64_t)c * units / clusters;
 }
 
+__host__ __device__ __forceinline__ bool fp8_range_holds(int64_t units, int32_t clusters, int32_t c)
+{
+    return fp8_range_begin(units, clusters, c) < fp8_range_begin(units, clusters, c + 1);
+}
+
+// The range that holds unit u.
+__host__ __device__ __forceinline__ int32_t fp8_range_of(int64_t units, int32_t clusters, int64_t u)
+{
+    return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
+}
+
 // A cluster's items in order: its range of the split tiles' units (a range is no
 // longer than a tile, since sk_tiles < clusters, so it touches at most two
 // tiles), then every clusters-th whole tile.  A range's first piece may start
@@ -523,6 +534,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         uint32_t acc_ph = 0;
         uint32_t item_parity = 0;
         uint32_t buf = 0;
+        const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
         while (wi.next(w)) {
             // one thread waits for the accumulator and posts the outcome, so that
             // all warps take the same branch; the word alternates with the item
@@ -540,7 +552,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             const int32_t yc = tc.nb * width;
             const bool contributor = w.kb0 > 0;
             const bool owner = w.kb0 == 0 && w.kb1 < KB;
-            // the clusters whose ranges start inside this tile, owner only
+            // the clusters whose ranges start inside this tile, owner only; a range
+            // may be empty (fewer units than clusters), and then leaves nothing
             int32_t last = cluster_id;
             bool parts = owner;
             if (owner && shared_tile) {
@@ -550,13 +563,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 __syncwarp();  // lane 0's acquire comes before the lanes' loads
                 parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
             } else if (owner) {
-                while (last + 1 < num_clusters &&
-                       fp8_range_begin(p.sk_units, num_clusters, last + 1) < (int64_t)(w.tile + 1) * KB) {
-                    ++last;
-                    // a give-up stores the tile unsummed, and the status says so
-                    parts = parts && warp_wait_flag(
-                                         ctl, p.flags + (last * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u, lane);
-                }
+                last = fp8_range_of(p.sk_units, num_clusters, (int64_t)(w.tile + 1) * KB - 1);
+                for (int32_t j2 = cluster_id + 1; parts && j2 <= last; ++j2)
+                    if (dense || fp8_range_holds(p.sk_units, num_clusters, j2))
+                        // a give-up stores the tile unsummed, and the status says so
+                        parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u, lane);
             }
             for (int c = half; c < nchunks; c += 2) {
                 uint32_t v[32];
@@ -604,6 +615,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     }
                 } else if (parts) {
                     for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
+                        if (!dense && !fp8_range_holds(p.sk_units, num_clusters, j2))
+                            continue;
                         const float4 *const part = fp8_partial(p.partials, j2 * CG + (int32_t)rank, ew, c >> 1, lane);
 #pragma unroll
                         for (int j = 0; j < 8; ++j) {
