@@ -53,7 +53,8 @@ typedef enum fp8_gemm_option {
     FP8_GEMM_OPT_CTA_GROUP = 1,   /* 0 = automatic, 1 = one SM per tile, 2 = SM pairs */
     FP8_GEMM_OPT_TRANSPOSED = 2,  /* 0 = automatic, 1 = A's rows on the MMA's row side, 2 = B's rows */
     FP8_GEMM_OPT_WIDTH = 3,       /* 0 = automatic, else the tile's width on the MMA's column side:
-                                     a multiple of 16 (32 for SM pairs), at most 224 */
+                                     a multiple of 16 (32 for SM pairs), at most 224 (192 for an fp32 D
+                                     with K > 4096) */
     FP8_GEMM_OPT_SPLIT = 4,       /* tiles that would leave SMs idle are split along K: 1 = among clusters of CTAs or
                                      through global memory (default), 2 = through global memory only, 0 = never */
     FP8_GEMM_OPT_WATCHDOG_NS = 5, /* limit of any wait inside the kernel (default 2e9) */

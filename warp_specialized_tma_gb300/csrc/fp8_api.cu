@@ -51,7 +51,8 @@ struct fp8_gemm {
     size_t max_smem = 0;
     int max_pairs = 0;  // SM pairs that are resident at once
     uint32_t *d_err = nullptr;
-    float *partials = nullptr;  // allocated by the first plan that splits tiles, at its final size
+    // workspace of split tiles, allocated at its final size by the first plan that needs it
+    float *partials = nullptr;
     uint32_t *flags = nullptr;
     int64_t opt[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0};
     Plan plans[kPlans];
@@ -198,6 +199,9 @@ struct Tiling {
     int cluster = 1;       // CTAs that share a tile in a cluster
 };
 
+// An fp32 D of a long sum is accumulated in segments.
+bool long_sums(const Plan &pl) { return pl.out_type == FP8_FP32 && pl.k_blocks > kFp8Segment; }
+
 int ring_stages(const fp8_gemm *h, int cta_group, int width)
 {
     int S = kFp8MaxStages;
@@ -212,9 +216,9 @@ cudaError_t configure(const fp8_gemm *h, const void *fn)
 }
 
 // How many clusters of c CTAs of a one-SM kernel are resident at once.
-int resident_clusters(const fp8_gemm *h, const Tiling &t, int c)
+int resident_clusters(const fp8_gemm *h, const Plan &pl, const Tiling &t, int c)
 {
-    const void *fn = fp8_gemm_kernel_fn(1, t.transposed);
+    const void *fn = fp8_gemm_kernel_fn(1, t.transposed, long_sums(pl));
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[1];
     int n = 0;
@@ -307,6 +311,8 @@ int make_plan(fp8_gemm_t h, Plan &pl)
                 const int64_t cols = tr ? pl.M : pl.N;
                 if (wd % 32 != 0 && (cg == 2 || wd < cols))
                     continue;
+                if (wd > kFp8MaxLongWidth && long_sums(pl))
+                    continue;
                 Tiling t = {tr != 0, cg, wd};
                 const double cost = tiling_cost(h, pl, t);
                 if (best.cta_group == 0 || cost < best_cost)
@@ -326,7 +332,7 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     // Rank 0 of a cluster waits for the others, so all clusters must be resident:
     // the largest size that the device can place so often.
     if (best.cluster > 1) {
-        while (best.cluster > 1 && resident_clusters(h, best, best.cluster) < pl.tiles)
+        while (best.cluster > 1 && resident_clusters(h, pl, best, best.cluster) < pl.tiles)
             --best.cluster;
         best.clusters = pl.tiles * best.cluster;
         best.sk_tiles = best.cluster > 1 ? pl.tiles : 0;
@@ -336,26 +342,20 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     pl.grid = (int)(best.clusters * best.cta_group);
     pl.stages = ring_stages(h, best.cta_group, best.width);
     pl.smem = fp8_smem_bytes(best.cta_group, best.width, pl.stages);
-    pl.fn = fp8_gemm_kernel_fn(best.cta_group, best.transposed);
+    pl.fn = fp8_gemm_kernel_fn(best.cta_group, best.transposed, long_sums(pl));
     cudaFuncAttributes a;
     if (configure(h, pl.fn) != cudaSuccess || cudaFuncGetAttributes(&a, pl.fn) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     pl.regs = a.numRegs;
-    if (pl.sk_tiles && pl.cluster == 1 && !h->partials) {
-        const size_t ctas = (size_t)std::max(h->num_sms, 2 * h->max_pairs);
-        void *f = nullptr, *g = nullptr;
-        int rc = alloc_zeroed(&f, ctas * kFp8PartialFloats * sizeof(float));
-        if (rc == FP8_OK)
-            rc = alloc_zeroed(&g, ctas * kFp8EpiWarps * sizeof(uint32_t));
-        if (rc != FP8_OK) {
-            if (f)
-                cudaFree(f);
-            return rc;
-        }
-        h->partials = static_cast<float *>(f);
-        h->flags = static_cast<uint32_t *>(g);
+    const size_t ctas = (size_t)std::max(h->num_sms, 2 * h->max_pairs);
+    int rc = FP8_OK;
+    if (pl.sk_tiles && pl.cluster == 1) {
+        if (!h->partials)
+            rc = alloc_zeroed((void **)&h->partials, ctas * kFp8PartialFloats * sizeof(float));
+        if (rc == FP8_OK && !h->flags)
+            rc = alloc_zeroed((void **)&h->flags, ctas * kFp8EpiWarps * sizeof(uint32_t));
     }
-    return FP8_OK;
+    return rc;
 }
 
 size_t flag_bytes(const fp8_gemm *h)
@@ -426,7 +426,7 @@ FP8_API int fp8_gemm_create(int device, fp8_gemm_t *out)
     h->max_smem = (size_t)optin;
     // SM pairs resident at once: half the SMs, unless some SM has no partner
     {
-        const void *fn = fp8_gemm_kernel_fn(2, false);
+        const void *fn = fp8_gemm_kernel_fn(2, false, false);
         cudaLaunchConfig_t cfg = {};
         cudaLaunchAttribute attr[1];
         int n = 0;

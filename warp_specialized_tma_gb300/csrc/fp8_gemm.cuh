@@ -31,6 +31,8 @@
 // Every wait is bounded by the watchdog (WaitCtl in ptx.cuh).
 #pragma once
 
+#include <stdint.h>
+
 #include "fp8_kernels.h"
 #include "fp8_ptx.cuh"
 #include "gemm_common.cuh"
@@ -56,6 +58,11 @@ __host__ __device__ __forceinline__ int32_t fp8_range_of(int64_t units, int32_t 
 {
     return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
 }
+
+// End of the accumulation that k-block kb belongs to (kLong): a multiple of 4, so
+// that a group of scales never spans two.
+__device__ __forceinline__ int32_t fp8_segment_end(int32_t kb) { return kb / kFp8Segment * kFp8Segment + kFp8Segment; }
+static_assert(kFp8Segment % 4 == 0, "scales come in groups of 4 k-blocks");
 
 // A cluster's items in order: its range of the split tiles' units (a range is no
 // longer than a tile, since sk_tiles < clusters, so it touches at most two
@@ -130,9 +137,8 @@ __device__ __forceinline__ uint32_t fp8_chunk_offset(uint32_t r, uint32_t c, boo
 // layout or its last columns do not allow one (a TMA store writes whole 16-byte
 // groups), by the warp's masked stores.
 __device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, const CUtensorMap *tmD, int32_t x, int32_t y,
-                                                const Fp8GemmParams &p)
+                                                bool fp32, const Fp8GemmParams &p)
 {
-    const bool fp32 = p.out_fp32 != 0;
     const int32_t group = fp32 ? 4 : 8;
     if (p.d_tma && (x + 32 <= p.D_cols || p.D_cols % group == 0)) {
         fence_proxy_async_shared();
@@ -209,7 +215,35 @@ __device__ __forceinline__ float4 *fp8_partial(float *partials, int32_t cta, int
     return reinterpret_cast<float4 *>(partials + (size_t)cta * kFp8PartialFloats) + ((ew * 4 + ci) * 8) * 32 + lane;
 }
 
-template <int CG, bool kTransposed>
+__device__ __forceinline__ void fp8_store_partial(const uint32_t (&v)[32], float4 *part)
+{
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        __stcg(part + j * 32, make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                          __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])));
+}
+
+template <int kBatch>
+__device__ __forceinline__ void fp8_add_partial(uint32_t (&v)[32], const float4 *part)
+{
+#pragma unroll
+    for (int j0 = 0; j0 < 8; j0 += kBatch) {
+        float4 f[kBatch];
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j)
+            f[j] = __ldcg(part + (j0 + j) * 32);
+#pragma unroll
+        for (int j = 0; j < kBatch; ++j) {
+            uint32_t *const x = &v[4 * (j0 + j)];
+            x[0] = __float_as_uint(__uint_as_float(x[0]) + f[j].x);
+            x[1] = __float_as_uint(__uint_as_float(x[1]) + f[j].y);
+            x[2] = __float_as_uint(__uint_as_float(x[2]) + f[j].z);
+            x[3] = __float_as_uint(__uint_as_float(x[3]) + f[j].w);
+        }
+    }
+}
+
+template <int CG, bool kTransposed, bool kLong>
 __global__ void __launch_bounds__(kFp8Threads, 1)
     fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmR, const __grid_constant__ CUtensorMap tmC,
                     const __grid_constant__ CUtensorMap tmD, const Fp8GemmParams p)
@@ -293,233 +327,248 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     wi.init(p, cluster_id, num_clusters);
     Fp8Item w;
 
-    if (warp == 0 && lane == 0) {
-        // ---------------- TMA producer ----------------
-        const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
-        int s = 0;
-        uint32_t ph = 0;
-        int32_t it = 0;
-        bool ok = true;
-        grid_dependency_wait();
-        while (ok && wi.next(w)) {
-            const TileCoord tc = fp8_tile_coord(w.tile, p);
-            const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta;
-            const int32_t yc = tc.nb * width + (int32_t)rank * (width / CG);
-            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                if (ring_group_first(s, 1u) &&
-                    !ctl.wait<kCluster>(empty_bar + 8u * ring_group(s, 1u), ring_empty_parity(ph), kRoleProducer,
-                                        (uint32_t)s)) {
-                    ok = false;
-                    break;
-                }
-                if (it != p.fault_skip_it) {
-                    if (!kCluster || rank == 0)
-                        mbar_arrive_expect_tx(full_bar + 8u * s, stage_bytes * CG);
-                    const uint32_t fb = full_target + 8u * s;
-                    const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
-                    if constexpr (kCluster) {
-                        tma_load_2d_pair(sa, &tmR, kb * kFp8BlockK, yr, fb);
-                        tma_load_2d_pair(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
-                    } else {
-                        tma_load_2d(sa, &tmR, kb * kFp8BlockK, yr, fb);
-                        tma_load_2d(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
-                    }
-                }
-                ++it;
-                ring_advance(s, ph, S);
-            }
-        }
-        grid_launch_dependents();
-        // Teardown: the last S loads may still be in flight if a role gave up.
-        if (!kCluster || rank == 0) {
-            const int32_t n = it < S ? it : S;
-            for (int32_t d = 1; d <= n; ++d) {
-                const int32_t j = it - d;
-                if (j == p.fault_skip_it)
-                    continue;
-                ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
-                                         (uint32_t)ring_stage_of(j, S));
-            }
-        } else if (ctl.aborted()) {
-            // the peer's loads complete on the leader's barriers, which this CTA
-            // cannot poll: a fixed grace period instead
-            const uint64_t t0 = globaltimer_ns();
-            while (globaltimer_ns() - t0 < 50000ull) {
-            }
-        }
-    } else if (warp == 1 && rank == 0) {
-        // ---------------- MMA issuer ----------------
-        const uint64_t rdesc0 = smem_desc_sw128(stage0);
-        const uint64_t cdesc0 = smem_desc_sw128(stage0 + kRBytes);
-        const uint64_t sdesc0 = smem_desc_scales(scales0);
-        const uint32_t idesc0 = idesc_mxf8(kFp8RowsPerCta * CG, 0) | ((uint32_t)(width >> 3) << 17);
-        const uint32_t step = stage_bytes >> 4;
-        const uint32_t leader = elect_one();
-        // Waits here are loops inside one statement, and a wait that runs out does
-        // not leave the k loop: it records the fact and the rest of the item runs
-        // with single probes (its result is wrong, and the status says so).
-        const uint32_t probe_ns = ctl.suspend_ns;
-        uint32_t tries = (uint32_t)(ctl.limit_ns / probe_ns) + 1u;
-        uint32_t bad = 0u;
-        auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role, uint32_t where) {
-            if (mbar_wait_tries(bar, parity, probe_ns, tries) == 0u) {
-                if (bad == 0u && leader)
-                    ctl.fail(role, where);
-                bad = 1u;
-                tries = 1u;
-            }
-        };
-        int s = 0;
-        uint32_t ph = 0;
-        int acc = 0;
-        uint32_t acc_ph = 0;
-        uint32_t group = 0;  // groups of 4 k-blocks so far: their parity picks the scales' buffer
-        while (wi.next(w)) {
-            wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
-            tc_fence_after_sync();
-            const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFp8MaxWidth);
-            uint32_t stm = 0;
-            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
-                tc_fence_after_sync();
-                if (kb == w.kb0 || (kb & 3) == 0) {
-                    // copies and MMAs of one thread execute in order: the copy
-                    // into a buffer follows the MMAs that last read it
-                    stm = tmem_base + kFp8ScaleCol + 32u * (group & 1u);
-                    ++group;
-                    const uint64_t sd = sdesc0 + (uint64_t)((uint32_t)s * (kFp8ScaleBytes >> 4));
-                    copy_scales<CG>(stm, sd, leader);
-                    copy_scales<CG>(stm + kFp8ScaleColB, sd + (512u >> 4), leader);
-                    if (width > 128)
-                        copy_scales<CG>(stm + kFp8ScaleColB + 4u, sd + (1024u >> 4), leader);
-                }
-                const uint64_t off = (uint64_t)((uint32_t)s * step);
-                const uint32_t idesc = idesc0 | scale_id((uint32_t)kb & 3u);
-#pragma unroll
-                for (int kk = 0; kk < kFp8BlockK / 32; ++kk)
-                    mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
-                                 stm + kFp8ScaleColB, (kb != w.kb0 || kk != 0) ? 1u : 0u, leader);
-                if (ring_group_last(s, 1u))
-                    mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);
-                ring_advance(s, ph, S);
-            }
-            mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
-            acc ^= 1;
-            if (acc == 0)
-                acc_ph ^= 1u;
-            if (__any_sync(0xFFFFFFFFu, bad))
-                break;
-        }
-        // no MMA may still be writing tensor memory when it is freed
-        mma_commit_elected<CG>(done_bar, leader);
-        if (leader)
-            ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
-        __syncwarp();
-    } else if (warp == 2 || warp == 3) {
-        // ---------------- scales ----------------
-        // The stage of a group's first k-block carries the group's words: 32 rows of
-        // four, the words of rows r, r + 32, r + 64 and r + 96 of the row side at
-        // 16 r, those of the column side's rows behind them in two such blocks.
-        // Rows past the end count as scale 1; they meet only zeros, in parts of the
-        // tile that are not stored.  The two warps bring groups in turn (one alone
-        // is busy 400 of the 450 clocks that a wide tile's k-block lasts), each with
-        // its next group's words in flight while it hands over the last ones.  Both
-        // wait for every release and arrive on every stage's full barrier: so the
-        // MMA issuer waits for scales and operands at once, and neither warp can
-        // run two phases of a barrier ahead or behind, which its parity would not
-        // tell.
-        const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
-        const uint32_t which = (uint32_t)warp & 1u;
-        Fp8Work wl = wi;  // the loads' place in the work
-        Fp8Item il = {0, 0, 0};
-        int32_t left = 0;       // groups of the loads' item still to come
-        uint32_t gl = 0;        // groups the loads have passed
-        uint32_t live = 0u;     // which of the twelve words exist
-        const uint32_t *sr = nullptr, *sc = nullptr;
-        uint32_t v[2][12];
-        auto load = [&](uint32_t(&x)[12]) {
-            for (;;) {
-                if (left == 0) {
-                    if (!wl.next(il))
-                        return;
-                    const TileCoord tc = fp8_tile_coord(il.tile, p);
-                    const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + lane;
-                    const int32_t yc = tc.nb * width + lane;
-                    const int32_t kt = il.kb0 >> 2;
-                    left = ((il.kb1 - 1) >> 2) + 1 - kt;
-                    sr = p.s_rows + (int64_t)kt * p.rows + yr;
-                    sc = p.s_cols + (int64_t)kt * p.cols + yc;
-                    live = 0u;
-#pragma unroll
-                    for (int j = 0; j < 12; ++j)
-                        if (j < 4 ? yr + 32 * j < p.rows : 32 * (j - 4) < width && yc + 32 * (j - 4) < p.cols)
-                            live |= 1u << j;
-                }
-                const bool mine = (gl & 1u) == which;
-                if (mine) {
-#pragma unroll
-                    for (int j = 0; j < 12; ++j)
-                        x[j] = live & (1u << j) ? (j < 4 ? sr[32 * j] : sc[32 * (j - 4)]) : 0x7F7F7F7Fu;
-                }
-                sr += p.rows;
-                sc += p.cols;
-                --left;
-                ++gl;
-                if (mine)
-                    return;
-            }
-        };
-        grid_dependency_wait();
-        load(v[0]);
-        load(v[1]);
-        int s = 0;
-        uint32_t ph = 0;
-        uint32_t g = 0;
-        bool ok = true;
-        while (ok && wi.next(w)) {
-            for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                if (ring_group_first(s, 1u)) {
-                    const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
-                    if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
-                        !warp_wait<false>(ctl, bar, parity, kRoleScales, (uint32_t)s, lane)) {
+    if (warp < 4) {
+        if (warp == 0 && lane == 0) {
+            // ---------------- TMA producer ----------------
+            const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
+            int s = 0;
+            uint32_t ph = 0;
+            int32_t it = 0;
+            bool ok = true;
+            grid_dependency_wait();
+            while (ok && wi.next(w)) {
+                const TileCoord tc = fp8_tile_coord(w.tile, p);
+                const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta;
+                const int32_t yc = tc.nb * width + (int32_t)rank * (width / CG);
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (ring_group_first(s, 1u) &&
+                        !ctl.wait<kCluster>(empty_bar + 8u * ring_group(s, 1u), ring_empty_parity(ph), kRoleProducer,
+                                            (uint32_t)s)) {
                         ok = false;
                         break;
                     }
+                    if (it != p.fault_skip_it) {
+                        if (!kCluster || rank == 0)
+                            mbar_arrive_expect_tx(full_bar + 8u * s, stage_bytes * CG);
+                        const uint32_t fb = full_target + 8u * s;
+                        const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
+                        if constexpr (kCluster) {
+                            tma_load_2d_pair(sa, &tmR, kb * kFp8BlockK, yr, fb);
+                            tma_load_2d_pair(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
+                        } else {
+                            tma_load_2d(sa, &tmR, kb * kFp8BlockK, yr, fb);
+                            tma_load_2d(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
+                        }
+                    }
+                    ++it;
+                    ring_advance(s, ph, S);
                 }
-                const bool first = kb == w.kb0 || (kb & 3) == 0;
-                const bool last = kb == w.kb1 - 1 || (kb & 3) == 3;
-                const bool mine = (g & 1u) == which;
-                if (mine && first) {
-                    const uint32_t at = scales0 + (uint32_t)s * kFp8ScaleBytes + 16u * (uint32_t)lane;
-                    st_shared_v4(at, v[0][0], v[0][1], v[0][2], v[0][3]);
-                    st_shared_v4(at + 512u, v[0][4], v[0][5], v[0][6], v[0][7]);
-                    if (width > 128)
-                        st_shared_v4(at + 1024u, v[0][8], v[0][9], v[0][10], v[0][11]);
-                    fence_proxy_async_shared();
-                    __syncwarp();
+            }
+            grid_launch_dependents();
+            // Teardown: the last S loads may still be in flight if a role gave up.
+            if (!kCluster || rank == 0) {
+                const int32_t n = it < S ? it : S;
+                for (int32_t d = 1; d <= n; ++d) {
+                    const int32_t j = it - d;
+                    if (j == p.fault_skip_it)
+                        continue;
+                    ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
+                                             (uint32_t)ring_stage_of(j, S));
                 }
-                // Each CTA's words stay in its own shared memory, where its own half
-                // of the paired copy reads them: the proxy fence has put them there
-                // before the arrive leaves.  So the arrive on the leader's barrier
-                // releases at CTA scope; at cluster scope it waits for all of this
-                // thread's memory traffic, loads too (measured 600 ns).
-                if (lane == 0) {
-                    if constexpr (kCluster)
-                        mbar_arrive_cluster_handoff(full_target + 8u * s);
-                    else
-                        mbar_arrive(full_target + 8u * s);
+            } else if (ctl.aborted()) {
+                // the peer's loads complete on the leader's barriers, which this CTA
+                // cannot poll: a fixed grace period instead
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 50000ull) {
                 }
-                if (mine && last) {
+            }
+        } else if (warp == 1 && rank == 0) {
+            // ---------------- MMA issuer ----------------
+            const uint64_t rdesc0 = smem_desc_sw128(stage0);
+            const uint64_t cdesc0 = smem_desc_sw128(stage0 + kRBytes);
+            const uint64_t sdesc0 = smem_desc_scales(scales0);
+            const uint32_t idesc0 = idesc_mxf8(kFp8RowsPerCta * CG, 0) | ((uint32_t)(width >> 3) << 17);
+            const uint32_t step = stage_bytes >> 4;
+            const uint32_t leader = elect_one();
+            // Waits here are loops inside one statement, and a wait that runs out does
+            // not leave the k loop: it records the fact and the rest of the item runs
+            // with single probes (its result is wrong, and the status says so).
+            const uint32_t probe_ns = ctl.suspend_ns;
+            uint32_t tries = (uint32_t)(ctl.limit_ns / probe_ns) + 1u;
+            uint32_t bad = 0u;
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role, uint32_t where) {
+                if (mbar_wait_tries(bar, parity, probe_ns, tries) == 0u) {
+                    if (bad == 0u && leader)
+                        ctl.fail(role, where);
+                    bad = 1u;
+                    tries = 1u;
+                }
+            };
+            int s = 0;
+            uint32_t ph = 0;
+            int acc = 0;
+            uint32_t acc_ph = 0;
+            uint32_t group = 0;  // groups of 4 k-blocks so far: their parity picks the scales' buffer
+            while (wi.next(w)) {
+                wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
+                tc_fence_after_sync();
+                uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFp8MaxWidth);
+                uint32_t stm = 0;
+                int32_t cut = kLong ? fp8_segment_end(w.kb0) : INT32_MAX;  // the accumulator's sums move on there
+                uint32_t fresh = 1u;                      // the accumulator starts over
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (kLong && kb == cut) {
+                        mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
+                        acc ^= 1;
+                        acc_ph ^= acc == 0 ? 1u : 0u;
+                        wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
+                        tc_fence_after_sync();
+                        d_tmem = tmem_base + (uint32_t)(acc * kFp8MaxWidth);
+                        cut = fp8_segment_end(kb);
+                        fresh = 1u;
+                    }
+                    wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
+                    tc_fence_after_sync();
+                    if (kb == w.kb0 || (kb & 3) == 0) {
+                        // copies and MMAs of one thread execute in order: the copy
+                        // into a buffer follows the MMAs that last read it
+                        stm = tmem_base + kFp8ScaleCol + 32u * (group & 1u);
+                        ++group;
+                        const uint64_t sd = sdesc0 + (uint64_t)((uint32_t)s * (kFp8ScaleBytes >> 4));
+                        copy_scales<CG>(stm, sd, leader);
+                        copy_scales<CG>(stm + kFp8ScaleColB, sd + (512u >> 4), leader);
+                        if (width > 128)
+                            copy_scales<CG>(stm + kFp8ScaleColB + 4u, sd + (1024u >> 4), leader);
+                    }
+                    const uint64_t off = (uint64_t)((uint32_t)s * step);
+                    const uint32_t idesc = idesc0 | scale_id((uint32_t)kb & 3u);
 #pragma unroll
-                    for (int j = 0; j < 12; ++j)
-                        v[0][j] = v[1][j];
-                    load(v[1]);
+                    for (int kk = 0; kk < kFp8BlockK / 32; ++kk)
+                        mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
+                                     stm + kFp8ScaleColB, kk != 0 ? 1u : fresh ^ 1u, leader);
+                    fresh = 0u;
+                    if (ring_group_last(s, 1u))
+                        mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);
+                    ring_advance(s, ph, S);
                 }
-                g += last ? 1u : 0u;
-                ring_advance(s, ph, S);
+                mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
+                acc ^= 1;
+                if (acc == 0)
+                    acc_ph ^= 1u;
+                if (__any_sync(0xFFFFFFFFu, bad))
+                    break;
+            }
+            // no MMA may still be writing tensor memory when it is freed
+            mma_commit_elected<CG>(done_bar, leader);
+            if (leader)
+                ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+            __syncwarp();
+        } else if (warp == 2 || warp == 3) {
+            // ---------------- scales ----------------
+            // The stage of a group's first k-block carries the group's words: 32 rows of
+            // four, the words of rows r, r + 32, r + 64 and r + 96 of the row side at
+            // 16 r, those of the column side's rows behind them in two such blocks.
+            // Rows past the end count as scale 1; they meet only zeros, in parts of the
+            // tile that are not stored.  The two warps bring groups in turn (one alone
+            // is busy 400 of the 450 clocks that a wide tile's k-block lasts), each with
+            // its next group's words in flight while it hands over the last ones.  Both
+            // wait for every release and arrive on every stage's full barrier: so the
+            // MMA issuer waits for scales and operands at once, and neither warp can
+            // run two phases of a barrier ahead or behind, which its parity would not
+            // tell.
+            const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
+            const uint32_t which = (uint32_t)warp & 1u;
+            Fp8Work wl = wi;  // the loads' place in the work
+            Fp8Item il = {0, 0, 0};
+            int32_t left = 0;       // groups of the loads' item still to come
+            uint32_t gl = 0;        // groups the loads have passed
+            uint32_t live = 0u;     // which of the twelve words exist
+            const uint32_t *sr = nullptr, *sc = nullptr;
+            uint32_t v[2][12];
+            auto load = [&](uint32_t(&x)[12]) {
+                for (;;) {
+                    if (left == 0) {
+                        if (!wl.next(il))
+                            return;
+                        const TileCoord tc = fp8_tile_coord(il.tile, p);
+                        const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + lane;
+                        const int32_t yc = tc.nb * width + lane;
+                        const int32_t kt = il.kb0 >> 2;
+                        left = ((il.kb1 - 1) >> 2) + 1 - kt;
+                        sr = p.s_rows + (int64_t)kt * p.rows + yr;
+                        sc = p.s_cols + (int64_t)kt * p.cols + yc;
+                        live = 0u;
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+                            if (j < 4 ? yr + 32 * j < p.rows : 32 * (j - 4) < width && yc + 32 * (j - 4) < p.cols)
+                                live |= 1u << j;
+                    }
+                    const bool mine = (gl & 1u) == which;
+                    if (mine) {
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+                            x[j] = live & (1u << j) ? (j < 4 ? sr[32 * j] : sc[32 * (j - 4)]) : 0x7F7F7F7Fu;
+                    }
+                    sr += p.rows;
+                    sc += p.cols;
+                    --left;
+                    ++gl;
+                    if (mine)
+                        return;
+                }
+            };
+            grid_dependency_wait();
+            load(v[0]);
+            load(v[1]);
+            int s = 0;
+            uint32_t ph = 0;
+            uint32_t g = 0;
+            bool ok = true;
+            while (ok && wi.next(w)) {
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (ring_group_first(s, 1u)) {
+                        const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                            !warp_wait<false>(ctl, bar, parity, kRoleScales, (uint32_t)s, lane)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    const bool first = kb == w.kb0 || (kb & 3) == 0;
+                    const bool last = kb == w.kb1 - 1 || (kb & 3) == 3;
+                    const bool mine = (g & 1u) == which;
+                    if (mine && first) {
+                        const uint32_t at = scales0 + (uint32_t)s * kFp8ScaleBytes + 16u * (uint32_t)lane;
+                        st_shared_v4(at, v[0][0], v[0][1], v[0][2], v[0][3]);
+                        st_shared_v4(at + 512u, v[0][4], v[0][5], v[0][6], v[0][7]);
+                        if (width > 128)
+                            st_shared_v4(at + 1024u, v[0][8], v[0][9], v[0][10], v[0][11]);
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                    }
+                    // Each CTA's words stay in its own shared memory, where its own half
+                    // of the paired copy reads them: the proxy fence has put them there
+                    // before the arrive leaves.  So the arrive on the leader's barrier
+                    // releases at CTA scope; at cluster scope it waits for all of this
+                    // thread's memory traffic, loads too (measured 600 ns).
+                    if (lane == 0) {
+                        if constexpr (kCluster)
+                            mbar_arrive_cluster_handoff(full_target + 8u * s);
+                        else
+                            mbar_arrive(full_target + 8u * s);
+                    }
+                    if (mine && last) {
+#pragma unroll
+                        for (int j = 0; j < 12; ++j)
+                            v[0][j] = v[1][j];
+                        load(v[1]);
+                    }
+                    g += last ? 1u : 0u;
+                    ring_advance(s, ph, S);
+                }
             }
         }
-    } else if (warp >= 4) {
+    } else {
         // ---------------- epilogue ----------------
         grid_dependency_wait();
         const int ew = warp - 4;
@@ -528,25 +577,42 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int nchunks = (width + 31) / 32;
         const uint32_t staging = staging0 + (uint32_t)ew * kFp8StagingBytes;
         const uint32_t acce_target = kCluster ? mapa_shared(acce_bar, 0u) : acce_bar;
-        const bool fp32 = p.out_fp32 != 0;
+        const bool fp32 = kLong || p.out_fp32 != 0;
         const int32_t cta = cluster_id * CG + (int32_t)rank;
         int acc = 0;
         uint32_t acc_ph = 0;
         uint32_t item_parity = 0;
         uint32_t buf = 0;
+        bool ok = true;
         const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
-        while (wi.next(w)) {
-            // one thread waits for the accumulator and posts the outcome, so that
-            // all warps take the same branch; the word alternates with the item
+        // one thread waits for the accumulator and posts the outcome, so that all
+        // warps take the same branch; the word alternates with the accumulations
+        auto accumulated = [&]() {
             const uint32_t go = go_words + 4u * item_parity;
             item_parity ^= 1u;
             if (threadIdx.x == 128)
                 st_volatile_shared_u32(
                     go, ctl.wait<kCluster>(accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc) ? 1u : 0u);
             named_barrier_sync(1u, kFp8EpiWarps * 32u);
-            if (ld_volatile_shared_u32(go) == 0u)
-                break;
-            tc_fence_after_sync();
+            return ld_volatile_shared_u32(go) != 0u;
+        };
+        // this warp has read its part of the accumulator: hand it back
+        auto hand_back = [&]() {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kCluster)
+                    mbar_arrive_cluster_handoff(acce_target + 8u * acc);
+                else
+                    mbar_arrive(acce_bar + 8u * acc);
+            }
+        };
+        auto load_chunk = [&](int c, uint32_t(&v)[32]) {
+            tmem_load_32x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kFp8MaxWidth + c * 32), v);
+            tmem_load_wait();
+            reg_fence(v);
+        };
+        while (wi.next(w)) {
             const TileCoord tc = fp8_tile_coord(w.tile, p);
             const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta + q * 32;
             const int32_t yc = tc.nb * width;
@@ -556,35 +622,24 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             // may be empty (fewer units than clusters), and then leaves nothing
             int32_t last = cluster_id;
             bool parts = owner;
-            if (owner && shared_tile) {
-                uint32_t got = 1u;
-                if (lane == 0)
-                    got = ctl.wait<true>(ready_bar + 8u * (uint32_t)ew, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
-                __syncwarp();  // lane 0's acquire comes before the lanes' loads
-                parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
-            } else if (owner) {
-                last = fp8_range_of(p.sk_units, num_clusters, (int64_t)(w.tile + 1) * KB - 1);
-                for (int32_t j2 = cluster_id + 1; parts && j2 <= last; ++j2)
-                    if (dense || fp8_range_holds(p.sk_units, num_clusters, j2))
-                        // a give-up stores the tile unsummed, and the status says so
-                        parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u, lane);
-            }
-            for (int c = half; c < nchunks; c += 2) {
-                uint32_t v[32];
-                tmem_load_32x32(tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc * kFp8MaxWidth + c * 32), v);
-                tmem_load_wait();
-                reg_fence(v);
-                if (c + 2 >= nchunks) {
-                    // this warp has read its part of the accumulator: hand it back
-                    tc_fence_before_sync();
-                    __syncwarp();
-                    if (lane == 0) {
-                        if constexpr (kCluster)
-                            mbar_arrive_cluster_handoff(acce_target + 8u * acc);
-                        else
-                            mbar_arrive(acce_bar + 8u * acc);
-                    }
+            auto collect = [&]() {
+                if (owner && shared_tile) {
+                    uint32_t got = 1u;
+                    if (lane == 0)
+                        got = ctl.wait<true>(ready_bar + 8u * (uint32_t)ew, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
+                    __syncwarp();  // lane 0's acquire comes before the lanes' loads
+                    parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
+                } else if (owner) {
+                    last = fp8_range_of(p.sk_units, num_clusters, (int64_t)(w.tile + 1) * KB - 1);
+                    for (int32_t j2 = cluster_id + 1; parts && j2 <= last; ++j2)
+                        if (dense || fp8_range_holds(p.sk_units, num_clusters, j2))
+                            // a give-up stores the tile unsummed, and the status says so
+                            parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u,
+                                                   lane);
                 }
+            };
+            // one chunk's sums: left for the tile's owner, or completed and stored
+            auto finish = [&](int c, uint32_t(&v)[32]) {
                 // The cluster form keeps a partial in the CTA's own ring: a
                 // contributor's only item has consumed all of its loads by now.
                 const uint32_t local = stage0 + (uint32_t)(((ew * 4 + (c >> 1)) * 8) * 32 + lane) * 16u;
@@ -592,45 +647,40 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         st_shared_v4(local + 512u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-                    continue;
+                    return;
                 }
                 if (contributor) {
-                    float4 *const mine = fp8_partial(p.partials, cta, ew, c >> 1, lane);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __stcg(mine + j * 32, make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
-                                                          __uint_as_float(v[4 * j + 2]), __uint_as_float(v[4 * j + 3])));
-                    continue;
+                    fp8_store_partial(v, fp8_partial(p.partials, cta, ew, c >> 1, lane));
+                    return;
                 }
                 if (parts && shared_tile) {
                     for (int32_t rk = 1; rk < p.cluster; ++rk) {
                         const uint32_t remote = mapa_shared(local, (uint32_t)rk);
-                        uint32_t x[32];  // all loads before the adds: their round trips overlap
+                        // several loads before their adds: the round trips overlap
+                        constexpr int kBatch = kLong ? 4 : 8;
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            ld_shared_cluster_v4(remote + 512u * j, x[4 * j], x[4 * j + 1], x[4 * j + 2], x[4 * j + 3]);
+                        for (int j0 = 0; j0 < 8; j0 += kBatch) {
+                            uint32_t x[4 * kBatch];
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(x[j]));
+                            for (int j = 0; j < kBatch; ++j)
+                                ld_shared_cluster_v4(remote + 512u * (j0 + j), x[4 * j], x[4 * j + 1], x[4 * j + 2],
+                                                     x[4 * j + 3]);
+#pragma unroll
+                            for (int j = 0; j < 4 * kBatch; ++j)
+                                v[4 * j0 + j] = __float_as_uint(__uint_as_float(v[4 * j0 + j]) + __uint_as_float(x[j]));
+                        }
                     }
                 } else if (parts) {
                     for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
                         if (!dense && !fp8_range_holds(p.sk_units, num_clusters, j2))
                             continue;
-                        const float4 *const part = fp8_partial(p.partials, j2 * CG + (int32_t)rank, ew, c >> 1, lane);
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float4 f = __ldcg(part + j * 32);
-                            v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f.x);
-                            v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f.y);
-                            v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f.z);
-                            v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f.w);
-                        }
+                        fp8_add_partial<kLong ? 4 : 8>(
+                            v, fp8_partial(p.partials, j2 * CG + (int32_t)rank, ew, c >> 1, lane));
                     }
                 }
                 const int32_t cols = yc + c * 32;
                 if (yr >= p.rows || cols >= p.cols)
-                    continue;
+                    return;
                 // the staging buffer is free once its last store has read it (or
                 // every lane has finished the masked path's loads)
                 if (lane == 0) {
@@ -644,17 +694,62 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 buf ^= 1u;
                 fp8_stage_chunk<kTransposed>(v, st, (uint32_t)lane, p.cols - cols, fp32);
                 if constexpr (kTransposed)
-                    fp8_store_chunk(st, lane, &tmD, yr, cols, p);
+                    fp8_store_chunk(st, lane, &tmD, yr, cols, fp32, p);
                 else
-                    fp8_store_chunk(st, lane, &tmD, cols, yr, p);
-            }
-            if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
-                if (lane == 0) {
-                    if constexpr (kCluster)
-                        mbar_arrive_cluster_handoff(acce_target + 8u * acc);
-                    else
-                        mbar_arrive(acce_bar + 8u * acc);
+                    fp8_store_chunk(st, lane, &tmD, cols, yr, fp32, p);
+            };
+
+            if constexpr (kLong) {
+                // The tensor core's additions lose up to a unit of the accumulator
+                // each, toward zero: 3e-6 of a sum over K = 32768.  bf16 hides that;
+                // for an fp32 D the accumulator takes a segment of k-blocks (2e-7
+                // with kFp8Segment of them) and the sums are added up here, in
+                // registers: so a tile is at most kFp8MaxLongWidth columns wide.
+                constexpr int kOwn = kFp8MaxLongWidth / 64;  // chunks of a warp
+                uint32_t run[kOwn][32];
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        run[i][j] = 0u;
+                for (int32_t cut = w.kb0; ok && cut < w.kb1;) {
+                    cut = fp8_segment_end(cut);
+                    if (!(ok = accumulated()))
+                        break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+                        if (half + 2 * i < nchunks)
+                            tmem_add_32x32(tmem_base + ((uint32_t)(q * 32) << 16) +
+                                               (uint32_t)(acc * kFp8MaxWidth + (half + 2 * i) * 32),
+                                           run[i]);
+                    hand_back();
+                    acc ^= 1;
+                    acc_ph ^= acc == 0 ? 1u : 0u;
                 }
+                if (!ok)
+                    break;
+                collect();
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i)
+                    if (half + 2 * i < nchunks)
+                        finish(half + 2 * i, run[i]);
+            } else {
+                if (!accumulated())
+                    break;
+                tc_fence_after_sync();
+                collect();
+                for (int c = half; c < nchunks; c += 2) {
+                    uint32_t v[32];
+                    load_chunk(c, v);
+                    if (c + 2 >= nchunks)
+                        hand_back();
+                    finish(c, v);
+                }
+                if (half >= nchunks)  // a tile of one chunk: the second group reads nothing
+                    hand_back();
+                acc ^= 1;
+                acc_ph ^= acc == 0 ? 1u : 0u;
             }
             if (contributor) {
                 __syncwarp();  // the warp's stores come before lane 0's release
@@ -669,9 +764,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 for (int32_t j2 = cluster_id + 1 + lane; j2 <= last; j2 += 32)
                     p.flags[(j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew] = 0u;
             }
-            acc ^= 1;
-            if (acc == 0)
-                acc_ph ^= 1u;
         }
         // the staging buffers have been read before the CTA exits
         if (lane == 0)

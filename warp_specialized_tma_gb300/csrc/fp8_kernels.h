@@ -84,6 +84,8 @@ constexpr int kFp8EpiWarps = 8;
 constexpr int kFp8ScaleBytes = 512 + 1024;  // a stage's scales: 128 words of the row side, 256 of the column side
 constexpr int kFp8StagingBytes = 4096;      // per epilogue warp: 32 rows of 32 fp32 (or two of 32 bf16)
 constexpr int kFp8MaxStages = 12;
+constexpr int kFp8MaxLongWidth = 192;  // the same where an fp32 D's sums are held in registers (three chunks a warp)
+constexpr int kFp8Segment = 32;             // k-blocks an accumulator takes before its sums are moved on (fp32 D)
 constexpr int kFp8PartialFloats = kFp8RowsPerCta * 256;  // one CTA's fp32 partial of a split tile
 
 struct Fp8GemmParams {
@@ -123,6 +125,7 @@ inline size_t fp8_smem_bytes(int cta_group, int width, int stages)
 }
 
 // (CUtensorMap rows, CUtensorMap cols, CUtensorMap D, Fp8GemmParams)
-const void *fp8_gemm_kernel_fn(int cta_group, bool transposed);
+// `long_sums`: fp32 D, accumulated in segments of kFp8Segment k-blocks.
+const void *fp8_gemm_kernel_fn(int cta_group, bool transposed, bool long_sums);
 
 }  // namespace wstma
