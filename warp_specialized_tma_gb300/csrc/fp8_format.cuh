@@ -79,6 +79,28 @@ __device__ __forceinline__ uint4 load8_bf16(const uint16_t *row, int32_t c, int3
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// Elements c .. c+7 of a bf16 row of C elements, from the 32 bytes that start at
+// the 16-byte group its first byte lies in, `mis` bytes (even) before it; elements
+// past the end are zero.
+__device__ __forceinline__ uint4 shift8(uint32_t (&w)[8], uint32_t mis, int32_t c, int32_t C)
+{
+    // shift right by mis bytes: two words, one word, half a word
+#pragma unroll
+    for (int k = 0; k < 6; ++k)
+        w[k] = mis & 8u ? w[k + 2] : w[k];
+#pragma unroll
+    for (int k = 0; k < 5; ++k)
+        w[k] = mis & 4u ? w[k + 1] : w[k];
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        o[k] = __funnelshift_r(w[k], w[k + 1], (mis & 2u) * 8u);
+        if (c + 2 * k + 1 >= C)
+            o[k] = c + 2 * k < C ? o[k] & 0xFFFFu : 0u;
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // The same from a row that is only 2-byte aligned: the 16 lanes of a half-warp
 // (all of them call this) hold the vectors of 128 consecutive columns, lane l
 // columns c = c0 + 8 l.  Each loads the aligned 16 bytes its vector starts in and
@@ -104,22 +126,7 @@ __device__ __forceinline__ uint4 load8_bf16_shifted(const uint16_t *row, int32_t
         const uint32_t n = __shfl_down_sync(0xFFFFFFFFu, w[k], 1, 16);
         w[4 + k] = l == 15 ? extra[k] : n;
     }
-    // shift right by mis bytes: two words, one word, half a word
-#pragma unroll
-    for (int k = 0; k < 6; ++k)
-        w[k] = mis & 8u ? w[k + 2] : w[k];
-#pragma unroll
-    for (int k = 0; k < 5; ++k)
-        w[k] = mis & 4u ? w[k + 1] : w[k];
-    uint32_t o[4];
-#pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        o[k] = __funnelshift_r(w[k], w[k + 1], (mis & 2u) * 8u);
-        // columns past the end
-        if (c + 2 * k + 1 >= C)
-            o[k] = c + 2 * k < C ? o[k] & 0xFFFFu : 0u;
-    }
-    return make_uint4(o[0], o[1], o[2], o[3]);
+    return shift8(w, mis, c, C);
 }
 
 __device__ __forceinline__ void load8_float(const float *row, int32_t c, int32_t C, bool vec, float (&f)[8])

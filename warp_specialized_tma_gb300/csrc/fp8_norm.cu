@@ -162,171 +162,134 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
     }
 }
 
-// A row's share of one thread.
-template <int V, bool kDres, bool kVec>
-struct BackwardRow {
-    uint4 dy[V], h[V], dres[kDres ? V : 1];
-    float rstd;
-
-    __device__ __forceinline__ void load(const NormBackwardParams &p, int64_t row, int t, int T)
-    {
+// d <- the gradient of 8 elements: d holds dy, x h, r dresidual.
+template <bool kDres>
+__device__ __forceinline__ void backward_values(float (&d)[8], const float (&x)[8], const float (&w)[8],
+                                                const float (&r)[8], float rstd, float mean)
+{
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int32_t c = (t + i * T) * 8;
-            dy[i] = load8_row(p.dy + row * p.lddy, c, p.C, kVec);
-            h[i] = load8_row(p.h + row * p.ldh, c, p.C, kVec);
-            if constexpr (kDres)
-                dres[i] = load8_row(p.dres + row * p.lddr, c, p.C, kVec);
-        }
-        rstd = p.rstd[row];
+    for (int j = 0; j < 8; ++j) {
+        d[j] = rstd * (d[j] * w[j] - x[j] * rstd * mean);
+        if constexpr (kDres)
+            d[j] += r[j];
     }
-};
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&d)[8])
+{
+    return make_uint4(bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]), bf16_pair(d[6], d[7]));
+}
 
 constexpr int kBackwardThreads = 512;
-constexpr int kRingMax = 32;               // slots of the ring of rows
+constexpr int kRingMax = 64;               // slots of a CTA's rings of rows
 constexpr int kRingBytes = 208 * 1024;     // of an SM's shared memory, shared by its CTAs
 
-// A CTA (or each of its warps) takes rows in a stride of the grid and keeps its
-// threads' share of dweight in registers; the CTAs' sums meet in `partials`,
-// one row of C floats each, which column_sum_kernel adds in a fixed order.  Bound
-// by HBM (4 to 8 bytes an element) if loads are always in flight: the next
-// row's are issued before the current row's reduction (V <= 2, where the registers
-// suffice).
-//
-// kThreads bounds the CTA: with V = 1, or up to 320 threads, two CTAs share an SM,
-// so that one's reduction overlaps the other's loads and stores.
-template <int V, bool kWarpRow, bool kDres, bool kVec, int kThreads>
-__global__ void __launch_bounds__(kThreads, kWarpRow ? 6 : (V == 1 || kThreads <= 320 ? 2 : 1))
-    rmsnorm_backward_kernel(const NormBackwardParams p)
+// Rows of more than 16 vectors a thread of the ring kernel below (C > 8192): a CTA
+// takes rows in a stride of the grid and keeps its threads' share of dweight in
+// registers.
+template <int V, bool kDres, bool kVec>
+__global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_kernel(const NormBackwardParams p)
 {
-    constexpr bool kAhead = V <= 2;
-    extern __shared__ float dw_smem[];  // warp rows: C floats
     __shared__ float red[32];
     grid_dependency_wait();
     grid_launch_dependents();
-    const int warps = (int)blockDim.x >> 5;
-    const int T = kWarpRow ? 32 : (int)blockDim.x;
-    const int t = kWarpRow ? (int)(threadIdx.x & 31u) : (int)threadIdx.x;
-    const int64_t row0 = kWarpRow ? (int64_t)blockIdx.x * warps + (threadIdx.x >> 5) : blockIdx.x;
-    const int64_t step = kWarpRow ? (int64_t)gridDim.x * warps : gridDim.x;
+    const int T = (int)blockDim.x, t = (int)threadIdx.x;
     const int32_t C = p.C;
     const float inv = 1.f / (float)C;
-    float dw[V][8], w[kAhead ? V : 1][8];
+    float dw[V][8];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.f;
-
-    BackwardRow<V, kDres, kVec> cur, next;
-    if (row0 < p.R)
-        cur.load(p, row0, t, T);
-    if constexpr (kAhead) {
+    for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x) {
+        uint4 dy[V], h[V];
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[i]);
-    }
-    for (int64_t row = row0; row < p.R; row += step) {
-        if constexpr (kAhead) {
-            if (row + step < p.R)
-                next.load(p, row + step, t, T);
+        for (int i = 0; i < V; ++i) {
+            dy[i] = load8_row(p.dy + row * p.lddy, (t + i * T) * 8, C, kVec);
+            h[i] = load8_row(p.h + row * p.ldh, (t + i * T) * 8, C, kVec);
         }
-        const float rstd = cur.rstd;
+        const float rstd = p.rstd[row];
         float dot = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float d[8], h[8];
-            unpack8(cur.dy[i], d);
-            unpack8(cur.h[i], h);
-            if constexpr (!kAhead)
-                load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[0]);
+            float d[8], x[8], w[8];
+            unpack8(dy[i], d);
+            unpack8(h[i], x);
+            load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w);
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                const float n = h[j] * rstd;
-                dot = fmaf(d[j] * w[kAhead ? i : 0][j], n, dot);
+                const float n = x[j] * rstd;
+                dot = fmaf(d[j] * w[j], n, dot);
                 dw[i][j] = fmaf(d[j], n, dw[i][j]);
             }
         }
-        const float mean = row_sum<kWarpRow>(dot, red) * inv;
+        const float mean = row_sum<false>(dot, red) * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            float d[8], h[8], r[8];
-            unpack8(cur.dy[i], d);
-            unpack8(cur.h[i], h);
-            if constexpr (!kAhead)
-                load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w[0]);
+            float d[8], x[8], w[8], r[8];
+            unpack8(dy[i], d);
+            unpack8(h[i], x);
+            load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w);
             if constexpr (kDres)
-                unpack8(cur.dres[i], r);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] = rstd * (d[j] * w[kAhead ? i : 0][j] - h[j] * rstd * mean);
-                if constexpr (kDres)
-                    d[j] += r[j];
-            }
-            store8_row(p.dx + row * p.lddx, c, C, kVec,
-                       make_uint4(bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]),
-                                  bf16_pair(d[6], d[7])));
+                unpack8(load8_row(p.dres + row * p.lddr, c, C, kVec), r);
+            backward_values<kDres>(d, x, w, r, rstd, mean);
+            store8_row(p.dx + row * p.lddx, c, C, kVec, pack8(d));
         }
-        if constexpr (kAhead)
-            cur = next;
-        else if (row + step < p.R)
-            cur.load(p, row + step, t, T);
     }
-
     float *const out = p.partials + (int64_t)blockIdx.x * C;
-    if constexpr (kWarpRow) {
-        // the warps add their sums one after another
-        for (int k = 0; k < warps; ++k) {
-            if ((int)(threadIdx.x >> 5) == k) {
 #pragma unroll
-                for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i)
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const int32_t c = (t + i * T) * 8 + j;
-                        if (c < C) {
-                            const float v = k == 0 ? dw[i][j] : dw_smem[c] + dw[i][j];
-                            if (k == warps - 1)
-                                out[c] = v;
-                            else
-                                dw_smem[c] = v;
-                        }
-                    }
-            }
-            __syncthreads();
-        }
-    } else {
-#pragma unroll
-        for (int i = 0; i < V; ++i)
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if ((t + i * T) * 8 + j < C)
-                    out[(t + i * T) * 8 + j] = dw[i][j];
-    }
+        for (int j = 0; j < 8; ++j)
+            if ((t + i * T) * 8 + j < C)
+                out[(t + i * T) * 8 + j] = dw[i][j];
 }
 
-// The same for rows that start and end at multiples of 16 bytes: rows come through
-// a ring of bulk copies in shared memory, slots of dy, h (and dresidual), so the
-// bytes in flight are the ring's (up to 200 KB an SM) and not what the registers
-// hold: that left HBM idle half of the time (6143 x 4104: 42 us with one row ahead
-// in registers).  Thread 0 refills a slot after the barrier in the next row's
-// reduction, which every thread reaches when it is done with the slot.
-template <int V, bool kDres, int kThreads>
+// Vector c .. c+7 of a row whose bytes lie in shared memory at `at`, `mis` bytes into
+// their first 16-byte group (shifts as in load8_bf16_shifted).
+template <bool kVec>
+__device__ __forceinline__ uint4 ring_vector(uint32_t at, uint32_t mis, int32_t c, int32_t C)
+{
+    uint32_t w[8];
+    ld_shared_v4(at + (uint32_t)c * 2u, w[0], w[1], w[2], w[3]);
+    if constexpr (kVec)
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    ld_shared_v4(at + (uint32_t)c * 2u + 16u, w[4], w[5], w[6], w[7]);
+    return shift8(w, mis, c, C);
+}
+
+// A group of T threads (a multiple of 32) takes rows in a stride of all groups,
+// `blockDim.x / T` groups to a CTA, and keeps its threads' share of dweight in
+// registers.  Rows come through a ring of bulk copies in shared memory, slots of
+// dy, h (and dresidual), so the bytes in flight are the ring's (up to 200 KB an SM)
+// and not what the registers hold: that left HBM idle half of the time (6143 x
+// 4104: 42 us with one row ahead in registers).  A group's first thread refills a
+// slot after the barrier in the next row's reduction, which every thread reaches
+// when it is done with the slot.  Rows that are not 16-byte aligned are copied
+// with the rest of their first and last 16-byte groups.  The CTAs' sums meet in
+// `partials`, one row of C floats each, which column_sum_kernel adds in a fixed
+// order.
+template <int V, bool kDres, bool kVec, bool kGroups, int kThreads>
 __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
-    rmsnorm_backward_ring_kernel(const NormBackwardParams p, const int32_t slots)
+    rmsnorm_backward_ring_kernel(const NormBackwardParams p, const int32_t group_threads, const int32_t slots,
+                                 const uint32_t pitch)
 {
     extern __shared__ __align__(128) uint8_t ring[];
     __shared__ float red[2][32];
     __shared__ __align__(8) uint64_t full[kRingMax];
     constexpr int kRows = kDres ? 3 : 2;
-    const int T = (int)blockDim.x, t = (int)threadIdx.x;
-    const int warp = t >> 5, lane = t & 31, warps = T >> 5;
+    const int T = kGroups ? group_threads : (int)blockDim.x;
+    const int groups = kGroups ? (int)blockDim.x / T : 1, g = kGroups ? (int)threadIdx.x / T : 0;
+    const int t = (int)threadIdx.x - g * T, lane = t & 31, warps = T >> 5;
     const int32_t C = p.C;
-    const uint32_t row_bytes = (uint32_t)C * 2u;
-    const uint32_t slot_bytes = row_bytes * kRows;
-    const uint32_t base = smem_u32(ring), bars = smem_u32(full);
+    const uint32_t slot_bytes = pitch * kRows;
+    const uint32_t base = smem_u32(ring) + (uint32_t)(g * slots) * slot_bytes;
+    const uint32_t bars = smem_u32(full) + 8u * (uint32_t)(g * slots);
     const float inv = 1.f / (float)C;
-    const int64_t step = gridDim.x;
+    const int64_t step = (int64_t)gridDim.x * groups;
+    const int64_t row0 = (int64_t)blockIdx.x * groups + g;
     if (t == 0) {
         for (int s = 0; s < slots; ++s)
             mbar_init(bars + 8u * s, 1);
@@ -336,17 +299,36 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     grid_dependency_wait();
     grid_launch_dependents();
 
-    auto fill = [&](int s, int64_t row) {
-        const uint32_t at = base + (uint32_t)s * slot_bytes, bar = bars + 8u * s;
-        mbar_arrive_expect_tx(bar, slot_bytes);
-        bulk_load(at, p.dy + row * p.lddy, row_bytes, bar);
-        bulk_load(at + row_bytes, p.h + row * p.ldh, row_bytes, bar);
-        if constexpr (kDres)
-            bulk_load(at + 2u * row_bytes, p.dres + row * p.lddr, row_bytes, bar);
+    const uint16_t *const src[3] = {p.dy, p.h, p.dres};
+    const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
+    // the first thread's place in the rows to come: it steps from one to the next
+    uintptr_t from[kRows];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k)
+        from[k] = reinterpret_cast<uintptr_t>(src[k] + row0 * ld[k]);
+    auto fill = [&](int s) {
+        const uint32_t bar = bars + 8u * s;
+        uint32_t bytes[kRows], all = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const uint32_t end = ((uint32_t)(from[k] & 15u) + 2u * (uint32_t)C + 15u) & ~15u;
+            bytes[k] = kVec ? 2u * (uint32_t)C : end;
+            all += bytes[k];
+        }
+        mbar_arrive_expect_tx(bar, all);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            bulk_load(base + (uint32_t)s * slot_bytes + (uint32_t)k * pitch,
+                      reinterpret_cast<const void *>(from[k] & ~(uintptr_t)15), bytes[k], bar);
+            from[k] += (uintptr_t)(2 * step * ld[k]);
+        }
+    };
+    auto mis = [&](int k, int64_t row) {
+        return kVec ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(src[k] + row * ld[k]) & 15u);
     };
     if (t == 0)
-        for (int s = 0; s < slots && blockIdx.x + s * step < p.R; ++s)
-            fill(s, blockIdx.x + s * step);
+        for (int s = 0; s < slots && row0 + s * step < p.R; ++s)
+            fill(s);
 
     float dw[V][8], w[V][8];
 #pragma unroll
@@ -356,13 +338,13 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.f;
     }
-    float rstd = blockIdx.x < p.R ? p.rstd[blockIdx.x] : 0.f;
+    float rstd = row0 < p.R ? p.rstd[row0] : 0.f;
     int s = 0;
     uint32_t ph = 0, buf = 0;
     bool ok = true;
-    int64_t refill = -1;  // row to load into the slot before this one
+    bool refill = false;  // a row is left for the slot before this one
     int before = 0;
-    for (int64_t row = blockIdx.x; row < p.R; row += step) {
+    for (int64_t row = row0; row < p.R; row += step) {
         const float next_rstd = row + step < p.R ? p.rstd[row + step] : 0.f;
         ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
         const uint32_t at = base + (uint32_t)s * slot_bytes;
@@ -373,8 +355,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
             const int32_t c = (t + i * T) * 8;
             dy[i] = h[i] = make_uint4(0u, 0u, 0u, 0u);
             if (c < C) {
-                ld_shared_v4(at + (uint32_t)c * 2u, dy[i].x, dy[i].y, dy[i].z, dy[i].w);
-                ld_shared_v4(at + row_bytes + (uint32_t)c * 2u, h[i].x, h[i].y, h[i].z, h[i].w);
+                dy[i] = ring_vector<kVec>(at, mis(0, row), c, C);
+                h[i] = ring_vector<kVec>(at + pitch, mis(1, row), c, C);
             }
             float d[8], x[8];
             unpack8(dy[i], d);
@@ -388,55 +370,88 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         }
         // one barrier a row: the sums alternate between two buffers
         dot = warp_sum(dot);
-        if (lane == 0)
-            red[buf][warp] = dot;
-        __syncthreads();
-        if (t == 0 && refill >= 0)
-            fill(before, refill);
-        const float mean = warp_sum(lane < warps ? red[buf][lane] : 0.f) * inv;
-        buf ^= 1u;
+        if (!kGroups || warps > 1) {
+            float *const mine = red[buf] + g * warps;
+            if (lane == 0)
+                mine[t >> 5] = dot;
+            if constexpr (kGroups)
+                named_barrier_sync(1u + (uint32_t)g, (uint32_t)T);
+            else
+                __syncthreads();
+            if constexpr (kGroups) {
+                dot = 0.f;  // few warps: every lane adds their sums
+                for (int k = 0; k < warps; ++k)
+                    dot += mine[k];
+            } else {
+                dot = warp_sum(lane < warps ? mine[lane] : 0.f);
+            }
+            buf ^= 1u;
+        } else {
+            __syncwarp();
+        }
+        if (t == 0 && refill)
+            fill(before);
+        const float mean = dot * inv;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            if (c >= C)
-                continue;
             float d[8], x[8], r[8];
             unpack8(dy[i], d);
             unpack8(h[i], x);
-            if constexpr (kDres) {
-                uint4 q;
-                ld_shared_v4(at + 2u * row_bytes + (uint32_t)c * 2u, q.x, q.y, q.z, q.w);
-                unpack8(q, r);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                d[j] = rstd * (d[j] * w[i][j] - x[j] * rstd * mean);
-                if constexpr (kDres)
-                    d[j] += r[j];
-            }
-            *reinterpret_cast<uint4 *>(p.dx + row * p.lddx + c) = make_uint4(
-                bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]), bf16_pair(d[6], d[7]));
+            if constexpr (kDres)
+                unpack8(c < C ? ring_vector<kVec>(at + 2u * pitch, mis(2, row), c, C) : make_uint4(0u, 0u, 0u, 0u), r);
+            backward_values<kDres>(d, x, w[i], r, rstd, mean);
+            store8_row(p.dx + row * p.lddx, c, C, kVec, pack8(d));
         }
         rstd = next_rstd;
         before = s;
-        refill = row + slots * step < p.R ? row + slots * step : -1;
+        refill = row + slots * step < p.R;
         if (++s == slots) {
             s = 0;
             ph ^= 1u;
         }
     }
     // a wait that ran out (its copies never landed): dweight says so
-    const float poison = ok ? 0.f : __int_as_float(0x7FFFFFFF);
+    if (!ok)
+        dw[0][0] = __int_as_float(0x7FFFFFFF);
+
     float *const out = p.partials + (int64_t)blockIdx.x * C;
+    if constexpr (!kGroups && kVec) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int32_t c = (t + i * T) * 8;
-        if (c < C) {
-            *reinterpret_cast<float4 *>(out + c) =
-                make_float4(dw[i][0] + poison, dw[i][1] + poison, dw[i][2] + poison, dw[i][3] + poison);
-            *reinterpret_cast<float4 *>(out + c + 4) =
-                make_float4(dw[i][4] + poison, dw[i][5] + poison, dw[i][6] + poison, dw[i][7] + poison);
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            if (c < C) {
+                *reinterpret_cast<float4 *>(out + c) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
+                *reinterpret_cast<float4 *>(out + c + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+            }
         }
+        return;
+    }
+    // the groups' sums meet in the ring, whose copies have all been used
+    float *const sums = reinterpret_cast<float *>(ring);
+    __syncthreads();
+    if (g > 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if ((t + i * T) * 8 + j < C)
+                    sums[(g - 1) * C + (t + i * T) * 8 + j] = dw[i][j];
+    }
+    __syncthreads();
+    if (g == 0) {
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int32_t c = (t + i * T) * 8 + j;
+                if (c < C) {
+                    float v = dw[i][j];
+                    for (int k = 0; k + 1 < groups; ++k)
+                        v += sums[k * C + c];
+                    out[c] = v;
+                }
+            }
     }
 }
 
@@ -491,17 +506,17 @@ struct RowSplit {
     int V;
 };
 
-// V is 1, 2, 4 or 8: the least that keeps a CTA within `most` threads, then up
-// to max_v while the CTA has more than `wanted`.
-RowSplit split_row(int64_t C, int max_v, int most, int wanted)
+// V is 1, 2 or 4: the least that keeps a CTA within 1024 threads, then up to max_v
+// while the CTA has more than 256.
+RowSplit split_row(int64_t C, int max_v)
 {
     const int64_t nv = (C + 7) / 8;
     if (nv <= 32 * max_v && nv <= 128)
         return {true, 128, nv <= 32 ? 1 : (nv <= 64 ? 2 : 4)};
     int V = 1;
-    while ((nv + V - 1) / V > most)
+    while ((nv + V - 1) / V > 1024)
         V *= 2;
-    while (V < max_v && (nv + V - 1) / V > wanted)
+    while (V < max_v && (nv + V - 1) / V > 256)
         V *= 2;
     return {false, (int)(((nv + V - 1) / V + 31) / 32 * 32), V};
 }
@@ -516,21 +531,44 @@ auto norm_fn(const RowSplit &s)
                     : (s.V == 2 ? &rmsnorm_kernel<2, false, kRes, kVec> : &rmsnorm_kernel<4, false, kRes, kVec>);
 }
 
+// How the gradient kernels share out rows of C columns: groups of T threads with V
+// vectors each, `groups` to a CTA and `blocks` CTAs to an SM.
+struct BackwardSplit {
+    bool ring;
+    int V, T, groups, blocks;
+};
+
+BackwardSplit split_backward(int64_t R, int64_t C, int num_sms)
+{
+    const int64_t nv = (C + 7) / 8;
+    BackwardSplit s;
+    s.V = 1;
+    while ((nv + s.V - 1) / s.V > kBackwardThreads)
+        s.V *= 2;
+    s.T = (int)(((nv + s.V - 1) / s.V + 31) / 32 * 32);
+    s.ring = s.V <= 2;
+    s.groups = std::min(kBackwardThreads / s.T, s.T == 32 ? 16 : 15);  // barriers 1..15
+    // few rows: on as many SMs as there are rows for
+    s.groups = (int)std::min<int64_t>(s.groups, std::max<int64_t>(1, R / num_sms));
+    s.blocks = s.V == 1 || (s.V == 2 && s.T <= 320) ? 2 : 1;
+    return s;
+}
+
 template <bool kDres, bool kVec>
-auto norm_backward_fn(const RowSplit &s)
+auto backward_ring_fn(const BackwardSplit &s)
 {
     constexpr int kT = kBackwardThreads;
-    if (s.warp_row)
-        return s.V == 1 ? &rmsnorm_backward_kernel<1, true, kDres, kVec, 128>
-                        : &rmsnorm_backward_kernel<2, true, kDres, kVec, 128>;
-    switch (s.V) {
-    case 1: return &rmsnorm_backward_kernel<1, false, kDres, kVec, kT>;
-    case 2:
-        return s.threads <= 320 ? &rmsnorm_backward_kernel<2, false, kDres, kVec, 320>
-                                : &rmsnorm_backward_kernel<2, false, kDres, kVec, kT>;
-    case 4: return &rmsnorm_backward_kernel<4, false, kDres, kVec, kT>;
-    default: return &rmsnorm_backward_kernel<8, false, kDres, kVec, kT>;
-    }
+    if (s.groups > 1)
+        return &rmsnorm_backward_ring_kernel<1, kDres, kVec, true, kT>;
+    return s.V == 1 ? &rmsnorm_backward_ring_kernel<1, kDres, kVec, false, kT>
+                    : (s.T <= 320 ? &rmsnorm_backward_ring_kernel<2, kDres, kVec, false, 320>
+                                  : &rmsnorm_backward_ring_kernel<2, kDres, kVec, false, kT>);
+}
+
+template <bool kDres, bool kVec>
+auto backward_wide_fn(const BackwardSplit &s)
+{
+    return s.V == 4 ? &rmsnorm_backward_wide_kernel<4, kDres, kVec> : &rmsnorm_backward_wide_kernel<8, kDres, kVec>;
 }
 
 // Rows of 8 vectors a thread end at 512 * 8 * 8 columns, the limit of the API.
@@ -541,56 +579,42 @@ static_assert(kBackwardThreads * 8 * 8 >= 32768, "every width up to the limit ha
 int launch_rmsnorm(const NormParams &p, int num_sms, cudaStream_t stream)
 {
     // few rows: more threads a row, for latency; many: 4 vectors a thread
-    const RowSplit s = split_row(p.C, p.R <= 2 * num_sms ? 1 : 4, 1024, 256);
+    const RowSplit s = split_row(p.C, p.R <= 2 * num_sms ? 1 : 4);
     const int64_t grid = s.warp_row ? ((int64_t)p.R + 3) / 4 : p.R;
     auto fn = p.residual ? (p.vec ? norm_fn<true, true>(s) : norm_fn<true, false>(s))
                          : (p.vec ? norm_fn<false, true>(s) : norm_fn<false, false>(s));
     return launch(fn, grid, s.threads, 0, stream, p);
 }
 
-// CTAs of the gradient kernel on an SM: the bounds of the kernels' registers.
-int backward_blocks(const RowSplit &s)
-{
-    if (s.warp_row)
-        return 6;
-    return s.V == 1 ? std::min(kBackwardThreads / s.threads * 2, 8) : (s.V == 2 && s.threads <= 320 ? 2 : 1);
-}
-
 int rmsnorm_backward_ctas(int64_t R, int64_t C, int num_sms)
 {
-    const RowSplit s = split_row(C, 2, kBackwardThreads, kBackwardThreads);
-    const int64_t rows = s.warp_row ? (R + 3) / 4 : R;
-    const int64_t most = (int64_t)num_sms * backward_blocks(s);
-    return (int)(rows < most ? rows : most);
-}
-
-template <bool kDres>
-auto norm_backward_ring_fn(const RowSplit &s)
-{
-    constexpr int kT = kBackwardThreads;
-    return s.V == 1 ? &rmsnorm_backward_ring_kernel<1, kDres, kT>
-                    : (s.threads <= 320 ? &rmsnorm_backward_ring_kernel<2, kDres, 320>
-                                        : &rmsnorm_backward_ring_kernel<2, kDres, kT>);
+    const BackwardSplit s = split_backward(R, C, num_sms);
+    const int64_t ctas = (R + s.groups - 1) / s.groups;
+    return (int)std::min<int64_t>(ctas, (int64_t)num_sms * s.blocks);
 }
 
 int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream_t stream)
 {
-    const RowSplit s = split_row(p.C, 2, kBackwardThreads, kBackwardThreads);
+    const BackwardSplit s = split_backward(p.R, p.C, num_sms);
     const int grid = rmsnorm_backward_ctas(p.R, p.C, num_sms);
-    auto fn = p.dres ? (p.vec ? norm_backward_fn<true, true>(s) : norm_backward_fn<true, false>(s))
-                     : (p.vec ? norm_backward_fn<false, true>(s) : norm_backward_fn<false, false>(s));
-    const size_t smem = s.warp_row ? (size_t)p.C * sizeof(float) : 0;
-    // the ring where rows are whole 16-byte groups and two or more slots fit
-    const int64_t slot = (int64_t)p.C * 2 * (p.dres ? 3 : 2);
-    const int64_t slots = std::min<int64_t>(kRingBytes / backward_blocks(s) / slot, kRingMax);
+    // whole 16-byte groups: plain vectors; else with room for the first and last group's rest
+    const bool vec = p.vec && p.C % 8 == 0;
     cudaError_t rc;
-    if (p.vec && p.C % 8 == 0 && !s.warp_row && s.V <= 2 && slots >= 2) {
-        auto ring = p.dres ? norm_backward_ring_fn<true>(s) : norm_backward_ring_fn<false>(s);
-        rc = cudaFuncSetAttribute(ring, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+    if (s.ring) {
+        const int64_t pitch = vec ? (int64_t)p.C * 2 : ((int64_t)p.C * 2 + 15) / 16 * 16 + 16;
+        const int64_t slot = pitch * (p.dres ? 3 : 2);
+        const int slots = (int)std::min<int64_t>(kRingBytes / s.blocks / s.groups / slot, kRingMax / s.groups);
+        const int64_t sums = (int64_t)(s.groups - 1) * p.C * (int64_t)sizeof(float);
+        auto fn = p.dres ? (vec ? backward_ring_fn<true, true>(s) : backward_ring_fn<true, false>(s))
+                         : (vec ? backward_ring_fn<false, true>(s) : backward_ring_fn<false, false>(s));
+        rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
         if (rc == cudaSuccess)
-            rc = launch(ring, grid, s.threads, (size_t)(slots * slot), stream, p, (int32_t)slots);
+            rc = launch(fn, grid, s.T * s.groups, (size_t)std::max<int64_t>(slots * slot * s.groups, sums), stream, p,
+                        (int32_t)s.T, (int32_t)slots, (uint32_t)pitch);
     } else {
-        rc = launch(fn, grid, s.threads, smem, stream, p);
+        auto fn = p.dres ? (vec ? backward_wide_fn<true, true>(s) : backward_wide_fn<true, false>(s))
+                         : (vec ? backward_wide_fn<false, true>(s) : backward_wide_fn<false, false>(s));
+        rc = launch(fn, grid, s.T, 0, stream, p);
     }
     if (rc != cudaSuccess)
         return rc;
