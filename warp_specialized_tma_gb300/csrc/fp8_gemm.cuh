@@ -13,7 +13,7 @@
 // tokens the weights take the row side, and the accumulator holds D transposed.
 //
 // Roles (384 threads, one CTA per SM):
-//   warp 0, lane 0   TMA producer: per (item, k-block) wait "empty", load both tiles
+//   warp 0           TMA producer: per (item, k-block) wait "empty", load both tiles
 //   warp 1           MMA issuer (leader CTA only in pairs), one elected lane
 //   warps 2, 3       scales: 4 k-blocks' words per row from global to shared memory,
 //                    with the ring stage of the first of them; warp 2 also allocates
@@ -328,9 +328,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     Fp8Item w;
 
     if (warp < 4) {
-        if (warp == 0 && lane == 0) {
+        if (warp == 0) {
             // ---------------- TMA producer ----------------
             const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
+            const uint32_t leader = elect_one();
             int s = 0;
             uint32_t ph = 0;
             int32_t it = 0;
@@ -341,24 +342,21 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta;
                 const int32_t yc = tc.nb * width + (int32_t)rank * (width / CG);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (ring_group_first(s, 1u) &&
-                        !ctl.wait<kCluster>(empty_bar + 8u * ring_group(s, 1u), ring_empty_parity(ph), kRoleProducer,
-                                            (uint32_t)s)) {
-                        ok = false;
-                        break;
+                    if (ring_group_first(s, 1u)) {
+                        const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                            !warp_wait<false>(ctl, bar, parity, kRoleProducer, (uint32_t)s, lane)) {
+                            ok = false;
+                            break;
+                        }
                     }
                     if (it != p.fault_skip_it) {
-                        if (!kCluster || rank == 0)
-                            mbar_arrive_expect_tx(full_bar + 8u * s, stage_bytes * CG);
+                        if (rank == 0)
+                            expect_tx_elected(full_bar + 8u * s, stage_bytes * CG, leader);
                         const uint32_t fb = full_target + 8u * s;
                         const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
-                        if constexpr (kCluster) {
-                            tma_load_2d_pair(sa, &tmR, kb * kFp8BlockK, yr, fb);
-                            tma_load_2d_pair(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
-                        } else {
-                            tma_load_2d(sa, &tmR, kb * kFp8BlockK, yr, fb);
-                            tma_load_2d(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb);
-                        }
+                        tma_load_2d_elected<CG>(sa, &tmR, kb * kFp8BlockK, yr, fb, leader);
+                        tma_load_2d_elected<CG>(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb, leader);
                     }
                     ++it;
                     ring_advance(s, ph, S);
@@ -366,7 +364,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             }
             grid_launch_dependents();
             // Teardown: the last S loads may still be in flight if a role gave up.
-            if (!kCluster || rank == 0) {
+            if (lane == 0 && rank == 0) {
                 const int32_t n = it < S ? it : S;
                 for (int32_t d = 1; d <= n; ++d) {
                     const int32_t j = it - d;
@@ -375,13 +373,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
                                              (uint32_t)ring_stage_of(j, S));
                 }
-            } else if (ctl.aborted()) {
+            } else if (lane == 0 && ctl.aborted()) {
                 // the peer's loads complete on the leader's barriers, which this CTA
                 // cannot poll: a fixed grace period instead
                 const uint64_t t0 = globaltimer_ns();
                 while (globaltimer_ns() - t0 < 50000ull) {
                 }
             }
+            __syncwarp();
         } else if (warp == 1 && rank == 0) {
             // ---------------- MMA issuer ----------------
             const uint64_t rdesc0 = smem_desc_sw128(stage0);

@@ -74,6 +74,40 @@ __device__ __forceinline__ void mma_commit_elected(uint32_t bar, uint32_t leader
             : "memory");
 }
 
+// mbar_arrive_expect_tx and the 2-D TMA load of the elected lane; in paired mode the
+// bytes complete on a barrier of either CTA, given by its shared::cluster address.
+__device__ __forceinline__ void expect_tx_elected(uint32_t bar, uint32_t bytes, uint32_t leader)
+{
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %2, 0;\n\t"
+        "@q mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n\t}" ::"r"(bar),
+        "r"(bytes), "r"(leader)
+        : "memory");
+}
+
+template <int CG>
+__device__ __forceinline__ void tma_load_2d_elected(uint32_t dst, const CUtensorMap *map, int32_t x, int32_t y,
+                                                    uint32_t bar, uint32_t leader)
+{
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred q;\n\t"
+            "setp.ne.b32 q, %5, 0;\n\t"
+            "@q cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+            " [%0], [%1, {%2, %3}], [%4];\n\t}" ::"r"(dst),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "r"(leader)
+            : "memory");
+}
+
 // Waits, up to `tries` probes of `suspend_ns` each, for the phase with this
 // parity; 0 if it did not complete.  A loop inside one statement: the warp
 // stays converged around it.
