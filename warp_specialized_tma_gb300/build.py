@@ -61,8 +61,8 @@ def bind_flags() -> tuple:
             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", INCLUDE]
     for path in include:
         comp += ["-isystem", path]
-    link = ["-shared", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10",
-            "-lc10_cuda", "-L", PKG, "-lfp8_ops", "-Wl,-rpath,$ORIGIN"]
+    link = ["-shared", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
+            "-lc10", "-lc10_cuda", "-L", PKG, "-lfp8_ops", "-Wl,-rpath,$ORIGIN"]
     return comp, link
 
 

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -120,7 +121,7 @@ void need_vector(const Tensor &t, int64_t n, const char *what)
 // The current stream of the tensors' device; allocations and the call run there.
 struct Place {
     std::optional<c10::cuda::CUDAGuard> guard;
-    at::TensorOptions on;
+    std::optional<c10::Device> on;
     void *stream;
     int index;
 
@@ -132,7 +133,7 @@ struct Place {
         index = dev.index();
         if (c10::cuda::current_device() != index)
             guard.emplace(dev);
-        on = at::TensorOptions().device(dev);
+        on = dev;
         stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();
     }
 
@@ -143,11 +144,18 @@ struct Place {
                         ")");
     }
 
-    // uninitialised codes (rows at multiples of 128 bytes) and scales of a rows x cols matrix
+    // Uninitialised tensors straight from the allocator: the dispatcher takes longer
+    // than the allocation.
+    Tensor empty(at::IntArrayRef size, at::ScalarType type) const
+    {
+        return at::detail::empty_cuda(size, type, on, std::nullopt);
+    }
+
+    // codes (rows at multiples of 128 bytes) and scales of a rows x cols matrix
     std::pair<Tensor, Tensor> quantized(int64_t rows, int64_t cols) const
     {
-        return {at::empty_strided({rows, cols}, {padded(cols), 1}, on.dtype(at::kFloat8_e4m3fn)),
-                at::empty({(cols + 511) / 512, rows, 4}, on.dtype(at::kFloat8_e8m0fnu))};
+        return {at::detail::empty_strided_cuda({rows, cols}, {padded(cols), 1}, at::kFloat8_e4m3fn, on),
+                empty({(cols + 511) / 512, rows, 4}, at::kFloat8_e8m0fnu)};
     }
 };
 
@@ -234,7 +242,7 @@ PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
             const at::ScalarType st = reinterpret_cast<THPDtype *>(args[6])->scalar_type;
             if (st != at::kBFloat16 && st != at::kFloat)
                 type_error("out_dtype must be bf16 or fp32");
-            out = at::empty({M, N}, at.on.dtype(st));
+            out = at.empty({M, N}, st);
         }
         const int type = element_type(out, "out");
         if (!h) {
@@ -310,11 +318,11 @@ PyObject *bind_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n)
         int64_t ldh = 0;
         Tensor h;
         if (res) {
-            h = out_h ? *out_h : at::empty({R, C}, at.on.dtype(at::kBFloat16));
+            h = out_h ? *out_h : at.empty({R, C}, at::kBFloat16);
             ldh = need_bf16(h, R, C, "out_h");
         }
         auto [q, s] = at.quantized(R, C);
-        Tensor rstd = at::empty({R}, at.on.dtype(at::kFloat));
+        Tensor rstd = at.empty({R}, at::kFloat);
         check(fp8_rmsnorm(data(x), ldx, data(res), ldr, data(w), wtype, R, C, (float)eps, res ? data(h) : nullptr, ldh,
                           data(q), padded(C), data(s), static_cast<float *>(data(rstd)), at.stream),
               "fp8_rmsnorm");
@@ -351,9 +359,9 @@ PyObject *bind_rmsnorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
         at.same(&h), at.same(&w), at.same(&rstd), at.same(dres);
         int64_t need = 0;
         check(fp8_rmsnorm_backward_workspace(R, C, &need), "fp8_rmsnorm_backward_workspace");
-        Tensor dx = at::empty({R, C}, at.on.dtype(at::kBFloat16)), dw = at::empty({C}, at.on.dtype(at::kFloat));
+        Tensor dx = at.empty({R, C}, at::kBFloat16), dw = at.empty({C}, at::kFloat);
         // freed on return, to this stream's later allocations: they run after it
-        Tensor work = at::empty({need}, at.on.dtype(at::kByte));
+        Tensor work = at.empty({need}, at::kByte);
         check(fp8_rmsnorm_backward(data(dy), lddy, data(h), ldh, data(w), wtype, static_cast<const float *>(data(rstd)),
                                    data(dres), lddr, data(dx), C, static_cast<float *>(data(dw)), R, C, data(work),
                                    need, at.stream),

@@ -101,6 +101,19 @@ __device__ __forceinline__ uint4 shift8(uint32_t (&w)[8], uint32_t mis, int32_t 
     return make_uint4(o[0], o[1], o[2], o[3]);
 }
 
+// Eight whole elements at a 2-byte aligned address: the words they lie in, shifted.
+// Only words that hold one of them are read.
+__device__ __forceinline__ uint4 load8_bf16_words(const uint16_t *at)
+{
+    const uintptr_t a = reinterpret_cast<uintptr_t>(at);
+    const uint32_t *const w = reinterpret_cast<const uint32_t *>(a & ~(uintptr_t)3);
+    const bool half = (a & 2u) != 0u;
+    const uint32_t w0 = w[0], w1 = w[1], w2 = w[2], w3 = w[3], w4 = half ? w[4] : 0u;
+    const uint32_t by = half ? 16u : 0u;
+    return make_uint4(__funnelshift_r(w0, w1, by), __funnelshift_r(w1, w2, by), __funnelshift_r(w2, w3, by),
+                      __funnelshift_r(w3, w4, by));
+}
+
 // The same from a row that is only 2-byte aligned: the 16 lanes of a half-warp
 // (all of them call this) hold the vectors of 128 consecutive columns, lane l
 // columns c = c0 + 8 l.  Each loads the aligned 16 bytes its vector starts in and

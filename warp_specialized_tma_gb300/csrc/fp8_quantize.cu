@@ -298,6 +298,12 @@ __global__ void __launch_bounds__(kThreads, kMode == kFloats ? 2 : 3) quantize_k
                 const uint4 q = *reinterpret_cast<const uint4 *>(x + i * p.ldx + c0);
                 y.v[i][0] = q.x, y.v[i][1] = q.y, y.v[i][2] = q.z, y.v[i][3] = q.w;
             }
+        } else if (full) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint4 q = load8_bf16_words(x + i * p.ldx + c0);
+                y.v[i][0] = q.x, y.v[i][1] = q.y, y.v[i][2] = q.z, y.v[i][3] = q.w;
+            }
         } else {
 #pragma unroll
             for (int i = 0; i < 8; ++i) {

@@ -213,7 +213,7 @@ class Gemm:
         if stream is not None:
             with _on(stream, a.device):
                 return self.run(a, a_scales, b, b_scales, out, out_dtype)
-        return _ops().gemm(self.h.value, a, a_scales, b, b_scales, out, out_dtype)
+        return (_bind or _ops()).gemm(self.h.value, a, a_scales, b, b_scales, out, out_dtype)
 
     def device_status(self):
         """(status, detail word) of the device watchdog; synchronises the last stream."""
@@ -248,15 +248,15 @@ def gemm(a, a_scales, b, b_scales, out=None, out_dtype=torch.bfloat16, stream=No
     if stream is not None:
         with _on(stream, a.device):
             return gemm(a, a_scales, b, b_scales, out, out_dtype)
-    return _ops().gemm(0, a, a_scales, b, b_scales, out, out_dtype)
+    return (_bind or _ops()).gemm(0, a, a_scales, b, b_scales, out, out_dtype)
 
 
 # ------------------------------------------------------------------ quantiser
 def _quantize(x, tile, rows, columns, row_factor, column_factor, stream):
     if stream is not None:
         with _on(stream, x.device):
-            return _ops().quantize(x, tile, rows, columns, row_factor, column_factor)
-    return _ops().quantize(x, tile, rows, columns, row_factor, column_factor)
+            return (_bind or _ops()).quantize(x, tile, rows, columns, row_factor, column_factor)
+    return (_bind or _ops()).quantize(x, tile, rows, columns, row_factor, column_factor)
 
 
 def quantize(x, tile: bool = False, row_factor=None, column_factor=None, stream=None):
@@ -289,8 +289,8 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, out_h=None, stream=None
     """
     if stream is not None:
         with _on(stream, x.device):
-            return _ops().rmsnorm(x, weight, residual, eps, out_h)
-    return _ops().rmsnorm(x, weight, residual, eps, out_h)
+            return (_bind or _ops()).rmsnorm(x, weight, residual, eps, out_h)
+    return (_bind or _ops()).rmsnorm(x, weight, residual, eps, out_h)
 
 
 def rmsnorm_backward(dy, h, weight, rstd, dresidual=None, stream=None):
@@ -301,5 +301,5 @@ def rmsnorm_backward(dy, h, weight, rstd, dresidual=None, stream=None):
     """
     if stream is not None:
         with _on(stream, dy.device):
-            return _ops().rmsnorm_backward(dy, h, weight, rstd, dresidual)
-    return _ops().rmsnorm_backward(dy, h, weight, rstd, dresidual)
+            return (_bind or _ops()).rmsnorm_backward(dy, h, weight, rstd, dresidual)
+    return (_bind or _ops()).rmsnorm_backward(dy, h, weight, rstd, dresidual)
