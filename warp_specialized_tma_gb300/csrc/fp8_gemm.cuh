@@ -816,16 +816,19 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 if (!accumulated())
                     break;
                 tc_fence_after_sync();
-                collect();
+                if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
+                    hand_back();
+                    collect();
+                }
                 for (int c = half; c < nchunks; c += 2) {
                     uint32_t v[32];
                     load_chunk(c, v);
                     if (c + 2 >= nchunks)
                         hand_back();
+                    if (c == half)
+                        collect();  // after this piece's own sums have been read
                     finish(c, v);
                 }
-                if (half >= nchunks)  // a tile of one chunk: the second group reads nothing
-                    hand_back();
                 acc ^= 1;
                 acc_ph ^= acc == 0 ? 1u : 0u;
             }
