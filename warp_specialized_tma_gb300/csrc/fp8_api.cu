@@ -33,8 +33,7 @@ struct Plan {
     int cta_group = 1, width = 32, stages = 2, grid = 0, cluster = 1;
     bool transposed = false;
     int64_t tiles = 0, row_tiles = 0, col_tiles = 0, k_blocks = 0, sk_tiles = 0;
-    int staged_stages = 2;  // where D is staged after all: its base is not 32-byte aligned
-    bool direct = false;
+    size_t smem = 0;
     int regs = 0;
     const void *fn = nullptr;
     // tensor maps and the pointers they were made for
@@ -203,11 +202,11 @@ struct Tiling {
 // An fp32 D of a long sum is accumulated in segments.
 bool long_sums(const Plan &pl) { return pl.out_type == FP8_FP32 && pl.k_blocks > kFp8Segment; }
 
-int ring_stages(const fp8_gemm *h, int cta_group, int width, bool staged)
+int ring_stages(const fp8_gemm *h, int cta_group, int width)
 {
     int S = kFp8MaxStages;
-    while (S > 2 && fp8_smem_bytes(cta_group, width, S, staged) > h->max_smem)
-        --S;
+    while (S > 2 && fp8_smem_bytes(cta_group, width, S) > h->max_smem)
+        S -= 2;
     return S;
 }
 
@@ -225,7 +224,7 @@ int resident_clusters(const fp8_gemm *h, const Plan &pl, const Tiling &t, int c)
     int n = 0;
     cfg.gridDim = dim3((unsigned)c, 1, 1);
     cfg.blockDim = dim3(kFp8Threads, 1, 1);
-    cfg.dynamicSmemBytes = fp8_smem_bytes(1, t.width, ring_stages(h, 1, t.width, true), true);
+    cfg.dynamicSmemBytes = fp8_smem_bytes(1, t.width, ring_stages(h, 1, t.width));
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = (unsigned)c;
     attr[0].val.clusterDim.y = 1;
@@ -341,13 +340,8 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     pl.sk_tiles = best.sk_tiles;
     pl.cluster = best.cluster;
     pl.grid = (int)(best.clusters * best.cta_group);
-    // A tile whose rows are rows of D is stored from registers where those are
-    // 32-byte aligned (see run), which leaves the ring a stage more: at 8192^3 and
-    // 224 columns 7 stages instead of 6.
-    const int64_t esize = pl.out_type == FP8_FP32 ? 4 : 2;
-    pl.direct = !best.transposed && (pl.ldd * esize) % 32 == 0;
-    pl.stages = ring_stages(h, best.cta_group, best.width, !pl.direct);
-    pl.staged_stages = ring_stages(h, best.cta_group, best.width, true);
+    pl.stages = ring_stages(h, best.cta_group, best.width);
+    pl.smem = fp8_smem_bytes(best.cta_group, best.width, pl.stages);
     pl.fn = fp8_gemm_kernel_fn(best.cta_group, best.transposed, long_sums(pl));
     cudaFuncAttributes a;
     if (configure(h, pl.fn) != cudaSuccess || cudaFuncGetAttributes(&a, pl.fn) != cudaSuccess)
@@ -438,7 +432,7 @@ FP8_API int fp8_gemm_create(int device, fp8_gemm_t *out)
         int n = 0;
         cfg.gridDim = dim3(2, 1, 1);
         cfg.blockDim = dim3(kFp8Threads, 1, 1);
-        cfg.dynamicSmemBytes = fp8_smem_bytes(2, kFp8MaxWidth, 4, true);
+        cfg.dynamicSmemBytes = fp8_smem_bytes(2, kFp8MaxWidth, 4);
         attr[0].id = cudaLaunchAttributeClusterDimension;
         attr[0].val.clusterDim.x = 2;
         attr[0].val.clusterDim.y = 1;
@@ -563,7 +557,7 @@ FP8_API int fp8_gemm_plan_info(fp8_gemm_t h, fp8_gemm_plan_info_t *info)
     info->width = pl.width;
     info->stages = pl.stages;
     info->split_tiles = (int32_t)pl.sk_tiles;
-    info->smem_bytes = (int32_t)fp8_smem_bytes(pl.cta_group, pl.width, pl.stages, !pl.direct);
+    info->smem_bytes = (int32_t)pl.smem;
     info->regs_per_thread = pl.regs;
     info->cluster = pl.cluster;
     return FP8_OK;
@@ -624,9 +618,7 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     p.num_tiles = (int32_t)pl.tiles;
     p.raster_group = h->opt[FP8_GEMM_OPT_RASTER_GROUP] ? (int32_t)h->opt[FP8_GEMM_OPT_RASTER_GROUP] : 8;
     p.width = pl.width;
-    const bool direct = pl.direct && aligned(D, 32);
-    p.stages = direct ? pl.stages : pl.staged_stages;
-    p.d_direct = direct ? 1 : 0;
+    p.stages = pl.stages;
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;
@@ -650,7 +642,7 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
     cfg.blockDim = dim3(kFp8Threads, 1, 1);
-    cfg.dynamicSmemBytes = fp8_smem_bytes(pl.cta_group, pl.width, p.stages, !direct);
+    cfg.dynamicSmemBytes = pl.smem;
     cfg.stream = st;
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;

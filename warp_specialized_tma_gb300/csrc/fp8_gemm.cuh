@@ -53,29 +53,6 @@ __host__ __device__ __forceinline__ bool fp8_range_holds(int64_t units, int32_t 
     return fp8_range_begin(units, clusters, c) < fp8_range_begin(units, clusters, c + 1);
 }
 
-// Ring iterations are released in pairs, (0, 1), (2, 3), ..., by one commit each (a
-// commit takes the issuer 100 clocks): pair q on barrier q mod Q, Q = (S + 1) / 2.
-// Iteration i may overwrite its stage once i - S is released, so its loader waits
-// at every i with i - S even, for pair (i - S) / 2 -- which, where S is odd, also
-// releases the next iteration's.  No barrier can be a phase further than the one
-// waited for: pair q + Q holds iterations from 2 q + S on, which need this wait.
-struct Fp8Release {
-    int32_t i, q;
-    uint32_t ph;
-
-    __device__ __forceinline__ void init(int S) { i = -S, q = 0, ph = 0u; }
-    // whether the iteration needs a wait for barrier q, parity ph
-    __device__ __forceinline__ bool due() const { return i >= 0 && (i & 1) == 0; }
-    __device__ __forceinline__ void next(int Q)
-    {
-        if (due() && ++q == Q) {
-            q = 0;
-            ph ^= 1u;
-        }
-        ++i;
-    }
-};
-
 // The range that holds unit u.
 __host__ __device__ __forceinline__ int32_t fp8_range_of(int64_t units, int32_t clusters, int64_t u)
 {
@@ -200,46 +177,6 @@ __device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, cons
     }
 }
 
-// Stores this thread's row y, columns x .. x+31, of D, whose rows are 32-byte
-// aligned: whole sectors from every lane, and shared memory left to the ring.
-__device__ __forceinline__ void fp8_store_direct(const uint32_t (&v)[32], int32_t y, int32_t x, bool fp32,
-                                                 const Fp8GemmParams &p)
-{
-    if (y >= p.D_rows)
-        return;
-    if (fp32) {
-        float *const row = static_cast<float *>(p.D) + (int64_t)y * p.ldd + x;
-#pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (x + j + 8 <= p.D_cols) {
-                st_global_v8(row + j, v[j], v[j + 1], v[j + 2], v[j + 3], v[j + 4], v[j + 5], v[j + 6], v[j + 7]);
-            } else {
-#pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (x + j + k < p.D_cols)
-                        row[j + k] = __uint_as_float(v[j + k]);
-            }
-        }
-        return;
-    }
-    uint16_t *const row = static_cast<uint16_t *>(p.D) + (int64_t)y * p.ldd + x;
-#pragma unroll
-    for (int j = 0; j < 32; j += 16) {
-        uint32_t q[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            q[k] = pack_bf16x2(v[j + 2 * k], v[j + 2 * k + 1]);
-        if (x + j + 16 <= p.D_cols) {
-            st_global_v8(row + j, q[0], q[1], q[2], q[3], q[4], q[5], q[6], q[7]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < 16; ++k)
-                if (x + j + k < p.D_cols)
-                    row[j + k] = (uint16_t)(q[k >> 1] >> (16 * (k & 1)));
-        }
-    }
-}
-
 // Stages the warp's 32 accumulator rows x 32 columns (thread = row) as a chunk of
 // D, `live` columns of it when D is the accumulator transposed.
 template <bool kTransposed>
@@ -318,11 +255,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int S = p.stages;
-    const int Q = (S + 1) / 2;  // release barriers
+    const int S = p.stages;  // even: stages are released in pairs
     const uint32_t stage0 = base;
     const uint32_t staging0 = base + (uint32_t)S * stage_bytes;
-    const uint32_t scales0 = staging0 + (p.d_direct ? 0u : (uint32_t)(kFp8EpiWarps * kFp8StagingBytes));
+    const uint32_t scales0 = staging0 + kFp8EpiWarps * kFp8StagingBytes;
     const uint32_t full_bar = scales0 + (uint32_t)S * kFp8ScaleBytes;
     const uint32_t empty_bar = full_bar + 8u * S;
     const uint32_t accf_bar = empty_bar + 8u * S;
@@ -341,7 +277,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar + 8u * s, 1 + 2 * CG);  // the producer's expect_tx, each CTA's two scale warps
-            mbar_init(empty_bar + 8u * s, 1);          // the first Q are used
+            mbar_init(empty_bar + 8u * s, 1);
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(accf_bar + 8u * a, 1);
@@ -397,8 +333,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             const uint32_t full_target = kCluster ? mapa_shared(full_bar, 0u) : full_bar;
             const uint32_t leader = elect_one();
             int s = 0;
-            Fp8Release rel;
-            rel.init(S);
+            uint32_t ph = 0;
             int32_t it = 0;
             bool ok = true;
             grid_dependency_wait();
@@ -407,15 +342,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 const int32_t yr = (tc.mb * CG + (int32_t)rank) * kFp8RowsPerCta;
                 const int32_t yc = tc.nb * width + (int32_t)rank * (width / CG);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (rel.due()) {
-                        const uint32_t bar = empty_bar + 8u * (uint32_t)rel.q;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, rel.ph, ctl.suspend_ns, 1u)) &&
-                            !warp_wait<false>(ctl, bar, rel.ph, kRoleProducer, (uint32_t)s, lane)) {
+                    if (ring_group_first(s, 1u)) {
+                        const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                            !warp_wait<false>(ctl, bar, parity, kRoleProducer, (uint32_t)s, lane)) {
                             ok = false;
                             break;
                         }
                     }
-                    rel.next(Q);
                     if (it != p.fault_skip_it) {
                         if (rank == 0)
                             expect_tx_elected(full_bar + 8u * s, stage_bytes * CG, leader);
@@ -425,7 +359,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                         tma_load_2d_elected<CG>(sa + kRBytes, &tmC, kb * kFp8BlockK, yc, fb, leader);
                     }
                     ++it;
-                    s = s + 1 == S ? 0 : s + 1;
+                    ring_advance(s, ph, S);
                 }
             }
             grid_launch_dependents();
@@ -471,8 +405,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             };
             int s = 0;
             uint32_t ph = 0;
-            int q = 0;         // release barrier of the current pair of iterations
-            bool odd = false;  // the pair's second
             int acc = 0;
             uint32_t acc_ph = 0;
             uint32_t group = 0;  // groups of 4 k-blocks so far: their parity picks the scales' buffer
@@ -514,11 +446,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                         mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
                                      stm + kFp8ScaleColB, kk != 0 ? 1u : fresh ^ 1u, leader);
                     fresh = 0u;
-                    if (odd) {
-                        mma_commit_elected<CG>(empty_bar + 8u * (uint32_t)q, leader);
-                        q = q + 1 == Q ? 0 : q + 1;
-                    }
-                    odd = !odd;
+                    if (ring_group_last(s, 1u))
+                        mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);
                     ring_advance(s, ph, S);
                 }
                 mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
@@ -591,21 +520,19 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             load(v[0]);
             load(v[1]);
             int s = 0;
-            Fp8Release rel;
-            rel.init(S);
+            uint32_t ph = 0;
             uint32_t g = 0;
             bool ok = true;
             while (ok && wi.next(w)) {
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
-                    if (rel.due()) {
-                        const uint32_t bar = empty_bar + 8u * (uint32_t)rel.q;
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, rel.ph, ctl.suspend_ns, 1u)) &&
-                            !warp_wait<false>(ctl, bar, rel.ph, kRoleScales, (uint32_t)s, lane)) {
+                    if (ring_group_first(s, 1u)) {
+                        const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                            !warp_wait<false>(ctl, bar, parity, kRoleScales, (uint32_t)s, lane)) {
                             ok = false;
                             break;
                         }
                     }
-                    rel.next(Q);
                     const bool first = kb == w.kb0 || (kb & 3) == 0;
                     const bool last = kb == w.kb1 - 1 || (kb & 3) == 3;
                     const bool mine = (g & 1u) == which;
@@ -636,7 +563,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                         load(v[1]);
                     }
                     g += last ? 1u : 0u;
-                    s = s + 1 == S ? 0 : s + 1;
+                    ring_advance(s, ph, S);
                 }
             }
         }
@@ -753,12 +680,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 const int32_t cols = yc + c * 32;
                 if (yr >= p.rows || cols >= p.cols)
                     return;
-                if constexpr (!kTransposed) {
-                    if (p.d_direct) {
-                        fp8_store_direct(v, yr + lane, cols, fp32, p);
-                        return;
-                    }
-                }
                 // the staging buffer is free once its last store has read it (or
                 // every lane has finished the masked path's loads)
                 if (lane == 0) {

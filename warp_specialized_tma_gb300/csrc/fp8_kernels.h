@@ -101,8 +101,7 @@ struct Fp8GemmParams {
     int32_t cluster;        // > 1 (one SM per tile only): each tile is split among the CTAs of a cluster
     int32_t D_rows, D_cols;
     int32_t out_fp32;
-    int32_t d_direct;       // D is stored from registers, 32 bytes of a row at a time: no staging buffers
-    int32_t d_tma;          // else: D's layout allows TMA stores
+    int32_t d_tma;          // D's layout allows TMA stores
     int64_t ldd;
     void *D;
     const uint32_t *s_rows; // scale words [ceil(K/512)][rows]
@@ -119,14 +118,10 @@ inline size_t fp8_stage_bytes(int cta_group, int width)
     return (size_t)kFp8RowsPerCta * kFp8BlockK + (size_t)(width / cta_group) * kFp8BlockK;
 }
 
-// Iterations of the ring are released in pairs: iterations 2 q and 2 q + 1 by the
-// barrier q mod this (see the MMA issuer).
-inline constexpr int fp8_release_bars(int stages) { return (stages + 1) / 2; }
-
-inline size_t fp8_smem_bytes(int cta_group, int width, int stages, bool staged)
+inline size_t fp8_smem_bytes(int cta_group, int width, int stages)
 {
     return 1024 /* alignment slack */ + (size_t)stages * (fp8_stage_bytes(cta_group, width) + kFp8ScaleBytes) +
-           (staged ? (size_t)kFp8EpiWarps * kFp8StagingBytes : 0) + 512 /* barriers */;
+           (size_t)kFp8EpiWarps * kFp8StagingBytes + 512 /* barriers */;
 }
 
 // (CUtensorMap rows, CUtensorMap cols, CUtensorMap D, Fp8GemmParams)
