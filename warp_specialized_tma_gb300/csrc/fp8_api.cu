@@ -601,8 +601,8 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
         pl.d_tma = aligned(D, 16) && (pl.ldd * (int64_t)esize) % 16 == 0 &&
                    encode_2d(&pl.tmD,
                              esize == 4 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, D,
-                             (uint64_t)pl.N, (uint64_t)pl.M, (uint64_t)pl.ldd * esize, 32, 32,
-                             esize == 4 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B) == FP8_OK;
+                             (uint64_t)pl.N, (uint64_t)pl.M, (uint64_t)pl.ldd * esize, (uint32_t)(64 / esize), 32,
+                             CU_TENSOR_MAP_SWIZZLE_64B) == FP8_OK;
         if (!pl.d_tma)
             std::memset(&pl.tmD, 0, sizeof(pl.tmD));  // passed, never used
         pl.mA = A, pl.mB = B, pl.mD = D;

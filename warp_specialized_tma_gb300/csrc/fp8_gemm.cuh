@@ -124,23 +124,23 @@ __host__ __device__ __forceinline__ TileCoord fp8_tile_coord(int32_t t, const Fp
 constexpr uint32_t kFp8ScaleCol = 2u * kFp8MaxWidth;  // tensor-memory columns of the scales: two buffers of 32
 constexpr uint32_t kFp8ScaleColB = 16u;               // inside a buffer: row side at 0..3, column side at 16..23
 
-// A 32 x 32 chunk of D, staged in shared memory as rows of D in the TMA swizzle
-// of its row size (64 bytes of bf16, 128 of fp32): byte offset of element (r, c).
-__device__ __forceinline__ uint32_t fp8_chunk_offset(uint32_t r, uint32_t c, bool fp32)
+// A piece of D, staged in shared memory as 32 rows of 64 bytes (32 columns of bf16,
+// 16 of fp32) in the TMA swizzle of that row size: byte offset of element (r, c).
+__device__ __forceinline__ uint32_t fp8_piece_offset(uint32_t r, uint32_t c, bool fp32)
 {
-    if (fp32)
-        return r * 128u + (((c >> 2) ^ (r & 7u)) << 4) + (c & 3u) * 4u;
-    return r * 64u + (((c >> 3) ^ ((r >> 1) & 3u)) << 4) + (c & 7u) * 2u;
+    const uint32_t byte = fp32 ? c * 4u : c * 2u;
+    return r * 64u + (((byte >> 4) ^ ((r >> 1) & 3u)) << 4) + (byte & 15u);
 }
 
-// Stores the staged chunk at D[y..y+31][x..x+31] by a TMA store, or, where D's
+// Stores the staged piece at D[y..y+31][x..] by a TMA store, or, where D's
 // layout or its last columns do not allow one (a TMA store writes whole 16-byte
 // groups), by the warp's masked stores.
-__device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, const CUtensorMap *tmD, int32_t x, int32_t y,
+__device__ __forceinline__ void fp8_store_piece(uint32_t staging, int lane, const CUtensorMap *tmD, int32_t x, int32_t y,
                                                 bool fp32, const Fp8GemmParams &p)
 {
-    const int32_t group = fp32 ? 4 : 8;
-    if (p.d_tma && (x + 32 <= p.D_cols || p.D_cols % group == 0)) {
+    if (x >= p.D_cols)
+        return;
+    if (p.d_tma && (x + (fp32 ? 16 : 32) <= p.D_cols || p.D_cols % (fp32 ? 4 : 8) == 0)) {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -150,21 +150,20 @@ __device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, cons
         return;
     }
     if (lane == 0)
-        bulk_wait_read_all();  // the next chunk counts on at most one store in flight, the last one
+        bulk_wait_read_all();  // the next piece counts on at most one store in flight, the last one
     __syncwarp();
     const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
-    if (fp32) {
-        float *const D = static_cast<float *>(p.D) + (int64_t)y * p.ldd + x + lane;
-        if (x + lane < p.D_cols)
-            for (int32_t r = 0; r < rows; ++r)
-                D[(int64_t)r * p.ldd] =
-                    __uint_as_float(ld_shared_u32(staging + fp8_chunk_offset((uint32_t)r, (uint32_t)lane, true)));
-        return;
-    }
-    // lanes 0-15 take even rows, 16-31 odd ones, two columns each
-    const int32_t c = (lane & 15) * 2;
+    // lanes 0-15 take even rows, 16-31 odd ones, four bytes each
     for (int32_t r = lane >> 4; r < rows; r += 2) {
-        const uint32_t w = ld_shared_u32(staging + fp8_chunk_offset((uint32_t)r, (uint32_t)c, false));
+        if (fp32) {
+            const int32_t c = lane & 15;
+            if (x + c < p.D_cols)
+                static_cast<float *>(p.D)[(int64_t)(y + r) * p.ldd + x + c] =
+                    __uint_as_float(ld_shared_u32(staging + fp8_piece_offset((uint32_t)r, (uint32_t)c, true)));
+            continue;
+        }
+        const int32_t c = (lane & 15) * 2;
+        const uint32_t w = ld_shared_u32(staging + fp8_piece_offset((uint32_t)r, (uint32_t)c, false));
         uint16_t *const dst = static_cast<uint16_t *>(p.D) + (int64_t)(y + r) * p.ldd + x + c;
         if (x + c + 1 < p.D_cols && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
             *reinterpret_cast<uint32_t *>(dst) = w;
@@ -177,34 +176,65 @@ __device__ __forceinline__ void fp8_store_chunk(uint32_t staging, int lane, cons
     }
 }
 
-// Stages the warp's 32 accumulator rows x 32 columns (thread = row) as a chunk of
-// D, `live` columns of it when D is the accumulator transposed.
+// The warp's two staging buffers take turns; each is free once its last store has
+// read it (or every lane has finished the masked path's loads).
+struct Fp8Staging {
+    uint32_t base, buf;
+
+    __device__ __forceinline__ uint32_t next(int lane)
+    {
+        if (lane == 0)
+            bulk_wait_read_one();
+        __syncwarp();
+        buf ^= 2048u;
+        return base + buf;
+    }
+};
+
+// Stores the warp's 32 accumulator rows x 32 columns (thread = row): accumulator
+// row `row`, column `col` onward.  D is the accumulator or (kTransposed) its transpose.
 template <bool kTransposed>
-__device__ __forceinline__ void fp8_stage_chunk(const uint32_t (&v)[32], uint32_t staging, uint32_t lane, int32_t live,
-                                                bool fp32)
+__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[32], Fp8Staging &staging, int lane, bool fp32,
+                                                const CUtensorMap *tmD, int32_t row, int32_t col, const Fp8GemmParams &p)
 {
     if constexpr (kTransposed) {
+        // columns of the accumulator are rows of D: `live` of them exist.  An fp32
+        // piece is half as wide: lanes 0-15 fill one, 16-31 the other.
+        const int32_t live = p.cols - col;
+        const uint32_t one = staging.next(lane);
+        const uint32_t two = fp32 ? staging.next(lane) : one;
+        const uint32_t mine = fp32 && lane >= 16 ? two : one;
 #pragma unroll
         for (uint32_t i = 0; i < 32; ++i) {
             if ((int32_t)i >= live)
                 break;
-            const uint32_t at = staging + fp8_chunk_offset(i, lane, fp32);
+            const uint32_t at = mine + fp8_piece_offset(i, fp32 ? (uint32_t)lane & 15u : (uint32_t)lane, fp32);
             if (fp32)
                 st_shared_u32(at, v[i]);
             else
                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pack_bf16x2(v[i], 0u)) : "memory");
         }
+        fp8_store_piece(one, lane, tmD, row, col, fp32, p);
+        if (fp32)
+            fp8_store_piece(two, lane, tmD, row + 16, col, fp32, p);
     } else if (fp32) {
 #pragma unroll
-        for (uint32_t u = 0; u < 8; ++u)
-            st_shared_v4(staging + fp8_chunk_offset(lane, 4 * u, true), v[4 * u], v[4 * u + 1], v[4 * u + 2],
-                         v[4 * u + 3]);
+        for (uint32_t h = 0; h < 2; ++h) {
+            const uint32_t st = staging.next(lane);
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                st_shared_v4(st + fp8_piece_offset((uint32_t)lane, 4 * u, true), v[16 * h + 4 * u], v[16 * h + 4 * u + 1],
+                             v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]);
+            fp8_store_piece(st, lane, tmD, col + 16 * (int32_t)h, row, true, p);
+        }
     } else {
+        const uint32_t st = staging.next(lane);
 #pragma unroll
         for (uint32_t u = 0; u < 4; ++u)
-            st_shared_v4(staging + fp8_chunk_offset(lane, 8 * u, false), pack_bf16x2(v[8 * u], v[8 * u + 1]),
+            st_shared_v4(st + fp8_piece_offset((uint32_t)lane, 8 * u, false), pack_bf16x2(v[8 * u], v[8 * u + 1]),
                          pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
                          pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+        fp8_store_piece(st, lane, tmD, col, row, false, p);
     }
 }
 
@@ -574,14 +604,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int q = warp & 3;         // tensor-memory lane quadrant
         const int half = ew >> 2;       // takes chunks half, half + 2, ... of 32 columns
         const int nchunks = (width + 31) / 32;
-        const uint32_t staging = staging0 + (uint32_t)ew * kFp8StagingBytes;
+        Fp8Staging staging = {staging0 + (uint32_t)ew * kFp8StagingBytes, 0u};
         const uint32_t acce_target = kCluster ? mapa_shared(acce_bar, 0u) : acce_bar;
         const bool fp32 = kLong || p.out_fp32 != 0;
         const int32_t cta = cluster_id * CG + (int32_t)rank;
         int acc = 0;
         uint32_t acc_ph = 0;
         uint32_t item_parity = 0;
-        uint32_t buf = 0;
         bool ok = true;
         const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
         // one thread waits for the accumulator and posts the outcome, so that all
@@ -680,22 +709,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 const int32_t cols = yc + c * 32;
                 if (yr >= p.rows || cols >= p.cols)
                     return;
-                // the staging buffer is free once its last store has read it (or
-                // every lane has finished the masked path's loads)
-                if (lane == 0) {
-                    if (fp32)
-                        bulk_wait_read_all();
-                    else
-                        bulk_wait_read_one();
-                }
-                __syncwarp();
-                const uint32_t st = staging + (fp32 ? 0u : buf * 2048u);
-                buf ^= 1u;
-                fp8_stage_chunk<kTransposed>(v, st, (uint32_t)lane, p.cols - cols, fp32);
-                if constexpr (kTransposed)
-                    fp8_store_chunk(st, lane, &tmD, yr, cols, fp32, p);
-                else
-                    fp8_store_chunk(st, lane, &tmD, cols, yr, fp32, p);
+                fp8_store_chunk<kTransposed>(v, staging, lane, fp32, &tmD, yr, cols, p);
             };
 
             if constexpr (kLong) {

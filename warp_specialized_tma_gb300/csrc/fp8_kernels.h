@@ -82,7 +82,7 @@ constexpr int kFp8MaxWidth = 224;     // column side of a tile: two accumulators
 constexpr int kFp8Threads = 384;      // warps 0-3: producer, MMA, tensor memory, scales; 4-11: epilogue
 constexpr int kFp8EpiWarps = 8;
 constexpr int kFp8ScaleBytes = 512 + 1024;  // a stage's scales: 128 words of the row side, 256 of the column side
-constexpr int kFp8StagingBytes = 4096;      // per epilogue warp: 32 rows of 32 fp32 (or two of 32 bf16)
+constexpr int kFp8StagingBytes = 4096;      // per epilogue warp: two buffers of 32 rows of 64 bytes
 constexpr int kFp8MaxStages = 12;
 constexpr int kFp8MaxLongWidth = 192;  // the same where an fp32 D's sums are held in registers (three chunks a warp)
 constexpr int kFp8Segment = 32;             // k-blocks an accumulator takes before its sums are moved on (fp32 D)
