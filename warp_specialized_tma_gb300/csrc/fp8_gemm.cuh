@@ -132,109 +132,111 @@ __device__ __forceinline__ uint32_t fp8_piece_offset(uint32_t r, uint32_t c, boo
     return r * 64u + (((byte >> 4) ^ ((r >> 1) & 3u)) << 4) + (byte & 15u);
 }
 
-// Stores the staged piece at D[y..y+31][x..] by a TMA store, or, where D's
-// layout or its last columns do not allow one (a TMA store writes whole 16-byte
-// groups), by the warp's masked stores.
-__device__ __forceinline__ void fp8_store_piece(uint32_t staging, int lane, const CUtensorMap *tmD, int32_t x, int32_t y,
-                                                bool fp32, const Fp8GemmParams &p)
+constexpr uint32_t kFp8PieceBytes = 2048;  // 32 rows of 64 bytes; a warp stages two
+
+// Stores one or two staged pieces, at D[y0..y0+31][x0..] and D[y1..][x1..], by TMA
+// stores, or, where D's layout or its last columns do not allow one (a TMA store
+// writes whole 16-byte groups), by the warp's masked stores.  Pieces outside D are
+// dropped.  One proxy fence serves both pieces: it takes 300 clocks.
+__device__ __forceinline__ void fp8_store_pieces(uint32_t staging, int lane, const CUtensorMap *tmD, int pieces,
+                                                 int32_t x0, int32_t y0, int32_t x1, int32_t y1, bool fp32,
+                                                 const Fp8GemmParams &p)
 {
-    if (x >= p.D_cols)
-        return;
-    if (p.d_tma && (x + (fp32 ? 16 : 32) <= p.D_cols || p.D_cols % (fp32 ? 4 : 8) == 0)) {
+    const int32_t wide = fp32 ? 16 : 32;
+    const int32_t far = pieces == 2 && x1 > x0 ? x1 : x0;
+    if (p.d_tma && (far + wide <= p.D_cols || p.D_cols % (fp32 ? 4 : 8) == 0)) {
         fence_proxy_async_shared();
         __syncwarp();
         if (lane == 0) {
-            tma_store_2d(tmD, staging, x, y);
+            if (x0 < p.D_cols && y0 < p.D_rows)
+                tma_store_2d(tmD, staging, x0, y0);
+            if (pieces == 2 && x1 < p.D_cols && y1 < p.D_rows)
+                tma_store_2d(tmD, staging + kFp8PieceBytes, x1, y1);
             bulk_commit_group();
         }
         return;
     }
-    if (lane == 0)
-        bulk_wait_read_all();  // the next piece counts on at most one store in flight, the last one
     __syncwarp();
-    const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
-    // lanes 0-15 take even rows, 16-31 odd ones, four bytes each
-    for (int32_t r = lane >> 4; r < rows; r += 2) {
-        if (fp32) {
-            const int32_t c = lane & 15;
-            if (x + c < p.D_cols)
-                static_cast<float *>(p.D)[(int64_t)(y + r) * p.ldd + x + c] =
-                    __uint_as_float(ld_shared_u32(staging + fp8_piece_offset((uint32_t)r, (uint32_t)c, true)));
-            continue;
-        }
-        const int32_t c = (lane & 15) * 2;
-        const uint32_t w = ld_shared_u32(staging + fp8_piece_offset((uint32_t)r, (uint32_t)c, false));
-        uint16_t *const dst = static_cast<uint16_t *>(p.D) + (int64_t)(y + r) * p.ldd + x + c;
-        if (x + c + 1 < p.D_cols && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
-            *reinterpret_cast<uint32_t *>(dst) = w;
-        } else {
-            if (x + c < p.D_cols)
-                dst[0] = (uint16_t)w;
-            if (x + c + 1 < p.D_cols)
-                dst[1] = (uint16_t)(w >> 16);
+    for (int k = 0; k < pieces; ++k) {
+        const uint32_t from = staging + (uint32_t)k * kFp8PieceBytes;
+        const int32_t x = k ? x1 : x0, y = k ? y1 : y0;
+        const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
+        // lanes 0-15 take even rows, 16-31 odd ones, four bytes each
+        for (int32_t r = lane >> 4; r < rows; r += 2) {
+            if (fp32) {
+                const int32_t c = lane & 15;
+                if (x + c < p.D_cols)
+                    static_cast<float *>(p.D)[(int64_t)(y + r) * p.ldd + x + c] =
+                        __uint_as_float(ld_shared_u32(from + fp8_piece_offset((uint32_t)r, (uint32_t)c, true)));
+                continue;
+            }
+            const int32_t c = (lane & 15) * 2;
+            const uint32_t w = ld_shared_u32(from + fp8_piece_offset((uint32_t)r, (uint32_t)c, false));
+            uint16_t *const dst = static_cast<uint16_t *>(p.D) + (int64_t)(y + r) * p.ldd + x + c;
+            if (x + c + 1 < p.D_cols && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
+                *reinterpret_cast<uint32_t *>(dst) = w;
+            } else {
+                if (x + c < p.D_cols)
+                    dst[0] = (uint16_t)w;
+                if (x + c + 1 < p.D_cols)
+                    dst[1] = (uint16_t)(w >> 16);
+            }
         }
     }
 }
 
-// The warp's two staging buffers take turns; each is free once its last store has
-// read it (or every lane has finished the masked path's loads).
-struct Fp8Staging {
-    uint32_t base, buf;
+// The staging buffers are free once their last stores have read them (or every
+// lane has finished the masked path's loads).
+__device__ __forceinline__ void fp8_staging_free(int lane)
+{
+    if (lane == 0)
+        bulk_wait_read_all();
+    __syncwarp();
+}
 
-    __device__ __forceinline__ uint32_t next(int lane)
-    {
-        if (lane == 0)
-            bulk_wait_read_one();
-        __syncwarp();
-        buf ^= 2048u;
-        return base + buf;
-    }
-};
+// Stages 32 accumulator rows x 32 columns (thread = row) of bf16 as one piece.
+__device__ __forceinline__ void fp8_stage_bf16(const uint32_t (&v)[32], uint32_t at, int lane)
+{
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+        st_shared_v4(at + fp8_piece_offset((uint32_t)lane, 8 * u, false), pack_bf16x2(v[8 * u], v[8 * u + 1]),
+                     pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
+                     pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
+}
 
 // Stores the warp's 32 accumulator rows x 32 columns (thread = row): accumulator
 // row `row`, column `col` onward.  D is the accumulator or (kTransposed) its transpose.
 template <bool kTransposed>
-__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[32], Fp8Staging &staging, int lane, bool fp32,
+__device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[32], uint32_t staging, int lane, bool fp32,
                                                 const CUtensorMap *tmD, int32_t row, int32_t col, const Fp8GemmParams &p)
 {
+    fp8_staging_free(lane);
     if constexpr (kTransposed) {
         // columns of the accumulator are rows of D: `live` of them exist.  An fp32
         // piece is half as wide: lanes 0-15 fill one, 16-31 the other.
         const int32_t live = p.cols - col;
-        const uint32_t one = staging.next(lane);
-        const uint32_t two = fp32 ? staging.next(lane) : one;
-        const uint32_t mine = fp32 && lane >= 16 ? two : one;
+        const uint32_t mine = staging + (fp32 && lane >= 16 ? kFp8PieceBytes : 0u);
+        const uint32_t at_lane = fp32 ? (uint32_t)lane & 15u : (uint32_t)lane;
 #pragma unroll
         for (uint32_t i = 0; i < 32; ++i) {
             if ((int32_t)i >= live)
                 break;
-            const uint32_t at = mine + fp8_piece_offset(i, fp32 ? (uint32_t)lane & 15u : (uint32_t)lane, fp32);
+            const uint32_t at = mine + fp8_piece_offset(i, at_lane, fp32);
             if (fp32)
                 st_shared_u32(at, v[i]);
             else
                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(at), "h"((uint16_t)pack_bf16x2(v[i], 0u)) : "memory");
         }
-        fp8_store_piece(one, lane, tmD, row, col, fp32, p);
-        if (fp32)
-            fp8_store_piece(two, lane, tmD, row + 16, col, fp32, p);
+        fp8_store_pieces(staging, lane, tmD, fp32 ? 2 : 1, row, col, row + 16, col, fp32, p);
     } else if (fp32) {
 #pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) {
-            const uint32_t st = staging.next(lane);
-#pragma unroll
-            for (uint32_t u = 0; u < 4; ++u)
-                st_shared_v4(st + fp8_piece_offset((uint32_t)lane, 4 * u, true), v[16 * h + 4 * u], v[16 * h + 4 * u + 1],
-                             v[16 * h + 4 * u + 2], v[16 * h + 4 * u + 3]);
-            fp8_store_piece(st, lane, tmD, col + 16 * (int32_t)h, row, true, p);
-        }
+        for (uint32_t u = 0; u < 8; ++u)
+            st_shared_v4(staging + (u >= 4 ? kFp8PieceBytes : 0u) + fp8_piece_offset((uint32_t)lane, 4 * (u & 3), true),
+                         v[4 * u], v[4 * u + 1], v[4 * u + 2], v[4 * u + 3]);
+        fp8_store_pieces(staging, lane, tmD, 2, col, row, col + 16, row, true, p);
     } else {
-        const uint32_t st = staging.next(lane);
-#pragma unroll
-        for (uint32_t u = 0; u < 4; ++u)
-            st_shared_v4(st + fp8_piece_offset((uint32_t)lane, 8 * u, false), pack_bf16x2(v[8 * u], v[8 * u + 1]),
-                         pack_bf16x2(v[8 * u + 2], v[8 * u + 3]), pack_bf16x2(v[8 * u + 4], v[8 * u + 5]),
-                         pack_bf16x2(v[8 * u + 6], v[8 * u + 7]));
-        fp8_store_piece(st, lane, tmD, col, row, false, p);
+        fp8_stage_bf16(v, staging, lane);
+        fp8_store_pieces(staging, lane, tmD, 1, col, row, col, row, false, p);
     }
 }
 
@@ -604,7 +606,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
         const int q = warp & 3;         // tensor-memory lane quadrant
         const int half = ew >> 2;       // takes chunks half, half + 2, ... of 32 columns
         const int nchunks = (width + 31) / 32;
-        Fp8Staging staging = {staging0 + (uint32_t)ew * kFp8StagingBytes, 0u};
+        const uint32_t staging = staging0 + (uint32_t)ew * kFp8StagingBytes;
         const uint32_t acce_target = kCluster ? mapa_shared(acce_bar, 0u) : acce_bar;
         const bool fp32 = kLong || p.out_fp32 != 0;
         const int32_t cta = cluster_id * CG + (int32_t)rank;
@@ -755,12 +757,29 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     hand_back();
                     collect();
                 }
-                for (int c = half; c < nchunks; c += 2) {
+                int c = half;
+                if (!kTransposed && !fp32 && !contributor && !owner) {
+                    // whole tiles of bf16, most of the work: two chunks at a time
+                    for (; c + 2 < nchunks; c += 4) {
+                        uint32_t v0[32], v1[32];
+                        load_chunk(c, v0);
+                        load_chunk(c + 2, v1);
+                        if (c + 4 >= nchunks)
+                            hand_back();
+                        if (yr >= p.rows || yc + c * 32 >= p.cols)
+                            continue;
+                        fp8_staging_free(lane);
+                        fp8_stage_bf16(v0, staging, lane);
+                        fp8_stage_bf16(v1, staging + kFp8PieceBytes, lane);
+                        fp8_store_pieces(staging, lane, &tmD, 2, yc + c * 32, yr, yc + c * 32 + 64, yr, false, p);
+                    }
+                }
+                for (; c < nchunks; c += 2) {
                     uint32_t v[32];
                     load_chunk(c, v);
                     if (c + 2 >= nchunks)
                         hand_back();
-                    if (c == half)
+                    if (c == half && owner)
                         collect();  // after this piece's own sums have been read
                     finish(c, v);
                 }
