@@ -124,6 +124,8 @@ __host__ __device__ __forceinline__ TileCoord fp8_tile_coord(int32_t t, const Fp
 constexpr uint32_t kFp8ScaleCol = 2u * kFp8MaxWidth;  // tensor-memory columns of the scales: two buffers of 32
 constexpr uint32_t kFp8ScaleColB = 16u;               // inside a buffer: row side at 0..3, column side at 16..23
 
+constexpr uint32_t kFp8PieceBytes = 2048;  // a warp stages two
+
 // A piece of D, staged in shared memory as 32 rows of 64 bytes (32 columns of bf16,
 // 16 of fp32) in the TMA swizzle of that row size: byte offset of element (r, c).
 __device__ __forceinline__ uint32_t fp8_piece_offset(uint32_t r, uint32_t c, bool fp32)
@@ -132,7 +134,51 @@ __device__ __forceinline__ uint32_t fp8_piece_offset(uint32_t r, uint32_t c, boo
     return r * 64u + (((byte >> 4) ^ ((r >> 1) & 3u)) << 4) + (byte & 15u);
 }
 
-constexpr uint32_t kFp8PieceBytes = 2048;  // 32 rows of 64 bytes; a warp stages two
+// Stores 32 x 32 staged elements (a piece of bf16, or two of fp32 side by side) by the
+// warp, a row at a time, an element a lane: whatever the row's alignment, its
+// sectors then leave in one request (pairs of bf16 to a lane diverge by alignment
+// and split the odd rows' sectors).  Eight rows' loads come before their stores.
+__device__ __forceinline__ void fp8_store_masked(uint32_t from, int lane, int32_t x, int32_t y, bool fp32,
+                                                 const Fp8GemmParams &p)
+{
+    const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
+    if (x + lane >= p.D_cols)
+        return;
+    const int64_t at = (int64_t)y * p.ldd + x + lane;
+    if (fp32) {
+        float *dst = static_cast<float *>(p.D) + at;
+        from += lane >= 16 ? kFp8PieceBytes : 0u;
+        for (int32_t r = 0; r < rows; r += 8) {
+            uint32_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                w[k] = ld_shared_u32(from + fp8_piece_offset((uint32_t)(r + k), (uint32_t)lane & 15u, true));
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (r + k < rows)
+                    *dst = __uint_as_float(w[k]);
+                dst += p.ldd;
+            }
+        }
+        return;
+    }
+    uint16_t *dst = static_cast<uint16_t *>(p.D) + at;
+    for (int32_t r = 0; r < rows; r += 8) {
+        uint16_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            asm volatile("ld.shared.u16 %0, [%1];"
+                         : "=h"(w[k])
+                         : "r"(from + fp8_piece_offset((uint32_t)(r + k), (uint32_t)lane, false))
+                         : "memory");
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            if (r + k < rows)
+                *dst = w[k];
+            dst += p.ldd;
+        }
+    }
+}
 
 // Stores one or two staged pieces, at D[y0..y0+31][x0..] and D[y1..][x1..], by TMA
 // stores, or, where D's layout or its last columns do not allow one (a TMA store
@@ -157,32 +203,9 @@ __device__ __forceinline__ void fp8_store_pieces(uint32_t staging, int lane, con
         return;
     }
     __syncwarp();
-    for (int k = 0; k < pieces; ++k) {
-        const uint32_t from = staging + (uint32_t)k * kFp8PieceBytes;
-        const int32_t x = k ? x1 : x0, y = k ? y1 : y0;
-        const int32_t rows = p.D_rows - y < 32 ? p.D_rows - y : 32;
-        // lanes 0-15 take even rows, 16-31 odd ones, four bytes each
-        for (int32_t r = lane >> 4; r < rows; r += 2) {
-            if (fp32) {
-                const int32_t c = lane & 15;
-                if (x + c < p.D_cols)
-                    static_cast<float *>(p.D)[(int64_t)(y + r) * p.ldd + x + c] =
-                        __uint_as_float(ld_shared_u32(from + fp8_piece_offset((uint32_t)r, (uint32_t)c, true)));
-                continue;
-            }
-            const int32_t c = (lane & 15) * 2;
-            const uint32_t w = ld_shared_u32(from + fp8_piece_offset((uint32_t)r, (uint32_t)c, false));
-            uint16_t *const dst = static_cast<uint16_t *>(p.D) + (int64_t)(y + r) * p.ldd + x + c;
-            if (x + c + 1 < p.D_cols && (reinterpret_cast<uintptr_t>(dst) & 3u) == 0) {
-                *reinterpret_cast<uint32_t *>(dst) = w;
-            } else {
-                if (x + c < p.D_cols)
-                    dst[0] = (uint16_t)w;
-                if (x + c + 1 < p.D_cols)
-                    dst[1] = (uint16_t)(w >> 16);
-            }
-        }
-    }
+    fp8_store_masked(staging, lane, x0, y0, fp32, p);
+    if (!fp32 && pieces == 2)
+        fp8_store_masked(staging + kFp8PieceBytes, lane, x1, y1, false, p);
 }
 
 // The staging buffers are free once their last stores have read them (or every

@@ -180,7 +180,4 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                  : "memory");
 }
 
-// Wait until at most one committed bulk store of this thread still reads shared memory.
-__device__ __forceinline__ void bulk_wait_read_one() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
-
 }  // namespace wstma
