@@ -150,3 +150,15 @@ def test_reference_gradient_is_that_of_the_norm():
     loss = lambda a, b: (dy * ref.rmsnorm(a, b, eps)[0]).sum()  # noqa: E731
     assert (loss(h + t * v, w) - loss(h - t * v, w)) / (2 * t) == pytest.approx((dx * v).sum(), rel=1e-6)
     assert (loss(h, w + t * u) - loss(h, w - t * u)) / (2 * t) == pytest.approx((dw * u).sum(), rel=1e-6)
+
+
+def test_work_split(tmp_path):
+    """The product's work split (host functions of its kernel's header): tests/fp8_split_check.cu."""
+    nvcc = libbuild.nvcc()
+    exe = tmp_path / "fp8_split_check"
+    build = subprocess.run(
+        [nvcc, "-std=c++17", "-O2", *libbuild.ARCH, "-I", libbuild.INCLUDE, "-I", libbuild.CSRC,
+         os.path.join(ROOT, "tests", "fp8_split_check.cu"), "-o", str(exe)], capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.endswith("splits\n"), run.stdout + run.stderr

@@ -19,6 +19,7 @@ using namespace wstma;
 namespace {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL;
+constexpr int64_t kMaxRows = kMaxDim - 1023;  // a tile past the last row still has a 32-bit index
 constexpr int64_t kMaxPitch = int64_t(1) << 38;
 constexpr int kNumOptions = 8;
 constexpr int kPlans = 32;          // plans a handle remembers
@@ -395,6 +396,8 @@ FP8_API int fp8_gemm_check_problem(int64_t M, int64_t N, int64_t K, int64_t lda,
         return FP8_ERR_INVALID_ARG;
     if (lda % 16 != 0 || ldb % 16 != 0)
         return FP8_ERR_ALIGNMENT;
+    if (M > kMaxRows || N > kMaxRows)
+        return FP8_ERR_UNSUPPORTED;
     return FP8_OK;
 }
 
@@ -706,7 +709,7 @@ FP8_API int fp8_quantize(const void *x, int x_type, int64_t ldx, int64_t R, int6
         return FP8_ERR_ALIGNMENT;
     if (cols && (!aligned(codes_t, 16) || ldqt % 16 != 0 || !aligned(scales_t, 4)))
         return FP8_ERR_ALIGNMENT;
-    if (ceil_div(R, kFp8BlockK) * ceil_div(C, kFp8BlockK) > kMaxDim)
+    if (R > kMaxRows || C > kMaxRows || ceil_div(R, kFp8BlockK) * ceil_div(C, kFp8BlockK) > kMaxDim)
         return FP8_ERR_UNSUPPORTED;
     int sms = 0;
     const int rc = current_sms(&sms);
