@@ -56,7 +56,58 @@ __device__ __forceinline__ void unpack8(const uint4 q, float (&f)[8])
     }
 }
 
-__device__ __forceinline__ float bf16_value(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+// Two fp32 in a register pair, and their products: one instruction for both.
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+
+__device__ __forceinline__ void f32x2_parts(uint64_t v, float &lo, float &hi)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+__device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// The largest of three magnitudes; NaN is passed over.
+__device__ __forceinline__ float max3_abs(float a, float b, float c)
+{
+    float r;
+    asm("max.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Eight bf16 -> fp32 pairs.
+__device__ __forceinline__ void unpack8_pairs(const uint4 q, uint64_t (&f)[4])
+{
+    const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        f[i] = f32x2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xFFFF0000u));
+}
+
+// Two pairs -> four e4m3 codes.
+__device__ __forceinline__ uint32_t pack_e4m3x4(uint64_t a, uint64_t b)
+{
+    float f[4];
+    f32x2_parts(a, f[0], f[1]);
+    f32x2_parts(b, f[2], f[3]);
+    return pack_e4m3x4(f[0], f[1], f[2], f[3]);
+}
 
 __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi)
 {

@@ -696,10 +696,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 // The cluster form keeps a partial in the CTA's own ring: a
                 // contributor's only item has consumed all of its loads by now.
                 const uint32_t local = stage0 + (uint32_t)(((ew * 4 + (c >> 1)) * 8) * 32 + lane) * 16u;
+                // (of a transposed D, only its rows' columns, four at a time)
+                const int live = kTransposed ? min(8, (p.cols - (yc + c * 32) + 3) >> 2) : 8;
                 if (contributor && shared_tile) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
-                        st_shared_v4(local + 512u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                        if (j < live)
+                            st_shared_v4(local + 512u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
                     return;
                 }
                 if (contributor) {
@@ -707,20 +710,44 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     return;
                 }
                 if (parts && shared_tile) {
-                    for (int32_t rk = 1; rk < p.cluster; ++rk) {
-                        const uint32_t remote = mapa_shared(local, (uint32_t)rk);
-                        // several loads before their adds: the round trips overlap
-                        constexpr int kBatch = kLong ? 4 : 8;
+                    // Several loads before their adds, so that the round trips
+                    // overlap: of one piece after another, or, where few columns
+                    // come from many pieces, of several at a time.
+                    constexpr int kBatch = kLong ? 4 : 8;
+                    if (!kLong && live <= 2) {
+                        for (int32_t rk = 1; rk < p.cluster; rk += 4) {
+                            uint32_t x[4][8];
 #pragma unroll
-                        for (int j0 = 0; j0 < 8; j0 += kBatch) {
-                            uint32_t x[4 * kBatch];
+                            for (int b = 0; b < 4; ++b) {
+                                const uint32_t remote = mapa_shared(local, (uint32_t)min(rk + b, p.cluster - 1));
 #pragma unroll
-                            for (int j = 0; j < kBatch; ++j)
-                                ld_shared_cluster_v4(remote + 512u * (j0 + j), x[4 * j], x[4 * j + 1], x[4 * j + 2],
-                                                     x[4 * j + 3]);
+                                for (int j = 0; j < 2; ++j)
+                                    ld_shared_cluster_v4(remote + 512u * j, x[b][4 * j], x[b][4 * j + 1],
+                                                         x[b][4 * j + 2], x[b][4 * j + 3]);
+                            }
 #pragma unroll
-                            for (int j = 0; j < 4 * kBatch; ++j)
-                                v[4 * j0 + j] = __float_as_uint(__uint_as_float(v[4 * j0 + j]) + __uint_as_float(x[j]));
+                            for (int b = 0; b < 4; ++b)
+                                if (rk + b < p.cluster) {
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j)
+                                        v[j] = __float_as_uint(__uint_as_float(v[j]) + __uint_as_float(x[b][j]));
+                                }
+                        }
+                    } else {
+                        for (int32_t rk = 1; rk < p.cluster; ++rk) {
+                            const uint32_t remote = mapa_shared(local, (uint32_t)rk);
+#pragma unroll
+                            for (int j0 = 0; j0 < 8; j0 += kBatch) {
+                                uint32_t x[4 * kBatch];
+#pragma unroll
+                                for (int j = 0; j < kBatch; ++j)
+                                    ld_shared_cluster_v4(remote + 512u * (j0 + j), x[4 * j], x[4 * j + 1],
+                                                         x[4 * j + 2], x[4 * j + 3]);
+#pragma unroll
+                                for (int j = 0; j < 4 * kBatch; ++j)
+                                    v[4 * j0 + j] =
+                                        __float_as_uint(__uint_as_float(v[4 * j0 + j]) + __uint_as_float(x[j]));
+                            }
                         }
                     }
                 } else if (parts) {

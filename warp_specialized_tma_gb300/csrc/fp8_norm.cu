@@ -46,6 +46,19 @@ __device__ __forceinline__ void load8_weight(const void *w, int fp32, int32_t c,
         unpack8(load8_bf16(static_cast<const uint16_t *>(w), c, C, vec), f);
 }
 
+__device__ __forceinline__ void load8_weight(const void *w, int fp32, int32_t c, int32_t C, bool vec, uint64_t (&f)[4])
+{
+    if (fp32) {
+        float g[8];
+        load8_float(static_cast<const float *>(w), c, C, vec, g);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            f[j] = f32x2(g[2 * j], g[2 * j + 1]);
+    } else {
+        unpack8_pairs(load8_bf16(static_cast<const uint16_t *>(w), c, C, vec), f);
+    }
+}
+
 // Rows that are not 16-byte aligned (an odd number of columns) go by aligned
 // accesses and shifts, 8 columns a lane all the same.
 __device__ __forceinline__ uint4 load8_row(const uint16_t *row, int32_t c, int32_t C, bool vec)
@@ -74,6 +87,22 @@ __device__ __forceinline__ uint4 add_bf16(uint4 x, uint4 r)
     for (int j = 0; j < 8; ++j)
         a[j] += b[j];
     return make_uint4(bf16_pair(a[0], a[1]), bf16_pair(a[2], a[3]), bf16_pair(a[4], a[5]), bf16_pair(a[6], a[7]));
+}
+
+__device__ __forceinline__ void add_squares(uint4 h, uint64_t &sum)
+{
+    uint64_t a[4];
+    unpack8_pairs(h, a);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        sum = fma_f32x2(a[j], a[j], sum);
+}
+
+__device__ __forceinline__ float both(uint64_t v)
+{
+    float lo, hi;
+    f32x2_parts(v, lo, hi);
+    return lo + hi;
 }
 
 // The 16-byte group of a row that starts `first` elements into it (less than 0, or
@@ -132,7 +161,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
     const uint16_t *const rr = kRes ? p.residual + row * p.ldr : nullptr;
 
     uint4 hv[V];
-    float sum = 0.f;
+    uint64_t sum2 = 0u;
+    float sum;
     if constexpr (kRows == kRowsAlike) {
         const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(xr) & 15u);
         const int32_t back = (int32_t)(mis >> 1);  // elements of the first group before the row
@@ -184,13 +214,9 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
                 w[4 + k] = lane == 31 ? own[k] : n;
             }
             hv[i] = shift8(w, mis, 0, 8);  // zeros stand past the row's end already
-            float a[8];
-            unpack8(hv[i], a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum = fmaf(a[j], a[j], sum);
+            add_squares(hv[i], sum2);
         }
-        sum = row_sum<kWarpRow>(sum, red);
+        sum = row_sum<kWarpRow>(both(sum2), red);
         // h may be x or residual: stored after every thread's loads
         if constexpr (kRes) {
 #pragma unroll
@@ -215,15 +241,11 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
         }
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float a[8];
-            unpack8(hv[i], a);
-#pragma unroll
-            for (int j = 0; j < 8; ++j)
-                sum = fmaf(a[j], a[j], sum);
+            add_squares(hv[i], sum2);
             if constexpr (kRes)
                 store8_row(p.h + row * p.ldh, (t + i * T) * 8, C, vec, hv[i]);
         }
-        sum = row_sum<kWarpRow>(sum, red);
+        sum = row_sum<kWarpRow>(both(sum2), red);
     }
     const float rstd = 1.f / sqrtf(sum / (float)C + p.eps);
     if (p.rstd && t == 0)
@@ -231,17 +253,20 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
 
     const int32_t KB = (C + kFp8Block - 1) / kFp8Block;
     uint8_t *const codes = p.codes + row * p.ldq;
+    const uint64_t rstd2 = f32x2(rstd, rstd);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int32_t c = (t + i * T) * 8;
-        float y[8], w[8];
-        unpack8(hv[i], y);
+        uint64_t y[4], w[4];
+        unpack8_pairs(hv[i], y);
         load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w);
         float amax = 0.f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            y[j] = y[j] * rstd * w[j];
-            amax = fmaxf(amax, fabsf(y[j]));
+        for (int j = 0; j < 4; ++j) {
+            y[j] = mul_f32x2(mul_f32x2(y[j], rstd2), w[j]);
+            float lo, hi;
+            f32x2_parts(y[j], lo, hi);
+            amax = max3_abs(amax, lo, hi);
         }
 #pragma unroll
         for (int d = 8; d > 0; d >>= 1)
@@ -250,20 +275,22 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
             // a block with an infinity: its scale is that of its finite values
             amax = 0.f;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                amax = fmaxf(amax, finite_abs(y[j]));
-                y[j] = inf_to_nan(y[j]);
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                f32x2_parts(y[j], lo, hi);
+                amax = fmaxf(amax, fmaxf(finite_abs(lo), finite_abs(hi)));
+                y[j] = f32x2(inf_to_nan(lo), inf_to_nan(hi));
             }
 #pragma unroll
             for (int d = 8; d > 0; d >>= 1)
                 amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
         }
         const uint32_t e = scale_byte(amax);
-        const float up = scale_inverse(e);
+        const uint64_t up = f32x2(scale_inverse(e), scale_inverse(e));
         if (c < C) {
             store8_codes(codes, c, C,
-                         make_uint2(pack_e4m3x4(y[0] * up, y[1] * up, y[2] * up, y[3] * up),
-                                    pack_e4m3x4(y[4] * up, y[5] * up, y[6] * up, y[7] * up)));
+                         make_uint2(pack_e4m3x4(mul_f32x2(y[0], up), mul_f32x2(y[1], up)),
+                                    pack_e4m3x4(mul_f32x2(y[2], up), mul_f32x2(y[3], up))));
             if ((t & 15) == 0) {
                 const int32_t kb = c / kFp8Block;
                 uint8_t *const word = p.scales + ((int64_t)(kb >> 2) * p.R + row) * 4;
