@@ -462,6 +462,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             uint32_t ph = 0;
             int acc = 0;
             uint32_t acc_ph = 0;
+            uint32_t ready = 0u;  // the next stage was seen full
             uint32_t group = 0;  // groups of 4 k-blocks so far: their parity picks the scales' buffer
             while (wi.next(w)) {
                 wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
@@ -481,7 +482,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                         cut = fp8_segment_end(kb);
                         fresh = 1u;
                     }
-                    wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
+                    if (!__all_sync(0xFFFFFFFFu, ready))
+                        wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
                     tc_fence_after_sync();
                     if (kb == w.kb0 || (kb & 3) == 0) {
                         // copies and MMAs of one thread execute in order: the copy
@@ -496,10 +498,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     }
                     const uint64_t off = (uint64_t)((uint32_t)s * step);
                     const uint32_t idesc = idesc0 | scale_id((uint32_t)kb & 3u);
-#pragma unroll
-                    for (int kk = 0; kk < kFp8BlockK / 32; ++kk)
-                        mma_mxf8<CG>(d_tmem, rdesc0 + off + 2u * kk, cdesc0 + off + 2u * kk, idesc, stm,
-                                     stm + kFp8ScaleColB, kk != 0 ? 1u : fresh ^ 1u, leader);
+                    int s1 = s;
+                    uint32_t ph1 = ph;
+                    ring_advance(s1, ph1, S);
+                    ready = mma_mxf8_block<CG>(d_tmem, rdesc0 + off, cdesc0 + off, idesc, stm, stm + kFp8ScaleColB,
+                                               fresh ^ 1u, leader, full_bar + 8u * s1, ring_full_parity(ph1));
                     fresh = 0u;
                     if (ring_group_last(s, 1u))
                         mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);

@@ -27,30 +27,58 @@ __device__ __forceinline__ uint32_t elect_one()
     return r;
 }
 
-// D[tmem] (+)= (A * sA) (B * sB)^T over 32 elements of k: e4m3 operands in
-// shared memory, one e8m0 scale per row for these 32 in tensor memory, fp32 sums.
+// D[tmem] (+)= (A * sA) (B * sB)^T over a block of 128 elements of k, as four MMAs of 32:
+// e4m3 operands in shared memory (32 bytes of a swizzled row apart), one e8m0 scale
+// per row in tensor memory, fp32 sums.  The first adds to D if `accumulate`.  Probes
+// the barrier of the next block on the way, so that the probe's 95 clocks pass
+// while the MMAs issue: 1 if its phase has completed.
 template <int CG>
-__device__ __forceinline__ void mma_mxf8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                         uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate, uint32_t leader)
+__device__ __forceinline__ uint32_t mma_mxf8_block(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                   uint32_t sa_tmem, uint32_t sb_tmem, uint32_t accumulate,
+                                                   uint32_t leader, uint32_t next_bar, uint32_t next_parity)
 {
+    uint32_t ready;
     if constexpr (CG == 1)
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader)
+            "{\n\t.reg .pred p, q, w;\n\t.reg .u64 a, b;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 w, [%9], %10;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "setp.ne.b32 q, %8, 0;\n\t"
+            "mov.u64 a, %2;\n\tmov.u64 b, %3;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "setp.ne.b32 p, 1, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "selp.u32 %0, 1, 0, w;\n\t}"
+            : "=r"(ready)
+            : "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader),
+              "r"(next_bar), "r"(next_parity)
             : "memory");
     else
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\t"
-            "setp.ne.b32 p, %6, 0;\n\t"
-            "setp.ne.b32 q, %7, 0;\n\t"
-            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d_tmem),
-            "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader)
+            "{\n\t.reg .pred p, q, w;\n\t.reg .u64 a, b;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 w, [%9], %10;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "setp.ne.b32 q, %8, 0;\n\t"
+            "mov.u64 a, %2;\n\tmov.u64 b, %3;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "setp.ne.b32 p, 1, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "add.u64 a, a, 2;\n\tadd.u64 b, b, 2;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X [%1], a, b, %4, [%5], [%6], p;\n\t"
+            "selp.u32 %0, 1, 0, w;\n\t}"
+            : "=r"(ready)
+            : "r"(d_tmem), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sa_tmem), "r"(sb_tmem), "r"(accumulate), "r"(leader),
+              "r"(next_bar), "r"(next_parity)
             : "memory");
+    return ready;
 }
 
 // mma_commit (CG = 1) or mma_commit_pair (CG = 2) of the elected lane.
