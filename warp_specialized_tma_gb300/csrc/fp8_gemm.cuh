@@ -348,6 +348,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     if (threadIdx.x == 32) {
         prefetch_tensormap(&tmR);
         prefetch_tensormap(&tmC);
+        if (p.d_tma)
+            prefetch_tensormap(&tmD);
     }
     // all CTAs of a cluster have initialised their barriers before any cross-CTA
     // arrive, TMA completion or the paired allocation
