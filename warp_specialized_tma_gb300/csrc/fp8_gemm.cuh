@@ -263,6 +263,67 @@ __device__ __forceinline__ void fp8_store_chunk(const uint32_t (&v)[32], uint32_
     }
 }
 
+// Stores accumulator row `row`, columns col .. col+3, to D or (kTransposed) its transpose.
+template <bool kTransposed>
+__device__ __forceinline__ void fp8_store_four(const uint32_t (&v)[4], int32_t row, int32_t col, bool fp32,
+                                               const Fp8GemmParams &p)
+{
+    if (row >= p.rows)
+        return;
+    const int64_t at = kTransposed ? (int64_t)col * p.ldd + row : (int64_t)row * p.ldd + col;
+    const int64_t step = kTransposed ? p.ldd : 1;
+    if (fp32) {
+        float *const d = static_cast<float *>(p.D) + at;
+        if (!kTransposed && col + 4 <= p.cols && (reinterpret_cast<uintptr_t>(d) & 15u) == 0) {
+            *reinterpret_cast<uint4 *>(d) = make_uint4(v[0], v[1], v[2], v[3]);
+            return;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (col + e < p.cols)
+                d[e * step] = __uint_as_float(v[e]);
+        return;
+    }
+    uint16_t *const d = static_cast<uint16_t *>(p.D) + at;
+    const uint32_t lo = pack_bf16x2(v[0], v[1]), hi = pack_bf16x2(v[2], v[3]);
+    if (!kTransposed && col + 4 <= p.cols && (reinterpret_cast<uintptr_t>(d) & 7u) == 0) {
+        *reinterpret_cast<uint2 *>(d) = make_uint2(lo, hi);
+        return;
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        if (col + e < p.cols)
+            d[e * step] = (uint16_t)((e < 2 ? lo : hi) >> (16 * (e & 1)));
+}
+
+// This rank's share of the float4s of its cluster's tile, each summed over the
+// ranks' shared memories in their order and stored.
+template <bool kTransposed>
+__device__ __forceinline__ void fp8_add_spread(const Fp8GemmParams &p, uint32_t sums, int32_t row0, int32_t col0,
+                                            int nchunks, int ew, int lane)
+{
+    const bool fp32 = p.out_fp32 != 0;
+    const int live = kTransposed && nchunks == 1 ? min(8, (p.cols - col0 + 3) >> 2) : 8;  // float4s of a chunk's row
+    const int units = nchunks * 4 * live;
+    for (int u = (int)cluster_ctarank() + p.cluster * ew; u < units; u += p.cluster * kFp8EpiWarps) {
+        const int j = u % live, c = (u / live) >> 2, quad = (u / live) & 3;
+        const uint32_t from = sums + (uint32_t)((((((c & 1) * 4 + quad) * 4 + (c >> 1)) * 8 + j) * 32 + lane) * 16);
+        uint32_t x[8][4];
+#pragma unroll
+        for (int rk = 0; rk < 8; ++rk)
+            if (rk < p.cluster)
+                ld_shared_cluster_v4(mapa_shared(from, (uint32_t)rk), x[rk][0], x[rk][1], x[rk][2], x[rk][3]);
+#pragma unroll
+        for (int rk = 1; rk < 8; ++rk)
+            if (rk < p.cluster) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    x[0][e] = __float_as_uint(__uint_as_float(x[0][e]) + __uint_as_float(x[rk][e]));
+            }
+        fp8_store_four<kTransposed>(x[0], row0 + quad * 32 + lane, col0 + c * 32 + 4 * j, fp32, p);
+    }
+}
+
 // This thread's 32 values of chunk number `ci` of its warp in a CTA's partial:
 // float4 groups, each 512 contiguous bytes over the warp.
 __device__ __forceinline__ float4 *fp8_partial(float *partials, int32_t cta, int ew, int ci, int lane)
@@ -322,12 +383,15 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const uint32_t tmem_slot = done_bar + 8u;
     const uint32_t abort_flag = tmem_slot + 4u;
     const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
-    const uint32_t ready_bar = go_words + 8u;   // cluster form, rank 0: one per epilogue warp
+    const uint32_t ready_bar = go_words + 8u;   // cluster form: one per epilogue warp of rank 0, or one per rank
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
     const uint32_t rank = kCluster ? cluster_ctarank() : 0u;  // in an SM pair
+    // the cluster form: rank 0 adds up the pieces, or each rank a part of the tile (not
+    // where the registers hold an fp32 D's sums already: they spill)
     const bool shared_tile = !kCluster && p.cluster > 1;
+    const bool spread = !kCluster && !kLong && p.cluster >= kFp8SpreadFrom;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -339,9 +403,11 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             mbar_init(acce_bar + 8u * a, kFp8EpiWarps * CG);
         }
         mbar_init(done_bar, 1);
-        if (shared_tile)
+        if (spread)
+            mbar_init(ready_bar, (uint32_t)p.cluster * kFp8EpiWarps);  // every epilogue warp of every rank
+        else if (shared_tile)
             for (int e = 0; e < kFp8EpiWarps; ++e)
-                mbar_init(ready_bar + 8u * e, (uint32_t)p.cluster - 1u);  // an arrival from every other rank
+                mbar_init(ready_bar + 8u * e, (uint32_t)p.cluster - 1u);  // that warp of every other rank
         st_shared_u32(abort_flag, 0u);
         fence_mbarrier_init();
     }
@@ -681,7 +747,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             int32_t last = cluster_id;
             bool parts = owner;
             auto collect = [&]() {
-                if (owner && shared_tile) {
+                if (owner && spread) {
+                    parts = false;  // they meet below
+                } else if (owner && shared_tile) {
                     uint32_t got = 1u;
                     if (lane == 0)
                         got = ctl.wait<true>(ready_bar + 8u * (uint32_t)ew, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
@@ -703,7 +771,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 const uint32_t local = stage0 + (uint32_t)(((ew * 4 + (c >> 1)) * 8) * 32 + lane) * 16u;
                 // (of a transposed D, only its rows' columns, four at a time)
                 const int live = kTransposed ? min(8, (p.cols - (yc + c * 32) + 3) >> 2) : 8;
-                if (contributor && shared_tile) {
+                if (spread || (contributor && shared_tile)) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j)
                         if (j < live)
@@ -841,7 +909,23 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 acc ^= 1;
                 acc_ph ^= acc == 0 ? 1u : 0u;
             }
-            if (contributor) {
+            if (spread) {
+                // Every rank's sums lie in its own shared memory: once all have
+                // arrived, each adds up its share of the tile's float4s, from all
+                // ranks at once and in their order.  (Rank 0 alone takes a round
+                // trip a piece: 50x146x12439 9.8 us that way, 8.5 this; 241x448x16859
+                // 13 and 12.  With four ranks 939x480x5185 loses 0.3 us by it.)
+                __syncwarp();  // the warp's stores come before its lanes' releases
+                if (lane < p.cluster)
+                    mbar_arrive_cluster(mapa_shared(ready_bar, (uint32_t)lane));
+                uint32_t got = 1u;
+                if (lane == 0)
+                    got = ctl.wait<true>(ready_bar, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
+                __syncwarp();  // lane 0's acquire comes before the lanes' loads
+                if (__shfl_sync(0xFFFFFFFFu, got, 0) == 0u)
+                    break;
+                fp8_add_spread<kTransposed>(p, stage0, tc.mb * kFp8RowsPerCta, yc, nchunks, ew, lane);
+            } else if (contributor) {
                 __syncwarp();  // the warp's stores come before lane 0's release
                 if (lane == 0 && shared_tile)
                     mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (uint32_t)ew, 0u));

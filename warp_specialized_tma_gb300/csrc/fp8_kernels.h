@@ -86,6 +86,7 @@ constexpr int kFp8StagingBytes = 4096;      // per epilogue warp: two buffers of
 constexpr int kFp8MaxStages = 12;
 constexpr int kFp8MaxLongWidth = 192;  // the same where an fp32 D's sums are held in registers (three chunks a warp)
 constexpr int kFp8Segment = 32;             // k-blocks an accumulator takes before its sums are moved on (fp32 D)
+constexpr int kFp8SpreadFrom = 5;            // CTAs of a cluster from which each of them adds up a part of their tile
 constexpr int kFp8PartialFloats = kFp8RowsPerCta * 256;  // one CTA's fp32 partial of a split tile
 
 struct Fp8GemmParams {
