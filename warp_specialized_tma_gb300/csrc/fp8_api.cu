@@ -767,6 +767,7 @@ FP8_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_
     p.w_fp32 = weight_type == FP8_FP32 ? 1 : 0;
     p.R = (int32_t)R;
     p.C = (int32_t)C;
+    p.inv_c = 1.f / (float)p.C;
     p.eps = eps;
     p.w_vec = aligned(weight, 16) ? 1 : 0;
     p.vec = aligned(x, 16) && ldx % 8 == 0 &&

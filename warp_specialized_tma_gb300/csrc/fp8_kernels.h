@@ -40,6 +40,7 @@ struct NormParams {
     const void *weight;
     int32_t w_fp32;
     int32_t R, C;
+    float inv_c;  // 1 / C
     float eps;
     int32_t vec;    // every row is 16-byte aligned
     int32_t w_vec;  // the weight is

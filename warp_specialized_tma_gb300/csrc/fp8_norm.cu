@@ -137,15 +137,109 @@ __device__ __forceinline__ void store_group(uint16_t *row, int32_t first, int32_
             row[first + j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
 }
 
+// Largest of the half-warp's 16 lanes for each of V values, of which lane l is left
+// with number l % V: lanes trade the values they do not keep, so that V maxima
+// together take 3 + V exchanges at most and not 4 V.
+template <int V>
+__device__ __forceinline__ float half_warp_max(const float (&a)[V])
+{
+    const int lane = (int)threadIdx.x;
+    float m = a[0];
+    if constexpr (V >= 2) {
+        const bool odd = lane & 1;
+        m = fmaxf(odd ? a[1] : a[0], __shfl_xor_sync(0xFFFFFFFFu, odd ? a[0] : a[1], 1));
+        if constexpr (V == 4) {
+            const float n = fmaxf(odd ? a[3] : a[2], __shfl_xor_sync(0xFFFFFFFFu, odd ? a[2] : a[3], 1));
+            const bool high = lane & 2;
+            m = fmaxf(high ? n : m, __shfl_xor_sync(0xFFFFFFFFu, high ? m : n, 2));
+        }
+    }
+#pragma unroll
+    for (int d = V; d < 16; d *= 2)
+        m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+    return m;
+}
+
+// A row's vectors t, t + T, ..., normalised and quantised: the maxima of a thread's
+// V blocks are found, turned into scales and stored together (one by one 8192 x 8192
+// without a residual takes 50 us, bound by its instructions; this way 44).
+template <int V>
+__device__ __forceinline__ void normalise(const NormParams &p, int64_t row, int t, int T, const uint4 (&h)[V],
+                                          float rstd)
+{
+    const int32_t C = p.C;
+    const uint64_t rstd2 = f32x2(rstd, rstd);
+    uint64_t y[V][4];
+    float amax[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        uint64_t w[4];
+        unpack8_pairs(h[i], y[i]);
+        load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w);
+        amax[i] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            y[i][j] = mul_f32x2(mul_f32x2(y[i][j], rstd2), w[j]);
+            float lo, hi;
+            f32x2_parts(y[i][j], lo, hi);
+            amax[i] = max3_abs(amax[i], lo, hi);
+        }
+    }
+    float mine = half_warp_max<V>(amax);
+    if (__any_sync(0xFFFFFFFFu, is_inf(mine))) {
+        // a block with an infinity: its scale is that of its finite values
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            amax[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                float lo, hi;
+                f32x2_parts(y[i][j], lo, hi);
+                amax[i] = fmaxf(amax[i], fmaxf(finite_abs(lo), finite_abs(hi)));
+                y[i][j] = f32x2(inf_to_nan(lo), inf_to_nan(hi));
+            }
+        }
+        mine = half_warp_max<V>(amax);
+    }
+    const uint32_t e = scale_byte(mine);
+    const float inverse = scale_inverse(e);
+    const int l = t & 15;
+    if (l < V) {
+        const int32_t KB = (C + kFp8Block - 1) / kFp8Block;
+        const int32_t kb = (t + l * T) / 16;
+        if (kb < KB) {
+            uint8_t *const word = p.scales + ((int64_t)(kb >> 2) * p.R + row) * 4;
+            word[kb & 3] = (uint8_t)e;
+            if (kb == KB - 1)
+                for (int32_t b = (kb & 3) + 1; b < 4; ++b)
+                    word[b] = 127;
+        }
+    }
+    uint8_t *const codes = p.codes + row * p.ldq;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int32_t c = (t + i * T) * 8;
+        const float f = __shfl_sync(0xFFFFFFFFu, inverse, i, 16);
+        const uint64_t up = f32x2(f, f);
+        if (c < C)
+            store8_codes(codes, c, C,
+                         make_uint2(pack_e4m3x4(mul_f32x2(y[i][0], up), mul_f32x2(y[i][1], up)),
+                                    pack_e4m3x4(mul_f32x2(y[i][2], up), mul_f32x2(y[i][3], up))));
+    }
+}
+
 // One pass over the row, which stays in registers as bf16 (h is what is normalised,
-// so nothing is lost): HBM-bound, 8192 x 8192 with a residual 73 us, 6.4 TB/s.
+// so nothing is lost): HBM-bound with a residual, 8192 x 8192 71 us, 6.6 TB/s; without
+// one, 44 us and 4.6 TB/s, by its instructions.
 // Vector v of a row is its columns 8 v .. 8 v + 7: thread t of the row's T holds
 // vectors t, t + T, ..., so the 16 lanes of a half-warp always hold one block of 128.
 // Rows that are shifted alike are loaded, added and stored by 16-byte groups, and
 // turned into vectors from two neighbouring lanes' groups; otherwise unaligned rows
-// go vector by vector (5772 x 5391: 69 us that way).
+// go vector by vector (5772 x 5391: 54 us, 69 that way).  Registers are capped at 64,
+// for 1024 threads an SM, or 48 where two vectors a thread fit them (8192 x 4096 with
+// a residual: 38 us, 41 with 50 registers).
 template <int V, bool kWarpRow, bool kRes, int kRows>
-__global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
+__global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_kernel(const NormParams p)
 {
     __shared__ float red[32];
     constexpr bool vec = kRows == kRowsAligned;
@@ -247,59 +341,17 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const NormParams p)
         }
         sum = row_sum<kWarpRow>(both(sum2), red);
     }
-    const float rstd = 1.f / sqrtf(sum / (float)C + p.eps);
+    const float rstd = __frsqrt_rn(sum * p.inv_c + p.eps);
     if (p.rstd && t == 0)
         p.rstd[row] = rstd;
-
-    const int32_t KB = (C + kFp8Block - 1) / kFp8Block;
-    uint8_t *const codes = p.codes + row * p.ldq;
-    const uint64_t rstd2 = f32x2(rstd, rstd);
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int32_t c = (t + i * T) * 8;
-        uint64_t y[4], w[4];
-        unpack8_pairs(hv[i], y);
-        load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w);
-        float amax = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            y[j] = mul_f32x2(mul_f32x2(y[j], rstd2), w[j]);
-            float lo, hi;
-            f32x2_parts(y[j], lo, hi);
-            amax = max3_abs(amax, lo, hi);
-        }
-#pragma unroll
-        for (int d = 8; d > 0; d >>= 1)
-            amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        if (__any_sync(0xFFFFFFFFu, is_inf(amax))) {
-            // a block with an infinity: its scale is that of its finite values
-            amax = 0.f;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                float lo, hi;
-                f32x2_parts(y[j], lo, hi);
-                amax = fmaxf(amax, fmaxf(finite_abs(lo), finite_abs(hi)));
-                y[j] = f32x2(inf_to_nan(lo), inf_to_nan(hi));
-            }
-#pragma unroll
-            for (int d = 8; d > 0; d >>= 1)
-                amax = fmaxf(amax, __shfl_xor_sync(0xFFFFFFFFu, amax, d));
-        }
-        const uint32_t e = scale_byte(amax);
-        const uint64_t up = f32x2(scale_inverse(e), scale_inverse(e));
-        if (c < C) {
-            store8_codes(codes, c, C,
-                         make_uint2(pack_e4m3x4(mul_f32x2(y[0], up), mul_f32x2(y[1], up)),
-                                    pack_e4m3x4(mul_f32x2(y[2], up), mul_f32x2(y[3], up))));
-            if ((t & 15) == 0) {
-                const int32_t kb = c / kFp8Block;
-                uint8_t *const word = p.scales + ((int64_t)(kb >> 2) * p.R + row) * 4;
-                word[kb & 3] = (uint8_t)e;
-                if (kb == KB - 1)
-                    for (int32_t b = (kb & 3) + 1; b < 4; ++b)
-                        word[b] = 127;
-            }
-        }
+    if constexpr (V == 4 && kRows != kRowsAligned) {
+        // two and two: the shifts leave no registers for four (6606 x 6634: 71 us, 75 with
+        // four; aligned rows take 4 together: 8192 x 8192 71.2, 71.7 with two and two)
+        const uint4 first[2] = {hv[0], hv[1]}, second[2] = {hv[2], hv[3]};
+        normalise<2>(p, row, t, T, first, rstd);
+        normalise<2>(p, row, t + 2 * T, T, second, rstd);
+    } else {
+        normalise<V>(p, row, t, T, hv, rstd);
     }
 }
 
