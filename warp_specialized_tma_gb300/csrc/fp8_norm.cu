@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <type_traits>
 
 #include "fp8_format.cuh"
 #include "fp8_kernels.h"
@@ -235,7 +236,7 @@ __device__ __forceinline__ void normalise(const NormParams &p, int64_t row, int 
 // vectors t, t + T, ..., so the 16 lanes of a half-warp always hold one block of 128.
 // Rows that are shifted alike are loaded, added and stored by 16-byte groups, and
 // turned into vectors from two neighbouring lanes' groups; otherwise unaligned rows
-// go vector by vector (5772 x 5391: 54 us, 69 that way).  Registers are capped at 64,
+// go vector by vector (5772 x 5391: 53 us, 69 that way).  Registers are capped at 64,
 // for 1024 threads an SM, or 48 where two vectors a thread fit them (8192 x 4096 with
 // a residual: 38 us, 41 with 50 registers).
 template <int V, bool kWarpRow, bool kRes, int kRows>
@@ -285,30 +286,46 @@ __global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_k
             __syncthreads();
         }
         uint4 group[V];
+        // by whole words, a case each (the row's is the same for all its threads), and
+        // half a word: only the words that a shift needs are exchanged
+        auto turn = [&](auto words) {
+            constexpr int kWords = decltype(words)::value;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            group[i] = hv[i];
-            uint4 right = make_uint4(0u, 0u, 0u, 0u);
-            if constexpr (kWarpRow) {
-                if (i + 1 < V) {
-                    const uint4 n = hv[i + 1 < V ? i + 1 : i];
-                    right = make_uint4(__shfl_sync(0xFFFFFFFFu, n.x, 0), __shfl_sync(0xFFFFFFFFu, n.y, 0),
-                                       __shfl_sync(0xFFFFFFFFu, n.z, 0), __shfl_sync(0xFFFFFFFFu, n.w, 0));
+            for (int i = 0; i < V; ++i) {
+                group[i] = hv[i];
+                uint4 right = make_uint4(0u, 0u, 0u, 0u);
+                if constexpr (kWarpRow) {
+                    if (i + 1 < V)
+                        right = hv[i + 1 < V ? i + 1 : i];
+                } else {
+                    const bool end = (warp + 1) * 32 == T;
+                    if (!end || i + 1 < V)
+                        right = edge[end ? (i + 1 < V ? i + 1 : i) : i][end ? 0 : warp + 1];
                 }
-            } else {
-                const bool end = (warp + 1) * 32 == T;
-                if (!end || i + 1 < V)
-                    right = edge[end ? (i + 1 < V ? i + 1 : i) : i][end ? 0 : warp + 1];
-            }
-            const uint32_t own[4] = {right.x, right.y, right.z, right.w};
-            uint32_t w[8] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w, 0u, 0u, 0u, 0u};
+                const uint32_t last[4] = {right.x, right.y, right.z, right.w};
+                uint32_t w[8] = {hv[i].x, hv[i].y, hv[i].z, hv[i].w};
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t n = __shfl_down_sync(0xFFFFFFFFu, w[k], 1);
-                w[4 + k] = lane == 31 ? own[k] : n;
+                for (int k = 0; k <= kWords; ++k) {
+                    if constexpr (kWarpRow) {
+                        w[4 + k] = __shfl_sync(0xFFFFFFFFu, lane == 0 ? last[k] : w[k], (lane + 1) & 31);
+                    } else {
+                        const uint32_t n = __shfl_down_sync(0xFFFFFFFFu, w[k], 1);
+                        w[4 + k] = lane == 31 ? last[k] : n;
+                    }
+                }
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    o[k] = __funnelshift_r(w[kWords + k], w[kWords + k + 1], (mis & 2u) * 8u);
+                hv[i] = make_uint4(o[0], o[1], o[2], o[3]);  // zeros stand past the row's end already
+                add_squares(hv[i], sum2);
             }
-            hv[i] = shift8(w, mis, 0, 8);  // zeros stand past the row's end already
-            add_squares(hv[i], sum2);
+        };
+        switch (mis >> 2) {
+        case 0: turn(std::integral_constant<int, 0>{}); break;
+        case 1: turn(std::integral_constant<int, 1>{}); break;
+        case 2: turn(std::integral_constant<int, 2>{}); break;
+        default: turn(std::integral_constant<int, 3>{}); break;
         }
         sum = row_sum<kWarpRow>(both(sum2), red);
         // h may be x or residual: stored after every thread's loads
@@ -345,7 +362,7 @@ __global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_k
     if (p.rstd && t == 0)
         p.rstd[row] = rstd;
     if constexpr (V == 4 && kRows != kRowsAligned) {
-        // two and two: the shifts leave no registers for four (6606 x 6634: 71 us, 75 with
+        // two and two: the shifts leave no registers for four (6606 x 6634: 71 us, 74 with
         // four; aligned rows take 4 together: 8192 x 8192 71.2, 71.7 with two and two)
         const uint4 first[2] = {hv[0], hv[1]}, second[2] = {hv[2], hv[3]};
         normalise<2>(p, row, t, T, first, rstd);
