@@ -457,17 +457,86 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_ker
                 out[(t + i * T) * 8 + j] = dw[i][j];
 }
 
-// Vector c .. c+7 of a row whose bytes lie in shared memory at `at`, `mis` bytes into
-// their first 16-byte group (shifts as in load8_bf16_shifted).
-template <bool kVec>
-__device__ __forceinline__ uint4 ring_vector(uint32_t at, uint32_t mis, int32_t c, int32_t C)
+// Eight elements from the 32 bytes at shared address `at`, which start kWords words
+// (and half a word, `by` = 16 bits) into them.
+template <int kWords>
+__device__ __forceinline__ uint4 shifted_vector(uint32_t at, uint32_t by)
 {
-    uint32_t w[8];
-    ld_shared_v4(at + (uint32_t)c * 2u, w[0], w[1], w[2], w[3]);
-    if constexpr (kVec)
-        return make_uint4(w[0], w[1], w[2], w[3]);
-    ld_shared_v4(at + (uint32_t)c * 2u + 16u, w[4], w[5], w[6], w[7]);
-    return shift8(w, mis, c, C);
+    uint32_t w[9], o[4];
+    ld_shared_v4(at, w[0], w[1], w[2], w[3]);
+    ld_shared_v4(at + 16u, w[4], w[5], w[6], w[7]);
+    w[8] = 0u;  // of a shift by four words, which are whole
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        o[k] = __funnelshift_r(w[kWords + k], w[kWords + k + 1], by);
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// A thread's vectors t, t + T, ... of a row whose bytes lie in shared memory at `at`,
+// `mis` bytes into their first 16-byte group.  A case for each shift by whole words:
+// `mis` is the same for all threads of a row.
+template <int V, bool kVec>
+__device__ __forceinline__ void ring_vectors(uint4 (&q)[V], uint32_t at, uint32_t mis, int t, int T, int32_t C)
+{
+    const uint32_t by = (mis & 2u) * 8u;
+    auto read = [&](auto words) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            q[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < C)
+                q[i] = shifted_vector<decltype(words)::value>(at + (uint32_t)c * 2u, by);
+            if (c < C && c + 8 > C) {  // what follows the row is not its
+                uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (c + 2 * k + 1 >= C)
+                        w[k] = c + 2 * k < C ? w[k] & 0xFFFFu : 0u;
+                q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+        }
+    };
+    if constexpr (kVec) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+            const int32_t c = (t + i * T) * 8;
+            q[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (c < C)
+                ld_shared_v4(at + (uint32_t)c * 2u, q[i].x, q[i].y, q[i].z, q[i].w);
+        }
+    } else {
+        switch (mis >> 2) {
+        case 0: read(std::integral_constant<int, 0>{}); break;
+        case 1: read(std::integral_constant<int, 1>{}); break;
+        case 2: read(std::integral_constant<int, 2>{}); break;
+        default: read(std::integral_constant<int, 3>{}); break;
+        }
+    }
+}
+
+// Stores the row that lies in shared memory 16 bytes behind `at` by the 16-byte groups
+// of its place in global memory, of which there may be one more than it has vectors.
+template <int V>
+__device__ __forceinline__ void store_staged(uint16_t *row, uint32_t at, int t, int T, int32_t C)
+{
+    const uint32_t mis = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+    const int32_t back = (int32_t)(mis >> 1);
+    const uint32_t by = (mis & 2u) * 8u;
+    auto write = [&](auto words) {
+#pragma unroll
+        for (int i = 0; i <= V; ++i) {
+            const int32_t v = t + i * T, first = v * 8 - back;
+            if (first < C)
+                store_group(row, first, C, shifted_vector<decltype(words)::value>(at + (uint32_t)v * 16u, by));
+        }
+    };
+    switch ((16u - mis) >> 2) {
+    case 0: write(std::integral_constant<int, 0>{}); break;
+    case 1: write(std::integral_constant<int, 1>{}); break;
+    case 2: write(std::integral_constant<int, 2>{}); break;
+    case 3: write(std::integral_constant<int, 3>{}); break;
+    default: write(std::integral_constant<int, 4>{}); break;
+    }
 }
 
 // A group of T threads (a multiple of 32) takes rows in a stride of all groups,
@@ -478,7 +547,10 @@ __device__ __forceinline__ uint4 ring_vector(uint32_t at, uint32_t mis, int32_t 
 // 4104: 42 us with one row ahead in registers).  A group's first thread refills a
 // slot after the barrier in the next row's reduction, which every thread reaches
 // when it is done with the slot.  Rows that are not 16-byte aligned are copied
-// with the rest of their first and last 16-byte groups.  The CTAs' sums meet in
+// with the rest of their first and last 16-byte groups, and their dx is left in shared
+// memory, two rows of it, from which it is stored by 16-byte groups after that barrier
+// (8000 x 4001: 65 us, 81 if lanes exchange their vectors; with several groups to a
+// CTA the exchange is faster, 8000 x 901 28 us against 37).  The CTAs' sums meet in
 // `partials`, one row of C floats each, which column_sum_kernel adds in a fixed
 // order.
 template <int V, bool kDres, bool kVec, bool kGroups, int kThreads>
@@ -490,6 +562,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     __shared__ float red[2][32];
     __shared__ __align__(8) uint64_t full[kRingMax];
     constexpr int kRows = kDres ? 3 : 2;
+    constexpr bool kStage = !kVec && !kGroups;
     const int T = kGroups ? group_threads : (int)blockDim.x;
     const int groups = kGroups ? (int)blockDim.x / T : 1, g = kGroups ? (int)threadIdx.x / T : 0;
     const int t = (int)threadIdx.x - g * T, lane = t & 31, warps = T >> 5;
@@ -497,6 +570,9 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     const uint32_t slot_bytes = pitch * kRows;
     const uint32_t base = smem_u32(ring) + (uint32_t)(g * slots) * slot_bytes;
     const uint32_t bars = smem_u32(full) + 8u * (uint32_t)(g * slots);
+    const uint32_t stage_bytes = pitch + 16u;
+    const uint32_t staging = smem_u32(ring) + (uint32_t)(groups * slots) * slot_bytes + (uint32_t)g * 2u * stage_bytes;
+    uint32_t staged = 0;  // which of the two
     const float inv = 1.f / (float)C;
     const int64_t step = (int64_t)gridDim.x * groups;
     const int64_t row0 = (int64_t)blockIdx.x * groups + g;
@@ -560,14 +636,10 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         const uint32_t at = base + (uint32_t)s * slot_bytes;
         uint4 dy[V], h[V];
         float dot = 0.f;
+        ring_vectors<V, kVec>(dy, at, mis(0, row), t, T, C);
+        ring_vectors<V, kVec>(h, at + pitch, mis(1, row), t, T, C);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int32_t c = (t + i * T) * 8;
-            dy[i] = h[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < C) {
-                dy[i] = ring_vector<kVec>(at, mis(0, row), c, C);
-                h[i] = ring_vector<kVec>(at + pitch, mis(1, row), c, C);
-            }
             float d[8], x[8];
             unpack8(dy[i], d);
             unpack8(h[i], x);
@@ -601,7 +673,14 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         }
         if (t == 0 && refill)
             fill(before);
+        if constexpr (kStage) {
+            if (row != row0)
+                store_staged<V>(p.dx + (row - step) * p.lddx, staging + (staged ^ 1u) * stage_bytes, t, T, C);
+        }
         const float mean = dot * inv;
+        uint4 dres[V];
+        if constexpr (kDres)
+            ring_vectors<V, kVec>(dres, at + 2u * pitch, mis(2, row), t, T, C);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
@@ -609,10 +688,17 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
             unpack8(dy[i], d);
             unpack8(h[i], x);
             if constexpr (kDres)
-                unpack8(c < C ? ring_vector<kVec>(at + 2u * pitch, mis(2, row), c, C) : make_uint4(0u, 0u, 0u, 0u), r);
+                unpack8(dres[i], r);
             backward_values<kDres>(d, x, w[i], r, rstd, mean);
-            store8_row(p.dx + row * p.lddx, c, C, kVec, pack8(d));
+            const uint4 q = pack8(d);
+            if constexpr (kStage) {
+                if (c < C)
+                    st_shared_v4(staging + staged * stage_bytes + 16u + 2u * (uint32_t)c, q.x, q.y, q.z, q.w);
+            } else {
+                store8_row(p.dx + row * p.lddx, c, C, kVec, q);
+            }
         }
+        staged ^= 1u;
         rstd = next_rstd;
         before = s;
         refill = row + slots * step < p.R;
@@ -620,6 +706,12 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
             s = 0;
             ph ^= 1u;
         }
+    }
+    if constexpr (kStage) {
+        __syncthreads();
+        if (row0 < p.R)
+            store_staged<V>(p.dx + (row0 + (p.R - 1 - row0) / step * step) * p.lddx,
+                            staging + (staged ^ 1u) * stage_bytes, t, T, C);
     }
     // a wait that ran out (its copies never landed): dweight says so
     if (!ok)
@@ -831,13 +923,15 @@ int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream
     if (s.ring) {
         const int64_t pitch = vec ? (int64_t)p.C * 2 : ((int64_t)p.C * 2 + 15) / 16 * 16 + 16;
         const int64_t slot = pitch * (p.dres ? 3 : 2);
-        const int slots = (int)std::min<int64_t>(kRingBytes / s.blocks / s.groups / slot, kRingMax / s.groups);
+        const int64_t staging = vec || s.groups > 1 ? 0 : 2 * (pitch + 16);
+        const int slots =
+            (int)std::min<int64_t>((kRingBytes / s.blocks / s.groups - staging) / slot, kRingMax / s.groups);
         const int64_t sums = (int64_t)(s.groups - 1) * p.C * (int64_t)sizeof(float);
         auto fn = p.dres ? (vec ? backward_ring_fn<true, true>(s) : backward_ring_fn<true, false>(s))
                          : (vec ? backward_ring_fn<false, true>(s) : backward_ring_fn<false, false>(s));
         rc = cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
         if (rc == cudaSuccess)
-            rc = launch(fn, grid, s.T * s.groups, (size_t)std::max<int64_t>(slots * slot * s.groups, sums), stream, p,
+            rc = launch(fn, grid, s.T * s.groups, (size_t)std::max<int64_t>((slots * slot + staging) * s.groups, sums), stream, p,
                         (int32_t)s.T, (int32_t)slots, (uint32_t)pitch);
     } else {
         auto fn = p.dres ? (vec ? backward_wide_fn<true, true>(s) : backward_wide_fn<true, false>(s))
