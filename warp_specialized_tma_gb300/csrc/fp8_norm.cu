@@ -549,8 +549,8 @@ __device__ __forceinline__ void store_staged(uint16_t *row, uint32_t at, int t, 
 // when it is done with the slot.  Rows that are not 16-byte aligned are copied
 // with the rest of their first and last 16-byte groups, and their dx is left in shared
 // memory, two rows of it, from which it is stored by 16-byte groups after that barrier
-// (8000 x 4001: 65 us, 81 if lanes exchange their vectors; with several groups to a
-// CTA the exchange is faster, 8000 x 901 28 us against 37).  The CTAs' sums meet in
+// (8000 x 4001: 58 us, 73 if lanes exchange their vectors; with several groups to a
+// CTA the exchange is as good, 5211 x 1363 23.5 us against 25.3).  The CTAs' sums meet in
 // `partials`, one row of C floats each, which column_sum_kernel adds in a fixed
 // order.
 template <int V, bool kDres, bool kVec, bool kGroups, int kThreads>
@@ -574,8 +574,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     const uint32_t staging = smem_u32(ring) + (uint32_t)(groups * slots) * slot_bytes + (uint32_t)g * 2u * stage_bytes;
     uint32_t staged = 0;  // which of the two
     const float inv = 1.f / (float)C;
-    const int64_t step = (int64_t)gridDim.x * groups;
-    const int64_t row0 = (int64_t)blockIdx.x * groups + g;
+    const uint32_t R = (uint32_t)p.R, step = gridDim.x * (uint32_t)groups;  // sums of rows fit 32 bits without a sign
+    const uint32_t row0 = blockIdx.x * (uint32_t)groups + (uint32_t)g;
     if (t == 0) {
         for (int s = 0; s < slots; ++s)
             mbar_init(bars + 8u * s, 1);
@@ -587,16 +587,13 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
 
     const uint16_t *const src[3] = {p.dy, p.h, p.dres};
     const int64_t ld[3] = {p.lddy, p.ldh, p.lddr};
-    // the first thread's place in the rows to come: it steps from one to the next
-    uintptr_t from[kRows];
-#pragma unroll
-    for (int k = 0; k < kRows; ++k)
-        from[k] = reinterpret_cast<uintptr_t>(src[k] + row0 * ld[k]);
-    auto fill = [&](int s) {
+    auto fill = [&](int s, uint32_t row) {
         const uint32_t bar = bars + 8u * s;
+        uintptr_t from[kRows];
         uint32_t bytes[kRows], all = 0;
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
+            from[k] = reinterpret_cast<uintptr_t>(src[k] + row * ld[k]);
             const uint32_t end = ((uint32_t)(from[k] & 15u) + 2u * (uint32_t)C + 15u) & ~15u;
             bytes[k] = kVec ? 2u * (uint32_t)C : end;
             all += bytes[k];
@@ -606,15 +603,15 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         for (int k = 0; k < kRows; ++k) {
             bulk_load(base + (uint32_t)s * slot_bytes + (uint32_t)k * pitch,
                       reinterpret_cast<const void *>(from[k] & ~(uintptr_t)15), bytes[k], bar);
-            from[k] += (uintptr_t)(2 * step * ld[k]);
         }
     };
-    auto mis = [&](int k, int64_t row) {
-        return kVec ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(src[k] + row * ld[k]) & 15u);
+    auto mis = [&](int k, uint32_t row) {  // of the address, whose lowest bits need no more than 32
+        return kVec ? 0u
+                    : ((uint32_t)reinterpret_cast<uintptr_t>(src[k]) + 2u * row * (uint32_t)ld[k]) & 15u;
     };
     if (t == 0)
-        for (int s = 0; s < slots && row0 + s * step < p.R; ++s)
-            fill(s);
+        for (int s = 0; s < slots && row0 + (uint32_t)s * step < R; ++s)
+            fill(s, row0 + (uint32_t)s * step);
 
     float dw[V][8], w[V][8];
 #pragma unroll
@@ -624,14 +621,13 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         for (int j = 0; j < 8; ++j)
             dw[i][j] = 0.f;
     }
-    float rstd = row0 < p.R ? p.rstd[row0] : 0.f;
+    float rstd = row0 < R ? p.rstd[row0] : 0.f;
     int s = 0;
     uint32_t ph = 0, buf = 0;
     bool ok = true;
-    bool refill = false;  // a row is left for the slot before this one
-    int before = 0;
-    for (int64_t row = row0; row < p.R; row += step) {
-        const float next_rstd = row + step < p.R ? p.rstd[row + step] : 0.f;
+    int before = -1;  // the slot of the row before, if a row is left for it
+    for (uint32_t row = row0; row < R; row += step) {
+        const float next_rstd = row + step < R ? p.rstd[row + step] : 0.f;
         ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
         const uint32_t at = base + (uint32_t)s * slot_bytes;
         uint4 dy[V], h[V];
@@ -671,11 +667,11 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         } else {
             __syncwarp();
         }
-        if (t == 0 && refill)
-            fill(before);
+        if (t == 0 && before >= 0)
+            fill(before, row + (uint32_t)(slots - 1) * step);
         if constexpr (kStage) {
             if (row != row0)
-                store_staged<V>(p.dx + (row - step) * p.lddx, staging + (staged ^ 1u) * stage_bytes, t, T, C);
+                store_staged<V>(p.dx + (int64_t)(row - step) * p.lddx, staging + (staged ^ 1u) * stage_bytes, t, T, C);
         }
         const float mean = dot * inv;
         uint4 dres[V];
@@ -695,13 +691,12 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
                 if (c < C)
                     st_shared_v4(staging + staged * stage_bytes + 16u + 2u * (uint32_t)c, q.x, q.y, q.z, q.w);
             } else {
-                store8_row(p.dx + row * p.lddx, c, C, kVec, q);
+                store8_row(p.dx + (int64_t)row * p.lddx, c, C, kVec, q);
             }
         }
         staged ^= 1u;
         rstd = next_rstd;
-        before = s;
-        refill = row + slots * step < p.R;
+        before = row + (uint32_t)slots * step < R ? s : -1;
         if (++s == slots) {
             s = 0;
             ph ^= 1u;
@@ -709,8 +704,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     }
     if constexpr (kStage) {
         __syncthreads();
-        if (row0 < p.R)
-            store_staged<V>(p.dx + (row0 + (p.R - 1 - row0) / step * step) * p.lddx,
+        if (row0 < R)
+            store_staged<V>(p.dx + (int64_t)(row0 + (R - 1 - row0) / step * step) * p.lddx,
                             staging + (staged ^ 1u) * stage_bytes, t, T, C);
     }
     // a wait that ran out (its copies never landed): dweight says so
