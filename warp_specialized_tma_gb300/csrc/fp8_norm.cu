@@ -39,14 +39,6 @@ __device__ __forceinline__ float row_sum(float v, float *red)
     }
 }
 
-__device__ __forceinline__ void load8_weight(const void *w, int fp32, int32_t c, int32_t C, bool vec, float (&f)[8])
-{
-    if (fp32)
-        load8_float(static_cast<const float *>(w), c, C, vec, f);
-    else
-        unpack8(load8_bf16(static_cast<const uint16_t *>(w), c, C, vec), f);
-}
-
 __device__ __forceinline__ void load8_weight(const void *w, int fp32, int32_t c, int32_t C, bool vec, uint64_t (&f)[4])
 {
     if (fp32) {
@@ -372,22 +364,52 @@ __global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_k
     }
 }
 
-// d <- the gradient of 8 elements: d holds dy, x h, r dresidual.
-template <bool kDres>
-__device__ __forceinline__ void backward_values(float (&d)[8], const float (&x)[8], const float (&w)[8],
-                                                const float (&r)[8], float rstd, float mean)
+// The sums over 8 elements, two at a time: dot += dy w n, dw += dy n with n = h rstd.
+__device__ __forceinline__ void backward_sums(uint4 dy, uint4 h, const uint64_t (&w)[4], uint64_t rstd2, uint64_t &dot,
+                                              uint64_t (&dw)[4])
 {
+    uint64_t d[4], x[4];
+    unpack8_pairs(dy, d);
+    unpack8_pairs(h, x);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        d[j] = rstd * (d[j] * w[j] - x[j] * rstd * mean);
-        if constexpr (kDres)
-            d[j] += r[j];
+    for (int j = 0; j < 4; ++j) {
+        const uint64_t n = mul_f32x2(x[j], rstd2);
+        dot = fma_f32x2(mul_f32x2(d[j], w[j]), n, dot);
+        dw[j] = fma_f32x2(d[j], n, dw[j]);
     }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&d)[8])
+// The gradient of 8 elements: rstd (dy w - n mean) + dresidual.
+template <bool kDres>
+__device__ __forceinline__ uint4 backward_values(uint4 dy, uint4 h, const uint64_t (&w)[4], uint4 dres, uint64_t rstd2,
+                                                 uint64_t minus_mean2)
 {
-    return make_uint4(bf16_pair(d[0], d[1]), bf16_pair(d[2], d[3]), bf16_pair(d[4], d[5]), bf16_pair(d[6], d[7]));
+    uint64_t d[4], x[4], r[4];
+    unpack8_pairs(dy, d);
+    unpack8_pairs(h, x);
+    if constexpr (kDres)
+        unpack8_pairs(dres, r);
+    uint32_t o[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        d[j] = fma_f32x2(mul_f32x2(x[j], rstd2), minus_mean2, mul_f32x2(d[j], w[j]));
+        if constexpr (kDres)
+            d[j] = fma_f32x2(d[j], rstd2, r[j]);
+        else
+            d[j] = mul_f32x2(d[j], rstd2);
+        float lo, hi;
+        f32x2_parts(d[j], lo, hi);
+        o[j] = bf16_pair(lo, hi);
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
+// Sums of 8 columns as floats.
+__device__ __forceinline__ void unpair8(const uint64_t (&v)[4], float (&f)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        f32x2_parts(v[j], f[2 * j], f[2 * j + 1]);
 }
 
 constexpr int kBackwardThreads = 512;
@@ -406,12 +428,12 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_ker
     const int T = (int)blockDim.x, t = (int)threadIdx.x;
     const int32_t C = p.C;
     const float inv = 1.f / (float)C;
-    float dw[V][8];
+    uint64_t dw[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dw[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j)
+            dw[i][j] = 0u;
     for (int64_t row = blockIdx.x; row < p.R; row += gridDim.x) {
         uint4 dy[V], h[V];
 #pragma unroll
@@ -420,41 +442,38 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_ker
             h[i] = load8_row(p.h + row * p.ldh, (t + i * T) * 8, C, kVec);
         }
         const float rstd = p.rstd[row];
-        float dot = 0.f;
+        const uint64_t rstd2 = f32x2(rstd, rstd);
+        uint64_t dot = 0u;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            float d[8], x[8], w[8];
-            unpack8(dy[i], d);
-            unpack8(h[i], x);
+            uint64_t w[4];
             load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = x[j] * rstd;
-                dot = fmaf(d[j] * w[j], n, dot);
-                dw[i][j] = fmaf(d[j], n, dw[i][j]);
-            }
+            backward_sums(dy[i], h[i], w, rstd2, dot, dw[i]);
         }
-        const float mean = row_sum<false>(dot, red) * inv;
+        const float mean = row_sum<false>(both(dot), red) * inv;
+        const uint64_t minus_mean2 = f32x2(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            float d[8], x[8], w[8], r[8];
-            unpack8(dy[i], d);
-            unpack8(h[i], x);
+            uint64_t w[4];
             load8_weight(p.weight, p.w_fp32, c, C, p.w_vec, w);
+            uint4 dres = make_uint4(0u, 0u, 0u, 0u);
             if constexpr (kDres)
-                unpack8(load8_row(p.dres + row * p.lddr, c, C, kVec), r);
-            backward_values<kDres>(d, x, w, r, rstd, mean);
-            store8_row(p.dx + row * p.lddx, c, C, kVec, pack8(d));
+                dres = load8_row(p.dres + row * p.lddr, c, C, kVec);
+            store8_row(p.dx + row * p.lddx, c, C, kVec,
+                       backward_values<kDres>(dy[i], h[i], w, dres, rstd2, minus_mean2));
         }
     }
     float *const out = p.partials + (int64_t)blockIdx.x * C;
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+        float f[8];
+        unpair8(dw[i], f);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
             if ((t + i * T) * 8 + j < C)
-                out[(t + i * T) * 8 + j] = dw[i][j];
+                out[(t + i * T) * 8 + j] = f[j];
+    }
 }
 
 // Eight elements from the 32 bytes at shared address `at`, which start kWords words
@@ -549,8 +568,8 @@ __device__ __forceinline__ void store_staged(uint16_t *row, uint32_t at, int t, 
 // when it is done with the slot.  Rows that are not 16-byte aligned are copied
 // with the rest of their first and last 16-byte groups, and their dx is left in shared
 // memory, two rows of it, from which it is stored by 16-byte groups after that barrier
-// (8000 x 4001: 58 us, 73 if lanes exchange their vectors; with several groups to a
-// CTA the exchange is as good, 5211 x 1363 23.5 us against 25.3).  The CTAs' sums meet in
+// (8000 x 4001 from 81 us, with lanes that exchange their vectors, to 65; with several
+// groups to a CTA the exchange is as good, 5211 x 1363 23.5 us against 25.3).  The CTAs' sums meet in
 // `partials`, one row of C floats each, which column_sum_kernel adds in a fixed
 // order.
 template <int V, bool kDres, bool kVec, bool kGroups, int kThreads>
@@ -613,13 +632,13 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         for (int s = 0; s < slots && row0 + (uint32_t)s * step < R; ++s)
             fill(s, row0 + (uint32_t)s * step);
 
-    float dw[V][8], w[V][8];
+    uint64_t dw[V][4], w[V][4];
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w[i]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-            dw[i][j] = 0.f;
+        for (int j = 0; j < 4; ++j)
+            dw[i][j] = 0u;
     }
     float rstd = row0 < R ? p.rstd[row0] : 0.f;
     int s = 0;
@@ -631,23 +650,15 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
         const uint32_t at = base + (uint32_t)s * slot_bytes;
         uint4 dy[V], h[V];
-        float dot = 0.f;
         ring_vectors<V, kVec>(dy, at, mis(0, row), t, T, C);
         ring_vectors<V, kVec>(h, at + pitch, mis(1, row), t, T, C);
+        const uint64_t rstd2 = f32x2(rstd, rstd);
+        uint64_t dot2 = 0u;
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            float d[8], x[8];
-            unpack8(dy[i], d);
-            unpack8(h[i], x);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float n = x[j] * rstd;
-                dot = fmaf(d[j] * w[i][j], n, dot);
-                dw[i][j] = fmaf(d[j], n, dw[i][j]);
-            }
-        }
+        for (int i = 0; i < V; ++i)
+            backward_sums(dy[i], h[i], w[i], rstd2, dot2, dw[i]);
         // one barrier a row: the sums alternate between two buffers
-        dot = warp_sum(dot);
+        float dot = warp_sum(both(dot2));
         if (!kGroups || warps > 1) {
             float *const mine = red[buf] + g * warps;
             if (lane == 0)
@@ -673,20 +684,14 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
             if (row != row0)
                 store_staged<V>(p.dx + (int64_t)(row - step) * p.lddx, staging + (staged ^ 1u) * stage_bytes, t, T, C);
         }
-        const float mean = dot * inv;
+        const uint64_t minus_mean2 = f32x2(-dot * inv, -dot * inv);
         uint4 dres[V];
         if constexpr (kDres)
             ring_vectors<V, kVec>(dres, at + 2u * pitch, mis(2, row), t, T, C);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            float d[8], x[8], r[8];
-            unpack8(dy[i], d);
-            unpack8(h[i], x);
-            if constexpr (kDres)
-                unpack8(dres[i], r);
-            backward_values<kDres>(d, x, w[i], r, rstd, mean);
-            const uint4 q = pack8(d);
+            const uint4 q = backward_values<kDres>(dy[i], h[i], w[i], dres[i], rstd2, minus_mean2);
             if constexpr (kStage) {
                 if (c < C)
                     st_shared_v4(staging + staged * stage_bytes + 16u + 2u * (uint32_t)c, q.x, q.y, q.z, q.w);
@@ -710,16 +715,20 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     }
     // a wait that ran out (its copies never landed): dweight says so
     if (!ok)
-        dw[0][0] = __int_as_float(0x7FFFFFFF);
+        dw[0][0] = f32x2(__int_as_float(0x7FFFFFFF), 0.f);
 
     float *const out = p.partials + (int64_t)blockIdx.x * C;
+    float f[V][8];
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        unpair8(dw[i], f[i]);
     if constexpr (!kGroups && kVec) {
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
             if (c < C) {
-                *reinterpret_cast<float4 *>(out + c) = make_float4(dw[i][0], dw[i][1], dw[i][2], dw[i][3]);
-                *reinterpret_cast<float4 *>(out + c + 4) = make_float4(dw[i][4], dw[i][5], dw[i][6], dw[i][7]);
+                *reinterpret_cast<float4 *>(out + c) = make_float4(f[i][0], f[i][1], f[i][2], f[i][3]);
+                *reinterpret_cast<float4 *>(out + c + 4) = make_float4(f[i][4], f[i][5], f[i][6], f[i][7]);
             }
         }
         return;
@@ -733,7 +742,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if ((t + i * T) * 8 + j < C)
-                    sums[(g - 1) * C + (t + i * T) * 8 + j] = dw[i][j];
+                    sums[(g - 1) * C + (t + i * T) * 8 + j] = f[i][j];
     }
     __syncthreads();
     if (g == 0) {
@@ -743,7 +752,7 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
             for (int j = 0; j < 8; ++j) {
                 const int32_t c = (t + i * T) * 8 + j;
                 if (c < C) {
-                    float v = dw[i][j];
+                    float v = f[i][j];
                     for (int k = 0; k + 1 < groups; ++k)
                         v += sums[k * C + c];
                     out[c] = v;
