@@ -480,6 +480,15 @@ def test_rmsnorm_backward(shape, wdtype, residual):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+# several rows to each group of threads, in every layout of the gradient's rows: aligned and
+# not, a warp's, part of a CTA's and a CTA's, up to four vectors of 8 columns a thread
+@pytest.mark.parametrize("residual", [False, True], ids=["plain", "residual"])
+@pytest.mark.parametrize("shape", [(6000, 75), (3000, 901), (2500, 1808), (1000, 4001), (700, 4500), (500, 6634),
+                                   (470, 9001), (470, 12288), (500, 16383)], ids=lambda s: "x".join(map(str, s)))
+def test_rmsnorm_backward_many_rows(shape, residual):
+    test_rmsnorm_backward(shape, torch.float32, residual)
+
+
 def test_rmsnorm_backward_against_differences():
     R, C, eps = 3, 96, 1e-6
     h, _, w = norm_inputs(R, C, 11, torch.float32, False)

@@ -416,9 +416,9 @@ constexpr int kBackwardThreads = 512;
 constexpr int kRingMax = 64;               // slots of a CTA's rings of rows
 constexpr int kRingBytes = 208 * 1024;     // of an SM's shared memory, shared by its CTAs
 
-// Rows of more than 16 vectors a thread of the ring kernel below (C > 8192): a CTA
-// takes rows in a stride of the grid and keeps its threads' share of dweight in
-// registers.
+// Rows of more than four vectors a thread (C > 16384), of which the ring of the kernel
+// below would not hold two: a CTA takes rows in a stride of the grid and keeps its
+// threads' share of dweight in registers.
 template <int V, bool kDres, bool kVec>
 __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_kernel(const NormBackwardParams p)
 {
@@ -572,6 +572,12 @@ __device__ __forceinline__ void store_staged(uint16_t *row, uint32_t at, int t, 
 // groups to a CTA the exchange is as good, 5211 x 1363 23.5 us against 25.3).  The CTAs' sums meet in
 // `partials`, one row of C floats each, which column_sum_kernel adds in a fixed
 // order.
+//
+// HBM-bound where rows are aligned and long: 8192 x 8192 with dresidual 80.5 us, 6.7
+// TB/s.  Four vectors a thread (C from 8193) read dy and h twice from shared memory, for
+// their registers: 4096 x 8200 47 us, 127 without the ring; 4096 x 16384 99 us, 146
+// without it (two slots leave gaps).  Short rows are bound by their instructions and
+// the barrier in each: 8192 x 1024 19 us, 3.5 TB/s; 8000 x 1810 40 us, 2.9 TB/s.
 template <int V, bool kDres, bool kVec, bool kGroups, int kThreads>
 __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     rmsnorm_backward_ring_kernel(const NormBackwardParams p, const int32_t group_threads, const int32_t slots,
@@ -581,7 +587,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     __shared__ float red[2][32];
     __shared__ __align__(8) uint64_t full[kRingMax];
     constexpr int kRows = kDres ? 3 : 2;
-    constexpr bool kStage = !kVec && !kGroups;
+    constexpr bool kStage = !kVec && !kGroups && V <= 2;
+    constexpr bool kHold = V <= 2;  // dy and h stay in registers between a row's two passes, else are read again
     const int T = kGroups ? group_threads : (int)blockDim.x;
     const int groups = kGroups ? (int)blockDim.x / T : 1, g = kGroups ? (int)threadIdx.x / T : 0;
     const int t = (int)threadIdx.x - g * T, lane = t & 31, warps = T >> 5;
@@ -649,14 +656,21 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         const float next_rstd = row + step < R ? p.rstd[row + step] : 0.f;
         ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
         const uint32_t at = base + (uint32_t)s * slot_bytes;
-        uint4 dy[V], h[V];
-        ring_vectors<V, kVec>(dy, at, mis(0, row), t, T, C);
-        ring_vectors<V, kVec>(h, at + pitch, mis(1, row), t, T, C);
+        uint4 dy[kHold ? V : 1], h[kHold ? V : 1];
         const uint64_t rstd2 = f32x2(rstd, rstd);
         uint64_t dot2 = 0u;
+        if constexpr (kHold) {
+            ring_vectors<V, kVec>(dy, at, mis(0, row), t, T, C);
+            ring_vectors<V, kVec>(h, at + pitch, mis(1, row), t, T, C);
+        }
 #pragma unroll
-        for (int i = 0; i < V; ++i)
-            backward_sums(dy[i], h[i], w[i], rstd2, dot2, dw[i]);
+        for (int i = 0; i < V; ++i) {
+            if constexpr (!kHold) {
+                ring_vectors<1, kVec>(dy, at, mis(0, row), t + i * T, T, C);
+                ring_vectors<1, kVec>(h, at + pitch, mis(1, row), t + i * T, T, C);
+            }
+            backward_sums(dy[kHold ? i : 0], h[kHold ? i : 0], w[i], rstd2, dot2, dw[i]);
+        }
         // one barrier a row: the sums alternate between two buffers
         float dot = warp_sum(both(dot2));
         if (!kGroups || warps > 1) {
@@ -685,13 +699,20 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
                 store_staged<V>(p.dx + (int64_t)(row - step) * p.lddx, staging + (staged ^ 1u) * stage_bytes, t, T, C);
         }
         const uint64_t minus_mean2 = f32x2(-dot * inv, -dot * inv);
-        uint4 dres[V];
-        if constexpr (kDres)
+        uint4 dres[kHold ? V : 1];
+        if constexpr (kDres && kHold)
             ring_vectors<V, kVec>(dres, at + 2u * pitch, mis(2, row), t, T, C);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int32_t c = (t + i * T) * 8;
-            const uint4 q = backward_values<kDres>(dy[i], h[i], w[i], dres[i], rstd2, minus_mean2);
+            if constexpr (!kHold) {
+                ring_vectors<1, kVec>(dy, at, mis(0, row), t + i * T, T, C);
+                ring_vectors<1, kVec>(h, at + pitch, mis(1, row), t + i * T, T, C);
+                if constexpr (kDres)
+                    ring_vectors<1, kVec>(dres, at + 2u * pitch, mis(2, row), t + i * T, T, C);
+            }
+            const int v = kHold ? i : 0;
+            const uint4 q = backward_values<kDres>(dy[v], h[v], w[i], dres[v], rstd2, minus_mean2);
             if constexpr (kStage) {
                 if (c < C)
                     st_shared_v4(staging + staged * stage_bytes + 16u + 2u * (uint32_t)c, q.x, q.y, q.z, q.w);
@@ -864,7 +885,7 @@ BackwardSplit split_backward(int64_t R, int64_t C, int num_sms)
     while ((nv + s.V - 1) / s.V > kBackwardThreads)
         s.V *= 2;
     s.T = (int)(((nv + s.V - 1) / s.V + 31) / 32 * 32);
-    s.ring = s.V <= 2;
+    s.ring = s.V <= 4;
     s.groups = std::min(kBackwardThreads / s.T, s.T == 32 ? 16 : 15);  // barriers 1..15
     // few rows: on as many SMs as there are rows for
     s.groups = (int)std::min<int64_t>(s.groups, std::max<int64_t>(1, R / num_sms));
@@ -878,15 +899,11 @@ auto backward_ring_fn(const BackwardSplit &s)
     constexpr int kT = kBackwardThreads;
     if (s.groups > 1)
         return &rmsnorm_backward_ring_kernel<1, kDres, kVec, true, kT>;
+    if (s.V == 4)
+        return &rmsnorm_backward_ring_kernel<4, kDres, kVec, false, kT>;
     return s.V == 1 ? &rmsnorm_backward_ring_kernel<1, kDres, kVec, false, kT>
                     : (s.T <= 320 ? &rmsnorm_backward_ring_kernel<2, kDres, kVec, false, 320>
                                   : &rmsnorm_backward_ring_kernel<2, kDres, kVec, false, kT>);
-}
-
-template <bool kDres, bool kVec>
-auto backward_wide_fn(const BackwardSplit &s)
-{
-    return s.V == 4 ? &rmsnorm_backward_wide_kernel<4, kDres, kVec> : &rmsnorm_backward_wide_kernel<8, kDres, kVec>;
 }
 
 // Rows of 8 vectors a thread end at 512 * 8 * 8 columns, the limit of the API.
@@ -927,7 +944,7 @@ int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream
     if (s.ring) {
         const int64_t pitch = vec ? (int64_t)p.C * 2 : ((int64_t)p.C * 2 + 15) / 16 * 16 + 16;
         const int64_t slot = pitch * (p.dres ? 3 : 2);
-        const int64_t staging = vec || s.groups > 1 ? 0 : 2 * (pitch + 16);
+        const int64_t staging = vec || s.groups > 1 || s.V == 4 ? 0 : 2 * (pitch + 16);  // V = 4: room for two slots
         const int slots =
             (int)std::min<int64_t>((kRingBytes / s.blocks / s.groups - staging) / slot, kRingMax / s.groups);
         const int64_t sums = (int64_t)(s.groups - 1) * p.C * (int64_t)sizeof(float);
@@ -938,8 +955,10 @@ int launch_rmsnorm_backward(const NormBackwardParams &p, int num_sms, cudaStream
             rc = launch(fn, grid, s.T * s.groups, (size_t)std::max<int64_t>((slots * slot + staging) * s.groups, sums), stream, p,
                         (int32_t)s.T, (int32_t)slots, (uint32_t)pitch);
     } else {
-        auto fn = p.dres ? (vec ? backward_wide_fn<true, true>(s) : backward_wide_fn<true, false>(s))
-                         : (vec ? backward_wide_fn<false, true>(s) : backward_wide_fn<false, false>(s));
+        auto fn = p.dres ? (vec ? &rmsnorm_backward_wide_kernel<8, true, true>
+                                : &rmsnorm_backward_wide_kernel<8, true, false>)
+                         : (vec ? &rmsnorm_backward_wide_kernel<8, false, true>
+                                : &rmsnorm_backward_wide_kernel<8, false, false>);
         rc = launch(fn, grid, s.T, 0, stream, p);
     }
     if (rc != cudaSuccess)
