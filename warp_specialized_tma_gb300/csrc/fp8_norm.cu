@@ -22,8 +22,9 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
-// Sum over the threads of a row: the warp's when the row is a warp's, else the CTA's.
-template <bool kWarpRow>
+// Sum over the threads of a row: the warp's when the row is a warp's, else the CTA's,
+// which may have more rows after this one (kAgain).
+template <bool kWarpRow, bool kAgain>
 __device__ __forceinline__ float row_sum(float v, float *red)
 {
     v = warp_sum(v);
@@ -31,7 +32,8 @@ __device__ __forceinline__ float row_sum(float v, float *red)
         return v;
     } else {
         const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, n = (int)blockDim.x >> 5;
-        __syncthreads();  // the previous row's sums have been read
+        if constexpr (kAgain)
+            __syncthreads();  // the previous row's sums have been read
         if (lane == 0)
             red[warp] = v;
         __syncthreads();
@@ -319,7 +321,7 @@ __global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_k
         case 2: turn(std::integral_constant<int, 2>{}); break;
         default: turn(std::integral_constant<int, 3>{}); break;
         }
-        sum = row_sum<kWarpRow>(both(sum2), red);
+        sum = row_sum<kWarpRow, false>(both(sum2), red);
         // h may be x or residual: stored after every thread's loads
         if constexpr (kRes) {
 #pragma unroll
@@ -348,7 +350,7 @@ __global__ void __maxnreg__(V == 2 && kRows == kRowsAligned ? 48 : 64) rmsnorm_k
             if constexpr (kRes)
                 store8_row(p.h + row * p.ldh, (t + i * T) * 8, C, vec, hv[i]);
         }
-        sum = row_sum<kWarpRow>(both(sum2), red);
+        sum = row_sum<kWarpRow, false>(both(sum2), red);
     }
     const float rstd = __frsqrt_rn(sum * p.inv_c + p.eps);
     if (p.rstd && t == 0)
@@ -450,7 +452,7 @@ __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_ker
             load8_weight(p.weight, p.w_fp32, (t + i * T) * 8, C, p.w_vec, w);
             backward_sums(dy[i], h[i], w, rstd2, dot, dw[i]);
         }
-        const float mean = row_sum<false>(both(dot), red) * inv;
+        const float mean = row_sum<false, true>(both(dot), red) * inv;
         const uint64_t minus_mean2 = f32x2(-mean, -mean);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
