@@ -246,7 +246,10 @@ int resident_clusters(const fp8_gemm *h, const Plan &pl, const Tiling &t, int c)
 // operands' time in HBM, if longer; then the epilogue and the exchange between a
 // split tile's pieces.  The exchanges' costs are fitted to measurements: through a
 // cluster 8x700x1500 loses 0.5 us by saving 8 of 12 stages; through global memory
-// 1x8192x8192 spends 4 us, 1000x1000x8000 in four pieces of 224 columns 14 us.  Fills in how the tiles are shared out.
+// 1x8192x8192 spends 4 us, 1000x1000x8000 in four pieces of 224 columns 14 us.  Where all
+// ranks of a cluster fetch at once, its size costs little (with the other formula for
+// these too 128x1024x4096 takes 9.3 us, not 8.5, 934x174x5658 10.7, not 9.6).
+// Fills in how the tiles are shared out.
 double tiling_cost(const fp8_gemm *h, const Plan &pl, Tiling &t)
 {
     const int64_t rows = t.transposed ? pl.N : pl.M, cols = t.transposed ? pl.M : pl.N;
@@ -266,8 +269,11 @@ double tiling_cost(const fp8_gemm *h, const Plan &pl, Tiling &t)
         // each tile shared by a cluster of CTAs
         const int64_t c = std::min<int64_t>({most / tiles, 8, KB});
         if (c >= 2) {
-            const double cost =
-                std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + 4500.0 + (400.0 + 8.0 * t.width) * (double)(c - 1);
+            // rank 0 fetches the others' pieces in turn, or all ranks fetch at once
+            const double exchange = c >= kFp8SpreadFrom && !long_sums(pl)
+                                        ? 6500.0 + 12.0 * t.width
+                                        : 4500.0 + (400.0 + 8.0 * t.width) * (double)(c - 1);
+            const double cost = std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + exchange;
             if (cost < best) {
                 best = cost;
                 t.clusters = tiles * c;
