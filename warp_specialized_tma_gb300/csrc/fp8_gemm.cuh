@@ -922,7 +922,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 // arrived, each adds up its share of the tile's float4s, from all
                 // ranks at once and in their order.  (Rank 0 alone takes a round
                 // trip a piece: 50x146x12439 9.8 us that way, 8.5 this; 241x448x16859
-                // 13 and 12, 10.8 with the clusters chosen for it.  With four ranks 939x480x5185 loses 0.3 us by it.)
+                // 13 and 12, 10.8 with the clusters chosen for it.  With four ranks
+                // 939x480x5185 loses 0.3 us by it.)
                 __syncwarp();  // the warp's stores come before its lanes' releases
                 if (lane < p.cluster)
                     mbar_arrive_cluster(mapa_shared(ready_bar, (uint32_t)lane));
