@@ -365,11 +365,6 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     return rc;
 }
 
-size_t flag_bytes(const fp8_gemm *h)
-{
-    return (size_t)std::max(h->num_sms, 2 * h->max_pairs) * kFp8EpiWarps * sizeof(uint32_t);
-}
-
 }  // namespace
 
 extern "C" {
@@ -647,6 +642,11 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
                                        h->opt[FP8_GEMM_OPT_FAULT_SKIP_LOAD] >= 0 ? 0 : (uint64_t)pl.k_blocks * 2000u);
     p.fault_skip_it = (int32_t)h->opt[FP8_GEMM_OPT_FAULT_SKIP_LOAD];
 
+    if (pl.sk_tiles && pl.cluster == 1) {
+        const int rc = from_cuda((cudaError_t)launch_fp8_clear(p.flags, pl.grid * kFp8EpiWarps, st));
+        if (rc != FP8_OK)
+            return rc;
+    }
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
@@ -686,9 +686,7 @@ FP8_API int fp8_gemm_device_status(fp8_gemm_t h, uint32_t *detail)
         return FP8_OK;
     if (detail)
         *detail = word;
-    // a launch that gave up may have left flags of partials nobody read
     if (cudaMemsetAsync(h->d_err, 0, sizeof(word), h->last_stream) != cudaSuccess ||
-        (h->flags && cudaMemsetAsync(h->flags, 0, flag_bytes(h), h->last_stream) != cudaSuccess) ||
         cudaStreamSynchronize(h->last_stream) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     return FP8_ERR_DEVICE_TIMEOUT;

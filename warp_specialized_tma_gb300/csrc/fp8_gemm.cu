@@ -13,7 +13,31 @@ const void *pick(bool long_sums)
                      : reinterpret_cast<const void *>(&fp8_gemm_kernel<CG, kTransposed, false>);
 }
 
+// The flags of a split launch, ahead of it.  Not left at 0 by the launch before: one that
+// gave up leaves some of them set, and the next would take old partials for its own.
+__global__ void __launch_bounds__(256) fp8_clear_kernel(uint32_t *flags, int32_t n)
+{
+    grid_dependency_wait();
+    grid_launch_dependents();
+    for (int32_t i = (int32_t)threadIdx.x; i < n; i += 256)
+        flags[i] = 0u;
+}
+
 }  // namespace
+
+int launch_fp8_clear(uint32_t *flags, int32_t n, cudaStream_t stream)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    cfg.gridDim = dim3(1, 1, 1);
+    cfg.blockDim = dim3(256, 1, 1);
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fp8_clear_kernel, flags, n);
+}
 
 const void *fp8_gemm_kernel_fn(int cta_group, bool transposed, bool long_sums)
 {

@@ -24,6 +24,8 @@
 // into one contiguous range per cluster; the other tiles are walked whole.  The
 // pieces of a split tile meet through global memory as fp32, added in range
 // order by the piece that holds k-block 0, so the result is the same every time.
+// A flag per CTA and epilogue warp says that its partial is there; a kernel of one
+// CTA ahead of each such launch sets them to 0 (fp8_clear_kernel).
 // Where the tiles times 2..8 nearly fill the GPU, the CTAs of a thread-block
 // cluster share a tile instead (the same ranges, every C-th of which starts at a
 // tile's start), and the pieces meet through distributed shared memory: the
@@ -940,12 +942,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (uint32_t)ew, 0u));
                 else if (lane == 0)
                     st_release_gpu_u32(p.flags + cta * kFp8EpiWarps + ew, 1u);
-            } else if (parts && !shared_tile) {
-                // every lane's loads have returned (their sums are stored): the
-                // flags go back to 0 for the next launch
-                __syncwarp();
-                for (int32_t j2 = cluster_id + 1 + lane; j2 <= last; j2 += 32)
-                    p.flags[(j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew] = 0u;
             }
         }
         // the staging buffers have been read before the CTA exits

@@ -109,7 +109,7 @@ struct Fp8GemmParams {
     const uint32_t *s_rows; // scale words [ceil(K/512)][rows]
     const uint32_t *s_cols;
     float *partials;        // per CTA: kFp8PartialFloats
-    uint32_t *flags;        // per CTA and epilogue warp: 1 while its partial waits to be read
+    uint32_t *flags;        // per CTA and epilogue warp: 1 once its partial can be read, 0 before the launch
     uint32_t *err;
     uint64_t watchdog_ns;
     int32_t fault_skip_it;
@@ -129,5 +129,8 @@ inline size_t fp8_smem_bytes(int cta_group, int width, int stages)
 // (CUtensorMap rows, CUtensorMap cols, CUtensorMap D, Fp8GemmParams)
 // `long_sums`: fp32 D, accumulated in segments of kFp8Segment k-blocks.
 const void *fp8_gemm_kernel_fn(int cta_group, bool transposed, bool long_sums);
+
+// Sets the n flags of the split launch that follows on the stream to 0 (a cudaError_t value).
+int launch_fp8_clear(uint32_t *flags, int32_t n, cudaStream_t stream);
 
 }  // namespace wstma
