@@ -33,3 +33,15 @@ def test_multicast_only_in_the_pair_commit():
     assert hits, "the SM-pair commit is expected to multicast its arrive"
     for name, line in hits:
         assert "tcgen05.commit" in line, f"{name}: {line}"
+
+
+def test_lanes_are_synchronised_after_lane_0_acquires_for_them():
+    """In the 8-bit product one lane waits for a partial that all lanes then load: a shuffle of the
+    outcome orders no memory, so a __syncwarp stands between the wait and the loads."""
+    text = dict(_sources())["fp8_gemm.cuh"]
+    collect = re.search(r"auto collect = \[&\]\(\) \{(.*?)\n {12}\};", text, re.S).group(1)
+    waits = re.findall(r"(?:warp_wait_flag\(|ctl\.wait<true>\(ready_bar)(.*?)(?=warp_wait_flag\(|ctl\.wait<true>|\Z)",
+                       collect, re.S)
+    assert len(waits) == 2
+    for after in waits:
+        assert "__syncwarp();" in after

@@ -772,6 +772,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                             // a give-up stores the tile unsummed, and the status says so
                             parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFp8EpiWarps + ew, 1u,
                                                    lane);
+                    __syncwarp();  // lane 0's acquires come before the lanes' loads
                 }
             };
             // one chunk's sums: left for the tile's owner, or completed and stored
