@@ -84,10 +84,11 @@ FP8_API const char *fp8_version(void);
 
 /* ---- product of two quantised matrices ---------------------------------- */
 
-/* A handle bound to CUDA device `device` (-1 = the current one).  It holds one
- * plan and its workspace; launches of one handle share that workspace, so they
- * must be ordered one after another (one stream, or events); use one handle
- * per stream otherwise. */
+/* A handle bound to CUDA device `device` (-1 = the current one).  It holds plans,
+ * the watchdog's status word and, for fp8_gemm_run, a workspace: launches by
+ * fp8_gemm_run of one handle share it, so they must run one after another (one
+ * stream, or events), replays of graphs that captured them among them.  Use a
+ * handle per stream and per graph, or fp8_gemm_run_in, otherwise. */
 FP8_API int fp8_gemm_create(int device, fp8_gemm_t *out);
 FP8_API int fp8_gemm_destroy(fp8_gemm_t h); /* waits for nothing; NULL is accepted */
 FP8_API int fp8_gemm_set_option(fp8_gemm_t h, int key, int64_t value);
@@ -97,7 +98,7 @@ FP8_API int fp8_gemm_get_option(fp8_gemm_t h, int key, int64_t *value);
  * 16); ldd: elements per row of D (any value >= N). */
 FP8_API int fp8_gemm_check_problem(int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldd,
                                    int out_type);
-/* Picks tile, grid and split and allocates the workspace; launches nothing. */
+/* Picks tile, grid and split; launches nothing. */
 FP8_API int fp8_gemm_plan(fp8_gemm_t h, int64_t M, int64_t N, int64_t K, int64_t lda, int64_t ldb, int64_t ldd,
                           int out_type);
 FP8_API int fp8_gemm_plan_info(fp8_gemm_t h, fp8_gemm_plan_info_t *info);
@@ -107,6 +108,13 @@ FP8_API int fp8_gemm_plan_info(fp8_gemm_t h, fp8_gemm_plan_info_t *info);
  * sub-matrix of D is written.  May be captured into a CUDA graph. */
 FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void *B, const void *SB, void *D,
                          void *stream);
+/* Bytes of workspace that a launch of the handle's plan needs: 0 unless tiles are
+ * split along K through global memory. */
+FP8_API int fp8_gemm_workspace(fp8_gemm_t h, int64_t *bytes);
+/* fp8_gemm_run with a workspace of the caller's (16-byte aligned, whatever it holds,
+ * held until the work has run): launches with workspaces of their own may overlap. */
+FP8_API int fp8_gemm_run_in(fp8_gemm_t h, const void *A, const void *SA, const void *B, const void *SB, void *D,
+                            void *workspace, int64_t workspace_bytes, void *stream);
 /* Waits for the handle's last stream; DEVICE_TIMEOUT with *detail = the
  * watchdog's word if a wait ran out since the last call, and clears it. */
 FP8_API int fp8_gemm_device_status(fp8_gemm_t h, uint32_t *detail);

@@ -162,3 +162,10 @@ def test_work_split(tmp_path):
     assert build.returncode == 0, build.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.endswith("splits\n"), run.stdout + run.stderr
+
+
+def test_a_launch_takes_its_workspace_from_the_caller(lib):
+    import ctypes
+    need = ctypes.c_int64(-1)
+    assert lib.fp8_gemm_workspace(None, ctypes.byref(need)) == fp8.ERR_INVALID_ARG
+    assert lib.fp8_gemm_run_in(None, 16, 16, 16, 16, 16, 256, 1 << 20, None) == fp8.ERR_INVALID_ARG

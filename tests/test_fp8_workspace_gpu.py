@@ -61,3 +61,101 @@ def test_a_launch_that_gave_up_leaves_nothing_to_the_next():
         assert g.device_status()[0] == fp8.ERR_DEVICE_TIMEOUT
         assert g.run(*args).cpu().equal(want)
         assert g.device_status()[0] == fp8.OK
+
+
+def test_a_workspace_may_hold_anything():
+    args, want = problem(20, 2560, 12000, 2)
+    out = torch.empty(20, 2560, dtype=torch.bfloat16, device="cuda")
+    lib = fp8.load()
+    with fp8.Gemm(0, **SPLIT) as g:
+        g.plan(20, 2560, 12000)
+        need = fp8._L()
+        assert lib.fp8_gemm_workspace(g.h, need) == fp8.OK and need.value > 0
+        work = torch.empty(need.value // 4, dtype=torch.int32, device="cuda")
+        ptrs = [t.data_ptr() for t in args] + [out.data_ptr()]
+        stream = torch.cuda.current_stream().cuda_stream
+        run = lambda w, n: lib.fp8_gemm_run_in(g.h, *ptrs, w, n, stream)  # noqa: E731
+        for value in (1, 0, -1, 1):  # 1: every flag set
+            work.fill_(value)
+            out.fill_(0)
+            assert run(work.data_ptr(), need.value) == fp8.OK
+            assert out.cpu().equal(want)
+        assert run(None, need.value) == fp8.ERR_INVALID_ARG
+        assert run(work.data_ptr(), need.value - 1) == fp8.ERR_INVALID_ARG
+        assert run(work.data_ptr() + 4, need.value) == fp8.ERR_ALIGNMENT
+        # a workspace of the handle's own
+        out.fill_(0)
+        assert lib.fp8_gemm_run(g.h, *ptrs, stream) == fp8.OK
+        assert out.cpu().equal(want)
+        assert g.device_status()[0] == fp8.OK
+
+
+# a product whose default plan splits tiles through global memory
+M, N, K = 588, 2033, 24654
+
+
+def splits_through_global_memory():
+    with fp8.Gemm(0) as g:
+        info = g.plan(M, N, K)
+    return info["split_tiles"] > 0 and info["cluster"] == 1
+
+
+def test_graphs_replayed_at_once_on_two_streams():
+    assert splits_through_global_memory()
+    work = [problem(M, N, K, seed) for seed in (3, 4)]
+    graphs, outs = [], []
+    for args, _ in work:  # both captured on torch's one stream for captures
+        graphs.append(torch.cuda.CUDAGraph())
+        outs.append(torch.empty(M, N, dtype=torch.bfloat16, device="cuda"))
+        with torch.cuda.graph(graphs[-1]):
+            for _ in range(3):
+                fp8.gemm(*args, out=outs[-1])
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(20):
+        for out in outs:
+            out.fill_(-1)
+        torch.cuda.synchronize()
+        for _ in range(4):
+            for graph, stream in zip(graphs, streams):
+                with torch.cuda.stream(stream):
+                    graph.replay()
+        torch.cuda.synchronize()
+        for out, (_, want) in zip(outs, work):
+            assert out.cpu().equal(want)
+
+
+def test_calls_at_once_on_two_streams_beside_a_graph():
+    work = [problem(M, N, K, seed) for seed in (5, 6, 7)]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    graph, held = torch.cuda.CUDAGraph(), torch.empty(M, N, dtype=torch.bfloat16, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=side):
+        fp8.gemm(*work[0][0], out=held)
+    with fp8.Gemm(0) as g:  # one handle on two streams: the calls' workspaces are their own
+        for _ in range(20):
+            held.fill_(-1)
+            torch.cuda.synchronize()
+            graph.replay()  # on the current stream
+            one = g.run(*work[1][0], stream=side)
+            two = g.run(*work[2][0], stream=other)
+            torch.cuda.synchronize()
+            for got, (_, want) in zip((held, one, two), work):
+                assert got.cpu().equal(want)
+        assert g.device_status()[0] == fp8.OK
+
+
+def test_no_workspace_is_kept_for_a_stream():
+    assert splits_through_global_memory()
+    args, want = problem(M, N, K, 8)
+    fp8.gemm(*args)
+    torch.cuda.synchronize()
+    torch.cuda.empty_cache()
+    free, _ = torch.cuda.mem_get_info()
+    for _ in range(20):
+        got = fp8.gemm(*args, stream=torch.cuda.Stream())
+        torch.cuda.synchronize()
+        assert got.cpu().equal(want)
+    del got
+    torch.cuda.empty_cache()
+    # 20 MB each, if they were
+    assert torch.cuda.mem_get_info()[0] > free - 100 * 2**20

@@ -22,7 +22,7 @@ constexpr int64_t kMaxDim = 0x7FFFFFFFLL;
 constexpr int64_t kMaxRows = kMaxDim - 1023;  // a tile past the last row still has a 32-bit index
 constexpr int64_t kMaxPitch = int64_t(1) << 38;
 constexpr int kNumOptions = 8;
-constexpr int kPlans = 32;          // plans a handle remembers
+constexpr int kPlans = 64;          // plans a handle remembers
 constexpr int kMaxCtas = 1024;      // bounds the workspace of split tiles
 constexpr int64_t kMinSplitBlocks = 4;  // k-blocks per cluster below which tiles are not split further
 
@@ -52,9 +52,7 @@ struct fp8_gemm {
     size_t max_smem = 0;
     int max_pairs = 0;  // SM pairs that are resident at once
     uint32_t *d_err = nullptr;
-    // workspace of split tiles, allocated at its final size by the first plan that needs it
-    float *partials = nullptr;
-    uint32_t *flags = nullptr;
+    void *workspace = nullptr;  // of split tiles, allocated at its final size by the first fp8_gemm_run that needs it
     int64_t opt[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0};
     Plan plans[kPlans];
     Plan *plan = nullptr;
@@ -354,15 +352,16 @@ int make_plan(fp8_gemm_t h, Plan &pl)
     if (configure(h, pl.fn) != cudaSuccess || cudaFuncGetAttributes(&a, pl.fn) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     pl.regs = a.numRegs;
-    const size_t ctas = (size_t)std::max(h->num_sms, 2 * h->max_pairs);
-    int rc = FP8_OK;
-    if (pl.sk_tiles && pl.cluster == 1) {
-        if (!h->partials)
-            rc = alloc_zeroed((void **)&h->partials, ctas * kFp8PartialFloats * sizeof(float));
-        if (rc == FP8_OK && !h->flags)
-            rc = alloc_zeroed((void **)&h->flags, ctas * kFp8EpiWarps * sizeof(uint32_t));
-    }
-    return rc;
+    return FP8_OK;
+}
+
+// A CTA's part of the workspace of split tiles: all partials come first, then all flags.
+constexpr size_t kPartialBytes = kFp8PartialFloats * sizeof(float);
+constexpr size_t kFlagBytes = kFp8EpiWarps * sizeof(uint32_t);
+
+size_t workspace_bytes(const Plan &pl)
+{
+    return pl.sk_tiles && pl.cluster == 1 ? (size_t)pl.grid * (kPartialBytes + kFlagBytes) : 0;
 }
 
 }  // namespace
@@ -467,10 +466,8 @@ FP8_API int fp8_gemm_destroy(fp8_gemm_t h)
     DeviceGuard guard(h->device);
     if (h->d_err)
         cudaFree(h->d_err);
-    if (h->partials)
-        cudaFree(h->partials);
-    if (h->flags)
-        cudaFree(h->flags);
+    if (h->workspace)
+        cudaFree(h->workspace);
     delete h;
     return FP8_OK;
 }
@@ -567,6 +564,17 @@ FP8_API int fp8_gemm_plan_info(fp8_gemm_t h, fp8_gemm_plan_info_t *info)
     return FP8_OK;
 }
 
+FP8_API int fp8_gemm_workspace(fp8_gemm_t h, int64_t *bytes)
+{
+    if (!h || !bytes)
+        return FP8_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (!h->plan)
+        return FP8_ERR_NOT_PLANNED;
+    *bytes = (int64_t)workspace_bytes(*h->plan);
+    return FP8_OK;
+}
+
 FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void *B, const void *SB, void *D,
                          void *stream)
 {
@@ -574,7 +582,31 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
         return FP8_ERR_INVALID_ARG;
     if (!h->plan)
         return FP8_ERR_NOT_PLANNED;
+    const size_t most = (size_t)std::max(h->num_sms, 2 * h->max_pairs) * (kPartialBytes + kFlagBytes);
+    if (!h->workspace && workspace_bytes(*h->plan)) {
+        DeviceGuard guard(h->device);
+        if (!guard.ok())
+            return FP8_ERR_CUDA;
+        const int rc = alloc_zeroed(&h->workspace, most);
+        if (rc != FP8_OK)
+            return rc;
+    }
+    return fp8_gemm_run_in(h, A, SA, B, SB, D, h->workspace, h->workspace ? (int64_t)most : 0, stream);
+}
+
+FP8_API int fp8_gemm_run_in(fp8_gemm_t h, const void *A, const void *SA, const void *B, const void *SB, void *D,
+                            void *workspace, int64_t size, void *stream)
+{
+    if (!h)
+        return FP8_ERR_INVALID_ARG;
+    if (!h->plan)
+        return FP8_ERR_NOT_PLANNED;
     Plan &pl = *h->plan;
+    const size_t need = workspace_bytes(pl);
+    if (need && (!workspace || size < (int64_t)need))
+        return FP8_ERR_INVALID_ARG;
+    if (need && !aligned(workspace, 16))
+        return FP8_ERR_ALIGNMENT;
     if (pl.M == 0 || pl.N == 0)
         return FP8_OK;
     const uintptr_t esize = pl.out_type == FP8_FP32 ? 4 : 2;
@@ -634,15 +666,15 @@ FP8_API int fp8_gemm_run(fp8_gemm_t h, const void *A, const void *SA, const void
     p.D = D;
     p.s_rows = static_cast<const uint32_t *>(pl.transposed ? SB : SA);
     p.s_cols = static_cast<const uint32_t *>(pl.transposed ? SA : SB);
-    p.partials = h->partials;
-    p.flags = h->flags;
+    p.partials = need ? static_cast<float *>(workspace) : nullptr;
+    p.flags = need ? reinterpret_cast<uint32_t *>(p.partials + (size_t)pl.grid * kFp8PartialFloats) : nullptr;
     p.err = h->d_err;
     // a tile's waits grow with K; 2 us a k-block is far above any measured
     p.watchdog_ns = std::max<uint64_t>((uint64_t)h->opt[FP8_GEMM_OPT_WATCHDOG_NS],
                                        h->opt[FP8_GEMM_OPT_FAULT_SKIP_LOAD] >= 0 ? 0 : (uint64_t)pl.k_blocks * 2000u);
     p.fault_skip_it = (int32_t)h->opt[FP8_GEMM_OPT_FAULT_SKIP_LOAD];
 
-    if (pl.sk_tiles && pl.cluster == 1) {
+    if (need) {
         const int rc = from_cuda((cudaError_t)launch_fp8_clear(p.flags, pl.grid * kFp8EpiWarps, st));
         if (rc != FP8_OK)
             return rc;

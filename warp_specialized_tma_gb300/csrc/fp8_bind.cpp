@@ -208,9 +208,9 @@ void need_args(Py_ssize_t got, Py_ssize_t want)
         type_error("expected " + std::to_string(want) + " arguments, got " + std::to_string(got));
 }
 
-// The product's handles by device and stream: calls on different streams share
-// no workspace.  Guarded by the interpreter lock; they live as long as the process.
-std::map<std::pair<int, void *>, fp8_gemm_t> handles;
+// The product's handles by device, for their plans: a call's workspace is its own.
+// Guarded by the interpreter lock; they live as long as the process.
+std::map<int, fp8_gemm_t> handles;
 
 // run(handle or 0, a, a_scales, b, b_scales, out or None, out_dtype) -> out
 PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
@@ -246,13 +246,20 @@ PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
         }
         const int type = element_type(out, "out");
         if (!h) {
-            fp8_gemm_t &kept = handles[{at.index, at.stream}];
+            fp8_gemm_t &kept = handles[at.index];
             if (!kept)
                 check(fp8_gemm_create(at.index, &kept), "fp8_gemm_create");
             h = kept;
         }
         check(fp8_gemm_plan(h, M, N, K, lda, ldb, pitch_of(out, "out"), type), "fp8_gemm_plan");
-        check(fp8_gemm_run(h, data(a), data(as), data(b), data(bs), data(out), at.stream), "fp8_gemm_run");
+        int64_t need = 0;
+        check(fp8_gemm_workspace(h, &need), "fp8_gemm_workspace");
+        Tensor work;  // freed on return, to this stream's (or this graph's) later allocations: they run after it
+        if (need)
+            work = at.empty({need}, at::kByte);
+        check(fp8_gemm_run_in(h, data(a), data(as), data(b), data(bs), data(out), need ? data(work) : nullptr, need,
+                              at.stream),
+              "fp8_gemm_run");
         return wrap(std::move(out));
     });
 }

@@ -73,6 +73,8 @@ _SIGNATURES = {
     "fp8_gemm_plan": (_I, [_P] + [_L] * 6 + [_I]),
     "fp8_gemm_plan_info": (_I, [_P, _P]),
     "fp8_gemm_run": (_I, [_P] * 7),
+    "fp8_gemm_workspace": (_I, [_P, ctypes.POINTER(_L)]),
+    "fp8_gemm_run_in": (_I, [_P] * 7 + [_L, _P]),
     "fp8_gemm_device_status": (_I, [_P, ctypes.POINTER(ctypes.c_uint32)]),
     "fp8_quantize": (_I, [_P, _I, _L, _L, _L, _I, _P, _P, _I, _P, _L, _P, _P, _L, _P, _P]),
     "fp8_rmsnorm": (_I, [_P, _L, _P, _L, _P, _I, _L, _L, ctypes.c_float, _P, _L, _P, _L, _P, _P, _P]),
@@ -175,7 +177,8 @@ class Gemm:
     """One handle of the product, for its options and its plan.
 
     ``Gemm(device=0, width=128, ...)`` takes any option of OPTIONS as a keyword.
-    Launches of one handle share its workspace: order them (one stream).
+    A call's workspace comes from torch's allocator for its stream, and from a
+    graph's memory where the call is captured, so calls may overlap.
     """
 
     def __init__(self, device: int = -1, **options):
@@ -242,8 +245,9 @@ class Gemm:
 def gemm(a, a_scales, b, b_scales, out=None, out_dtype=torch.bfloat16, stream=None):
     """a @ b.T for quantised a (M x K) and b (N x K): bf16 or fp32, M x N, summed in fp32.
 
-    Runs on a handle kept for the device and stream, so calls on different
-    streams share no workspace.
+    Runs on a handle kept for the device.  A call's workspace comes from torch's
+    allocator for its stream, and from a graph's memory where the call is
+    captured: calls on different streams, and graphs, share none.
     """
     if stream is not None:
         with _on(stream, a.device):
