@@ -17,8 +17,9 @@ const void *pick(bool long_sums)
 // gave up leaves some of them set, and the next would take old partials for its own.
 __global__ void __launch_bounds__(256) fp8_clear_kernel(uint32_t *flags, int32_t n)
 {
-    grid_dependency_wait();
+    // the product's start overlaps the kernel before this one, and its wait is for this one
     grid_launch_dependents();
+    grid_dependency_wait();
     for (int32_t i = (int32_t)threadIdx.x; i < n; i += 256)
         flags[i] = 0u;
 }
