@@ -63,6 +63,36 @@ def test_a_launch_that_gave_up_leaves_nothing_to_the_next():
         assert g.device_status()[0] == fp8.OK
 
 
+# one SM and pairs, whole tiles, tiles split through global memory and among clusters (rank 0
+# adding the pieces, and every rank its part), an fp32 D in segments
+@pytest.mark.parametrize("options,dtype", [
+    (SPLIT, torch.bfloat16),
+    ({"cta_group": 1, "transposed": 2, "width": 32, "split": 0}, torch.bfloat16),
+    ({"cta_group": 2, "transposed": 1, "width": 224, "split": 0}, torch.bfloat16),
+    ({"cta_group": 2, "transposed": 2, "width": 64, "split": 2}, torch.bfloat16),
+    ({"cta_group": 1, "transposed": 1, "width": 224, "split": 1}, torch.bfloat16),
+    ({"cta_group": 1, "transposed": 2, "width": 32, "split": 1}, torch.bfloat16),
+    ({"cta_group": 2, "transposed": 1, "width": 96, "split": 2}, torch.float32),
+], ids=["ranges", "whole", "pairs", "pair-ranges", "clusters", "spread", "segments"])
+def test_a_launch_may_give_up_at_any_load(options, dtype):
+    # loads in the ring's first lap and later ones: stages that follow the missing load
+    # are not filled again, and the next launch is right
+    args, want = problem(200, 2560, 12000, 10)
+    with fp8.Gemm(0, **options) as g:
+        for skip in (0, 1, 2, 7, 8, 9, 13, 20, 40):
+            g.set_option("watchdog_ns", 4000000)
+            g.set_option("fault_skip_load", skip)
+            g.run(*args, out_dtype=dtype)
+            st, _ = g.device_status()
+            assert st in (fp8.ERR_DEVICE_TIMEOUT, fp8.OK)  # OK: no CTA has that many loads
+            assert st == fp8.ERR_DEVICE_TIMEOUT or skip > 1
+            g.set_option("fault_skip_load", -1)
+            g.set_option("watchdog_ns", 2000000000)
+            d = g.run(*args, out_dtype=dtype)
+            assert d.cpu().to(torch.bfloat16).equal(want)
+            assert g.device_status() == (fp8.OK, 0)
+
+
 def test_a_workspace_may_hold_anything():
     args, want = problem(20, 2560, 12000, 2)
     out = torch.empty(20, 2560, dtype=torch.bfloat16, device="cuda")

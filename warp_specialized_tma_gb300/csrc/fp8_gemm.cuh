@@ -393,7 +393,8 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     const uint32_t tmem_slot = done_bar + 8u;
     const uint32_t abort_flag = tmem_slot + 4u;
     const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
-    const uint32_t ready_bar = go_words + 8u;   // cluster form: one per epilogue warp of rank 0, or one per rank
+    const uint32_t ready_bar = go_words + 8u;   // cluster form: one per epilogue warp of rank 0, or one per rank;
+                                                // behind its eight, one that nothing waits for
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
@@ -413,6 +414,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             mbar_init(acce_bar + 8u * a, kFp8EpiWarps * CG);
         }
         mbar_init(done_bar, 1);
+        mbar_init(ready_bar + 64u, 1);
         if (spread)
             mbar_init(ready_bar, (uint32_t)p.cluster * kFp8EpiWarps);  // every epilogue warp of every rank
         else if (shared_tile)
@@ -452,6 +454,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     ctl.peer_abort_flag = kCluster ? mapa_shared(abort_flag, rank ^ 1u) : 0u;
     ctl.err = p.err;
     ctl.set_limit(p.watchdog_ns);
+    // Copies and MMAs in flight are waited for at the end however short the limit is:
+    // they land in a few microseconds, and must not outlive the CTA.
+    WaitCtl drain = ctl;
+    drain.limit_ns = ctl.limit_ns > 20000000ull ? ctl.limit_ns : 20000000ull;
 
     const int32_t cluster_id = (int32_t)blockIdx.x / CG;
     const int32_t num_clusters = (int32_t)gridDim.x / CG;
@@ -503,8 +509,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                     const int32_t j = it - d;
                     if (j == p.fault_skip_it)
                         continue;
-                    ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
-                                             (uint32_t)ring_stage_of(j, S));
+                    // one that runs out has outlasted the others' loads too
+                    if (!drain.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S),
+                                                    ring_parity_of(j, S), (uint32_t)ring_stage_of(j, S)))
+                        break;
                 }
             } else if (lane == 0 && ctl.aborted()) {
                 // the peer's loads complete on the leader's barriers, which this CTA
@@ -523,9 +531,13 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             const uint32_t step = stage_bytes >> 4;
             const uint32_t leader = elect_one();
             // Waits here are loops inside one statement, and a wait that runs out does
-            // not leave the k loop: it records the fact and the rest of the item runs
-            // with single probes (its result is wrong, and the status says so).
-            const uint32_t probe_ns = ctl.suspend_ns;
+            // not leave the k loop (a branch out of it costs an fp32 D 4 to 20 %): it records
+            // the fact, and the rest of the item runs with short single probes and tells
+            // nobody.  Above all it releases no stage: one filled again before its first
+            // load has landed would count arrivals into a phase that has all of them,
+            // which faults.
+            const uint32_t nobody_bar = ready_bar + 64u;
+            uint32_t probe_ns = ctl.suspend_ns;
             uint32_t tries = (uint32_t)(ctl.limit_ns / probe_ns) + 1u;
             uint32_t bad = 0u;
             auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role, uint32_t where) {
@@ -534,6 +546,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                         ctl.fail(role, where);
                     bad = 1u;
                     tries = 1u;
+                    probe_ns = 1u;
                 }
             };
             int s = 0;
@@ -551,7 +564,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                 uint32_t fresh = 1u;                      // the accumulator starts over
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
                     if (kLong && kb == cut) {
-                        mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
+                        mma_commit_elected<CG>(bad ? nobody_bar : accf_bar + 8u * acc, leader);
                         acc ^= 1;
                         acc_ph ^= acc == 0 ? 1u : 0u;
                         wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
@@ -583,10 +596,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
                                                fresh ^ 1u, leader, full_bar + 8u * s1, ring_full_parity(ph1));
                     fresh = 0u;
                     if (ring_group_last(s, 1u))
-                        mma_commit_elected<CG>(empty_bar + 8u * ring_group(s, 1u), leader);
+                        mma_commit_elected<CG>(bad ? nobody_bar : empty_bar + 8u * ring_group(s, 1u), leader);
                     ring_advance(s, ph, S);
                 }
-                mma_commit_elected<CG>(accf_bar + 8u * acc, leader);
+                mma_commit_elected<CG>(bad ? nobody_bar : accf_bar + 8u * acc, leader);
                 acc ^= 1;
                 if (acc == 0)
                     acc_ph ^= 1u;
@@ -596,7 +609,7 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             // no MMA may still be writing tensor memory when it is freed
             mma_commit_elected<CG>(done_bar, leader);
             if (leader)
-                ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+                drain.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
             __syncwarp();
         } else if (warp == 2 || warp == 3) {
             // ---------------- scales ----------------
