@@ -90,7 +90,10 @@ FP8_API const char *fp8_version(void);
  * stream, or events), replays of graphs that captured them among them.  Use a
  * handle per stream and per graph, or fp8_gemm_run_in, otherwise. */
 FP8_API int fp8_gemm_create(int device, fp8_gemm_t *out);
-FP8_API int fp8_gemm_destroy(fp8_gemm_t h); /* waits for nothing; NULL is accepted */
+/* Frees the handle's memory, which may wait for the device's work.  No launch of the
+ * handle may come after it, nor a replay of a graph that captured one: the launches hold the
+ * address of the handle's status word (and of its workspace).  NULL is accepted. */
+FP8_API int fp8_gemm_destroy(fp8_gemm_t h);
 FP8_API int fp8_gemm_set_option(fp8_gemm_t h, int key, int64_t value);
 FP8_API int fp8_gemm_get_option(fp8_gemm_t h, int key, int64_t *value);
 
@@ -115,8 +118,10 @@ FP8_API int fp8_gemm_workspace(fp8_gemm_t h, int64_t *bytes);
  * held until the work has run): launches with workspaces of their own may overlap. */
 FP8_API int fp8_gemm_run_in(fp8_gemm_t h, const void *A, const void *SA, const void *B, const void *SB, void *D,
                             void *workspace, int64_t workspace_bytes, void *stream);
-/* Waits for the handle's last stream; DEVICE_TIMEOUT with *detail = the
- * watchdog's word if a wait ran out since the last call, and clears it. */
+/* Waits for the handle's device (so not while a stream is being captured);
+ * DEVICE_TIMEOUT with *detail = the watchdog's word if a wait ran out in any
+ * launch of the handle, on whatever stream or from a graph, since the last call,
+ * and clears it. */
 FP8_API int fp8_gemm_device_status(fp8_gemm_t h, uint32_t *detail);
 
 /* ---- quantiser ----------------------------------------------------------- */

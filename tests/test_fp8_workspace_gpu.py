@@ -189,3 +189,19 @@ def test_no_workspace_is_kept_for_a_stream():
     torch.cuda.empty_cache()
     # 20 MB each, if they were
     assert torch.cuda.mem_get_info()[0] > free - 100 * 2**20
+
+
+def test_status_of_a_graph_replayed_on_another_stream():
+    args, want = problem(20, 2560, 12000, 9)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with fp8.Gemm(0, watchdog_ns=20000000, fault_skip_load=1, **SPLIT) as g:
+        g.run(*args)
+        assert g.device_status()[0] == fp8.ERR_DEVICE_TIMEOUT
+        with torch.cuda.graph(graph):
+            g.run(*args)
+        for _ in range(3):
+            with torch.cuda.stream(side):
+                graph.replay()
+            st, detail = g.device_status()  # waits for the replay
+            assert st == fp8.ERR_DEVICE_TIMEOUT and detail != 0
+            assert g.device_status() == (fp8.OK, 0)

@@ -57,7 +57,6 @@ struct fp8_gemm {
     Plan plans[kPlans];
     Plan *plan = nullptr;
     uint64_t clock = 0;
-    cudaStream_t last_stream = nullptr;
 };
 
 namespace {
@@ -695,10 +694,7 @@ FP8_API int fp8_gemm_run_in(fp8_gemm_t h, const void *A, const void *SA, const v
     cfg.attrs = attr;
     cfg.numAttrs = together > 1 ? 2 : 1;
     void *args[4] = {&pl.tmR, &pl.tmC, &pl.tmD, &p};
-    const int rc = from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
-    if (rc == FP8_OK)
-        h->last_stream = st;
-    return rc;
+    return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
 }
 
 FP8_API int fp8_gemm_device_status(fp8_gemm_t h, uint32_t *detail)
@@ -710,16 +706,18 @@ FP8_API int fp8_gemm_device_status(fp8_gemm_t h, uint32_t *detail)
     DeviceGuard guard(h->device);
     if (!guard.ok())
         return FP8_ERR_CUDA;
+    // The whole device: a launch may run again on any stream, from a graph that captured
+    // it, and the stream it was first made on may be gone.
     uint32_t word = 0;
-    if (cudaMemcpyAsync(&word, h->d_err, sizeof(word), cudaMemcpyDeviceToHost, h->last_stream) != cudaSuccess ||
-        cudaStreamSynchronize(h->last_stream) != cudaSuccess)
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(&word, h->d_err, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     if (word == 0)
         return FP8_OK;
     if (detail)
         *detail = word;
-    if (cudaMemsetAsync(h->d_err, 0, sizeof(word), h->last_stream) != cudaSuccess ||
-        cudaStreamSynchronize(h->last_stream) != cudaSuccess)
+    const uint32_t none = 0;
+    if (cudaMemcpy(h->d_err, &none, sizeof(none), cudaMemcpyHostToDevice) != cudaSuccess)
         return from_cuda(cudaErrorUnknown);
     return FP8_ERR_DEVICE_TIMEOUT;
 }
