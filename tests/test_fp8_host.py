@@ -169,3 +169,11 @@ def test_a_launch_takes_its_workspace_from_the_caller(lib):
     need = ctypes.c_int64(-1)
     assert lib.fp8_gemm_workspace(None, ctypes.byref(need)) == fp8.ERR_INVALID_ARG
     assert lib.fp8_gemm_run_in(None, 16, 16, 16, 16, 16, 256, 1 << 20, None) == fp8.ERR_INVALID_ARG
+
+
+def test_the_module_level_product_has_a_status(lib):
+    with pytest.raises(ValueError, match="device"):
+        fp8.device_status(-1)
+    if not torch.cuda.is_available():
+        with pytest.raises(fp8.Fp8Error):
+            fp8.device_status(0)

@@ -205,3 +205,20 @@ def test_status_of_a_graph_replayed_on_another_stream():
             st, detail = g.device_status()  # waits for the replay
             assert st == fp8.ERR_DEVICE_TIMEOUT and detail != 0
             assert g.device_status() == (fp8.OK, 0)
+
+
+def test_status_of_the_module_level_product():
+    args, want = problem(20, 2560, 12000, 11)
+    assert fp8.gemm(*args).cpu().equal(want)
+    assert fp8.device_status() == (fp8.OK, 0)
+    lib, kept = fp8.load(), fp8._P(fp8._ops().kept_handle(0))
+    option = lambda name, value: lib.fp8_gemm_set_option(kept, fp8.OPTIONS[name], value)  # noqa: E731
+    assert option("watchdog_ns", 4000000) == fp8.OK and option("fault_skip_load", 1) == fp8.OK
+    try:
+        fp8.gemm(*args, stream=torch.cuda.Stream())
+        st, detail = fp8.device_status("cuda:0")
+        assert st == fp8.ERR_DEVICE_TIMEOUT and detail != 0
+    finally:
+        assert option("watchdog_ns", 2000000000) == fp8.OK and option("fault_skip_load", -1) == fp8.OK
+    assert fp8.gemm(*args).cpu().equal(want)
+    assert fp8.device_status(torch.device("cuda", 0)) == (fp8.OK, 0)

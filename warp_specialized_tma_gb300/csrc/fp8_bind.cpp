@@ -212,6 +212,14 @@ void need_args(Py_ssize_t got, Py_ssize_t want)
 // Guarded by the interpreter lock; they live as long as the process.
 std::map<int, fp8_gemm_t> handles;
 
+fp8_gemm_t kept_handle(int device)
+{
+    fp8_gemm_t &kept = handles[device];
+    if (!kept)
+        check(fp8_gemm_create(device, &kept), "fp8_gemm_create");
+    return kept;
+}
+
 // run(handle or 0, a, a_scales, b, b_scales, out or None, out_dtype) -> out
 PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
@@ -245,12 +253,8 @@ PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
             out = at.empty({M, N}, st);
         }
         const int type = element_type(out, "out");
-        if (!h) {
-            fp8_gemm_t &kept = handles[at.index];
-            if (!kept)
-                check(fp8_gemm_create(at.index, &kept), "fp8_gemm_create");
-            h = kept;
-        }
+        if (!h)
+            h = kept_handle(at.index);
         check(fp8_gemm_plan(h, M, N, K, lda, ldb, pitch_of(out, "out"), type), "fp8_gemm_plan");
         int64_t need = 0;
         check(fp8_gemm_workspace(h, &need), "fp8_gemm_workspace");
@@ -377,6 +381,19 @@ PyObject *bind_rmsnorm_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
     });
 }
 
+// kept_handle(device) -> the address of the handle that gemm() runs on there
+PyObject *bind_kept_handle(PyObject *, PyObject *device)
+{
+    return guarded([&]() -> PyObject * {
+        const long index = PyLong_AsLong(device);
+        if (index == -1 && PyErr_Occurred())
+            throw python_error();
+        if (index < 0 || index > 0xFFFF)
+            value_error("no such device");
+        return PyLong_FromVoidPtr(kept_handle((int)index));
+    });
+}
+
 PyObject *bind_set_error(PyObject *, PyObject *type)
 {
     Py_INCREF(type);
@@ -395,6 +412,7 @@ PyMethodDef methods[] = {
     {"quantize", fast(&bind_quantize), METH_FASTCALL, nullptr},
     {"rmsnorm", fast(&bind_rmsnorm), METH_FASTCALL, nullptr},
     {"rmsnorm_backward", fast(&bind_rmsnorm_backward), METH_FASTCALL, nullptr},
+    {"kept_handle", &bind_kept_handle, METH_O, nullptr},
     {"set_error", &bind_set_error, METH_O, nullptr},
     {nullptr, nullptr, 0, nullptr},
 };

@@ -1,6 +1,7 @@
 """8-bit operators of a pre-norm projection, over the C ABI of ``include/fp8_ops.h``.
 
     gemm                D = A @ B.T of two quantised matrices
+    device_status       whether a product's watchdog ran out
     quantize            codes and scales of a matrix's rows
     quantize_columns    ... of its columns (a transposed result)
     quantize_both       ... of both, from one read
@@ -173,6 +174,12 @@ def empty_quantized(rows: int, cols: int, device="cuda"):
 
 
 # ------------------------------------------------------------------ product
+def _status(handle):
+    w = ctypes.c_uint32()
+    st = load().fp8_gemm_device_status(handle, ctypes.byref(w))
+    return st, w.value
+
+
 class Gemm:
     """One handle of the product, for its options and its plan.
 
@@ -219,10 +226,8 @@ class Gemm:
         return (_bind or _ops()).gemm(self.h.value, a, a_scales, b, b_scales, out, out_dtype)
 
     def device_status(self):
-        """(status, detail word) of the device watchdog; synchronises the last stream."""
-        w = ctypes.c_uint32()
-        st = load().fp8_gemm_device_status(self.h, ctypes.byref(w))
-        return st, w.value
+        """(status, detail word) of the watchdog over this handle's launches; waits for the device."""
+        return _status(self.h)
 
     def close(self) -> None:
         if getattr(self, "h", None) is not None:
@@ -247,12 +252,26 @@ def gemm(a, a_scales, b, b_scales, out=None, out_dtype=torch.bfloat16, stream=No
 
     Runs on a handle kept for the device.  A call's workspace comes from torch's
     allocator for its stream, and from a graph's memory where the call is
-    captured: calls on different streams, and graphs, share none.
+    captured: calls on different streams, and graphs, share none.  A wait inside the
+    kernel that runs out is reported by device_status().
     """
     if stream is not None:
         with _on(stream, a.device):
             return gemm(a, a_scales, b, b_scales, out, out_dtype)
     return (_bind or _ops()).gemm(0, a, a_scales, b, b_scales, out, out_dtype)
+
+
+def device_status(device=None):
+    """(status, detail word) of the watchdog over every gemm() on a CUDA device (default: the current one).
+
+    Waits for the device.  ERR_DEVICE_TIMEOUT if, since the last call, a wait inside a
+    product ran out (two seconds and more, where none should take a millisecond): that
+    call's result is wrong.
+    """
+    index = device if isinstance(device, int) else torch.device(device or "cuda").index
+    if index is None:
+        index = torch.cuda.current_device()
+    return _status(_P(_ops().kept_handle(index)))
 
 
 # ------------------------------------------------------------------ quantiser
