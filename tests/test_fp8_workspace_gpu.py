@@ -222,3 +222,20 @@ def test_status_of_the_module_level_product():
         assert option("watchdog_ns", 2000000000) == fp8.OK and option("fault_skip_load", -1) == fp8.OK
     assert fp8.gemm(*args).cpu().equal(want)
     assert fp8.device_status(torch.device("cuda", 0)) == (fp8.OK, 0)
+
+
+def test_the_default_stream_by_its_raw_handle():
+    side = torch.cuda.Stream()
+    for raw in (torch.cuda.default_stream().cuda_stream, 1):
+        with torch.cuda.stream(side):  # not the current stream
+            with fp8._on(raw, torch.device("cuda", 0)):
+                assert torch.cuda.current_stream() == torch.cuda.default_stream()
+    with fp8._on(side.cuda_stream, torch.device("cuda", 0)):
+        assert torch.cuda.current_stream().cuda_stream == side.cuda_stream
+    # ordered behind the default stream's work
+    x = torch.zeros(8192, 8192, device="cuda")
+    for value in (1.0, 2.0, 3.0):
+        x.fill_(value)
+        q, s = fp8.quantize(x, stream=0)
+        torch.cuda.synchronize()
+        assert bool((q.float() * torch.exp2(s.view(torch.uint8)[0, :, :1].float() - 127) == value).all())

@@ -163,7 +163,15 @@ def _on(stream, device):
     """Context in which `stream` (a torch stream or a raw handle) is the current one: what a call
     allocates then belongs to the stream that it runs on."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
+        handle = int(stream)
+        if handle in (0, 1):  # the default stream (cudaStreamLegacy), of which torch makes no ExternalStream
+            stream = torch.cuda.default_stream(device)
+        else:
+            stream = torch.cuda.ExternalStream(handle, device=device)
+            if stream.cuda_stream != handle:
+                raise ValueError(f"stream {handle:#x} is none that torch can run on")
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     return torch.cuda.stream(stream)
 
 
