@@ -45,3 +45,12 @@ def test_lanes_are_synchronised_after_lane_0_acquires_for_them():
     assert len(waits) == 2
     for after in waits:
         assert "__syncwarp();" in after
+
+
+def test_the_gradients_ring_is_not_refilled_after_a_wait_that_ran_out():
+    """A slot whose copies have not landed must not be given another arrival, and the waits
+    that follow one that ran out must be short: there may be a million rows."""
+    text = dict(_sources())["fp8_norm.cu"]
+    assert re.search(r"if \(t == 0 && before >= 0 && ok\)\s*fill\(before", text)
+    assert len(re.findall(r"\bfill\(", text)) == 2  # that, and the first lap's
+    assert "ok ? 200u : 1u" in text

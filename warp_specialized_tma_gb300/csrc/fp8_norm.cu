@@ -656,7 +656,8 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
     int before = -1;  // the slot of the row before, if a row is left for it
     for (uint32_t row = row0; row < R; row += step) {
         const float next_rstd = row + step < R ? p.rstd[row + step] : 0.f;
-        ok = mbar_wait_tries(bars + 8u * s, ph, 10000000u, 200u) != 0u && ok;  // 2 s at most
+        // 2 s at most, and no more once that has run out
+        ok = mbar_wait_tries(bars + 8u * s, ph, ok ? 10000000u : 1u, ok ? 200u : 1u) != 0u && ok;
         const uint32_t at = base + (uint32_t)s * slot_bytes;
         uint4 dy[kHold ? V : 1], h[kHold ? V : 1];
         const uint64_t rstd2 = f32x2(rstd, rstd);
@@ -694,7 +695,9 @@ __global__ void __launch_bounds__(kThreads, V == 1 || kThreads <= 320 ? 2 : 1)
         } else {
             __syncwarp();
         }
-        if (t == 0 && before >= 0)
+        // not after a wait that ran out: a slot filled again before its copies have landed
+        // would count an arrival too many into its barrier's phase, which faults
+        if (t == 0 && before >= 0 && ok)
             fill(before, row + (uint32_t)(slots - 1) * step);
         if constexpr (kStage) {
             if (row != row0)
