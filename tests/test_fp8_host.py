@@ -177,3 +177,14 @@ def test_the_module_level_product_has_a_status(lib):
     if not torch.cuda.is_available():
         with pytest.raises(fp8.Fp8Error):
             fp8.device_status(0)
+
+
+def test_tile_order(tmp_path):
+    """The product's tile order for any band height and number of tiles: tests/fp8_tiles_check.cu."""
+    exe = tmp_path / "fp8_tiles_check"
+    build = subprocess.run(
+        [libbuild.nvcc(), "-std=c++17", "-O2", *libbuild.ARCH, "-I", libbuild.INCLUDE, "-I", libbuild.CSRC,
+         os.path.join(ROOT, "tests", "fp8_tiles_check.cu"), "-o", str(exe)], capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.endswith("orders\n"), run.stdout + run.stderr

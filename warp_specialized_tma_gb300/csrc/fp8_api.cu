@@ -651,7 +651,7 @@ FP8_API int fp8_gemm_run_in(fp8_gemm_t h, const void *A, const void *SA, const v
     p.num_row_tiles = (int32_t)pl.row_tiles;
     p.num_col_tiles = (int32_t)pl.col_tiles;
     p.num_tiles = (int32_t)pl.tiles;
-    p.raster_group = h->opt[FP8_GEMM_OPT_RASTER_GROUP] ? (int32_t)h->opt[FP8_GEMM_OPT_RASTER_GROUP] : 8;
+    p.raster_group = fp8_raster_group(h->opt[FP8_GEMM_OPT_RASTER_GROUP], pl.row_tiles);
     p.width = pl.width;
     p.stages = pl.stages;
     p.sk_tiles = (int32_t)pl.sk_tiles;

@@ -115,6 +115,14 @@ struct Fp8GemmParams {
     int32_t fault_skip_it;
 };
 
+// Height in row tiles of the bands that tiles are walked in: 8 unless asked for, and never more
+// than there are, so that a band's tiles can be counted in 32 bits.
+inline int32_t fp8_raster_group(int64_t asked, int64_t row_tiles)
+{
+    const int64_t group = asked ? asked : 8;
+    return (int32_t)(group < row_tiles ? group : row_tiles);
+}
+
 inline size_t fp8_stage_bytes(int cta_group, int width)
 {
     return (size_t)kFp8RowsPerCta * kFp8BlockK + (size_t)(width / cta_group) * kFp8BlockK;
