@@ -4,7 +4,8 @@ for sm_103a, and the Python binding of the latter, _fp8_bind.so, with the host c
 The translation units compile in parallel; the CUDA runtime is linked
 statically and every symbol except the C ABIs of include/gemm_bf16.h and
 include/fp8_ops.h is hidden, so each library loads (and exports its ABI) on a
-machine without a GPU.
+machine without a GPU.  The libraries need nvcc alone; the binding is built where
+torch is installed, after them.
 """
 from __future__ import annotations
 
@@ -100,6 +101,19 @@ def _stamp_path() -> str:
     return os.path.join(BUILD_DIR, "stamp.txt")
 
 
+def _bind_stamp_path() -> str:
+    return os.path.join(BUILD_DIR, "bind_stamp.txt")
+
+
+def torch_version() -> str | None:
+    """Version of the installed torch, against which the binding is built; None without one."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    return torch.__version__
+
+
 def _nvcc_version(cc: str) -> str:
     try:
         res = subprocess.run([cc, "--version"], capture_output=True, text=True)
@@ -113,21 +127,41 @@ def build_stamp(cc: str | None = None) -> str:
     was linked for, the compiler and the flags.  A library built on another
     machine (an x86_64 build seen on an aarch64 host) never matches."""
     cc = cc or nvcc()
-    import torch
-    return "\n".join([source_digest(), "torch=" + torch.__version__, "machine=" + platform.machine(), "nvcc=" + _nvcc_version(cc),
+    return "\n".join([source_digest(), "machine=" + platform.machine(), "nvcc=" + _nvcc_version(cc),
                       "flags=" + " ".join(ARCH + FLAGS)])
 
 
-def up_to_date(cc: str | None = None) -> bool:
-    if not (os.path.exists(LIB) and os.path.exists(FP8_LIB) and os.path.exists(FP8_BIND) and os.path.exists(_stamp_path())):
+def bind_stamp() -> str:
+    """What the built binding depends on besides."""
+    return "\n".join([source_digest(), "machine=" + platform.machine(), f"torch={torch_version()}"])
+
+
+def _stamped(path: str, stamp: str, *built: str) -> bool:
+    if not all(os.path.exists(f) for f in (path, *built)):
         return False
-    with open(_stamp_path()) as fh:
-        return fh.read().strip() == build_stamp(cc)
+    with open(path) as fh:
+        return fh.read().strip() == stamp
+
+
+def libraries_up_to_date(cc: str | None = None) -> bool:
+    return _stamped(_stamp_path(), build_stamp(cc), LIB, FP8_LIB)
+
+
+def binding_up_to_date() -> bool:
+    """Also where there is no torch to build it against."""
+    return torch_version() is None or _stamped(_bind_stamp_path(), bind_stamp(), FP8_BIND)
+
+
+def up_to_date(cc: str | None = None) -> bool:
+    return libraries_up_to_date(cc) and binding_up_to_date()
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
+    """Builds what is not up to date (with `force`, everything) and returns libgemm_bf16.so's path."""
     cc = nvcc()
-    if not force and up_to_date(cc):
+    libraries = force or not libraries_up_to_date(cc)
+    binding = torch_version() is not None and (force or not binding_up_to_date())
+    if not libraries and not binding:
         return LIB
     os.makedirs(BUILD_DIR, exist_ok=True)
 
@@ -159,17 +193,22 @@ def build(force: bool = False, verbose: bool = False) -> str:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, lib)
 
-    sources = SOURCES + FP8_SOURCES
+    def stamp(path: str, text: str) -> None:
+        with open(path, "w") as fh:
+            fh.write(text)
+
+    sources = SOURCES + FP8_SOURCES if libraries else []
     with ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
-        bind_obj = ex.submit(compile_bind)
+        bind_obj = ex.submit(compile_bind) if binding else None
         objs = list(ex.map(compile_one, sources))
-        bind_obj = bind_obj.result()
-    shared = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL"]
-    link(LIB, [*shared, *objs[:len(SOURCES)]])
-    link(FP8_LIB, [*shared, *objs[len(SOURCES):]])
-    link(FP8_BIND, [cxx(), bind_obj, *bind_flags()[1]])
-    with open(_stamp_path(), "w") as fh:
-        fh.write(build_stamp(cc))
+        if libraries:
+            shared = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL"]
+            link(LIB, [*shared, *objs[:len(SOURCES)]])
+            link(FP8_LIB, [*shared, *objs[len(SOURCES):]])
+            stamp(_stamp_path(), build_stamp(cc))
+        if binding:  # its failure leaves the libraries built
+            link(FP8_BIND, [cxx(), bind_obj.result(), *bind_flags()[1]])
+            stamp(_bind_stamp_path(), bind_stamp())
     return LIB
 
 
