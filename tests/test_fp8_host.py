@@ -188,3 +188,31 @@ def test_tile_order(tmp_path):
     assert build.returncode == 0, build.stderr
     run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0 and run.stdout.endswith("orders\n"), run.stdout + run.stderr
+
+
+def test_tensors_that_require_a_gradient_are_refused(lib):
+    # on the CPU: with or without, the tensors are on the wrong device, which is found later
+    x = torch.zeros(2, 128, dtype=torch.bfloat16)
+    w, rstd = torch.ones(128), torch.ones(2)
+    q, s = torch.zeros(2, 128, dtype=torch.uint8).view(torch.float8_e4m3fn), torch.zeros(1, 2, 4, dtype=torch.uint8)
+    out = torch.zeros(2, 2)
+    calls = {
+        "x": lambda t: fp8.quantize(t(x)),
+        "row_factor": lambda t: fp8.quantize_columns(x, row_factor=t(rstd)),
+        "column_factor": lambda t: fp8.quantize_both(x, column_factor=t(w)),
+        "weight": lambda t: fp8.rmsnorm(x, t(w)),
+        "residual": lambda t: fp8.rmsnorm(x, w, residual=t(x)),
+        "out_h": lambda t: fp8.rmsnorm(x, w, residual=x, out_h=t(x)),
+        "dy": lambda t: fp8.rmsnorm_backward(t(x), x, w, rstd),
+        "h": lambda t: fp8.rmsnorm_backward(x, t(x), w, rstd),
+        "rstd": lambda t: fp8.rmsnorm_backward(x, x, w, t(rstd)),
+        "dresidual": lambda t: fp8.rmsnorm_backward(x, x, w, rstd, dresidual=t(x)),
+        "out": lambda t: fp8._ops().gemm(0, q, s, q, s, t(out), torch.float32),
+    }
+    for name, call in calls.items():
+        with pytest.raises(ValueError, match=f"^{name} requires a gradient"):
+            call(lambda t: t.clone().requires_grad_())
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA device"):
+            call(lambda t: t.clone().requires_grad_())
+        with pytest.raises(ValueError, match="CUDA device"):
+            call(lambda t: t)

@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
@@ -51,7 +52,12 @@ const Tensor &tensor(PyObject *o, const char *what)
 {
     if (!THPVariable_Check(o))
         type_error(std::string(what) + " must be a tensor");
-    return THPVariable_Unpack(o);
+    const Tensor &t = THPVariable_Unpack(o);
+    // the result would be detached from it without a word
+    if (t.requires_grad() && at::GradMode::is_enabled())
+        value_error(std::string(what) + " requires a gradient, which these operators do not record: call them under "
+                                        "torch.no_grad(), or in the forward of a torch.autograd.Function");
+    return t;
 }
 
 const Tensor *maybe_tensor(PyObject *o, const char *what) { return o == Py_None ? nullptr : &tensor(o, what); }
