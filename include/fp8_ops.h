@@ -38,7 +38,8 @@ extern "C" {
 
 typedef enum fp8_status {
     FP8_OK = 0,
-    FP8_ERR_INVALID_ARG = -1,    /* null pointer, negative or too large size, pitch below the width */
+    FP8_ERR_INVALID_ARG = -1,    /* null pointer, negative or too large size, pitch below the width, rows
+                                    written over part of rows that are read */
     FP8_ERR_ALIGNMENT = -2,      /* a base or pitch that the call documents as aligned is not */
     FP8_ERR_NOT_PLANNED = -3,    /* fp8_gemm_run before fp8_gemm_plan */
     FP8_ERR_CUDA = -4,           /* a CUDA runtime call failed */
@@ -146,7 +147,7 @@ FP8_API int fp8_quantize(const void *x, int x_type, int64_t ldx, int64_t R, int6
  * rstd[r] = 1 / sqrt(mean_c h[r][c]^2 + eps);  y[r][c] = h[r][c] * rstd[r] * weight[c]
  * and y is quantised along its rows into codes and scales.  x, residual, h:
  * bf16; weight: weight_type; rstd: fp32, R values, or NULL.  h may be x or
- * residual itself.  C <= FP8_NORM_MAX_COLUMNS. */
+ * residual itself; rows of h over part of theirs are refused (INVALID_ARG).  C <= FP8_NORM_MAX_COLUMNS. */
 FP8_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
                         int weight_type, int64_t R, int64_t C, float eps, void *h, int64_t ldh, void *codes,
                         int64_t ldq, void *scales, float *rstd, void *stream);
@@ -158,7 +159,8 @@ FP8_API int fp8_rmsnorm_backward_workspace(int64_t R, int64_t C, int64_t *bytes)
  *   dx[r][c] = rstd[r] * (g[r][c] - n[r][c] * mean_c(g[r] * n[r])) (+ dresidual[r][c])
  *   dweight[c] = sum_r dy[r][c] * n[r][c]
  * dx is the gradient of both x and residual.  dy, h, dresidual (or NULL), dx:
- * bf16 (dx may be dy or dresidual itself); dweight: fp32, C values, summed in a
+ * bf16 (dx may be dy or dresidual itself; rows of dx over part of theirs or of h's
+ * are refused); dweight: fp32, C values, summed in a
  * fixed order.  workspace: 16-byte aligned, held until the work has run. */
 FP8_API int fp8_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, int64_t ldh, const void *weight,
                                  int weight_type, const float *rstd, const void *dresidual, int64_t lddr, void *dx,

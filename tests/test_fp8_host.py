@@ -216,3 +216,25 @@ def test_tensors_that_require_a_gradient_are_refused(lib):
             call(lambda t: t.clone().requires_grad_())
         with pytest.raises(ValueError, match="CUDA device"):
             call(lambda t: t)
+
+
+def test_rows_written_over_part_of_rows_read(lib, tmp_path):
+    """csrc/fp8_overlap.h against a count of every byte, and that the calls refuse what it finds."""
+    exe = tmp_path / "fp8_overlap_check"
+    build = subprocess.run([libbuild.cxx(), "-std=c++17", "-O2", "-I", libbuild.CSRC,
+                            os.path.join(ROOT, "tests", "fp8_overlap_check.cpp"), "-o", str(exe)],
+                           capture_output=True, text=True)
+    assert build.returncode == 0, build.stderr
+    run = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0 and run.stdout.endswith("clash\n"), run.stdout + run.stderr
+    far = 1 << 20
+    norm = lambda x, r, h: lib.fp8_rmsnorm(x, 128, r, 128, 256, 0, 4, 128, 1e-6, h, 128, 256, 128, 256, None, None)  # noqa: E731
+    back = lambda dy, h, dr, dx: lib.fp8_rmsnorm_backward(dy, 128, h, 128, 256, 0, 256, dr, 128, dx, 128, 256, 4, 128,  # noqa: E731
+                                                          256, 1 << 40, None)
+    assert norm(far, 2 * far, far + 2) == fp8.ERR_INVALID_ARG
+    assert norm(far, 2 * far, far + 256) == fp8.ERR_INVALID_ARG  # a row further
+    assert norm(far, 2 * far, 2 * far - 768) == fp8.ERR_INVALID_ARG  # its last row over residual's first
+    if torch.cuda.is_available():
+        return  # the workspace's size is asked of the device first; from here a GPU is expected
+    for dx in (far + 2, 2 * far - 768, 3 * far + 254):
+        assert back(far, 2 * far, 3 * far, dx) in (fp8.ERR_INVALID_ARG, fp8.ERR_CUDA, fp8.ERR_UNSUPPORTED)

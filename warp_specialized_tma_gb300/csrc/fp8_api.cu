@@ -13,6 +13,7 @@
 #include <new>
 
 #include "fp8_kernels.h"
+#include "fp8_overlap.h"
 
 using namespace wstma;
 
@@ -788,6 +789,9 @@ FP8_API int fp8_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_
     if (!aligned(x, 2) || !aligned(residual, 2) || !aligned(h, 2) || !aligned(weight, wsize) || !aligned(rstd, 4) ||
         !aligned(codes, 16) || ldq % 16 != 0 || !aligned(scales, 4))
         return FP8_ERR_ALIGNMENT;
+    if (residual &&
+        (rows_clash(x, 2 * ldx, h, 2 * ldh, R, 2 * C) || rows_clash(residual, 2 * ldr, h, 2 * ldh, R, 2 * C)))
+        return FP8_ERR_INVALID_ARG;
     int sms = 0;
     const int rc = current_sms(&sms);
     if (rc != FP8_OK)
@@ -855,6 +859,9 @@ FP8_API int fp8_rmsnorm_backward(const void *dy, int64_t lddy, const void *h, in
     if (!aligned(dy, 2) || !aligned(h, 2) || !aligned(weight, weight_type == FP8_FP32 ? 4 : 2) || !aligned(rstd, 4) ||
         !aligned(dresidual, 2) || !aligned(dx, 2) || !aligned(workspace, 16))
         return FP8_ERR_ALIGNMENT;
+    if (rows_clash(dy, 2 * lddy, dx, 2 * lddx, R, 2 * C) || rows_clash(h, 2 * ldh, dx, 2 * lddx, R, 2 * C) ||
+        (dresidual && rows_clash(dresidual, 2 * lddr, dx, 2 * lddx, R, 2 * C)))
+        return FP8_ERR_INVALID_ARG;
     int sms = 0;
     if ((rc = current_sms(&sms)) != FP8_OK)
         return rc;

@@ -22,6 +22,7 @@
 #include <utility>
 
 #include "fp8_ops.h"
+#include "fp8_overlap.h"
 
 namespace {
 
@@ -337,6 +338,9 @@ PyObject *bind_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n)
         if (res) {
             h = out_h ? *out_h : at.empty({R, C}, at::kBFloat16);
             ldh = need_bf16(h, R, C, "out_h");
+            if (out_h && (wstma::rows_clash(data(x), 2 * ldx, data(h), 2 * ldh, R, 2 * C) ||
+                          wstma::rows_clash(data(res), 2 * ldr, data(h), 2 * ldh, R, 2 * C)))
+                value_error("out_h lies over part of x or residual: it may be one of them, or apart");
         }
         auto [q, s] = at.quantized(R, C);
         Tensor rstd = at.empty({R}, at::kFloat);

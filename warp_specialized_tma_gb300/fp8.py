@@ -317,7 +317,7 @@ def rmsnorm(x, weight, residual=None, eps: float = 1e-6, out_h=None, stream=None
 
     x, residual: bf16 matrices; weight: bf16 or fp32.  Returns (codes, scales, h,
     rstd): h is the updated residual stream in bf16 (x itself without a residual;
-    written to ``out_h``, which may be x or residual, where given), rstd the rows'
+    written to ``out_h``, which may be x or residual but not part of them, where given), rstd the rows'
     1 / rms in fp32 for the backward pass.
     """
     if stream is not None:
