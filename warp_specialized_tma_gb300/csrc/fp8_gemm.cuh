@@ -49,6 +49,10 @@
 
 namespace wstma {
 
+// Copies and MMAs in flight are waited for at a CTA's end however short the watchdog's
+// limit is: they land in a few microseconds, and must not outlive it.
+constexpr uint64_t kFp8DrainNs = 20000000;
+
 struct Fp8Item {
     int32_t tile, kb0, kb1;
 };
@@ -454,10 +458,6 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
     ctl.peer_abort_flag = kCluster ? mapa_shared(abort_flag, rank ^ 1u) : 0u;
     ctl.err = p.err;
     ctl.set_limit(p.watchdog_ns);
-    // Copies and MMAs in flight are waited for at the end however short the limit is:
-    // they land in a few microseconds, and must not outlive the CTA.
-    WaitCtl drain = ctl;
-    drain.limit_ns = ctl.limit_ns > 20000000ull ? ctl.limit_ns : 20000000ull;
 
     const int32_t cluster_id = (int32_t)blockIdx.x / CG;
     const int32_t num_clusters = (int32_t)gridDim.x / CG;
@@ -504,13 +504,14 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             grid_launch_dependents();
             // Teardown: the last S loads may still be in flight if a role gave up.
             if (lane == 0 && rank == 0) {
+                ctl.limit_ns = max(ctl.limit_ns, kFp8DrainNs);
                 const int32_t n = it < S ? it : S;
                 for (int32_t d = 1; d <= n; ++d) {
                     const int32_t j = it - d;
                     if (j == p.fault_skip_it)
                         continue;
                     // one that runs out has outlasted the others' loads too
-                    if (!drain.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S),
+                    if (!ctl.wait_drain<kCluster>(full_bar + 8u * (uint32_t)ring_stage_of(j, S),
                                                     ring_parity_of(j, S), (uint32_t)ring_stage_of(j, S)))
                         break;
                 }
@@ -608,8 +609,10 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             }
             // no MMA may still be writing tensor memory when it is freed
             mma_commit_elected<CG>(done_bar, leader);
-            if (leader)
-                drain.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+            if (leader) {
+                ctl.limit_ns = max(ctl.limit_ns, kFp8DrainNs);
+                ctl.wait_drain<kCluster>(done_bar, 0u, 0xFFFu);
+            }
             __syncwarp();
         } else if (warp == 2 || warp == 3) {
             // ---------------- scales ----------------
