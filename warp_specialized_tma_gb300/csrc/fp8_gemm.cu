@@ -14,7 +14,8 @@ const void *pick(bool long_sums)
 }
 
 // The flags of a split launch, ahead of it.  Not left at 0 by the launch before: one that
-// gave up leaves some of them set, and the next would take old partials for its own.
+// gave up leaves some of them set, and the next would take old partials for its own.  Hidden
+// behind the kernel before: 0.9 us of 114 for 6143 x 5999 x 4104, nothing of 8192^3.
 __global__ void __launch_bounds__(256) fp8_clear_kernel(uint32_t *flags, int32_t n)
 {
     // the product's start overlaps the kernel before this one, and its wait is for this one

@@ -35,10 +35,11 @@
 // What bounds it, and what it measured.  Many tokens: the tensor pipe.  An SM pair's
 // 256 x 224 tile keeps both accumulators in tensor memory beside the scales and asks
 // L2 for the fewest bytes a product (17 TB/s all the same); 8192^3 takes 305 us in a
-// burst, 3.6 PFLOP/s, with the pipe 89 % active, and 360 us under the power cap; 6143 x
-// 5999 x 4104 97 us, 3.1 PFLOP/s; an fp32 D 2048 x 2048 x 32768 93 us, 2.9 PFLOP/s.  Few
-// tokens: the weights' stream, 67 MB in 16.7 us (4.0 TB/s) for 1 x 8192 x 8192, of
-// which about 5 us are the launch, the first loads and the pieces' meeting.
+// burst, 3.6 PFLOP/s, with the pipe 89 % active, and 360 us under the power cap.  On the
+// GPU alone (replayed from a graph) and, in brackets, as a call on changing inputs: 6143 x
+// 5999 x 4104 99 us, 3.1 PFLOP/s (114); an fp32 D 2048 x 2048 x 32768 95 us, 2.9 PFLOP/s
+// (105).  Few tokens: the weights' stream, 67 MB in 16.9 us (4.0 TB/s) for 1 x 8192 x 8192
+// (17.4), of which about 5 us are the launch, the first loads and the pieces' meeting.
 #pragma once
 
 #include <stdint.h>
@@ -532,8 +533,9 @@ __global__ void __launch_bounds__(kFp8Threads, 1)
             const uint32_t step = stage_bytes >> 4;
             const uint32_t leader = elect_one();
             // Waits here are loops inside one statement, and a wait that runs out does
-            // not leave the k loop (a branch out of it costs an fp32 D 4 to 20 %): it records
-            // the fact, and the rest of the item runs with short single probes and tells
+            // not leave the k loop (a branch out of it takes 1 x 8192 x 8192 from 16.8 to 17.3
+            // us; a leader that is not constant takes 8192^3 from 304 to 345): it records the
+            // fact, and the rest of the item runs with short single probes and tells
             // nobody.  Above all it releases no stage: one filled again before its first
             // load has landed would count arrivals into a phase that has all of them,
             // which faults.

@@ -156,8 +156,8 @@ __device__ __forceinline__ float half_warp_max(const float (&a)[V])
 }
 
 // A row's vectors t, t + T, ..., normalised and quantised: the maxima of a thread's
-// V blocks are found, turned into scales and stored together (one by one 8192 x 8192
-// without a residual takes 50 us, bound by its instructions; this way 44).
+// V blocks are found, turned into scales and stored together (one by one, with more
+// instructions, 8192 x 8192 without a residual takes 50 us; this way 44).
 template <int V>
 __device__ __forceinline__ void normalise(const NormParams &p, int64_t row, int t, int T, const uint4 (&h)[V],
                                           float rstd)
@@ -225,7 +225,8 @@ __device__ __forceinline__ void normalise(const NormParams &p, int64_t row, int 
 
 // One pass over the row, which stays in registers as bf16 (h is what is normalised,
 // so nothing is lost): HBM-bound with a residual, 8192 x 8192 71 us, 6.6 TB/s; without
-// one, 44 us and 4.6 TB/s, by its instructions.
+// one, 44 us and 4.6 TB/s, with no unit full: issue slots 58 % busy, DRAM 48 %, a warp
+// waiting mostly for its loads with 29 of an SM's 64 warps there.
 // Vector v of a row is its columns 8 v .. 8 v + 7: thread t of the row's T holds
 // vectors t, t + T, ..., so the 16 lanes of a half-warp always hold one block of 128.
 // Rows that are shifted alike are loaded, added and stored by 16-byte groups, and
@@ -418,9 +419,11 @@ constexpr int kBackwardThreads = 512;
 constexpr int kRingMax = 64;               // slots of a CTA's rings of rows
 constexpr int kRingBytes = 208 * 1024;     // of an SM's shared memory, shared by its CTAs
 
-// Rows of more than four vectors a thread (C > 16384), of which the ring of the kernel
-// below would not hold two: a CTA takes rows in a stride of the grid and keeps its
-// threads' share of dweight in registers.
+// Rows of more than four vectors a thread (C > 16384): a CTA takes rows in a stride of the
+// grid and keeps its threads' share of dweight in registers.  The ring of the kernel below
+// keeps the weights there too, and with eight vectors the two would take all of a
+// thread's 128 registers; its memory would hold two rows up to C = 26624 (17749 with
+// dresidual).  4096 x 20000 332 us, 2.0 TB/s; 2048 x 32768 219 us, 2.5 TB/s.
 template <int V, bool kDres, bool kVec>
 __global__ void __launch_bounds__(kBackwardThreads, 1) rmsnorm_backward_wide_kernel(const NormBackwardParams p)
 {

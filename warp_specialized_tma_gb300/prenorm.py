@@ -107,7 +107,7 @@ def main(argv=None) -> int:
     out = {"tokens": T, "width": C, "loss_first": losses[0], "loss_last": losses[-1],
            "forward_backward_ms": _event_ms(step, 20), "decode_us": 1e3 * _event_ms(graph.replay, 200)}
     print(json.dumps(out))
-    return 0 if losses[-1] < losses[0] else 1
+    return 0 if losses[-1] < losses[0] and fp8.device_status()[0] == fp8.OK else 1
 
 
 if __name__ == "__main__":
