@@ -58,7 +58,7 @@ typedef enum fp8_gemm_option {
                                      with K > 4096) */
     FP8_GEMM_OPT_SPLIT = 4,       /* tiles that would leave SMs idle are split along K: 1 = among clusters of CTAs or
                                      through global memory (default), 2 = through global memory only, 0 = never */
-    FP8_GEMM_OPT_WATCHDOG_NS = 5, /* limit of any wait inside the kernel (default 2e9) */
+    FP8_GEMM_OPT_WATCHDOG_NS = 5, /* limit of any wait inside the kernel (default 2e9, 1e5 to 6e10) */
     FP8_GEMM_OPT_FAULT_SKIP_LOAD = 6, /* test hook: each producer leaves out this load (-1 = none), so that
                                          a bounded wait runs out and the call reports DEVICE_TIMEOUT */
     FP8_GEMM_OPT_RASTER_GROUP = 7 /* tiles are walked in bands of this many row tiles; 0 = automatic */

@@ -239,3 +239,12 @@ def test_the_default_stream_by_its_raw_handle():
         q, s = fp8.quantize(x, stream=0)
         torch.cuda.synchronize()
         assert bool((q.float() * torch.exp2(s.view(torch.uint8)[0, :, :1].float() - 127) == value).all())
+
+
+def test_the_watchdogs_limit_is_no_shorter_than_loads_take():
+    with fp8.Gemm(0) as g:
+        for limit in (0, 1000, 99999, 60000000001):
+            with pytest.raises(fp8.Fp8Error, match="invalid"):
+                g.set_option("watchdog_ns", limit)
+        g.set_option("watchdog_ns", 100000)
+        assert g.get_option("watchdog_ns") == 100000
