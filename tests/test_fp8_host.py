@@ -174,6 +174,8 @@ def test_a_launch_takes_its_workspace_from_the_caller(lib):
 def test_the_module_level_product_has_a_status(lib):
     with pytest.raises(ValueError, match="device"):
         fp8.device_status(-1)
+    with pytest.raises(ValueError, match="device"):
+        fp8.device_status("cpu")
     if not torch.cuda.is_available():
         with pytest.raises(fp8.Fp8Error):
             fp8.device_status(0)

@@ -278,9 +278,12 @@ def device_status(device=None):
     product ran out (two seconds and more, where none should take a millisecond): that
     call's result is wrong.
     """
-    index = device if isinstance(device, int) else torch.device(device or "cuda").index
-    if index is None:
-        index = torch.cuda.current_device()
+    index = device
+    if not isinstance(device, int):
+        dev = torch.device("cuda" if device is None else device)
+        if dev.type != "cuda":
+            raise ValueError(f"{dev} is no CUDA device")
+        index = torch.cuda.current_device() if dev.index is None else dev.index
     return _status(_P(_ops().kept_handle(index)))
 
 
