@@ -1,10 +1,10 @@
-"""Builds the libraries in-tree from csrc/: libgemm_bf16.so and libfp8_ops.so with nvcc
-for sm_103a, and the Python binding of the latter, _fp8_bind.so, with the host compiler.
+"""Builds the libraries in-tree from csrc/: libgemm_bf16.so, libfp8_ops.so and libffn_ops.so with
+nvcc for sm_103a, and the Python binding of the latter two, _fp8_bind.so, with the host compiler.
 
 The translation units compile in parallel; the CUDA runtime is linked
-statically and every symbol except the C ABIs of include/gemm_bf16.h and
-include/fp8_ops.h is hidden, so each library loads (and exports its ABI) on a
-machine without a GPU.  The libraries need nvcc alone; the binding is built where
+statically and every symbol except the C ABIs of include/gemm_bf16.h,
+include/fp8_ops.h and include/ffn_ops.h is hidden, so each library loads (and exports its ABI)
+on a machine without a GPU.  The libraries need nvcc alone; the binding is built where
 torch is installed, after them.
 """
 from __future__ import annotations
@@ -29,10 +29,16 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["gemm_bf16_api.cu", "gemm_ws_c1.cu", "gemm_ws_c2.cu", "gemm_nows.cu", "gemm_bf16_noalloc.cu",
            "gemm_repack.cu", "gemm_thin.cu"]
 FP8_SOURCES = ["fp8_api.cu", "fp8_gemm.cu", "fp8_quantize.cu", "fp8_norm.cu"]
+FFN_SOURCES = ["ffn_api.cu", "ffn_gemm_plain.cu", "ffn_gemm_gated.cu", "ffn_gemm_grad.cu", "ffn_rows.cu"]
 FP8_BIND_SOURCE = "fp8_bind.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "-I", INCLUDE, "-I", CSRC]
+
+
+def ffn_lib() -> str:
+    """libffn_ops.so, beside the library that the same binding serves."""
+    return os.path.join(os.path.dirname(FP8_LIB), "libffn_ops.so")
 
 
 def nvcc() -> str:
@@ -63,7 +69,7 @@ def bind_flags() -> tuple:
     for path in include:
         comp += ["-isystem", path]
     link = ["-shared", "-L", os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda",
-            "-lc10", "-lc10_cuda", "-L", PKG, "-lfp8_ops", "-Wl,-rpath,$ORIGIN"]
+            "-lc10", "-lc10_cuda", "-L", PKG, "-lfp8_ops", "-lffn_ops", "-Wl,-rpath,$ORIGIN"]
     return comp, link
 
 
@@ -144,7 +150,7 @@ def _stamped(path: str, stamp: str, *built: str) -> bool:
 
 
 def libraries_up_to_date(cc: str | None = None) -> bool:
-    return _stamped(_stamp_path(), build_stamp(cc), LIB, FP8_LIB)
+    return _stamped(_stamp_path(), build_stamp(cc), LIB, FP8_LIB, ffn_lib())
 
 
 def binding_up_to_date() -> bool:
@@ -197,14 +203,15 @@ def build(force: bool = False, verbose: bool = False) -> str:
         with open(path, "w") as fh:
             fh.write(text)
 
-    sources = SOURCES + FP8_SOURCES if libraries else []
+    sources = SOURCES + FP8_SOURCES + FFN_SOURCES if libraries else []
     with ThreadPoolExecutor(max_workers=len(sources) + 1) as ex:
         bind_obj = ex.submit(compile_bind) if binding else None
         objs = list(ex.map(compile_one, sources))
         if libraries:
             shared = [cc, *ARCH, "-shared", "-cudart", "static", "-Xlinker", "--exclude-libs,ALL"]
             link(LIB, [*shared, *objs[:len(SOURCES)]])
-            link(FP8_LIB, [*shared, *objs[len(SOURCES):]])
+            link(FP8_LIB, [*shared, *objs[len(SOURCES):-len(FFN_SOURCES)]])
+            link(ffn_lib(), [*shared, *objs[-len(FFN_SOURCES):]])
             stamp(_stamp_path(), build_stamp(cc))
         if binding:  # its failure leaves the libraries built
             link(FP8_BIND, [cxx(), bind_obj.result(), *bind_flags()[1]])

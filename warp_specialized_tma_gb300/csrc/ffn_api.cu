@@ -1,0 +1,1047 @@
+// Host side of the C ABI declared in include/ffn_ops.h: argument checks, plans,
+// TMA tensor maps and launches.
+#include "ffn_ops.h"
+
+#include <cuda.h>
+#include <cuda_runtime.h>
+#include <cudaTypedefs.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <initializer_list>
+#include <mutex>
+
+#include "ffn_kernels.h"
+#include "fp8_overlap.h"
+
+using namespace wstma;
+
+namespace {
+
+constexpr int64_t kMaxDim = 0x7FFFFFFFLL - 1023;  // a tile past the last row still has a 32-bit index
+constexpr int64_t kMaxPitch = int64_t(1) << 37;
+constexpr int kNumOptions = 8;
+constexpr int kPlans = 64;              // plans a thread remembers
+constexpr int kMaxCtas = 1024;          // bounds the workspace of split tiles
+constexpr int64_t kMinSplitBlocks = 8;  // k-blocks per cluster below which tiles are not split further
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+bool aligned(const void *p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
+int from_cuda(cudaError_t e)
+{
+    if (e == cudaSuccess)
+        return FFN_OK;
+    cudaGetLastError();
+    return FFN_ERR_CUDA;
+}
+
+// --------------------------------------------------------------- device
+struct Device {
+    int index = -1;
+    int sms = 0;
+    int max_smem = 0;
+    int max_pairs = 0;  // SM pairs that are resident at once
+};
+
+// The current device, looked up once per device.
+int current_device(Device *out)
+{
+    static Device known[64];
+    static std::mutex lock;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return from_cuda(cudaErrorUnknown);
+    if (dev >= 64)
+        return FFN_ERR_UNSUPPORTED;
+    std::lock_guard<std::mutex> hold(lock);
+    if (known[dev].index < 0) {
+        Device d;
+        int major = 0, minor = 0;
+        if (cudaDeviceGetAttribute(&d.sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&minor, cudaDevAttrComputeCapabilityMinor, dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&d.max_smem, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess)
+            return from_cuda(cudaErrorUnknown);
+        if (major != 10 || minor != 3)
+            return FFN_ERR_UNSUPPORTED;
+        d.sms = std::min(d.sms, kMaxCtas);
+        const void *fn = ffn_plain_fn(2, false);
+        cudaLaunchConfig_t cfg = {};
+        cudaLaunchAttribute attr[1];
+        int n = 0;
+        cfg.gridDim = dim3(2, 1, 1);
+        cfg.blockDim = dim3(kFfnThreads, 1, 1);
+        cfg.dynamicSmemBytes = ffn_smem_bytes(32768, 4);
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = 2;
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem) != cudaSuccess ||
+            cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess || n < 1)
+            return from_cuda(cudaErrorUnknown);
+        d.max_pairs = std::min(n, d.sms / 2);
+        d.index = dev;
+        known[dev] = d;
+    }
+    *out = known[dev];
+    return FFN_OK;
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn()
+{
+    static std::once_flag once;
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+bool encode_2d(CUtensorMap *m, bool fp32, const void *ptr, int64_t cols, int64_t rows, int64_t row_bytes, int box_cols,
+               int box_rows, CUtensorMapSwizzle swizzle)
+{
+    auto fn = encode_fn();
+    if (!fn)
+        return false;
+    cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows};
+    cuuint64_t strides[1] = {(cuuint64_t)row_bytes};
+    cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return fn(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+              const_cast<void *>(ptr), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// --------------------------------------------------------------- a product
+// One operand: `rows` (rows or columns of the result) by k, contiguous along k, or (mn) along
+// its rows: in memory then k rows of `rows` elements.
+struct Operand {
+    const void *p = nullptr;
+    int64_t ld = 0;
+};
+
+enum Form : int32_t {
+    kOne = 0,    // A[0] B[0]
+    kSum = 1,    // A[0] B[0] + A[1] B[1]
+    kStack = 2,  // A[0] B[0] and A[1] B[0], results D[0] and D[1]
+    kDual = 3    // A[0] B[0] and A[0] B[1], both sums of an element in one thread
+};
+
+struct Product {
+    int epilogue = kFfnPlain;
+    Form form = kOne;
+    int64_t M = 0, N = 0, K = 0;
+    bool a_mn = false, b_mn = false;
+    Operand A[2], B[2];
+    FfnParams p = {};  // what the epilogue needs
+    bool no_split = false, not_transposed = false;
+};
+
+struct Options {
+    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0};
+};
+thread_local Options options;
+
+// What a plan follows from; compared as bytes.
+struct PlanKey {
+    int64_t M, N, K;
+    int64_t opt[5];
+    int32_t device, epilogue, form, flags;
+};
+
+struct Plan {
+    PlanKey key;
+    uint64_t used;
+    bool transposed;
+    int cta_group, width, c_rows, stages, grid, cluster;
+    int64_t row_tiles, row_split, col_tiles, tiles, k_blocks, k_split, sk_tiles;
+    size_t smem, stage_bytes;
+    const void *fn;
+};
+
+thread_local Plan plans[kPlans];
+thread_local uint64_t plan_clock = 0;
+thread_local Plan last_plan;
+thread_local bool have_last_plan = false;
+thread_local int32_t last_packed = 0;
+
+const void *kernel_fn(int epilogue, int cta_group, bool transposed)
+{
+    return epilogue == kFfnGated  ? ffn_gated_fn(cta_group, transposed)
+           : epilogue == kFfnGrad ? ffn_grad_fn(cta_group, transposed)
+                                  : ffn_plain_fn(cta_group, transposed);
+}
+
+// A way to tile a product, and what it costs.
+struct Tiling {
+    bool transposed;
+    int cta_group, width;
+    // found by tiling_cost()
+    int c_rows = 0;
+    size_t stage_bytes = 0;
+    int64_t clusters = 0;  // SM pairs, or CTAs, of the grid
+    int64_t sk_tiles = 0;
+    int cluster = 1;  // CTAs that share a tile in a cluster
+};
+
+struct Sides {
+    int64_t rows, cols;  // of the accumulator
+    int64_t row_tiles, col_tiles;
+    bool c_mn;
+};
+
+Sides sides_of(const Product &x, const Tiling &t)
+{
+    Sides s;
+    s.rows = t.transposed ? x.N : x.M;
+    s.cols = t.transposed ? x.M : x.N;
+    s.row_tiles = ceil_div(s.rows, kFfnRowsPerCta * t.cta_group) * (x.form == kStack ? 2 : 1);
+    s.col_tiles = ceil_div(s.cols, t.width);
+    s.c_mn = t.transposed ? x.a_mn : x.b_mn;
+    return s;
+}
+
+int ring_stages(const Device &d, size_t stage_bytes)
+{
+    int S = kFfnMaxStages;
+    while (S > 2 && ffn_smem_bytes(stage_bytes, S) > (size_t)d.max_smem)
+        S -= 2;
+    return S;
+}
+
+// Estimated time of a tiling, in clocks of an SM (1.9 GHz), without what every launch costs:
+// the stages (k-blocks) of the longest chain, each the longest of its MMAs (4096 multiply-adds a
+// clock and SM), its loads (56 bytes a clock and SM with all SMs loading) and what the MMA
+// issuer needs (250 clocks); or the operands' time in HBM, if longer; then the epilogue and the
+// exchange between a split tile's pieces.  Fills in how the tiles are shared out.
+double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
+{
+    const Sides s = sides_of(x, t);
+    const bool dual = x.form == kDual;
+    if (dual && !t.transposed)
+        t.c_rows = t.cta_group == 2 ? kFfnDualWidth : 2 * kFfnDualWidth;
+    else
+        t.c_rows = ffn_chunk_rows(s.c_mn, t.width / t.cta_group);
+    t.stage_bytes = (size_t)kFfnRowsPerCta * 128 * (dual && t.transposed ? 2 : 1) + (size_t)t.c_rows * 128;
+    const int64_t tiles = s.row_tiles * s.col_tiles;
+    const int64_t split = x.no_split ? 0 : options.v[FFN_OPT_SPLIT];
+    const int64_t most = t.cta_group == 2 ? d.max_pairs : d.sms;
+    const double sums = (dual ? 2.0 : 1.0) * t.width;  // columns of sums a row
+    const double stage = std::max({2.0 * sums, 250.0, (double)t.stage_bytes / 56.0});
+    const double hbm = (double)(x.M + x.N * (dual ? 2 : 1)) * (double)x.K * 2.0 / 3500.0;
+    const double epilogue = (x.epilogue == kFfnGrad ? 24.0 : 8.0) * sums;
+
+    t.clusters = std::min(tiles, most);
+    t.sk_tiles = 0;
+    t.cluster = 1;
+    double best = std::max((double)(ceil_div(tiles, t.clusters) * KB) * stage, hbm) + epilogue;
+    if (split == 1 && t.cta_group == 1) {
+        // each tile shared by a cluster of CTAs
+        const int64_t c = std::min<int64_t>({most / tiles, kFfnMaxCluster, KB});
+        if (c >= 2) {
+            const double exchange = 4500.0 + (400.0 + 8.0 * sums) * (double)(c - 1);
+            const double cost = std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + exchange;
+            if (cost < best) {
+                best = cost;
+                t.clusters = tiles * c;
+                t.sk_tiles = tiles;
+                t.cluster = (int)c;
+            }
+        }
+    }
+    if (split) {
+        // the last, partial wave of tiles (or all, if they do not fill one) shared by all clusters
+        const int64_t sk = tiles % most;
+        const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
+        if (sk && C > sk) {
+            // behind whole tiles the exchange is out of sight: the split tiles come first
+            const int64_t whole = (tiles - sk) / C;
+            const double exchange = whole ? 3000.0 : 7500.0 + (700.0 + 12.0 * sums) * (double)C / (double)sk;
+            const double cost =
+                std::max((double)(whole * KB + ceil_div(sk * KB, C)) * stage, hbm) + epilogue + exchange;
+            if (cost < best) {
+                best = cost;
+                t.clusters = C;
+                t.sk_tiles = sk;
+                t.cluster = 1;
+            }
+        }
+    }
+    return best;
+}
+
+// How many clusters of c CTAs of a one-SM kernel are resident at once.
+int resident_clusters(const Device &d, const void *fn, size_t smem, int c)
+{
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[1];
+    int n = 0;
+    cfg.gridDim = dim3((unsigned)c, 1, 1);
+    cfg.blockDim = dim3(kFfnThreads, 1, 1);
+    cfg.dynamicSmemBytes = smem;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&n, fn, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    return n;
+}
+
+int make_plan(const Device &d, const Product &x, Plan &pl)
+{
+    const int64_t *opt = options.v;
+    const int64_t KB = ceil_div(x.K, kFfnBlockK) * (x.form == kSum ? 2 : 1);
+    Tiling best = {false, 0, 0};
+    double best_cost = 0.0;
+    for (int cg = 1; cg <= 2; ++cg)
+        for (int tr = 0; tr <= 1; ++tr) {
+            if ((opt[FFN_OPT_CTA_GROUP] && cg != opt[FFN_OPT_CTA_GROUP]) ||
+                (tr && (x.not_transposed || x.form == kStack)) ||
+                (opt[FFN_OPT_TRANSPOSED] && tr + 1 != opt[FFN_OPT_TRANSPOSED] && !x.not_transposed &&
+                 x.form != kStack))
+                continue;
+            const bool fixed = x.form == kDual && !tr;
+            const int widest = x.form == kDual ? kFfnDualWidth : kFfnMaxWidth;
+            for (int wd = fixed ? kFfnDualWidth : 16; wd <= widest; wd += 16) {
+                if (opt[FFN_OPT_WIDTH] && wd != opt[FFN_OPT_WIDTH] && !fixed)
+                    continue;
+                // chunks of 32 columns: a narrower tile must be the only one
+                const int64_t cols = tr ? x.M : x.N;
+                if (wd % 32 != 0 && (cg == 2 || wd < cols))
+                    continue;
+                Tiling t = {tr != 0, cg, wd};
+                const double cost = tiling_cost(d, x, KB, t);
+                if (best.cta_group == 0 || cost < best_cost)
+                    best = t, best_cost = cost;
+            }
+        }
+    if (best.cta_group == 0)
+        return FFN_ERR_UNSUPPORTED;
+    const Sides s = sides_of(x, best);
+    pl.transposed = best.transposed;
+    pl.cta_group = best.cta_group;
+    pl.width = best.width;
+    pl.c_rows = best.c_rows;
+    pl.stage_bytes = best.stage_bytes;
+    pl.row_tiles = s.row_tiles;
+    pl.row_split = x.form == kStack ? s.row_tiles / 2 : s.row_tiles;
+    pl.col_tiles = s.col_tiles;
+    pl.tiles = s.row_tiles * s.col_tiles;
+    pl.k_blocks = KB;
+    pl.k_split = x.form == kSum ? KB / 2 : KB;
+    if (pl.tiles > kMaxDim || KB > kMaxDim)
+        return FFN_ERR_UNSUPPORTED;
+    pl.stages = ring_stages(d, pl.stage_bytes);
+    pl.smem = ffn_smem_bytes(pl.stage_bytes, pl.stages);
+    pl.fn = kernel_fn(x.epilogue, pl.cta_group, pl.transposed);
+    // Rank 0 of a cluster waits for the others, so all clusters must be resident:
+    // the largest size that the device can place so often.
+    if (best.cluster > 1) {
+        while (best.cluster > 1 && resident_clusters(d, pl.fn, pl.smem, best.cluster) < pl.tiles)
+            --best.cluster;
+        best.clusters = pl.tiles * best.cluster;
+        best.sk_tiles = best.cluster > 1 ? pl.tiles : 0;
+    }
+    pl.sk_tiles = best.sk_tiles;
+    pl.cluster = best.cluster;
+    pl.grid = (int)(best.clusters * best.cta_group);
+    return from_cuda(cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem));
+}
+
+int find_plan(const Device &d, const Product &x, const Plan **out)
+{
+    PlanKey key;
+    std::memset(&key, 0, sizeof(key));
+    key.M = x.M, key.N = x.N, key.K = x.K;
+    for (int i = FFN_OPT_CTA_GROUP; i <= FFN_OPT_SPLIT; ++i)
+        key.opt[i] = options.v[i];
+    key.device = d.index, key.epilogue = x.epilogue, key.form = x.form;
+    key.flags = (x.a_mn ? 1 : 0) | (x.b_mn ? 2 : 0) | (x.no_split ? 4 : 0) | (x.not_transposed ? 8 : 0);
+    Plan *slot = &plans[0];
+    for (Plan &pl : plans) {
+        if (pl.used && std::memcmp(&pl.key, &key, sizeof(key)) == 0) {
+            pl.used = ++plan_clock;
+            *out = &pl;
+            return FFN_OK;
+        }
+        if (pl.used < slot->used)
+            slot = &pl;
+    }
+    Plan pl;
+    std::memset(&pl, 0, sizeof(pl));
+    const int rc = make_plan(d, x, pl);
+    if (rc != FFN_OK)
+        return rc;
+    pl.key = key;
+    pl.used = ++plan_clock;
+    *slot = pl;
+    *out = slot;
+    return FFN_OK;
+}
+
+// --------------------------------------------------------------- workspace
+// A call runs twice over its workspace: once to measure it, launching nothing, then in earnest.
+struct Call {
+    Device dev;
+    cudaStream_t stream = nullptr;
+    uint8_t *base = nullptr;  // null: measuring
+    size_t used = 0;
+    size_t shared = 0;  // split tiles' partials and flags: the products of a call run one after another
+    bool measuring() const { return base == nullptr; }
+
+    // a part of the workspace: its place (null when measuring)
+    void *take(size_t bytes)
+    {
+        const size_t at = used;
+        used += (bytes + 255) / 256 * 256;
+        return base ? base + at : nullptr;
+    }
+};
+
+int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
+
+// Whether a tensor map can describe rows of this pitch (a single row has none).
+bool mappable(const Operand &o, int64_t mem_rows) { return aligned(o.p, 16) && (o.ld % 8 == 0 || mem_rows <= 1); }
+
+// An operand's rows as a tensor map takes them: as they are, or copied.
+int prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int32_t *packed)
+{
+    if (mem_rows < 1 || mem_cols < 1)
+        return FFN_OK;
+    if (mappable(o, mem_rows)) {
+        if (mem_rows <= 1)
+            o.ld = padded(mem_cols);
+        return FFN_OK;
+    }
+    const int64_t ld = padded(mem_cols);
+    void *const to = c.take((size_t)(mem_rows * ld) * 2);
+    ++*packed;
+    if (!c.measuring()) {
+        const int rc = from_cuda((cudaError_t)launch_ffn_pack(static_cast<const uint16_t *>(o.p), o.ld,
+                                                              static_cast<uint16_t *>(to), ld, mem_rows, mem_cols,
+                                                              c.dev.sms, c.stream));
+        if (rc != FFN_OK)
+            return rc;
+    }
+    o.p = to;
+    o.ld = ld;
+    return FFN_OK;
+}
+
+int set_out(FfnOut &out, CUtensorMap *map, const ffn_matrix &m, bool fp32, int64_t rows, int64_t cols)
+{
+    out.p = m.data;
+    out.ld = rows > 1 ? m.ld : padded(cols);
+    const int esize = fp32 ? 4 : 2;
+    out.tma = aligned(m.data, 16) && out.ld * esize % 16 == 0 &&
+              encode_2d(map, fp32, m.data, cols, rows, out.ld * esize, 64 / esize, 32, CU_TENSOR_MAP_SWIZZLE_64B);
+    return FFN_OK;
+}
+
+FfnAux aux_of(const ffn_matrix &m)
+{
+    FfnAux a;
+    a.p = m.data;
+    a.ld = m.ld;
+    a.vec = aligned(m.data, 16) && m.ld % 8 == 0;
+    return a;
+}
+
+FfnAux aux_of(const ffn_quantized &q)
+{
+    FfnAux a;
+    a.p = q.codes;
+    a.ld = q.ld;
+    a.vec = 1;
+    a.scales = static_cast<const uint8_t *>(q.scales);
+    return a;
+}
+
+// Runs one product; results D[0..2] (fp32: of D[0], and D[1] of kStack).
+int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
+{
+    if (x.M == 0 || x.N == 0)
+        return FFN_OK;
+    const Plan *found = nullptr;
+    int rc = find_plan(c.dev, x, &found);
+    if (rc != FFN_OK)
+        return rc;
+    const Plan &pl = *found;
+    int32_t packed = 0;
+    for (int i = 0; i < 2; ++i) {
+        const bool has_a = i == 0 || x.form == kSum || x.form == kStack, has_b = i == 0 || x.form == kSum || x.form == kDual;
+        if (has_a && (rc = prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, &packed)) != FFN_OK)
+            return rc;
+        if (has_b && (rc = prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, &packed)) != FFN_OK)
+            return rc;
+    }
+    const size_t partial_bytes = pl.sk_tiles && pl.cluster == 1
+                                     ? (size_t)pl.grid * (kFfnPartialFloats * sizeof(float) + kFfnEpiWarps * sizeof(uint32_t))
+                                     : 0;
+    if (c.measuring()) {
+        c.shared = std::max(c.shared, partial_bytes);
+        return FFN_OK;
+    }
+    FfnMaps maps;
+    std::memset(&maps, 0, sizeof(maps));
+    FfnParams &p = x.p;
+    const Operand *R = pl.transposed ? x.B : x.A, *C = pl.transposed ? x.A : x.B;
+    const int64_t rows = pl.transposed ? x.N : x.M, cols = pl.transposed ? x.M : x.N;
+    p.r_mn = pl.transposed ? x.b_mn : x.a_mn;
+    p.c_mn = pl.transposed ? x.a_mn : x.b_mn;
+    const bool two_r = x.form == kSum || x.form == kStack || (x.form == kDual && pl.transposed);
+    const bool two_c = x.form == kSum || (x.form == kDual && !pl.transposed);
+    const int c_box = x.form == kDual && !pl.transposed ? kFfnDualWidth : pl.width / pl.cta_group;
+    auto encode = [&](CUtensorMap *m, const Operand &o, bool mn, int64_t extent, int box_rows) {
+        return mn ? encode_2d(m, false, o.p, extent, x.K, o.ld * 2, 64, kFfnBlockK, CU_TENSOR_MAP_SWIZZLE_128B)
+                  : encode_2d(m, false, o.p, x.K, extent, o.ld * 2, kFfnBlockK, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    if (pl.k_blocks) {
+        for (int i = 0; i < 2; ++i)
+            if ((i < (two_r ? 2 : 1) && !encode(&maps.R[i], R[i], p.r_mn, rows, kFfnRowsPerCta)) ||
+                (i < (two_c ? 2 : 1) && !encode(&maps.C[i], C[i], p.c_mn, cols, c_box)))
+                return FFN_ERR_TENSORMAP;
+    }
+    for (int i = 0; i < outs; ++i)
+        if (D[i].data)
+            set_out(p.D[i], &maps.D[i], D[i], fp32 && (i == 0 || x.form == kStack), x.M, x.N);
+    p.rows = (int32_t)rows;
+    p.cols = (int32_t)cols;
+    p.D_rows = (int32_t)x.M;
+    p.D_cols = (int32_t)x.N;
+    p.num_k_blocks = (int32_t)pl.k_blocks;
+    p.k_split = (int32_t)pl.k_split;
+    p.num_row_tiles = (int32_t)pl.row_tiles;
+    p.num_col_tiles = (int32_t)pl.col_tiles;
+    p.num_tiles = (int32_t)pl.tiles;
+    p.row_split = (int32_t)pl.row_split;
+    p.width = pl.width;
+    p.c_rows = pl.c_rows;
+    p.stages = pl.stages;
+    const int64_t band = options.v[FFN_OPT_RASTER_GROUP] ? options.v[FFN_OPT_RASTER_GROUP] : 8;
+    p.raster_group = (int32_t)std::min(band, pl.row_tiles);
+    p.sk_tiles = (int32_t)pl.sk_tiles;
+    p.sk_units = pl.sk_tiles * pl.k_blocks;
+    p.cluster = pl.cluster;
+    p.out_fp32 = fp32 ? 1 : 0;
+    // behind the call's other parts, whose size the first run has measured
+    p.partials = partial_bytes ? reinterpret_cast<float *>(c.base + c.shared) : nullptr;
+    p.flags = partial_bytes ? reinterpret_cast<uint32_t *>(p.partials + (size_t)pl.grid * kFfnPartialFloats) : nullptr;
+    p.err = ffn_status_word();
+    if (!p.err)
+        return FFN_ERR_CUDA;
+    // a tile's waits grow with K; 2 us a k-block is far above any measured
+    p.watchdog_ns = std::max<uint64_t>((uint64_t)options.v[FFN_OPT_WATCHDOG_NS],
+                                       options.v[FFN_OPT_FAULT_SKIP_LOAD] >= 0 ? 0 : (uint64_t)pl.k_blocks * 2000u);
+    p.fault_skip_it = (int32_t)options.v[FFN_OPT_FAULT_SKIP_LOAD];
+
+    if (partial_bytes &&
+        (rc = from_cuda((cudaError_t)launch_ffn_clear(p.flags, pl.grid * kFfnEpiWarps, c.stream))) != FFN_OK)
+        return rc;
+    cudaLaunchConfig_t cfg = {};
+    cudaLaunchAttribute attr[2];
+    cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
+    cfg.blockDim = dim3(kFfnThreads, 1, 1);
+    cfg.dynamicSmemBytes = pl.smem;
+    cfg.stream = c.stream;
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    const int together = pl.cta_group * pl.cluster;  // one of the two is 1
+    attr[1].val.clusterDim.x = (unsigned)together;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = together > 1 ? 2 : 1;
+    void *args[2] = {&maps, &p};
+    last_plan = pl;
+    last_packed = packed;
+    have_last_plan = true;
+    return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
+}
+
+// --------------------------------------------------------------- checks
+bool bad_dim(int64_t n) { return n < 0 || n > kMaxDim; }
+
+// A matrix that must be there (if it has elements), with rows that do not overlap.
+bool bad_matrix(const ffn_matrix &m, int64_t rows, int64_t cols, int esize = 2)
+{
+    if (rows == 0 || cols == 0)
+        return false;
+    return !m.data || !aligned(m.data, (uintptr_t)esize) || (rows > 1 && (m.ld < cols || m.ld > kMaxPitch));
+}
+
+int check_quantized(const ffn_quantized &q, int64_t rows, int64_t cols, int64_t step)
+{
+    if (rows == 0 || cols == 0)
+        return FFN_OK;
+    if (!q.codes || !q.scales || q.ld < cols || q.ld > kMaxPitch)
+        return FFN_ERR_INVALID_ARG;
+    return aligned(q.codes, 16) && q.ld % step == 0 && aligned(q.scales, 4) ? FFN_OK : FFN_ERR_ALIGNMENT;
+}
+
+bool bad_act(int32_t a) { return a < FFN_ACT_NONE || a > FFN_ACT_GELU_TANH; }
+bool bad_type(int32_t t) { return t != FFN_BF16 && t != FFN_FP32; }
+
+// Bytes that a call reads or writes: rows of `width` bytes, `ld` bytes apart.
+struct Span {
+    const void *p;
+    int64_t ld, width, rows;
+    bool same_allowed = false;  // with the first result
+};
+
+Span span(const ffn_matrix &m, int64_t rows, int64_t cols, int esize = 2) { return {m.data, m.ld * esize, cols * esize, rows}; }
+
+// Whether two spans share a byte; spans of different pitches that reach over each other count as sharing.
+bool touch(const Span &a, const Span &b)
+{
+    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1)
+        return false;
+    using Wide = __int128;
+    const Wide at_a = (Wide) reinterpret_cast<uintptr_t>(a.p), at_b = (Wide) reinterpret_cast<uintptr_t>(b.p);
+    if (at_a + (Wide)(a.rows - 1) * a.ld + a.width <= at_b || at_b + (Wide)(b.rows - 1) * b.ld + b.width <= at_a)
+        return false;
+    if (a.rows == 1 || b.rows == 1 || a.ld != b.ld)
+        return true;
+    // one pitch: b's rows start d bytes behind a's, or behind the row before
+    Wide d = (at_b - at_a) % a.ld;
+    if (d < 0)
+        d += a.ld;
+    return d < a.width || d + b.width > a.ld;
+}
+
+// Results lie apart from what is read and from each other.
+bool apart(std::initializer_list<Span> writes, std::initializer_list<Span> reads)
+{
+    for (const Span *w = writes.begin(); w != writes.end(); ++w) {
+        for (const Span *o = w + 1; o != writes.end(); ++o)
+            if (touch(*w, *o))
+                return false;
+        for (const Span &r : reads) {
+            if (r.same_allowed && w == writes.begin() && r.p == w->p && r.width == w->width &&
+                (r.ld == w->ld || r.rows == 1))
+                continue;
+            if (touch(*w, r))
+                return false;
+        }
+    }
+    return true;
+}
+
+// Checks the workspace and runs `body` to measure it, then in earnest.
+template <typename F>
+int run_call(F body, void *workspace, int64_t size, void *stream)
+{
+    Call c;
+    int rc = current_device(&c.dev);
+    if (rc != FFN_OK)
+        return rc;
+    if ((rc = body(c)) != FFN_OK)
+        return rc;
+    const size_t need = c.used + c.shared;
+    if (need && (!workspace || size < (int64_t)need))
+        return FFN_ERR_WORKSPACE;
+    if (need && !aligned(workspace, 16))
+        return FFN_ERR_ALIGNMENT;
+    Call run;
+    run.dev = c.dev;
+    run.stream = static_cast<cudaStream_t>(stream);
+    static uint8_t none;  // never used: such a call takes nothing
+    run.base = need ? static_cast<uint8_t *>(workspace) : &none;
+    run.shared = c.used;  // where the split tiles' part starts
+    return body(run);
+}
+
+template <typename F>
+int measure_call(F body, int64_t *bytes)
+{
+    Call c;
+    int rc = current_device(&c.dev);
+    if (rc != FFN_OK)
+        return rc;
+    if ((rc = body(c)) == FFN_OK)
+        *bytes = (int64_t)(c.used + c.shared);
+    return rc;
+}
+
+// --------------------------------------------------------------- linear
+int check_linear(const ffn_linear_args &a)
+{
+    if (bad_dim(a.M) || bad_dim(a.N) || bad_dim(a.K) || bad_act(a.activation) || bad_type(a.y_type) ||
+        (a.bias && bad_type(a.bias_type)))
+        return FFN_ERR_INVALID_ARG;
+    const int esize = a.y_type == FFN_FP32 ? 4 : 2;
+    const bool out = a.M > 0 && a.N > 0;
+    if (bad_matrix(a.y, a.M, a.N, esize) || (out && (bad_matrix(a.x, a.M, a.K) || bad_matrix(a.weight, a.N, a.K))) ||
+        (a.residual.data && bad_matrix(a.residual, a.M, a.N)) || (a.z.data && bad_matrix(a.z, a.M, a.N)))
+        return FFN_ERR_INVALID_ARG;
+    const int bsize = a.bias_type == FFN_FP32 ? 4 : 2;
+    if (a.bias && !aligned(a.bias, (uintptr_t)bsize))
+        return FFN_ERR_ALIGNMENT;
+    Span residual = span(a.residual, a.M, a.N);
+    residual.same_allowed = true;
+    if (!apart({span(a.y, a.M, a.N, esize), span(a.z, a.M, a.N)},
+               {span(a.x, a.M, a.K), span(a.weight, a.N, a.K), residual, {a.bias, 0, a.N * bsize, 1}}))
+        return FFN_ERR_INVALID_ARG;
+    return FFN_OK;
+}
+
+int body_linear(Call &c, const ffn_linear_args &a)
+{
+    Product x;
+    x.M = a.M, x.N = a.N, x.K = a.K;
+    x.A[0] = {a.x.data, a.x.ld};
+    x.B[0] = {a.weight.data, a.weight.ld};
+    x.p.act = a.activation;
+    x.p.bias = a.bias;
+    x.p.bias_fp32 = a.bias_type == FFN_FP32;
+    x.p.aux[0] = aux_of(a.residual);
+    x.p.save = a.z.data ? 1 : 0;
+    const ffn_matrix D[2] = {a.y, a.z};
+    return run_product(c, x, D, 2, a.y_type == FFN_FP32);
+}
+
+int check_linear_backward(const ffn_linear_backward_args &a)
+{
+    if (bad_dim(a.M) || bad_dim(a.N) || bad_dim(a.K) || bad_act(a.activation) || bad_type(a.dweight_type))
+        return FFN_ERR_INVALID_ARG;
+    const int wsize = a.dweight_type == FFN_FP32 ? 4 : 2;
+    if (bad_matrix(a.dy, a.M, a.N) || (a.activation && bad_matrix(a.z, a.M, a.N)) ||
+        (a.dx.data && (bad_matrix(a.dx, a.M, a.K) || bad_matrix(a.weight, a.N, a.K))) ||
+        (a.dweight.data && (bad_matrix(a.dweight, a.N, a.K, wsize) || bad_matrix(a.x, a.M, a.K))) ||
+        !aligned(a.dbias, 4))
+        return FFN_ERR_INVALID_ARG;
+    if (!apart({span(a.dx, a.M, a.K), span(a.dweight, a.N, a.K, wsize), {a.dbias, 0, a.N * 4, 1}},
+               {span(a.dy, a.M, a.N), span(a.x, a.M, a.K), span(a.weight, a.N, a.K), span(a.z, a.M, a.N)}))
+        return FFN_ERR_INVALID_ARG;
+    return FFN_OK;
+}
+
+int body_linear_backward(Call &c, const ffn_linear_backward_args &a)
+{
+    ffn_matrix dz = a.dy;
+    const bool products = a.dx.data || a.dweight.data;
+    if (a.N > 0 && ((a.activation && products && a.M > 0) || a.dbias)) {
+        FfnSlopeParams s = {};
+        s.dy = static_cast<const uint16_t *>(a.dy.data);
+        s.lddy = a.dy.ld;
+        s.R = (int32_t)a.M, s.C = (int32_t)a.N;
+        s.vec = aligned(a.dy.data, 16) && (a.dy.ld % 8 == 0 || a.M <= 1);
+        s.act = a.activation;
+        if (a.activation) {
+            s.z = static_cast<const uint16_t *>(a.z.data);
+            s.ldz = a.z.ld;
+            s.vec = s.vec && aligned(a.z.data, 16) && (a.z.ld % 8 == 0 || a.M <= 1);
+            dz.ld = padded(a.N);
+            dz.data = c.take((size_t)(a.M * dz.ld) * 2);
+            s.dz = static_cast<uint16_t *>(dz.data);
+            s.lddz = dz.ld;
+        }
+        if (a.dbias) {
+            s.dbias = a.dbias;
+            const int slices = ffn_slope_slices(a.M, a.N, c.dev.sms);
+            s.partials = static_cast<float *>(c.take((size_t)slices * (size_t)a.N * sizeof(float)));
+        }
+        if (!c.measuring()) {
+            const int rc = from_cuda((cudaError_t)launch_ffn_slope(s, c.dev.sms, c.stream));
+            if (rc != FFN_OK)
+                return rc;
+        }
+    }
+    if (a.dx.data) {
+        Product x;
+        x.M = a.M, x.N = a.K, x.K = a.N;
+        x.b_mn = true;
+        x.A[0] = {dz.data, dz.ld};
+        x.B[0] = {a.weight.data, a.weight.ld};
+        const int rc = run_product(c, x, &a.dx, 1, false);
+        if (rc != FFN_OK)
+            return rc;
+    }
+    if (a.dweight.data) {
+        Product x;
+        x.M = a.N, x.N = a.K, x.K = a.M;
+        x.a_mn = x.b_mn = true;
+        x.A[0] = {dz.data, dz.ld};
+        x.B[0] = {a.x.data, a.x.ld};
+        return run_product(c, x, &a.dweight, 1, a.dweight_type == FFN_FP32);
+    }
+    return FFN_OK;
+}
+
+// --------------------------------------------------------------- gated
+int check_gated(const ffn_gated_args &a)
+{
+    if (bad_dim(a.M) || bad_dim(a.F) || bad_dim(a.C) || bad_act(a.activation))
+        return FFN_ERR_INVALID_ARG;
+    const bool bf16 = a.g.data || a.u.data, bits8 = a.qg.codes || a.qu.codes;
+    if (bad_matrix(a.h, a.M, a.F) || bad_matrix(a.x, a.M, a.C) || bad_matrix(a.w_gate, a.F, a.C) ||
+        bad_matrix(a.w_up, a.F, a.C) || (bf16 && bits8) ||
+        (bf16 && (!a.g.data || !a.u.data || bad_matrix(a.g, a.M, a.F) || bad_matrix(a.u, a.M, a.F))))
+        return FFN_ERR_INVALID_ARG;
+    if (bits8) {
+        for (const ffn_quantized *q : {&a.qg, &a.qu}) {
+            const int rc = check_quantized(*q, a.M, a.F, 128);
+            if (rc != FFN_OK)
+                return rc;
+        }
+    }
+    const int64_t words = ceil_div(a.F, 512) * a.M * 4;
+    // whole rows of codes: bytes behind a row's last code may be written
+    if (!apart({span(a.h, a.M, a.F), span(a.g, a.M, a.F), span(a.u, a.M, a.F), {a.qg.codes, a.qg.ld, a.qg.ld, a.M},
+                {a.qu.codes, a.qu.ld, a.qu.ld, a.M}, {a.qg.scales, 0, words, 1}, {a.qu.scales, 0, words, 1}},
+               {span(a.x, a.M, a.C), span(a.w_gate, a.F, a.C), span(a.w_up, a.F, a.C)}))
+        return FFN_ERR_INVALID_ARG;
+    return FFN_OK;
+}
+
+int body_gated(Call &c, const ffn_gated_args &a)
+{
+    Product x;
+    x.epilogue = kFfnGated;
+    x.form = kDual;
+    x.M = a.M, x.N = a.F, x.K = a.C;
+    x.A[0] = {a.x.data, a.x.ld};
+    x.B[0] = {a.w_gate.data, a.w_gate.ld};
+    x.B[1] = {a.w_up.data, a.w_up.ld};
+    x.p.act = a.activation;
+    x.p.save = a.g.data ? 1 : a.qg.codes ? 2 : 0;
+    if (x.p.save == 2) {
+        // a thread sees a whole block of a row's sums only where rows are on the row side and a
+        // tile's sums lie in one CTA
+        x.no_split = x.not_transposed = true;
+        x.p.codes[0] = static_cast<uint8_t *>(a.qg.codes);
+        x.p.codes[1] = static_cast<uint8_t *>(a.qu.codes);
+        x.p.scales[0] = static_cast<uint8_t *>(a.qg.scales);
+        x.p.scales[1] = static_cast<uint8_t *>(a.qu.scales);
+        x.p.ldq[0] = a.qg.ld;
+        x.p.ldq[1] = a.qu.ld;
+    }
+    const ffn_matrix D[3] = {a.h, a.g, a.u};
+    return run_product(c, x, D, 3, false);
+}
+
+int check_gated_backward(const ffn_gated_backward_args &a)
+{
+    if (bad_dim(a.M) || bad_dim(a.F) || bad_dim(a.C) || bad_dim(a.N) || bad_act(a.activation) ||
+        bad_type(a.dweight_type))
+        return FFN_ERR_INVALID_ARG;
+    const int wsize = a.dweight_type == FFN_FP32 ? 4 : 2;
+    const bool bf16 = a.g.data || a.u.data, bits8 = a.qg.codes || a.qu.codes;
+    if (bf16 && bits8)
+        return FFN_ERR_INVALID_ARG;
+    if (bits8) {
+        for (const ffn_quantized *q : {&a.qg, &a.qu}) {
+            const int rc = check_quantized(*q, a.M, a.F, 16);
+            if (rc != FFN_OK)
+                return rc;
+        }
+    } else if (bad_matrix(a.g, a.M, a.F) || bad_matrix(a.u, a.M, a.F)) {
+        return FFN_ERR_INVALID_ARG;
+    }
+    if (bad_matrix(a.dy, a.M, a.N) || bad_matrix(a.w_down, a.N, a.F) || !a.dw_gate.data != !a.dw_up.data ||
+        (a.dx.data &&
+         (bad_matrix(a.dx, a.M, a.C) || bad_matrix(a.w_gate, a.F, a.C) || bad_matrix(a.w_up, a.F, a.C))) ||
+        (a.dw_gate.data && (bad_matrix(a.dw_gate, a.F, a.C, wsize) || bad_matrix(a.dw_up, a.F, a.C, wsize) ||
+                            bad_matrix(a.x, a.M, a.C))) ||
+        (a.dw_down.data && bad_matrix(a.dw_down, a.N, a.F, wsize)))
+        return FFN_ERR_INVALID_ARG;
+    const int64_t words = ceil_div(a.F, 512) * a.M * 4;
+    if (!apart({span(a.dx, a.M, a.C), span(a.dw_gate, a.F, a.C, wsize), span(a.dw_up, a.F, a.C, wsize),
+                span(a.dw_down, a.N, a.F, wsize)},
+               {span(a.dy, a.M, a.N), span(a.x, a.M, a.C), span(a.g, a.M, a.F), span(a.u, a.M, a.F),
+                {a.qg.codes, a.qg.ld, a.F, a.M}, {a.qu.codes, a.qu.ld, a.F, a.M}, {a.qg.scales, 0, words, 1},
+                {a.qu.scales, 0, words, 1}, span(a.w_gate, a.F, a.C), span(a.w_up, a.F, a.C), span(a.w_down, a.N, a.F)}))
+        return FFN_ERR_INVALID_ARG;
+    return FFN_OK;
+}
+
+int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
+{
+    ffn_matrix t[3];  // dg, du, h
+    for (ffn_matrix &m : t) {
+        m.ld = padded(a.F);
+        m.data = c.take((size_t)(a.M * m.ld) * 2);
+        if (c.measuring())
+            m.data = nullptr;
+    }
+    int rc;
+    {
+        Product x;
+        x.epilogue = kFfnGrad;
+        x.M = a.M, x.N = a.F, x.K = a.N;
+        x.b_mn = true;
+        x.A[0] = {a.dy.data, a.dy.ld};
+        x.B[0] = {a.w_down.data, a.w_down.ld};
+        x.p.act = a.activation;
+        const bool bits8 = a.qg.codes != nullptr;
+        x.p.aux[0] = bits8 ? aux_of(a.qg) : aux_of(a.g);
+        x.p.aux[1] = bits8 ? aux_of(a.qu) : aux_of(a.u);
+        if ((rc = run_product(c, x, t, 3, false)) != FFN_OK)
+            return rc;
+    }
+    if (a.dx.data) {
+        Product x;
+        x.form = kSum;
+        x.M = a.M, x.N = a.C, x.K = a.F;
+        x.b_mn = true;
+        x.A[0] = {t[0].data, t[0].ld};
+        x.A[1] = {t[1].data, t[1].ld};
+        x.B[0] = {a.w_gate.data, a.w_gate.ld};
+        x.B[1] = {a.w_up.data, a.w_up.ld};
+        if ((rc = run_product(c, x, &a.dx, 1, false)) != FFN_OK)
+            return rc;
+    }
+    if (a.dw_gate.data) {
+        Product x;
+        x.form = kStack;
+        x.M = a.F, x.N = a.C, x.K = a.M;
+        x.a_mn = x.b_mn = true;
+        x.A[0] = {t[0].data, t[0].ld};
+        x.A[1] = {t[1].data, t[1].ld};
+        x.B[0] = {a.x.data, a.x.ld};
+        const ffn_matrix D[2] = {a.dw_gate, a.dw_up};
+        if ((rc = run_product(c, x, D, 2, a.dweight_type == FFN_FP32)) != FFN_OK)
+            return rc;
+    }
+    if (a.dw_down.data) {
+        Product x;
+        x.M = a.N, x.N = a.F, x.K = a.M;
+        x.a_mn = x.b_mn = true;
+        x.A[0] = {a.dy.data, a.dy.ld};
+        x.B[0] = {t[2].data, t[2].ld};
+        return run_product(c, x, &a.dw_down, 1, a.dweight_type == FFN_FP32);
+    }
+    return FFN_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+FFN_API const char *ffn_strerror(int status)
+{
+    switch (status) {
+    case FFN_OK: return "ok";
+    case FFN_ERR_INVALID_ARG: return "invalid argument";
+    case FFN_ERR_ALIGNMENT: return "alignment of a pointer or a pitch";
+    case FFN_ERR_WORKSPACE: return "the workspace is missing or too small";
+    case FFN_ERR_CUDA: return "a CUDA runtime call failed";
+    case FFN_ERR_TENSORMAP: return "TMA tensor-map encoding failed";
+    case FFN_ERR_DEVICE_TIMEOUT: return "device watchdog: a barrier wait ran out and the kernel returned early";
+    case FFN_ERR_UNSUPPORTED: return "unsupported device, size or option combination";
+    default: return "unknown status";
+    }
+}
+
+FFN_API const char *ffn_version(void) { return "ffn_ops 1.0 sm_103a"; }
+
+FFN_API int ffn_set_option(int key, int64_t value)
+{
+    bool ok = false;
+    switch (key) {
+    case FFN_OPT_CTA_GROUP: ok = value >= 0 && value <= 2; break;
+    case FFN_OPT_TRANSPOSED: ok = value >= 0 && value <= 2; break;
+    case FFN_OPT_WIDTH: ok = value >= 0 && value <= kFfnMaxWidth && value % 16 == 0; break;
+    case FFN_OPT_SPLIT: ok = value >= 0 && value <= 2; break;
+    // far above what any load takes to land: the CTAs of a pair that give up at different
+    // times count on each other's having landed
+    case FFN_OPT_WATCHDOG_NS: ok = value >= 100000 && value <= 60000000000LL; break;
+    case FFN_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
+    case FFN_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
+    default: break;
+    }
+    if (!ok)
+        return FFN_ERR_INVALID_ARG;
+    options.v[key] = value;
+    return FFN_OK;
+}
+
+FFN_API int ffn_get_option(int key, int64_t *value)
+{
+    if (!value || key < 1 || key >= kNumOptions)
+        return FFN_ERR_INVALID_ARG;
+    *value = options.v[key];
+    return FFN_OK;
+}
+
+FFN_API int ffn_plan_info(ffn_plan_info_t *info)
+{
+    if (!info || !have_last_plan)
+        return FFN_ERR_INVALID_ARG;
+    std::memset(info, 0, sizeof(*info));
+    info->tiles = last_plan.tiles;
+    info->k_blocks = last_plan.k_blocks;
+    info->grid_ctas = last_plan.grid;
+    info->cta_group = last_plan.cta_group;
+    info->transposed = last_plan.transposed ? 1 : 0;
+    info->width = last_plan.width;
+    info->stages = last_plan.stages;
+    info->split_tiles = (int32_t)last_plan.sk_tiles;
+    info->cluster = last_plan.cluster;
+    info->packed = last_packed;
+    return FFN_OK;
+}
+
+#define FFN_ENTRY(name)                                                                                               \
+    FFN_API int ffn_##name##_workspace(const ffn_##name##_args *args, int64_t *bytes)                                 \
+    {                                                                                                                 \
+        if (!args || !bytes)                                                                                          \
+            return FFN_ERR_INVALID_ARG;                                                                               \
+        *bytes = 0;                                                                                                   \
+        const int rc = check_##name(*args);                                                                           \
+        return rc != FFN_OK ? rc : measure_call([args](Call &c) { return body_##name(c, *args); }, bytes);            \
+    }                                                                                                                 \
+    FFN_API int ffn_##name(const ffn_##name##_args *args, void *workspace, int64_t workspace_bytes, void *stream)     \
+    {                                                                                                                 \
+        if (!args)                                                                                                    \
+            return FFN_ERR_INVALID_ARG;                                                                               \
+        const int rc = check_##name(*args);                                                                           \
+        return rc != FFN_OK                                                                                           \
+                   ? rc                                                                                               \
+                   : run_call([args](Call &c) { return body_##name(c, *args); }, workspace, workspace_bytes, stream); \
+    }
+
+FFN_ENTRY(linear)
+FFN_ENTRY(linear_backward)
+FFN_ENTRY(gated)
+FFN_ENTRY(gated_backward)
+
+FFN_API int ffn_device_status(uint32_t *detail)
+{
+    if (detail)
+        *detail = 0;
+    uint32_t *const at = ffn_status_word();
+    if (!at)
+        return FFN_ERR_CUDA;
+    // the whole device: a launch may run again on any stream, from a graph that captured it
+    uint32_t word = 0;
+    if (cudaDeviceSynchronize() != cudaSuccess ||
+        cudaMemcpy(&word, at, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess)
+        return from_cuda(cudaErrorUnknown);
+    if (word == 0)
+        return FFN_OK;
+    if (detail)
+        *detail = word;
+    const uint32_t none = 0;
+    if (cudaMemcpy(at, &none, sizeof(none), cudaMemcpyHostToDevice) != cudaSuccess)
+        return from_cuda(cudaErrorUnknown);
+    return FFN_ERR_DEVICE_TIMEOUT;
+}
+
+}  // extern "C"

@@ -1,0 +1,1125 @@
+// The bf16 products of a feed-forward block, with what follows them in the epilogue.
+//
+//   plain   S = sum over k of A B (or of two products, added up); D0 = act(S + bias) + residual, D1 = S + bias
+//   gated   S = x Wg^T and S2 = x Wu^T over the same x; D0 = act(S) S2, and S and S2 kept in bf16 or 8 bits
+//   grad    S = dh = dy Wd, with g and u: D0 = dh u act'(g), D1 = dh act(g), D2 = act(g) u
+//
+// Either operand may be contiguous along k or along its rows, so a forward product, an input's
+// gradient (the weight is contiguous along the columns of the result) and a weight's gradient
+// (both operands are contiguous along their rows) are the same kernel: tcgen05.mma reads
+// both forms from shared memory, by the descriptors' strides and a bit of the instruction
+// descriptor, and nothing is transposed in memory.
+//
+// One operand is on the MMA's row side (128 rows to a CTA, 256 to an SM pair), the other on
+// its column side (`width` columns to a tile).  For few tokens the weights take the row side,
+// and the accumulator holds the result transposed.  A gated tile keeps two accumulators: next
+// to each other as one MMA of 256 columns, 128 of each weight, or, transposed, one per weight
+// and 128 rows of it, so that either way one thread holds both sums of an element.
+//
+// Roles (384 threads, one CTA per SM):
+//   warp 0           TMA producer: per (item, k-block) wait "empty", load the tiles
+//   warp 1           MMA issuer (leader CTA only in pairs), one elected lane
+//   warp 2           allocates and frees tensor memory
+//   warps 4..11      epilogue: tensor memory -> registers -> results
+//
+// Work: tiles [0, sk_tiles) are split along k, their (tile, k-block) units cut into one
+// contiguous range per cluster; the other tiles are walked whole.  The pieces of a split tile
+// meet as fp32 through global memory, or, where the CTAs of a thread-block cluster share a
+// tile, through distributed shared memory; they are added in range order by the piece that
+// holds k-block 0, so the result is the same every time.  Every wait is bounded by the
+// watchdog (WaitCtl in ptx.cuh).
+#pragma once
+
+#include <stdint.h>
+
+#include "ffn_kernels.h"
+#include "ffn_math.cuh"
+#include "fp8_ptx.cuh"
+#include "gemm_common.cuh"
+
+namespace wstma {
+
+// Copies and MMAs in flight are waited for at a CTA's end however short the watchdog's limit is.
+constexpr uint64_t kFfnDrainNs = 20000000;
+
+struct FfnItem {
+    int32_t tile, kb0, kb1;
+};
+
+__host__ __device__ __forceinline__ int64_t ffn_range_begin(int64_t units, int32_t clusters, int32_t c)
+{
+    return (int64_t)c * units / clusters;
+}
+
+__host__ __device__ __forceinline__ bool ffn_range_holds(int64_t units, int32_t clusters, int32_t c)
+{
+    return ffn_range_begin(units, clusters, c) < ffn_range_begin(units, clusters, c + 1);
+}
+
+// The range that holds unit u.
+__host__ __device__ __forceinline__ int32_t ffn_range_of(int64_t units, int32_t clusters, int64_t u)
+{
+    return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
+}
+
+// A cluster's items in order: its range of the split tiles' units (a range is no longer than a
+// tile, since sk_tiles < clusters, so it touches at most two tiles), then every clusters-th
+// whole tile.  A range's first piece may start inside a tile (it then leaves a partial); a piece
+// that starts at k-block 0 and does not reach the tile's end is the last of its range.  So no
+// cluster waits for a partial before it has left its own.
+struct FfnWork {
+    int64_t u, u_end;
+    int32_t dp, C, T, KB;
+
+    __host__ __device__ __forceinline__ void init(const FfnParams &p, int32_t cluster, int32_t clusters)
+    {
+        KB = p.num_k_blocks;
+        C = clusters;
+        T = p.num_tiles;
+        dp = p.sk_tiles + cluster;
+        u = ffn_range_begin(p.sk_units, clusters, cluster);
+        u_end = ffn_range_begin(p.sk_units, clusters, cluster + 1);
+    }
+
+    __host__ __device__ __forceinline__ bool next(FfnItem &w)
+    {
+        if (u < u_end) {
+            const int64_t t = u / KB;
+            const int64_t k0 = u - t * KB;
+            const int64_t k1 = k0 + (u_end - u) < KB ? k0 + (u_end - u) : KB;
+            w.tile = (int32_t)t;
+            w.kb0 = (int32_t)k0;
+            w.kb1 = (int32_t)k1;
+            u += k1 - k0;
+            return true;
+        }
+        if (dp < T) {
+            w.tile = dp;
+            w.kb0 = 0;
+            w.kb1 = KB;
+            dp += C;
+            return true;
+        }
+        return false;
+    }
+};
+
+struct FfnTile {
+    int32_t row, col;
+};
+
+// Tile -> (row tile, column tile): bands of raster_group row tiles, walked column by column, odd
+// bands right to left, so that tiles running at the same time share operands in L2.
+__host__ __device__ __forceinline__ FfnTile ffn_tile_coord(int32_t t, const FfnParams &p)
+{
+    const int64_t span = (int64_t)p.raster_group * p.num_col_tiles;
+    const int32_t band = (int32_t)(t / span);
+    const int32_t first = band * p.raster_group;
+    const int32_t rows = p.num_row_tiles - first < p.raster_group ? p.num_row_tiles - first : p.raster_group;
+    const int32_t r = (int32_t)(t - band * span);
+    const int32_t col = r / rows;
+    return {first + r % rows, (band & 1) ? p.num_col_tiles - 1 - col : col};
+}
+
+// ---------------------------------------------------------------- PTX of this kernel
+// Shared-memory descriptor of an operand that is contiguous along its rows, as TMA lays it out
+// with 128-byte swizzling: chunks of 64 rows x 64 k, a k of a chunk in 128 bytes, 8 k's in 1024
+// (the stride offset), chunks 8192 bytes apart (the leading offset).  The other fields are as
+// in smem_desc_sw128.  Advancing k by 16 adds 2048 bytes.
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t saddr)
+{
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr & 0x3FFFFu) >> 4);
+    d |= (uint64_t)(8192u >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+
+// D[tmem] (+)= R C^T over a block of 64 elements of k, as four MMAs of 16 whose operands are
+// rstep and cstep (in 16 bytes) apart.  Probes the barrier of the next block on the way, so that
+// the probe's latency passes while the MMAs issue: 1 if its phase has completed.
+template <int CG>
+__device__ __forceinline__ uint32_t mma_bf16_block(uint32_t d_tmem, uint64_t rdesc, uint64_t cdesc, uint32_t idesc,
+                                                   uint64_t rstep, uint64_t cstep, uint32_t accumulate,
+                                                   uint32_t leader, uint32_t next_bar, uint32_t next_parity)
+{
+    uint32_t ready;
+    if constexpr (CG == 1)
+        asm volatile(
+            "{\n\t.reg .pred p, q, w;\n\t.reg .u64 a, b;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 w, [%9], %10;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "setp.ne.b32 q, %8, 0;\n\t"
+            "mov.u64 a, %2;\n\tmov.u64 b, %3;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "setp.ne.b32 p, 1, 0;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::1.kind::f16 [%1], a, b, %4, p;\n\t"
+            "selp.u32 %0, 1, 0, w;\n\t}"
+            : "=r"(ready)
+            : "r"(d_tmem), "l"(rdesc), "l"(cdesc), "r"(idesc), "l"(rstep), "l"(cstep), "r"(accumulate), "r"(leader),
+              "r"(next_bar), "r"(next_parity)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p, q, w;\n\t.reg .u64 a, b;\n\t"
+            "mbarrier.test_wait.parity.shared::cta.b64 w, [%9], %10;\n\t"
+            "setp.ne.b32 p, %7, 0;\n\t"
+            "setp.ne.b32 q, %8, 0;\n\t"
+            "mov.u64 a, %2;\n\tmov.u64 b, %3;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "setp.ne.b32 p, 1, 0;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, p;\n\t"
+            "add.u64 a, a, %5;\n\tadd.u64 b, b, %6;\n\t"
+            "@q tcgen05.mma.cta_group::2.kind::f16 [%1], a, b, %4, p;\n\t"
+            "selp.u32 %0, 1, 0, w;\n\t}"
+            : "=r"(ready)
+            : "r"(d_tmem), "l"(rdesc), "l"(cdesc), "r"(idesc), "l"(rstep), "l"(cstep), "r"(accumulate), "r"(leader),
+              "r"(next_bar), "r"(next_parity)
+            : "memory");
+    return ready;
+}
+
+// All but the newest committed bulk store of this thread have finished reading shared memory.
+__device__ __forceinline__ void bulk_wait_read_all_but_one()
+{
+    asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+}
+
+// ---------------------------------------------------------------- results through shared memory
+// A piece of a result, staged in shared memory as 32 rows of 64 bytes (32 columns of bf16, 16 of
+// fp32) in the TMA swizzle of that row size: byte offset of byte `byte` of row r.
+__device__ __forceinline__ uint32_t ffn_piece_offset(uint32_t r, uint32_t byte)
+{
+    return r * 64u + (((byte >> 4) ^ ((r >> 1) & 3u)) << 4) + (byte & 15u);
+}
+
+// A warp's two staging buffers, used in turn; every use ends with a commit, so that all but the
+// newest group is what used the buffer that comes next.
+struct FfnStager {
+    uint32_t base;
+    int lane;
+    uint32_t slot;
+
+    __device__ __forceinline__ uint32_t acquire()
+    {
+        if (lane == 0)
+            bulk_wait_read_all_but_one();
+        __syncwarp();
+        const uint32_t at = base + slot * kFfnPieceBytes;
+        slot ^= 1u;
+        return at;
+    }
+};
+
+// Stores a staged piece at out[y..y+31][x..] by a TMA store, or, where the layout or the last
+// columns do not allow one (a TMA store writes whole 16-byte groups), by the warp, a row at a
+// time, an element a lane.
+__device__ __forceinline__ void ffn_store_piece(uint32_t at, int lane, const CUtensorMap *map, const FfnOut &out,
+                                                int32_t x, int32_t y, bool fp32, int32_t D_rows, int32_t D_cols)
+{
+    const int32_t wide = fp32 ? 16 : 32;
+    if (out.tma && (x + wide <= D_cols || D_cols % (fp32 ? 4 : 8) == 0)) {
+        fence_proxy_async_shared();
+        __syncwarp();
+        if (lane == 0) {
+            if (x < D_cols && y < D_rows)
+                tma_store_2d(map, at, x, y);
+            bulk_commit_group();
+        }
+        return;
+    }
+    __syncwarp();
+    const int32_t rows = D_rows - y < 32 ? D_rows - y : 32;
+    if (fp32) {
+        // half a warp a row
+        const int32_t c = lane & 15;
+        if (x + c < D_cols) {
+            float *dst = static_cast<float *>(out.p) + (int64_t)y * out.ld + x + c;
+            for (int32_t r = lane >> 4; r < rows; r += 2)
+                dst[r * out.ld] = __uint_as_float(ld_shared_u32(at + ffn_piece_offset((uint32_t)r, 4u * (uint32_t)c)));
+        }
+    } else if (x + lane < D_cols) {
+        uint16_t *dst = static_cast<uint16_t *>(out.p) + (int64_t)y * out.ld + x + lane;
+        for (int32_t r = 0; r < rows; r += 8) {  // eight rows' loads come before their stores
+            uint16_t w[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                asm volatile("ld.shared.u16 %0, [%1];"
+                             : "=h"(w[k])
+                             : "r"(at + ffn_piece_offset((uint32_t)(r + k), 2u * (uint32_t)lane))
+                             : "memory");
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (r + k < rows)
+                    *dst = w[k];
+                dst += out.ld;
+            }
+        }
+    }
+    __syncwarp();
+    if (lane == 0)
+        bulk_commit_group();
+}
+
+// Stores a chunk of 32 x 32 results: w holds pairs of bf16.  Not transposed: thread = row `row`
+// + lane, pairs along the columns from `col`.  Transposed: thread = column `col` + lane, pairs
+// along the rows.
+template <bool kT>
+__device__ __forceinline__ void ffn_store_bf16(const uint32_t (&w)[16], FfnStager &st, const CUtensorMap *map,
+                                               const FfnOut &out, int32_t row, int32_t col, const FfnParams &p)
+{
+    const uint32_t at = st.acquire();
+    if constexpr (kT) {
+        const int32_t live = p.D_rows - row;
+#pragma unroll
+        for (uint32_t i = 0; i < 16; ++i) {
+            if ((int32_t)(2 * i) >= live)
+                break;
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + ffn_piece_offset(2 * i, 2u * (uint32_t)st.lane)),
+                         "h"((uint16_t)w[i])
+                         : "memory");
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + ffn_piece_offset(2 * i + 1, 2u * (uint32_t)st.lane)),
+                         "h"((uint16_t)(w[i] >> 16))
+                         : "memory");
+        }
+    } else {
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u)
+            st_shared_v4(at + ffn_piece_offset((uint32_t)st.lane, 16u * u), w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                         w[4 * u + 3]);
+    }
+    ffn_store_piece(at, st.lane, map, out, col, row, false, p.D_rows, p.D_cols);
+}
+
+template <bool kT>
+__device__ __forceinline__ void ffn_store_fp32(const float (&v)[32], FfnStager &st, const CUtensorMap *map,
+                                               const FfnOut &out, int32_t row, int32_t col, const FfnParams &p)
+{
+    if constexpr (kT) {
+        // lanes 0-15 fill one piece, 16-31 the other: both buffers are free first
+        const uint32_t first = st.acquire();
+        if (st.lane == 0)
+            bulk_wait_read_all();
+        __syncwarp();
+        const uint32_t second = first == st.base ? st.base + kFfnPieceBytes : st.base;
+        const uint32_t mine = st.lane < 16 ? first : second;
+        const int32_t live = p.D_rows - row;
+#pragma unroll
+        for (uint32_t i = 0; i < 32; ++i) {
+            if ((int32_t)i >= live)
+                break;
+            st_shared_u32(mine + ffn_piece_offset(i, 4u * ((uint32_t)st.lane & 15u)), __float_as_uint(v[i]));
+        }
+        ffn_store_piece(first, st.lane, map, out, col, row, true, p.D_rows, p.D_cols);
+        st.slot ^= 1u;
+        ffn_store_piece(second, st.lane, map, out, col + 16, row, true, p.D_rows, p.D_cols);
+    } else {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t at = st.acquire();
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                st_shared_v4(at + ffn_piece_offset((uint32_t)st.lane, 16u * u), __float_as_uint(v[16 * h + 4 * u]),
+                             __float_as_uint(v[16 * h + 4 * u + 1]), __float_as_uint(v[16 * h + 4 * u + 2]),
+                             __float_as_uint(v[16 * h + 4 * u + 3]));
+            ffn_store_piece(at, st.lane, map, out, col + 16 * h, row, true, p.D_rows, p.D_cols);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- what an epilogue reads
+// Raw words of a chunk of an FfnAux for this thread: 32 bf16 as 16 words, or 32 codes as 8 words
+// and their scale's byte.
+struct FfnRaw {
+    uint32_t w[16];
+};
+
+// Not transposed, aligned rows: 32 columns of this thread's row, by 16 bytes.  Asynchronous to
+// what follows until the words are used.
+__device__ __forceinline__ void ffn_load_rows(FfnRaw &x, const FfnAux &a, int32_t row, int32_t col, const FfnParams &p)
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        x.w[i] = 0u;
+    if (row >= p.D_rows)
+        return;
+    if (a.scales) {
+        const uint8_t *const src = static_cast<const uint8_t *>(a.p) + (int64_t)row * a.ld + col;
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+            if (col + 16 * u < p.D_cols) {  // rows are whole groups of 16
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src + 16 * u));
+                x.w[4 * u] = q.x, x.w[4 * u + 1] = q.y, x.w[4 * u + 2] = q.z, x.w[4 * u + 3] = q.w;
+            }
+        if (col < p.D_cols)
+            x.w[8] = __ldg(a.scales + ((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3));
+        return;
+    }
+    const uint16_t *const src = static_cast<const uint16_t *>(a.p) + (int64_t)row * a.ld + col;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        if (col + 8 * u + 8 <= p.D_cols) {
+            const uint4 q = *reinterpret_cast<const uint4 *>(src + 8 * u);
+            x.w[4 * u] = q.x, x.w[4 * u + 1] = q.y, x.w[4 * u + 2] = q.z, x.w[4 * u + 3] = q.w;
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (col + 8 * u + i < p.D_cols)
+                    x.w[4 * u + (i >> 1)] |= (uint32_t)src[8 * u + i] << (16 * (i & 1));
+        }
+    }
+}
+
+// Not transposed, any rows: read by the warp a row at a time, an element a lane, and turned
+// through a staging buffer.
+__device__ __forceinline__ void ffn_load_rows_any(FfnRaw &x, FfnStager &st, const FfnAux &a, int32_t row0, int32_t col,
+                                                  const FfnParams &p)
+{
+    const uint32_t at = st.acquire();
+    const uint16_t *src = static_cast<const uint16_t *>(a.p) + (int64_t)row0 * a.ld + col + st.lane;
+    const int32_t rows = col + st.lane < p.D_cols ? p.D_rows - row0 : 0;
+    for (int32_t r = 0; r < 32; r += 8) {
+        uint16_t w[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            w[k] = r + k < rows ? src[(r + k) * a.ld] : (uint16_t)0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + ffn_piece_offset((uint32_t)(r + k), 2u * (uint32_t)st.lane)),
+                         "h"(w[k])
+                         : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (uint32_t u = 0; u < 4; ++u)
+        ld_shared_v4(at + ffn_piece_offset((uint32_t)st.lane, 16u * u), x.w[4 * u], x.w[4 * u + 1], x.w[4 * u + 2],
+                     x.w[4 * u + 3]);
+    __syncwarp();
+    if (st.lane == 0)
+        bulk_commit_group();
+}
+
+// Transposed: column `col` (this thread's) of rows row .. row+31, as fp32.
+__device__ __forceinline__ void ffn_load_column(float (&v)[32], const FfnAux &a, int32_t row, int32_t col,
+                                                const FfnParams &p)
+{
+    const int32_t live = col < p.D_cols ? p.D_rows - row : 0;
+    if (a.scales) {
+        const uint8_t *const src = static_cast<const uint8_t *>(a.p) + (int64_t)row * a.ld + col;
+        const uint8_t *const sc = a.scales + ((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[i] = 0.0f;
+            if (i < live) {
+                float hi;
+                ffn_from_e4m3x2(src[i * a.ld], v[i], hi);
+                v[i] *= ffn_scale(sc[4 * i]);
+            }
+        }
+        return;
+    }
+    const uint16_t *const src = static_cast<const uint16_t *>(a.p) + (int64_t)row * a.ld + col;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = i < live ? __uint_as_float((uint32_t)src[i * a.ld] << 16) : 0.0f;
+}
+
+__device__ __forceinline__ void ffn_raw_floats(float (&v)[32], const FfnRaw &x, const FfnAux &a)
+{
+    if (a.scales) {
+        const float s = ffn_scale(x.w[8]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            ffn_from_e4m3x2(x.w[i >> 1] >> (16 * (i & 1)), v[2 * i], v[2 * i + 1]);
+            v[2 * i] *= s;
+            v[2 * i + 1] *= s;
+        }
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        v[2 * i] = bf16_low(x.w[i]);
+        v[2 * i + 1] = bf16_high(x.w[i]);
+    }
+}
+
+// Adds bias[at] (kT: one value, this thread's column) or bias[at .. at+31] to the sums.
+template <bool kT>
+__device__ __forceinline__ void ffn_add_bias(float (&v)[32], int32_t at, const FfnParams &p)
+{
+    if (p.bias == nullptr)
+        return;
+    if constexpr (kT) {
+        float b = 0.0f;
+        if (at < p.D_cols)
+            b = p.bias_fp32 ? static_cast<const float *>(p.bias)[at]
+                            : __uint_as_float((uint32_t) static_cast<const uint16_t *>(p.bias)[at] << 16);
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            v[i] += b;
+    } else if (p.bias_fp32) {
+        const float *const b = static_cast<const float *>(p.bias) + at;
+        if (at + 32 <= p.D_cols && (reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float4 q = __ldg(reinterpret_cast<const float4 *>(b) + u);
+                v[4 * u] += q.x, v[4 * u + 1] += q.y, v[4 * u + 2] += q.z, v[4 * u + 3] += q.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (at + i < p.D_cols)
+                    v[i] += __ldg(b + i);
+        }
+    } else {
+        const uint16_t *const b = static_cast<const uint16_t *>(p.bias) + at;
+        if (at + 32 <= p.D_cols && (reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(b) + u);
+                const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v[8 * u + 2 * i] += bf16_low(w[i]);
+                    v[8 * u + 2 * i + 1] += bf16_high(w[i]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (at + i < p.D_cols)
+                    v[i] += __uint_as_float((uint32_t)__ldg(b + i) << 16);
+        }
+    }
+}
+
+__device__ __forceinline__ void ffn_pack(uint32_t (&w)[16], const float (&v)[32])
+{
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        w[i] = bf16_pair(v[2 * i], v[2 * i + 1]);
+}
+
+__device__ __forceinline__ float *ffn_partial(float *partials, int32_t cta, int ew, int slot, int lane)
+{
+    return partials + (size_t)cta * kFfnPartialFloats + (size_t)((((ew * 4 + slot) * 8) * 32 + lane) * 4);
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int CG, bool kT, int kEpi>
+__global__ void __launch_bounds__(kFfnThreads, 1)
+    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnParams p)
+{
+    constexpr bool kPair = CG == 2;
+    constexpr bool kDual = kEpi == kFfnGated;
+    constexpr int kAccs = kDual ? 2 : 1;  // accumulators of an element
+    constexpr uint32_t kTileRBytes = (uint32_t)kFfnRowsPerCta * 128u;
+    constexpr uint32_t kRBytes = kTileRBytes * (kDual && kT ? 2u : 1u);
+    const int32_t width = p.width;
+    const uint32_t stage_bytes = kRBytes + (uint32_t)p.c_rows * 128u;  // a multiple of 1024
+
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const int S = p.stages;  // even: stages are released in pairs
+    const uint32_t stage0 = base;
+    const uint32_t staging0 = base + (uint32_t)S * stage_bytes;
+    const uint32_t full_bar = staging0 + kFfnEpiWarps * kFfnStagingBytes;
+    const uint32_t empty_bar = full_bar + 8u * S;
+    const uint32_t accf_bar = empty_bar + 8u * S;
+    const uint32_t acce_bar = accf_bar + 16u;
+    const uint32_t done_bar = acce_bar + 16u;
+    const uint32_t tmem_slot = done_bar + 8u;
+    const uint32_t abort_flag = tmem_slot + 4u;
+    const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
+    const uint32_t ready_bar = go_words + 8u;   // cluster form: one per epilogue warp of rank 0;
+                                                // behind its eight, one that nothing waits for
+
+    const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
+    const int lane = threadIdx.x & 31;
+    const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // in an SM pair
+    const bool shared_tile = !kPair && p.cluster > 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar + 8u * s, 1);
+            mbar_init(empty_bar + 8u * s, 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(accf_bar + 8u * a, 1);
+            mbar_init(acce_bar + 8u * a, kFfnEpiWarps * CG);
+        }
+        mbar_init(done_bar, 1);
+        mbar_init(ready_bar + 64u, 1);
+        if (shared_tile)
+            for (int e = 0; e < kFfnEpiWarps; ++e)
+                mbar_init(ready_bar + 8u * e, (uint32_t)p.cluster - 1u);  // that warp of every other rank
+        st_shared_u32(abort_flag, 0u);
+        fence_mbarrier_init();
+    }
+    if (threadIdx.x == 32) {
+        if (p.num_k_blocks) {  // an empty sum's operands have no maps
+            prefetch_tensormap(&maps.R[0]);
+            prefetch_tensormap(&maps.C[0]);
+        }
+        if (p.D[0].tma)
+            prefetch_tensormap(&maps.D[0]);
+    }
+    // all CTAs of a cluster have initialised their barriers before any cross-CTA
+    // arrive, TMA completion or the paired allocation
+    if (kPair || shared_tile) {
+        __syncwarp();
+        cluster_arrive_wait();
+    } else {
+        __syncthreads();
+    }
+    if (warp == 2) {
+        tmem_alloc<CG>(tmem_slot, 512);
+        tmem_relinquish<CG>();
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem_base = ld_shared_u32(tmem_slot);
+    // Up to here only shared and tensor memory was touched: it overlaps the
+    // previous kernel on the stream.  Every role that reads or writes global
+    // memory waits for that kernel first.
+
+    WaitCtl ctl;
+    ctl.abort_flag = abort_flag;
+    ctl.peer_abort_flag = kPair ? mapa_shared(abort_flag, rank ^ 1u) : 0u;
+    ctl.err = p.err;
+    ctl.set_limit(p.watchdog_ns);
+
+    const int32_t cluster_id = (int32_t)blockIdx.x / CG;
+    const int32_t num_clusters = (int32_t)gridDim.x / CG;
+    const int32_t KB = p.num_k_blocks;
+    FfnWork wi;
+    wi.init(p, cluster_id, num_clusters);
+    FfnItem w;
+
+    if (warp < 4) {
+        if (warp == 0) {
+            // ---------------- TMA producer ----------------
+            const uint32_t full_target = kPair ? mapa_shared(full_bar, 0u) : full_bar;
+            const uint32_t leader = elect_one();
+            int s = 0;
+            uint32_t ph = 0;
+            int32_t it = 0;
+            bool ok = true;
+            grid_dependency_wait();
+            while (ok && wi.next(w)) {
+                const FfnTile tc = ffn_tile_coord(w.tile, p);
+                const bool other = tc.row >= p.row_split;  // tiles of the second row operand
+                const int32_t yr =
+                    ((other ? tc.row - p.row_split : tc.row) * CG + (int32_t)rank) * kFfnRowsPerCta;
+                const int32_t yc = kDual && !kT ? tc.col * kFfnDualWidth
+                                                : tc.col * width + (int32_t)rank * (width / CG);
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (ring_group_first(s, 1u)) {
+                        const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
+                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                            !warp_wait<false>(ctl, bar, parity, kRoleProducer, (uint32_t)s, lane)) {
+                            ok = false;
+                            break;
+                        }
+                    }
+                    if (it != p.fault_skip_it) {
+                        if (rank == 0)
+                            expect_tx_elected(full_bar + 8u * s, stage_bytes * CG, leader);
+                        const uint32_t fb = full_target + 8u * s;
+                        const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
+                        const bool second = kb >= p.k_split;
+                        const int32_t k = (second ? kb - p.k_split : kb) * kFfnBlockK;
+                        if constexpr (kDual && kT) {
+                            tma_load_2d_elected<CG>(sa, &maps.R[0], k, yr, fb, leader);
+                            tma_load_2d_elected<CG>(sa + kTileRBytes, &maps.R[1], k, yr, fb, leader);
+                        } else {
+                            const CUtensorMap *mr = second || other ? &maps.R[1] : &maps.R[0];
+                            if (p.r_mn) {
+                                tma_load_2d_elected<CG>(sa, mr, yr, k, fb, leader);
+                                tma_load_2d_elected<CG>(sa + 8192u, mr, yr + 64, k, fb, leader);
+                            } else {
+                                tma_load_2d_elected<CG>(sa, mr, k, yr, fb, leader);
+                            }
+                        }
+                        const uint32_t sc = sa + kRBytes;
+                        if constexpr (kDual && !kT) {
+                            if constexpr (CG == 2) {
+                                // the pair's MMA takes its first 128 columns from rank 0, the rest from rank 1
+                                tma_load_2d_elected<CG>(sc, rank == 0 ? &maps.C[0] : &maps.C[1], k, yc, fb, leader);
+                            } else {
+                                tma_load_2d_elected<CG>(sc, &maps.C[0], k, yc, fb, leader);
+                                tma_load_2d_elected<CG>(sc + kTileRBytes, &maps.C[1], k, yc, fb, leader);
+                            }
+                        } else {
+                            const CUtensorMap *mc = second ? &maps.C[1] : &maps.C[0];
+                            if (p.c_mn) {
+                                for (int32_t j = 0; j < p.c_rows; j += 64)
+                                    tma_load_2d_elected<CG>(sc + (uint32_t)j * 128u, mc, yc + j, k, fb, leader);
+                            } else {
+                                tma_load_2d_elected<CG>(sc, mc, k, yc, fb, leader);
+                            }
+                        }
+                    }
+                    ++it;
+                    ring_advance(s, ph, S);
+                }
+            }
+            grid_launch_dependents();
+            // Teardown: the last S loads may still be in flight if a role gave up.
+            if (lane == 0 && rank == 0) {
+                ctl.limit_ns = max(ctl.limit_ns, kFfnDrainNs);
+                const int32_t n = it < S ? it : S;
+                for (int32_t d = 1; d <= n; ++d) {
+                    const int32_t j = it - d;
+                    if (j == p.fault_skip_it)
+                        continue;
+                    // one that runs out has outlasted the others' loads too
+                    if (!ctl.wait_drain<kPair>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
+                                               (uint32_t)ring_stage_of(j, S)))
+                        break;
+                }
+            } else if (lane == 0 && ctl.aborted()) {
+                // the peer's loads complete on the leader's barriers, which this CTA
+                // cannot poll: a fixed grace period instead
+                const uint64_t t0 = globaltimer_ns();
+                while (globaltimer_ns() - t0 < 50000ull) {
+                }
+            }
+            __syncwarp();
+        } else if (warp == 1 && rank == 0) {
+            // ---------------- MMA issuer ----------------
+            const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
+            const uint64_t cdesc0 = p.c_mn ? smem_desc_mn_sw128(stage0 + kRBytes) : smem_desc_sw128(stage0 + kRBytes);
+            const uint64_t rstep = p.r_mn ? 2048u >> 4 : 32u >> 4, cstep = p.c_mn ? 2048u >> 4 : 32u >> 4;
+            const int32_t mma_n = kDual && !kT ? 2 * kFfnDualWidth : width;
+            const uint32_t idesc = idesc_bf16_f32(kFfnRowsPerCta * CG, 0) | ((uint32_t)(mma_n >> 3) << 17) |
+                                   (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
+            const uint32_t step = stage_bytes >> 4;
+            const uint32_t leader = elect_one();
+            // A wait that runs out does not leave the k loop: it records the fact, and the rest
+            // of the item runs with short single probes and tells nobody.  Above all it releases
+            // no stage: one filled again before its first load has landed would count arrivals
+            // into a phase that has all of them, which faults.
+            const uint32_t nobody_bar = ready_bar + 64u;
+            uint32_t probe_ns = ctl.suspend_ns;
+            uint32_t tries = (uint32_t)(ctl.limit_ns / probe_ns) + 1u;
+            uint32_t bad = 0u;
+            auto wait = [&](uint32_t bar, uint32_t parity, uint32_t role, uint32_t where) {
+                if (mbar_wait_tries(bar, parity, probe_ns, tries) == 0u) {
+                    if (bad == 0u && leader)
+                        ctl.fail(role, where);
+                    bad = 1u;
+                    tries = 1u;
+                    probe_ns = 1u;
+                }
+            };
+            int s = 0;
+            uint32_t ph = 0;
+            int acc = 0;
+            uint32_t acc_ph = 0;
+            uint32_t ready = 0u;  // the next stage was seen full
+            while (wi.next(w)) {
+                wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
+                tc_fence_after_sync();
+                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFfnMaxWidth);
+                for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (!__all_sync(0xFFFFFFFFu, ready))
+                        wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
+                    tc_fence_after_sync();
+                    const uint64_t off = (uint64_t)((uint32_t)s * step);
+                    int s1 = s;
+                    uint32_t ph1 = ph;
+                    ring_advance(s1, ph1, S);
+                    const uint32_t add = kb > w.kb0 ? 1u : 0u;
+                    if constexpr (kDual && kT)
+                        mma_bf16_block<CG>(d_tmem + kFfnDualWidth, rdesc0 + off + (kTileRBytes >> 4), cdesc0 + off,
+                                           idesc, rstep, cstep, add, leader, full_bar + 8u * s1, ring_full_parity(ph1));
+                    ready = mma_bf16_block<CG>(d_tmem, rdesc0 + off, cdesc0 + off, idesc, rstep, cstep, add, leader,
+                                               full_bar + 8u * s1, ring_full_parity(ph1));
+                    if (ring_group_last(s, 1u))
+                        mma_commit_elected<CG>(bad ? nobody_bar : empty_bar + 8u * ring_group(s, 1u), leader);
+                    ring_advance(s, ph, S);
+                }
+                mma_commit_elected<CG>(bad ? nobody_bar : accf_bar + 8u * acc, leader);
+                acc ^= 1;
+                if (acc == 0)
+                    acc_ph ^= 1u;
+                if (__any_sync(0xFFFFFFFFu, bad))
+                    break;
+            }
+            // no MMA may still be writing tensor memory when it is freed
+            mma_commit_elected<CG>(done_bar, leader);
+            if (leader) {
+                ctl.limit_ns = max(ctl.limit_ns, kFfnDrainNs);
+                ctl.wait_drain<kPair>(done_bar, 0u, 0xFFFu);
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------- epilogue ----------------
+        grid_dependency_wait();
+        const int ew = warp - 4;
+        const int q = warp & 3;    // tensor-memory lane quadrant
+        const int half = ew >> 2;  // takes chunks half, half + 2, ... of 32 columns
+        const int nchunks = (width + 31) / 32;
+        FfnStager st = {staging0 + (uint32_t)ew * kFfnStagingBytes, lane, 0u};
+        const uint32_t acce_target = kPair ? mapa_shared(acce_bar, 0u) : acce_bar;
+        const int32_t cta = cluster_id * CG + (int32_t)rank;
+        int acc = 0;
+        uint32_t acc_ph = 0;
+        uint32_t item_parity = 0;
+        const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
+        // one thread waits for the accumulator and posts the outcome, so that all
+        // warps take the same branch; the word alternates with the accumulations
+        auto accumulated = [&]() {
+            const uint32_t go = go_words + 4u * item_parity;
+            item_parity ^= 1u;
+            if (threadIdx.x == 128)
+                st_volatile_shared_u32(
+                    go, ctl.wait<kPair>(accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc) ? 1u : 0u);
+            named_barrier_sync(1u, kFfnEpiWarps * 32u);
+            return ld_volatile_shared_u32(go) != 0u;
+        };
+        // this warp has read its part of the accumulator: hand it back
+        auto hand_back = [&]() {
+            tc_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) {
+                if constexpr (kPair)
+                    mbar_arrive_cluster_handoff(acce_target + 8u * acc);
+                else
+                    mbar_arrive(acce_bar + 8u * acc);
+            }
+        };
+        auto load_chunk = [&](int a, int c, uint32_t(&v)[32]) {
+            tmem_load_32x32(tmem_base + ((uint32_t)(q * 32) << 16) +
+                                (uint32_t)(acc * kFfnMaxWidth + a * kFfnDualWidth + c * 32),
+                            v);
+        };
+        while (wi.next(w)) {
+            const FfnTile tc = ffn_tile_coord(w.tile, p);
+            const bool other = tc.row >= p.row_split;
+            // the accumulator's rows and columns of this warp
+            const int32_t yr =
+                ((other ? tc.row - p.row_split : tc.row) * CG + (int32_t)rank) * kFfnRowsPerCta + q * 32;
+            const int32_t yc = tc.col * width;
+            const bool contributor = w.kb0 > 0;
+            const bool owner = w.kb0 == 0 && w.kb1 < KB;
+            // the clusters whose ranges start inside this tile, owner only; a range
+            // may be empty (fewer units than clusters), and then leaves nothing
+            int32_t last = cluster_id;
+            bool parts = owner;
+            auto collect = [&]() {
+                if (owner && shared_tile) {
+                    uint32_t got = 1u;
+                    if (lane == 0)
+                        got = ctl.wait<true>(ready_bar + 8u * (uint32_t)ew, 0u, kRoleFixup, (uint32_t)ew) ? 1u : 0u;
+                    __syncwarp();  // lane 0's acquire comes before the lanes' loads
+                    parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
+                } else if (owner) {
+                    last = ffn_range_of(p.sk_units, num_clusters, (int64_t)(w.tile + 1) * KB - 1);
+                    for (int32_t j2 = cluster_id + 1; parts && j2 <= last; ++j2)
+                        if (dense || ffn_range_holds(p.sk_units, num_clusters, j2))
+                            // a give-up stores the tile unsummed, and the status says so
+                            parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFfnEpiWarps + ew, 1u,
+                                                   lane);
+                    __syncwarp();  // lane 0's acquires come before the lanes' loads
+                }
+            };
+            // one chunk's sums of one accumulator: left for the tile's owner, or completed; false if left
+            auto complete = [&](int a, int c, uint32_t(&v)[32]) {
+                const int slot = (c >> 1) + 2 * a;
+                // The cluster form keeps a partial in the CTA's own ring: a
+                // contributor's only item has consumed all of its loads by now.
+                const uint32_t local = stage0 + (uint32_t)((((ew * 4 + slot) * 8) * 32 + lane) * 16);
+                // (of a transposed result, only its rows' columns, four at a time)
+                const int live = kT ? min(8, (p.cols - (yc + c * 32) + 3) >> 2) : 8;
+                if (contributor && shared_tile) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < live)
+                            st_shared_v4(local + 512u * j, v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+                    return false;
+                }
+                if (contributor) {
+                    float4 *const part = reinterpret_cast<float4 *>(ffn_partial(p.partials, cta, ew, slot, lane));
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        if (j < live)
+                            __stcg(part + j * 32, make_float4(__uint_as_float(v[4 * j]), __uint_as_float(v[4 * j + 1]),
+                                                              __uint_as_float(v[4 * j + 2]),
+                                                              __uint_as_float(v[4 * j + 3])));
+                    return false;
+                }
+                if (parts && shared_tile) {
+                    for (int32_t rk = 1; rk < p.cluster; ++rk) {
+                        const uint32_t remote = mapa_shared(local, (uint32_t)rk);
+                        uint32_t x[32];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < live)
+                                ld_shared_cluster_v4(remote + 512u * j, x[4 * j], x[4 * j + 1], x[4 * j + 2],
+                                                     x[4 * j + 3]);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < live)
+#pragma unroll
+                                for (int e = 4 * j; e < 4 * j + 4; ++e)
+                                    v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(x[e]));
+                    }
+                } else if (parts) {
+                    for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
+                        if (!dense && !ffn_range_holds(p.sk_units, num_clusters, j2))
+                            continue;
+                        const float4 *const part = reinterpret_cast<const float4 *>(
+                            ffn_partial(p.partials, j2 * CG + (int32_t)rank, ew, slot, lane));
+                        float4 f[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < live)
+                                f[j] = __ldcg(part + j * 32);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            if (j < live) {
+                                v[4 * j] = __float_as_uint(__uint_as_float(v[4 * j]) + f[j].x);
+                                v[4 * j + 1] = __float_as_uint(__uint_as_float(v[4 * j + 1]) + f[j].y);
+                                v[4 * j + 2] = __float_as_uint(__uint_as_float(v[4 * j + 2]) + f[j].z);
+                                v[4 * j + 3] = __float_as_uint(__uint_as_float(v[4 * j + 3]) + f[j].w);
+                            }
+                    }
+                }
+                return true;
+            };
+            // where chunk c lies in the results, for this thread or (kT) this warp's first row
+            const int32_t d_row0 = kT ? yc : yr;
+            const int32_t d_col0 = kT ? yr : yc;
+            constexpr int kAux = kEpi == kFfnGrad ? 2 : kEpi == kFfnPlain ? 1 : 0;
+            // rows that are read by 16 bytes are asked for ahead of their use
+            FfnRaw raw[kAux > 0 ? kAux : 1];
+            auto ahead = [&](int c) {
+                if constexpr (!kT && kAux > 0) {
+#pragma unroll
+                    for (int i = 0; i < kAux; ++i)
+                        if (p.aux[i].p && (p.aux[i].vec || p.aux[i].scales))
+                            ffn_load_rows(raw[i], p.aux[i], yr + lane, yc + c * 32, p);
+                }
+            };
+            auto aux_floats = [&](int i, int c, float(&f)[32]) {
+                if constexpr (kT) {
+                    ffn_load_column(f, p.aux[i], yc + c * 32, yr + lane, p);
+                } else {
+                    if (!p.aux[i].vec && !p.aux[i].scales)
+                        ffn_load_rows_any(raw[i], st, p.aux[i], yr, yc + c * 32, p);
+                    ffn_raw_floats(f, raw[i], p.aux[i]);
+                }
+            };
+            if (!contributor && half < nchunks)
+                ahead(half);
+            if (!accumulated())
+                break;
+            tc_fence_after_sync();
+            if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
+                hand_back();
+                collect();
+            }
+            float inv[2] = {0.0f, 0.0f};  // 8-bit checkpoints: this thread's row's scales, inverted
+            if constexpr (kDual && !kT) {
+                if (p.save == 2) {
+                    // a block of the format is the tile's 128 columns: each warp looks at them all
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        float top = 0.0f;
+                        for (int c = 0; c < 4; ++c) {
+                            uint32_t v[32];
+                            load_chunk(a, c, v);
+                            tmem_load_wait();
+                            reg_fence(v);
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                top = fmaxf(top, finite_abs(__uint_as_float(v[i])));
+                        }
+                        const uint32_t byte = scale_byte(KB ? top : 0.0f);
+                        inv[a] = scale_inverse(byte);
+                        const int32_t row = yr + lane, block = tc.col;
+                        if (half == a && row < p.D_rows) {
+                            uint8_t *const word = p.scales[a] + ((int64_t)(block >> 2) * p.D_rows + row) * 4;
+                            word[block & 3] = (uint8_t)byte;
+                            if (block == p.num_col_tiles - 1)
+                                for (int i = (block & 3) + 1; i < 4; ++i)
+                                    word[i] = 127;
+                        }
+                    }
+                }
+            }
+            for (int c = half; c < nchunks; c += 2) {
+                uint32_t v[kAccs][32];
+#pragma unroll
+                for (int a = 0; a < kAccs; ++a)
+                    load_chunk(a, c, v[a]);
+                tmem_load_wait();
+#pragma unroll
+                for (int a = 0; a < kAccs; ++a) {
+                    reg_fence(v[a]);
+                    if (KB == 0) {  // an empty sum
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            v[a][i] = 0u;
+                    }
+                }
+                if (c + 2 >= nchunks)
+                    hand_back();
+                if (c == half && owner)
+                    collect();  // after this piece's own sums have been read
+                bool whole = true;
+#pragma unroll
+                for (int a = 0; a < kAccs; ++a)
+                    whole = complete(a, c, v[a]);
+                const int32_t row = d_row0 + (kT ? c * 32 : 0), col = d_col0 + (kT ? 0 : c * 32);
+                if (!whole || row >= p.D_rows || col >= p.D_cols) {
+                    if (whole && c + 2 < nchunks)
+                        ahead(c + 2);
+                    continue;
+                }
+                uint32_t pk[16];
+                if constexpr (kEpi == kFfnPlain) {
+                    float f[32];
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        f[i] = __uint_as_float(v[0][i]);
+                    const FfnOut &out = other ? p.D[1] : p.D[0];
+                    const CUtensorMap *const map = other ? &maps.D[1] : &maps.D[0];
+                    ffn_add_bias<kT>(f, kT ? col + lane : col, p);
+                    if (p.save) {
+                        ffn_pack(pk, f);
+                        ffn_store_bf16<kT>(pk, st, &maps.D[1], p.D[1], row, col, p);
+                    }
+                    if (p.act != kActNone)
+                        ffn_with_act(p.act, [&](auto tag) {
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                f[i] = ffn_act<decltype(tag)::value>(f[i]);
+                        });
+                    if (p.aux[0].p) {
+                        float r[32];
+                        aux_floats(0, c, r);
+                        if (c + 2 < nchunks)
+                            ahead(c + 2);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            f[i] += r[i];
+                    }
+                    if (p.out_fp32) {
+                        ffn_store_fp32<kT>(f, st, map, out, row, col, p);
+                    } else {
+                        ffn_pack(pk, f);
+                        ffn_store_bf16<kT>(pk, st, map, out, row, col, p);
+                    }
+                } else if constexpr (kEpi == kFfnGated) {
+                    if (p.save == 1) {
+#pragma unroll
+                        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pk[i] = pack_bf16x2(v[a][2 * i], v[a][2 * i + 1]);
+                            ffn_store_bf16<kT>(pk, st, &maps.D[1 + a], p.D[1 + a], row, col, p);
+                        }
+                    }
+                    if constexpr (!kT) {
+                        if (p.save == 2 && row + lane < p.D_rows) {
+                            // 32 codes of this thread's row, one sector
+#pragma unroll
+                            for (int a = 0; a < 2; ++a) {
+                                uint32_t code[8];
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    float e[4];
+#pragma unroll
+                                    for (int j = 0; j < 4; ++j)
+                                        e[j] = inf_to_nan(__uint_as_float(v[a][4 * i + j])) * inv[a];
+                                    code[i] = pack_e4m3x4(e[0], e[1], e[2], e[3]);
+                                }
+                                uint4 *const dst =
+                                    reinterpret_cast<uint4 *>(p.codes[a] + (int64_t)(row + lane) * p.ldq[a] + col);
+                                dst[0] = make_uint4(code[0], code[1], code[2], code[3]);
+                                dst[1] = make_uint4(code[4], code[5], code[6], code[7]);
+                            }
+                        }
+                    }
+                    ffn_with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            pk[i] = bf16_pair(
+                                ffn_act<decltype(tag)::value>(__uint_as_float(v[0][2 * i])) * __uint_as_float(v[1][2 * i]),
+                                ffn_act<decltype(tag)::value>(__uint_as_float(v[0][2 * i + 1])) *
+                                    __uint_as_float(v[1][2 * i + 1]));
+                    });
+                    ffn_store_bf16<kT>(pk, st, &maps.D[0], p.D[0], row, col, p);
+                } else {
+                    float g[32], u[32];
+                    aux_floats(0, c, g);
+                    aux_floats(1, c, u);
+                    if (c + 2 < nchunks)
+                        ahead(c + 2);
+                    uint32_t pdu[16], ph[16];
+                    ffn_with_act(p.act, [&](auto tag) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            float dg[2], du[2], h[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                float a, d;
+                                ffn_act_slope<decltype(tag)::value>(g[2 * i + e], a, d);
+                                const float dh = __uint_as_float(v[0][2 * i + e]);
+                                dg[e] = dh * u[2 * i + e] * d;
+                                du[e] = dh * a;
+                                h[e] = a * u[2 * i + e];
+                            }
+                            pk[i] = bf16_pair(dg[0], dg[1]);
+                            pdu[i] = bf16_pair(du[0], du[1]);
+                            ph[i] = bf16_pair(h[0], h[1]);
+                        }
+                    });
+                    ffn_store_bf16<kT>(pk, st, &maps.D[0], p.D[0], row, col, p);
+                    ffn_store_bf16<kT>(pdu, st, &maps.D[1], p.D[1], row, col, p);
+                    ffn_store_bf16<kT>(ph, st, &maps.D[2], p.D[2], row, col, p);
+                }
+            }
+            acc ^= 1;
+            acc_ph ^= acc == 0 ? 1u : 0u;
+            if (contributor) {
+                __syncwarp();  // the warp's stores come before lane 0's release
+                if (lane == 0 && shared_tile)
+                    mbar_arrive_cluster(mapa_shared(ready_bar + 8u * (uint32_t)ew, 0u));
+                else if (lane == 0)
+                    st_release_gpu_u32(p.flags + cta * kFfnEpiWarps + ew, 1u);
+            }
+        }
+        // the staging buffers have been read before the CTA exits
+        if (lane == 0)
+            bulk_wait_read_all();
+        __syncwarp();
+    }
+
+    // ---------------- teardown ----------------
+    tc_fence_before_sync();
+    __syncthreads();
+    if (kPair || shared_tile)
+        cluster_arrive_wait();  // the peer is done with this CTA's memory
+    if (warp == 2) {
+        tc_fence_after_sync();
+        tmem_dealloc<CG>(tmem_base, 512);
+    }
+}
+
+}  // namespace wstma
