@@ -7,15 +7,16 @@
  *                        dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h
  *
  * Matrices are bf16 with contiguous rows, `ld` elements apart; sums are fp32.  Any
- * base and pitch will do; an operand of a product whose rows do not start at
- * multiples of 16 bytes is first copied to the workspace.  dz, and dg, du and h of
+ * base and pitch will do; rows at multiples of 128 bytes are fastest.  An operand of a
+ * product whose rows do not start at multiples of 16 bytes is first copied to the
+ * workspace, as is a large one whose rows do not at multiples of 128.  dz, and dg, du and h of
  * ffn_gated_backward, are rounded to bf16, in which the products that follow take them.
  *
  * Calls return a status code, never throw, and only enqueue work on `stream` (a
  * cudaStream_t) of the calling thread's current device; argument errors are returned
  * before anything is enqueued.  Results must lie apart from what a call reads and from
  * each other, but for y, which may be the residual's rows themselves.  A call's
- * workspace (16-byte aligned, whatever it holds) is the caller's until the work has
+ * workspace (256-byte aligned, whatever it holds) is the caller's until the work has
  * run: calls with workspaces of their own may overlap, and calls may be captured into
  * CUDA graphs.  Sizes of zero are allowed: an empty sum is zero. */
 #ifndef FFN_OPS_H
@@ -66,7 +67,9 @@ typedef enum ffn_option {
     FFN_OPT_WATCHDOG_NS = 5, /* limit of any wait inside a kernel (default 2e9, 1e5 to 6e10) */
     FFN_OPT_FAULT_SKIP_LOAD = 6, /* test hook: each producer leaves out this load (-1 = none), so that a bounded
                                     wait runs out and ffn_device_status reports DEVICE_TIMEOUT */
-    FFN_OPT_RASTER_GROUP = 7 /* tiles are walked in bands of this many row tiles */
+    FFN_OPT_RASTER_GROUP = 7, /* tiles are walked in bands of this many row tiles */
+    FFN_OPT_REPACK = 8        /* operands whose rows do not start at multiples of 128 bytes: 1 = copied first, 2 =
+                                 read as they are where a tensor map can describe them */
 } ffn_option;
 
 typedef struct ffn_plan_info_s {

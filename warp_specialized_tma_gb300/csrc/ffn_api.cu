@@ -20,8 +20,9 @@ using namespace wstma;
 namespace {
 
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL - 1023;  // a tile past the last row still has a 32-bit index
+constexpr size_t kWorkAlign = 256;    // of the parts of a workspace
 constexpr int64_t kMaxPitch = int64_t(1) << 37;
-constexpr int kNumOptions = 8;
+constexpr int kNumOptions = 9;
 constexpr int kPlans = 64;              // plans a thread remembers
 constexpr int kMaxCtas = 1024;          // bounds the workspace of split tiles
 constexpr int64_t kMinSplitBlocks = 8;  // k-blocks per cluster below which tiles are not split further
@@ -147,7 +148,7 @@ struct Product {
 };
 
 struct Options {
-    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0};
+    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0};
 };
 thread_local Options options;
 
@@ -408,39 +409,39 @@ struct Call {
     void *take(size_t bytes)
     {
         const size_t at = used;
-        used += (bytes + 255) / 256 * 256;
+        used += (bytes + kWorkAlign - 1) / kWorkAlign * kWorkAlign;
         return base ? base + at : nullptr;
     }
 };
 
-int64_t padded(int64_t cols) { return (cols + 7) / 8 * 8; }
+// Rows that the library makes start at multiples of 128 bytes.
+int64_t padded(int64_t cols) { return (cols + 63) / 64 * 64; }
 
-// Whether a tensor map can describe rows of this pitch (a single row has none).
-bool mappable(const Operand &o, int64_t mem_rows) { return aligned(o.p, 16) && (o.ld % 8 == 0 || mem_rows <= 1); }
-
-// An operand's rows as a tensor map takes them: as they are, or copied.
-int prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int32_t *packed)
+// An operand's rows as a product reads them: as they are, or listed in `jobs` to be copied first.
+// Copied are rows that no tensor map describes (not at multiples of 16 bytes), and long operands
+// whose rows are not at multiples of 128: each 128-byte row of a box then straddles two lines of
+// L2, which bounds the product.  `readers` rows on the other side pay for the copy from 4096 on.
+void prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int64_t readers, FfnPackJobs &jobs)
 {
     if (mem_rows < 1 || mem_cols < 1)
-        return FFN_OK;
-    if (mappable(o, mem_rows)) {
+        return;
+    const bool describable = aligned(o.p, 16) && (o.ld % 8 == 0 || mem_rows <= 1);
+    const bool straddles = mem_rows > 1 && (o.ld % 64 != 0 || !aligned(o.p, 128));
+    const int64_t mode = options.v[FFN_OPT_REPACK];
+    if (describable && !(straddles && (mode == 1 || (mode == 0 && readers >= 4096)))) {
         if (mem_rows <= 1)
             o.ld = padded(mem_cols);
-        return FFN_OK;
+        return;
     }
-    const int64_t ld = padded(mem_cols);
-    void *const to = c.take((size_t)(mem_rows * ld) * 2);
-    ++*packed;
-    if (!c.measuring()) {
-        const int rc = from_cuda((cudaError_t)launch_ffn_pack(static_cast<const uint16_t *>(o.p), o.ld,
-                                                              static_cast<uint16_t *>(to), ld, mem_rows, mem_cols,
-                                                              c.dev.sms, c.stream));
-        if (rc != FFN_OK)
-            return rc;
-    }
-    o.p = to;
-    o.ld = ld;
-    return FFN_OK;
+    FfnPackJob &job = jobs.job[jobs.n++];
+    job.src = static_cast<const uint16_t *>(o.p);
+    job.lds = o.ld;
+    job.ldd = padded(mem_cols);
+    job.dst = static_cast<uint16_t *>(c.take((size_t)(mem_rows * job.ldd) * 2));
+    job.R = mem_rows;
+    job.C = (int32_t)mem_cols;
+    o.p = job.dst;
+    o.ld = job.ldd;
 }
 
 int set_out(FfnOut &out, CUtensorMap *map, const ffn_matrix &m, bool fp32, int64_t rows, int64_t cols)
@@ -482,14 +483,18 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     if (rc != FFN_OK)
         return rc;
     const Plan &pl = *found;
-    int32_t packed = 0;
+    FfnPackJobs jobs;
+    jobs.n = 0;
     for (int i = 0; i < 2; ++i) {
-        const bool has_a = i == 0 || x.form == kSum || x.form == kStack, has_b = i == 0 || x.form == kSum || x.form == kDual;
-        if (has_a && (rc = prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, &packed)) != FFN_OK)
-            return rc;
-        if (has_b && (rc = prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, &packed)) != FFN_OK)
-            return rc;
+        const bool has_a = i == 0 || x.form == kSum || x.form == kStack;
+        const bool has_b = i == 0 || x.form == kSum || x.form == kDual;
+        if (has_a)
+            prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, x.N, jobs);
+        if (has_b)
+            prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, x.M, jobs);
     }
+    if (jobs.n && !c.measuring() && (rc = from_cuda((cudaError_t)launch_ffn_pack(jobs, c.dev.sms, c.stream))) != FFN_OK)
+        return rc;
     const size_t partial_bytes = pl.sk_tiles && pl.cluster == 1
                                      ? (size_t)pl.grid * (kFfnPartialFloats * sizeof(float) + kFfnEpiWarps * sizeof(uint32_t))
                                      : 0;
@@ -570,7 +575,7 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     cfg.numAttrs = together > 1 ? 2 : 1;
     void *args[2] = {&maps, &p};
     last_plan = pl;
-    last_packed = packed;
+    last_packed = jobs.n;
     have_last_plan = true;
     return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
 }
@@ -656,7 +661,7 @@ int run_call(F body, void *workspace, int64_t size, void *stream)
     const size_t need = c.used + c.shared;
     if (need && (!workspace || size < (int64_t)need))
         return FFN_ERR_WORKSPACE;
-    if (need && !aligned(workspace, 16))
+    if (need && !aligned(workspace, kWorkAlign))
         return FFN_ERR_ALIGNMENT;
     Call run;
     run.dev = c.dev;
@@ -964,6 +969,7 @@ FFN_API int ffn_set_option(int key, int64_t value)
     case FFN_OPT_WATCHDOG_NS: ok = value >= 100000 && value <= 60000000000LL; break;
     case FFN_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
     case FFN_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
+    case FFN_OPT_REPACK: ok = value >= 0 && value <= 2; break;
     default: break;
     }
     if (!ok)

@@ -23,10 +23,10 @@ inline ffn_matrix matrix(const Tensor &t, int64_t R, int64_t C, const char *what
     return {data(t), need_bf16(t, R, C, what)};
 }
 
-// An R x C result whose rows start at multiples of 16 bytes.
-inline Tensor rows16(const Place &at, int64_t R, int64_t C, at::ScalarType type)
+// An R x C result whose rows start at multiples of 128 bytes.
+inline Tensor whole_rows(const Place &at, int64_t R, int64_t C, at::ScalarType type)
 {
-    const int64_t per = type == at::kFloat ? 4 : 8, ld = (C + per - 1) / per * per;
+    const int64_t per = type == at::kFloat ? 32 : 64, ld = (C + per - 1) / per * per;
     return ld == C ? at.empty({R, C}, type) : at::detail::empty_strided_cuda({R, C}, {ld, 1}, type, at.on);
 }
 
@@ -114,12 +114,12 @@ inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
                 value_error("out must be " + size_text(M, N));
             a.y = {data(y), pitch_of(y, "out")};
         } else {
-            y = rows16(at, M, N, result_type(args[7], "out_dtype"));
+            y = whole_rows(at, M, N, result_type(args[7], "out_dtype"));
             a.y = result(y);
         }
         a.y_type = element_type(y, "out");
         if (save) {
-            z = rows16(at, M, N, at::kBFloat16);
+            z = whole_rows(at, M, N, at::kBFloat16);
             a.z = result(z);
         }
         run(at, a, &ffn_linear_workspace, &ffn_linear, "ffn_linear");
@@ -153,7 +153,7 @@ inline PyObject *linear_backward(PyObject *, PyObject *const *args, Py_ssize_t n
         a.dweight_type = wtype == at::kFloat ? FFN_FP32 : FFN_BF16;
         Place at(dy);
         at.same(&x), at.same(&w), at.same(z);
-        Tensor dx = rows16(at, M, K, at::kBFloat16), dw = rows16(at, N, K, wtype), db;
+        Tensor dx = whole_rows(at, M, K, at::kBFloat16), dw = whole_rows(at, N, K, wtype), db;
         a.dx = result(dx);
         a.dweight = result(dw);
         if (bias) {
@@ -187,10 +187,10 @@ inline PyObject *gated(PyObject *, PyObject *const *args, Py_ssize_t n)
         const int32_t save = activation(args[4]);
         Place at(x);
         at.same(&wg), at.same(&wu);
-        Tensor h = rows16(at, M, F, at::kBFloat16), g, u, gs, us;
+        Tensor h = whole_rows(at, M, F, at::kBFloat16), g, u, gs, us;
         a.h = result(h);
         if (save == 1) {
-            g = rows16(at, M, F, at::kBFloat16), u = rows16(at, M, F, at::kBFloat16);
+            g = whole_rows(at, M, F, at::kBFloat16), u = whole_rows(at, M, F, at::kBFloat16);
             a.g = result(g), a.u = result(u);
         } else if (save == 2) {
             std::tie(g, gs) = at.quantized(M, F);
@@ -243,8 +243,8 @@ inline PyObject *gated_backward(PyObject *, PyObject *const *args, Py_ssize_t n)
         }
         const at::ScalarType wtype = result_type(args[7], "grad_dtype");
         a.dweight_type = wtype == at::kFloat ? FFN_FP32 : FFN_BF16;
-        Tensor dx = rows16(at, M, C, at::kBFloat16), dwg = rows16(at, F, C, wtype), dwu = rows16(at, F, C, wtype),
-               dwd = rows16(at, N, F, wtype);
+        Tensor dx = whole_rows(at, M, C, at::kBFloat16), dwg = whole_rows(at, F, C, wtype), dwu = whole_rows(at, F, C, wtype),
+               dwd = whole_rows(at, N, F, wtype);
         a.dx = result(dx);
         a.dw_gate = result(dwg);
         a.dw_up = result(dwu);

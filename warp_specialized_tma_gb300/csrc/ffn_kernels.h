@@ -98,9 +98,24 @@ int launch_ffn_clear(uint32_t *flags, int32_t n, cudaStream_t stream);  // a cud
 uint32_t *ffn_status_word();  // of the current device, or null
 
 // ----------------------------------------------------------------- rows
-// Copies R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8).
-int launch_ffn_pack(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int64_t R, int64_t C, int num_sms,
-                    cudaStream_t stream);
+// Copies of R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8).
+struct FfnPackJob {
+    const uint16_t *src;
+    int64_t lds;
+    uint16_t *dst;
+    int64_t ldd;
+    int64_t R;
+    int32_t C;
+    int32_t blocks;  // the launch's: units of a row, and in all; whether rows are 16-byte aligned
+    int64_t units;
+    int32_t vec;
+};
+struct FfnPackJobs {
+    FfnPackJob job[4];
+    int n;
+    int64_t units;
+};
+int launch_ffn_pack(FfnPackJobs &jobs, int num_sms, cudaStream_t stream);
 
 struct FfnSlopeParams {
     const uint16_t *dy;

@@ -17,12 +17,13 @@ constexpr int kSlopeWarps = 8;
 constexpr int kSlopeColumns = 256;  // of a warp: 8 a lane
 constexpr int kSlopeMaxSlices = 128;
 
-// Vector c .. c+7 of a row, whatever its alignment.
+// Vector c .. c+7 of a row, whatever its alignment; zero past the row's end.  `live` holds for all
+// lanes or none: a lane behind the row's end still loads what its neighbour's vector ends in.
 template <bool kVec>
 __device__ __forceinline__ uint4 load8_any(const uint16_t *row, int32_t c, int32_t C, bool live)
 {
     if constexpr (kVec)
-        return live ? load8_bf16(row, c, C, true) : make_uint4(0u, 0u, 0u, 0u);
+        return live && c < C ? load8_bf16(row, c, C, true) : make_uint4(0u, 0u, 0u, 0u);
     else
         return load8_bf16_shifted(row, c, C, live);
 }
@@ -50,7 +51,7 @@ __global__ void __launch_bounds__(kSlopeWarps * 32) ffn_slope_kernel(const FfnSl
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
             const int32_t row = r + k * kSlopeWarps;
-            const bool live = row < r1 && c < p.C;
+            const bool live = row < r1;
             dy[k] = load8_any<kVec>(p.dy + (int64_t)min(row, r1 - 1) * p.lddy, c, p.C, live);
             if constexpr (A != kActNone)
                 z[k] = load8_any<kVec>(p.z + (int64_t)min(row, r1 - 1) * p.ldz, c, p.C, live);
@@ -121,36 +122,45 @@ __global__ void __launch_bounds__(256) ffn_column_sum_kernel(const float *partia
     }
 }
 
-// A copy at the copy's bandwidth: every lane reads whole 16-byte groups of the source and
-// takes what its own group lacks from its neighbour.
-__global__ void __launch_bounds__(256) ffn_pack_kernel(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd,
-                                                       int64_t R, int32_t C, int32_t blocks_per_row)
+// Copies of up to four matrices at the copy's bandwidth.  A warp's unit is 1024 columns of a row,
+// four vectors a lane in flight.  Rows that are not 16-byte aligned are read by whole 16-byte
+// groups too: every lane takes what its own group lacks from its neighbour.
+constexpr int kPackVectors = 4;
+__global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackJobs jobs)
 {
-    grid_dependency_wait();
     const int lane = threadIdx.x & 31;
-    const int64_t units = R * blocks_per_row;
     const int64_t step = (int64_t)gridDim.x * 8;
-    for (int64_t u0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u0 < units; u0 += 4 * step) {
-        uint4 q[4];
+    grid_dependency_wait();
+    for (int64_t u0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u0 < jobs.units; u0 += step) {
+        int64_t u = u0;
+        int n = 0;
+        while (u >= jobs.job[n].units)
+            u -= jobs.job[n++].units;
+        const FfnPackJob &j = jobs.job[n];
+        const int64_t r = j.blocks == 1 ? u : u / j.blocks;
+        const int32_t c = (int32_t)(u - r * j.blocks) * (kPackVectors * kSlopeColumns) + 8 * lane;
+        const uint16_t *const from = j.src + r * j.lds;
+        uint4 q[kPackVectors];
+        if (j.vec) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t u = u0 + k * step;
-            const bool live = u < units;
-            const int64_t r = live ? u / blocks_per_row : 0;
-            const int32_t c = live ? (int32_t)(u - r * blocks_per_row) * kSlopeColumns + 8 * lane : 0;
-            q[k] = load8_bf16_shifted(src + r * lds, c, C, live && c < C);
+            for (int k = 0; k < kPackVectors; ++k) {
+                const int32_t at = c + k * kSlopeColumns;
+                if (at + 8 <= j.C)
+                    q[k] = __ldcs(reinterpret_cast<const uint4 *>(from + at));
+                else
+                    q[k] = load8_bf16(from, at, j.C, false);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kPackVectors; ++k)
+                q[k] = load8_bf16_shifted(from, c + k * kSlopeColumns, j.C, true);
         }
 #pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int64_t u = u0 + k * step;
-            if (u >= units)
-                continue;
-            const int64_t r = u / blocks_per_row;
-            const int32_t c = (int32_t)(u - r * blocks_per_row) * kSlopeColumns + 8 * lane;
-            if (c < C)
-                *reinterpret_cast<uint4 *>(dst + r * ldd + c) = q[k];
-        }
+        for (int k = 0; k < kPackVectors; ++k)
+            if (c + k * kSlopeColumns < j.C)
+                *reinterpret_cast<uint4 *>(j.dst + r * j.ldd + c + k * kSlopeColumns) = q[k];
     }
+    grid_launch_dependents();
 }
 
 // The flags of a split launch, set to 0 ahead of it.
@@ -196,12 +206,18 @@ int launch_ffn_clear(uint32_t *flags, int32_t n, cudaStream_t stream)
     return launch(ffn_clear_kernel, dim3(1), stream, flags, n);
 }
 
-int launch_ffn_pack(const uint16_t *src, int64_t lds, uint16_t *dst, int64_t ldd, int64_t R, int64_t C, int num_sms,
-                    cudaStream_t stream)
+int launch_ffn_pack(FfnPackJobs &jobs, int num_sms, cudaStream_t stream)
 {
-    const int64_t blocks = (C + kSlopeColumns - 1) / kSlopeColumns;
-    const int64_t ctas = std::min<int64_t>((R * blocks + 31) / 32, (int64_t)num_sms * 8);
-    return launch(ffn_pack_kernel, dim3((unsigned)ctas), stream, src, lds, dst, ldd, R, (int32_t)C, (int32_t)blocks);
+    jobs.units = 0;
+    for (int i = 0; i < jobs.n; ++i) {
+        FfnPackJob &j = jobs.job[i];
+        j.blocks = (j.C + kPackVectors * kSlopeColumns - 1) / (kPackVectors * kSlopeColumns);
+        j.vec = (reinterpret_cast<uintptr_t>(j.src) & 15u) == 0 && j.lds % 8 == 0;
+        j.units = j.R * j.blocks;
+        jobs.units += j.units;
+    }
+    const int64_t ctas = std::min<int64_t>((jobs.units + 7) / 8, (int64_t)num_sms * 8);
+    return launch(ffn_pack_kernel, dim3((unsigned)ctas), stream, jobs);
 }
 
 // Slices of the rows: enough CTAs to fill the GPU four times over, 16 rows a slice at least.

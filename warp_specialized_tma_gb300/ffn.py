@@ -7,10 +7,11 @@
     gated_backward     gradients of gated() and of the product with w_down that follows it
     device_status      whether a kernel's watchdog ran out
 
-Matrices are bf16 CUDA tensors with contiguous rows, at any pitch and offset.  Results that
-are not given have rows at multiples of 16 bytes, so their pitch is above their width where
-that is odd.  Sums are fp32; each result is rounded once.  A matrix whose rows do not start
-at multiples of 16 bytes is copied first where a product reads it.
+Matrices are bf16 CUDA tensors with contiguous rows, at any pitch and offset; sums are fp32, and
+each result is rounded once.  Results that are not given have rows at multiples of 128 bytes, as
+the quantisers' have: the next product reads them fastest.  Their pitch is above their width where
+that is no multiple of 64.  Operands whose rows do not start at multiples of 16 bytes are copied
+first, and large ones whose rows do not at multiples of 128.
 
 What gated() saves in 8 bits is in fp8's format: codes (float8_e4m3fn) and scales
 (float8_e8m0fnu), a power of two for each row and block of 128 columns.
@@ -59,6 +60,7 @@ OPTIONS = {
     "watchdog_ns": 5,
     "fault_skip_load": 6,
     "raster_group": 7,
+    "repack": 8,
 }
 
 _P = ctypes.c_void_p
