@@ -22,7 +22,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL - 1023;  // a tile past the last row still has a 32-bit index
 constexpr size_t kWorkAlign = 256;    // of the parts of a workspace
 constexpr int64_t kMaxPitch = int64_t(1) << 37;
-constexpr int kNumOptions = 9;
+constexpr int kNumOptions = 10;
 constexpr int kPlans = 64;              // plans a thread remembers
 constexpr int kMaxCtas = 1024;          // bounds the workspace of split tiles
 constexpr int64_t kMinSplitBlocks = 8;  // k-blocks per cluster below which tiles are not split further
@@ -148,7 +148,7 @@ struct Product {
 };
 
 struct Options {
-    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0};
+    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0, 0};
 };
 thread_local Options options;
 
@@ -473,11 +473,63 @@ FfnAux aux_of(const ffn_quantized &q)
     return a;
 }
 
+// Whether a product goes to the kernel for few tokens (ffn_stream.cu, with both sides' times): a
+// forward product whose operands are as its 16-byte loads need them, and whose rows fit its one pass.
+// Up to 8 tokens it is the faster one throughout, up to 16 but for a large gated pair (16 x 16384 x
+// 4096 52 us against 47), up to 32 for small weights (4096 x 4096 12.3 us against 13.4, 8192 x 8192
+// 36 against 34).
+bool streams(const Call &c, const Product &x)
+{
+    const bool dual = x.form == kDual;
+    if (options.v[FFN_OPT_STREAM] == 2 || x.M > kFfnStreamTokens || x.K < 1 || x.K % 8 != 0 || x.a_mn || x.b_mn ||
+        x.N > ffn_stream_rows(c.dev.sms) || !(dual ? x.p.save != 2 : x.form == kOne && x.epilogue == kFfnPlain))
+        return false;
+    if (!aligned(x.A[0].p, 16) || (x.M > 1 && x.A[0].ld % 8 != 0))
+        return false;
+    for (int i = 0; i < (dual ? 2 : 1); ++i)
+        if (!aligned(x.B[i].p, 16) || (x.N > 1 && x.B[i].ld % 8 != 0))
+            return false;
+    if (options.v[FFN_OPT_STREAM] == 1 || x.M <= 8)
+        return true;
+    return x.M <= 16 ? !dual || x.N * x.K <= 1 << 25 : x.N * x.K <= 1 << 24;
+}
+
+int run_stream(Call &c, const Product &x, const ffn_matrix *D, int outs, bool fp32)
+{
+    if (c.measuring())
+        return FFN_OK;
+    FfnStreamParams p = {};
+    p.x = static_cast<const uint16_t *>(x.A[0].p);
+    p.ldx = x.A[0].ld;
+    for (int i = 0; i < (x.form == kDual ? 2 : 1); ++i) {
+        p.w[i] = static_cast<const uint16_t *>(x.B[i].p);
+        p.ldw[i] = x.B[i].ld;
+    }
+    p.M = (int32_t)x.M, p.N = (int32_t)x.N, p.K = (int32_t)x.K;
+    p.act = x.p.act;
+    p.bias = x.p.bias;
+    p.bias_fp32 = x.p.bias_fp32;
+    p.residual = static_cast<const uint16_t *>(x.p.aux[0].p);
+    p.ldr = x.p.aux[0].ld;
+    for (int i = 0; i < outs; ++i) {
+        p.D[i].p = D[i].data;
+        p.D[i].ld = D[i].ld;
+    }
+    p.out_fp32 = fp32 ? 1 : 0;
+    p.save = x.p.save;
+    std::memset(&last_plan, 0, sizeof(last_plan));
+    last_packed = 0;
+    have_last_plan = true;
+    return from_cuda((cudaError_t)launch_ffn_stream(p, c.dev.sms, c.stream));
+}
+
 // Runs one product; results D[0..2] (fp32: of D[0], and D[1] of kStack).
 int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
 {
     if (x.M == 0 || x.N == 0)
         return FFN_OK;
+    if (streams(c, x))
+        return run_stream(c, x, D, outs, fp32);
     const Plan *found = nullptr;
     int rc = find_plan(c.dev, x, &found);
     if (rc != FFN_OK)
@@ -969,6 +1021,7 @@ FFN_API int ffn_set_option(int key, int64_t value)
     case FFN_OPT_WATCHDOG_NS: ok = value >= 100000 && value <= 60000000000LL; break;
     case FFN_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
     case FFN_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
+    case FFN_OPT_STREAM: ok = value >= 0 && value <= 2; break;
     case FFN_OPT_REPACK: ok = value >= 0 && value <= 2; break;
     default: break;
     }

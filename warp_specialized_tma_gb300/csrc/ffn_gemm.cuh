@@ -358,11 +358,11 @@ __device__ __forceinline__ void ffn_load_rows(FfnRaw &x, const FfnAux &a, int32_
 #pragma unroll
         for (int u = 0; u < 2; ++u)
             if (col + 16 * u < p.D_cols) {  // rows are whole groups of 16
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(src + 16 * u));
+                const uint4 q = *reinterpret_cast<const uint4 *>(src + 16 * u);
                 x.w[4 * u] = q.x, x.w[4 * u + 1] = q.y, x.w[4 * u + 2] = q.z, x.w[4 * u + 3] = q.w;
             }
         if (col < p.D_cols)
-            x.w[8] = __ldg(a.scales + ((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3));
+            x.w[8] = a.scales[((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3)];
         return;
     }
     const uint16_t *const src = static_cast<const uint16_t *>(a.p) + (int64_t)row * a.ld + col;
@@ -472,21 +472,21 @@ __device__ __forceinline__ void ffn_add_bias(float (&v)[32], int32_t at, const F
         if (at + 32 <= p.D_cols && (reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                const float4 q = __ldg(reinterpret_cast<const float4 *>(b) + u);
+                const float4 q = reinterpret_cast<const float4 *>(b)[u];
                 v[4 * u] += q.x, v[4 * u + 1] += q.y, v[4 * u + 2] += q.z, v[4 * u + 3] += q.w;
             }
         } else {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (at + i < p.D_cols)
-                    v[i] += __ldg(b + i);
+                    v[i] += b[i];
         }
     } else {
         const uint16_t *const b = static_cast<const uint16_t *>(p.bias) + at;
         if (at + 32 <= p.D_cols && (reinterpret_cast<uintptr_t>(b) & 15u) == 0) {
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
-                const uint4 q = __ldg(reinterpret_cast<const uint4 *>(b) + u);
+                const uint4 q = reinterpret_cast<const uint4 *>(b)[u];
                 const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -498,7 +498,7 @@ __device__ __forceinline__ void ffn_add_bias(float (&v)[32], int32_t at, const F
 #pragma unroll
             for (int i = 0; i < 32; ++i)
                 if (at + i < p.D_cols)
-                    v[i] += __uint_as_float((uint32_t)__ldg(b + i) << 16);
+                    v[i] += __uint_as_float((uint32_t)b[i] << 16);
         }
     }
 }

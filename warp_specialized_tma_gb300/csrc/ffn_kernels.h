@@ -97,6 +97,29 @@ const void *ffn_grad_fn(int cta_group, bool transposed);
 int launch_ffn_clear(uint32_t *flags, int32_t n, cudaStream_t stream);  // a cudaError_t value
 uint32_t *ffn_status_word();  // of the current device, or null
 
+// ----------------------------------------------------------------- few tokens
+constexpr int kFfnStreamTokens = 32;  // at most
+
+struct FfnStreamParams {
+    const uint16_t *x;
+    int64_t ldx;
+    const uint16_t *w[2];  // the second null, or gated
+    int64_t ldw[2];
+    int32_t M, N, K;       // rows of x and w 16-byte aligned, K a multiple of 8
+    int32_t groups;        // the launch's: of up to 16 rows that a CTA works on at once
+    int32_t act;
+    int32_t bias_fp32;
+    const void *bias;
+    const uint16_t *residual;
+    int64_t ldr;
+    FfnOut D[3];           // as in FfnParams
+    int32_t out_fp32;
+    int32_t save;
+};
+
+int64_t ffn_stream_rows(int num_sms);  // N at most
+int launch_ffn_stream(FfnStreamParams &p, int num_sms, cudaStream_t stream);  // a cudaError_t value
+
 // ----------------------------------------------------------------- rows
 // Copies of R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8).
 struct FfnPackJob {

@@ -61,6 +61,7 @@ OPTIONS = {
     "fault_skip_load": 6,
     "raster_group": 7,
     "repack": 8,
+    "stream": 9,
 }
 
 _P = ctypes.c_void_p
