@@ -17,9 +17,9 @@
 // and 128 rows of it, so that either way one thread holds both sums of an element.
 //
 // Roles (384 threads, one CTA per SM):
-//   warp 0           TMA producer: per (item, k-block) wait "empty", load the tiles
+//   warps 0, 2, 3    TMA producers, in turn: per two k-blocks wait "empty", load the tiles;
+//                    warp 2 also allocates and frees tensor memory
 //   warp 1           MMA issuer (leader CTA only in pairs), one elected lane
-//   warp 2           allocates and frees tensor memory
 //   warps 4..11      epilogue: tensor memory -> registers -> results
 //
 // Work: tiles [0, sk_tiles) are split along k, their (tile, k-block) units cut into one
@@ -608,14 +608,22 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     FfnItem w;
 
     if (warp < 4) {
-        if (warp == 0) {
-            // ---------------- TMA producer ----------------
+        if (warp != 1) {
+            // ---------------- TMA producers ----------------
+            // Waiting for a stage, announcing its bytes and issuing its loads take one warp 427
+            // clocks a k-block (and 55 more for each load beyond two), as long as 100 columns'
+            // MMAs: so the groups of two stages go round the producers.  The stages are released in
+            // order, so a producer that has waited for its group before knows that every group two
+            // laps behind its next one has been released, as long as there are no more producers
+            // than groups in the ring: no parity is mistaken for that of two phases before.
+            const int producers = S / 2 < 3 ? S / 2 : 3, me = warp == 0 ? 0 : warp - 1;
+            int turn = producers - 1;  // whose group this is
             const uint32_t full_target = kPair ? mapa_shared(full_bar, 0u) : full_bar;
             const uint32_t leader = elect_one();
             int s = 0;
             uint32_t ph = 0;
             int32_t it = 0;
-            bool ok = true;
+            bool ok = me < producers;
             grid_dependency_wait();
             while (ok && wi.next(w)) {
                 const FfnTile tc = ffn_tile_coord(w.tile, p);
@@ -626,14 +634,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                                                 : tc.col * width + (int32_t)rank * (width / CG);
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
                     if (ring_group_first(s, 1u)) {
+                        turn = turn + 1 == producers ? 0 : turn + 1;
                         const uint32_t bar = empty_bar + 8u * ring_group(s, 1u), parity = ring_empty_parity(ph);
-                        if (!__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
+                        if (turn == me && !__all_sync(0xFFFFFFFFu, mbar_wait_tries(bar, parity, ctl.suspend_ns, 1u)) &&
                             !warp_wait<false>(ctl, bar, parity, kRoleProducer, (uint32_t)s, lane)) {
                             ok = false;
                             break;
                         }
                     }
-                    if (it != p.fault_skip_it) {
+                    if (turn == me && it != p.fault_skip_it) {
                         if (rank == 0)
                             expect_tx_elected(full_bar + 8u * s, stage_bytes * CG, leader);
                         const uint32_t fb = full_target + 8u * s;
@@ -682,7 +691,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 const int32_t n = it < S ? it : S;
                 for (int32_t d = 1; d <= n; ++d) {
                     const int32_t j = it - d;
-                    if (j == p.fault_skip_it)
+                    if (j == p.fault_skip_it || (j >> 1) % producers != me)
                         continue;
                     // one that runs out has outlasted the others' loads too
                     if (!ctl.wait_drain<kPair>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
@@ -697,7 +706,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 }
             }
             __syncwarp();
-        } else if (warp == 1 && rank == 0) {
+        } else if (rank == 0) {
             // ---------------- MMA issuer ----------------
             const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
             const uint64_t cdesc0 = p.c_mn ? smem_desc_mn_sw128(stage0 + kRBytes) : smem_desc_sw128(stage0 + kRBytes);
