@@ -144,6 +144,7 @@ struct Product {
     bool a_mn = false, b_mn = false;
     Operand A[2], B[2];
     FfnParams p = {};  // what the epilogue needs
+    bool own_a = false, own_b = false;  // operands that an earlier step of the call has made
     bool no_split = false, not_transposed = false;
 };
 
@@ -402,20 +403,31 @@ int find_plan(const Device &d, const Product &x, const Plan **out)
 }
 
 // --------------------------------------------------------------- workspace
-// A call runs twice over its workspace: once to measure it, launching nothing, then in earnest.
+// A call runs twice: once to measure its workspace and to list the operands that it copies, launching
+// nothing, then in earnest.  The copies of all its products come first, in one launch, which also
+// clears the flags of all their split tiles.  The workspace holds, in this order: what the call's steps
+// hand on, the copies, the flags, and the split tiles' partials, which the products share since they
+// run one after another.
 struct Call {
     Device dev;
     cudaStream_t stream = nullptr;
     uint8_t *base = nullptr;  // null: measuring
-    size_t used = 0;
-    size_t shared = 0;  // split tiles' partials and flags: the products of a call run one after another
+    size_t used = 0;          // of the first part
+    size_t flags = 0;         // words so far
+    FfnPackJobs jobs = {};    // measuring: `dst` is an offset from the first copy
+    size_t copies = 0;        // their bytes
+    size_t partials = 0;      // measuring: the largest product's bytes; else where they start
+    uint32_t *flag_words = nullptr;
     bool measuring() const { return base == nullptr; }
 
-    // a part of the workspace: its place (null when measuring)
+    static size_t whole(size_t bytes) { return (bytes + kWorkAlign - 1) / kWorkAlign * kWorkAlign; }
+    size_t bytes() const { return used + copies + whole(flags * sizeof(uint32_t)) + partials; }
+
+    // a part of the workspace for this call's steps: its place (null when measuring)
     void *take(size_t bytes)
     {
         const size_t at = used;
-        used += (bytes + kWorkAlign - 1) / kWorkAlign * kWorkAlign;
+        used += whole(bytes);
         return base ? base + at : nullptr;
     }
 };
@@ -423,31 +435,51 @@ struct Call {
 // Rows that the library makes start at multiples of 128 bytes.
 int64_t padded(int64_t cols) { return (cols + 63) / 64 * 64; }
 
-// An operand's rows as a product reads them: as they are, or listed in `jobs` to be copied first.
-// Copied are rows that no tensor map describes (not at multiples of 16 bytes), and long operands
-// whose rows are not at multiples of 128: each 128-byte row of a box then straddles two lines of
-// L2, which bounds the product.  `readers` rows on the other side pay for the copy from 4096 on.
-void prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int64_t readers, FfnPackJobs &jobs)
+// A matrix's copy: listed when measuring, found later.
+void copy_first(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols);
+
+// An operand's rows as a product reads them: as they are, or copied.  Copied are rows that no tensor
+// map describes (not at multiples of 16 bytes), and long operands whose rows are not at multiples of
+// 128: each 128-byte row of a box then straddles two lines of L2, which bounds the product (6143 x 5999
+// x 4104 takes 200 us with both copied, of which the copy is 29, and 224 as they are).  `readers` rows
+// on the other side pay for the copy from 4096 on.  What an earlier step of the call has made
+// (`own`) needs none.
+void prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int64_t readers, bool own)
 {
     if (mem_rows < 1 || mem_cols < 1)
         return;
     const bool describable = aligned(o.p, 16) && (o.ld % 8 == 0 || mem_rows <= 1);
     const bool straddles = mem_rows > 1 && (o.ld % 64 != 0 || !aligned(o.p, 128));
     const int64_t mode = options.v[FFN_OPT_REPACK];
-    if (describable && !(straddles && (mode == 1 || (mode == 0 && readers >= 4096)))) {
+    if (own || (describable && !(straddles && (mode == 1 || (mode == 0 && readers >= 4096))))) {
         if (mem_rows <= 1)
             o.ld = padded(mem_cols);
         return;
     }
-    FfnPackJob &job = jobs.job[jobs.n++];
-    job.src = static_cast<const uint16_t *>(o.p);
-    job.lds = o.ld;
-    job.ldd = padded(mem_cols);
-    job.dst = static_cast<uint16_t *>(c.take((size_t)(mem_rows * job.ldd) * 2));
-    job.R = mem_rows;
-    job.C = (int32_t)mem_cols;
-    o.p = job.dst;
-    o.ld = job.ldd;
+    copy_first(c, o, mem_rows, mem_cols);
+}
+
+void copy_first(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols)
+{
+    const FfnPackJob *found = nullptr;  // two products may read one matrix
+    for (int i = 0; i < c.jobs.n; ++i) {
+        const FfnPackJob &j = c.jobs.job[i];
+        if (j.src == o.p && j.lds == o.ld && j.R == mem_rows && j.C == mem_cols)
+            found = &j;
+    }
+    if (!found) {  // measuring
+        FfnPackJob &job = c.jobs.job[c.jobs.n++];
+        job.src = static_cast<const uint16_t *>(o.p);
+        job.lds = o.ld;
+        job.ldd = padded(mem_cols);
+        job.dst = reinterpret_cast<uint16_t *>(c.copies);
+        c.copies += Call::whole((size_t)(mem_rows * job.ldd) * 2);
+        job.R = mem_rows;
+        job.C = (int32_t)mem_cols;
+        found = &job;
+    }
+    o.p = found->dst;
+    o.ld = found->ldd;
 }
 
 int set_out(FfnOut &out, CUtensorMap *map, const ffn_matrix &m, bool fp32, int64_t rows, int64_t cols)
@@ -465,7 +497,6 @@ FfnAux aux_of(const ffn_matrix &m)
     FfnAux a;
     a.p = m.data;
     a.ld = m.ld;
-    a.vec = aligned(m.data, 16) && m.ld % 8 == 0;
     return a;
 }
 
@@ -474,7 +505,6 @@ FfnAux aux_of(const ffn_quantized &q)
     FfnAux a;
     a.p = q.codes;
     a.ld = q.ld;
-    a.vec = 1;
     a.scales = static_cast<const uint8_t *>(q.scales);
     return a;
 }
@@ -541,23 +571,28 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     if (rc != FFN_OK)
         return rc;
     const Plan &pl = *found;
-    FfnPackJobs jobs;
-    jobs.n = 0;
     for (int i = 0; i < 2; ++i) {
         const bool has_a = i == 0 || x.form == kSum || x.form == kStack;
         const bool has_b = i == 0 || x.form == kSum || x.form == kDual;
         if (has_a)
-            prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, x.N, jobs);
+            prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, x.N, x.own_a);
         if (has_b)
-            prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, x.M, jobs);
+            prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, x.M, x.own_b);
     }
-    if (jobs.n && !c.measuring() && (rc = from_cuda((cudaError_t)launch_ffn_pack(jobs, c.dev.sms, c.stream))) != FFN_OK)
-        return rc;
-    const size_t partial_bytes = pl.sk_tiles && pl.cluster == 1
-                                     ? (size_t)pl.grid * (kFfnPartialFloats * sizeof(float) + kFfnEpiWarps * sizeof(uint32_t))
-                                     : 0;
+    // What an epilogue reads a row a thread, it reads by 16 bytes (element by element, through shared
+    // memory, the gradient of 2047 x 5999 took 227 us, not 62); a column a thread, as it is.
+    for (FfnAux &a : x.p.aux)
+        if (a.p && !a.scales && !pl.transposed && (!aligned(a.p, 16) || (a.ld % 8 != 0 && x.M > 1))) {
+            Operand o = {a.p, a.ld};
+            copy_first(c, o, x.M, x.N);
+            a.p = o.p;
+            a.ld = o.ld;
+        }
+    const bool meets = pl.sk_tiles && pl.cluster == 1;  // tiles' pieces meet through global memory
+    const size_t flags = meets ? (size_t)pl.grid * kFfnEpiWarps : 0, first_flag = c.flags;
+    c.flags += flags;
     if (c.measuring()) {
-        c.shared = std::max(c.shared, partial_bytes);
+        c.partials = std::max(c.partials, meets ? (size_t)pl.grid * kFfnPartialFloats * sizeof(float) : 0);
         return FFN_OK;
     }
     FfnMaps maps;
@@ -602,9 +637,8 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;
     p.out_fp32 = fp32 ? 1 : 0;
-    // behind the call's other parts, whose size the first run has measured
-    p.partials = partial_bytes ? reinterpret_cast<float *>(c.base + c.shared) : nullptr;
-    p.flags = partial_bytes ? reinterpret_cast<uint32_t *>(p.partials + (size_t)pl.grid * kFfnPartialFloats) : nullptr;
+    p.partials = meets ? reinterpret_cast<float *>(c.base + c.partials) : nullptr;
+    p.flags = meets ? c.flag_words + first_flag : nullptr;
     p.err = ffn_status_word();
     if (!p.err)
         return FFN_ERR_CUDA;
@@ -613,9 +647,6 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
                                        options.v[FFN_OPT_FAULT_SKIP_LOAD] >= 0 ? 0 : (uint64_t)pl.k_blocks * 2000u);
     p.fault_skip_it = (int32_t)options.v[FFN_OPT_FAULT_SKIP_LOAD];
 
-    if (partial_bytes &&
-        (rc = from_cuda((cudaError_t)launch_ffn_clear(p.flags, pl.grid * kFfnEpiWarps, c.stream))) != FFN_OK)
-        return rc;
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
@@ -633,7 +664,7 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     cfg.numAttrs = together > 1 ? 2 : 1;
     void *args[2] = {&maps, &p};
     last_plan = pl;
-    last_packed = jobs.n;
+    last_packed = c.jobs.n;
     have_last_plan = true;
     return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
 }
@@ -716,7 +747,7 @@ int run_call(F body, void *workspace, int64_t size, void *stream)
         return rc;
     if ((rc = body(c)) != FFN_OK)
         return rc;
-    const size_t need = c.used + c.shared;
+    const size_t need = c.bytes();
     if (need && (!workspace || size < (int64_t)need))
         return FFN_ERR_WORKSPACE;
     if (need && !aligned(workspace, kWorkAlign))
@@ -726,7 +757,18 @@ int run_call(F body, void *workspace, int64_t size, void *stream)
     run.stream = static_cast<cudaStream_t>(stream);
     static uint8_t none;  // never used: such a call takes nothing
     run.base = need ? static_cast<uint8_t *>(workspace) : &none;
-    run.shared = c.used;  // where the split tiles' part starts
+    run.jobs = c.jobs;
+    for (int i = 0; i < run.jobs.n; ++i) {
+        FfnPackJob &j = run.jobs.job[i];
+        j.dst = reinterpret_cast<uint16_t *>(run.base + c.used + reinterpret_cast<size_t>(j.dst));
+    }
+    run.flag_words = reinterpret_cast<uint32_t *>(run.base + c.used + c.copies);
+    run.partials = need - c.partials;
+    run.jobs.flags = c.flags ? run.flag_words : nullptr;
+    run.jobs.num_flags = (int32_t)c.flags;
+    if ((c.jobs.n || c.flags) &&
+        (rc = from_cuda((cudaError_t)launch_ffn_pack(run.jobs, run.dev.sms, run.stream))) != FFN_OK)
+        return rc;
     return body(run);
 }
 
@@ -738,7 +780,7 @@ int measure_call(F body, int64_t *bytes)
     if (rc != FFN_OK)
         return rc;
     if ((rc = body(c)) == FFN_OK)
-        *bytes = (int64_t)(c.used + c.shared);
+        *bytes = (int64_t)c.bytes();
     return rc;
 }
 
@@ -830,6 +872,7 @@ int body_linear_backward(Call &c, const ffn_linear_backward_args &a)
         Product x;
         x.M = a.M, x.N = a.K, x.K = a.N;
         x.b_mn = true;
+        x.own_a = a.activation != FFN_ACT_NONE;
         x.A[0] = {dz.data, dz.ld};
         x.B[0] = {a.weight.data, a.weight.ld};
         const int rc = run_product(c, x, &a.dx, 1, false);
@@ -840,6 +883,7 @@ int body_linear_backward(Call &c, const ffn_linear_backward_args &a)
         Product x;
         x.M = a.N, x.N = a.K, x.K = a.M;
         x.a_mn = x.b_mn = true;
+        x.own_a = a.activation != FFN_ACT_NONE;
         x.A[0] = {dz.data, dz.ld};
         x.B[0] = {a.x.data, a.x.ld};
         return run_product(c, x, &a.dweight, 1, a.dweight_type == FFN_FP32);
@@ -962,7 +1006,7 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
         Product x;
         x.form = kSum;
         x.M = a.M, x.N = a.C, x.K = a.F;
-        x.b_mn = true;
+        x.b_mn = x.own_a = true;
         x.A[0] = {t[0].data, t[0].ld};
         x.A[1] = {t[1].data, t[1].ld};
         x.B[0] = {a.w_gate.data, a.w_gate.ld};
@@ -974,7 +1018,7 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
         Product x;
         x.form = kStack;
         x.M = a.F, x.N = a.C, x.K = a.M;
-        x.a_mn = x.b_mn = true;
+        x.a_mn = x.b_mn = x.own_a = true;
         x.A[0] = {t[0].data, t[0].ld};
         x.A[1] = {t[1].data, t[1].ld};
         x.B[0] = {a.x.data, a.x.ld};
@@ -985,7 +1029,7 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
     if (a.dw_down.data) {
         Product x;
         x.M = a.N, x.N = a.F, x.K = a.M;
-        x.a_mn = x.b_mn = true;
+        x.a_mn = x.b_mn = x.own_b = true;
         x.A[0] = {a.dy.data, a.dy.ld};
         x.B[0] = {t[2].data, t[2].ld};
         return run_product(c, x, &a.dw_down, 1, a.dweight_type == FFN_FP32);

@@ -189,6 +189,8 @@ __device__ __forceinline__ uint32_t mma_bf16_block(uint32_t d_tmem, uint64_t rde
     return ready;
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // All but the newest committed bulk store of this thread have finished reading shared memory.
 __device__ __forceinline__ void bulk_wait_read_all_but_one()
 {
@@ -380,35 +382,6 @@ __device__ __forceinline__ void ffn_load_rows(FfnRaw &x, const FfnAux &a, int32_
     }
 }
 
-// Not transposed, any rows: read by the warp a row at a time, an element a lane, and turned
-// through a staging buffer.
-__device__ __forceinline__ void ffn_load_rows_any(FfnRaw &x, FfnStager &st, const FfnAux &a, int32_t row0, int32_t col,
-                                                  const FfnParams &p)
-{
-    const uint32_t at = st.acquire();
-    const uint16_t *src = static_cast<const uint16_t *>(a.p) + (int64_t)row0 * a.ld + col + st.lane;
-    const int32_t rows = col + st.lane < p.D_cols ? p.D_rows - row0 : 0;
-    for (int32_t r = 0; r < 32; r += 8) {
-        uint16_t w[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            w[k] = r + k < rows ? src[(r + k) * a.ld] : (uint16_t)0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            asm volatile("st.shared.u16 [%0], %1;" ::"r"(at + ffn_piece_offset((uint32_t)(r + k), 2u * (uint32_t)st.lane)),
-                         "h"(w[k])
-                         : "memory");
-    }
-    __syncwarp();
-#pragma unroll
-    for (uint32_t u = 0; u < 4; ++u)
-        ld_shared_v4(at + ffn_piece_offset((uint32_t)st.lane, 16u * u), x.w[4 * u], x.w[4 * u + 1], x.w[4 * u + 2],
-                     x.w[4 * u + 3]);
-    __syncwarp();
-    if (st.lane == 0)
-        bulk_commit_group();
-}
-
 // Transposed: column `col` (this thread's) of rows row .. row+31, as fp32.
 __device__ __forceinline__ void ffn_load_column(float (&v)[32], const FfnAux &a, int32_t row, int32_t col,
                                                 const FfnParams &p)
@@ -422,7 +395,7 @@ __device__ __forceinline__ void ffn_load_column(float (&v)[32], const FfnAux &a,
             v[i] = 0.0f;
             if (i < live) {
                 float hi;
-                ffn_from_e4m3x2(src[i * a.ld], v[i], hi);
+                f32x2_parts(pair_of_e4m3(src[i * a.ld]).v, v[i], hi);
                 v[i] *= ffn_scale(sc[4 * i]);
             }
         }
@@ -434,23 +407,10 @@ __device__ __forceinline__ void ffn_load_column(float (&v)[32], const FfnAux &a,
         v[i] = i < live ? __uint_as_float((uint32_t)src[i * a.ld] << 16) : 0.0f;
 }
 
-__device__ __forceinline__ void ffn_raw_floats(float (&v)[32], const FfnRaw &x, const FfnAux &a)
+// Values 2 i and 2 i + 1 of a chunk's words (`scale`: what codes are multiplied by).
+__device__ __forceinline__ Pair ffn_raw_pair(const FfnRaw &x, int i, bool codes, float scale)
 {
-    if (a.scales) {
-        const float s = ffn_scale(x.w[8]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            ffn_from_e4m3x2(x.w[i >> 1] >> (16 * (i & 1)), v[2 * i], v[2 * i + 1]);
-            v[2 * i] *= s;
-            v[2 * i + 1] *= s;
-        }
-        return;
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        v[2 * i] = bf16_low(x.w[i]);
-        v[2 * i + 1] = bf16_high(x.w[i]);
-    }
+    return codes ? pair_of_e4m3(x.w[i >> 1] >> (16 * (i & 1))) * both(scale) : pair_of_bf16(x.w[i]);
 }
 
 // Adds bias[at] (kT: one value, this thread's column) or bias[at .. at+31] to the sums.
@@ -540,9 +500,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const uint32_t done_bar = acce_bar + 16u;
     const uint32_t tmem_slot = done_bar + 8u;
     const uint32_t abort_flag = tmem_slot + 4u;
-    const uint32_t go_words = abort_flag + 4u;  // 2 words, alternating by item
-    const uint32_t ready_bar = go_words + 8u;   // cluster form: one per epilogue warp of rank 0;
-                                                // behind its eight, one that nothing waits for
+    const uint32_t ready_bar = abort_flag + 4u;  // cluster form: one per epilogue warp of rank 0;
+                                                 // behind its eight, one that nothing waits for
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
@@ -787,18 +746,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         const int32_t cta = cluster_id * CG + (int32_t)rank;
         int acc = 0;
         uint32_t acc_ph = 0;
-        uint32_t item_parity = 0;
         const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
-        // one thread waits for the accumulator and posts the outcome, so that all
-        // warps take the same branch; the word alternates with the accumulations
+        // each warp for itself: the warps of a tile need not keep step
         auto accumulated = [&]() {
-            const uint32_t go = go_words + 4u * item_parity;
-            item_parity ^= 1u;
-            if (threadIdx.x == 128)
-                st_volatile_shared_u32(
-                    go, ctl.wait<kPair>(accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc) ? 1u : 0u);
-            named_barrier_sync(1u, kFfnEpiWarps * 32u);
-            return ld_volatile_shared_u32(go) != 0u;
+            return warp_wait<kPair>(ctl, accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc, lane);
         };
         // this warp has read its part of the accumulator: hand it back
         auto hand_back = [&]() {
@@ -914,27 +865,44 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             const int32_t d_row0 = kT ? yc : yr;
             const int32_t d_col0 = kT ? yr : yc;
             constexpr int kAux = kEpi == kFfnGrad ? 2 : kEpi == kFfnPlain ? 1 : 0;
-            // rows that are read by 16 bytes are asked for ahead of their use
+            // rows are asked for ahead of their use
             FfnRaw raw[kAux > 0 ? kAux : 1];
             auto ahead = [&](int c) {
                 if constexpr (!kT && kAux > 0) {
 #pragma unroll
                     for (int i = 0; i < kAux; ++i)
-                        if (p.aux[i].p && (p.aux[i].vec || p.aux[i].scales))
+                        if (p.aux[i].p)
                             ffn_load_rows(raw[i], p.aux[i], yr + lane, yc + c * 32, p);
                 }
             };
-            auto aux_floats = [&](int i, int c, float(&f)[32]) {
+            auto aux_pairs = [&](int i, int c, Pair(&f)[16]) {
                 if constexpr (kT) {
-                    ffn_load_column(f, p.aux[i], yc + c * 32, yr + lane, p);
+                    float v[32];
+                    ffn_load_column(v, p.aux[i], yc + c * 32, yr + lane, p);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        f[e] = pair(v[2 * e], v[2 * e + 1]);
                 } else {
-                    if (!p.aux[i].vec && !p.aux[i].scales)
-                        ffn_load_rows_any(raw[i], st, p.aux[i], yr, yc + c * 32, p);
-                    ffn_raw_floats(f, raw[i], p.aux[i]);
+                    const bool codes = p.aux[i].scales != nullptr;
+                    const float scale = codes ? ffn_scale(raw[i].w[8]) : 1.0f;
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        f[e] = ffn_raw_pair(raw[i], e, codes, scale);
                 }
             };
             if (!contributor && half < nchunks)
                 ahead(half);
+            if constexpr (kT && kAux > 0) {
+                // columns are read where they are used, from L2 by then: a line a lane
+                if (!contributor && d_col0 < p.D_cols)
+                    for (int c = half; c < nchunks; c += 2)
+#pragma unroll
+                        for (int i = 0; i < kAux; ++i)
+                            if (p.aux[i].p && d_row0 + c * 32 + lane < p.D_rows)
+                                prefetch_l2(static_cast<const uint8_t *>(p.aux[i].p) +
+                                            ((int64_t)(d_row0 + c * 32 + lane) * p.aux[i].ld + d_col0) *
+                                                (p.aux[i].scales ? 1 : 2));
+            }
             if (!accumulated())
                 break;
             tc_fence_after_sync();
@@ -1016,17 +984,18 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                     if (p.act != kActNone)
                         ffn_with_act(p.act, [&](auto tag) {
 #pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                f[i] = ffn_act<decltype(tag)::value>(f[i]);
+                            for (int i = 0; i < 16; ++i)
+                                f32x2_parts(ffn_act<decltype(tag)::value>(pair(f[2 * i], f[2 * i + 1])).v, f[2 * i],
+                                            f[2 * i + 1]);
                         });
                     if (p.aux[0].p) {
-                        float r[32];
-                        aux_floats(0, c, r);
+                        Pair r[16];
+                        aux_pairs(0, c, r);
                         if (c + 2 < nchunks)
                             ahead(c + 2);
 #pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            f[i] += r[i];
+                        for (int i = 0; i < 16; ++i)
+                            f32x2_parts((pair(f[2 * i], f[2 * i + 1]) + r[i]).v, f[2 * i], f[2 * i + 1]);
                     }
                     if (p.out_fp32) {
                         ffn_store_fp32<kT>(f, st, map, out, row, col, p);
@@ -1069,34 +1038,27 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
                             pk[i] = bf16_pair(
-                                ffn_act<decltype(tag)::value>(__uint_as_float(v[0][2 * i])) * __uint_as_float(v[1][2 * i]),
-                                ffn_act<decltype(tag)::value>(__uint_as_float(v[0][2 * i + 1])) *
-                                    __uint_as_float(v[1][2 * i + 1]));
+                                ffn_act<decltype(tag)::value>(
+                                    pair(__uint_as_float(v[0][2 * i]), __uint_as_float(v[0][2 * i + 1]))) *
+                                pair(__uint_as_float(v[1][2 * i]), __uint_as_float(v[1][2 * i + 1])));
                     });
                     ffn_store_bf16<kT>(pk, st, &maps.D[0], p.D[0], row, col, p);
                 } else {
-                    float g[32], u[32];
-                    aux_floats(0, c, g);
-                    aux_floats(1, c, u);
+                    Pair g[16], u[16];
+                    aux_pairs(0, c, g);
+                    aux_pairs(1, c, u);
                     if (c + 2 < nchunks)
                         ahead(c + 2);
                     uint32_t pdu[16], ph[16];
                     ffn_with_act(p.act, [&](auto tag) {
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            float dg[2], du[2], h[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                float a, d;
-                                ffn_act_slope<decltype(tag)::value>(g[2 * i + e], a, d);
-                                const float dh = __uint_as_float(v[0][2 * i + e]);
-                                dg[e] = dh * u[2 * i + e] * d;
-                                du[e] = dh * a;
-                                h[e] = a * u[2 * i + e];
-                            }
-                            pk[i] = bf16_pair(dg[0], dg[1]);
-                            pdu[i] = bf16_pair(du[0], du[1]);
-                            ph[i] = bf16_pair(h[0], h[1]);
+                            const Pair dh = pair(__uint_as_float(v[0][2 * i]), __uint_as_float(v[0][2 * i + 1]));
+                            Pair a, d;
+                            ffn_act_slope<decltype(tag)::value>(g[i], a, d);
+                            pk[i] = bf16_pair(dh * u[i] * d);
+                            pdu[i] = bf16_pair(dh * a);
+                            ph[i] = bf16_pair(a * u[i]);
                         }
                     });
                     ffn_store_bf16<kT>(pk, st, &maps.D[0], p.D[0], row, col, p);

@@ -37,11 +37,11 @@ struct FfnOut {
     int32_t tma = 0;  // its layout allows TMA stores
 };
 
-// One bf16 matrix that an epilogue reads, of the results' size; or 8-bit codes with scales.
+// One bf16 matrix that an epilogue reads, of the results' size; or 8-bit codes with scales.  Rows
+// are 16-byte aligned where a thread reads a row (the result is not transposed).
 struct FfnAux {
     const void *p = nullptr;
     int64_t ld = 0;
-    int32_t vec = 0;  // its rows are 16-byte aligned
     const uint8_t *scales = nullptr;  // not null: codes
 };
 
@@ -94,7 +94,6 @@ const void *ffn_plain_fn(int cta_group, bool transposed);
 const void *ffn_gated_fn(int cta_group, bool transposed);
 const void *ffn_grad_fn(int cta_group, bool transposed);
 
-int launch_ffn_clear(uint32_t *flags, int32_t n, cudaStream_t stream);  // a cudaError_t value
 uint32_t *ffn_status_word();  // of the current device, or null
 
 // ----------------------------------------------------------------- few tokens
@@ -121,7 +120,7 @@ int64_t ffn_stream_rows(int num_sms);  // N at most
 int launch_ffn_stream(FfnStreamParams &p, int num_sms, cudaStream_t stream);  // a cudaError_t value
 
 // ----------------------------------------------------------------- rows
-// Copies of R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8).
+// Copies of R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8), a cudaError_t value.
 struct FfnPackJob {
     const uint16_t *src;
     int64_t lds;
@@ -134,9 +133,11 @@ struct FfnPackJob {
     int32_t vec;
 };
 struct FfnPackJobs {
-    FfnPackJob job[4];
+    FfnPackJob job[7];  // gated_backward reads seven matrices that may be copied
     int n;
     int64_t units;
+    uint32_t *flags;  // set to 0 on the way
+    int32_t num_flags;
 };
 int launch_ffn_pack(FfnPackJobs &jobs, int num_sms, cudaStream_t stream);
 

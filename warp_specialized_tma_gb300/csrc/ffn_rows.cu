@@ -40,10 +40,10 @@ __global__ void __launch_bounds__(kSlopeWarps * 32) ffn_slope_kernel(const FfnSl
     const int32_t c = (int32_t)blockIdx.x * kSlopeColumns + 8 * lane;
     const int32_t r0 = (int32_t)blockIdx.y * slice_rows;
     const int32_t r1 = min(r0 + slice_rows, p.R);
-    float sum[8];
+    Pair sum[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        sum[i] = 0.0f;
+    for (int i = 0; i < 4; ++i)
+        sum[i] = both(0.0f);
     grid_dependency_wait();
     constexpr int kRows = 2;
     for (int32_t r = r0 + warp; r < r1; r += kRows * kSlopeWarps) {
@@ -59,34 +59,35 @@ __global__ void __launch_bounds__(kSlopeWarps * 32) ffn_slope_kernel(const FfnSl
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
             const int32_t row = r + k * kSlopeWarps;
-            float f[8];
-            unpack8(dy[k], f);
-            if constexpr (A != kActNone) {
-                float x[8];
-                unpack8(z[k], x);
+            const uint32_t yw[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w};
+            Pair f[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    float a, d;
-                    ffn_act_slope<A>(x[i], a, d);
-                    f[i] *= d;
+            for (int i = 0; i < 4; ++i)
+                f[i] = pair_of_bf16(yw[i]);
+            if constexpr (A != kActNone) {
+                const uint32_t zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    Pair a, d;
+                    ffn_act_slope<A>(pair_of_bf16(zw[i]), a, d);
+                    f[i] = f[i] * d;
                 }
                 if (row < r1 && c < p.C)  // rows of dz are whole 16-byte groups, of which the last may be padding
                     *reinterpret_cast<uint4 *>(p.dz + (int64_t)row * p.lddz + c) =
-                        make_uint4(bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
-                                   bf16_pair(f[6], f[7]));
+                        make_uint4(bf16_pair(f[0]), bf16_pair(f[1]), bf16_pair(f[2]), bf16_pair(f[3]));
             }
             if (row < r1) {
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    sum[i] += f[i];
+                for (int i = 0; i < 4; ++i)
+                    sum[i] = sum[i] + f[i];
             }
         }
     }
     if (p.dbias == nullptr)
         return;
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        sums[warp][8 * lane + i] = sum[i];
+    for (int i = 0; i < 4; ++i)
+        f32x2_parts(sum[i].v, sums[warp][8 * lane + 2 * i], sums[warp][8 * lane + 2 * i + 1]);
     __syncthreads();
     const int32_t col = (int32_t)blockIdx.x * kSlopeColumns + (int32_t)threadIdx.x;
     if (col < p.C) {
@@ -122,7 +123,9 @@ __global__ void __launch_bounds__(256) ffn_column_sum_kernel(const float *partia
     }
 }
 
-// Copies of up to four matrices at the copy's bandwidth.  A warp's unit is 1024 columns of a row,
+// What a call's products need before they start: copies of operands at the copy's bandwidth, and the
+// flags of split tiles at 0 (not left so by the launch before: one that gave up leaves some set, and
+// the next would take old partials for its own).  A warp's unit is 1024 columns of a row,
 // four vectors a lane in flight.  Rows that are not 16-byte aligned are read by whole 16-byte
 // groups too: every lane takes what its own group lacks from its neighbour.
 constexpr int kPackVectors = 4;
@@ -130,7 +133,12 @@ __global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackJobs jobs)
 {
     const int lane = threadIdx.x & 31;
     const int64_t step = (int64_t)gridDim.x * 8;
+    if (jobs.n == 0)
+        grid_launch_dependents();  // the product's start overlaps the kernel before this one
     grid_dependency_wait();
+    if (blockIdx.x == 0)
+        for (int32_t i = (int32_t)threadIdx.x; i < jobs.num_flags; i += 256)
+            jobs.flags[i] = 0u;
     for (int64_t u0 = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5); u0 < jobs.units; u0 += step) {
         int64_t u = u0;
         int n = 0;
@@ -163,15 +171,6 @@ __global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackJobs jobs)
     grid_launch_dependents();
 }
 
-// The flags of a split launch, set to 0 ahead of it.
-__global__ void __launch_bounds__(256) ffn_clear_kernel(uint32_t *flags, int32_t n)
-{
-    grid_launch_dependents();
-    grid_dependency_wait();
-    for (int32_t i = (int32_t)threadIdx.x; i < n; i += 256)
-        flags[i] = 0u;
-}
-
 template <typename... P, typename... A>
 cudaError_t launch(void (*fn)(P...), dim3 grid, cudaStream_t stream, A... args)
 {
@@ -201,11 +200,6 @@ cudaError_t launch_slope(const FfnSlopeParams &p, dim3 grid, int32_t rows, cudaS
 
 }  // namespace
 
-int launch_ffn_clear(uint32_t *flags, int32_t n, cudaStream_t stream)
-{
-    return launch(ffn_clear_kernel, dim3(1), stream, flags, n);
-}
-
 int launch_ffn_pack(FfnPackJobs &jobs, int num_sms, cudaStream_t stream)
 {
     jobs.units = 0;
@@ -216,7 +210,7 @@ int launch_ffn_pack(FfnPackJobs &jobs, int num_sms, cudaStream_t stream)
         j.units = j.R * j.blocks;
         jobs.units += j.units;
     }
-    const int64_t ctas = std::min<int64_t>((jobs.units + 7) / 8, (int64_t)num_sms * 8);
+    const int64_t ctas = std::max<int64_t>(1, std::min<int64_t>((jobs.units + 7) / 8, (int64_t)num_sms * 8));
     return launch(ffn_pack_kernel, dim3((unsigned)ctas), stream, jobs);
 }
 
