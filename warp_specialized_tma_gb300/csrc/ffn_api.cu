@@ -595,6 +595,8 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
         c.partials = std::max(c.partials, meets ? (size_t)pl.grid * kFfnPartialFloats * sizeof(float) : 0);
         return FFN_OK;
     }
+    for (FfnAux &a : x.p.aux)
+        a.sectors = aligned(a.p, 32) && (a.ld * (a.scales ? 1 : 2) % 32 == 0 || x.M <= 1);
     FfnMaps maps;
     std::memset(&maps, 0, sizeof(maps));
     FfnParams &p = x.p;

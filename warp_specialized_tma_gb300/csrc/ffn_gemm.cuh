@@ -346,28 +346,43 @@ struct FfnRaw {
     uint32_t w[16];
 };
 
-// Not transposed, aligned rows: 32 columns of this thread's row, by 16 bytes.  Asynchronous to
-// what follows until the words are used.
+__device__ __forceinline__ void load_32_bytes(uint32_t *w, const void *p)
+{
+    asm volatile("ld.global.L1::no_allocate.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+
+// Not transposed: 32 columns of this thread's row.  Rows that start at multiples of 32 bytes come a
+// sector a load.  Asynchronous to what follows until the words are used.
 __device__ __forceinline__ void ffn_load_rows(FfnRaw &x, const FfnAux &a, int32_t row, int32_t col, const FfnParams &p)
 {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
         x.w[i] = 0u;
-    if (row >= p.D_rows)
+    if (row >= p.D_rows || col >= p.D_cols)
         return;
     if (a.scales) {
         const uint8_t *const src = static_cast<const uint8_t *>(a.p) + (int64_t)row * a.ld + col;
+        if (a.sectors && col + 32 <= p.D_cols) {
+            load_32_bytes(x.w, src);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 2; ++u)
-            if (col + 16 * u < p.D_cols) {  // rows are whole groups of 16
-                const uint4 q = *reinterpret_cast<const uint4 *>(src + 16 * u);
-                x.w[4 * u] = q.x, x.w[4 * u + 1] = q.y, x.w[4 * u + 2] = q.z, x.w[4 * u + 3] = q.w;
-            }
-        if (col < p.D_cols)
-            x.w[8] = a.scales[((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3)];
+            for (int u = 0; u < 2; ++u)
+                if (col + 16 * u < p.D_cols) {  // rows are whole groups of 16
+                    const uint4 q = *reinterpret_cast<const uint4 *>(src + 16 * u);
+                    x.w[4 * u] = q.x, x.w[4 * u + 1] = q.y, x.w[4 * u + 2] = q.z, x.w[4 * u + 3] = q.w;
+                }
+        }
+        x.w[8] = a.scales[((int64_t)(col >> 9) * p.D_rows + row) * 4 + ((col >> 7) & 3)];
         return;
     }
     const uint16_t *const src = static_cast<const uint16_t *>(a.p) + (int64_t)row * a.ld + col;
+    if (a.sectors && col + 32 <= p.D_cols) {
+        load_32_bytes(x.w, src);
+        load_32_bytes(x.w + 8, src + 16);
+        return;
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
         if (col + 8 * u + 8 <= p.D_cols) {

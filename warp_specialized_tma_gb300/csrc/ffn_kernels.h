@@ -43,6 +43,7 @@ struct FfnAux {
     const void *p = nullptr;
     int64_t ld = 0;
     const uint8_t *scales = nullptr;  // not null: codes
+    int32_t sectors = 0;  // rows start at multiples of 32 bytes
 };
 
 struct FfnParams {
