@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 namespace wstma {
 
@@ -17,16 +18,78 @@ constexpr int kSlopeWarps = 8;
 constexpr int kSlopeColumns = 256;  // of a warp: 8 a lane
 constexpr int kSlopeMaxSlices = 128;
 
-// Vector c .. c+7 of a row, whatever its alignment; zero past the row's end.  `live` holds for all
-// lanes or none: a lane behind the row's end still loads what its neighbour's vector ends in.
-template <bool kVec>
-__device__ __forceinline__ uint4 load8_any(const uint16_t *row, int32_t c, int32_t C, bool live)
+// The five words from word W on of a lane's 16-byte group and the next one, two bytes further if
+// `half`: four words.  The next group is the next lane's; the last lane's is `last`.
+template <int W>
+__device__ __forceinline__ uint4 turn(const uint4 q, const uint4 last, bool half)
 {
-    if constexpr (kVec)
-        return live && c < C ? load8_bf16(row, c, C, true) : make_uint4(0u, 0u, 0u, 0u);
-    else
-        return load8_bf16_shifted(row, c, C, live);
+    const uint32_t own[4] = {q.x, q.y, q.z, q.w}, behind[4] = {last.x, last.y, last.z, last.w};
+    const bool end = (threadIdx.x & 31u) == 31u;
+    uint32_t w[5];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) {
+        if (W + k < 4) {
+            w[k] = own[W + k];
+        } else {
+            const uint32_t n = __shfl_down_sync(0xFFFFFFFFu, own[W + k - 4], 1);
+            w[k] = end ? behind[W + k - 4] : n;
+        }
+    }
+    const uint32_t by = half ? 16u : 0u;
+    return make_uint4(__funnelshift_r(w[0], w[1], by), __funnelshift_r(w[1], w[2], by),
+                      __funnelshift_r(w[2], w[3], by), __funnelshift_r(w[3], w[4], by));
 }
+
+// Eight columns c .. c+7 of a row, c = 8 lane + a multiple of 256: loaded by get(), which several calls
+// of may precede value(), so that their loads are in flight together.  `live` and the row hold for
+// all lanes.  A row that is only 2-byte aligned is read by whole 16-byte groups, each lane the one its
+// vector starts in; the shift is one of four cases, the same for the warp.  Only groups that hold a
+// byte of the row are read; past its end the values are zero.
+template <bool kVec>
+struct Vector8 {
+    uint4 q, last;
+
+    __device__ __forceinline__ void get(const uint16_t *row, int32_t c, int32_t C, bool live)
+    {
+        q = make_uint4(0u, 0u, 0u, 0u);
+        if constexpr (kVec) {
+            if (live && c < C)
+                q = load8_bf16(row, c, C, true);
+        } else {
+            last = q;
+            const uint32_t mis = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+            const int32_t first = c - (int32_t)(mis >> 1);  // of the group
+            if (live && first < C)
+                q = *reinterpret_cast<const uint4 *>(row + first);
+            if (live && (threadIdx.x & 31u) == 31u && mis != 0u && first + 8 < C)
+                last = *reinterpret_cast<const uint4 *>(row + first + 8);
+        }
+    }
+
+    __device__ __forceinline__ uint4 value(const uint16_t *row, int32_t c, int32_t C) const
+    {
+        if constexpr (kVec)
+            return q;
+        const uint32_t mis = (uint32_t)reinterpret_cast<uintptr_t>(row) & 15u;
+        const bool half = (mis & 2u) != 0u;
+        uint4 o;
+        switch (__shfl_sync(0xFFFFFFFFu, mis >> 2, 0)) {
+        case 0: o = turn<0>(q, last, half); break;
+        case 1: o = turn<1>(q, last, half); break;
+        case 2: o = turn<2>(q, last, half); break;
+        default: o = turn<3>(q, last, half); break;
+        }
+        if (c + 8 > C) {
+            const int32_t n = max(C - c, 0);
+            uint32_t w[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = 2 * k + 1 < n ? w[k] : 2 * k < n ? w[k] & 0xFFFFu : 0u;
+            o = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return o;
+    }
+};
 
 // dz = dy act'(z), and its sums over a slice of the rows before it is rounded.  One pass over
 // dy and z; a warp takes 256 columns of every eighth row of its slice, two rows at a time, so
@@ -47,25 +110,27 @@ __global__ void __launch_bounds__(kSlopeWarps * 32) ffn_slope_kernel(const FfnSl
     grid_dependency_wait();
     constexpr int kRows = 2;
     for (int32_t r = r0 + warp; r < r1; r += kRows * kSlopeWarps) {
-        uint4 dy[kRows], z[kRows];
+        Vector8<kVec> dy[kRows], z[kRows];
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            const int32_t row = r + k * kSlopeWarps;
-            const bool live = row < r1;
-            dy[k] = load8_any<kVec>(p.dy + (int64_t)min(row, r1 - 1) * p.lddy, c, p.C, live);
+            const int32_t row = min(r + k * kSlopeWarps, r1 - 1);
+            const bool live = r + k * kSlopeWarps < r1;
+            dy[k].get(p.dy + (int64_t)row * p.lddy, c, p.C, live);
             if constexpr (A != kActNone)
-                z[k] = load8_any<kVec>(p.z + (int64_t)min(row, r1 - 1) * p.ldz, c, p.C, live);
+                z[k].get(p.z + (int64_t)row * p.ldz, c, p.C, live);
         }
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            const int32_t row = r + k * kSlopeWarps;
-            const uint32_t yw[4] = {dy[k].x, dy[k].y, dy[k].z, dy[k].w};
+            const int32_t row = r + k * kSlopeWarps, at = min(row, r1 - 1);
+            const uint4 y = dy[k].value(p.dy + (int64_t)at * p.lddy, c, p.C);
+            const uint32_t yw[4] = {y.x, y.y, y.z, y.w};
             Pair f[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 f[i] = pair_of_bf16(yw[i]);
             if constexpr (A != kActNone) {
-                const uint32_t zw[4] = {z[k].x, z[k].y, z[k].z, z[k].w};
+                const uint4 x = z[k].value(p.z + (int64_t)at * p.ldz, c, p.C);
+                const uint32_t zw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     Pair a, d;
@@ -126,8 +191,7 @@ __global__ void __launch_bounds__(256) ffn_column_sum_kernel(const float *partia
 // What a call's products need before they start: copies of operands at the copy's bandwidth, and the
 // flags of split tiles at 0 (not left so by the launch before: one that gave up leaves some set, and
 // the next would take old partials for its own).  A warp's unit is 1024 columns of a row,
-// four vectors a lane in flight.  Rows that are not 16-byte aligned are read by whole 16-byte
-// groups too: every lane takes what its own group lacks from its neighbour.
+// four vectors a lane in flight.
 constexpr int kPackVectors = 4;
 __global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackJobs jobs)
 {
@@ -148,25 +212,24 @@ __global__ void __launch_bounds__(256) ffn_pack_kernel(const FfnPackJobs jobs)
         const int64_t r = j.blocks == 1 ? u : u / j.blocks;
         const int32_t c = (int32_t)(u - r * j.blocks) * (kPackVectors * kSlopeColumns) + 8 * lane;
         const uint16_t *const from = j.src + r * j.lds;
-        uint4 q[kPackVectors];
-        if (j.vec) {
+        uint16_t *const to = j.dst + r * j.ldd;
+        auto copy = [&](auto vec) {
+            Vector8<decltype(vec)::value> v[kPackVectors];
+#pragma unroll
+            for (int k = 0; k < kPackVectors; ++k)
+                v[k].get(from, c + k * kSlopeColumns, j.C, true);
 #pragma unroll
             for (int k = 0; k < kPackVectors; ++k) {
                 const int32_t at = c + k * kSlopeColumns;
-                if (at + 8 <= j.C)
-                    q[k] = __ldcs(reinterpret_cast<const uint4 *>(from + at));
-                else
-                    q[k] = load8_bf16(from, at, j.C, false);
+                const uint4 q = v[k].value(from, at, j.C);
+                if (at < j.C)
+                    *reinterpret_cast<uint4 *>(to + at) = q;
             }
-        } else {
-#pragma unroll
-            for (int k = 0; k < kPackVectors; ++k)
-                q[k] = load8_bf16_shifted(from, c + k * kSlopeColumns, j.C, true);
-        }
-#pragma unroll
-        for (int k = 0; k < kPackVectors; ++k)
-            if (c + k * kSlopeColumns < j.C)
-                *reinterpret_cast<uint4 *>(j.dst + r * j.ldd + c + k * kSlopeColumns) = q[k];
+        };
+        if (j.vec)
+            copy(std::true_type{});
+        else
+            copy(std::false_type{});
     }
     grid_launch_dependents();
 }
