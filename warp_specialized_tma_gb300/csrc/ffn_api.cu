@@ -222,11 +222,11 @@ int ring_stages(const Device &d, size_t stage_bytes)
 
 // Estimated time of a tiling, in clocks of an SM (1.9 GHz), without what every launch costs:
 // the tiles of the longest chain, each its stages (k-blocks: the longest of the MMAs, 4096
-// multiply-adds a clock and SM, the loads, 63 bytes a clock and SM, and a stage's handling, 392
+// multiply-adds a clock and SM, the loads, 63 bytes a clock and SM, and a stage's handling, 341
 // clocks) or its epilogue; or all operands' time in HBM or all loads' in L2, if longer; then the last
 // epilogue and the exchange between a split tile's pieces.  The constants are fitted to 3000 measured
 // tilings of 37 products in all forms: the tiling of least estimate took at most 10 % longer than the
-// best of them, 1.2 % in the mean.
+// best of them, 1 % in the mean.
 // Fills in how the tiles are shared out.
 double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
 {
@@ -241,12 +241,17 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const int64_t split = x.no_split ? 0 : options.v[FFN_OPT_SPLIT];
     const int64_t most = t.cta_group == 2 ? d.max_pairs : d.sms;
     const double sums = (dual ? 2.0 : 1.0) * t.width;  // columns of sums a row
-    const double stage = std::max({2.0 * sums, 392.0, (double)t.stage_bytes / 62.8});
+    const double stage = std::max({2.0 * sums, 341.0, (double)t.stage_bytes / 62.8});
     const double hbm = std::max((double)(x.M + x.N * (dual ? 2 : 1)) * (double)x.K * 2.0 / 3884.0,
                                 (double)tiles * (double)KB * (double)t.stage_bytes * t.cta_group / 8791.0);
-    const double results = x.epilogue == kFfnGrad ? 3.0 : 1.0;  // and two more matrices that are read
-    const double epilogue = 26.0 * sums * results;
-    const double tile = std::max((double)KB * stage, (10.9 * sums + 1419.0) * results);
+    // What an epilogue does with a chunk, in stores of one: a transposed result's rows are read an element
+    // at a time (the gradient of 800 x 5256 x 3872 from 8 bits takes 173 us that way, and 75 not transposed).
+    double results = x.epilogue == kFfnGrad ? (t.transposed ? 3.0 : 9.0) : x.p.save == 1 ? (dual ? 3.0 : 2.0) : 1.0;
+    for (const FfnAux &a : x.p.aux)
+        if (a.p)
+            results += t.transposed ? (a.scales ? 14.0 : 6.4) : 0.5;
+    const double epilogue = 29.0 * sums * results;
+    const double tile = std::max((double)KB * stage, (5.1 * sums + 1696.0) * results * (t.transposed ? 1.8 : 1.0));
 
     t.clusters = std::min(tiles, most);
     t.sk_tiles = 0;
@@ -256,7 +261,7 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
         // each tile shared by a cluster of CTAs
         const int64_t c = std::min<int64_t>({most / tiles, kFfnMaxCluster, KB});
         if (c >= 2) {
-            const double exchange = 4944.0 + (91.0 + 14.0 * sums) * (double)(c - 1);
+            const double exchange = 4912.0 + (73.0 + 13.8 * sums) * (double)(c - 1);
             const double cost = std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + exchange;
             if (cost < best) {
                 best = cost;
@@ -273,7 +278,7 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
         if (sk && C > sk) {
             // behind whole tiles the exchange is out of sight: the split tiles come first
             const int64_t whole = (tiles - sk) / C;
-            const double exchange = whole ? 4776.0 : 8488.0 + (337.0 + 20.8 * sums) * (double)C / (double)sk;
+            const double exchange = whole ? 4824.0 : 9682.0 + (93.0 + 22.5 * sums) * (double)C / (double)sk;
             const double cost =
                 std::max((double)whole * tile + (double)ceil_div(sk * KB, C) * stage, hbm) + epilogue + exchange;
             if (cost < best) {
@@ -379,7 +384,8 @@ int find_plan(const Device &d, const Product &x, const Plan **out)
     for (int i = FFN_OPT_CTA_GROUP; i <= FFN_OPT_SPLIT; ++i)
         key.opt[i] = options.v[i];
     key.device = d.index, key.epilogue = x.epilogue, key.form = x.form;
-    key.flags = (x.a_mn ? 1 : 0) | (x.b_mn ? 2 : 0) | (x.no_split ? 4 : 0) | (x.not_transposed ? 8 : 0);
+    key.flags = (x.a_mn ? 1 : 0) | (x.b_mn ? 2 : 0) | (x.no_split ? 4 : 0) | (x.not_transposed ? 8 : 0) |
+                (x.p.aux[0].p ? 16 : 0) | (x.p.aux[0].scales ? 32 : 0) | (x.p.save << 6);
     Plan *slot = &plans[0];
     for (Plan &pl : plans) {
         if (pl.used && std::memcmp(&pl.key, &key, sizeof(key)) == 0) {
@@ -440,10 +446,11 @@ void copy_first(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols);
 
 // An operand's rows as a product reads them: as they are, or copied.  Copied are rows that no tensor
 // map describes (not at multiples of 16 bytes), and long operands whose rows are not at multiples of
-// 128: each 128-byte row of a box then straddles two lines of L2, which bounds the product (6143 x 5999
-// x 4104 takes 200 us with both copied, of which the copy is 29, and 224 as they are).  `readers` rows
-// on the other side pay for the copy from 4096 on.  What an earlier step of the call has made
-// (`own`) needs none.
+// 128: each 128-byte row of a box then straddles two lines of L2, a quarter more clocks a k-block.  The
+// copy moves the operand twice; that pays from some 3600 `readers`, rows on the other side, on, and
+// for some more its launch: 4096 x 4104 x 4104 takes 105 us with both operands copied and 108.5 as they
+// are, 2000 x 4104 x 4104 63 and 57, 6143 x 5999 x 4104 196 and 224.  What an earlier step of the call has
+// made (`own`) needs none.
 void prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, int64_t readers, bool own)
 {
     if (mem_rows < 1 || mem_cols < 1)
@@ -451,7 +458,7 @@ void prepare_operand(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols, in
     const bool describable = aligned(o.p, 16) && (o.ld % 8 == 0 || mem_rows <= 1);
     const bool straddles = mem_rows > 1 && (o.ld % 64 != 0 || !aligned(o.p, 128));
     const int64_t mode = options.v[FFN_OPT_REPACK];
-    if (own || (describable && !(straddles && (mode == 1 || (mode == 0 && readers >= 4096))))) {
+    if (own || (describable && !(straddles && (mode == 1 || (mode == 0 && (double)(readers - 3600) * (double)mem_rows * (double)mem_cols > 8e9))))) {
         if (mem_rows <= 1)
             o.ld = padded(mem_cols);
         return;
