@@ -13,7 +13,7 @@
 #include <mutex>
 
 #include "ffn_kernels.h"
-#include "fp8_overlap.h"
+#include "ffn_overlap.h"
 
 using namespace wstma;
 
@@ -701,32 +701,7 @@ int check_quantized(const ffn_quantized &q, int64_t rows, int64_t cols, int64_t 
 bool bad_act(int32_t a) { return a < FFN_ACT_NONE || a > FFN_ACT_GELU_TANH; }
 bool bad_type(int32_t t) { return t != FFN_BF16 && t != FFN_FP32; }
 
-// Bytes that a call reads or writes: rows of `width` bytes, `ld` bytes apart.
-struct Span {
-    const void *p;
-    int64_t ld, width, rows;
-    bool same_allowed = false;  // with the first result
-};
-
 Span span(const ffn_matrix &m, int64_t rows, int64_t cols, int esize = 2) { return {m.data, m.ld * esize, cols * esize, rows}; }
-
-// Whether two spans share a byte; spans of different pitches that reach over each other count as sharing.
-bool touch(const Span &a, const Span &b)
-{
-    if (!a.p || !b.p || a.rows < 1 || b.rows < 1 || a.width < 1 || b.width < 1)
-        return false;
-    using Wide = __int128;
-    const Wide at_a = (Wide) reinterpret_cast<uintptr_t>(a.p), at_b = (Wide) reinterpret_cast<uintptr_t>(b.p);
-    if (at_a + (Wide)(a.rows - 1) * a.ld + a.width <= at_b || at_b + (Wide)(b.rows - 1) * b.ld + b.width <= at_a)
-        return false;
-    if (a.rows == 1 || b.rows == 1 || a.ld != b.ld)
-        return true;
-    // one pitch: b's rows start d bytes behind a's, or behind the row before
-    Wide d = (at_b - at_a) % a.ld;
-    if (d < 0)
-        d += a.ld;
-    return d < a.width || d + b.width > a.ld;
-}
 
 // Results lie apart from what is read and from each other.
 bool apart(std::initializer_list<Span> writes, std::initializer_list<Span> reads)

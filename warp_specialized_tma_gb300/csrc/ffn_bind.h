@@ -5,6 +5,7 @@
 
 #include "bind_tensors.h"
 #include "ffn_ops.h"
+#include "ffn_overlap.h"
 
 namespace ffn_bind {
 
@@ -48,6 +49,18 @@ inline at::ScalarType result_type(PyObject *o, const char *what)
     if (st != at::kBFloat16 && st != at::kFloat)
         type_error(std::string(what) + " must be bf16 or fp32");
     return st;
+}
+
+inline wstma::Span span(const Tensor &t)
+{
+    const int64_t size = t.element_size();
+    return {data(t), (t.size(0) > 1 ? t.stride(0) : t.size(1)) * size, t.size(1) * size, t.size(0)};
+}
+
+inline void need_apart(const Tensor &out, const Tensor &in, const char *what)
+{
+    if (wstma::touch(span(out), span(in)))
+        value_error(std::string("out lies over ") + what + ": it may be the residual itself, or apart");
 }
 
 inline int truth(PyObject *o)
@@ -113,6 +126,14 @@ inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
             if (y.dim() != 2 || y.size(0) != M || y.size(1) != N)
                 value_error("out must be " + size_text(M, N));
             a.y = {data(y), pitch_of(y, "out")};
+            need_apart(y, x, "x");
+            need_apart(y, w, "weight");
+            if (bias)
+                need_apart(y, bias->unsqueeze(0), "bias");
+            const bool same = res && data(res) == data(y) && res->scalar_type() == y.scalar_type() &&
+                              (M <= 1 || a.residual.ld == a.y.ld);
+            if (res && !same)
+                need_apart(y, *res, "residual");
         } else {
             y = whole_rows(at, M, N, result_type(args[7], "out_dtype"));
             a.y = result(y);

@@ -225,9 +225,13 @@ def device_status(device=None):
     ran out (two seconds and more, where none should take a millisecond): that call's result is
     wrong.
     """
-    dev = torch.device("cuda" if device is None else device if not isinstance(device, int) else f"cuda:{device}")
+    if isinstance(device, int) and device < 0:
+        raise ValueError(f"no such device: {device}")
+    dev = torch.device("cuda" if device is None else device)
     if dev.type != "cuda":
         raise ValueError(f"{dev} is no CUDA device")
+    if not torch.cuda.is_available():
+        raise FfnError(ERR_CUDA, "ffn_device_status")
     word = ctypes.c_uint32()
     with torch.cuda.device(dev):
         st = load().ffn_device_status(ctypes.byref(word))
