@@ -566,6 +566,21 @@ int run_stream(Call &c, const Product &x, const ffn_matrix *D, int outs, bool fp
     return from_cuda((cudaError_t)launch_ffn_stream(p, c.dev.sms, c.stream));
 }
 
+// Height of the bands that tiles are walked in: as many row tiles as 32 MB of the row operand hold, so
+// that they stay in L2 from one column to the next, but 8 at least, and all if there are no more than 16;
+// bands of one height.  Under the power cap, with bands of 8 and of 16 or 32: 4096 x 16384 x 4096 329 and 319
+// us, gated 616 and 600, 8192 x 8192 x 2048 gated 312 and 303, 16384 x 8192 x 4096 627 and 620; 8192^3 648 and
+// 655 (here 8 hold 32 MB).
+int32_t band_of(const Plan &pl, int64_t K)
+{
+    const int64_t asked = options.v[FFN_OPT_RASTER_GROUP];
+    if (asked)
+        return (int32_t)std::min(asked, pl.row_tiles);
+    const int64_t tile = (int64_t)kFfnRowsPerCta * pl.cta_group * std::max<int64_t>(K, 1);
+    const int64_t most = pl.row_tiles <= 16 ? 16 : std::max<int64_t>(8, (int64_t(1) << 24) / tile);
+    return (int32_t)ceil_div(pl.row_tiles, ceil_div(pl.row_tiles, most));
+}
+
 // Runs one product; results D[0..2] (fp32: of D[0], and D[1] of kStack).
 int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
 {
@@ -640,8 +655,7 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     p.width = pl.width;
     p.c_rows = pl.c_rows;
     p.stages = pl.stages;
-    const int64_t band = options.v[FFN_OPT_RASTER_GROUP] ? options.v[FFN_OPT_RASTER_GROUP] : 8;
-    p.raster_group = (int32_t)std::min(band, pl.row_tiles);
+    p.raster_group = band_of(pl, x.K);
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;
