@@ -222,12 +222,11 @@ int ring_stages(const Device &d, size_t stage_bytes)
 
 // Estimated time of a tiling, in clocks of an SM (1.9 GHz), without what every launch costs:
 // the tiles of the longest chain, each its stages (k-blocks: the longest of the MMAs, 4096
-// multiply-adds a clock and SM, the loads, 63 bytes a clock and SM, and a stage's handling, 341
-// clocks) or its epilogue; or all operands' time in HBM or all loads' in L2, if longer; then the last
-// epilogue and the exchange between a split tile's pieces.  The constants are fitted to 3000 measured
-// tilings of 37 products in all forms: the tiling of least estimate took at most 10 % longer than the
-// best of them, 1 % in the mean.
-// Fills in how the tiles are shared out.
+// multiply-adds a clock and SM, the loads, 62 bytes a clock and SM and 9231 over all SMs, and a stage's
+// handling, 394 clocks) or its epilogue; or the operands' time in HBM and their repeated loads', if longer;
+// then the last epilogue and the exchange between a split tile's pieces.  The constants are fitted to 4000
+// measured tilings of 51 products in all forms: the tiling of least estimate took at most 11 % longer
+// than the best of them, 0.9 % in the mean.  Fills in how the tiles are shared out.
 double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
 {
     const Sides s = sides_of(x, t);
@@ -241,17 +240,24 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const int64_t split = x.no_split ? 0 : options.v[FFN_OPT_SPLIT];
     const int64_t most = t.cta_group == 2 ? d.max_pairs : d.sms;
     const double sums = (dual ? 2.0 : 1.0) * t.width;  // columns of sums a row
-    const double stage = std::max({2.0 * sums, 341.0, (double)t.stage_bytes / 62.8});
-    const double hbm = std::max((double)(x.M + x.N * (dual ? 2 : 1)) * (double)x.K * 2.0 / 3884.0,
-                                (double)tiles * (double)KB * (double)t.stage_bytes * t.cta_group / 8791.0);
+    const double l2 = (double)t.stage_bytes * (double)(std::min(tiles, most) * t.cta_group) / 9231.0;
+    const double stage = std::max({2.0 * sums, 394.0, (double)t.stage_bytes / 62.5, l2});
+    const double once = (double)(x.M + x.N * (dual ? 2 : 1)) * (double)x.K * 2.0;
+    const double loads = (double)tiles * (double)KB * (double)t.stage_bytes * t.cta_group;
+    const double hbm = once / 4661.0 + std::max(0.0, loads - once) / 40743.0;
     // What an epilogue does with a chunk, in stores of one: a transposed result's rows are read an element
     // at a time (the gradient of 800 x 5256 x 3872 from 8 bits takes 173 us that way, and 75 not transposed).
-    double results = x.epilogue == kFfnGrad ? (t.transposed ? 3.0 : 9.0) : x.p.save == 1 ? (dual ? 3.0 : 2.0) : 1.0;
+    const bool grad = x.epilogue == kFfnGrad;
+    double results = grad || (dual && x.p.save == 1) ? 3.0 : x.p.save == 1 ? 2.0 : 1.0;
     for (const FfnAux &a : x.p.aux)
-        if (a.p)
-            results += t.transposed ? (a.scales ? 14.0 : 6.4) : 0.5;
-    const double epilogue = 29.0 * sums * results;
-    const double tile = std::max((double)KB * stage, (5.1 * sums + 1696.0) * results * (t.transposed ? 1.8 : 1.0));
+        if (a.p && t.transposed)
+            results += a.scales ? 14.0 : 6.4;
+    const double epilogue = 15.6 * sums * results;
+    const double chunks = grad && !t.transposed ? 90.0 * sums + 4800.0
+                                                : (4.0 * sums + 1853.0) * results * (t.transposed ? 1.7 : 1.0);
+    // a gradient's epilogue and the loads of the next tile slow each other down
+    const double tile =
+        std::max((double)KB * stage, chunks) + (grad ? 0.15 * std::min((double)KB * stage, chunks) : 0.0);
 
     t.clusters = std::min(tiles, most);
     t.sk_tiles = 0;
@@ -261,7 +267,7 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
         // each tile shared by a cluster of CTAs
         const int64_t c = std::min<int64_t>({most / tiles, kFfnMaxCluster, KB});
         if (c >= 2) {
-            const double exchange = 4912.0 + (73.0 + 13.8 * sums) * (double)(c - 1);
+            const double exchange = 7685.0 + (130.0 + 14.1 * sums) * (double)(c - 1);
             const double cost = std::max((double)ceil_div(KB, c) * stage, hbm) + epilogue + exchange;
             if (cost < best) {
                 best = cost;
@@ -271,22 +277,25 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
             }
         }
     }
-    if (split) {
-        // the last, partial wave of tiles (or all, if they do not fill one) shared by all clusters
-        const int64_t sk = tiles % most;
-        const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
-        if (sk && C > sk) {
-            // behind whole tiles the exchange is out of sight: the split tiles come first
-            const int64_t whole = (tiles - sk) / C;
-            const double exchange = whole ? 4824.0 : 9682.0 + (93.0 + 22.5 * sums) * (double)C / (double)sk;
-            const double cost =
-                std::max((double)whole * tile + (double)ceil_div(sk * KB, C) * stage, hbm) + epilogue + exchange;
-            if (cost < best) {
-                best = cost;
-                t.clusters = C;
-                t.sk_tiles = sk;
-                t.cluster = 1;
-            }
+    // The last, partial wave of tiles (or all, if they do not fill one) shared by all clusters.  (With a wave
+    // more of tiles shared, so that few pieces make a tile, nothing was gained: 160 tiles, 84 and 8 of them
+    // shared by 76 pairs, 98 and 94 us.)
+    const int64_t sk = tiles % most;
+    const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
+    const int64_t whole = C ? (tiles - sk) / C : 0;
+    // (a gradient's epilogues are what its tiles wait for: 1000 x 3000 x 1000 takes 26 us with its last wave
+    // shared, and 20)
+    if (split && sk && C > sk && !(grad && whole)) {
+        // behind whole tiles the exchange is out of sight for as long as one takes: the split tiles come first
+        const double meet = 11435.0 + (59.0 + 25.4 * sums) * (double)C / (double)sk;
+        const double exchange = whole ? std::max(6396.0, meet - tile) : meet;
+        const double cost =
+            std::max((double)whole * tile + (double)ceil_div(sk * KB, C) * stage, hbm) + epilogue + exchange;
+        if (cost < best) {
+            best = cost;
+            t.clusters = C;
+            t.sk_tiles = sk;
+            t.cluster = 1;
         }
     }
     return best;

@@ -62,11 +62,10 @@ __host__ __device__ __forceinline__ int32_t ffn_range_of(int64_t units, int32_t 
     return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
 }
 
-// A cluster's items in order: its range of the split tiles' units (a range is no longer than a
-// tile, since sk_tiles < clusters, so it touches at most two tiles), then every clusters-th
-// whole tile.  A range's first piece may start inside a tile (it then leaves a partial); a piece
-// that starts at k-block 0 and does not reach the tile's end is the last of its range.  So no
-// cluster waits for a partial before it has left its own.
+// A cluster's items in order: its range of the split tiles' units (a piece of each tile that it
+// touches), then every clusters-th whole tile.  Only a range's first piece may start inside a tile (it
+// then leaves a partial); a piece that starts at k-block 0 and does not reach the tile's end is the
+// last of its range.  So no cluster waits for a partial before it has left its own.
 struct FfnWork {
     int64_t u, u_end;
     int32_t dp, C, T, KB;
