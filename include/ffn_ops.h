@@ -70,6 +70,8 @@ typedef enum ffn_option {
     FFN_OPT_RASTER_GROUP = 7, /* tiles are walked in bands of this many row tiles */
     FFN_OPT_STREAM = 9,       /* forward products of few tokens on the kernel that streams the weights: 1 = up to
                                  32 tokens, 2 = never */
+    FFN_OPT_TOGETHER = 10,    /* a gradient's products that need none of each other in one launch: 1 = always, 2 =
+                                 never */
     FFN_OPT_REPACK = 8        /* operands whose rows do not start at multiples of 128 bytes: 1 = copied first, 2 =
                                  read as they are where a tensor map can describe them */
 } ffn_option;
@@ -85,6 +87,8 @@ typedef struct ffn_plan_info_s {
     int32_t split_tiles;  /* tiles split along K */
     int32_t cluster;      /* CTAs of a cluster that share a tile (1: none) */
     int32_t packed;       /* operands copied to the workspace first */
+    int32_t products;     /* of the launch */
+    int32_t reserved;
 } ffn_plan_info_t;
 
 /* Rows of bf16 (or, where a type is named, of that), `ld` elements apart. */
@@ -107,7 +111,7 @@ FFN_API const char *ffn_version(void);
 
 FFN_API int ffn_set_option(int key, int64_t value);
 FFN_API int ffn_get_option(int key, int64_t *value);
-/* The plan of the calling thread's last product. */
+/* The plan of the calling thread's last product (the first of its launch). */
 FFN_API int ffn_plan_info(ffn_plan_info_t *info);
 
 /* ---- product with bias, activation and residual -------------------------- */

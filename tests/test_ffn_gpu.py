@@ -55,6 +55,18 @@ VARIANTS = {
 }
 variants = pytest.mark.parametrize("variant", VARIANTS.values(), ids=VARIANTS.keys())
 
+# a gradient's products one after the other, in each of these, or in one launch
+GRADIENTS = {k: dict(v, together=2) for k, v in VARIANTS.items()}
+GRADIENTS |= {
+    "together": dict(together=1),
+    "together-one": dict(together=1, cta_group=1),
+    "together-pair": dict(together=1, cta_group=2),
+    "together-narrow": dict(together=1, cta_group=1, width=32),
+    "together-wide": dict(together=1, cta_group=2, width=256),
+    "auto": dict(),
+}
+gradients = pytest.mark.parametrize("variant", GRADIENTS.values(), ids=GRADIENTS.keys())
+
 
 def check_linear(M, N, K, *, activation=None, bias=None, residual=False, save=False, dtype=bf, seed=0, **options):
     x, w = randn(M, K, seed=seed), randn(N, K, seed=seed + 1, scale=max(K, 1) ** -0.5)
@@ -212,7 +224,7 @@ def test_results_over_what_is_read_are_refused():
 
 
 # ------------------------------------------------------------------ linear_backward
-@variants
+@gradients
 @pytest.mark.parametrize("M,N,K", [(128, 128, 128), (1, 1, 1), (300, 257, 520), (16, 600, 1000), (700, 72, 33), (3, 520, 8)])
 def test_linear_backward_variants(variant, M, N, K):
     x, w, dy, z = randn(M, K, seed=1), randn(N, K, seed=2, scale=0.1), randn(M, N, seed=3), randn(M, N, seed=4)
@@ -233,7 +245,7 @@ def test_linear_backward_variants(variant, M, N, K):
     assert ref.close(db, wb, (ref.ACT_ERROR * 2.2 + M * 2.0**-24 * 1.13) * dy.double().abs().sum(0), torch.float32)
 
 
-@variants
+@gradients
 def test_gradients_of_integers_are_exact(variant):
     M, N, K = 400, 264, 328
     x, w, dy, z = ints(M, K, seed=1), ints(N, K, seed=2), ints(M, N, seed=3), ints(M, N, seed=4)
@@ -302,7 +314,7 @@ def test_checkpoints_in_8_bits(M, C, F, cta_group):
         assert qc.view(torch.uint8).equal(codes.view(torch.uint8)) and qs.view(torch.uint8).equal(scales.view(torch.uint8))
 
 
-@variants
+@gradients
 @pytest.mark.parametrize("save", ["bf16", "e4m3"])
 @pytest.mark.parametrize("M,C,F,N", [(128, 128, 128, 128), (1, 1, 1, 1), (300, 136, 257, 200), (20, 520, 600, 264), (70, 33, 1030, 7)])
 def test_gated_backward_variants(variant, save, M, C, F, N):
@@ -337,7 +349,7 @@ def test_gated_backward_variants(variant, save, M, C, F, N):
             assert ref.close_rms(b, w, bf if w is want[0] else torch.float32, extra=2.0**-10)
 
 
-@variants
+@gradients
 def test_gated_gradients_of_integers_are_exact(variant):
     M, C, F, N = 200, 136, 264, 72
     x, wg, wu, wd = ints(M, C, seed=1, top=1), ints(F, C, seed=2, top=1), ints(F, C, seed=3, top=1), ints(N, F, seed=4, top=1)
@@ -627,6 +639,24 @@ def test_a_launch_may_give_up_at_any_load(variant):
         assert st == ffn.ERR_DEVICE_TIMEOUT or skip > 1
         with ffn.options(stream=2, **variant):
             assert ffn.linear(x, w).cpu().equal(want)
+        assert ffn.device_status() == (ffn.OK, 0)
+
+
+def test_products_of_one_launch_may_give_up():
+    x, w, _ = problem(300, 640, 2000, 1)
+    dy = ints(300, 640, seed=3).cuda()
+    for variant, skip in itertools.product((dict(cta_group=1, width=64), dict(cta_group=2, width=256), dict(cta_group=2, width=32)), (0, 1, 6, 17)):
+        with ffn.options(together=1, **variant):
+            want = ffn.linear_backward(dy, x, w, grad_dtype=torch.float32)
+            assert ffn.plan_info()["products"] == 2
+        with ffn.options(together=1, watchdog_ns=4000000, fault_skip_load=skip, **variant):
+            ffn.linear_backward(dy, x, w)
+            st, _ = ffn.device_status()
+        assert st == ffn.ERR_DEVICE_TIMEOUT or (st == ffn.OK and skip > 6)
+        with ffn.options(together=1, **variant):
+            got = ffn.linear_backward(dy, x, w, grad_dtype=torch.float32)
+        assert got[0].equal(want[0]) and got[1].equal(want[1])
+        assert got[1].double().equal(dy.double().T @ x.double())
         assert ffn.device_status() == (ffn.OK, 0)
 
 

@@ -22,7 +22,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL - 1023;  // a tile past the last row still has a 32-bit index
 constexpr size_t kWorkAlign = 256;    // of the parts of a workspace
 constexpr int64_t kMaxPitch = int64_t(1) << 37;
-constexpr int kNumOptions = 10;
+constexpr int kNumOptions = 11;
 constexpr int kPlans = 64;              // plans a thread remembers
 constexpr int kMaxCtas = 1024;          // bounds the workspace of split tiles
 constexpr int64_t kMinSplitBlocks = 8;  // k-blocks per cluster below which tiles are not split further
@@ -146,10 +146,12 @@ struct Product {
     FfnParams p = {};  // what the epilogue needs
     bool own_a = false, own_b = false;  // operands that an earlier step of the call has made
     bool no_split = false, not_transposed = false;
+    ffn_matrix D[3] = {};  // results
+    bool fp32 = false;     // of D[0], and D[1] of kStack
 };
 
 struct Options {
-    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0, 0};
+    int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0, 0, 0};
 };
 thread_local Options options;
 
@@ -168,13 +170,23 @@ struct Plan {
     int64_t row_tiles, row_split, col_tiles, tiles, k_blocks, k_split, sk_tiles;
     size_t smem, stage_bytes;
     const void *fn;
+    double cost;
+};
+
+// Up to kFfnMaxProducts products in one launch, if that takes less time than one after the other.
+struct Together {
+    PlanKey key[kFfnMaxProducts];
+    uint64_t used;
+    bool yes;
+    Plan plan[kFfnMaxProducts];
 };
 
 thread_local Plan plans[kPlans];
+thread_local Together togethers[16];
 thread_local uint64_t plan_clock = 0;
 thread_local Plan last_plan;
 thread_local bool have_last_plan = false;
-thread_local int32_t last_packed = 0;
+thread_local int32_t last_packed = 0, last_products = 0;
 
 const void *kernel_fn(int epilogue, int cta_group, bool transposed)
 {
@@ -193,6 +205,7 @@ struct Tiling {
     int64_t clusters = 0;  // SM pairs, or CTAs, of the grid
     int64_t sk_tiles = 0;
     int cluster = 1;  // CTAs that share a tile in a cluster
+    double tile = 0.0, epilogue = 0.0, hbm = 0.0;
 };
 
 struct Sides {
@@ -259,6 +272,9 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const double tile =
         std::max((double)KB * stage, chunks) + (grad ? 0.15 * std::min((double)KB * stage, chunks) : 0.0);
 
+    t.tile = tile;
+    t.epilogue = epilogue;
+    t.hbm = hbm;
     t.clusters = std::min(tiles, most);
     t.sk_tiles = 0;
     t.cluster = 1;
@@ -324,10 +340,32 @@ int resident_clusters(const Device &d, const void *fn, size_t smem, int c)
     return n;
 }
 
+int64_t k_blocks_of(const Product &x) { return ceil_div(x.K, kFfnBlockK) * (x.form == kSum ? 2 : 1); }
+
+// The plan of a tiling, without its ring and grid.
+int plan_tiles(const Product &x, const Tiling &t, Plan &pl)
+{
+    const Sides s = sides_of(x, t);
+    pl.transposed = t.transposed;
+    pl.cta_group = t.cta_group;
+    pl.width = t.width;
+    pl.c_rows = t.c_rows;
+    pl.stage_bytes = t.stage_bytes;
+    pl.row_tiles = s.row_tiles;
+    pl.row_split = x.form == kStack ? s.row_tiles / 2 : s.row_tiles;
+    pl.col_tiles = s.col_tiles;
+    pl.tiles = s.row_tiles * s.col_tiles;
+    pl.k_blocks = k_blocks_of(x);
+    pl.k_split = x.form == kSum ? pl.k_blocks / 2 : pl.k_blocks;
+    pl.sk_tiles = 0;
+    pl.cluster = 1;
+    return pl.tiles > kMaxDim || pl.k_blocks > kMaxDim ? FFN_ERR_UNSUPPORTED : FFN_OK;
+}
+
 int make_plan(const Device &d, const Product &x, Plan &pl)
 {
     const int64_t *opt = options.v;
-    const int64_t KB = ceil_div(x.K, kFfnBlockK) * (x.form == kSum ? 2 : 1);
+    const int64_t KB = k_blocks_of(x);
     Tiling best = {false, 0, 0};
     double best_cost = 0.0;
     for (int cg = 1; cg <= 2; ++cg)
@@ -354,20 +392,10 @@ int make_plan(const Device &d, const Product &x, Plan &pl)
         }
     if (best.cta_group == 0)
         return FFN_ERR_UNSUPPORTED;
-    const Sides s = sides_of(x, best);
-    pl.transposed = best.transposed;
-    pl.cta_group = best.cta_group;
-    pl.width = best.width;
-    pl.c_rows = best.c_rows;
-    pl.stage_bytes = best.stage_bytes;
-    pl.row_tiles = s.row_tiles;
-    pl.row_split = x.form == kStack ? s.row_tiles / 2 : s.row_tiles;
-    pl.col_tiles = s.col_tiles;
-    pl.tiles = s.row_tiles * s.col_tiles;
-    pl.k_blocks = KB;
-    pl.k_split = x.form == kSum ? KB / 2 : KB;
-    if (pl.tiles > kMaxDim || KB > kMaxDim)
-        return FFN_ERR_UNSUPPORTED;
+    const int rc = plan_tiles(x, best, pl);
+    if (rc != FFN_OK)
+        return rc;
+    pl.cost = best_cost;
     pl.stages = ring_stages(d, pl.stage_bytes);
     pl.smem = ffn_smem_bytes(pl.stage_bytes, pl.stages);
     pl.fn = kernel_fn(x.epilogue, pl.cta_group, pl.transposed);
@@ -385,21 +413,28 @@ int make_plan(const Device &d, const Product &x, Plan &pl)
     return from_cuda(cudaFuncSetAttribute(pl.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem));
 }
 
-int find_plan(const Device &d, const Product &x, const Plan **out)
+PlanKey key_of(const Device &d, const Product &x)
 {
     PlanKey key;
     std::memset(&key, 0, sizeof(key));
     key.M = x.M, key.N = x.N, key.K = x.K;
     for (int i = FFN_OPT_CTA_GROUP; i <= FFN_OPT_SPLIT; ++i)
         key.opt[i] = options.v[i];
+    key.opt[0] = options.v[FFN_OPT_TOGETHER];
     key.device = d.index, key.epilogue = x.epilogue, key.form = x.form;
     key.flags = (x.a_mn ? 1 : 0) | (x.b_mn ? 2 : 0) | (x.no_split ? 4 : 0) | (x.not_transposed ? 8 : 0) |
                 (x.p.aux[0].p ? 16 : 0) | (x.p.aux[0].scales ? 32 : 0) | (x.p.save << 6);
+    return key;
+}
+
+int find_plan(const Device &d, const Product &x, Plan *out)
+{
+    const PlanKey key = key_of(d, x);
     Plan *slot = &plans[0];
     for (Plan &pl : plans) {
         if (pl.used && std::memcmp(&pl.key, &key, sizeof(key)) == 0) {
             pl.used = ++plan_clock;
-            *out = &pl;
+            *out = pl;
             return FFN_OK;
         }
         if (pl.used < slot->used)
@@ -413,6 +448,109 @@ int find_plan(const Device &d, const Product &x, const Plan **out)
     pl.key = key;
     pl.used = ++plan_clock;
     *slot = pl;
+    *out = pl;
+    return FFN_OK;
+}
+
+// What each launch costs beyond its estimate: 3.7 us for the least product.
+constexpr double kLaunchClocks = 8000.0;
+
+// Whether n plain products, none of which needs another's result, take less time in one launch, and
+// their plans there: one kind of tile, the products with the longest tiles first, every cluster taking
+// each clusters-th tile of all.  (linear_backward of 16 x 512 x 512 takes 7.5 us so, and 13.7 in two
+// launches; of 4096^3 164 and 173; gated_backward of 4115 x 361 x 888 45 and 62.)
+int find_together(const Device &d, Product **xs, const Plan *alone, int n, const Together **out)
+{
+    PlanKey key[kFfnMaxProducts];
+    std::memset(key, 0, sizeof(key));
+    for (int i = 0; i < n; ++i)
+        key[i] = key_of(d, *xs[i]);
+    Together *slot = &togethers[0];
+    for (Together &t : togethers) {
+        if (t.used && std::memcmp(t.key, key, sizeof(key)) == 0) {
+            t.used = ++plan_clock;
+            *out = &t;
+            return FFN_OK;
+        }
+        if (t.used < slot->used)
+            slot = &t;
+    }
+    const int64_t *opt = options.v;
+    double separate = (n - 1) * kLaunchClocks;
+    for (int i = 0; i < n; ++i)
+        separate += alone[i].cost;
+    Tiling best[kFfnMaxProducts];
+    double best_cost = 0.0;
+    int best_cg = 0;
+    for (int cg = 1; cg <= 2; ++cg)
+        for (int wd = 32; wd <= kFfnMaxWidth; wd += 32) {
+            if ((opt[FFN_OPT_CTA_GROUP] && cg != opt[FFN_OPT_CTA_GROUP]) || opt[FFN_OPT_TRANSPOSED] == 2 ||
+                (opt[FFN_OPT_WIDTH] && wd != opt[FFN_OPT_WIDTH]))
+                continue;
+            Tiling t[kFfnMaxProducts];
+            const int64_t C = cg == 2 ? d.max_pairs : d.sms;
+            double hbm = 0.0, epilogue = 0.0;
+            int64_t count[kFfnMaxProducts], total = 0;
+            for (int i = 0; i < n; ++i) {
+                t[i] = {false, cg, wd};
+                tiling_cost(d, *xs[i], k_blocks_of(*xs[i]), t[i]);
+                const Sides s = sides_of(*xs[i], t[i]);
+                count[i] = s.row_tiles * s.col_tiles;
+                total += count[i];
+                hbm += t[i].hbm;
+                epilogue = std::max(epilogue, t[i].epilogue);
+            }
+            // the cluster whose tiles take longest
+            double chain = 0.0;
+            for (int64_t c = 0; c < std::min(C, total); ++c) {
+                double sum = 0.0;
+                int64_t first = 0;
+                for (int i = 0; i < n; ++i) {
+                    const auto upto = [&](int64_t end) { return end > c ? (end - c - 1) / C + 1 : 0; };
+                    sum += (double)(upto(first + count[i]) - upto(first)) * t[i].tile;
+                    first += count[i];
+                }
+                chain = std::max(chain, sum);
+            }
+            const double cost = std::max(chain, hbm) + epilogue;
+            if (best_cg == 0 || cost < best_cost) {
+                best_cg = cg;
+                best_cost = cost;
+                for (int i = 0; i < n; ++i)
+                    best[i] = t[i];
+            }
+        }
+    Together g;
+    std::memset(&g, 0, sizeof(g));
+    g.yes = best_cg && opt[FFN_OPT_TOGETHER] != 2 && (opt[FFN_OPT_TOGETHER] == 1 || best_cost < separate);
+    if (g.yes) {
+        size_t stage_bytes = 0;
+        int64_t total = 0;
+        for (int i = 0; i < n; ++i) {
+            const int rc = plan_tiles(*xs[i], best[i], g.plan[i]);
+            if (rc != FFN_OK)
+                return rc;
+            stage_bytes = std::max(stage_bytes, g.plan[i].stage_bytes);
+            total += g.plan[i].tiles;
+        }
+        if (total > kMaxDim)
+            return FFN_ERR_UNSUPPORTED;
+        for (int i = 0; i < n; ++i) {
+            Plan &pl = g.plan[i];
+            pl.stage_bytes = stage_bytes;
+            pl.stages = ring_stages(d, stage_bytes);
+            pl.smem = ffn_smem_bytes(stage_bytes, pl.stages);
+            pl.fn = ffn_together_fn(best_cg);
+            pl.grid = (int)std::min<int64_t>(total, best_cg == 2 ? d.max_pairs : d.sms) * best_cg;
+        }
+        const int rc = from_cuda(
+            cudaFuncSetAttribute(g.plan[0].fn, cudaFuncAttributeMaxDynamicSharedMemorySize, d.max_smem));
+        if (rc != FFN_OK)
+            return rc;
+    }
+    std::memcpy(g.key, key, sizeof(key));
+    g.used = ++plan_clock;
+    *slot = g;
     *out = slot;
     return FFN_OK;
 }
@@ -546,7 +684,9 @@ bool streams(const Call &c, const Product &x)
     return x.M <= 16 ? !dual || x.N * x.K <= 1 << 25 : x.N * x.K <= 1 << 24;
 }
 
-int run_stream(Call &c, const Product &x, const ffn_matrix *D, int outs, bool fp32)
+void remember(const Call &c, const Plan &pl, int products);
+
+int run_stream(Call &c, const Product &x)
 {
     if (c.measuring())
         return FFN_OK;
@@ -563,15 +703,15 @@ int run_stream(Call &c, const Product &x, const ffn_matrix *D, int outs, bool fp
     p.bias_fp32 = x.p.bias_fp32;
     p.residual = static_cast<const uint16_t *>(x.p.aux[0].p);
     p.ldr = x.p.aux[0].ld;
-    for (int i = 0; i < outs; ++i) {
-        p.D[i].p = D[i].data;
-        p.D[i].ld = D[i].ld;
+    for (int i = 0; i < 3; ++i) {
+        p.D[i].p = x.D[i].data;
+        p.D[i].ld = x.D[i].ld;
     }
-    p.out_fp32 = fp32 ? 1 : 0;
+    p.out_fp32 = x.fp32 ? 1 : 0;
     p.save = x.p.save;
-    std::memset(&last_plan, 0, sizeof(last_plan));
-    last_packed = 0;
-    have_last_plan = true;
+    Plan none;
+    std::memset(&none, 0, sizeof(none));
+    remember(c, none, 1);
     return from_cuda((cudaError_t)launch_ffn_stream(p, c.dev.sms, c.stream));
 }
 
@@ -590,47 +730,35 @@ int32_t band_of(const Plan &pl, int64_t K)
     return (int32_t)ceil_div(pl.row_tiles, ceil_div(pl.row_tiles, most));
 }
 
-// Runs one product; results D[0..2] (fp32: of D[0], and D[1] of kStack).
-int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
+// A product's operands, and what its epilogue reads, as its kernel takes them: as they are, or copied.
+void prepare(Call &c, Product &x, const Plan &pl)
 {
-    if (x.M == 0 || x.N == 0)
-        return FFN_OK;
-    if (streams(c, x))
-        return run_stream(c, x, D, outs, fp32);
-    const Plan *found = nullptr;
-    int rc = find_plan(c.dev, x, &found);
-    if (rc != FFN_OK)
-        return rc;
-    const Plan &pl = *found;
     for (int i = 0; i < 2; ++i) {
         const bool has_a = i == 0 || x.form == kSum || x.form == kStack;
         const bool has_b = i == 0 || x.form == kSum || x.form == kDual;
         if (has_a)
             prepare_operand(c, x.A[i], x.a_mn ? x.K : x.M, x.a_mn ? x.M : x.K, x.N, x.own_a);
         if (has_b)
-            prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, x.M, x.own_b);
+            prepare_operand(c, x.B[i], x.b_mn ? x.K : x.N, x.b_mn ? x.N : x.K, x.form == kStack ? 2 * x.M : x.M,
+                            x.own_b);
     }
     // What an epilogue reads a row a thread, it reads by 16 bytes (element by element, through shared
     // memory, the gradient of 2047 x 5999 took 227 us, not 62); a column a thread, as it is.
-    for (FfnAux &a : x.p.aux)
+    for (FfnAux &a : x.p.aux) {
         if (a.p && !a.scales && !pl.transposed && (!aligned(a.p, 16) || (a.ld % 8 != 0 && x.M > 1))) {
             Operand o = {a.p, a.ld};
             copy_first(c, o, x.M, x.N);
             a.p = o.p;
             a.ld = o.ld;
         }
-    const bool meets = pl.sk_tiles && pl.cluster == 1;  // tiles' pieces meet through global memory
-    const size_t flags = meets ? (size_t)pl.grid * kFfnEpiWarps : 0, first_flag = c.flags;
-    c.flags += flags;
-    if (c.measuring()) {
-        c.partials = std::max(c.partials, meets ? (size_t)pl.grid * kFfnPartialFloats * sizeof(float) : 0);
-        return FFN_OK;
-    }
-    for (FfnAux &a : x.p.aux)
         a.sectors = aligned(a.p, 32) && (a.ld * (a.scales ? 1 : 2) % 32 == 0 || x.M <= 1);
-    FfnMaps maps;
-    std::memset(&maps, 0, sizeof(maps));
-    FfnParams &p = x.p;
+    }
+}
+
+// The kernel's view of a product that has been prepared.
+int describe(const Product &x, const Plan &pl, FfnMaps &maps, FfnParams &p)
+{
+    p = x.p;
     const Operand *R = pl.transposed ? x.B : x.A, *C = pl.transposed ? x.A : x.B;
     const int64_t rows = pl.transposed ? x.N : x.M, cols = pl.transposed ? x.M : x.N;
     p.r_mn = pl.transposed ? x.b_mn : x.a_mn;
@@ -648,9 +776,9 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
                 (i < (two_c ? 2 : 1) && !encode(&maps.C[i], C[i], p.c_mn, cols, c_box)))
                 return FFN_ERR_TENSORMAP;
     }
-    for (int i = 0; i < outs; ++i)
-        if (D[i].data)
-            set_out(p.D[i], &maps.D[i], D[i], fp32 && (i == 0 || x.form == kStack), x.M, x.N);
+    for (int i = 0; i < 3; ++i)
+        if (x.D[i].data)
+            set_out(p.D[i], &maps.D[i], x.D[i], x.fp32 && (i == 0 || x.form == kStack), x.M, x.N);
     p.rows = (int32_t)rows;
     p.cols = (int32_t)cols;
     p.D_rows = (int32_t)x.M;
@@ -663,14 +791,13 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     p.row_split = (int32_t)pl.row_split;
     p.width = pl.width;
     p.c_rows = pl.c_rows;
+    p.stage_bytes = (int32_t)pl.stage_bytes;
     p.stages = pl.stages;
     p.raster_group = band_of(pl, x.K);
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;
-    p.out_fp32 = fp32 ? 1 : 0;
-    p.partials = meets ? reinterpret_cast<float *>(c.base + c.partials) : nullptr;
-    p.flags = meets ? c.flag_words + first_flag : nullptr;
+    p.out_fp32 = x.fp32 ? 1 : 0;
     p.err = ffn_status_word();
     if (!p.err)
         return FFN_ERR_CUDA;
@@ -678,7 +805,11 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     p.watchdog_ns = std::max<uint64_t>((uint64_t)options.v[FFN_OPT_WATCHDOG_NS],
                                        options.v[FFN_OPT_FAULT_SKIP_LOAD] >= 0 ? 0 : (uint64_t)pl.k_blocks * 2000u);
     p.fault_skip_it = (int32_t)options.v[FFN_OPT_FAULT_SKIP_LOAD];
+    return FFN_OK;
+}
 
+int launch(const Call &c, const Plan &pl, void *arg)
+{
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     cfg.gridDim = dim3((unsigned)pl.grid, 1, 1);
@@ -694,11 +825,86 @@ int run_product(Call &c, Product &x, const ffn_matrix *D, int outs, bool fp32)
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = together > 1 ? 2 : 1;
-    void *args[2] = {&maps, &p};
+    void *args[1] = {arg};
+    return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
+}
+
+void remember(const Call &c, const Plan &pl, int products)
+{
     last_plan = pl;
     last_packed = c.jobs.n;
+    last_products = products;
     have_last_plan = true;
-    return from_cuda(cudaLaunchKernelExC(&cfg, pl.fn, args));
+}
+
+// Runs one product.
+int run_product(Call &c, Product &x)
+{
+    if (x.M == 0 || x.N == 0)
+        return FFN_OK;
+    if (streams(c, x))
+        return run_stream(c, x);
+    Plan pl;
+    int rc = find_plan(c.dev, x, &pl);
+    if (rc != FFN_OK)
+        return rc;
+    prepare(c, x, pl);
+    const bool meets = pl.sk_tiles && pl.cluster == 1;  // tiles' pieces meet through global memory
+    const size_t flags = meets ? (size_t)pl.grid * kFfnEpiWarps : 0, first_flag = c.flags;
+    c.flags += flags;
+    if (c.measuring()) {
+        c.partials = std::max(c.partials, meets ? (size_t)pl.grid * kFfnPartialFloats * sizeof(float) : 0);
+        return FFN_OK;
+    }
+    FfnArgs<1> args;
+    std::memset(static_cast<void *>(&args), 0, sizeof(args));
+    if ((rc = describe(x, pl, args.maps[0], args.p[0])) != FFN_OK)
+        return rc;
+    args.p[0].partials = meets ? reinterpret_cast<float *>(c.base + c.partials) : nullptr;
+    args.p[0].flags = meets ? c.flag_words + first_flag : nullptr;
+    remember(c, pl, 1);
+    return launch(c, pl, &args);
+}
+
+// Runs plain products, none of which needs another's result, in one launch or one after the other.
+int run_products(Call &c, Product *all, int count)
+{
+    Product *xs[kFfnMaxProducts];
+    int n = 0, rc;
+    for (int i = 0; i < count; ++i)
+        if (all[i].M > 0 && all[i].N > 0)
+            xs[n++] = &all[i];
+    const Together *group = nullptr;
+    if (n > 1 && options.v[FFN_OPT_TOGETHER] != 2) {
+        // those with the longest tiles first, so that the last tiles are short ones
+        std::stable_sort(xs, xs + n, [](const Product *a, const Product *b) { return k_blocks_of(*a) > k_blocks_of(*b); });
+        Plan alone[kFfnMaxProducts];
+        for (int i = 0; i < n; ++i)
+            if ((rc = find_plan(c.dev, *xs[i], &alone[i])) != FFN_OK)
+                return rc;
+        if ((rc = find_together(c.dev, xs, alone, n, &group)) != FFN_OK)
+            return rc;
+    }
+    if (!group || !group->yes) {
+        for (int i = 0; i < n; ++i)
+            if ((rc = run_product(c, *xs[i])) != FFN_OK)
+                return rc;
+        return FFN_OK;
+    }
+    for (int i = 0; i < n; ++i)
+        prepare(c, *xs[i], group->plan[i]);
+    if (c.measuring())
+        return FFN_OK;
+    FfnArgs<kFfnMaxProducts> args;
+    std::memset(static_cast<void *>(&args), 0, sizeof(args));
+    for (int i = 0; i < kFfnMaxProducts; ++i) {
+        if (i < n && (rc = describe(*xs[i], group->plan[i], args.maps[i], args.p[i])) != FFN_OK)
+            return rc;
+        args.first[i + 1] = args.first[i] + args.p[i].num_tiles;
+        args.p[0].watchdog_ns = std::max(args.p[0].watchdog_ns, args.p[i].watchdog_ns);
+    }
+    remember(c, group->plan[0], n);
+    return launch(c, group->plan[0], &args);
 }
 
 // --------------------------------------------------------------- checks
@@ -824,8 +1030,10 @@ int body_linear(Call &c, const ffn_linear_args &a)
     x.p.bias_fp32 = a.bias_type == FFN_FP32;
     x.p.aux[0] = aux_of(a.residual);
     x.p.save = a.z.data ? 1 : 0;
-    const ffn_matrix D[2] = {a.y, a.z};
-    return run_product(c, x, D, 2, a.y_type == FFN_FP32);
+    x.D[0] = a.y;
+    x.D[1] = a.z;
+    x.fp32 = a.y_type == FFN_FP32;
+    return run_product(c, x);
 }
 
 int check_linear_backward(const ffn_linear_backward_args &a)
@@ -875,27 +1083,28 @@ int body_linear_backward(Call &c, const ffn_linear_backward_args &a)
                 return rc;
         }
     }
+    Product xs[2];
+    int n = 0;
     if (a.dx.data) {
-        Product x;
+        Product &x = xs[n++];
         x.M = a.M, x.N = a.K, x.K = a.N;
         x.b_mn = true;
         x.own_a = a.activation != FFN_ACT_NONE;
         x.A[0] = {dz.data, dz.ld};
         x.B[0] = {a.weight.data, a.weight.ld};
-        const int rc = run_product(c, x, &a.dx, 1, false);
-        if (rc != FFN_OK)
-            return rc;
+        x.D[0] = a.dx;
     }
     if (a.dweight.data) {
-        Product x;
+        Product &x = xs[n++];
         x.M = a.N, x.N = a.K, x.K = a.M;
         x.a_mn = x.b_mn = true;
         x.own_a = a.activation != FFN_ACT_NONE;
         x.A[0] = {dz.data, dz.ld};
         x.B[0] = {a.x.data, a.x.ld};
-        return run_product(c, x, &a.dweight, 1, a.dweight_type == FFN_FP32);
+        x.D[0] = a.dweight;
+        x.fp32 = a.dweight_type == FFN_FP32;
     }
-    return FFN_OK;
+    return run_products(c, xs, n);
 }
 
 // --------------------------------------------------------------- gated
@@ -946,8 +1155,10 @@ int body_gated(Call &c, const ffn_gated_args &a)
         x.p.ldq[0] = a.qg.ld;
         x.p.ldq[1] = a.qu.ld;
     }
-    const ffn_matrix D[3] = {a.h, a.g, a.u};
-    return run_product(c, x, D, 3, false);
+    x.D[0] = a.h;
+    x.D[1] = a.g;
+    x.D[2] = a.u;
+    return run_product(c, x);
 }
 
 int check_gated_backward(const ffn_gated_backward_args &a)
@@ -1006,11 +1217,15 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
         const bool bits8 = a.qg.codes != nullptr;
         x.p.aux[0] = bits8 ? aux_of(a.qg) : aux_of(a.g);
         x.p.aux[1] = bits8 ? aux_of(a.qu) : aux_of(a.u);
-        if ((rc = run_product(c, x, t, 3, false)) != FFN_OK)
+        for (int i = 0; i < 3; ++i)
+            x.D[i] = t[i];
+        if ((rc = run_product(c, x)) != FFN_OK)
             return rc;
     }
+    Product xs[3];
+    int n = 0;
     if (a.dx.data) {
-        Product x;
+        Product &x = xs[n++];
         x.form = kSum;
         x.M = a.M, x.N = a.C, x.K = a.F;
         x.b_mn = x.own_a = true;
@@ -1018,30 +1233,30 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
         x.A[1] = {t[1].data, t[1].ld};
         x.B[0] = {a.w_gate.data, a.w_gate.ld};
         x.B[1] = {a.w_up.data, a.w_up.ld};
-        if ((rc = run_product(c, x, &a.dx, 1, false)) != FFN_OK)
-            return rc;
+        x.D[0] = a.dx;
     }
     if (a.dw_gate.data) {
-        Product x;
+        Product &x = xs[n++];
         x.form = kStack;
         x.M = a.F, x.N = a.C, x.K = a.M;
         x.a_mn = x.b_mn = x.own_a = true;
         x.A[0] = {t[0].data, t[0].ld};
         x.A[1] = {t[1].data, t[1].ld};
         x.B[0] = {a.x.data, a.x.ld};
-        const ffn_matrix D[2] = {a.dw_gate, a.dw_up};
-        if ((rc = run_product(c, x, D, 2, a.dweight_type == FFN_FP32)) != FFN_OK)
-            return rc;
+        x.D[0] = a.dw_gate;
+        x.D[1] = a.dw_up;
+        x.fp32 = a.dweight_type == FFN_FP32;
     }
     if (a.dw_down.data) {
-        Product x;
+        Product &x = xs[n++];
         x.M = a.N, x.N = a.F, x.K = a.M;
         x.a_mn = x.b_mn = x.own_b = true;
         x.A[0] = {a.dy.data, a.dy.ld};
         x.B[0] = {t[2].data, t[2].ld};
-        return run_product(c, x, &a.dw_down, 1, a.dweight_type == FFN_FP32);
+        x.D[0] = a.dw_down;
+        x.fp32 = a.dweight_type == FFN_FP32;
     }
-    return FFN_OK;
+    return run_products(c, xs, n);
 }
 
 }  // namespace
@@ -1078,6 +1293,7 @@ FFN_API int ffn_set_option(int key, int64_t value)
     case FFN_OPT_WATCHDOG_NS: ok = value >= 100000 && value <= 60000000000LL; break;
     case FFN_OPT_FAULT_SKIP_LOAD: ok = value >= -1 && value <= 0x7FFFFFFF; break;
     case FFN_OPT_RASTER_GROUP: ok = value >= 0 && value <= 1024; break;
+    case FFN_OPT_TOGETHER: ok = value >= 0 && value <= 2; break;
     case FFN_OPT_STREAM: ok = value >= 0 && value <= 2; break;
     case FFN_OPT_REPACK: ok = value >= 0 && value <= 2; break;
     default: break;
@@ -1111,6 +1327,7 @@ FFN_API int ffn_plan_info(ffn_plan_info_t *info)
     info->split_tiles = (int32_t)last_plan.sk_tiles;
     info->cluster = last_plan.cluster;
     info->packed = last_packed;
+    info->products = last_products;
     return FFN_OK;
 }
 

@@ -44,6 +44,7 @@ constexpr uint64_t kFfnDrainNs = 20000000;
 
 struct FfnItem {
     int32_t tile, kb0, kb1;
+    int32_t product;  // of the launch
 };
 
 __host__ __device__ __forceinline__ int64_t ffn_range_begin(int64_t units, int32_t clusters, int32_t c)
@@ -100,6 +101,39 @@ struct FfnWork {
             return true;
         }
         return false;
+    }
+};
+
+// The items of a cluster: of one product, or every clusters-th tile of several.
+template <int kN>
+struct FfnWalk {
+    FfnWork one;
+    int32_t t, step;
+
+    __host__ __device__ __forceinline__ void init(const FfnArgs<kN> &a, int32_t cluster, int32_t clusters)
+    {
+        if constexpr (kN == 1)
+            one.init(a.p[0], cluster, clusters);
+        t = cluster;
+        step = clusters;
+    }
+
+    __host__ __device__ __forceinline__ bool next(const FfnArgs<kN> &a, FfnItem &w)
+    {
+        w.product = 0;
+        if constexpr (kN == 1) {
+            return one.next(w);
+        } else {
+            if (t >= a.first[kN])
+                return false;
+            while (t >= a.first[w.product + 1])
+                ++w.product;
+            w.tile = t - a.first[w.product];
+            w.kb0 = 0;
+            w.kb1 = a.p[w.product].num_k_blocks;
+            t += step;
+            return true;
+        }
     }
 };
 
@@ -519,21 +553,21 @@ __device__ __forceinline__ float *ffn_partial(float *partials, int32_t cta, int 
 }
 
 // ---------------------------------------------------------------- the kernel
-template <int CG, bool kT, int kEpi>
-__global__ void __launch_bounds__(kFfnThreads, 1)
-    ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnParams p)
+template <int CG, bool kT, int kEpi, int kN = 1>
+__global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs<kN> args)
 {
     constexpr bool kPair = CG == 2;
     constexpr bool kDual = kEpi == kFfnGated;
     constexpr int kAccs = kDual ? 2 : 1;  // accumulators of an element
     constexpr uint32_t kTileRBytes = (uint32_t)kFfnRowsPerCta * 128u;
     constexpr uint32_t kRBytes = kTileRBytes * (kDual && kT ? 2u : 1u);
-    const int32_t width = p.width;
-    const uint32_t stage_bytes = kRBytes + (uint32_t)p.c_rows * 128u;  // a multiple of 1024
+    static_assert(kN == 1 || (kEpi == kFfnPlain && !kT), "several products in one launch are plain ones");
+    const FfnParams &p0 = args.p[0];  // what all products share
+    const uint32_t stage_bytes = (uint32_t)p0.stage_bytes;  // a multiple of 1024
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    const int S = p.stages;  // even: stages are released in pairs
+    const int S = p0.stages;  // even: stages are released in pairs
     const uint32_t stage0 = base;
     const uint32_t staging0 = base + (uint32_t)S * stage_bytes;
     const uint32_t full_bar = staging0 + kFfnEpiWarps * kFfnStagingBytes;
@@ -549,7 +583,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
     const uint32_t rank = kPair ? cluster_ctarank() : 0u;  // in an SM pair
-    const bool shared_tile = !kPair && p.cluster > 1;
+    const bool shared_tile = kN == 1 && !kPair && p0.cluster > 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < S; ++s) {
@@ -564,17 +598,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         mbar_init(ready_bar + 64u, 1);
         if (shared_tile)
             for (int e = 0; e < kFfnEpiWarps; ++e)
-                mbar_init(ready_bar + 8u * e, (uint32_t)p.cluster - 1u);  // that warp of every other rank
+                mbar_init(ready_bar + 8u * e, (uint32_t)p0.cluster - 1u);  // that warp of every other rank
         st_shared_u32(abort_flag, 0u);
         fence_mbarrier_init();
     }
     if (threadIdx.x == 32) {
-        if (p.num_k_blocks) {  // an empty sum's operands have no maps
-            prefetch_tensormap(&maps.R[0]);
-            prefetch_tensormap(&maps.C[0]);
+        for (int i = 0; i < kN; ++i) {
+            if (args.p[i].num_k_blocks) {  // an empty sum's operands have no maps
+                prefetch_tensormap(&args.maps[i].R[0]);
+                prefetch_tensormap(&args.maps[i].C[0]);
+            }
+            if (args.p[i].D[0].tma)
+                prefetch_tensormap(&args.maps[i].D[0]);
         }
-        if (p.D[0].tma)
-            prefetch_tensormap(&maps.D[0]);
     }
     // all CTAs of a cluster have initialised their barriers before any cross-CTA
     // arrive, TMA completion or the paired allocation
@@ -599,14 +635,13 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
     WaitCtl ctl;
     ctl.abort_flag = abort_flag;
     ctl.peer_abort_flag = kPair ? mapa_shared(abort_flag, rank ^ 1u) : 0u;
-    ctl.err = p.err;
-    ctl.set_limit(p.watchdog_ns);
+    ctl.err = p0.err;
+    ctl.set_limit(p0.watchdog_ns);
 
     const int32_t cluster_id = (int32_t)blockIdx.x / CG;
     const int32_t num_clusters = (int32_t)gridDim.x / CG;
-    const int32_t KB = p.num_k_blocks;
-    FfnWork wi;
-    wi.init(p, cluster_id, num_clusters);
+    FfnWalk<kN> wi;
+    wi.init(args, cluster_id, num_clusters);
     FfnItem w;
 
     if (warp < 4) {
@@ -627,7 +662,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             int32_t it = 0;
             bool ok = me < producers;
             grid_dependency_wait();
-            while (ok && wi.next(w)) {
+            while (ok && wi.next(args, w)) {
+                const FfnParams &p = args.p[w.product];
+                const FfnMaps &maps = args.maps[w.product];
+                const int32_t width = p.width;
+                const uint32_t loaded = (kRBytes + (uint32_t)p.c_rows * 128u) * CG;  // of a stage
                 const FfnTile tc = ffn_tile_coord(w.tile, p);
                 const bool other = tc.row >= p.row_split;  // tiles of the second row operand
                 const int32_t yr =
@@ -644,9 +683,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                             break;
                         }
                     }
-                    if (turn == me && it != p.fault_skip_it) {
+                    if (turn == me && it != p0.fault_skip_it) {
                         if (rank == 0)
-                            expect_tx_elected(full_bar + 8u * s, stage_bytes * CG, leader);
+                            expect_tx_elected(full_bar + 8u * s, loaded, leader);
                         const uint32_t fb = full_target + 8u * s;
                         const uint32_t sa = stage0 + (uint32_t)s * stage_bytes;
                         const bool second = kb >= p.k_split;
@@ -693,7 +732,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 const int32_t n = it < S ? it : S;
                 for (int32_t d = 1; d <= n; ++d) {
                     const int32_t j = it - d;
-                    if (j == p.fault_skip_it || (j >> 1) % producers != me)
+                    if (j == p0.fault_skip_it || (j >> 1) % producers != me)
                         continue;
                     // one that runs out has outlasted the others' loads too
                     if (!ctl.wait_drain<kPair>(full_bar + 8u * (uint32_t)ring_stage_of(j, S), ring_parity_of(j, S),
@@ -710,12 +749,6 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             __syncwarp();
         } else if (rank == 0) {
             // ---------------- MMA issuer ----------------
-            const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
-            const uint64_t cdesc0 = p.c_mn ? smem_desc_mn_sw128(stage0 + kRBytes) : smem_desc_sw128(stage0 + kRBytes);
-            const uint64_t rstep = p.r_mn ? 2048u >> 4 : 32u >> 4, cstep = p.c_mn ? 2048u >> 4 : 32u >> 4;
-            const int32_t mma_n = kDual && !kT ? 2 * kFfnDualWidth : width;
-            const uint32_t idesc = idesc_bf16_f32(kFfnRowsPerCta * CG, 0) | ((uint32_t)(mma_n >> 3) << 17) |
-                                   (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
             const uint32_t step = stage_bytes >> 4;
             const uint32_t leader = elect_one();
             // A wait that runs out does not leave the k loop: it records the fact, and the rest
@@ -740,7 +773,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
             int acc = 0;
             uint32_t acc_ph = 0;
             uint32_t ready = 0u;  // the next stage was seen full
-            while (wi.next(w)) {
+            while (wi.next(args, w)) {
+                const FfnParams &p = args.p[w.product];
+                const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
+                const uint64_t cdesc0 =
+                    p.c_mn ? smem_desc_mn_sw128(stage0 + kRBytes) : smem_desc_sw128(stage0 + kRBytes);
+                const uint64_t rstep = p.r_mn ? 2048u >> 4 : 32u >> 4, cstep = p.c_mn ? 2048u >> 4 : 32u >> 4;
+                const int32_t mma_n = kDual && !kT ? 2 * kFfnDualWidth : p.width;
+                const uint32_t idesc = idesc_bf16_f32(kFfnRowsPerCta * CG, 0) | ((uint32_t)(mma_n >> 3) << 17) |
+                                       (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
                 wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
                 tc_fence_after_sync();
                 const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFfnMaxWidth);
@@ -783,13 +824,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
         const int ew = warp - 4;
         const int q = warp & 3;    // tensor-memory lane quadrant
         const int half = ew >> 2;  // takes chunks half, half + 2, ... of 32 columns
-        const int nchunks = (width + 31) / 32;
         FfnStager st = {staging0 + (uint32_t)ew * kFfnStagingBytes, lane, 0u};
         const uint32_t acce_target = kPair ? mapa_shared(acce_bar, 0u) : acce_bar;
         const int32_t cta = cluster_id * CG + (int32_t)rank;
         int acc = 0;
         uint32_t acc_ph = 0;
-        const bool dense = p.sk_units >= num_clusters;  // every range holds a unit
+        const bool dense = p0.sk_units >= num_clusters;  // every range holds a unit
         // each warp for itself: the warps of a tile need not keep step
         auto accumulated = [&]() {
             return warp_wait<kPair>(ctl, accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc, lane);
@@ -810,15 +850,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                                 (uint32_t)(acc * kFfnMaxWidth + a * kFfnDualWidth + c * 32),
                             v);
         };
-        while (wi.next(w)) {
+        while (wi.next(args, w)) {
+            const FfnParams &p = args.p[w.product];
+            const FfnMaps &maps = args.maps[w.product];
+            const int32_t KB = p.num_k_blocks, width = p.width;
+            const int nchunks = (width + 31) / 32;
             const FfnTile tc = ffn_tile_coord(w.tile, p);
             const bool other = tc.row >= p.row_split;
             // the accumulator's rows and columns of this warp
             const int32_t yr =
                 ((other ? tc.row - p.row_split : tc.row) * CG + (int32_t)rank) * kFfnRowsPerCta + q * 32;
             const int32_t yc = tc.col * width;
-            const bool contributor = w.kb0 > 0;
-            const bool owner = w.kb0 == 0 && w.kb1 < KB;
+            const bool contributor = kN == 1 && w.kb0 > 0;
+            const bool owner = kN == 1 && w.kb0 == 0 && w.kb1 < KB;
             // the clusters whose ranges start inside this tile, owner only; a range
             // may be empty (fewer units than clusters), and then leaves nothing
             int32_t last = cluster_id;

@@ -13,4 +13,10 @@ const void *ffn_plain_fn(int cta_group, bool transposed)
                       : reinterpret_cast<const void *>(&ffn_gemm_kernel<1, false, kFfnPlain>);
 }
 
+const void *ffn_together_fn(int cta_group)
+{
+    return cta_group == 2 ? reinterpret_cast<const void *>(&ffn_gemm_kernel<2, false, kFfnPlain, kFfnMaxProducts>)
+                          : reinterpret_cast<const void *>(&ffn_gemm_kernel<1, false, kFfnPlain, kFfnMaxProducts>);
+}
+
 }  // namespace wstma

@@ -56,6 +56,7 @@ struct FfnParams {
     int32_t r_mn, c_mn;        // operand's rows are contiguous (an operand is contiguous along k otherwise)
     int32_t width;             // of a tile on the column side, per accumulator
     int32_t c_rows;            // rows of the column operand that a CTA loads per stage
+    int32_t stage_bytes;       // of the ring, the same for all products of a launch
     int32_t stages;
     int32_t raster_group;
     int32_t sk_tiles;          // tiles [0, sk_tiles) are split along k among all clusters
@@ -82,6 +83,16 @@ struct FfnMaps {
     CUtensorMap R[2], C[2], D[3];
 };
 
+// The products of one launch; more than one (of the plain epilogue, none split) one after the other,
+// product i's tiles first[i] .. first[i + 1] - 1.
+constexpr int kFfnMaxProducts = 3;
+template <int kN>
+struct FfnArgs {
+    FfnMaps maps[kN];
+    FfnParams p[kN];
+    int32_t first[kN + 1];
+};
+
 inline int ffn_chunk_rows(bool mn, int rows) { return mn ? (rows + 63) / 64 * 64 : rows; }
 
 inline size_t ffn_smem_bytes(size_t stage_bytes, int stages)
@@ -90,10 +101,11 @@ inline size_t ffn_smem_bytes(size_t stage_bytes, int stages)
            512 /* barriers */;
 }
 
-// (FfnMaps, FfnParams)
+// (FfnArgs<1>), the last (FfnArgs<kFfnMaxProducts>)
 const void *ffn_plain_fn(int cta_group, bool transposed);
 const void *ffn_gated_fn(int cta_group, bool transposed);
 const void *ffn_grad_fn(int cta_group, bool transposed);
+const void *ffn_together_fn(int cta_group);
 
 uint32_t *ffn_status_word();  // of the current device, or null
 

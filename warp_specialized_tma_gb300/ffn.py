@@ -62,6 +62,7 @@ OPTIONS = {
     "raster_group": 7,
     "repack": 8,
     "stream": 9,
+    "together": 10,
 }
 
 _P = ctypes.c_void_p
@@ -92,6 +93,8 @@ class PlanInfo(ctypes.Structure):
         ("split_tiles", ctypes.c_int32),
         ("cluster", ctypes.c_int32),
         ("packed", ctypes.c_int32),
+        ("products", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
     ]
 
     def as_dict(self) -> dict:
