@@ -263,8 +263,8 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const bool grad = x.epilogue == kFfnGrad;
     double results = grad || (dual && x.p.save == 1) ? 3.0 : x.p.save == 1 ? 2.0 : 1.0;
     for (const FfnAux &a : x.p.aux)
-        if (a.p && t.transposed)
-            results += a.scales ? 14.0 : 6.4;
+        if (a.p && t.transposed)  // a residual's first chunk is asked for ahead, all of it up to a width of 64
+            results += a.scales ? 14.0 : !grad && t.width <= 64 ? 2.0 : 6.4;
     const double epilogue = 15.6 * sums * results;
     const double chunks = grad && !t.transposed ? 90.0 * sums + 4800.0
                                                 : (4.0 * sums + 1853.0) * results * (t.transposed ? 1.7 : 1.0);

@@ -962,8 +962,26 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                             ffn_load_rows(raw[i], p.aux[i], yr + lane, yc + c * 32, p);
                 }
             };
+            // transposed, a residual's first chunk: a column, an element a load, all of them ahead too (64 x
+            // 8192 x 8192 with a residual and a bias 34.7 us without)
+            constexpr bool kEarly = kT && kEpi == kFfnPlain;
+            uint16_t early[kEarly ? 32 : 1];
+            auto ahead_column = [&]() {
+                if constexpr (kEarly) {
+                    const int32_t row = yc + half * 32, live = yr + lane < p.D_cols ? p.D_rows - row : 0;
+                    const uint16_t *const src = static_cast<const uint16_t *>(p.aux[0].p) + (int64_t)row * p.aux[0].ld + yr + lane;
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        early[e] = e < live ? src[e * p.aux[0].ld] : (uint16_t)0;
+                }
+            };
             auto aux_pairs = [&](int i, int c, Pair(&f)[16]) {
-                if constexpr (kT) {
+                if (kEarly && c == half) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        f[e] = pair(__uint_as_float((uint32_t)early[kEarly ? 2 * e : 0] << 16),
+                                    __uint_as_float((uint32_t)early[kEarly ? 2 * e + 1 : 0] << 16));
+                } else if constexpr (kT) {
                     float v[32];
                     ffn_load_column(v, p.aux[i], yc + c * 32, yr + lane, p);
 #pragma unroll
@@ -977,12 +995,15 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                         f[e] = ffn_raw_pair(raw[i], e, codes, scale);
                 }
             };
-            if (!contributor && half < nchunks)
+            if (!contributor && half < nchunks) {
                 ahead(half);
+                if (kEarly && p.aux[0].p)
+                    ahead_column();
+            }
             if constexpr (kT && kAux > 0) {
                 // columns are read where they are used, from L2 by then: a line a lane
                 if (!contributor && d_col0 < p.D_cols)
-                    for (int c = half; c < nchunks; c += 2)
+                    for (int c = kEarly ? half + 2 : half; c < nchunks; c += 2)
 #pragma unroll
                         for (int i = 0; i < kAux; ++i)
                             if (p.aux[i].p && d_row0 + c * 32 + lane < p.D_rows)
