@@ -1,7 +1,8 @@
 // CPU check of the feed-forward products' work split and tile order (host functions of
 // ffn_gemm.cuh): every (tile, k-block) is one cluster's, a cluster leaves at most one partial and
 // before it waits for any, an owner's list of pieces is exactly the ranges that start inside its
-// tile, and every tile has a place of its own.
+// tile, those ranges are of clusters with lower indices (in the cluster form: of the owner's own cluster),
+// and every tile has a place of its own.
 #include <cstdio>
 #include <map>
 #include <set>
@@ -11,19 +12,23 @@
 
 using namespace wstma;
 
-static int check(int32_t tiles, int32_t KB, int32_t C, int32_t sk)
+static int check(int32_t tiles, int32_t KB, int32_t C, int32_t sk, int32_t cluster = 1)
 {
     FfnParams p = {};
+    p.cluster = cluster;
     p.num_k_blocks = KB;
     p.num_tiles = tiles;
     p.sk_tiles = sk;
     p.sk_units = (int64_t)sk * KB;
     std::map<std::pair<int, int>, int> seen;
-    std::map<int, std::set<int>> pieces;  // tile -> clusters that leave a partial of it
-    std::map<int, int> owner;
+    std::map<int, std::set<int>> pieces;  // tile -> ranges that leave a partial of it
+    std::map<int, int> owner;             // tile -> its owner's range
     for (int c = 0; c < C; ++c) {
         FfnWork w;
         w.init(p, c, C);
+        const int32_t range = ffn_range_at(p, C, c);
+        if (ffn_range_at(p, C, range) != c)
+            return 8;
         FfnItem it;
         int partials = 0, owned = 0;
         while (w.next(it)) {
@@ -37,11 +42,11 @@ static int check(int32_t tiles, int32_t KB, int32_t C, int32_t sk)
             if (it.kb0 > 0) {
                 if (++partials > 1 || owned)
                     return 3;
-                pieces[it.tile].insert(c);
+                pieces[it.tile].insert(range);
             } else if (it.kb1 < KB) {
                 if (owner.count(it.tile))
                     return 4;
-                owner[it.tile] = c;
+                owner[it.tile] = range;
                 ++owned;
             }
         }
@@ -56,6 +61,12 @@ static int check(int32_t tiles, int32_t KB, int32_t C, int32_t sk)
                 listed.insert(j);
         if (listed != pieces[o.first])
             return 6;
+        const int own = ffn_range_at(p, C, o.second);
+        for (int j : listed) {
+            const int other = ffn_range_at(p, C, j);
+            if (cluster > 1 ? own % cluster != 0 || other / cluster != own / cluster : other >= own)
+                return 9;
+        }
         pieces.erase(o.first);
     }
     return pieces.empty() ? 0 : 7;
@@ -89,7 +100,7 @@ int main()
                 if (tiles < C && KB)
                     splits.insert(tiles);
                 if (tiles * 4 <= C && KB >= 4)  // a tile per cluster of four CTAs
-                    if (const int e = check(tiles, KB, tiles * 4, tiles)) {
+                    if (const int e = check(tiles, KB, tiles * 4, tiles, 4)) {
                         std::printf("cluster form: tiles %d KB %d: %d\n", tiles, KB, e);
                         return 1;
                     }

@@ -606,6 +606,25 @@ def test_calls_at_once_on_streams_of_their_own():
         assert all(t.cpu().equal(want) for t in o)
 
 
+def test_split_tiles_meet_beside_other_streams():
+    """Launches of SM pairs and of single SMs, all split, on streams of two priorities: each finds its places
+    piecemeal, and none may wait for a CTA that the others keep from starting."""
+    low, high = torch.cuda.Stream(priority=0), torch.cuda.Stream(priority=-1)
+    work = [(low, dict(SPLIT, cta_group=2, width=64), problem(300, 2560, 6000, 5)),
+            (high, SPLIT, problem(20, 2560, 6000, 16)),
+            (low, dict(SPLIT, width=64), problem(100, 2600, 4000, 27)),
+            (high, dict(SPLIT, cta_group=2, width=64), problem(260, 2000, 4000, 38))]
+    torch.cuda.synchronize()
+    outs = [[] for _ in work]
+    for _ in range(30):
+        for o, (stream, options, (x, w, _)) in zip(outs, work):
+            with ffn.options(**options):
+                o.append(ffn.linear(x, w, stream=stream))
+    assert ffn.device_status() == (ffn.OK, 0)
+    for o, (_, _, (_, _, want)) in zip(outs, work):
+        assert all(t.cpu().equal(want) for t in o)
+
+
 def test_a_backward_pass_from_a_graph():
     M, C, F, N = 200, 136, 264, 136
     x, wg, wu, wd = (ints(*s, seed=i, top=1).cuda() for i, s in enumerate(((M, C), (F, C), (F, C), (N, F))))

@@ -63,6 +63,15 @@ __host__ __device__ __forceinline__ int32_t ffn_range_of(int64_t units, int32_t 
     return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
 }
 
+// Which range is cluster c's, and whose range c is: the last cluster has the first one.  A tile's owner
+// waits for the ranges behind its own, so for clusters with lower indices, which the GPU places
+// before it: whatever else runs there, another stream's split tiles say, no cluster that is waited for still
+// needs a place.  (The CTAs of a cluster that share a tile have their places together.)
+__host__ __device__ __forceinline__ int32_t ffn_range_at(const FfnParams &p, int32_t clusters, int32_t c)
+{
+    return p.cluster > 1 ? c : clusters - 1 - c;
+}
+
 // A cluster's items in order: its range of the split tiles' units (a piece of each tile that it
 // touches), then every clusters-th whole tile.  Only a range's first piece may start inside a tile (it
 // then leaves a partial); a piece that starts at k-block 0 and does not reach the tile's end is the
@@ -77,8 +86,9 @@ struct FfnWork {
         C = clusters;
         T = p.num_tiles;
         dp = p.sk_tiles + cluster;
-        u = ffn_range_begin(p.sk_units, clusters, cluster);
-        u_end = ffn_range_begin(p.sk_units, clusters, cluster + 1);
+        const int32_t range = ffn_range_at(p, clusters, cluster);
+        u = ffn_range_begin(p.sk_units, clusters, range);
+        u_end = ffn_range_begin(p.sk_units, clusters, range + 1);
     }
 
     __host__ __device__ __forceinline__ bool next(FfnItem &w)
@@ -827,6 +837,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
         FfnStager st = {staging0 + (uint32_t)ew * kFfnStagingBytes, lane, 0u};
         const uint32_t acce_target = kPair ? mapa_shared(acce_bar, 0u) : acce_bar;
         const int32_t cta = cluster_id * CG + (int32_t)rank;
+        // the CTA of this rank that a range is of, where tiles meet through global memory
+        auto cta_of = [&](int32_t range) { return (num_clusters - 1 - range) * CG + (int32_t)rank; };
         int acc = 0;
         uint32_t acc_ph = 0;
         const bool dense = p0.sk_units >= num_clusters;  // every range holds a unit
@@ -863,9 +875,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             const int32_t yc = tc.col * width;
             const bool contributor = kN == 1 && w.kb0 > 0;
             const bool owner = kN == 1 && w.kb0 == 0 && w.kb1 < KB;
-            // the clusters whose ranges start inside this tile, owner only; a range
-            // may be empty (fewer units than clusters), and then leaves nothing
-            int32_t last = cluster_id;
+            // the ranges that start inside this tile, up to the last, owner only; a range may be empty
+            // (fewer units than clusters), and then leaves nothing
+            const int32_t range = num_clusters - 1 - cluster_id;
+            int32_t last = range;
             bool parts = owner;
             auto collect = [&]() {
                 if (owner && shared_tile) {
@@ -876,11 +889,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                     parts = __shfl_sync(0xFFFFFFFFu, got, 0) != 0u;
                 } else if (owner) {
                     last = ffn_range_of(p.sk_units, num_clusters, (int64_t)(w.tile + 1) * KB - 1);
-                    for (int32_t j2 = cluster_id + 1; parts && j2 <= last; ++j2)
+                    for (int32_t j2 = range + 1; parts && j2 <= last; ++j2)
                         if (dense || ffn_range_holds(p.sk_units, num_clusters, j2))
                             // a give-up stores the tile unsummed, and the status says so
-                            parts = warp_wait_flag(ctl, p.flags + (j2 * CG + (int32_t)rank) * kFfnEpiWarps + ew, 1u,
-                                                   lane);
+                            parts = warp_wait_flag(ctl, p.flags + cta_of(j2) * kFfnEpiWarps + ew, 1u, lane);
                     __syncwarp();  // lane 0's acquires come before the lanes' loads
                 }
             };
@@ -926,11 +938,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                                     v[e] = __float_as_uint(__uint_as_float(v[e]) + __uint_as_float(x[e]));
                     }
                 } else if (parts) {
-                    for (int32_t j2 = cluster_id + 1; j2 <= last; ++j2) {
+                    for (int32_t j2 = range + 1; j2 <= last; ++j2) {
                         if (!dense && !ffn_range_holds(p.sk_units, num_clusters, j2))
                             continue;
                         const float4 *const part = reinterpret_cast<const float4 *>(
-                            ffn_partial(p.partials, j2 * CG + (int32_t)rank, ew, slot, lane));
+                            ffn_partial(p.partials, cta_of(j2), ew, slot, lane));
                         float4 f[8];
 #pragma unroll
                         for (int j = 0; j < 8; ++j)
