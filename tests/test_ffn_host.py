@@ -98,6 +98,7 @@ def linear_args(**over):
     (dict(residual=ffn.Matrix(0x30002, 16)), ffn.ERR_INVALID_ARG),  # over part of the residual
     (dict(z=ffn.Matrix(0x30010, 16)), ffn.ERR_INVALID_ARG),       # results over each other
     (dict(bias=0x30010), ffn.ERR_INVALID_ARG),
+    (dict(M=1 << 20, x=ffn.Matrix(0x10000, 1 << 36)), ffn.ERR_INVALID_ARG),  # sizes that overflow
 ])
 def test_linear_refuses(lib, over, want):
     n = ctypes.c_int64(-1)
@@ -188,6 +189,9 @@ def gated_backward_args(**over):
     (dict(dx=ffn.Matrix(0x10000, 8)), ffn.ERR_INVALID_ARG),
     (dict(dw_down=ffn.Matrix(0x30000, 160)), ffn.ERR_INVALID_ARG),
     (dict(activation=7), ffn.ERR_INVALID_ARG),
+    (dict(M=1 << 30, F=1 << 30, g=ffn.Matrix(0x30000, 1 << 30), u=ffn.Matrix(0x30000, 1 << 30)), ffn.ERR_INVALID_ARG),
+    (dict(M=1 << 30, F=1 << 30, g=ffn.Matrix(None, 0), u=ffn.Matrix(None, 0),
+          qg=ffn.Quantized(0xc0000, 1 << 30, 0xd0000), qu=ffn.Quantized(0xe0000, 1 << 30, 0xf0000)), ffn.ERR_INVALID_ARG),
 ])
 def test_gated_backward_refuses(lib, over, want):
     n = ctypes.c_int64(-1)

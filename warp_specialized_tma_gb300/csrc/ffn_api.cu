@@ -22,6 +22,7 @@ namespace {
 constexpr int64_t kMaxDim = 0x7FFFFFFFLL - 1023;  // a tile past the last row still has a 32-bit index
 constexpr size_t kWorkAlign = 256;    // of the parts of a workspace
 constexpr int64_t kMaxPitch = int64_t(1) << 37;
+constexpr int64_t kMaxElements = int64_t(1) << 50;  // of a matrix, pitch and all: a call's sizes and offsets fit 64 bits
 constexpr int kNumOptions = 11;
 constexpr int kPlans = 64;              // plans a thread remembers
 constexpr int kMaxCtas = 1024;          // bounds the workspace of split tiles
@@ -399,8 +400,7 @@ int make_plan(const Device &d, const Product &x, Plan &pl)
     pl.stages = ring_stages(d, pl.stage_bytes);
     pl.smem = ffn_smem_bytes(pl.stage_bytes, pl.stages);
     pl.fn = kernel_fn(x.epilogue, pl.cta_group, pl.transposed);
-    // Rank 0 of a cluster waits for the others, so all clusters must be resident:
-    // the largest size that the device can place so often.
+    // All clusters at once: the largest size that the device can place so often.
     if (best.cluster > 1) {
         while (best.cluster > 1 && resident_clusters(d, pl.fn, pl.smem, best.cluster) < pl.tiles)
             --best.cluster;
@@ -915,14 +915,15 @@ bool bad_matrix(const ffn_matrix &m, int64_t rows, int64_t cols, int esize = 2)
 {
     if (rows == 0 || cols == 0)
         return false;
-    return !m.data || !aligned(m.data, (uintptr_t)esize) || (rows > 1 && (m.ld < cols || m.ld > kMaxPitch));
+    return !m.data || !aligned(m.data, (uintptr_t)esize) ||
+           (rows > 1 && (m.ld < cols || m.ld > kMaxPitch || rows > kMaxElements / m.ld));
 }
 
 int check_quantized(const ffn_quantized &q, int64_t rows, int64_t cols, int64_t step)
 {
     if (rows == 0 || cols == 0)
         return FFN_OK;
-    if (!q.codes || !q.scales || q.ld < cols || q.ld > kMaxPitch)
+    if (!q.codes || !q.scales || q.ld < cols || q.ld > kMaxPitch || rows > kMaxElements / q.ld)
         return FFN_ERR_INVALID_ARG;
     return aligned(q.codes, 16) && q.ld % step == 0 && aligned(q.scales, 4) ? FFN_OK : FFN_ERR_ALIGNMENT;
 }
@@ -1202,8 +1203,6 @@ int body_gated_backward(Call &c, const ffn_gated_backward_args &a)
     for (ffn_matrix &m : t) {
         m.ld = padded(a.F);
         m.data = c.take((size_t)(a.M * m.ld) * 2);
-        if (c.measuring())
-            m.data = nullptr;
     }
     int rc;
     {
