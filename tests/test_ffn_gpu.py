@@ -223,6 +223,19 @@ def test_results_over_what_is_read_are_refused():
         ffn.linear(x, w.cpu())
 
 
+@pytest.mark.parametrize("cta_group", (1, 2))
+@pytest.mark.parametrize("width", range(32, 257, 32))
+def test_every_chunk_of_many_tiles_is_stored(width, cta_group):
+    """Short sums, so that a tile's chunks follow each other at once, an odd number of them a warp or an even one."""
+    x, w, want = problem(1400, 5896, 144, 51)
+    shifted = torch.empty(1400, 5897, dtype=bf, device="cuda")[:, 1:]
+    with ffn.options(cta_group=cta_group, transposed=1, width=width, stream=2):
+        for out in (None, shifted):
+            for _ in range(3):
+                assert ffn.linear(x, w, out=out).cpu().equal(want)
+        assert all(t.cpu().equal(want) for t in ffn.linear(x, w, save=True))
+
+
 # ------------------------------------------------------------------ linear_backward
 @gradients
 @pytest.mark.parametrize("M,N,K", [(128, 128, 128), (1, 1, 1), (300, 257, 520), (16, 600, 1000), (700, 72, 33), (3, 520, 8)])

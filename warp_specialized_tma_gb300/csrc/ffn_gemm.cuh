@@ -346,7 +346,8 @@ __device__ __forceinline__ void ffn_store_bf16(const uint32_t (&w)[16], FfnStage
     ffn_store_piece(at, st.lane, map, out, col, row, false, p.D_rows, p.D_cols);
 }
 
-// Stores two chunks of 32 rows x 32 columns, 64 columns apart, with one fence and one wait.
+// Stores two chunks of 32 rows x 32 columns, 64 columns apart, with one fence and one wait.  A group for
+// each buffer, as acquire() counts them: the first is free before the second.
 __device__ __forceinline__ void ffn_store_two(const uint32_t (&w)[2][16], FfnStager &st, const CUtensorMap *map,
                                               const FfnOut &out, int32_t row, int32_t col, const FfnParams &p)
 {
@@ -364,15 +365,19 @@ __device__ __forceinline__ void ffn_store_two(const uint32_t (&w)[2][16], FfnSta
         __syncwarp();
         if (st.lane == 0) {
             tma_store_2d(map, st.base, col, row);
+            bulk_commit_group();
             if (col + 64 < p.D_cols)
                 tma_store_2d(map, st.base + kFfnPieceBytes, col + 64, row);
             bulk_commit_group();
         }
-        return;
+    } else {
+        ffn_store_piece(st.base, st.lane, map, out, col, row, false, p.D_rows, p.D_cols);
+        if (col + 64 < p.D_cols)
+            ffn_store_piece(st.base + kFfnPieceBytes, st.lane, map, out, col + 64, row, false, p.D_rows, p.D_cols);
+        else if (st.lane == 0)
+            bulk_commit_group();
     }
-    ffn_store_piece(st.base, st.lane, map, out, col, row, false, p.D_rows, p.D_cols);
-    if (col + 64 < p.D_cols)
-        ffn_store_piece(st.base + kFfnPieceBytes, st.lane, map, out, col + 64, row, false, p.D_rows, p.D_cols);
+    st.slot = 0u;
 }
 
 template <bool kT>
