@@ -1068,7 +1068,29 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             if constexpr (kEpi == kFfnPlain && !kT) {
                 // whole tiles of bf16, most of the work: two chunks at a time, whose loads, stores and
                 // fences overlap (the gradient of a 4096 x 4096 weight over 64 tokens 16.2 to 14 us)
-                if (!p.out_fp32 && !contributor && !owner)
+                const bool two = !p.out_fp32 && !contributor && !owner;
+                if (two && KB && !p.bias && p.act == kActNone && !p.aux[0].p && !p.save)
+                    // the sums as they are, as in every gradient: apart, in little code
+                    for (; c0 + 2 < nchunks; c0 += 4) {
+                        uint32_t v[2][32], pk[2][16];
+                        load_chunk(0, c0, v[0]);
+                        load_chunk(0, c0 + 2, v[1]);
+                        tmem_load_wait();
+                        reg_fence(v[0]);
+                        reg_fence(v[1]);
+                        if (c0 + 4 >= nchunks)
+                            hand_back();
+                        const int32_t col = d_col0 + c0 * 32;
+                        if (yr >= p.D_rows || col >= p.D_cols)
+                            continue;
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+#pragma unroll
+                            for (int i = 0; i < 16; ++i)
+                                pk[h][i] = pack_bf16x2(v[h][2 * i], v[h][2 * i + 1]);
+                        ffn_store_two(pk, st, other ? &maps.D[1] : &maps.D[0], other ? p.D[1] : p.D[0], yr, col, p);
+                    }
+                else if (two)
                     for (; c0 + 2 < nchunks; c0 += 4) {
                         uint32_t v[2][32];
                         load_chunk(0, c0, v[0]);
