@@ -1068,8 +1068,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             if constexpr (kEpi == kFfnPlain && !kT) {
                 // whole tiles of bf16, most of the work: two chunks at a time, whose loads, stores and
                 // fences overlap (the gradient of a 4096 x 4096 weight over 64 tokens 16.2 to 14 us)
-                const bool two = !p.out_fp32 && !contributor && !owner;
-                if (two && KB && !p.bias && p.act == kActNone && !p.aux[0].p && !p.save)
+                const bool two = KB && !p.out_fp32 && !contributor && !owner;
+                if (two && !p.bias && p.act == kActNone && !p.aux[0].p && !p.save)
                     // the sums as they are, as in every gradient: apart, in little code
                     for (; c0 + 2 < nchunks; c0 += 4) {
                         uint32_t v[2][32], pk[2][16];
@@ -1108,7 +1108,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                         for (int h = 0; h < 2; ++h) {
 #pragma unroll
                             for (int i = 0; i < 32; ++i)
-                                f[h][i] = KB ? __uint_as_float(v[h][i]) : 0.0f;
+                                f[h][i] = __uint_as_float(v[h][i]);
                             ffn_add_bias<false>(f[h], col + 64 * h, p);
                         }
                         uint32_t pk[2][16];
