@@ -78,6 +78,7 @@ static int check_order(int32_t rows, int32_t cols, int32_t band)
     p.num_row_tiles = rows;
     p.num_col_tiles = cols;
     p.raster_group = band < rows ? band : rows;
+    p.band_tiles = ffn_band_tiles(p.raster_group, cols);
     std::set<std::pair<int, int>> seen;
     for (int32_t t = 0; t < rows * cols; ++t) {
         const FfnTile c = ffn_tile_coord(t, p);
@@ -119,6 +120,8 @@ int main()
                     std::printf("order: %d x %d in bands of %d\n", rows, cols, band);
                     return 1;
                 }
+    if (ffn_band_tiles(1024, 1 << 27) != 0x7FFFFFFFu || ffn_band_tiles(8, 31) != 248u)
+        return 1;
     std::printf("%d splits\n", n);
     return 0;
 }

@@ -794,6 +794,7 @@ int describe(const Product &x, const Plan &pl, FfnMaps &maps, FfnParams &p)
     p.stage_bytes = (int32_t)pl.stage_bytes;
     p.stages = pl.stages;
     p.raster_group = band_of(pl, x.K);
+    p.band_tiles = ffn_band_tiles(p.raster_group, pl.col_tiles);
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;

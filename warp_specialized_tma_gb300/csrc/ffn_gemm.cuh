@@ -155,13 +155,12 @@ struct FfnTile {
 // bands right to left, so that tiles running at the same time share operands in L2.
 __host__ __device__ __forceinline__ FfnTile ffn_tile_coord(int32_t t, const FfnParams &p)
 {
-    const int64_t span = (int64_t)p.raster_group * p.num_col_tiles;
-    const int32_t band = (int32_t)(t / span);
-    const int32_t first = band * p.raster_group;
+    const uint32_t band = (uint32_t)t / p.band_tiles;
+    const int32_t first = (int32_t)band * p.raster_group;
     const int32_t rows = p.num_row_tiles - first < p.raster_group ? p.num_row_tiles - first : p.raster_group;
-    const int32_t r = (int32_t)(t - band * span);
-    const int32_t col = r / rows;
-    return {first + r % rows, (band & 1) ? p.num_col_tiles - 1 - col : col};
+    const uint32_t r = (uint32_t)t - band * p.band_tiles;
+    const int32_t col = (int32_t)(r / (uint32_t)rows);
+    return {first + (int32_t)r - col * rows, (band & 1u) ? p.num_col_tiles - 1 - col : col};
 }
 
 // ---------------------------------------------------------------- PTX of this kernel

@@ -59,6 +59,7 @@ struct FfnParams {
     int32_t stage_bytes;       // of the ring, the same for all products of a launch
     int32_t stages;
     int32_t raster_group;
+    uint32_t band_tiles;       // ffn_band_tiles()
     int32_t sk_tiles;          // tiles [0, sk_tiles) are split along k among all clusters
     int64_t sk_units;          // sk_tiles * num_k_blocks
     int32_t cluster;           // > 1 (one SM per tile only): each tile is split among the CTAs of a cluster
@@ -92,6 +93,13 @@ struct FfnArgs {
     FfnParams p[kN];
     int32_t first[kN + 1];
 };
+
+// Tiles of a band of row tiles, as many as 32 bits hold: there are fewer in all.
+inline uint32_t ffn_band_tiles(int64_t raster_group, int64_t col_tiles)
+{
+    const int64_t n = raster_group * col_tiles;
+    return n < 0x7FFFFFFF ? (uint32_t)n : 0x7FFFFFFFu;
+}
 
 inline int ffn_chunk_rows(bool mn, int rows) { return mn ? (rows + 63) / 64 * 64 : rows; }
 
