@@ -68,8 +68,8 @@ typedef enum ffn_option {
     FFN_OPT_FAULT_SKIP_LOAD = 6, /* test hook: each producer leaves out this load (-1 = none), so that a bounded
                                     wait runs out and ffn_device_status reports DEVICE_TIMEOUT */
     FFN_OPT_RASTER_GROUP = 7, /* tiles are walked in bands of this many row tiles */
-    FFN_OPT_STREAM = 9,       /* forward products of few tokens on the kernel that streams the weights: 1 = up to
-                                 32 tokens, 2 = never */
+    FFN_OPT_STREAM = 9,       /* products of few tokens on the kernels that stream the weights: 1 = up to 32
+                                 tokens, 16 in a gradient, 2 = never */
     FFN_OPT_TOGETHER = 10,    /* a gradient's products that need none of each other in one launch: 1 = always, 2 =
                                  never */
     FFN_OPT_REPACK = 8        /* operands whose rows do not start at multiples of 128 bytes: 1 = copied first, 2 =
@@ -77,7 +77,7 @@ typedef enum ffn_option {
 } ffn_option;
 
 typedef struct ffn_plan_info_s {
-    int64_t tiles;        /* 0: the kernel that streams the weights, for few tokens */
+    int64_t tiles;        /* 0: a kernel that streams the weights, for few tokens */
     int64_t k_blocks;     /* of 64 */
     int32_t grid_ctas;
     int32_t cta_group;

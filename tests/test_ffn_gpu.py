@@ -56,13 +56,14 @@ VARIANTS = {
 variants = pytest.mark.parametrize("variant", VARIANTS.values(), ids=VARIANTS.keys())
 
 # a gradient's products one after the other, in each of these, or in one launch
-GRADIENTS = {k: dict(v, together=2) for k, v in VARIANTS.items()}
+GRADIENTS = {k: dict(v, together=2, stream=2) for k, v in VARIANTS.items()}
 GRADIENTS |= {
-    "together": dict(together=1),
-    "together-one": dict(together=1, cta_group=1),
-    "together-pair": dict(together=1, cta_group=2),
-    "together-narrow": dict(together=1, cta_group=1, width=32),
-    "together-wide": dict(together=1, cta_group=2, width=256),
+    "together": dict(together=1, stream=2),
+    "together-one": dict(together=1, cta_group=1, stream=2),
+    "together-pair": dict(together=1, cta_group=2, stream=2),
+    "together-narrow": dict(together=1, cta_group=1, width=32, stream=2),
+    "together-wide": dict(together=1, cta_group=2, width=256, stream=2),
+    "stream": dict(stream=1),
     "auto": dict(),
 }
 gradients = pytest.mark.parametrize("variant", GRADIENTS.values(), ids=GRADIENTS.keys())
@@ -279,6 +280,45 @@ def test_bias_gradients(M, N):
     dx, _, db = ffn.linear_backward(*gpu(dy, x, w, z), activation="relu", bias=True)
     dz = dy.double() * (z.double() > 0)
     assert db.cpu().double().equal(dz.sum(0)) and dx.cpu().equal((dz @ w.double()).to(bf))
+
+
+@pytest.mark.parametrize("N,K", [(1, 8), (15, 1), (16, 520), (33, 584), (500, 4096), (1003, 7), (40, 20000), (6000, 72), (2040, 8200)])
+@pytest.mark.parametrize("M", [1, 2, 8, 9, 16])
+def test_gradients_of_few_tokens(M, N, K):
+    x, w, dy = randn(M, K, seed=1), ints(N, K, seed=2), ints(M, N, seed=3)
+    pitch = -(-K // 8) * 8 + 8
+    for rows in (lambda t: t.cuda(), lambda t: strided(t, pitch, 8)):
+        held = strided(dy, -(-N // 8) * 8 + 8, 8)
+        with ffn.options(stream=1):
+            dx, dw, _ = ffn.linear_backward(held, x.cuda(), rows(w))
+            again = ffn.linear_backward(held, x.cuda(), rows(w))[0]
+        assert dx.cpu().equal((dy.double() @ w.double()).to(bf)) and dx.equal(again)
+        want, mag = ref.product(dy.T, x.T)
+        assert ref.close(dw, want, ref.sum_error(M) * mag)
+    dyr, wr = randn(M, N, seed=4), randn(N, K, seed=5)
+    with ffn.options(stream=1):
+        dx = ffn.linear_backward(strided(dyr, -(-N // 8) * 8, 8), x.cuda(), strided(wr, pitch, 0))[0]
+    want, mag = ref.product(dyr, wr.T)
+    assert ref.close(dx, want, ref.sum_error(N) * mag)
+
+
+@pytest.mark.parametrize("activation", [None, "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("save", ["bf16", "e4m3"])
+@pytest.mark.parametrize("M,C,F,N", [(1, 8, 8, 8), (3, 40, 1032, 24), (16, 520, 136, 1000), (9, 1000, 5000, 33)])
+def test_gated_gradients_of_few_tokens(M, C, F, N, save, activation):
+    x, wg, wu = randn(M, C, seed=1), randn(F, C, seed=2, scale=C**-0.5), randn(F, C, seed=3, scale=C**-0.5)
+    wd, dy = randn(N, F, seed=4, scale=F**-0.5), randn(M, N, seed=5)
+    _, saved = ffn.gated(*gpu(x, wg, wu), activation=activation, save=save)
+    g, u = saved if save == "bf16" else (torch.from_numpy(fp8ref.values(saved[i].cpu(), saved[i + 1].cpu())) for i in (0, 2))
+    rows = [strided(t, -(-t.shape[1] // 8) * 8, 0) for t in (dy, x)]
+    weights = [strided(t, -(-t.shape[1] // 8) * 8, 8) for t in (wg, wu, wd)]
+    with ffn.options(stream=1):
+        got = ffn.gated_backward(*rows, saved, *weights, activation=activation)
+        again = ffn.gated_backward(*rows, saved, *weights, activation=activation)
+    want = ref.gated_backward(dy, x, g.cpu(), u.cpu(), wg, wu, wd, activation)
+    for a, b, v in zip(got, again, want):
+        # as in test_gated_backward_variants
+        assert ref.close_rms(a, v, extra=2.0**-10) and a.equal(b)
 
 
 # ------------------------------------------------------------------ gated

@@ -684,7 +684,61 @@ bool streams(const Call &c, const Product &x)
     return x.M <= 16 ? !dual || x.N * x.K <= 1 << 25 : x.N * x.K <= 1 << 24;
 }
 
+// Whether a product goes to the kernel for few tokens and weights that are contiguous along the result's
+// columns (ffn_stream_back.cu, with both sides' times).  A gated gradient's do up to 8 tokens, and, where the
+// weights are of a middling size, up to 16; the whole gradient takes (us, so and without)
+//   1024 x 4096     8 tokens 25.4, 38.7;   16 tokens 31.3, 39.7
+//   2048 x 8192     8 tokens 52.9, 75.5;   16 tokens 61.8, 75.0
+//   4096 x 16384    8 tokens 175, 184;     16 tokens 182, 168
+//   512 x 1024      8 tokens 15.1, 15.6;   16 tokens 19.9, 15.7
+// A single dx does where its sum is long; shorter ones do better beside dW in one launch:
+//   4096 x 4096     8 tokens 23.6, 27.2;   16 tokens 27.1, 26.6
+//   12288 x 512     8 tokens 17.0, 20.9;   2048 x 2048  8 tokens 12.5, 9.3
+//   8192 x 8192     8 tokens 58.5, 59.0;   16 tokens 65.2, 59.4
+bool streams_back(const Call &c, const Product &x)
+{
+    if (options.v[FFN_OPT_STREAM] == 2 || x.M > kFfnStreamBackTokens || x.K < 1 || x.a_mn || !x.b_mn || x.fp32 ||
+        x.N > ffn_stream_back_columns(c.dev.sms) ||
+        !(x.epilogue == kFfnGrad || (x.epilogue == kFfnPlain && (x.form == kOne || x.form == kSum))))
+        return false;
+    for (int i = 0; i < (x.form == kSum ? 2 : 1); ++i)
+        if (!aligned(x.A[i].p, 8) || (x.M > 1 && x.A[i].ld % 4 != 0) || !aligned(x.B[i].p, 16) ||
+            (x.K > 1 && x.B[i].ld % 8 != 0))
+            return false;
+    if (options.v[FFN_OPT_STREAM] == 1)
+        return true;
+    if (x.epilogue == kFfnGrad || x.form == kSum)
+        return x.M <= 8 || (x.N * x.K > 1 << 21 && x.N * x.K <= 1 << 25);
+    return x.M <= 8 && x.K >= 4096;
+}
+
 void remember(const Call &c, const Plan &pl, int products);
+
+int run_stream_back(Call &c, const Product &x)
+{
+    if (c.measuring())
+        return FFN_OK;
+    FfnStreamBackParams p = {};
+    p.products = x.form == kSum ? 2 : 1;
+    for (int i = 0; i < p.products; ++i) {
+        p.d[i] = static_cast<const uint16_t *>(x.A[i].p);
+        p.ldd[i] = x.A[i].ld;
+        p.w[i] = static_cast<const uint16_t *>(x.B[i].p);
+        p.ldw[i] = x.B[i].ld;
+    }
+    p.M = (int32_t)x.M, p.N = (int32_t)x.K, p.C = (int32_t)x.N;
+    p.act = x.p.act;
+    for (int i = 0; i < 2; ++i)
+        p.aux[i] = x.p.aux[i];
+    for (int i = 0; i < 3; ++i) {
+        p.D[i].p = x.D[i].data;
+        p.D[i].ld = x.D[i].ld;
+    }
+    Plan none;
+    std::memset(&none, 0, sizeof(none));
+    remember(c, none, 1);
+    return from_cuda((cudaError_t)launch_ffn_stream_back(p, c.dev.index, c.dev.sms, c.stream));
+}
 
 int run_stream(Call &c, const Product &x)
 {
@@ -845,6 +899,8 @@ int run_product(Call &c, Product &x)
         return FFN_OK;
     if (streams(c, x))
         return run_stream(c, x);
+    if (streams_back(c, x))
+        return run_stream_back(c, x);
     Plan pl;
     int rc = find_plan(c.dev, x, &pl);
     if (rc != FFN_OK)
@@ -867,14 +923,21 @@ int run_product(Call &c, Product &x)
     return launch(c, pl, &args);
 }
 
-// Runs plain products, none of which needs another's result, in one launch or one after the other.
+// Runs plain products, none of which needs another's result: those that stream their weights, then the
+// others in one launch or one after the other.
 int run_products(Call &c, Product *all, int count)
 {
     Product *xs[kFfnMaxProducts];
     int n = 0, rc;
     for (int i = 0; i < count; ++i)
-        if (all[i].M > 0 && all[i].N > 0)
+        if (all[i].M > 0 && all[i].N > 0) {
+            if (streams_back(c, all[i])) {
+                if ((rc = run_stream_back(c, all[i])) != FFN_OK)
+                    return rc;
+                continue;
+            }
             xs[n++] = &all[i];
+        }
     const Together *group = nullptr;
     if (n > 1 && options.v[FFN_OPT_TOGETHER] != 2) {
         // those with the longest tiles first, so that the last tiles are short ones

@@ -140,6 +140,25 @@ struct FfnStreamParams {
 int64_t ffn_stream_rows(int num_sms);  // N at most
 int launch_ffn_stream(FfnStreamParams &p, int num_sms, cudaStream_t stream);  // a cudaError_t value
 
+constexpr int kFfnStreamBackTokens = 16;  // at most
+
+// D0 = d[0] w[0] (+ d[1] w[1]); with aux, the gated gradient's results (kFfnGrad) of that sum.
+struct FfnStreamBackParams {
+    const uint16_t *d[2];  // M x N, rows 8-byte aligned
+    int64_t ldd[2];
+    const uint16_t *w[2];  // N x C, rows 16-byte aligned
+    int64_t ldw[2];
+    int32_t products;
+    int32_t M, N, C;
+    int32_t ranks, share, groups;  // the launch's: CTAs of a cluster, eights of columns of one, their groups
+    int32_t act;
+    FfnAux aux[2];         // g and u
+    FfnOut D[3];
+};
+
+int64_t ffn_stream_back_columns(int num_sms);  // C at most
+int launch_ffn_stream_back(FfnStreamBackParams &p, int device, int num_sms, cudaStream_t stream);
+
 // ----------------------------------------------------------------- rows
 // Copies of R rows of C bf16 to rows that are 16-byte aligned (ldd a multiple of 8), a cudaError_t value.
 struct FfnPackJob {
