@@ -167,7 +167,7 @@ struct Plan {
     PlanKey key;
     uint64_t used;
     bool transposed;
-    int cta_group, width, c_rows, stages, grid, cluster;
+    int cta_group, width, c_rows, r_rows, stages, grid, cluster;
     int64_t row_tiles, row_split, col_tiles, tiles, k_blocks, k_split, sk_tiles;
     size_t smem, stage_bytes;
     const void *fn;
@@ -201,7 +201,7 @@ struct Tiling {
     bool transposed;
     int cta_group, width;
     // found by tiling_cost()
-    int c_rows = 0;
+    int c_rows = 0, r_rows = 0;
     size_t stage_bytes = 0;
     int64_t clusters = 0;  // SM pairs, or CTAs, of the grid
     int64_t sk_tiles = 0;
@@ -237,7 +237,7 @@ int ring_stages(const Device &d, size_t stage_bytes)
 // Estimated time of a tiling, in clocks of an SM (1.9 GHz), without what every launch costs:
 // the tiles of the longest chain, each its stages (k-blocks: the longest of the MMAs, 4096
 // multiply-adds a clock and SM, the loads, 62 bytes a clock and SM and 9231 over all SMs, and a stage's
-// handling, 394 clocks) or its epilogue; or the operands' time in HBM and their repeated loads', if longer;
+// handling, 394 clocks, or 345 where half of its rows are loaded) or its epilogue; or the operands' time in HBM and their repeated loads', if longer;
 // then the last epilogue and the exchange between a split tile's pieces.  The constants are fitted to 4000
 // measured tilings of 51 products in all forms: the tiling of least estimate took at most 11 % longer
 // than the best of them, 0.9 % in the mean.  Fills in how the tiles are shared out.
@@ -249,16 +249,22 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
         t.c_rows = t.cta_group == 2 ? kFfnDualWidth : 2 * kFfnDualWidth;
     else
         t.c_rows = ffn_chunk_rows(s.c_mn, t.width / t.cta_group);
-    t.stage_bytes = (size_t)kFfnRowsPerCta * 128 * (dual && t.transposed ? 2 : 1) + (size_t)t.c_rows * 128;
+    // Up to 64 tokens on the row side: half the stage, and half again as many of them in flight (64 x 8192 x 8192
+    // in tiles of 64 columns 30.6 us, and 27.5 so; with bias and residual 31.6 and 28.5).
+    t.r_rows = !t.transposed && !x.a_mn && t.cta_group == 1 && x.M <= 64 ? 64 : kFfnRowsPerCta;
+    t.stage_bytes = (size_t)t.r_rows * 128 * (dual && t.transposed ? 2 : 1) + (size_t)t.c_rows * 128;
     const int64_t tiles = s.row_tiles * s.col_tiles;
     const int64_t split = x.no_split ? 0 : options.v[FFN_OPT_SPLIT];
     const int64_t most = t.cta_group == 2 ? d.max_pairs : d.sms;
     const double sums = (dual ? 2.0 : 1.0) * t.width;  // columns of sums a row
     const double l2 = (double)t.stage_bytes * (double)(std::min(tiles, most) * t.cta_group) / 9231.0;
-    const double stage = std::max({2.0 * sums, 394.0, (double)t.stage_bytes / 62.5, l2});
+    const double handling = t.r_rows < kFfnRowsPerCta ? 345.0 : 394.0;
+    const double stage = std::max({2.0 * sums, handling, (double)t.stage_bytes / 62.5, l2});
     const double once = (double)(x.M + x.N * (dual ? 2 : 1)) * (double)x.K * 2.0;
     const double loads = (double)tiles * (double)KB * (double)t.stage_bytes * t.cta_group;
-    const double hbm = once / 4661.0 + std::max(0.0, loads - once) / 40743.0;
+    // (the measured tilings' operands were in L2 in part; 134 MB of them take HBM's own rate)
+    const double read = std::min(once / 3530.0, once / 4661.0 + std::max(0.0, once - 6.4e7) / 7600.0);
+    const double hbm = read + std::max(0.0, loads - once) / 40743.0;
     // What an epilogue does with a chunk, in stores of one: a transposed result's rows are read an element
     // at a time (the gradient of 800 x 5256 x 3872 from 8 bits takes 173 us that way, and 75 not transposed).
     const bool grad = x.epilogue == kFfnGrad;
@@ -351,6 +357,7 @@ int plan_tiles(const Product &x, const Tiling &t, Plan &pl)
     pl.cta_group = t.cta_group;
     pl.width = t.width;
     pl.c_rows = t.c_rows;
+    pl.r_rows = t.r_rows;
     pl.stage_bytes = t.stage_bytes;
     pl.row_tiles = s.row_tiles;
     pl.row_split = x.form == kStack ? s.row_tiles / 2 : s.row_tiles;
@@ -826,7 +833,7 @@ int describe(const Product &x, const Plan &pl, FfnMaps &maps, FfnParams &p)
     };
     if (pl.k_blocks) {
         for (int i = 0; i < 2; ++i)
-            if ((i < (two_r ? 2 : 1) && !encode(&maps.R[i], R[i], p.r_mn, rows, kFfnRowsPerCta)) ||
+            if ((i < (two_r ? 2 : 1) && !encode(&maps.R[i], R[i], p.r_mn, rows, pl.r_rows)) ||
                 (i < (two_c ? 2 : 1) && !encode(&maps.C[i], C[i], p.c_mn, cols, c_box)))
                 return FFN_ERR_TENSORMAP;
     }
@@ -845,6 +852,7 @@ int describe(const Product &x, const Plan &pl, FfnMaps &maps, FfnParams &p)
     p.row_split = (int32_t)pl.row_split;
     p.width = pl.width;
     p.c_rows = pl.c_rows;
+    p.r_rows = pl.r_rows;
     p.stage_bytes = (int32_t)pl.stage_bytes;
     p.stages = pl.stages;
     p.raster_group = band_of(pl, x.K);

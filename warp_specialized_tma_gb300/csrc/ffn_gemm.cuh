@@ -583,10 +583,12 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
     constexpr bool kDual = kEpi == kFfnGated;
     constexpr int kAccs = kDual ? 2 : 1;  // accumulators of an element
     constexpr uint32_t kTileRBytes = (uint32_t)kFfnRowsPerCta * 128u;
-    constexpr uint32_t kRBytes = kTileRBytes * (kDual && kT ? 2u : 1u);
     static_assert(kN == 1 || (kEpi == kFfnPlain && !kT), "several products in one launch are plain ones");
     const FfnParams &p0 = args.p[0];  // what all products share
     const uint32_t stage_bytes = (uint32_t)p0.stage_bytes;  // a multiple of 1024
+    // Of 64 rows only these are loaded: the MMA takes what lies behind them for the other 64, whose sums
+    // nothing reads.
+    auto r_bytes_of = [](const FfnParams &p) { return (uint32_t)p.r_rows * 128u * (kDual && kT ? 2u : 1u); };
 
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
@@ -689,7 +691,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                 const FfnParams &p = args.p[w.product];
                 const FfnMaps &maps = args.maps[w.product];
                 const int32_t width = p.width;
-                const uint32_t loaded = (kRBytes + (uint32_t)p.c_rows * 128u) * CG;  // of a stage
+                const uint32_t r_bytes = r_bytes_of(p), loaded = (r_bytes + (uint32_t)p.c_rows * 128u) * CG;  // of a stage
                 const FfnTile tc = ffn_tile_coord(w.tile, p);
                 const bool other = tc.row >= p.row_split;  // tiles of the second row operand
                 const int32_t yr =
@@ -725,7 +727,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                                 tma_load_2d_elected<CG>(sa, mr, k, yr, fb, leader);
                             }
                         }
-                        const uint32_t sc = sa + kRBytes;
+                        const uint32_t sc = sa + r_bytes;
                         if constexpr (kDual && !kT) {
                             if constexpr (CG == 2) {
                                 // the pair's MMA takes its first 128 columns from rank 0, the rest from rank 1
@@ -799,8 +801,9 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             while (wi.next(args, w)) {
                 const FfnParams &p = args.p[w.product];
                 const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
+                const uint32_t r_bytes = r_bytes_of(p);
                 const uint64_t cdesc0 =
-                    p.c_mn ? smem_desc_mn_sw128(stage0 + kRBytes) : smem_desc_sw128(stage0 + kRBytes);
+                    p.c_mn ? smem_desc_mn_sw128(stage0 + r_bytes) : smem_desc_sw128(stage0 + r_bytes);
                 const uint64_t rstep = p.r_mn ? 2048u >> 4 : 32u >> 4, cstep = p.c_mn ? 2048u >> 4 : 32u >> 4;
                 const int32_t mma_n = kDual && !kT ? 2 * kFfnDualWidth : p.width;
                 const uint32_t idesc = idesc_bf16_f32(kFfnRowsPerCta * CG, 0) | ((uint32_t)(mma_n >> 3) << 17) |

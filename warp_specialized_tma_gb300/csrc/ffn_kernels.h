@@ -56,6 +56,7 @@ struct FfnParams {
     int32_t r_mn, c_mn;        // operand's rows are contiguous (an operand is contiguous along k otherwise)
     int32_t width;             // of a tile on the column side, per accumulator
     int32_t c_rows;            // rows of the column operand that a CTA loads per stage
+    int32_t r_rows;            // and of the row operand (of each, transposed gated): 128, or 64 where there are no more
     int32_t stage_bytes;       // of the ring, the same for all products of a launch
     int32_t stages;
     int32_t raster_group;
