@@ -32,7 +32,7 @@
 // Measured (us in a burst, from a graph; the operations' or, for few tokens, the bytes' time):
 //   linear 8192^3, silu, bias, residual                565 (572): tensor pipe 91 % active, at the power cap's clock
 //   gated 4096 x 4096 x 16384, g and u kept in bf16    561 (572): the same
-//   linear 64 x 8192 x 8192, bias, residual            31.3 (20.3): HBM; a third are the start and the transposed epilogue
+//   linear 64 x 8192 x 8192, bias, residual            28.5 (20.3): HBM; a launch's start, first loads and last epilogue
 //   dx and dW of 4096^3 in one launch                  144 (143, under the profiler): tensor pipe 83 %, 3.4 waves
 //   dg, du, h of 8192 x 2048 x 8192 from 8 bits        204 (143): the epilogue, 11.7 us a tile beside 8.6 of MMAs
 //   dW of 8192 x 8192 from 64 tokens                   25.4 (20.2): the epilogue's chain; stores at 5.3 TB/s
