@@ -566,6 +566,29 @@ def test_only_the_results_rows_are_written(M, N, K):
         assert scales[i][:-8].equal(qs.view(torch.uint8).flatten()) and bool((scales[i][-8:] == 3).all())
 
 
+@pytest.mark.parametrize("M", (1, 7, 13))
+def test_streamed_gradients_write_their_rows_alone(M):
+    N, K = 264, 520
+    x, w, dy = ints(M, K, seed=1).cuda(), ints(N, K, seed=2).cuda(), ints(M, N, seed=3).cuda()
+    want = (dy.double() @ w.double()).to(bf)
+    for offset, pitch in ((8, K + 72), (7, K + 71)):
+        base = torch.full((M, pitch), 5.0, dtype=bf, device="cuda")
+        dx = base[:, offset:offset + K]
+        with ffn.options(stream=1):
+            c_call("linear_backward", ffn.LinearBackwardArgs(M=M, N=N, K=K, dy=matrix(dy), x=matrix(x), weight=matrix(w),
+                                                             dx=ffn.Matrix(dx.data_ptr(), pitch)))
+        assert ffn.plan_info()["tiles"] == 0
+        assert dx.equal(want) and bool((base[:, :offset] == 5.0).all()) and bool((base[:, offset + K:] == 5.0).all())
+    # what is not finite stays in its token and its column
+    dy[M - 1, 40], w[100, 300] = float("inf"), float("nan")
+    with ffn.options(stream=1):
+        dx = ffn.linear_backward(dy, x, w)[0]
+    clean = torch.ones(M, K, dtype=torch.bool)
+    clean[M - 1], clean[:, 300] = False, False
+    assert dx.cpu()[clean].equal(want.cpu()[clean]) and not dx[:, 300].isfinite().any()
+    assert not dx[M - 1, w[40] != 0].isfinite().any()
+
+
 def test_gated_backward_parts():
     M, C, F, N = 40, 72, 136, 24
     x, wg, wu, wd = ints(M, C, seed=1, top=1), ints(F, C, seed=2, top=1), ints(F, C, seed=3, top=1), ints(N, F, seed=4, top=1)
