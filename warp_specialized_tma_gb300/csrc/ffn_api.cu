@@ -198,8 +198,8 @@ const void *kernel_fn(int epilogue, int cta_group, bool transposed)
 
 // A way to tile a product, and what it costs.
 struct Tiling {
-    bool transposed;
-    int cta_group, width;
+    bool transposed = false;
+    int cta_group = 0, width = 0;
     // found by tiling_cost()
     int c_rows = 0, r_rows = 0;
     size_t stage_bytes = 0;
@@ -307,8 +307,8 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
     const int64_t whole = C ? (tiles - sk) / C : 0;
     // (a gradient's epilogues are what its tiles wait for: 1000 x 3000 x 1000 takes 26 us with its last wave
-    // shared, and 20)
-    if (split && sk && C > sk && !(grad && whole)) {
+    // shared, and 20.  An empty sum has no k-blocks to share: its tiles are walked whole.)
+    if (split && KB && sk && C > sk && !(grad && whole)) {
         // behind whole tiles the exchange is out of sight for as long as one takes: the split tiles come first
         const double meet = 11435.0 + (59.0 + 25.4 * sums) * (double)C / (double)sk;
         const double exchange = whole ? std::max(6396.0, meet - tile) : meet;
@@ -367,15 +367,16 @@ int plan_tiles(const Product &x, const Tiling &t, Plan &pl)
     pl.k_split = x.form == kSum ? pl.k_blocks / 2 : pl.k_blocks;
     pl.sk_tiles = 0;
     pl.cluster = 1;
-    return pl.tiles > kMaxDim || pl.k_blocks > kMaxDim ? FFN_ERR_UNSUPPORTED : FFN_OK;
+    // pieces of an empty sum are none: its tiles would be nobody's
+    return pl.tiles > kMaxDim || pl.k_blocks > kMaxDim || (t.sk_tiles && !pl.k_blocks) ? FFN_ERR_UNSUPPORTED : FFN_OK;
 }
 
-int make_plan(const Device &d, const Product &x, Plan &pl)
+// The tiling of least estimate, and how its tiles are shared out; false if the options allow none.
+bool choose_tiling(const Device &d, const Product &x, Tiling &best, double &best_cost)
 {
     const int64_t *opt = options.v;
     const int64_t KB = k_blocks_of(x);
-    Tiling best = {false, 0, 0};
-    double best_cost = 0.0;
+    best = {false, 0, 0};
     for (int cg = 1; cg <= 2; ++cg)
         for (int tr = 0; tr <= 1; ++tr) {
             if ((opt[FFN_OPT_CTA_GROUP] && cg != opt[FFN_OPT_CTA_GROUP]) ||
@@ -398,7 +399,14 @@ int make_plan(const Device &d, const Product &x, Plan &pl)
                     best = t, best_cost = cost;
             }
         }
-    if (best.cta_group == 0)
+    return best.cta_group != 0;
+}
+
+int make_plan(const Device &d, const Product &x, Plan &pl)
+{
+    Tiling best;
+    double best_cost = 0.0;
+    if (!choose_tiling(d, x, best, best_cost))
         return FFN_ERR_UNSUPPORTED;
     const int rc = plan_tiles(x, best, pl);
     if (rc != FFN_OK)
