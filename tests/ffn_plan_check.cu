@@ -13,9 +13,12 @@
 namespace wstma {
 static const void *const nothing = nullptr;
 const void *ffn_plain_fn(int, bool) { return nothing; }
+const void *ffn_plain_segments_fn(int, bool) { return nothing; }
 const void *ffn_gated_fn(int, bool) { return nothing; }
+const void *ffn_gated_codes_fn(int) { return nothing; }
 const void *ffn_grad_fn(int, bool) { return nothing; }
 const void *ffn_together_fn(int) { return nothing; }
+const void *ffn_together_segments_fn(int) { return nothing; }
 uint32_t *ffn_status_word() { return nullptr; }
 int64_t ffn_stream_rows(int) { return 0; }
 int launch_ffn_stream(FfnStreamParams &, int, cudaStream_t) { return 1; }

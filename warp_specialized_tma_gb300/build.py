@@ -29,8 +29,8 @@ BUILD_DIR = os.path.join(PKG, "_build")
 SOURCES = ["gemm_bf16_api.cu", "gemm_ws_c1.cu", "gemm_ws_c2.cu", "gemm_nows.cu", "gemm_bf16_noalloc.cu",
            "gemm_repack.cu", "gemm_thin.cu"]
 FP8_SOURCES = ["fp8_api.cu", "fp8_gemm.cu", "fp8_quantize.cu", "fp8_norm.cu"]
-FFN_SOURCES = ["ffn_api.cu", "ffn_gemm_plain.cu", "ffn_gemm_gated.cu", "ffn_gemm_grad.cu", "ffn_rows.cu",
-               "ffn_stream.cu", "ffn_stream_back.cu"]
+FFN_SOURCES = ["ffn_api.cu", "ffn_gemm_plain.cu", "ffn_gemm_gated.cu", "ffn_gemm_grad.cu",
+               "ffn_gemm_segments.cu", "ffn_rows.cu", "ffn_stream.cu", "ffn_stream_back.cu"]
 FP8_BIND_SOURCE = "fp8_bind.cpp"
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-std=c++17", "-O3", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

@@ -151,6 +151,8 @@ struct Product {
     bool fp32 = false;     // of D[0], and D[1] of kStack
 };
 
+int64_t k_blocks_of(const Product &x) { return ceil_div(x.K, kFfnBlockK) * (x.form == kSum ? 2 : 1); }
+
 struct Options {
     int64_t v[kNumOptions] = {0, 0, 0, 0, 1, 2000000000, -1, 0, 0, 0, 0};
 };
@@ -189,11 +191,23 @@ thread_local Plan last_plan;
 thread_local bool have_last_plan = false;
 thread_local int32_t last_packed = 0, last_products = 0;
 
-const void *kernel_fn(int epilogue, int cta_group, bool transposed)
+// Sums that go to 8 bits are always added up in segments, those of an fp32 result where there are several.
+bool to_codes(const Product &x) { return x.epilogue == kFfnGated && x.p.save == 2; }
+bool long_sum(const Product &x) { return x.fp32 && k_blocks_of(x) > kFfnSegment; }
+
+const void *kernel_fn(const Product &x, int cta_group, bool transposed)
 {
-    return epilogue == kFfnGated  ? ffn_gated_fn(cta_group, transposed)
-           : epilogue == kFfnGrad ? ffn_grad_fn(cta_group, transposed)
-                                  : ffn_plain_fn(cta_group, transposed);
+    return to_codes(x)                ? ffn_gated_codes_fn(cta_group)
+           : x.epilogue == kFfnGated  ? ffn_gated_fn(cta_group, transposed)
+           : x.epilogue == kFfnGrad   ? ffn_grad_fn(cta_group, transposed)
+           : long_sum(x)              ? ffn_plain_segments_fn(cta_group, transposed)
+                                      : ffn_plain_fn(cta_group, transposed);
+}
+
+// The widest tile of a product on the column side.
+int widest_tile(const Product &x, int cta_group, bool transposed)
+{
+    return x.form == kDual ? kFfnDualWidth : long_sum(x) ? ffn_long_width(cta_group, transposed) : kFfnMaxWidth;
 }
 
 // A way to tile a product, and what it costs.
@@ -307,8 +321,9 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const int64_t C = tiles > most ? most : std::max(tiles, std::min(most, tiles * KB / kMinSplitBlocks));
     const int64_t whole = C ? (tiles - sk) / C : 0;
     // (a gradient's epilogues are what its tiles wait for: 1000 x 3000 x 1000 takes 26 us with its last wave
-    // shared, and 20.  An empty sum has no k-blocks to share: its tiles are walked whole.)
-    if (split && KB && sk && C > sk && !(grad && whole)) {
+    // shared, and 20.  Sums held in registers wait with the next tile's segments: fp32 4096^3 98.7 and 87.0, 6143 x
+    // 5999 x 4104 216 either way.  An empty sum has no k-blocks to share: its tiles are walked whole.)
+    if (split && KB && sk && C > sk && !((grad || long_sum(x)) && whole)) {
         // behind whole tiles the exchange is out of sight for as long as one takes: the split tiles come first
         const double meet = 11435.0 + (59.0 + 25.4 * sums) * (double)C / (double)sk;
         const double exchange = whole ? std::max(6396.0, meet - tile) : meet;
@@ -347,8 +362,6 @@ int resident_clusters(const Device &d, const void *fn, size_t smem, int c)
     return n;
 }
 
-int64_t k_blocks_of(const Product &x) { return ceil_div(x.K, kFfnBlockK) * (x.form == kSum ? 2 : 1); }
-
 // The plan of a tiling, without its ring and grid.
 int plan_tiles(const Product &x, const Tiling &t, Plan &pl)
 {
@@ -385,9 +398,11 @@ bool choose_tiling(const Device &d, const Product &x, Tiling &best, double &best
                  x.form != kStack))
                 continue;
             const bool fixed = x.form == kDual && !tr;
-            const int widest = x.form == kDual ? kFfnDualWidth : kFfnMaxWidth;
+            const int widest = widest_tile(x, cg, tr != 0);
+            // a width that sums in segments do not have stands for the widest that they have
+            const int64_t asked = long_sum(x) ? std::min<int64_t>(opt[FFN_OPT_WIDTH], widest) : opt[FFN_OPT_WIDTH];
             for (int wd = fixed ? kFfnDualWidth : 16; wd <= widest; wd += 16) {
-                if (opt[FFN_OPT_WIDTH] && wd != opt[FFN_OPT_WIDTH] && !fixed)
+                if (asked && wd != asked && !fixed)
                     continue;
                 // chunks of 32 columns: a narrower tile must be the only one
                 const int64_t cols = tr ? x.M : x.N;
@@ -414,7 +429,7 @@ int make_plan(const Device &d, const Product &x, Plan &pl)
     pl.cost = best_cost;
     pl.stages = ring_stages(d, pl.stage_bytes);
     pl.smem = ffn_smem_bytes(pl.stage_bytes, pl.stages);
-    pl.fn = kernel_fn(x.epilogue, pl.cta_group, pl.transposed);
+    pl.fn = kernel_fn(x, pl.cta_group, pl.transposed);
     // All clusters at once: the largest size that the device can place so often.
     if (best.cluster > 1) {
         while (best.cluster > 1 && resident_clusters(d, pl.fn, pl.smem, best.cluster) < pl.tiles)
@@ -438,7 +453,7 @@ PlanKey key_of(const Device &d, const Product &x)
     key.opt[0] = options.v[FFN_OPT_TOGETHER];
     key.device = d.index, key.epilogue = x.epilogue, key.form = x.form;
     key.flags = (x.a_mn ? 1 : 0) | (x.b_mn ? 2 : 0) | (x.no_split ? 4 : 0) | (x.not_transposed ? 8 : 0) |
-                (x.p.aux[0].p ? 16 : 0) | (x.p.aux[0].scales ? 32 : 0) | (x.p.save << 6);
+                (x.p.aux[0].p ? 16 : 0) | (x.p.aux[0].scales ? 32 : 0) | (x.p.save << 6) | (long_sum(x) ? 256 : 0);
     return key;
 }
 
@@ -492,15 +507,19 @@ int find_together(const Device &d, Product **xs, const Plan *alone, int n, const
     }
     const int64_t *opt = options.v;
     double separate = (n - 1) * kLaunchClocks;
-    for (int i = 0; i < n; ++i)
+    bool segments = false;
+    for (int i = 0; i < n; ++i) {
         separate += alone[i].cost;
+        segments = segments || long_sum(*xs[i]);
+    }
     Tiling best[kFfnMaxProducts];
     double best_cost = 0.0;
     int best_cg = 0;
     for (int cg = 1; cg <= 2; ++cg)
-        for (int wd = 32; wd <= kFfnMaxWidth; wd += 32) {
+        for (int wd = 32; wd <= (segments ? ffn_long_width(cg, false) : kFfnMaxWidth); wd += 32) {
             if ((opt[FFN_OPT_CTA_GROUP] && cg != opt[FFN_OPT_CTA_GROUP]) || opt[FFN_OPT_TRANSPOSED] == 2 ||
-                (opt[FFN_OPT_WIDTH] && wd != opt[FFN_OPT_WIDTH]))
+                (opt[FFN_OPT_WIDTH] && wd != (segments ? std::min<int64_t>(opt[FFN_OPT_WIDTH], ffn_long_width(cg, false))
+                                                       : opt[FFN_OPT_WIDTH])))
                 continue;
             Tiling t[kFfnMaxProducts];
             const int64_t C = cg == 2 ? d.max_pairs : d.sms;
@@ -555,7 +574,7 @@ int find_together(const Device &d, Product **xs, const Plan *alone, int n, const
             pl.stage_bytes = stage_bytes;
             pl.stages = ring_stages(d, stage_bytes);
             pl.smem = ffn_smem_bytes(stage_bytes, pl.stages);
-            pl.fn = ffn_together_fn(best_cg);
+            pl.fn = segments ? ffn_together_segments_fn(best_cg) : ffn_together_fn(best_cg);
             pl.grid = (int)std::min<int64_t>(total, best_cg == 2 ? d.max_pairs : d.sms) * best_cg;
         }
         const int rc = from_cuda(
@@ -865,6 +884,7 @@ int describe(const Product &x, const Plan &pl, FfnMaps &maps, FfnParams &p)
     p.stages = pl.stages;
     p.raster_group = band_of(pl, x.K);
     p.band_tiles = ffn_band_tiles(p.raster_group, pl.col_tiles);
+    p.segment = to_codes(x) ? kFfnCodesSegment : long_sum(x) ? kFfnSegment : 0x7FFFFFFF;
     p.sk_tiles = (int32_t)pl.sk_tiles;
     p.sk_units = pl.sk_tiles * pl.k_blocks;
     p.cluster = pl.cluster;

@@ -72,6 +72,12 @@ __host__ __device__ __forceinline__ int32_t ffn_range_of(int64_t units, int32_t 
     return (int32_t)(((u + 1) * clusters + units - 1) / units) - 1;
 }
 
+// End of the segment that k-block kb belongs to (kLong).
+__host__ __device__ __forceinline__ int32_t ffn_segment_end(int32_t kb, int32_t segment)
+{
+    return kb / segment * segment + segment;
+}
+
 // Which range is cluster c's, and whose range c is: the last cluster has the first one.  A tile's owner
 // waits for the ranges behind its own, so for clusters with lower indices, which the GPU places
 // before it: whatever else runs there, another stream's split tiles say, no cluster that is waited for still
@@ -238,6 +244,31 @@ __device__ __forceinline__ uint32_t mma_bf16_block(uint32_t d_tmem, uint64_t rde
               "r"(next_bar), "r"(next_parity)
             : "memory");
     return ready;
+}
+
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v)
+{
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr)
+{
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// One probe: 1 if the phase with this parity has completed.
+__device__ __forceinline__ uint32_t mbar_test(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}"
+                 : "=r"(ok)
+                 : "r"(bar), "r"(parity)
+                 : "memory");
+    return ok;
 }
 
 __device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -575,13 +606,51 @@ __device__ __forceinline__ float *ffn_partial(float *partials, int32_t cta, int 
     return partials + (size_t)cta * kFfnPartialFloats + (size_t)((((ew * 4 + slot) * 8) * 32 + lane) * 4);
 }
 
+// v += the 32 fp32 columns of tensor memory at taddr (this warp's 32 lanes), kAtOnce loaded at a time.
+template <int kAtOnce>
+__device__ __forceinline__ void ffn_add_chunk(uint32_t taddr, uint32_t (&v)[32])
+{
+#pragma unroll
+    for (int h = 0; h < 32; h += kAtOnce) {
+        uint32_t t[kAtOnce];
+        if constexpr (kAtOnce == 32)
+            tmem_load_32x32(taddr, t);
+        else
+            tmem_load_32x16(taddr + (uint32_t)h, t);
+        tmem_load_wait();
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i)
+            asm volatile("" : "+r"(t[i])::"memory");
+#pragma unroll
+        for (int i = 0; i < kAtOnce; i += 2) {
+            float lo, hi;
+            f32x2_parts((pair(__uint_as_float(v[h + i]), __uint_as_float(v[h + i + 1])) +
+                         pair(__uint_as_float(t[i]), __uint_as_float(t[i + 1]))).v,
+                        lo, hi);
+            v[h + i] = __float_as_uint(lo);
+            v[h + i + 1] = __float_as_uint(hi);
+        }
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
-template <int CG, bool kT, int kEpi, int kN = 1>
+// kLong: sums are added up in segments.  The tensor core's additions lose up to a unit of the accumulator each,
+// toward zero: a sum over 16384 was off by 1.9e-5 of its size, growing with its length.  bf16 hides that; for a
+// result in fp32, and for the codes of 8 bits (of which 8e-4 then rounded to the other side, by up to an eighth),
+// the accumulator takes p.segment k-blocks and the sums are added up in the epilogue's registers, rounded to
+// nearest: fp32 results are off by 4.8e-7 at any length with segments of 8 (1.0e-6 with 16, 2.1e-6 with 32; products
+// in plain fp32 by 2 to 4e-7), and of the codes 4e-5 round to the other side with segments of 16, as after plain fp32
+// sums.  Measured (us, with one accumulation and in segments): fp32 linear 4096^3 80.7 and 87.0, 64 x 8192 x 8192
+// 27.8 and 29.4, gradients of 4096^3 147.7 and 146.8; gated 8192 x 2048 x 8192 to 8 bits 290 and 287 (331 with
+// segments of 8: what follows a tile's sums must pass while the next tile's first two segments do).
+template <int CG, bool kT, int kEpi, int kN = 1, bool kLong = false>
 __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_constant__ FfnArgs<kN> args)
 {
     constexpr bool kPair = CG == 2;
     constexpr bool kDual = kEpi == kFfnGated;
     constexpr int kAccs = kDual ? 2 : 1;  // accumulators of an element
+    constexpr bool kCodes = kDual && kLong;  // the gated pair to 8 bits
+    static_assert(!kLong || kEpi == kFfnPlain || (kDual && !kT), "forms that segments are made for");
     constexpr uint32_t kTileRBytes = (uint32_t)kFfnRowsPerCta * 128u;
     static_assert(kN == 1 || (kEpi == kFfnPlain && !kT), "several products in one launch are plain ones");
     const FfnParams &p0 = args.p[0];  // what all products share
@@ -604,6 +673,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
     const uint32_t abort_flag = tmem_slot + 4u;
     const uint32_t ready_bar = abort_flag + 4u;  // cluster form: one per epilogue warp of rank 0;
                                                  // behind its eight, one that nothing waits for
+    const uint32_t go_words = ready_bar + 72u;   // kCodes: whether the epilogue's wait succeeded, two in turn,
+    const uint32_t block_bytes = full_bar + kFfnBarrierBytes;  // and the epilogue warps' scales, 512 bytes twice
 
     const int warp = __shfl_sync(0xFFFFFFFFu, (int)(threadIdx.x >> 5), 0);  // uniform, and known to be
     const int lane = threadIdx.x & 31;
@@ -798,6 +869,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             int acc = 0;
             uint32_t acc_ph = 0;
             uint32_t ready = 0u;  // the next stage was seen full
+            uint32_t drained = 0u;
             while (wi.next(args, w)) {
                 const FfnParams &p = args.p[w.product];
                 const uint64_t rdesc0 = p.r_mn ? smem_desc_mn_sw128(stage0) : smem_desc_sw128(stage0);
@@ -810,8 +882,21 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                                        (p.r_mn ? 1u << 15 : 0u) | (p.c_mn ? 1u << 16 : 0u);
                 wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
                 tc_fence_after_sync();
-                const uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFfnMaxWidth);
+                uint32_t d_tmem = tmem_base + (uint32_t)(acc * kFfnMaxWidth);
+                int32_t first = w.kb0;  // of the accumulator's k-blocks
+                int32_t cut = kLong ? ffn_segment_end(first, p.segment) : 0;
                 for (int32_t kb = w.kb0; kb < w.kb1; ++kb) {
+                    if (kLong && kb == cut) {
+                        mma_commit_elected<CG>(bad ? nobody_bar : accf_bar + 8u * acc, leader);
+                        acc ^= 1;
+                        acc_ph ^= acc == 0 ? 1u : 0u;
+                        if (!__all_sync(0xFFFFFFFFu, drained))
+                            wait(acce_bar + 8u * acc, acc_ph ^ 1u, kRoleMmaAcc, (uint32_t)acc);
+                        tc_fence_after_sync();
+                        d_tmem = tmem_base + (uint32_t)(acc * kFfnMaxWidth);
+                        first = kb;
+                        cut += p.segment;
+                    }
                     if (!__all_sync(0xFFFFFFFFu, ready))
                         wait(full_bar + 8u * s, ring_full_parity(ph), kRoleMmaFull, (uint32_t)s);
                     tc_fence_after_sync();
@@ -819,12 +904,14 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                     int s1 = s;
                     uint32_t ph1 = ph;
                     ring_advance(s1, ph1, S);
-                    const uint32_t add = kb > w.kb0 ? 1u : 0u;
+                    const uint32_t add = kb > (kLong ? first : w.kb0) ? 1u : 0u;
                     if constexpr (kDual && kT)
                         mma_bf16_block<CG>(d_tmem + kFfnDualWidth, rdesc0 + off + (kTileRBytes >> 4), cdesc0 + off,
                                            idesc, rstep, cstep, add, leader, full_bar + 8u * s1, ring_full_parity(ph1));
                     ready = mma_bf16_block<CG>(d_tmem, rdesc0 + off, cdesc0 + off, idesc, rstep, cstep, add, leader,
                                                full_bar + 8u * s1, ring_full_parity(ph1));
+                    if (kLong && kb + 1 == cut)  // the other accumulator's barrier, as the next stage's
+                        drained = mbar_test(acce_bar + 8u * (acc ^ 1), (acc == 1 ? acc_ph ^ 1u : acc_ph) ^ 1u);
                     if (ring_group_last(s, 1u))
                         mma_commit_elected<CG>(bad ? nobody_bar : empty_bar + 8u * ring_group(s, 1u), leader);
                     ring_advance(s, ph, S);
@@ -858,9 +945,22 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
         int acc = 0;
         uint32_t acc_ph = 0;
         const bool dense = p0.sk_units >= num_clusters;  // every range holds a unit
-        // each warp for itself: the warps of a tile need not keep step
+        uint32_t go_parity = 0u, block_parity = 0u;
+        // each warp for itself: the warps of a tile need not keep step.  But where warps exchange block maxima
+        // (kCodes) one thread waits and posts the outcome, so that all take the same branch; the word
+        // alternates.
         auto accumulated = [&]() {
-            return warp_wait<kPair>(ctl, accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc, lane);
+            if constexpr (kCodes) {
+                const uint32_t go = go_words + 4u * go_parity;
+                go_parity ^= 1u;
+                if (threadIdx.x == 128)
+                    st_volatile_shared_u32(
+                        go, ctl.wait<kPair>(accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc) ? 1u : 0u);
+                named_barrier_sync(1u, kFfnEpiWarps * 32u);
+                return ld_volatile_shared_u32(go) != 0u;
+            } else {
+                return warp_wait<kPair>(ctl, accf_bar + 8u * acc, acc_ph, kRoleEpilogue, (uint32_t)acc, lane);
+            }
         };
         // this warp has read its part of the accumulator: hand it back
         auto hand_back = [&]() {
@@ -873,11 +973,11 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                     mbar_arrive(acce_bar + 8u * acc);
             }
         };
-        auto load_chunk = [&](int a, int c, uint32_t(&v)[32]) {
-            tmem_load_32x32(tmem_base + ((uint32_t)(q * 32) << 16) +
-                                (uint32_t)(acc * kFfnMaxWidth + a * kFfnDualWidth + c * 32),
-                            v);
+        auto chunk_at = [&](int a, int c) {
+            return tmem_base + ((uint32_t)(q * 32) << 16) +
+                   (uint32_t)(acc * kFfnMaxWidth + a * kFfnDualWidth + c * 32);
         };
+        auto load_chunk = [&](int a, int c, uint32_t(&v)[32]) { tmem_load_32x32(chunk_at(a, c), v); };
         while (wi.next(args, w)) {
             const FfnParams &p = args.p[w.product];
             const FfnMaps &maps = args.maps[w.product];
@@ -992,7 +1092,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             };
             // transposed, a residual's first chunk: a column, an element a load, all of them ahead too (64 x
             // 8192 x 8192 with a residual and a bias 34.7 us without)
-            constexpr bool kEarly = kT && kEpi == kFfnPlain;
+            constexpr bool kEarly = kT && kEpi == kFfnPlain && !kLong;
             uint16_t early[kEarly ? 32 : 1];
             auto ahead_column = [&]() {
                 if constexpr (kEarly) {
@@ -1023,7 +1123,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                         f[e] = ffn_raw_pair(raw[i], e, codes, scale);
                 }
             };
-            if (!contributor && half < nchunks) {
+            if (!kLong && !contributor && half < nchunks) {
                 ahead(half);
                 if (kEarly && p.aux[0].p)
                     ahead_column();
@@ -1039,148 +1139,19 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                                             ((int64_t)(d_row0 + c * 32 + lane) * p.aux[i].ld + d_col0) *
                                                 (p.aux[i].scales ? 1 : 2));
             }
-            if (!accumulated())
-                break;
-            tc_fence_after_sync();
-            if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
-                hand_back();
-                collect();
-            }
-            float inv[2] = {0.0f, 0.0f};  // 8-bit checkpoints: this thread's row's scales, inverted
-            if constexpr (kDual && !kT) {
-                if (p.save == 2) {
-                    // a block of the format is the tile's 128 columns: each warp looks at them all
-#pragma unroll
-                    for (int a = 0; a < 2; ++a) {
-                        float top = 0.0f;
-                        for (int c = 0; c < 4; ++c) {
-                            uint32_t v[32];
-                            load_chunk(a, c, v);
-                            tmem_load_wait();
-                            reg_fence(v);
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                top = fmaxf(top, finite_abs(__uint_as_float(v[i])));
-                        }
-                        const uint32_t byte = scale_byte(KB ? top : 0.0f);
-                        inv[a] = scale_inverse(byte);
-                        const int32_t row = yr + lane, block = tc.col;
-                        if (half == a && row < p.D_rows) {
-                            uint8_t *const word = p.scales[a] + ((int64_t)(block >> 2) * p.D_rows + row) * 4;
-                            word[block & 3] = (uint8_t)byte;
-                            if (block == p.num_col_tiles - 1)
-                                for (int i = (block & 3) + 1; i < 4; ++i)
-                                    word[i] = 127;
-                        }
-                    }
-                }
-            }
-            int c0 = half;
-            if constexpr (kEpi == kFfnPlain && !kT) {
-                // whole tiles of bf16, most of the work: two chunks at a time, whose loads, stores and
-                // fences overlap (4096 x 8192 x 128 with relu 23.1 us, and 30.9 one by one)
-                const bool two = KB && !p.out_fp32 && !contributor && !owner;
-                if (two && !p.bias && p.act == kActNone && !p.aux[0].p && !p.save)
-                    // the sums as they are, as in every gradient: apart, in little code, since fetching it is
-                    // what counts (8192 x 8192 x 64 25.4 us, and 35.3 through the loop below)
-                    for (; c0 + 2 < nchunks; c0 += 4) {
-                        uint32_t v[2][32], pk[2][16];
-                        load_chunk(0, c0, v[0]);
-                        load_chunk(0, c0 + 2, v[1]);
-                        tmem_load_wait();
-                        reg_fence(v[0]);
-                        reg_fence(v[1]);
-                        if (c0 + 4 >= nchunks)
-                            hand_back();
-                        const int32_t col = d_col0 + c0 * 32;
-                        if (yr >= p.D_rows || col >= p.D_cols)
-                            continue;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h)
-#pragma unroll
-                            for (int i = 0; i < 16; ++i)
-                                pk[h][i] = pack_bf16x2(v[h][2 * i], v[h][2 * i + 1]);
-                        ffn_store_two(pk, st, other ? &maps.D[1] : &maps.D[0], other ? p.D[1] : p.D[0], yr, col, p);
-                    }
-                else if (two)
-                    for (; c0 + 2 < nchunks; c0 += 4) {
-                        uint32_t v[2][32];
-                        load_chunk(0, c0, v[0]);
-                        load_chunk(0, c0 + 2, v[1]);
-                        tmem_load_wait();
-                        reg_fence(v[0]);
-                        reg_fence(v[1]);
-                        if (c0 + 4 >= nchunks)
-                            hand_back();
-                        const int32_t col = d_col0 + c0 * 32;
-                        if (yr >= p.D_rows || col >= p.D_cols)
-                            continue;
-                        float f[2][32];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-#pragma unroll
-                            for (int i = 0; i < 32; ++i)
-                                f[h][i] = __uint_as_float(v[h][i]);
-                            ffn_add_bias<false>(f[h], col + 64 * h, p);
-                        }
-                        uint32_t pk[2][16];
-                        if (p.save) {
-                            ffn_pack(pk[0], f[0]);
-                            ffn_pack(pk[1], f[1]);
-                            ffn_store_two(pk, st, &maps.D[1], p.D[1], yr, col, p);
-                        }
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            if (p.act != kActNone)
-                                ffn_with_act(p.act, [&](auto tag) {
-#pragma unroll
-                                    for (int i = 0; i < 16; ++i)
-                                        f32x2_parts(ffn_act<decltype(tag)::value>(pair(f[h][2 * i], f[h][2 * i + 1])).v,
-                                                    f[h][2 * i], f[h][2 * i + 1]);
-                                });
-                            if (p.aux[0].p) {
-                                Pair r[16];
-                                aux_pairs(0, c0 + 2 * h, r);
-                                if (c0 + 2 * h + 2 < nchunks)
-                                    ahead(c0 + 2 * h + 2);
-#pragma unroll
-                                for (int i = 0; i < 16; ++i)
-                                    f32x2_parts((pair(f[h][2 * i], f[h][2 * i + 1]) + r[i]).v, f[h][2 * i],
-                                                f[h][2 * i + 1]);
-                            }
-                            ffn_pack(pk[h], f[h]);
-                        }
-                        ffn_store_two(pk, st, other ? &maps.D[1] : &maps.D[0], other ? p.D[1] : p.D[0], yr, col, p);
-                    }
-            }
-            for (int c = c0; c < nchunks; c += 2) {
-                uint32_t v[kAccs][32];
-#pragma unroll
-                for (int a = 0; a < kAccs; ++a)
-                    load_chunk(a, c, v[a]);
-                tmem_load_wait();
-#pragma unroll
-                for (int a = 0; a < kAccs; ++a) {
-                    reg_fence(v[a]);
-                    if (KB == 0) {  // an empty sum
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            v[a][i] = 0u;
-                    }
-                }
-                if (c + 2 >= nchunks)
-                    hand_back();
-                if (c == half && owner)
-                    collect();  // after this piece's own sums have been read
+            float inv[2] = {0.0f, 0.0f};  // kCodes: this thread's row's scales, inverted
+            bool infinite = false;        // and whether this warp holds infinities, whose codes are NaN
+            // one chunk's sums: left for the tile's owner, or completed and stored
+            auto finish = [&](int c, uint32_t(&v)[kAccs][32]) {
                 bool whole = true;
 #pragma unroll
                 for (int a = 0; a < kAccs; ++a)
                     whole = complete(a, c, v[a]);
                 const int32_t row = d_row0 + (kT ? c * 32 : 0), col = d_col0 + (kT ? 0 : c * 32);
                 if (!whole || row >= p.D_rows || col >= p.D_cols) {
-                    if (whole && c + 2 < nchunks)
+                    if (!kLong && whole && c + 2 < nchunks)
                         ahead(c + 2);
-                    continue;
+                    return;
                 }
                 uint32_t pk[16];
                 if constexpr (kEpi == kFfnPlain) {
@@ -1204,8 +1175,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                         });
                     if (p.aux[0].p) {
                         Pair r[16];
+                        if constexpr (kLong)
+                            ahead(c);  // its words would take registers from the sums before
                         aux_pairs(0, c, r);
-                        if (c + 2 < nchunks)
+                        if (!kLong && c + 2 < nchunks)
                             ahead(c + 2);
 #pragma unroll
                         for (int i = 0; i < 16; ++i)
@@ -1218,7 +1191,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                         ffn_store_bf16<kT>(pk, st, map, out, row, col, p);
                     }
                 } else if constexpr (kEpi == kFfnGated) {
-                    if (p.save == 1) {
+                    if (!kCodes && p.save) {
 #pragma unroll
                         for (int a = 0; a < 2; ++a) {
 #pragma unroll
@@ -1227,8 +1200,8 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                             ffn_store_bf16<kT>(pk, st, &maps.D[1 + a], p.D[1 + a], row, col, p);
                         }
                     }
-                    if constexpr (!kT) {
-                        if (p.save == 2 && row + lane < p.D_rows) {
+                    if constexpr (kCodes) {
+                        if (row + lane < p.D_rows) {
                             // 32 codes of this thread's row, one sector
 #pragma unroll
                             for (int a = 0; a < 2; ++a) {
@@ -1237,8 +1210,10 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                                 for (int i = 0; i < 8; ++i) {
                                     float e[4];
 #pragma unroll
-                                    for (int j = 0; j < 4; ++j)
-                                        e[j] = inf_to_nan(__uint_as_float(v[a][4 * i + j])) * inv[a];
+                                    for (int j = 0; j < 4; ++j) {
+                                        e[j] = __uint_as_float(v[a][4 * i + j]);
+                                        e[j] = (infinite ? inf_to_nan(e[j]) : e[j]) * inv[a];
+                                    }
                                     code[i] = pack_e4m3x4(e[0], e[1], e[2], e[3]);
                                 }
                                 uint4 *const dst =
@@ -1279,9 +1254,212 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
                     ffn_store_bf16<kT>(pdu, st, &maps.D[1], p.D[1], row, col, p);
                     ffn_store_bf16<kT>(ph, st, &maps.D[2], p.D[2], row, col, p);
                 }
+            };
+            if constexpr (kLong) {
+                constexpr int kOwn = (kDual ? kFfnDualWidth : ffn_long_width(CG, kT)) / 64;  // chunks of a warp
+                uint32_t run[kOwn][kAccs][32];
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                    for (int a = 0; a < kAccs; ++a)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            run[i][a][j] = 0u;
+                bool ok = accumulated();
+                if (!ok)
+                    break;
+                tc_fence_after_sync();
+                if (KB) {  // an empty sum's accumulator holds nothing
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+                        if (half + 2 * i < nchunks) {
+#pragma unroll
+                            for (int a = 0; a < kAccs; ++a)
+                                load_chunk(a, half + 2 * i, run[i][a]);
+                        }
+                    tmem_load_wait();
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                        for (int a = 0; a < kAccs; ++a)
+                            reg_fence(run[i][a]);
+                }
+                for (int32_t cut = ffn_segment_end(w.kb0, p.segment);; cut += p.segment) {
+                    hand_back();
+                    acc ^= 1;
+                    acc_ph ^= acc == 0 ? 1u : 0u;
+                    if (cut >= w.kb1 || !(ok = accumulated()))
+                        break;
+                    tc_fence_after_sync();
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+                        if (half + 2 * i < nchunks) {
+#pragma unroll
+                            for (int a = 0; a < kAccs; ++a)
+                                ffn_add_chunk<kOwn * kAccs == 4 ? 16 : 32>(chunk_at(a, half + 2 * i), run[i][a]);
+                        }
+                }
+                if (!ok)
+                    break;
+                collect();
+                if constexpr (kCodes) {
+                    // A block of the format is the tile's 128 columns, of which this warp holds half, and another
+                    // the other half.
+                    float top[2] = {0.0f, 0.0f};
+#pragma unroll
+                    for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                        for (int a = 0; a < 2; ++a)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                top[a] = fmaxf(top[a], fabsf(__uint_as_float(run[i][a][j])));
+                    infinite = __any_sync(0xFFFFFFFFu, is_inf(top[0]) || is_inf(top[1]));
+                    if (infinite) {  // infinities are no part of it
+                        top[0] = top[1] = 0.0f;
+#pragma unroll
+                        for (int i = 0; i < kOwn; ++i)
+#pragma unroll
+                            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                                for (int j = 0; j < 32; ++j)
+                                    top[a] = fmaxf(top[a], finite_abs(__uint_as_float(run[i][a][j])));
+                    }
+                    // The larger of the two halves' scales: a byte each, in two places used in turn, so that one
+                    // barrier does: whoever writes to a place has passed the barrier behind its last reads.
+                    uint32_t mine = scale_byte(top[0]) | scale_byte(top[1]) << 8, theirs;
+                    const uint32_t at = block_bytes + 512u * block_parity + 2u * (uint32_t)lane;
+                    block_parity ^= 1u;
+                    st_shared_u16(at + 64u * (uint32_t)ew, mine);
+                    named_barrier_sync(2u + (uint32_t)q, 64u);
+                    theirs = ld_shared_u16(at + 64u * (uint32_t)(ew ^ 4));
+#pragma unroll
+                    for (int a = 0; a < 2; ++a) {
+                        const uint32_t byte = max(mine >> (8 * a) & 0xFFu, theirs >> (8 * a) & 0xFFu);
+                        inv[a] = scale_inverse(byte);
+                        const int32_t row = yr + lane, block = tc.col;
+                        if (half == a && row < p.D_rows) {
+                            uint8_t *const word = p.scales[a] + ((int64_t)(block >> 2) * p.D_rows + row) * 4;
+                            word[block & 3] = (uint8_t)byte;
+                            if (block == p.num_col_tiles - 1)
+                                for (int i = (block & 3) + 1; i < 4; ++i)
+                                    word[i] = 127;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i)
+                    if (half + 2 * i < nchunks)
+                        finish(half + 2 * i, run[i]);
+            } else {
+                if (!accumulated())
+                    break;
+                tc_fence_after_sync();
+                if (half >= nchunks) {  // a tile of one chunk: the second group reads nothing
+                    hand_back();
+                    collect();
+                }
+                int c0 = half;
+                if constexpr (kEpi == kFfnPlain && !kT) {
+                    // whole tiles of bf16, most of the work: two chunks at a time, whose loads, stores and
+                    // fences overlap (4096 x 8192 x 128 with relu 23.1 us, and 30.9 one by one)
+                    const bool two = KB && !p.out_fp32 && !contributor && !owner;
+                    if (two && !p.bias && p.act == kActNone && !p.aux[0].p && !p.save)
+                        // the sums as they are, as in every gradient: apart, in little code, since fetching it is
+                        // what counts (8192 x 8192 x 64 25.4 us, and 35.3 through the loop below)
+                        for (; c0 + 2 < nchunks; c0 += 4) {
+                            uint32_t v[2][32], pk[2][16];
+                            load_chunk(0, c0, v[0]);
+                            load_chunk(0, c0 + 2, v[1]);
+                            tmem_load_wait();
+                            reg_fence(v[0]);
+                            reg_fence(v[1]);
+                            if (c0 + 4 >= nchunks)
+                                hand_back();
+                            const int32_t col = d_col0 + c0 * 32;
+                            if (yr >= p.D_rows || col >= p.D_cols)
+                                continue;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                                for (int i = 0; i < 16; ++i)
+                                    pk[h][i] = pack_bf16x2(v[h][2 * i], v[h][2 * i + 1]);
+                            ffn_store_two(pk, st, other ? &maps.D[1] : &maps.D[0], other ? p.D[1] : p.D[0], yr, col, p);
+                        }
+                    else if (two)
+                        for (; c0 + 2 < nchunks; c0 += 4) {
+                            uint32_t v[2][32];
+                            load_chunk(0, c0, v[0]);
+                            load_chunk(0, c0 + 2, v[1]);
+                            tmem_load_wait();
+                            reg_fence(v[0]);
+                            reg_fence(v[1]);
+                            if (c0 + 4 >= nchunks)
+                                hand_back();
+                            const int32_t col = d_col0 + c0 * 32;
+                            if (yr >= p.D_rows || col >= p.D_cols)
+                                continue;
+                            float f[2][32];
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                                for (int i = 0; i < 32; ++i)
+                                    f[h][i] = __uint_as_float(v[h][i]);
+                                ffn_add_bias<false>(f[h], col + 64 * h, p);
+                            }
+                            uint32_t pk[2][16];
+                            if (p.save) {
+                                ffn_pack(pk[0], f[0]);
+                                ffn_pack(pk[1], f[1]);
+                                ffn_store_two(pk, st, &maps.D[1], p.D[1], yr, col, p);
+                            }
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                if (p.act != kActNone)
+                                    ffn_with_act(p.act, [&](auto tag) {
+#pragma unroll
+                                        for (int i = 0; i < 16; ++i)
+                                            f32x2_parts(ffn_act<decltype(tag)::value>(pair(f[h][2 * i], f[h][2 * i + 1])).v,
+                                                        f[h][2 * i], f[h][2 * i + 1]);
+                                    });
+                                if (p.aux[0].p) {
+                                    Pair r[16];
+                                    aux_pairs(0, c0 + 2 * h, r);
+                                    if (c0 + 2 * h + 2 < nchunks)
+                                        ahead(c0 + 2 * h + 2);
+#pragma unroll
+                                    for (int i = 0; i < 16; ++i)
+                                        f32x2_parts((pair(f[h][2 * i], f[h][2 * i + 1]) + r[i]).v, f[h][2 * i],
+                                                    f[h][2 * i + 1]);
+                                }
+                                ffn_pack(pk[h], f[h]);
+                            }
+                            ffn_store_two(pk, st, other ? &maps.D[1] : &maps.D[0], other ? p.D[1] : p.D[0], yr, col, p);
+                        }
+                }
+                for (int c = c0; c < nchunks; c += 2) {
+                    uint32_t v[kAccs][32];
+#pragma unroll
+                    for (int a = 0; a < kAccs; ++a)
+                        load_chunk(a, c, v[a]);
+                    tmem_load_wait();
+#pragma unroll
+                    for (int a = 0; a < kAccs; ++a) {
+                        reg_fence(v[a]);
+                        if (KB == 0) {  // an empty sum
+#pragma unroll
+                            for (int i = 0; i < 32; ++i)
+                                v[a][i] = 0u;
+                        }
+                    }
+                    if (c + 2 >= nchunks)
+                        hand_back();
+                    if (c == half && owner)
+                        collect();  // after this piece's own sums have been read
+                    finish(c, v);
+                }
+                acc ^= 1;
+                acc_ph ^= acc == 0 ? 1u : 0u;
             }
-            acc ^= 1;
-            acc_ph ^= acc == 0 ? 1u : 0u;
             if (contributor) {
                 __syncwarp();  // the warp's stores come before lane 0's release
                 if (lane == 0 && shared_tile)

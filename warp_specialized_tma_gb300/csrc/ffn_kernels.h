@@ -21,6 +21,17 @@ constexpr int kFfnStagingBytes = 2 * kFfnPieceBytes;  // per epilogue warp
 constexpr int kFfnMaxStages = 12;
 constexpr int kFfnPartialFloats = kFfnRowsPerCta * 256;  // one CTA's fp32 partial of a split tile
 constexpr int kFfnMaxCluster = 8;
+// k-blocks that an accumulator takes before its sums are moved on
+constexpr int kFfnSegment = 8;        // of an fp32 result
+constexpr int kFfnCodesSegment = 16;  // of 8-bit codes
+// The widest tile whose sums are then held in registers: four chunks a warp for the large tiles of SM pairs, three
+// elsewhere (with four 64 x 8192 x 8192 took 32.8 us, not 28.9, for what spills).
+__host__ __device__ constexpr int ffn_long_width(int cta_group, bool transposed)
+{
+    return cta_group == 2 && !transposed ? 256 : 192;
+}
+constexpr int kFfnBarrierBytes = 512;
+constexpr int kFfnBlockBytes = 1024;  // where the warps of the gated form to 8 bits exchange scales
 
 enum FfnEpilogue : int32_t {
     kFfnPlain = 0,   // D0 = act(S + bias) + residual, D1 = S + bias
@@ -61,6 +72,7 @@ struct FfnParams {
     int32_t stages;
     int32_t raster_group;
     uint32_t band_tiles;       // ffn_band_tiles()
+    int32_t segment;           // kernels that add up segments: their k-blocks (a bf16 result's: all)
     int32_t sk_tiles;          // tiles [0, sk_tiles) are split along k among all clusters
     int64_t sk_units;          // sk_tiles * num_k_blocks
     int32_t cluster;           // > 1 (one SM per tile only): each tile is split among the CTAs of a cluster
@@ -70,7 +82,7 @@ struct FfnParams {
     FfnAux aux[2];             // kFfnPlain: residual; kFfnGrad: g, u
     const void *bias;
     int32_t bias_fp32;
-    int32_t save;              // kFfnPlain: 1 = D1; kFfnGated: 1 = D1 and D2, 2 = codes
+    int32_t save;              // kFfnPlain: 1 = D1; kFfnGated: 1 = D1 and D2, 2 = codes, by a kernel of their own
     uint8_t *codes[2];         // kFfnGated, save == 2: of g and u
     uint8_t *scales[2];
     int64_t ldq[2];
@@ -107,14 +119,18 @@ inline int ffn_chunk_rows(bool mn, int rows) { return mn ? (rows + 63) / 64 * 64
 inline size_t ffn_smem_bytes(size_t stage_bytes, int stages)
 {
     return 1024 /* alignment slack */ + (size_t)stages * stage_bytes + (size_t)kFfnEpiWarps * kFfnStagingBytes +
-           512 /* barriers */;
+           kFfnBarrierBytes + kFfnBlockBytes;
 }
 
-// (FfnArgs<1>), the last (FfnArgs<kFfnMaxProducts>)
+// (FfnArgs<1>), the last (FfnArgs<kFfnMaxProducts>).  Sums that are not rounded to bf16 at once, but
+// stay in fp32 or go to 8 bits, are added up in segments (`segments`, `codes`).
 const void *ffn_plain_fn(int cta_group, bool transposed);
+const void *ffn_plain_segments_fn(int cta_group, bool transposed);
 const void *ffn_gated_fn(int cta_group, bool transposed);
+const void *ffn_gated_codes_fn(int cta_group);
 const void *ffn_grad_fn(int cta_group, bool transposed);
 const void *ffn_together_fn(int cta_group);
+const void *ffn_together_segments_fn(int cta_group);
 
 uint32_t *ffn_status_word();  // of the current device, or null
 

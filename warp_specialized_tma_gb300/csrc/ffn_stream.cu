@@ -65,8 +65,12 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// Chunks of a warp whose products the MMA adds up before its sums move on, to this thread's places in shared memory
+// (kLong: fp32 results of long sums; see ffn_gemm.cuh).
+constexpr int kStreamSegment = kFfnSegment;
+
 // kTiles * 8 tokens; kDual: two weights.
-template <int kTiles, bool kDual>
+template <int kTiles, bool kDual, bool kLong>
 __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const FfnStreamParams p)
 {
     constexpr int kW = kDual ? 2 : 1;
@@ -105,6 +109,25 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const 
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 acc[a][b][e] = 0.0f;
+    float *const mine = sums + warp * kWarpSums;
+    auto place = [&](int a, int b, int e) { return (a * kTiles + b) * 128 + (g + 8 * (e >> 1)) * 8 + 2 * t + (e & 1); };
+    auto move_on = [&]() {
+#pragma unroll
+        for (int a = 0; a < kW; ++a)
+#pragma unroll
+            for (int b = 0; b < kTiles; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    mine[place(a, b, e)] += acc[a][b][e];
+                    acc[a][b][e] = 0.0f;
+                }
+    };
+    if constexpr (kLong)
+#pragma unroll
+        for (int i = 0; i < kWarpSums / 32; ++i)
+            mine[i * 32 + lane] = 0.0f;
+    if constexpr (kLong)
+        __syncwarp();
     // `whole`: the chunk lies inside the rows
     auto load = [&](uint4(&to)[kW][2][2], uint4(&xs)[kTiles][2], int32_t i, bool whole) {
         const int32_t k = (wk + i * ranges) * kStreamK;
@@ -151,12 +174,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const 
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
             load(w[d], x[d], d, true);
-        for (int32_t i = 1; i < rounds; ++i)
+        for (int32_t i = 1; i < rounds; ++i) {
+            if (kLong && i % (kStreamSegment / kDepth) == 0)
+                move_on();
 #pragma unroll
             for (int d = 0; d < kDepth; ++d) {
                 use(w[d], x[d]);
                 load(w[d], x[d], i * kDepth + d, true);
             }
+        }
+        if (kLong)
+            move_on();
 #pragma unroll
         for (int d = 0; d < kDepth; ++d)
             use(w[d], x[d]);
@@ -169,14 +197,17 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const 
     for (int d = 0; d < kDepth; ++d)
         if (rounds * kDepth + d < n)
             use(w[d], x[d]);
-    float *const mine = sums + warp * kWarpSums;
+    if constexpr (kLong) {
+        move_on();
+    } else {
 #pragma unroll
-    for (int a = 0; a < kW; ++a)
+        for (int a = 0; a < kW; ++a)
 #pragma unroll
-        for (int b = 0; b < kTiles; ++b)
+            for (int b = 0; b < kTiles; ++b)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                mine[(a * kTiles + b) * 128 + (g + 8 * (e >> 1)) * 8 + 2 * t + (e & 1)] = acc[a][b][e];
+                for (int e = 0; e < 4; ++e)
+                    mine[place(a, b, e)] = acc[a][b][e];
+    }
     __syncthreads();
     // one result a thread: rows fastest, so that a token's results are stored together
     for (int32_t i = (int32_t)threadIdx.x; i < R * p.M; i += kStreamWarps * 32) {
@@ -220,7 +251,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const 
     }
 }
 
-template <int kTiles, bool kDual>
+template <int kTiles, bool kDual, bool kLong = false>
 cudaError_t run(const FfnStreamParams &p, unsigned grid, cudaStream_t stream)
 {
     cudaLaunchConfig_t cfg = {};
@@ -234,13 +265,13 @@ cudaError_t run(const FfnStreamParams &p, unsigned grid, cudaStream_t stream)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (cfg.dynamicSmemBytes > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(ffn_stream_kernel<kTiles, kDual>,
+        const cudaError_t e = cudaFuncSetAttribute(ffn_stream_kernel<kTiles, kDual, kLong>,
                                                    cudaFuncAttributeMaxDynamicSharedMemorySize,
                                                    (int)cfg.dynamicSmemBytes);
         if (e != cudaSuccess)
             return e;
     }
-    return cudaLaunchKernelEx(&cfg, ffn_stream_kernel<kTiles, kDual>, p);
+    return cudaLaunchKernelEx(&cfg, ffn_stream_kernel<kTiles, kDual, kLong>, p);
 }
 
 }  // namespace
@@ -251,6 +282,11 @@ int launch_ffn_stream(FfnStreamParams &p, int num_sms, cudaStream_t stream)
     const int64_t rows = ((int64_t)p.N + grid - 1) / grid;
     p.groups = (int32_t)((rows + 15) / 16);
     const bool dual = p.w[1] != nullptr;
+    const int64_t chunks = ((int64_t)p.K + kStreamK - 1) / kStreamK;
+    if (!dual && p.out_fp32 && chunks > (int64_t)kStreamSegment * (kStreamWarps / p.groups))
+        return p.M <= 8    ? run<1, false, true>(p, grid, stream)
+               : p.M <= 16 ? run<2, false, true>(p, grid, stream)
+                           : run<4, false, true>(p, grid, stream);
     if (p.M <= 8)
         return dual ? run<1, true>(p, grid, stream) : run<1, false>(p, grid, stream);
     if (p.M <= 16)
