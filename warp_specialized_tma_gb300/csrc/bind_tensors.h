@@ -46,6 +46,10 @@ inline const Tensor &tensor(PyObject *o, const char *what)
     if (t.requires_grad() && at::GradMode::is_enabled())
         value_error(std::string(what) + " requires a gradient, which these operators do not record: call them under "
                                         "torch.no_grad(), or in the forward of a torch.autograd.Function");
+    // and so from its tangent (undefined where forward-mode derivatives are not recorded)
+    if (t._fw_grad(/* level */ 0).defined())
+        value_error(std::string(what) + " has a forward-mode tangent, which these operators do not carry on: call them on "
+                                        "its primal, or in the forward of a torch.autograd.Function with a jvp");
     return t;
 }
 

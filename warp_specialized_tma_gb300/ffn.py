@@ -19,7 +19,8 @@ What gated() saves in 8 bits is in fp8's format: codes (float8_e4m3fn) and scale
 Every function enqueues its work on ``stream`` (default: the current stream of the tensors'
 device) and returns without waiting.  The work is done by ``libffn_ops.so``; there is no
 fallback.  Nothing is recorded for autograd: tensors that require a gradient are refused while
-gradients are recorded, and the backward passes are called by name (as ``feedforward`` does).
+gradients are recorded, and tensors with a forward-mode tangent while tangents are; the backward
+passes are called by name (as ``feedforward`` does).
 """
 from __future__ import annotations
 

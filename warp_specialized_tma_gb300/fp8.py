@@ -20,7 +20,8 @@ current stream of the tensors' device) and returns without waiting.  The work is
 done by ``libfp8_ops.so``; ``_fp8_bind.so`` checks and marshals tensors, and the
 handle's settings go through ctypes.  There is no fallback.  Nothing is recorded for
 autograd: tensors that require a gradient are refused while gradients are
-recorded, and rmsnorm_backward is called by name (as ``prenorm`` does).
+recorded, and tensors with a forward-mode tangent while tangents are; rmsnorm_backward is
+called by name (as ``prenorm`` does).
 """
 from __future__ import annotations
 
