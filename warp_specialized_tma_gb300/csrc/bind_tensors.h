@@ -161,6 +161,14 @@ struct Place {
 inline void *data(const Tensor &t) { return const_cast<void *>(t.const_data_ptr()); }
 inline void *data(const Tensor *t) { return t ? data(*t) : nullptr; }
 
+// The caller's tensor has been written to: autograd finds by its version that a tensor saved for a backward
+// pass is no longer what was saved.  (A tensor of inference mode is never saved, and has no version.)
+inline void written(const Tensor *t)
+{
+    if (t && !t->is_inference())
+        t->unsafeGetTensorImpl()->bump_version();
+}
+
 inline PyObject *tuple_of(std::initializer_list<PyObject *> items)
 {
     PyObject *t = PyTuple_New((Py_ssize_t)items.size());

@@ -144,6 +144,7 @@ inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
             a.z = result(z);
         }
         run(at, a, &ffn_linear_workspace, &ffn_linear, "ffn_linear");
+        written(given);
         if (!save)
             return wrap(std::move(y));
         return tuple_of({wrap(std::move(y)), wrap(std::move(z))});

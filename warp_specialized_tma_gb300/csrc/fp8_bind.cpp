@@ -80,6 +80,7 @@ PyObject *bind_gemm(PyObject *, PyObject *const *args, Py_ssize_t n)
         check(fp8_gemm_run_in(h, data(a), data(as), data(b), data(bs), data(out), need ? data(work) : nullptr, need,
                               at.stream),
               "fp8_gemm_run");
+        written(given);
         return wrap(std::move(out));
     });
 }
@@ -156,6 +157,7 @@ PyObject *bind_rmsnorm(PyObject *, PyObject *const *args, Py_ssize_t n)
         check(fp8_rmsnorm(data(x), ldx, data(res), ldr, data(w), wtype, R, C, (float)eps, res ? data(h) : nullptr, ldh,
                           data(q), padded(C), data(s), static_cast<float *>(data(rstd)), at.stream),
               "fp8_rmsnorm");
+        written(out_h);
         PyObject *hp = args[0];  // without a residual h is x itself
         if (out_h)
             hp = args[4];
