@@ -95,7 +95,7 @@ void run(const Place &at, const Args &args, int (*measure)(const Args *, int64_t
     check(call(&args, need ? data(work) : nullptr, need, at.stream), name);
 }
 
-// linear(x, weight, bias or None, activation, residual or None, save, out or None, out_dtype) -> y or (y, z)
+// linear(x, weight, bias or None, activation, residual or None, save, out or None, out_dtype or None) -> y or (y, z)
 inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
 {
     return guarded([&]() -> PyObject * {
@@ -118,6 +118,11 @@ inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
         if (res)
             a.residual = matrix(*res, M, N, "residual");
         const int save = truth(args[5]);
+        const at::ScalarType type = args[7] != Py_None ? result_type(args[7], "out_dtype")
+                                    : given            ? given->scalar_type()
+                                                       : at::kBFloat16;
+        if (given && given->scalar_type() != type)
+            value_error("out is not of out_dtype");
         Place at(x);
         at.same(&w), at.same(bias), at.same(res), at.same(given);
         Tensor y, z;
@@ -135,7 +140,7 @@ inline PyObject *linear(PyObject *, PyObject *const *args, Py_ssize_t n)
             if (res && !same)
                 need_apart(y, *res, "residual");
         } else {
-            y = whole_rows(at, M, N, result_type(args[7], "out_dtype"));
+            y = whole_rows(at, M, N, type);
             a.y = result(y);
         }
         a.y_type = element_type(y, "out");

@@ -243,8 +243,8 @@ def device_status(device=None):
 
 
 def linear(x, weight, bias=None, activation=None, residual=None, save: bool = False, out=None,
-           out_dtype=torch.bfloat16, stream=None):
-    """act(x @ weight.T + bias) + residual: M x N in bf16 or fp32.
+           out_dtype=None, stream=None):
+    """act(x @ weight.T + bias) + residual: M x N in bf16 or fp32 (``out_dtype``: out's, or else bf16).
 
     x: M x K, weight: N x K, residual: M x N; bias: N values, bf16 or fp32.  With ``save`` returns
     (y, z), z being x @ weight.T + bias in bf16, which linear_backward() needs for an activation.
