@@ -25,11 +25,13 @@ from . import ffn
 
 
 class GatedFeedForward:
-    """w_gate, w_up: F x C; w_down: N x F; bf16."""
+    """w_gate, w_up: F x C; w_down: N x F; bf16.  ``save`` is how forward_train() keeps the projections: "bf16" or
+    "e4m3", or None for a block that only serves."""
 
     def __init__(self, w_gate, w_up, w_down, activation="silu", save="bf16"):
         if w_gate.shape != w_up.shape or w_down.shape[1] != w_gate.shape[0]:
             raise ValueError("w_gate and w_up must be F x C, w_down N x F")
+        ffn._choice(ffn.SAVES, save, "save")
         self.w_gate, self.w_up, self.w_down = w_gate, w_up, w_down
         self.activation, self.save = activation, save
 
@@ -40,6 +42,8 @@ class GatedFeedForward:
 
     def forward_train(self, x, residual=None):
         """(y, saved): saved is what backward() needs."""
+        if self.save is None:
+            raise ValueError("this block keeps nothing for a backward pass: save must be 'bf16' or 'e4m3'")
         h, kept = ffn.gated(x, self.w_gate, self.w_up, self.activation, save=self.save)
         return ffn.linear(h, self.w_down, residual=residual), (x, kept)
 
