@@ -284,8 +284,8 @@ double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
     const bool grad = x.epilogue == kFfnGrad;
     double results = grad || (dual && x.p.save == 1) ? 3.0 : x.p.save == 1 ? 2.0 : 1.0;
     for (const FfnAux &a : x.p.aux)
-        if (a.p && t.transposed)  // a residual's first chunk is asked for ahead, all of it up to a width of 64
-            results += a.scales ? 14.0 : !grad && t.width <= 64 ? 2.0 : 6.4;
+        if (a.p && t.transposed)  // of a residual, what the kernel asks for ahead costs little
+            results += a.scales ? 14.0 : !grad && !long_sum(x) && t.width <= kFfnEarlyColumns ? 2.0 : 6.4;
     const double epilogue = 15.6 * sums * results;
     const double chunks = grad && !t.transposed ? 90.0 * sums + 4800.0
                                                 : (4.0 * sums + 1853.0) * results * (t.transposed ? 1.7 : 1.0);
@@ -670,14 +670,13 @@ void copy_first(Call &c, Operand &o, int64_t mem_rows, int64_t mem_cols)
     o.ld = found->ldd;
 }
 
-int set_out(FfnOut &out, CUtensorMap *map, const ffn_matrix &m, bool fp32, int64_t rows, int64_t cols)
+void set_out(FfnOut &out, CUtensorMap *map, const ffn_matrix &m, bool fp32, int64_t rows, int64_t cols)
 {
     out.p = m.data;
     out.ld = rows > 1 ? m.ld : padded(cols);
     const int esize = fp32 ? 4 : 2;
     out.tma = aligned(m.data, 16) && out.ld * esize % 16 == 0 &&
               encode_2d(map, fp32, m.data, cols, rows, out.ld * esize, 64 / esize, 32, CU_TENSOR_MAP_SWIZZLE_64B);
-    return FFN_OK;
 }
 
 FfnAux aux_of(const ffn_matrix &m)

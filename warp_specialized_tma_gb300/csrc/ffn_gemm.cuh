@@ -1093,6 +1093,7 @@ __global__ void __launch_bounds__(kFfnThreads, 1) ffn_gemm_kernel(const __grid_c
             // transposed, a residual's first chunk: a column, an element a load, all of them ahead too (64 x
             // 8192 x 8192 with a residual and a bias 34.7 us without)
             constexpr bool kEarly = kT && kEpi == kFfnPlain && !kLong;
+            static_assert(kFfnEarlyColumns == 2 * 32, "the two halves' first chunks");
             uint16_t early[kEarly ? 32 : 1];
             auto ahead_column = [&]() {
                 if constexpr (kEarly) {

@@ -30,6 +30,7 @@ __host__ __device__ constexpr int ffn_long_width(int cta_group, bool transposed)
 {
     return cta_group == 2 && !transposed ? 256 : 192;
 }
+constexpr int kFfnEarlyColumns = 64;  // of a transposed tile, whose residual is loaded ahead: each half's first chunk
 constexpr int kFfnBarrierBytes = 512;
 constexpr int kFfnBlockBytes = 1024;  // where the warps of the gated form to 8 bits exchange scales
 

@@ -25,6 +25,7 @@
 // latency; from 16 tokens on the tokens' words, read from L1 by every warp, cost as much as the
 // weights'.
 #include "ffn_math.cuh"
+#include "ffn_stream.cuh"
 #include "gemm_common.cuh"
 
 #include <algorithm>
@@ -35,35 +36,6 @@ namespace {
 
 constexpr int kStreamWarps = 16;
 constexpr int kStreamK = 64;  // of a chunk: 128 bytes of a row
-
-// Not through the read-only path: what the kernel before wrote may have been read there.
-__device__ __forceinline__ uint4 load_once(const uint16_t *p)
-{
-    uint4 q;
-    asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                 : "l"(p));
-    return q;
-}
-
-__device__ __forceinline__ uint4 load_again(const uint16_t *p)
-{
-    uint4 q;
-    asm volatile("ld.global.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                 : "l"(p));
-    return q;
-}
-
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
 
 // Chunks of a warp whose products the MMA adds up before its sums move on, to this thread's places in shared memory
 // (kLong: fp32 results of long sums; see ffn_gemm.cuh).
@@ -141,7 +113,7 @@ __global__ void __launch_bounds__(kStreamWarps * 32, 1) ffn_stream_kernel(const 
                         to[a][h][r] = load_once(wrow[a][r] + k + 32 * h);
 #pragma unroll
                 for (int b = 0; b < kTiles; ++b)
-                    xs[b][h] = load_again(xrow[b] + k + 32 * h);
+                    xs[b][h] = load_again_16(xrow[b] + k + 32 * h);
             } else {
 #pragma unroll
                 for (int a = 0; a < kW; ++a)

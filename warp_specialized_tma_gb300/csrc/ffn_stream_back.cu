@@ -23,6 +23,7 @@
 // One token's are bound by HBM (up to 6.4 TB/s); with more the tokens' words, read from L1 by every warp,
 // count.
 #include "ffn_math.cuh"
+#include "ffn_stream.cuh"
 #include "gemm_common.cuh"
 
 #include <algorithm>
@@ -36,37 +37,11 @@ constexpr int kBackWarps = 16;
 constexpr int kBackRows = 16;  // of a unit
 constexpr int kBackColumns = 64;
 
-__device__ __forceinline__ uint4 load_once(const uint16_t *p)
-{
-    uint4 q;
-    asm volatile("ld.global.L1::no_allocate.L2::128B.v4.u32 {%0, %1, %2, %3}, [%4];"
-                 : "=r"(q.x), "=r"(q.y), "=r"(q.z), "=r"(q.w)
-                 : "l"(p));
-    return q;
-}
-
-__device__ __forceinline__ uint2 load_again(const uint16_t *p)
-{
-    uint2 q;
-    asm volatile("ld.global.v2.u32 {%0, %1}, [%2];" : "=r"(q.x), "=r"(q.y) : "l"(p));
-    return q;
-}
-
 __device__ __forceinline__ float ld_shared_cluster_f32(uint32_t addr)
 {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
-}
-
-// D (16 x 8, fp32) += A (16 x 16) B (16 x 8).
-__device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1)
-{
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
-                 "{%0, %1, %2, %3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 __device__ __forceinline__ float aux_value(const FfnAux &a, int32_t m, int32_t c, int32_t M)
@@ -127,7 +102,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 1) ffn_stream_back_kernel(con
             to[r] = load_once(from + r * p.ldw[which]);
 #pragma unroll
         for (int b = 0; b < kTiles; ++b)
-            ds[b] = load_again(p.d[which] + (int64_t)min(g + 8 * b, p.M - 1) * p.ldd[which] + row);
+            ds[b] = load_again_8(p.d[which] + (int64_t)min(g + 8 * b, p.M - 1) * p.ldd[which] + row);
     };
     auto use = [&](uint4(&from)[4], uint2(&ds)[kTiles]) {
         const uint32_t r[4][4] = {{from[0].x, from[0].y, from[0].z, from[0].w},
