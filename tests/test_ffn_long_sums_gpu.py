@@ -255,3 +255,53 @@ def test_products_of_one_launch_may_give_up():
             dx, dw, _ = ffn.linear_backward(dy, x, w, grad_dtype=torch.float32)
         assert dx.equal((dy.double() @ w.double()).to(bf)) and dw.double().equal(dy.double().T @ x.double())
         assert ffn.device_status() == (ffn.OK, 0)
+
+
+# ------------------------------------------------------------------ calls at once
+def test_calls_at_once_on_streams_of_their_own():
+    x, w = ints(20, 6000, seed=1), ints(2560, 6000, seed=2)
+    tall = ints(300, 6000, seed=3)
+    want = [(t.double() @ w.double().T).float() for t in (x, tall)]
+    split = dict(cta_group=1, transposed=2, width=32, split=2, stream=2)  # tiles meet through global memory
+    with ffn.options(cta_group=1):
+        codes = ffn.gated(tall, w, w, "relu", save="e4m3")
+    streams = [torch.cuda.Stream(priority=-1), torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[], [], []]
+    for _ in range(20):
+        with ffn.options(**split):
+            got[0].append(ffn.linear(x, w, out_dtype=torch.float32, stream=streams[0]))
+        with ffn.options(cta_group=2, transposed=1, width=64, split=2):
+            got[1].append(ffn.linear(tall, w, out_dtype=torch.float32, stream=streams[1]))
+        got[2].append(ffn.gated(tall, w, w, "relu", save="e4m3", stream=streams[2]))
+    assert ffn.device_status() == (ffn.OK, 0)
+    for a, e in zip(got, want):
+        assert all(t.equal(e) for t in a)
+    for h, saved in got[2]:
+        assert h.equal(codes[0])
+        assert all(a.view(torch.uint8).equal(b.view(torch.uint8)) for a, b in zip(saved, codes[1]))
+
+
+def test_graphs_replayed_at_once_share_no_workspace():
+    work = [(ints(20, 6000, seed=s), ints(2560, 6000, seed=s + 1)) for s in (1, 5)]
+    graphs, outs = [], []
+    with ffn.options(cta_group=1, transposed=2, width=32, split=2, stream=2):
+        for x, w in work:
+            graphs.append(torch.cuda.CUDAGraph())
+            outs.append(torch.empty(20, 2560, device="cuda"))
+            torch.cuda.synchronize()
+            with torch.cuda.graph(graphs[-1]):
+                for _ in range(8):
+                    ffn.linear(x, w, out=outs[-1])
+        assert ffn.plan_info()["split_tiles"] > 0
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(5):
+        for o in outs:
+            o.fill_(0)
+        torch.cuda.synchronize()
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+        torch.cuda.synchronize()
+        for o, (x, w) in zip(outs, work):
+            assert o.double().equal(x.double() @ w.double().T)
