@@ -6,10 +6,15 @@
  *   ffn_gated_backward   of y = h Wd^T: dh = dy Wd;  dg = dh u act'(g), du = dh act(g), h = act(g) u;
  *                        dx = dg Wg + du Wu, dWg = dg^T x, dWu = du^T x, dWd = dy^T h
  *
- * Matrices are bf16 with contiguous rows, `ld` elements apart; sums are fp32.  Any
- * base and pitch will do; rows at multiples of 128 bytes are fastest.  An operand of a
- * product whose rows do not start at multiples of 16 bytes is first copied to the
- * workspace, as is a large one whose rows do not at multiples of 128.  dz, and dg, du and h of
+ * Matrices are bf16 with contiguous rows, `ld` elements apart; sums are fp32.  Those of an
+ * fp32 result, and those that are kept in 8 bits, are rounded to nearest every 512 (1024)
+ * terms at least, so that their error does not grow with their length; a bf16 result's may be
+ * added up in the tensor core alone, whose additions truncate: 1e-9 of the sum a term.
+ *
+ * Any base and pitch will do; rows at multiples of 128 bytes are fastest.  An operand of a
+ * product whose rows do not start at multiples of 16 bytes is copied to the workspace first,
+ * by every call, as is a large one whose rows do not at multiples of 128: weights that are
+ * used again and again are better laid out so once.  dz, and dg, du and h of
  * ffn_gated_backward, are rounded to bf16, in which the products that follow take them.
  *
  * Calls return a status code, never throw, and only enqueue work on `stream` (a
@@ -61,7 +66,8 @@ typedef enum ffn_option {
     FFN_OPT_CTA_GROUP = 1,   /* 1 = one SM per tile, 2 = SM pairs */
     FFN_OPT_TRANSPOSED = 2,  /* 1 = the result's rows on the MMA's row side, 2 = its columns */
     FFN_OPT_WIDTH = 3,       /* the tile's width on the MMA's column side: a multiple of 16 (32 for SM pairs), at
-                                most 256 (128 for a transposed ffn_gated, whose width is fixed otherwise) */
+                                most 256 (128 for a transposed ffn_gated, whose width is fixed otherwise; for
+                                long sums of an fp32 result 192 stands for more, but for pairs not transposed) */
     FFN_OPT_SPLIT = 4,       /* tiles that would leave SMs idle are split along K: 1 = among clusters of CTAs or
                                 through global memory (default), 2 = through global memory only, 0 = never */
     FFN_OPT_WATCHDOG_NS = 5, /* limit of any wait inside a kernel (default 2e9, 1e5 to 6e10) */

@@ -252,9 +252,12 @@ int ring_stages(const Device &d, size_t stage_bytes)
 // the tiles of the longest chain, each its stages (k-blocks: the longest of the MMAs, 4096
 // multiply-adds a clock and SM, the loads, 62 bytes a clock and SM and 9231 over all SMs, and a stage's
 // handling, 394 clocks, or 345 where half of its rows are loaded) or its epilogue; or the operands' time in HBM and their repeated loads', if longer;
-// then the last epilogue and the exchange between a split tile's pieces.  The constants are fitted to 4000
-// measured tilings of 51 products in all forms: the tiling of least estimate took at most 11 % longer
-// than the best of them, 0.9 % in the mean.  Fills in how the tiles are shared out.
+// then the last epilogue and the exchange between a split tile's pieces.  The constants were fitted to 3400
+// measured tilings of 51 products in all forms, of which the one of least estimate took at most 11 % longer
+// than the best, 0.9 % in the mean.  What came later (stages of half the rows, HBM's own rate, a residual asked for
+// ahead) follows kernels that changed: against the same measurements it is 21 % at most and 2.8 % in the mean.
+// The products had rows at multiples of 128 bytes: where rows straddle lines the choice can be further off (852 x
+// 1328 x 8840 takes 40 us, and 30.5 in pairs of 192 columns).  Fills in how the tiles are shared out.
 double tiling_cost(const Device &d, const Product &x, int64_t KB, Tiling &t)
 {
     const Sides s = sides_of(x, t);
@@ -487,8 +490,9 @@ constexpr double kLaunchClocks = 8000.0;
 
 // Whether n plain products, none of which needs another's result, take less time in one launch, and
 // their plans there: one kind of tile, the products with the longest tiles first, every cluster taking
-// each clusters-th tile of all.  (linear_backward of 16 x 512 x 512 takes 7.5 us so, and 13.7 in two
-// launches; of 4096^3 164 and 173; gated_backward of 4115 x 361 x 888 45 and 62.)
+// each clusters-th tile of all.  (In one launch and in several, from a graph: linear_backward of 16 x 512 x 512 4.8
+// and 9.3 us, of 4096^3 143 and 151 to 155, the same with gelu by tanh and a bias 168 to 171 and 174;
+// gated_backward of 4115 x 361 x 888 52 and 70, of 2047 x 2056 x 5999 240 and 252.)
 int find_together(const Device &d, Product **xs, const Plan *alone, int n, const Together **out)
 {
     PlanKey key[kFfnMaxProducts];
@@ -700,7 +704,9 @@ FfnAux aux_of(const ffn_quantized &q)
 // forward product whose operands are as its 16-byte loads need them, and whose rows fit its one pass.
 // Up to 8 tokens it is the faster one throughout, up to 16 but for a large gated pair (16 x 16384 x
 // 4096 52 us against 47), up to 32 for small weights (4096 x 4096 12.3 us against 13.4, 8192 x 8192
-// 36 against 34).
+// 36 against 34).  Between these points, and with this kernel's times first: 24 x 4096 x 6144 15.2 and 16.9,
+// gated 24 x 6144 x 4096 23.8 and 31.2, gated 12 x 8192 x 8192 48.7 and 58.9, which go to the other one; 12 x 14336 x
+// 4096 24.8 and 22.1, which does not.
 bool streams(const Call &c, const Product &x)
 {
     const bool dual = x.form == kDual;
@@ -724,10 +730,15 @@ bool streams(const Call &c, const Product &x)
 //   2048 x 8192     8 tokens 52.9, 75.5;   16 tokens 61.8, 75.0
 //   4096 x 16384    8 tokens 175, 184;     16 tokens 182, 168
 //   512 x 1024      8 tokens 15.1, 15.6;   16 tokens 19.9, 15.7
+// The limits lie between those points; close to them the other choice may be the better one (512 x 2048, 12
+// tokens, 19.7 and 23.5, goes to the other kernel; 1024 x 2048 23.0 and 28.0 as well).
 // A single dx does where its sum is long; shorter ones do better beside dW in one launch:
 //   4096 x 4096     8 tokens 23.6, 27.2;   16 tokens 27.1, 26.6
 //   12288 x 512     8 tokens 17.0, 20.9;   2048 x 2048  8 tokens 12.5, 9.3
 //   8192 x 8192     8 tokens 58.5, 59.0;   16 tokens 65.2, 59.4
+//   4096 x 1024    12 tokens 14.6, 18.8;   3584 x 2048  8 tokens 17.3, 21.0: both go to the other kernel
+// (253 products of few tokens in all four forms: the choice takes 2.5 % longer than the better of the two in the
+// mean, 32 % at most.)
 bool streams_back(const Call &c, const Product &x)
 {
     if (options.v[FFN_OPT_STREAM] == 2 || x.M > kFfnStreamBackTokens || x.K < 1 || x.a_mn || !x.b_mn || x.fp32 ||

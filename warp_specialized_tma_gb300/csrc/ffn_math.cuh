@@ -70,9 +70,10 @@ __device__ __forceinline__ Pair ffn_sigmoid(Pair x)
 
 // Phi(x), the normal distribution's, and e = exp(-x^2 / 2).  The lower tail is e times a
 // function of |x| that decays like 1 / |x|: a polynomial in u = 1 / (1 + q |x|), fitted to it by
-// least squares whose weights were raised where the relative error was largest, over |x| <= 13.4.
-// Off by 4.4e-7 of Phi at most, in the tail too, where 1 + erf cancels; and the slope needs e
-// besides.  With erfcf the slope kernel was bound by its arithmetic (6143 x 5999: 115 us, of which
+// least squares whose weights were raised where the relative error was largest, over |x| <= 13.4, to 1.0e-7.
+// In 32 bits, exp2's own error aside, off by 4.5e-7 of Phi at most down to x = -2, where 1 + erf cancels, 7.6e-7 to -4, 2.7e-6 to
+// -8 and 5e-6 to -10: x^2 is rounded before it is an exponent, which a result in bf16 does not show and one in
+// fp32 does.  The slope needs e besides.  With erfcf the slope kernel was bound by its arithmetic (6143 x 5999: 115 us, of which
 // HBM's are 33).
 __device__ __forceinline__ void ffn_normal(Pair x, Pair &cdf, Pair &e)
 {

@@ -11,7 +11,8 @@ Matrices are bf16 CUDA tensors with contiguous rows, at any pitch and offset; su
 each result is rounded once.  Results that are not given have rows at multiples of 128 bytes, as
 the quantisers' have: the next product reads them fastest.  Their pitch is above their width where
 that is no multiple of 64.  Operands whose rows do not start at multiples of 16 bytes are copied
-first, and large ones whose rows do not at multiples of 128.
+first, and large ones whose rows do not at multiples of 128, in every call: weights that are used
+again and again are better laid out so once.
 
 What gated() saves in 8 bits is in fp8's format: codes (float8_e4m3fn) and scales
 (float8_e8m0fnu), a power of two for each row and block of 128 columns.
@@ -259,7 +260,7 @@ def linear_backward(dy, x, weight, z=None, activation=None, bias: bool = False, 
     """Gradients of linear() from dy, the gradient of its result: (dx, dweight, dbias).
 
     dz = dy * act'(z) is rounded to bf16, in which the products take it; dx is bf16, dweight of
-    grad_dtype (bf16 or fp32).  dbias, with ``bias``, is fp32 (else None).  The residual's gradient is
+    grad_dtype (bf16 or fp32); both are always computed.  dbias, with ``bias``, is fp32 (else None).  The residual's gradient is
     dy itself.
     """
     act = _choice(ACTIVATIONS, activation, "activation")
@@ -284,7 +285,7 @@ def gated_backward(dy, x, saved, w_gate, w_up, w_down, activation="silu", grad_d
     """Gradients of y = h @ w_down.T with h = gated(x, w_gate, w_up), from dy: (dx, dw_gate, dw_up, dw_down).
 
     ``saved`` is what gated() saved; h is made again from it.  dg, du and h are rounded to bf16,
-    in which the products take them.
+    in which the products take them.  All four gradients are always computed.
     """
     act = _choice(ACTIVATIONS, activation, "activation")
     with _stream(stream, dy):
